@@ -6,7 +6,10 @@
  *     built with a GPU open-addressing hash table over int64 cell keys;
  *   - the output coordinate set of a strided sparse conv (sort + unique);
  *   - the convolution forward, its input gradient (dinput) and its weight
- *     gradient (dfilter) as implicit GEMMs over that map.
+ *     gradient (dfilter) as implicit GEMMs over that map;
+ *   - the layers that stand between convolutions: group norm with an activation
+ *     per sample, dropout, and products of rows with the weight of their expert,
+ *     each with its gradients, over rows grouped into segments.
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -67,7 +70,8 @@ typedef enum {
     SPC_ERR_UNSUPPORTED = 6,   /* a valid request this build does not implement */
     SPC_ERR_CUDA = 7,          /* a CUDA runtime call failed (launch, copy) */
     SPC_ERR_WORKSPACE = 8,     /* workspace missing or smaller than required */
-    SPC_ERR_TIMEOUT = 9        /* an internal GPU wait exceeded its bound (spc_set_wait_limit_ns); results invalid */
+    SPC_ERR_TIMEOUT = 9,       /* an internal GPU wait exceeded its bound (spc_set_wait_limit_ns); results invalid */
+    SPC_ERR_ROW_INDEX = 10     /* a segment offset or a row index lies outside its range */
 } spc_status;
 
 typedef enum { SPC_F32 = 0, SPC_F16 = 1, SPC_BF16 = 2 } spc_dtype;
@@ -78,8 +82,9 @@ typedef enum { SPC_F32 = 0, SPC_F16 = 1, SPC_BF16 = 2 } spc_dtype;
  * multiply (accumulation stays fp32); ignored for fp16/bf16. */
 typedef enum { SPC_PREC_EXACT = 0, SPC_PREC_TF32 = 1 } spc_precision;
 
-/* Activation of the fused forward epilogue (spc_conv_fwd_fused). */
-typedef enum { SPC_ACT_NONE = 0, SPC_ACT_RELU = 1 } spc_activation;
+/* Activation of the fused forward epilogue (spc_conv_fwd_fused: NONE and RELU)
+ * and of group norm (all three; SILU is z / (1 + exp(-z))). */
+typedef enum { SPC_ACT_NONE = 0, SPC_ACT_RELU = 1, SPC_ACT_SILU = 2 } spc_activation;
 
 /* How spc_conv_dgrad reads its map argument. */
 typedef enum {
@@ -474,6 +479,151 @@ SPC_API spc_status spc_conv_wgrad(const void* x, const void* dy, const int32_t* 
                                   int64_t n_in, int64_t n_out, int32_t cin, int32_t cout,
                                   spc_dtype dt, spc_precision prec, float* dw, int32_t* status,
                                   void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------- row segments
+ * A segment is the set of rows that share a small key: the voxels of one sample
+ * (the batch index of their coordinates) or the rows of one expert.  The layers
+ * below read rows in grouped order:
+ *   seg   [segments + 1] int32: segment s holds the positions seg[s] .. seg[s+1)-1;
+ *         offsets that are not in order or pass the number of rows set
+ *         SPC_ERR_ROW_INDEX.  A segment may be empty.  Positions before seg[0]
+ *         or from seg[segments] on belong to no segment.
+ *   order [n] int32 or NULL: the row that stands at each position (NULL: row r
+ *         at position r); a permutation of 0 .. n-1.  An entry out of range
+ *         sets SPC_ERR_ROW_INDEX and is skipped; a repeated one is not detected
+ *         (its row is written more than once).
+ *
+ * spc_row_segments -- the grouping itself: seg[s] = the number of rows i with
+ * 0 <= ids[i] < s, and order = the rows sorted by id, rows of one id in row
+ * order, then the rows whose id lies outside [0, segments) in row order.
+ *
+ *  ids       [n] int32, element i at ids[i * id_stride]: with id_stride 4 the
+ *            batch column of a coordinate array serves as it is.
+ *  segments  1 .. SPC_MAX_SEGMENTS.
+ *  seg       [segments + 1] int32 out.     order [n] int32 out, or NULL.
+ *  ws        spc_row_segments_workspace_size(n, segments) bytes.
+ */
+#define SPC_MAX_SEGMENTS 4096
+
+SPC_API size_t spc_row_segments_workspace_size(int64_t n, int32_t segments);
+SPC_API spc_status spc_row_segments(const int32_t* ids, int64_t id_stride, int64_t n,
+                                    int32_t segments, int32_t* seg, int32_t* order, void* ws,
+                                    size_t ws_bytes, void* stream);
+
+/* --------------------------------------------------------------- group norm
+ * spc_group_norm_fwd -- per segment s and group g of c / groups neighbouring
+ * channels: mean and variance (divided by the count) over the segment's rows
+ * and the group's channels, rstd = 1 / sqrt(variance + eps), and
+ *   y = act(gamma (x - mean) rstd + beta).
+ * Sums run in fp32 around a pivot near the mean, merged in a fixed order: results are
+ * run-to-run bit-identical.  An empty segment has mean 0 and variance 0; the
+ * rows of no segment give zeros.
+ *
+ *  x      [n, c] of dtype dt.      y [n, c] of dtype dt out (may be x itself).
+ *  gamma, beta  [c] fp32, or NULL (1 and 0).
+ *  seg, order   as above (order NULL: rows lie in grouped order).
+ *  groups divides c.    eps > 0.
+ *  mean, rstd   [segments, groups] fp32 out (what the backward pass reads).
+ *  status device int32 sticky error word, or NULL.
+ *  ws     spc_group_norm_workspace_size(...) bytes, 256-byte aligned; serves both
+ *         passes.
+ *  Rows are read in 16-byte words when x and y are 16-byte aligned and c is a
+ *  multiple of 16 bytes, else element by element.
+ */
+SPC_API size_t spc_group_norm_workspace_size(int64_t n, int32_t c, int32_t segments, int32_t groups,
+                                             spc_dtype dt);
+SPC_API spc_status spc_group_norm_fwd(const void* x, const float* gamma, const float* beta,
+                                      const int32_t* seg, const int32_t* order, int32_t segments,
+                                      int64_t n, int32_t c, int32_t groups, float eps,
+                                      spc_activation act, spc_dtype dt, void* y, float* mean,
+                                      float* rstd, int32_t* status, void* ws, size_t ws_bytes,
+                                      void* stream);
+
+/* spc_group_norm_bwd -- the gradients of spc_group_norm_fwd: with xh = (x - mean)
+ * rstd, z = gamma xh + beta, dz = dy act'(z), and N the number of elements of
+ * (s, g),
+ *   dgamma[c] = sum of dz xh and dbeta[c] = sum of dz over the rows of all segments,
+ *   dx = rstd (gamma dz - sum(gamma dz) / N - xh sum(gamma dz xh) / N),
+ * the two sums over (s, g).  act'(0) = 0 for RELU.  Rows of no segment give
+ * dx = 0.  Sums run in fp32 in a fixed order.
+ *
+ *  mean, rstd  [segments, groups] fp32 from the forward pass.
+ *  dx     [n, c] of dtype dt out (may be dy or x itself).
+ *  dgamma, dbeta  [c] fp32 out, or NULL.
+ *  Other arguments as for spc_group_norm_fwd.
+ */
+SPC_API spc_status spc_group_norm_bwd(const void* dy, const void* x, const float* gamma,
+                                      const float* beta, const float* mean, const float* rstd,
+                                      const int32_t* seg, const int32_t* order, int32_t segments,
+                                      int64_t n, int32_t c, int32_t groups, spc_activation act,
+                                      spc_dtype dt, void* dx, float* dgamma, float* dbeta,
+                                      int32_t* status, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------ dropout
+ * spc_dropout_fwd -- y[i] = residual[i] + (keep(i) ? x[i] / (1 - p) : 0), one
+ * rounding to dt.  The mask is a function of the element's index and is never
+ * stored: word i % 4 of the block (i / 4) of the counter-based generator
+ * Philox4x32-10 (Salmon, Moraes, Dror, Shaw: "Parallel random numbers: as easy as
+ * 1, 2, 3", SC 2011) with key = rng[0] and counter = (i / 4, rng[1]), low words
+ * first; element i is kept when its word >= round(p 2^32).
+ *
+ *  rng       [2] uint64 on the DEVICE: seed and offset.  A graph that holds the call draws
+ *            a new mask at every replay in which the caller advanced the offset.
+ *  x, y      [n] of dtype dt; y may be x.    residual [n] of dtype dt or NULL.
+ *  p         0 <= p <= 1 (p = 1 drops everything; a dropped element adds exact
+ *            0 whatever x holds).
+ */
+SPC_API spc_status spc_dropout_fwd(const void* x, const void* residual, int64_t n, double p,
+                                   const uint64_t* rng, spc_dtype dt, void* y, void* stream);
+
+/* spc_dropout_bwd -- dx[i] = keep(i) ? dy[i] / (1 - p) : 0 with the mask of the
+ * forward call that had the same rng and p (the residual's gradient is dy). */
+SPC_API spc_status spc_dropout_bwd(const void* dy, int64_t n, double p, const uint64_t* rng,
+                                   spc_dtype dt, void* dx, void* stream);
+
+/* --------------------------------------------------------- grouped products
+ * Products of each row with the weight of its segment (expert) g:
+ *   spc_grouped_fwd    y[yr(r)]  = x[xr(r)] W[g]            positions r of segment g
+ *   spc_grouped_dgrad  dx[xr(r)] = dy[yr(r)] W[g]^T
+ *   spc_grouped_wgrad  dW[g]     = sum of x[xr(r)]^T dy[yr(r)] over g's positions
+ * with xr(r) = x_rows[r], or r when x_rows is NULL, and yr likewise.  Segment
+ * sizes are read on the device: no call waits for them, and any split of the m
+ * positions (empty segments, all rows in one) is valid.
+ *
+ *  x      [n_x, cin], dy [n_y, cout] of dtype dt.   w [segments, cin, cout] of dtype dt.
+ *  seg    [segments + 1] as above; positions 0 .. m-1.
+ *  x_rows, y_rows  [m] int32 or NULL.  The list of the operand that is read may repeat
+ *         rows (a token that several experts take); the list of the result must be a
+ *         permutation of 0 .. m-1 (y of the forward and dx of dgrad have m
+ *         rows).  Entries out of range set SPC_ERR_ROW_INDEX: such a row reads
+ *         as zeros, such a result is not written.
+ *  y, dx  [m, .] of dtype dt out: fp32 accumulate, one rounding; positions of no
+ *         segment give rows of zeros (and add nothing to dW).
+ *  dw     [segments, cin, cout] fp32 out, overwritten (zeros for an empty segment).
+ *  status device int32 sticky error word, or NULL (also SPC_ERR_TIMEOUT).
+ *  ws     spc_grouped_workspace_size(...) bytes, 256-byte aligned; serves all three.
+ *  x, dy, w and the result must be 16-byte aligned.  Results are run-to-run
+ *  bit-identical.
+ *  Kernels: tcgen05 tensor cores for fp16 / bf16 with cin and cout multiples of 8,
+ *  else a tiled CUDA-core kernel (fp32 in full fp32 multiplies).
+ */
+SPC_API size_t spc_grouped_workspace_size(int32_t segments, int64_t m, int32_t cin, int32_t cout,
+                                          spc_dtype dt);
+SPC_API spc_status spc_grouped_fwd(const void* x, const void* w, const int32_t* seg,
+                                   const int32_t* x_rows, const int32_t* y_rows, int32_t segments,
+                                   int64_t n_x, int64_t m, int32_t cin, int32_t cout, spc_dtype dt,
+                                   void* y, int32_t* status, void* ws, size_t ws_bytes,
+                                   void* stream);
+SPC_API spc_status spc_grouped_dgrad(const void* dy, const void* w, const int32_t* seg,
+                                     const int32_t* x_rows, const int32_t* y_rows, int32_t segments,
+                                     int64_t n_y, int64_t m, int32_t cin, int32_t cout,
+                                     spc_dtype dt, void* dx, int32_t* status, void* ws,
+                                     size_t ws_bytes, void* stream);
+SPC_API spc_status spc_grouped_wgrad(const void* x, const void* dy, const int32_t* seg,
+                                     const int32_t* x_rows, const int32_t* y_rows, int32_t segments,
+                                     int64_t n_x, int64_t n_y, int64_t m, int32_t cin, int32_t cout,
+                                     spc_dtype dt, float* dw, int32_t* status, void* ws,
+                                     size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

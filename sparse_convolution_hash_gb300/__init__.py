@@ -1,5 +1,7 @@
 """GB300-native sparse 3-D convolution: indice maps, strided output sets and
-implicit-GEMM conv forward / dinput / dfilter, behind the C ABI of libspc.so.
+implicit-GEMM conv forward / dinput / dfilter, and the layers between convolutions
+(group norm with activation, dropout, products grouped by expert), behind the C
+ABI of libspc.so.
 
 ``binding`` holds the Python functions, named after the C entry points; the
 library is built in-tree by ``build.build()``.
@@ -24,6 +26,15 @@ from .binding import (  # noqa: F401
     spc_set_wait_limit_ns,
     SPC_ACT_NONE,
     SPC_ACT_RELU,
+    SPC_ACT_SILU,
+    spc_row_segments,
+    spc_group_norm_fwd,
+    spc_group_norm_bwd,
+    spc_dropout_fwd,
+    spc_dropout_bwd,
+    spc_grouped_fwd,
+    spc_grouped_dgrad,
+    spc_grouped_wgrad,
     spc_conv_inverse,
     spc_map_row_order,
     spc_maxpool_fwd,

@@ -24,7 +24,7 @@ SPC_OK = 0
 STATUS_NAMES = {
     0: "SPC_OK", 1: "SPC_ERR_INVALID_ARG", 2: "SPC_ERR_COORD_RANGE", 3: "SPC_ERR_DUPLICATE",
     4: "SPC_ERR_TABLE_FULL", 5: "SPC_ERR_CAPACITY", 6: "SPC_ERR_UNSUPPORTED", 7: "SPC_ERR_CUDA",
-    8: "SPC_ERR_WORKSPACE", 9: "SPC_ERR_TIMEOUT",
+    8: "SPC_ERR_WORKSPACE", 9: "SPC_ERR_TIMEOUT", 10: "SPC_ERR_ROW_INDEX",
 }
 SPC_F32, SPC_F16, SPC_BF16 = 0, 1, 2
 SPC_PREC_EXACT, SPC_PREC_TF32 = 0, 1
@@ -138,6 +138,31 @@ def lib():
             L.spc_conv_wgrad.argtypes = [_p, _p, _p, _i32, _i64, _i64, _i32, _i32, _i32, _i32,
                                          _p, _p, _p, _sz, _p]
             L.spc_conv_wgrad.restype = _i32
+            _f = ctypes.c_float
+            L.spc_row_segments_workspace_size.argtypes = [_i64, _i32]
+            L.spc_row_segments_workspace_size.restype = _sz
+            L.spc_row_segments.argtypes = [_p, _i64, _i64, _i32, _p, _p, _p, _sz, _p]
+            L.spc_row_segments.restype = _i32
+            L.spc_group_norm_workspace_size.argtypes = [_i64, _i32, _i32, _i32, _i32]
+            L.spc_group_norm_workspace_size.restype = _sz
+            L.spc_group_norm_fwd.argtypes = [_p, _p, _p, _p, _p, _i32, _i64, _i32, _i32, _f, _i32, _i32,
+                                             _p, _p, _p, _p, _p, _sz, _p]
+            L.spc_group_norm_fwd.restype = _i32
+            L.spc_group_norm_bwd.argtypes = [_p, _p, _p, _p, _p, _p, _p, _p, _i32, _i64, _i32, _i32, _i32,
+                                             _i32, _p, _p, _p, _p, _p, _sz, _p]
+            L.spc_group_norm_bwd.restype = _i32
+            L.spc_dropout_fwd.argtypes = [_p, _p, _i64, ctypes.c_double, _p, _i32, _p, _p]
+            L.spc_dropout_fwd.restype = _i32
+            L.spc_dropout_bwd.argtypes = [_p, _i64, ctypes.c_double, _p, _i32, _p, _p]
+            L.spc_dropout_bwd.restype = _i32
+            L.spc_grouped_workspace_size.argtypes = [_i32, _i64, _i32, _i32, _i32]
+            L.spc_grouped_workspace_size.restype = _sz
+            for f in (L.spc_grouped_fwd, L.spc_grouped_dgrad):
+                f.argtypes = [_p, _p, _p, _p, _p, _i32, _i64, _i64, _i32, _i32, _i32, _p, _p, _p, _sz, _p]
+                f.restype = _i32
+            L.spc_grouped_wgrad.argtypes = [_p, _p, _p, _p, _p, _i32, _i64, _i64, _i64, _i32, _i32, _i32,
+                                            _p, _p, _p, _sz, _p]
+            L.spc_grouped_wgrad.restype = _i32
             _lib = L
     return _lib
 
@@ -314,7 +339,7 @@ def spc_conv_fwd(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor],
     return y
 
 
-SPC_ACT_NONE, SPC_ACT_RELU = 0, 1
+SPC_ACT_NONE, SPC_ACT_RELU, SPC_ACT_SILU = 0, 1, 2
 
 
 def spc_conv_fwd_fused(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor],
@@ -509,4 +534,241 @@ def spc_conv_wgrad(x: torch.Tensor, dy: torch.Tensor, imap: Optional[torch.Tenso
                                 dt, precision, _ptr(dw), _ptr(status), _ptr(ws), ws.numel(),
                                 _stream(x.device))
     _check(code, "spc_conv_wgrad")
+    return dw
+
+
+def _int_list(t: Optional[torch.Tensor], name: str) -> Optional[torch.Tensor]:
+    """An int32 index list on the device (offsets, row orders), or None."""
+    return None if t is None else _cuda(t, name).to(torch.int32)
+
+
+def _values(t: torch.Tensor, name: str, like: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """A feature tensor of a supported type, or of `like`'s type."""
+    t = _cuda(t, name)
+    if like is not None:
+        return t.to(like.dtype)
+    if t.dtype not in _DTYPES:
+        raise ValueError(f"{name} must be float32, float16 or bfloat16, not {t.dtype}")
+    return t
+
+
+def _shape(t: Optional[torch.Tensor], shape, name: str):
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _result(out: Optional[torch.Tensor], shape, dtype, device, name: str) -> torch.Tensor:
+    """The caller's output buffer, checked, or a new one."""
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if tuple(out.shape) != tuple(shape) or out.dtype != dtype or out.device != device or not out.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+    return out
+
+
+def spc_row_segments(ids: torch.Tensor, segments: int, with_order: bool = True,
+                     out: Optional[torch.Tensor] = None, order: Optional[torch.Tensor] = None,
+                     ws: Optional[torch.Tensor] = None):
+    """Rows grouped by a small key: (seg [segments + 1], order [n] or None), both int32.
+
+    `ids` [n] is the key of each row (a column of a coordinate array is read in
+    place); rows whose key lies outside [0, segments) come last in `order`.
+    Pass `out` (seg), `order` and `ws` to call without allocating."""
+    if ids.dim() != 1:
+        raise ValueError("ids must have one dimension")
+    if not ids.is_cuda:
+        raise ValueError("ids must be a CUDA tensor")
+    ids = ids.to(torch.int32)
+    n, dev = ids.shape[0], ids.device
+    if n > 1 and ids.stride(0) < 1:
+        ids = ids.contiguous()
+    seg = _result(out, (segments + 1,), torch.int32, dev, "out")
+    if with_order:
+        order = _result(order, (n,), torch.int32, dev, "order")
+    nbytes = int(lib().spc_row_segments_workspace_size(n, segments))
+    if ws is None or ws.numel() < nbytes:
+        ws = _workspace(nbytes, dev)
+    code = lib().spc_row_segments(_ptr(ids), ids.stride(0) if n > 1 else 1, n, segments, _ptr(seg),
+                                  _ptr(order) if with_order else None, _ptr(ws), ws.numel(), _stream(dev))
+    _check(code, "spc_row_segments")
+    return seg, (order if with_order else None)
+
+
+def _norm_ws(ws, x, segments, groups):
+    n, c = x.shape
+    nbytes = int(lib().spc_group_norm_workspace_size(n, c, segments, groups, _DTYPES[x.dtype]))
+    return _workspace(nbytes, x.device) if ws is None or ws.numel() < nbytes else ws
+
+
+def _affine(t, c, name):
+    t = None if t is None else _cuda(t, name).to(torch.float32)
+    _shape(t, (c,), name)
+    return t
+
+
+def spc_group_norm_fwd(x: torch.Tensor, gamma: Optional[torch.Tensor], beta: Optional[torch.Tensor],
+                       seg: torch.Tensor, groups: int, order: Optional[torch.Tensor] = None,
+                       eps: float = 1e-5, act: int = SPC_ACT_NONE, out: Optional[torch.Tensor] = None,
+                       mean: Optional[torch.Tensor] = None, rstd: Optional[torch.Tensor] = None,
+                       status: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None):
+    """y = act(gamma (x - mean) rstd + beta) with statistics per segment (sample) and group of
+    channels: returns (y [n, C], mean [S, groups], rstd [S, groups]).
+
+    `seg` / `order` from spc_row_segments (order None: rows lie in grouped order);
+    pass `out`, `mean`, `rstd` and `ws` to call without allocating."""
+    x = _values(x, "x")
+    n, c = x.shape
+    seg, order = _int_list(seg, "seg"), _int_list(order, "order")
+    segments = seg.shape[0] - 1
+    _shape(order, (n,), "order")
+    gamma, beta = _affine(gamma, c, "gamma"), _affine(beta, c, "beta")
+    y = _result(out, (n, c), x.dtype, x.device, "out")
+    mean = _result(mean, (segments, groups), torch.float32, x.device, "mean")
+    rstd = _result(rstd, (segments, groups), torch.float32, x.device, "rstd")
+    ws = _norm_ws(ws, x, segments, groups)
+    code = lib().spc_group_norm_fwd(_ptr(x), _ptr(gamma), _ptr(beta), _ptr(seg), _ptr(order), segments, n, c,
+                                    groups, eps, act, _DTYPES[x.dtype], _ptr(y), _ptr(mean), _ptr(rstd),
+                                    _ptr(status), _ptr(ws), ws.numel(), _stream(x.device))
+    _check(code, "spc_group_norm_fwd")
+    return y, mean, rstd
+
+
+def spc_group_norm_bwd(dy: torch.Tensor, x: torch.Tensor, gamma: Optional[torch.Tensor],
+                       beta: Optional[torch.Tensor], mean: torch.Tensor, rstd: torch.Tensor,
+                       seg: torch.Tensor, groups: int, order: Optional[torch.Tensor] = None,
+                       act: int = SPC_ACT_NONE, out: Optional[torch.Tensor] = None,
+                       status: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None):
+    """Gradients of spc_group_norm_fwd: (dx [n, C], dgamma [C] fp32, dbeta [C] fp32).
+    `mean` and `rstd` come from the forward call."""
+    x = _values(x, "x")
+    dy = _values(dy, "dy", x)
+    n, c = x.shape
+    _shape(dy, (n, c), "dy")
+    seg, order = _int_list(seg, "seg"), _int_list(order, "order")
+    segments = seg.shape[0] - 1
+    _shape(order, (n,), "order")
+    gamma, beta = _affine(gamma, c, "gamma"), _affine(beta, c, "beta")
+    mean, rstd = _cuda(mean, "mean").to(torch.float32), _cuda(rstd, "rstd").to(torch.float32)
+    _shape(mean, (segments, groups), "mean")
+    _shape(rstd, (segments, groups), "rstd")
+    dx = _result(out, (n, c), x.dtype, x.device, "out")
+    params = torch.empty((2, c), dtype=torch.float32, device=x.device)
+    ws = _norm_ws(ws, x, segments, groups)
+    code = lib().spc_group_norm_bwd(_ptr(dy), _ptr(x), _ptr(gamma), _ptr(beta), _ptr(mean), _ptr(rstd),
+                                    _ptr(seg), _ptr(order), segments, n, c, groups, act, _DTYPES[x.dtype],
+                                    _ptr(dx), params.data_ptr(), params.data_ptr() + 4 * c, _ptr(status),
+                                    _ptr(ws), ws.numel(), _stream(x.device))
+    _check(code, "spc_group_norm_bwd")
+    return dx, params[0], params[1]
+
+
+def _rng(rng: torch.Tensor) -> torch.Tensor:
+    rng = _cuda(rng, "rng")
+    if rng.dtype not in (torch.int64, torch.uint64) or rng.numel() != 2:
+        raise ValueError("rng must hold two 64-bit integers: seed and offset")
+    return rng
+
+
+def spc_dropout_fwd(x: torch.Tensor, p: float, rng: torch.Tensor,
+                    residual: Optional[torch.Tensor] = None,
+                    out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y = residual + (x / (1 - p) where kept, else 0).  `rng` [2] int64 on the device holds
+    seed and offset; the mask is computed from them and the element's index, never stored."""
+    x = _values(x, "x")
+    res = _values(residual, "residual", x) if residual is not None else None
+    _shape(res, x.shape, "residual")
+    rng = _rng(rng)
+    y = _result(out, x.shape, x.dtype, x.device, "out")
+    code = lib().spc_dropout_fwd(_ptr(x), _ptr(res), x.numel(), p, _ptr(rng), _DTYPES[x.dtype],
+                                 _ptr(y), _stream(x.device))
+    _check(code, "spc_dropout_fwd")
+    return y
+
+
+def spc_dropout_bwd(dy: torch.Tensor, p: float, rng: torch.Tensor,
+                    out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """dx = dy / (1 - p) where the forward call with this rng and p kept the element, else 0."""
+    dy = _values(dy, "dy")
+    rng = _rng(rng)
+    dx = _result(out, dy.shape, dy.dtype, dy.device, "out")
+    code = lib().spc_dropout_bwd(_ptr(dy), dy.numel(), p, _ptr(rng), _DTYPES[dy.dtype], _ptr(dx),
+                                 _stream(dy.device))
+    _check(code, "spc_dropout_bwd")
+    return dx
+
+
+def _grouped(seg, x_rows, y_rows, rows):
+    """Offsets, row lists and the number of positions (a list's length, else the operand's rows)."""
+    seg, x_rows, y_rows = _int_list(seg, "seg"), _int_list(x_rows, "x_rows"), _int_list(y_rows, "y_rows")
+    m = x_rows.shape[0] if x_rows is not None else y_rows.shape[0] if y_rows is not None else rows
+    _shape(x_rows, (m,), "x_rows")
+    _shape(y_rows, (m,), "y_rows")
+    return seg, x_rows, y_rows, m
+
+
+def _grouped_ws(ws, segments, m, cin, cout, like):
+    nbytes = int(lib().spc_grouped_workspace_size(segments, m, cin, cout, _DTYPES[like.dtype]))
+    return _workspace(nbytes, like.device) if nbytes and (ws is None or ws.numel() < nbytes) else ws
+
+
+def spc_grouped_fwd(x: torch.Tensor, w: torch.Tensor, seg: torch.Tensor,
+                    x_rows: Optional[torch.Tensor] = None, y_rows: Optional[torch.Tensor] = None,
+                    out: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                    ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y[y_rows[r]] = x[x_rows[r]] W[g] for the positions r of each segment (expert) g:
+    w [segments, cin, cout]; returns y [m, cout].  A list left out means row r at position r."""
+    x = _values(x, "x")
+    w = _values(w, "w", x)
+    segments, cin, cout = w.shape
+    _shape(x, (x.shape[0], cin), "x")
+    seg, x_rows, y_rows, m = _grouped(seg, x_rows, y_rows, x.shape[0])
+    _shape(seg, (segments + 1,), "seg")
+    y = _result(out, (m, cout), x.dtype, x.device, "out")
+    ws = _grouped_ws(ws, segments, m, cin, cout, x)
+    code = lib().spc_grouped_fwd(_ptr(x), _ptr(w), _ptr(seg), _ptr(x_rows), _ptr(y_rows), segments,
+                                 x.shape[0], m, cin, cout, _DTYPES[x.dtype], _ptr(y), _ptr(status),
+                                 _ptr(ws), 0 if ws is None else ws.numel(), _stream(x.device))
+    _check(code, "spc_grouped_fwd")
+    return y
+
+
+def spc_grouped_dgrad(dy: torch.Tensor, w: torch.Tensor, seg: torch.Tensor,
+                      x_rows: Optional[torch.Tensor] = None, y_rows: Optional[torch.Tensor] = None,
+                      out: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                      ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """dx[x_rows[r]] = dy[y_rows[r]] W[g]^T; returns dx [m, cin].  Where the forward's x_rows
+    repeat rows, pass the list of slots instead and sum a row's slots."""
+    dy = _values(dy, "dy")
+    w = _values(w, "w", dy)
+    segments, cin, cout = w.shape
+    _shape(dy, (dy.shape[0], cout), "dy")
+    seg, x_rows, y_rows, m = _grouped(seg, x_rows, y_rows, dy.shape[0])
+    _shape(seg, (segments + 1,), "seg")
+    dx = _result(out, (m, cin), dy.dtype, dy.device, "out")
+    ws = _grouped_ws(ws, segments, m, cin, cout, dy)
+    code = lib().spc_grouped_dgrad(_ptr(dy), _ptr(w), _ptr(seg), _ptr(x_rows), _ptr(y_rows), segments,
+                                   dy.shape[0], m, cin, cout, _DTYPES[dy.dtype], _ptr(dx), _ptr(status),
+                                   _ptr(ws), 0 if ws is None else ws.numel(), _stream(dy.device))
+    _check(code, "spc_grouped_dgrad")
+    return dx
+
+
+def spc_grouped_wgrad(x: torch.Tensor, dy: torch.Tensor, seg: torch.Tensor,
+                      x_rows: Optional[torch.Tensor] = None, y_rows: Optional[torch.Tensor] = None,
+                      out: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                      ws: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """dW[g] = sum over the positions r of segment g of x[x_rows[r]]^T dy[y_rows[r]],
+    float32 [segments, cin, cout]."""
+    x = _values(x, "x")
+    dy = _values(dy, "dy", x)
+    cin, cout = x.shape[1], dy.shape[1]
+    seg, x_rows, y_rows, m = _grouped(seg, x_rows, y_rows, max(x.shape[0], dy.shape[0]))
+    segments = seg.shape[0] - 1
+    dw = _result(out, (segments, cin, cout), torch.float32, x.device, "out")
+    ws = _grouped_ws(ws, segments, m, cin, cout, x)
+    code = lib().spc_grouped_wgrad(_ptr(x), _ptr(dy), _ptr(seg), _ptr(x_rows), _ptr(y_rows), segments,
+                                   x.shape[0], dy.shape[0], m, cin, cout, _DTYPES[x.dtype], _ptr(dw),
+                                   _ptr(status), _ptr(ws), 0 if ws is None else ws.numel(),
+                                   _stream(x.device))
+    _check(code, "spc_grouped_wgrad")
     return dw

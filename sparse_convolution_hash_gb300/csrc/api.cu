@@ -64,6 +64,7 @@ const char* spc_status_string(spc_status s)
     case SPC_ERR_CUDA: return "CUDA runtime error";
     case SPC_ERR_WORKSPACE: return "workspace missing or too small";
     case SPC_ERR_TIMEOUT: return "an internal GPU wait exceeded its bound";
+    case SPC_ERR_ROW_INDEX: return "segment offset or row index out of range";
     }
     return "unknown status";
 }

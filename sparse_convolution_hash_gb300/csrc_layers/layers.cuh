@@ -1,0 +1,107 @@
+// layers.cuh -- internal launch interfaces of the layers between convolutions,
+// and what their kernels share: how positions, rows and segments are read.
+// Argument validation happens in layers_api.cu before these are called.
+#pragma once
+
+#include "common.cuh"
+
+namespace spc {
+
+// ------------------------------------------------------------- row segments
+size_t row_segments_ws_bytes(int64_t n, int32_t segments);
+spc_status row_segments(const int32_t* ids, int64_t id_stride, int64_t n, int32_t segments,
+                        int32_t* seg, int32_t* order, void* ws, cudaStream_t st);
+
+// --------------------------------------------------------------- group norm
+struct NormArgs {
+    const void* x;
+    const void* dy;         // backward only
+    const float* gamma;     // or NULL
+    const float* beta;      // or NULL
+    const int32_t* seg;
+    const int32_t* order;   // or NULL
+    void* out;              // y, or dx
+    float* mean;            // written by the forward pass, read by the backward one
+    float* rstd;
+    float* dgamma;          // backward only, or NULL
+    float* dbeta;
+    int32_t* status;
+    int64_t n;
+    int32_t segments, c, groups, act;
+    float eps;
+};
+size_t group_norm_ws_bytes(int64_t n, int32_t c, int32_t segments, int32_t groups, spc_dtype dt);
+spc_status group_norm_fwd(const NormArgs& a, spc_dtype dt, void* ws, cudaStream_t st);
+spc_status group_norm_bwd(const NormArgs& a, spc_dtype dt, void* ws, cudaStream_t st);
+
+// ------------------------------------------------------------------ dropout
+spc_status dropout(const void* x, const void* residual, int64_t n, double p, const uint64_t* rng,
+                   spc_dtype dt, void* y, cudaStream_t st);
+
+// --------------------------------------------------------- grouped products
+// out[out_rows(r)] = in[in_rows(r)] B[g], B[g] = w[g] ([k, n] row-major), or its
+// transpose of a stored [n, k] when w_transposed.
+struct GroupedArgs {
+    const void* in;
+    const void* w;
+    const int32_t* seg;
+    const int32_t* in_rows;   // or NULL
+    const int32_t* out_rows;  // or NULL
+    void* out;
+    int32_t* status;
+    int64_t in_n, m;
+    int32_t segments, k, n, w_transposed;
+};
+// dw[g] = sum over g's positions of x[x_rows(r)]^T dy[y_rows(r)]
+struct GroupedWgradArgs {
+    const void* x;
+    const void* dy;
+    const int32_t* seg;
+    const int32_t* x_rows;
+    const int32_t* y_rows;
+    float* dw;
+    int32_t* status;
+    int64_t n_x, n_y, m;
+    int32_t segments, cin, cout;
+};
+spc_status grouped_simt(const GroupedArgs& a, spc_dtype dt, cudaStream_t st);
+spc_status grouped_wgrad_simt(const GroupedWgradArgs& a, spc_dtype dt, cudaStream_t st);
+
+// ------------------------------------------------------------ device helpers
+// Segment s as positions [lo, hi) inside [0, n): offsets out of range or out of
+// order are reported and read as an empty (or cut) segment.
+__device__ __forceinline__ void segment_bounds(const int32_t* seg, int s, int64_t n, int32_t* status,
+                                               int64_t& lo, int64_t& hi)
+{
+    const int64_t a = __ldg(seg + s), b = __ldg(seg + s + 1);
+    lo = a < 0 ? 0 : (a > n ? n : a);
+    hi = b < lo ? lo : (b > n ? n : b);
+    if (lo != a || hi != b) set_status(status, SPC_ERR_ROW_INDEX);
+}
+
+// The segment that holds position r: the last s with seg[s] <= r, -1 before the
+// first, `segments` from seg[segments] on.
+__device__ __forceinline__ int segment_of(const int32_t* seg, int segments, int64_t r)
+{
+    int lo = 0, hi = segments + 1;  // first index with seg[index] > r
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(seg + mid) > r) hi = mid;
+        else lo = mid + 1;
+    }
+    return lo - 1;
+}
+
+// The row at position r, or -1 (reported) when the list names one out of [0, rows).
+__device__ __forceinline__ int64_t row_at(const int32_t* list, int64_t r, int64_t rows, int32_t* status)
+{
+    if (!list) return r;
+    const int32_t i = __ldg(list + r);
+    if (i < 0 || i >= rows) {
+        set_status(status, SPC_ERR_ROW_INDEX);
+        return -1;
+    }
+    return i;
+}
+
+}  // namespace spc
