@@ -65,6 +65,8 @@ struct GroupedWgradArgs {
     int32_t segments, cin, cout;
 };
 spc_status grouped_simt(const GroupedArgs& a, spc_dtype dt, cudaStream_t st);
+bool grouped_tc_supported(int32_t k, int32_t n, int64_t in_n, spc_dtype dt);
+spc_status grouped_tc(const GroupedArgs& a, spc_dtype dt, cudaStream_t st);
 spc_status grouped_wgrad_simt(const GroupedWgradArgs& a, spc_dtype dt, cudaStream_t st);
 
 // ------------------------------------------------------------ device helpers

@@ -67,6 +67,16 @@ spc_status check_grouped(const void* a, const void* b, const void* out, const in
     return SPC_OK;
 }
 
+// Tensor cores for 16-bit rows that TMA can load, else CUDA cores.
+spc_status grouped_product(const GroupedArgs& a, spc_dtype dt, cudaStream_t st)
+{
+    if (grouped_tc_supported(a.k, a.n, a.in_n, dt)) {
+        const spc_status s = grouped_tc(a, dt, st);
+        if (s != SPC_ERR_UNSUPPORTED) return s;
+    }
+    return grouped_simt(a, dt, st);
+}
+
 }  // namespace
 
 extern "C" {
@@ -163,7 +173,7 @@ spc_status spc_grouped_fwd(const void* x, const void* w, const int32_t* seg, con
     if (m == 0) return SPC_OK;
     if (!w || !y || (n_x > 0 && !x)) return SPC_ERR_INVALID_ARG;
     const GroupedArgs a{x, w, seg, x_rows, y_rows, y, status, n_x, m, segments, cin, cout, 0};
-    return grouped_simt(a, dt, static_cast<cudaStream_t>(stream));
+    return grouped_product(a, dt, static_cast<cudaStream_t>(stream));
 }
 
 spc_status spc_grouped_dgrad(const void* dy, const void* w, const int32_t* seg,
@@ -178,7 +188,7 @@ spc_status spc_grouped_dgrad(const void* dy, const void* w, const int32_t* seg,
     if (!w || !dx || (n_y > 0 && !dy)) return SPC_ERR_INVALID_ARG;
     // W[g] as stored is [cin, cout]: the [n, k] of the product dy W[g]^T
     const GroupedArgs a{dy, w, seg, y_rows, x_rows, dx, status, n_y, m, segments, cout, cin, 1};
-    return grouped_simt(a, dt, static_cast<cudaStream_t>(stream));
+    return grouped_product(a, dt, static_cast<cudaStream_t>(stream));
 }
 
 spc_status spc_grouped_wgrad(const void* x, const void* dy, const int32_t* seg,
