@@ -4,9 +4,12 @@
 //
 // Persistent: one CTA (or one pair of CTAs that share each tile, CG = 2) per SM
 // walks over 128 CG x BN tiles of all segments.  In a CTA
-//   warp 0 loads the stages: 64 of the reduction at a time, the rows as one TMA box
-//     or, through a row list, four rows per TMA gather; the weights as 3-D TMA
-//     boxes, so what lies past a segment's weights reads as zeros, not as its neighbour's;
+//   warp 0 loads the stages: 64 of the reduction at a time, the rows as one TMA box,
+//     the weights as 3-D TMA boxes, so that what lies past a segment's weights
+//     reads as zeros, not as its neighbour's;
+//   with a row list, warps 6-13 copy the rows instead, 16 bytes per cp.async
+//     (a TMA gather of four rows takes about 85 cycles whatever the rows, 128 rows per 1.4 us,
+//     a third of the pace of the MMAs; the copies keep up with them);
 //   warp 1 issues the MMAs into one of two fp32 accumulators in tensor memory;
 //   warps 2-5 empty the other one: round once, transpose through shared memory,
 //     store whole 128-byte row pieces.  Rows past the segment's end are not stored.
@@ -25,6 +28,7 @@ namespace spc {
 namespace {
 
 constexpr int kThreads = 192;
+constexpr int kGatherWarps = 8, kGatherThreads = kGatherWarps * 32;
 constexpr int kChunk = 64;  // reduction elements per stage: 128-byte rows
 constexpr uint64_t kDrainNs = 200000000ull;  // bound of the waits for a CTA's own copies and MMAs
 
@@ -50,11 +54,12 @@ template <> struct Fmt<__nv_bfloat16> { static constexpr uint32_t v = 1; static 
 
 // BMN: B as stored is [k][n] (the forward).  GATHER: rows come through in_rows.
 template <typename T, int CG, int BN, bool BMN, bool GATHER>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(GATHER ? kThreads + kGatherThreads : kThreads, 1)
 k_grouped_tc(GroupedArgs a, uint64_t wait_ns, const __grid_constant__ CUtensorMap map_in,
              const __grid_constant__ CUtensorMap map_w)
 {
     using S = Shape<CG, BN>;
+    constexpr int kAll = GATHER ? kThreads + kGatherThreads : kThreads;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     uint8_t* staging = smem + (size_t)S::kStages * S::kStage;
@@ -69,7 +74,7 @@ k_grouped_tc(GroupedArgs a, uint64_t wait_ns, const __grid_constant__ CUtensorMa
 
     if (tid == 0) {
         for (int s = 0; s < S::kStages; ++s) {
-            ptx::mbar_init(&full[s], 1);
+            ptx::mbar_init(&full[s], GATHER ? 1 + kGatherThreads : 1);  // the TMA loads, each gather thread
             ptx::mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -83,7 +88,7 @@ k_grouped_tc(GroupedArgs a, uint64_t wait_ns, const __grid_constant__ CUtensorMa
     if (warp == 1) ptx::tmem_alloc_cg<CG>(s_ctrl, S::kTmemCols);
     const int cols = (a.n + BN - 1) / BN;
     const int32_t tiles = tile_starts(a.seg, a.segments, a.m, S::kRows, cols, s_start,
-                                      blockIdx.x == 0 ? a.status : nullptr, tid, kThreads);
+                                      blockIdx.x == 0 ? a.status : nullptr, tid, kAll);
     ptx::tc_fence_before();
     if constexpr (CG == 2) ptx::cluster_sync();
     else __syncthreads();
@@ -101,21 +106,6 @@ k_grouped_tc(GroupedArgs a, uint64_t wait_ns, const __grid_constant__ CUtensorMa
             const TileWalk::Tile k = walk.at(t);
             if (k.g < 0) continue;
             const int64_t row0 = k.lo + rank * 128;
-            int32_t r[4] = {0, 0, 0, 0};
-            if constexpr (GATHER) {
-                // lane l brings rows 4 l .. 4 l + 3; past the segment, and for an
-                // entry out of range, a row past the tensor: zeros
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int64_t p = row0 + lane * 4 + j;
-                    r[j] = (int32_t)a.in_n;
-                    if (p < k.hi) {
-                        const int32_t i = __ldg(a.in_rows + p);
-                        if (i >= 0 && i < a.in_n) r[j] = i;
-                        else set_status(a.status, SPC_ERR_ROW_INDEX);
-                    }
-                }
-            }
             const int n0 = k.col * BN + (int)rank * S::kHalfN;
             for (int c = 0; c < chunks; ++c, ++it) {
                 const int s = it % S::kStages;
@@ -127,11 +117,9 @@ k_grouped_tc(GroupedArgs a, uint64_t wait_ns, const __grid_constant__ CUtensorMa
                 const uint32_t base = ptx::smem_u32(smem + (size_t)s * S::kStage);
                 uint32_t bar = ptx::smem_u32(&full[s]);
                 if constexpr (CG == 2) bar = ptx::map_rank(bar, 0);
-                if (rank == 0 && lane == 0) ptx::mbar_arrive_expect_tx(&full[s], CG * S::kStage);
+                if (rank == 0 && lane == 0) ptx::mbar_arrive_expect_tx(&full[s], CG * (GATHER ? S::kBBytes : S::kStage));
                 __syncwarp();
-                if constexpr (GATHER) {
-                    ptx::tma_gather4<CG>(base + lane * 512, &map_in, c * kChunk, r[0], r[1], r[2], r[3], bar);
-                } else {
+                if constexpr (!GATHER) {
                     if (lane == 0) ptx::tma_load2d<CG>(base, &map_in, c * kChunk, (int32_t)row0, bar);
                 }
                 if (lane == 0) {
@@ -170,6 +158,9 @@ k_grouped_tc(GroupedArgs a, uint64_t wait_ns, const __grid_constant__ CUtensorMa
                     const int s = it % S::kStages;
                     ok = ptx::mbar_wait(&full[s], (it / S::kStages) & 1, wait_ns);
                     if (!ok) break;
+                    // gathered rows came through the generic proxy: order them before the
+                    // tensor core's reads
+                    if constexpr (GATHER) ptx::fence_proxy_async_smem();
                     ptx::tc_fence_after();
                     const uint32_t base = ptx::smem_u32(smem + (size_t)s * S::kStage);
                     const uint64_t ad = ptx::desc_k_sw128(base);
@@ -189,6 +180,45 @@ k_grouped_tc(GroupedArgs a, uint64_t wait_ns, const __grid_constant__ CUtensorMa
             // MMAs in flight read shared memory: wait for the last stages' commits
             const uint32_t from = it > S::kStages ? it - S::kStages : 0;
             for (uint32_t j = from; j < it; ++j) ptx::mbar_wait(&empty[j % S::kStages], (j / S::kStages) & 1, kDrainNs);
+        }
+    } else if (warp >= kThreads / 32) {
+        // ------------------------------------------------------ row copies
+        // thread e copies piece e % 8 of rows e / 8 + 32 j: a warp instruction takes four
+        // whole 128-byte pieces of rows
+        if constexpr (GATHER) {
+            static_assert(CG == 1, "a pair's rows would have to arrive on the leader's barrier");
+            const int e = tid - kThreads, piece = e & 7, r0 = e >> 3;
+            const uint8_t* in = static_cast<const uint8_t*>(a.in);
+            const uint32_t off = (uint32_t)r0 * 128 + ((uint32_t)(piece ^ (r0 & 7)) << 4);
+            uint32_t it = 0;
+            for (int32_t t = first; t < tiles && ok; t += step) {
+                const TileWalk::Tile k = walk.at(t);
+                if (k.g < 0) continue;
+                const uint8_t* src[4];
+                bool there[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int64_t p = k.lo + r0 + 32 * j;
+                    const int64_t row = p < k.hi ? row_at(a.in_rows, p, a.in_n, a.status) : -1;
+                    there[j] = row >= 0;
+                    src[j] = in + ((there[j] ? row : 0) * a.k + piece * 8) * 2;
+                }
+                for (int c = 0; c < chunks; ++c, ++it) {
+                    const int s = it % S::kStages;
+                    if (it >= S::kStages) ok = ptx::mbar_wait(&empty[s], ((it / S::kStages) - 1) & 1, wait_ns);
+                    if (!ok) break;
+                    const uint32_t dst = ptx::smem_u32(smem + (size_t)s * S::kStage) + off;
+                    const bool inside = c * kChunk + piece * 8 < a.k;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const bool take = there[j] && inside;
+                        ptx::cp_async16(dst + j * 32 * 128, take ? src[j] + (int64_t)c * kChunk * 2 : in, take ? 16u : 0u);
+                    }
+                    ptx::cp_async_arrive_noinc(&full[s]);
+                }
+            }
+            if (!ok) set_status(a.status, SPC_ERR_TIMEOUT);
+            ptx::cp_async_wait_all();  // nothing of ours may still land when the CTA ends
         }
     } else {
         // --------------------------------------------------------- epilogue
@@ -283,7 +313,7 @@ spc_status launch(const GroupedArgs& a, cudaStream_t st)
 {
     using S = Shape<CG, BN>;
     CUtensorMap map_in, map_w;
-    if (!tmap<T>(&map_in, a.in, (uint64_t)a.k, (uint64_t)a.in_n, 1, kChunk, GATHER ? 1 : 128, 2)) return SPC_ERR_CUDA;
+    if (!tmap<T>(&map_in, a.in, (uint64_t)a.k, (uint64_t)a.in_n, 1, kChunk, 128, 2)) return SPC_ERR_CUDA;
     const bool w_ok = BMN ? tmap<T>(&map_w, a.w, (uint64_t)a.n, (uint64_t)a.k, (uint64_t)a.segments, 64, kChunk, 3)
                           : tmap<T>(&map_w, a.w, (uint64_t)a.k, (uint64_t)a.n, (uint64_t)a.segments, kChunk, S::kHalfN, 3);
     if (!w_ok) return SPC_ERR_CUDA;
@@ -294,7 +324,7 @@ spc_status launch(const GroupedArgs& a, cudaStream_t st)
     const int groups = (int)std::min<int64_t>(sm_count() / CG, most);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(groups * CG));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(GATHER ? kThreads + kGatherThreads : kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -311,8 +341,9 @@ spc_status launch(const GroupedArgs& a, cudaStream_t st)
 template <typename T, int CG, int BN>
 spc_status pick(const GroupedArgs& a, cudaStream_t st)
 {
-    if (a.w_transposed) return a.in_rows ? launch<T, CG, BN, false, true>(a, st) : launch<T, CG, BN, false, false>(a, st);
-    return a.in_rows ? launch<T, CG, BN, true, true>(a, st) : launch<T, CG, BN, true, false>(a, st);
+    if constexpr (CG == 1)
+        if (a.in_rows) return a.w_transposed ? launch<T, CG, BN, false, true>(a, st) : launch<T, CG, BN, true, true>(a, st);
+    return a.w_transposed ? launch<T, CG, BN, false, false>(a, st) : launch<T, CG, BN, true, false>(a, st);
 }
 
 }  // namespace

@@ -1,5 +1,5 @@
 // tc2.cuh -- inline-PTX wrappers beyond csrc/ptx.cuh: thread-block clusters, TMA
-// loads of row lists and of 3-D tiles, and the tensor-core operations in their
+// loads of 2-D and 3-D tiles, and the tensor-core operations in their
 // one-CTA (CG = 1) and CTA-pair (CG = 2) forms.
 #pragma once
 
@@ -60,24 +60,6 @@ __device__ __forceinline__ void tma_load3d(uint32_t dst, const void* tmap, int32
     else
         asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
                      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst), "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar)
-                     : "memory");
-}
-
-// Four listed rows of a 2-D tensor (box one row high) into consecutive rows of
-// shared memory; a row past the tensor reads as zeros.
-template <int CG>
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const void* tmap, int32_t x, int32_t r0, int32_t r1,
-                                            int32_t r2, int32_t r3, uint32_t bar)
-{
-    if constexpr (CG == 1)
-        asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
-                     " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst), "l"(tmap), "r"(x), "r"(r0), "r"(r1),
-                     "r"(r2), "r"(r3), "r"(bar)
-                     : "memory");
-    else
-        asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2"
-                     " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst), "l"(tmap), "r"(x), "r"(r0), "r"(r1),
-                     "r"(r2), "r"(r3), "r"(bar)
                      : "memory");
 }
 
