@@ -154,12 +154,9 @@ spc_status spc_dropout_bwd(const void* dy, int64_t n, double p, const uint64_t* 
 
 size_t spc_grouped_workspace_size(int32_t segments, int64_t m, int32_t cin, int32_t cout, spc_dtype dt)
 {
-    (void)segments;
-    (void)m;
-    (void)cin;
-    (void)cout;
-    (void)dt;
-    return 0;
+    if (!segments_ok(segments) || m < 0 || cin < 1 || cout < 1 || !dtype_ok(dt)) return 0;
+    // the gradient by the weights on tensor cores keeps parts of tiles there
+    return dt == SPC_F32 || cin % 8 || cout % 8 ? 0 : grouped_wgrad_tc_ws_bytes();
 }
 
 spc_status spc_grouped_fwd(const void* x, const void* w, const int32_t* seg, const int32_t* x_rows,
@@ -202,7 +199,8 @@ spc_status spc_grouped_wgrad(const void* x, const void* dy, const int32_t* seg,
     if (s != SPC_OK) return s;
     if (!dw || (n_x > 0 && !x) || (n_y > 0 && !dy)) return SPC_ERR_INVALID_ARG;
     const GroupedWgradArgs a{x, dy, seg, x_rows, y_rows, dw, status, n_x, n_y, m, segments, cin, cout};
-    return grouped_wgrad_simt(a, dt, static_cast<cudaStream_t>(stream));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return grouped_wgrad_tc_supported(a, dt) ? grouped_wgrad_tc(a, dt, ws, st) : grouped_wgrad_simt(a, dt, st);
 }
 
 }  // extern "C"
