@@ -503,7 +503,7 @@ SPC_API spc_status spc_conv_wgrad(const void* x, const void* dy, const int32_t* 
  *  seg       [segments + 1] int32 out.     order [n] int32 out, or NULL.
  *  ws        spc_row_segments_workspace_size(n, segments) bytes.
  */
-#define SPC_MAX_SEGMENTS 4096
+#define SPC_MAX_SEGMENTS 1024
 
 SPC_API size_t spc_row_segments_workspace_size(int64_t n, int32_t segments);
 SPC_API spc_status spc_row_segments(const int32_t* ids, int64_t id_stride, int64_t n,

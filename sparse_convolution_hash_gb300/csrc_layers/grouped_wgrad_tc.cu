@@ -28,6 +28,7 @@ constexpr int kGatherThreads = 256;
 constexpr int kUnit = 64;    // rows of a unit
 constexpr int kTileM = 128;  // input channels of a tile
 constexpr int kJoinRows = 4;
+constexpr int kMaxParts = 192;  // CTAs at most: one thread of the smaller block plans for each
 constexpr int kAtom = kUnit * 128;  // 64 rows x 64 channels
 constexpr uint64_t kDrainNs = 200000000ull;
 
@@ -41,7 +42,7 @@ struct Shape {
     static constexpr int kStaging = 4 * 32 * 128;
     static size_t smem(int segments)
     {
-        return 1024 + (size_t)kStages * kStage + kStaging + 8 * (2 * kStages + 4) + 16 + 4 * ((size_t)segments + 1);
+        return 1024 + (size_t)kStages * kStage + kStaging + 8 * (2 * kStages + 4) + 16 + 4 * (2 * (size_t)segments + 1);
     }
 };
 
@@ -54,99 +55,226 @@ struct Piece {
     int32_t g, tile;
     int32_t k0, k1, units;
     int64_t lo, hi;  // positions of the segment
+    int32_t slot;    // of a part: 0 at the start of its CTA's share, else 1
     __device__ __forceinline__ bool whole() const { return k0 == 0 && k1 == units; }
 };
 
-// The shares: s_start[g] = units (of 64 rows, at least one) of the segments before g.
-struct Shares {
-    const int32_t* start;
+// The plan of a call, the same in every CTA: a function of `seg` and the grid alone.
+// Segments are listed with those of at most an even share (total units / CTAs) first,
+// the longer ones after them.  The tiles of that list in turn: the first `waves` x CTAs
+// are whole tiles, tile c + i CTAs for CTA c, so that neighbouring tiles read the same
+// rows at the same time; the units of the tiles after them go to the CTAs in
+// contiguous shares, each as long as evens out what its whole tiles took.
+struct Plan {
+    int32_t waves;
+    int32_t parts;               // CTAs
+    int64_t base;                // first unit of the shares
+    int64_t first[kMaxParts + 1];  // share c: units base + first[c] .. base + first[c + 1)
+    int32_t id[kMaxParts];       // number of CTA c among those that have a share
+    int64_t sum;
+    int32_t count;
+    int64_t warp_sum[32];
+    int32_t warp_count[32];
+};
+
+struct Walk {
+    const int32_t* start;  // units of a tile of the listed segments before j, summed
+    const int32_t* list;   // segment j of the list
     const int32_t* seg;
+    const Plan* plan;
     int64_t m;
     int32_t segments, tiles;  // tiles of one segment
-    int64_t total;            // units of all tiles
-    int32_t parts;
+    int32_t wave, c;
+    int64_t u, begin, end;
 
-    __device__ __forceinline__ int64_t first(int32_t part) const { return total * part / parts; }
-    __device__ __forceinline__ Piece at(int64_t u, int64_t end) const
+    __device__ __forceinline__ void piece(Piece& p, int j, int32_t tile) const
     {
-        const int32_t f = (int32_t)(u / tiles);
-        int lo = 0, hi = segments;  // last g with start[g] <= f
+        p.g = list[j];
+        p.tile = tile;
+        p.units = start[j + 1] - start[j];
+        segment_bounds(seg, p.g, m, nullptr, p.lo, p.hi);
+    }
+    __device__ __forceinline__ void reset(int32_t cta)
+    {
+        c = cta;
+        wave = 0;
+        u = begin = plan->base + plan->first[c];
+        end = plan->base + plan->first[c + 1];
+    }
+    __device__ __forceinline__ bool more() const { return wave < plan->waves || u < end; }
+    __device__ __forceinline__ Piece next()
+    {
+        Piece p;
+        if (wave < plan->waves) {
+            const int64_t t = c + (int64_t)wave * plan->parts;
+            const int32_t j = (int32_t)(t / tiles);
+            piece(p, j, (int32_t)(t - (int64_t)j * tiles));
+            p.k0 = p.slot = 0;
+            p.k1 = p.units;
+            ++wave;
+            return p;
+        }
+        p = at(u);
+        const int64_t left = end - u;
+        p.slot = u == begin ? 0 : 1;
+        p.k1 = p.units - p.k0 <= left ? p.units : p.k0 + (int32_t)left;
+        u += p.k1 - p.k0;
+        return p;
+    }
+    // The piece that begins at unit v and runs to its tile's end.
+    __device__ __forceinline__ Piece at(int64_t v) const
+    {
+        const int32_t f = (int32_t)(v / tiles);
+        int lo = 0, hi = segments;  // last j with start[j] <= f
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
             if (start[mid] <= f) lo = mid;
             else hi = mid;
         }
+        const int64_t in = v - (int64_t)start[lo] * tiles;
+        const int32_t units = start[lo + 1] - start[lo], tile = (int32_t)(in / units);
         Piece p;
-        p.g = lo;
-        p.units = start[lo + 1] - start[lo];
-        const int64_t in = u - (int64_t)start[lo] * tiles;
-        p.tile = (int32_t)(in / p.units);
-        p.k0 = (int32_t)(in - (int64_t)p.tile * p.units);
-        const int64_t left = end - u;
-        p.k1 = p.units - p.k0 <= left ? p.units : p.k0 + (int32_t)left;
-        segment_bounds(seg, lo, m, nullptr, p.lo, p.hi);
+        piece(p, lo, tile);
+        p.k0 = (int32_t)(in - (int64_t)tile * units);
+        p.k1 = units;
+        p.slot = 0;
         return p;
     }
 };
 
-// Fills s_start [segments + 1]; every thread of the block calls it.
-__device__ __forceinline__ void unit_starts(const int32_t* seg, int segments, int64_t m, int32_t* s_start,
-                                            int32_t* status, int tid, int threads)
+// Inclusive sum over the block; every thread calls it.
+template <typename V>
+__device__ __forceinline__ V block_scan(V v, V* s_warp, int tid, int threads, V& total)
 {
-    __shared__ int32_t s_warp[32];
     const int lane = tid & 31, warp = tid >> 5;
-    int32_t carry = 0;
-    for (int g0 = 0; g0 < segments; g0 += threads) {
-        const int g = g0 + tid;
-        int32_t units = 0;
-        if (g < segments) {
-            int64_t a, b;
-            segment_bounds(seg, g, m, status, a, b);
-            units = b > a ? (int32_t)((b - a + kUnit - 1) / kUnit) : 1;
-        }
-        int32_t inc = units;
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int32_t u = __shfl_up_sync(FULL_MASK, inc, d);
-            if (lane >= d) inc += u;
-        }
-        if (lane == 31) s_warp[warp] = inc;
-        __syncthreads();
-        int32_t base = carry;
-        for (int w = 0; w < threads / 32; ++w) {
-            if (w < warp) base += s_warp[w];
-            carry += s_warp[w];
-        }
-        if (g < segments) s_start[g] = base + inc - units;
-        __syncthreads();
+    for (int d = 1; d < 32; d <<= 1) {
+        const V u = __shfl_up_sync(FULL_MASK, v, d);
+        if (lane >= d) v += u;
     }
-    if (tid == 0) s_start[segments] = carry;
+    __syncthreads();
+    if (lane == 31) s_warp[warp] = v;
+    __syncthreads();
+    total = 0;
+    for (int w = 0; w < threads / 32; ++w) {
+        if (w < warp) v += s_warp[w];
+        total += s_warp[w];
+    }
+    return v;
+}
+
+// Fills the list, its unit sums [segments + 1] and the plan; every thread of the block calls it.
+__device__ __forceinline__ void make_plan(const int32_t* seg, int segments, int64_t m, int tiles, int parts,
+                                          int32_t* s_start, int32_t* s_list, Plan* plan, int32_t* status, int tid,
+                                          int threads)
+{
+    auto units_of = [&](int g) -> int32_t {
+        int64_t a, b;
+        segment_bounds(seg, g, m, status, a, b);
+        return b > a ? (int32_t)((b - a + kUnit - 1) / kUnit) : 1;
+    };
+    int64_t all = 0, t64;
+    for (int g = tid; g < segments; g += threads) all += units_of(g);
+    block_scan<int64_t>(all, plan->warp_sum, tid, threads, t64);
+    const int64_t total = t64 * tiles, even = total / parts;
+    status = nullptr;
+    int32_t listed = 0, shorter = 0, t32;
+    for (int pass = 0; pass < 2; ++pass)
+        for (int g0 = 0; g0 < segments; g0 += threads) {
+            const int g = g0 + tid;
+            const bool mine = g < segments && (units_of(g) <= even) == (pass == 0);
+            const int32_t at = block_scan<int32_t>(mine ? 1 : 0, plan->warp_count, tid, threads, t32);
+            if (mine) s_list[listed + at - 1] = g;
+            listed += t32;
+            if (pass == 0) shorter += t32;
+        }
+    __syncthreads();
+    int32_t carry = 0;
+    for (int j0 = 0; j0 < segments; j0 += threads) {
+        const int j = j0 + tid;
+        const int32_t units = j < segments ? units_of(s_list[j]) : 0;
+        const int32_t at = block_scan<int32_t>(units, plan->warp_count, tid, threads, t32);
+        if (j < segments) s_start[j + 1] = carry + at;
+        carry += t32;
+    }
+    if (tid == 0) s_start[0] = 0;
+    __syncthreads();
+    // whole waves: all there are, less one where too little would be left to even out
+    int32_t waves = (int32_t)((int64_t)shorter * tiles / parts);
+    auto unit_of_tile = [&](int64_t t) -> int64_t {
+        const int32_t j = (int32_t)(t / tiles);
+        if (j >= segments) return total;
+        return (int64_t)s_start[j] * tiles + (t - (int64_t)j * tiles) * (s_start[j + 1] - s_start[j]);
+    };
+    if (waves > 0 && (total - unit_of_tile((int64_t)waves * parts)) * 8 < total / waves) --waves;
+    const int64_t base = unit_of_tile((int64_t)waves * parts), rest = total - base;
+    int64_t took = 0;
+    if (tid < parts)
+        for (int i = 0; i < waves; ++i) {
+            const int32_t j = (int32_t)((tid + (int64_t)i * parts) / tiles);
+            took += s_start[j + 1] - s_start[j];
+        }
+    // the level to which the shares fill every CTA that is below it
+    bool below = tid < parts;
+    int64_t level = 0, extra = 0, rank = 0;
+    for (int round = 0; round < 8; ++round) {
+        int64_t sum;
+        int32_t n;
+        block_scan<int64_t>(below ? took : 0, plan->warp_sum, tid, threads, sum);
+        const int32_t at = block_scan<int32_t>(below ? 1 : 0, plan->warp_count, tid, threads, n);
+        rank = at - 1;
+        level = (rest + sum) / n;
+        extra = (rest + sum) - level * n;
+        const bool still = below && took <= level;
+        int32_t kept;
+        block_scan<int32_t>(still ? 1 : 0, plan->warp_count, tid, threads, kept);
+        if (kept == n) break;
+        if (round < 7) below = still;
+    }
+    int64_t share = below ? level - took + (rank < extra ? 1 : 0) : 0;
+    if (share < 0) share = 0;
+    int64_t sum;
+    int32_t n;
+    const int64_t to = block_scan<int64_t>(share, plan->warp_sum, tid, threads, sum);
+    const int32_t at = block_scan<int32_t>(share > 0 ? 1 : 0, plan->warp_count, tid, threads, n);
+    if (tid < parts) {
+        plan->first[tid + 1] = tid == parts - 1 || to > rest ? rest : to;
+        plan->id[tid] = at - 1;
+    }
+    if (tid == 0) {
+        plan->first[0] = 0;
+        plan->waves = waves;
+        plan->parts = parts;
+        plan->base = base;
+    }
     __syncthreads();
 }
 
-// The tile that starts in share c and ends in a later one: its parts are slot `slot` of c
-// and the first slots of the `more` shares after it (0: there is none).
+// The tile that starts in the share of a CTA and ends in a later one: its parts are slot `slot`
+// of that share and the first slots of the `more` shares after it (0: there is none).
 struct Join {
     int32_t g, tile, slot, more;
 };
 
-__device__ __forceinline__ Join join_plan(const Shares& sh, int c, int64_t u0, int64_t u1)
+__device__ __forceinline__ Join join_of(const Walk& walk, int c)
 {
+    const Plan* plan = walk.plan;
+    const int64_t u0 = plan->base + plan->first[c], u1 = plan->base + plan->first[c + 1];
     Join j{0, 0, 0, 0};
-    if (u0 == u1) return j;
-    const Piece p = sh.at(u1 - 1, u1);
+    const Piece p = walk.at(u1 - 1);
     const int64_t first = u1 - 1 - p.k0, end = first + p.units;
     if (first < u0 || end <= u1) return j;
     j.g = p.g;
     j.tile = p.tile;
     j.slot = first == u0 ? 0 : 1;
-    while (c + 1 + j.more < sh.parts && sh.first(c + 1 + j.more) < end) ++j.more;
+    for (int q = c + 1; q < plan->parts && plan->base + plan->first[q] < end; ++q)
+        if (plan->first[q + 1] > plan->first[q]) ++j.more;
     return j;
 }
 
 template <typename T, int BN, bool GATHER>
 __global__ void __launch_bounds__(GATHER ? kThreads + kGatherThreads : kThreads, 1)
-k_grouped_wgrad_tc(GroupedWgradArgs a, float* __restrict__ part, Join* __restrict__ plan, uint64_t wait_ns,
+k_grouped_wgrad_tc(GroupedWgradArgs a, float* __restrict__ part, Join* __restrict__ joins, uint64_t wait_ns,
                    const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_dy)
 {
     using S = Shape<BN>;
@@ -160,6 +288,8 @@ k_grouped_wgrad_tc(GroupedWgradArgs a, float* __restrict__ part, Join* __restric
     uint64_t* acc_empty = acc_full + 2;
     uint32_t* s_ctrl = reinterpret_cast<uint32_t*>(acc_empty + 2);
     int32_t* s_start = reinterpret_cast<int32_t*>(s_ctrl + 4);
+    int32_t* s_list = s_start + a.segments + 1;
+    __shared__ Plan plan;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (tid == 0) {
@@ -178,27 +308,27 @@ k_grouped_wgrad_tc(GroupedWgradArgs a, float* __restrict__ part, Join* __restric
         }
     }
     if (warp == 1) ptx::tmem_alloc_cg<1>(s_ctrl, S::kTmemCols);
-    unit_starts(a.seg, a.segments, a.m, s_start, blockIdx.x == 0 ? a.status : nullptr, tid, kAll);
+    const int cols = (a.cout + BN - 1) / BN, tiles = (a.cin + kTileM - 1) / kTileM * cols;
+    make_plan(a.seg, a.segments, a.m, tiles, gridDim.x, s_start, s_list, &plan, blockIdx.x == 0 ? a.status : nullptr, tid, kAll);
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = s_ctrl[0];
-    const int cols = (a.cout + BN - 1) / BN, tiles = (a.cin + kTileM - 1) / kTileM * cols;
-    const int64_t total = (int64_t)s_start[a.segments] * tiles;
-    const int32_t parts = total < (int64_t)gridDim.x ? (int32_t)total : (int32_t)gridDim.x;
-    const Shares sh{s_start, a.seg, a.m, a.segments, tiles, total, parts};
-    const bool at_work = (int)blockIdx.x < parts;
-    const int64_t u0 = at_work ? sh.first(blockIdx.x) : 0, u1 = at_work ? sh.first(blockIdx.x + 1) : 0;
+    Walk walk{s_start, s_list, a.seg, &plan, a.m, a.segments, tiles, 0, 0, 0, 0, 0};
+    walk.reset(blockIdx.x);
     bool ok = true;
-    if (tid == 0) plan[blockIdx.x] = join_plan(sh, blockIdx.x, u0, u1);
+    if (blockIdx.x == 0 && tid < plan.parts && plan.first[tid + 1] > plan.first[tid]) joins[plan.id[tid]] = join_of(walk, tid);
+    if (blockIdx.x == 0 && tid >= 1 && tid <= plan.parts) {  // numbers that no share has
+        const int n = plan.id[plan.parts - 1] + 1;
+        if (n + tid - 1 < plan.parts) joins[n + tid - 1] = Join{0, 0, 0, 0};
+    }
 
     if (warp == 0) {
         // ------------------------------------------------------ dense loads
         if (!GATHER && lane == 0) {
             uint32_t it = 0;
-            for (int64_t u = u0; u < u1 && ok;) {
-                const Piece p = sh.at(u, u1);
-                u += p.k1 - p.k0;
+            while (walk.more() && ok) {
+                const Piece p = walk.next();
                 if (p.lo == p.hi) continue;
                 const int c0 = p.tile / cols * kTileM, n0 = p.tile % cols * BN;
                 for (int k = p.k0; k < p.k1; ++k, ++it) {
@@ -223,9 +353,8 @@ k_grouped_wgrad_tc(GroupedWgradArgs a, float* __restrict__ part, Join* __restric
         // ------------------------------------------------------------- MMAs
         const uint32_t idesc = ptx::idesc_make(Fmt<T>::v, kTileM, BN) | (1u << 15) | (1u << 16);
         uint32_t it = 0, n = 0;
-        for (int64_t u = u0; u < u1 && ok;) {
-            const Piece p = sh.at(u, u1);
-            u += p.k1 - p.k0;
+        while (walk.more() && ok) {
+            const Piece p = walk.next();
             if (p.lo == p.hi) continue;
             const uint32_t b = n & 1;
             if (n >= 2) ok = __all_sync(FULL_MASK, ptx::mbar_wait(&acc_empty[b], ((n >> 1) - 1) & 1, wait_ns));
@@ -274,9 +403,8 @@ k_grouped_wgrad_tc(GroupedWgradArgs a, float* __restrict__ part, Join* __restric
             const uint8_t* dy = static_cast<const uint8_t*>(a.dy);
             const uint32_t off = (uint32_t)r0 * 128 + ((uint32_t)(piece ^ (r0 & 7)) << 4);
             uint32_t it = 0;
-            for (int64_t u = u0; u < u1 && ok;) {
-                const Piece p = sh.at(u, u1);
-                u += p.k1 - p.k0;
+            while (walk.more() && ok) {
+                const Piece p = walk.next();
                 if (p.lo == p.hi) continue;
                 const int c0 = p.tile / cols * kTileM + piece * 8, n0 = p.tile % cols * BN + piece * 8;
                 // the rows of thread e's two reduction indices of unit k (-1: zeros)
@@ -328,10 +456,8 @@ k_grouped_wgrad_tc(GroupedWgradArgs a, float* __restrict__ part, Join* __restric
         const int quarter = warp & 3;
         uint8_t* box = staging + (warp - 2) * (32 * 128);
         uint32_t n = 0;
-        for (int64_t u = u0; u < u1 && ok;) {
-            const Piece p = sh.at(u, u1);
-            const bool at_start = u == u0;
-            u += p.k1 - p.k0;
+        while (walk.more() && ok) {
+            const Piece p = walk.next();
             const uint32_t b = n & 1;
             const bool some = p.lo != p.hi;
             if (some) {
@@ -351,7 +477,7 @@ k_grouped_wgrad_tc(GroupedWgradArgs a, float* __restrict__ part, Join* __restric
                 rows = a.cin - c0;
                 width = a.cout - n0;
             } else {
-                dst = part + ((int64_t)blockIdx.x * 2 + (at_start ? 0 : 1)) * (kTileM * BN) + quarter * 32 * BN;
+                dst = part + ((int64_t)plan.id[blockIdx.x] * 2 + p.slot) * (kTileM * BN) + quarter * 32 * BN;
                 pitch = BN;
                 rows = 32;
                 width = BN;
@@ -402,10 +528,10 @@ k_grouped_wgrad_tc(GroupedWgradArgs a, float* __restrict__ part, Join* __restric
 // of its parts, in the order of the shares.
 template <int BN>
 __global__ void __launch_bounds__(kJoinRows * BN / 4)
-k_grouped_wgrad_join(GroupedWgradArgs a, const float* __restrict__ part, const Join* __restrict__ plan)
+k_grouped_wgrad_join(GroupedWgradArgs a, const float* __restrict__ part, const Join* __restrict__ joins)
 {
     const int c = blockIdx.x;
-    const Join j = plan[c];
+    const Join j = joins[c];
     if (j.more == 0) return;
     const int cols = (a.cout + BN - 1) / BN;
     const int r = blockIdx.y * kJoinRows + threadIdx.x / (BN / 4), n = threadIdx.x % (BN / 4) * 4;
@@ -438,10 +564,10 @@ spc_status launch(const GroupedWgradArgs& a, float* part, cudaStream_t st)
     const size_t smem = S::smem(a.segments);
     SPC_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
     const int parts = grouped_wgrad_parts();
-    Join* plan = reinterpret_cast<Join*>(part + (int64_t)parts * 2 * kTileM * 256);
-    kernel<<<parts, GATHER ? kThreads + kGatherThreads : kThreads, smem, st>>>(a, part, plan, wait_limit_ns(), mx, my);
+    Join* joins = reinterpret_cast<Join*>(part + (int64_t)parts * 2 * kTileM * 256);
+    kernel<<<parts, GATHER ? kThreads + kGatherThreads : kThreads, smem, st>>>(a, part, joins, wait_limit_ns(), mx, my);
     SPC_LAUNCH_CHECK();
-    k_grouped_wgrad_join<BN><<<dim3(parts, kTileM / kJoinRows), kJoinRows * BN / 4, 0, st>>>(a, part, plan);
+    k_grouped_wgrad_join<BN><<<dim3(parts, kTileM / kJoinRows), kJoinRows * BN / 4, 0, st>>>(a, part, joins);
     SPC_LAUNCH_CHECK();
     return SPC_OK;
 }
@@ -454,7 +580,7 @@ spc_status pick(const GroupedWgradArgs& a, float* part, cudaStream_t st)
 
 }  // namespace
 
-int grouped_wgrad_parts() { return sm_count(); }
+int grouped_wgrad_parts() { return std::min(sm_count(), kMaxParts); }
 
 // Two parts of a tile for each CTA.
 size_t grouped_wgrad_tc_ws_bytes()

@@ -82,13 +82,13 @@ def test_row_segments_refusals(L):
     def f(ids=P(256), stride=1, n=4, s=2, seg=P(256), order=P(256), ws=P(256), nb=1 << 20):
         return L.spc_row_segments(ids, stride, n, s, seg, order, ws, nb, None)
 
-    assert f(n=-1) == INVALID and f(s=0) == INVALID and f(s=4097) == INVALID
+    assert f(n=-1) == INVALID and f(s=0) == INVALID and f(s=1025) == INVALID
     assert f(stride=0) == INVALID and f(ids=None) == INVALID and f(seg=None) == INVALID
     assert f(ids=P(258)) == INVALID and f(order=P(257)) == INVALID
     assert f(n=2 ** 31) == UNSUPPORTED and f(stride=2 ** 62) == UNSUPPORTED
     assert f(ws=None) == WORKSPACE and f(nb=4) == WORKSPACE
     assert L.spc_row_segments_workspace_size(-1, 2) == 0
-    assert L.spc_row_segments_workspace_size(5, 4097) == 0
+    assert L.spc_row_segments_workspace_size(5, 1025) == 0
     assert L.spc_row_segments_workspace_size(0, 1) > 0
 
 
@@ -140,7 +140,7 @@ def test_grouped_refusals(L):
         assert fwd(f=f, x=None) == INVALID and fwd(f=f, w=None) == INVALID and fwd(f=f, y=None) == INVALID
         assert fwd(f=f, seg=None) == INVALID and fwd(f=f, x=P(264)) == INVALID and fwd(f=f, w=P(264)) == INVALID
         assert fwd(f=f, m=-1) == INVALID and fwd(f=f, n=-1) == INVALID and fwd(f=f, ci=0) == INVALID
-        assert fwd(f=f, co=0) == INVALID and fwd(f=f, s=0) == INVALID and fwd(f=f, s=4097) == INVALID
+        assert fwd(f=f, co=0) == INVALID and fwd(f=f, s=0) == INVALID and fwd(f=f, s=1025) == INVALID
         assert fwd(f=f, dt=-1) == INVALID
         # an operand without a row list has a row for every position
         assert fwd(f=f, n=3) == INVALID
