@@ -188,21 +188,36 @@ k_grouped_tc(GroupedArgs a, uint64_t wait_ns, const __grid_constant__ CUtensorMa
         if constexpr (GATHER) {
             static_assert(CG == 1, "a pair's rows would have to arrive on the leader's barrier");
             const int e = tid - kThreads, piece = e & 7, r0 = e >> 3;
-            const uint8_t* in = static_cast<const uint8_t*>(a.in);
+            const uint8_t* in_base = static_cast<const uint8_t*>(a.in);
             const uint32_t off = (uint32_t)r0 * 128 + ((uint32_t)(piece ^ (r0 & 7)) << 4);
             uint32_t it = 0;
-            for (int32_t t = first; t < tiles && ok; t += step) {
-                const TileWalk::Tile k = walk.at(t);
-                if (k.g < 0) continue;
+            // the list entries of tile t, read one tile ahead and checked when they are used
+            // (-1 past the segment's end)
+            TileWalk ahead = walk;
+            auto entries = [&](int32_t t, int32_t (&v)[4], TileWalk::Tile& k) {
+                k = ahead.at(t);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int64_t p = k.lo + r0 + 32 * j;
+                    v[j] = p < k.hi && k.g >= 0 ? __ldg(a.in_rows + p) : -1;
+                }
+            };
+            int32_t entry[4] = {-1, -1, -1, -1}, after[4];
+            TileWalk::Tile k, k_after;
+            if (first < tiles) entries(first, entry, k);
+            for (int32_t t = first; t < tiles && ok; t += step, k = k_after) {
+                if (t + step < tiles) entries(t + step, after, k_after);
                 const uint8_t* src[4];
                 bool there[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const int64_t p = k.lo + r0 + 32 * j;
-                    const int64_t row = p < k.hi ? row_at(a.in_rows, p, a.in_n, a.status) : -1;
-                    there[j] = row >= 0;
-                    src[j] = in + ((there[j] ? row : 0) * a.k + piece * 8) * 2;
+                    const bool in = k.lo + r0 + 32 * j < k.hi && k.g >= 0;
+                    there[j] = in && entry[j] >= 0 && entry[j] < a.in_n;
+                    if (in && !there[j]) set_status(a.status, SPC_ERR_ROW_INDEX);
+                    src[j] = in_base + ((int64_t)(there[j] ? entry[j] : 0) * a.k + piece * 8) * 2;
+                    entry[j] = after[j];
                 }
+                if (k.g < 0) continue;
                 for (int c = 0; c < chunks; ++c, ++it) {
                     const int s = it % S::kStages;
                     if (it >= S::kStages) ok = ptx::mbar_wait(&empty[s], ((it / S::kStages) - 1) & 1, wait_ns);
@@ -212,7 +227,7 @@ k_grouped_tc(GroupedArgs a, uint64_t wait_ns, const __grid_constant__ CUtensorMa
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const bool take = there[j] && inside;
-                        ptx::cp_async16(dst + j * 32 * 128, take ? src[j] + (int64_t)c * kChunk * 2 : in, take ? 16u : 0u);
+                        ptx::cp_async16(dst + j * 32 * 128, take ? src[j] + (int64_t)c * kChunk * 2 : in_base, take ? 16u : 0u);
                     }
                     ptx::cp_async_arrive_noinc(&full[s]);
                 }

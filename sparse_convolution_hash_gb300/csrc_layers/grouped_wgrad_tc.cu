@@ -407,26 +407,33 @@ k_grouped_wgrad_tc(GroupedWgradArgs a, float* __restrict__ part, Join* __restric
                 const Piece p = walk.next();
                 if (p.lo == p.hi) continue;
                 const int c0 = p.tile / cols * kTileM + piece * 8, n0 = p.tile % cols * BN + piece * 8;
-                // the rows of thread e's two reduction indices of unit k (-1: zeros)
-                auto rows = [&](int k, int64_t (&xr)[2], int64_t (&yr)[2]) {
+                // the list entries of thread e's two reduction indices of unit k, read one
+                // unit ahead and checked when they are used
+                auto entries = [&](int k, int32_t (&xe)[2], int32_t (&ye)[2]) {
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         const int64_t r = p.lo + (int64_t)k * kUnit + r0 + 32 * j;
-                        xr[j] = yr[j] = -1;
-                        if (k < p.k1 && r < p.hi) {
-                            xr[j] = row_at(a.x_rows, r, a.n_x, a.status);
-                            yr[j] = row_at(a.y_rows, r, a.n_y, a.status);
-                            if (xr[j] < 0 || yr[j] < 0) xr[j] = yr[j] = -1;
-                        }
+                        const bool in = k < p.k1 && r < p.hi;
+                        xe[j] = !in ? -1 : a.x_rows ? __ldg(a.x_rows + r) : (int32_t)r;
+                        ye[j] = !in ? -1 : a.y_rows ? __ldg(a.y_rows + r) : (int32_t)r;
                     }
                 };
-                int64_t xr[2], yr[2], xn[2], yn[2];
-                rows(p.k0, xr, yr);
+                int32_t xe[2], ye[2], xn[2], yn[2];
+                entries(p.k0, xe, ye);
                 for (int k = p.k0; k < p.k1; ++k, ++it) {
-                    rows(k + 1, xn, yn);
+                    entries(k + 1, xn, yn);
                     const int s = it % S::kStages;
                     if (it >= S::kStages) ok = ptx::mbar_wait(&empty[s], ((it / S::kStages) - 1) & 1, wait_ns);
                     if (!ok) break;
+                    int64_t xr[2], yr[2];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const bool in = p.lo + (int64_t)k * kUnit + r0 + 32 * j < p.hi;
+                        const bool good = xe[j] >= 0 && xe[j] < a.n_x && ye[j] >= 0 && ye[j] < a.n_y;
+                        if (in && !good) set_status(a.status, SPC_ERR_ROW_INDEX);
+                        xr[j] = good ? xe[j] : -1;
+                        yr[j] = good ? ye[j] : -1;
+                    }
                     const uint32_t dst = ptx::smem_u32(smem + (size_t)s * S::kStage) + off;
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
@@ -442,8 +449,8 @@ k_grouped_wgrad_tc(GroupedWgradArgs a, float* __restrict__ part, Join* __restric
                             ptx::cp_async16(dst + S::kABytes + q * kAtom + j * 32 * 128,
                                             take ? dy + (yr[j] * a.cout + n0 + 64 * q) * 2 : dy, take ? 16u : 0u);
                         }
-                        xr[j] = xn[j];
-                        yr[j] = yn[j];
+                        xe[j] = xn[j];
+                        ye[j] = yn[j];
                     }
                     ptx::cp_async_arrive_noinc(&full[s]);
                 }
