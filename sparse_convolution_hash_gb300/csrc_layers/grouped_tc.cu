@@ -7,12 +7,13 @@
 //   warp 0 loads the stages: 64 of the reduction at a time, the rows as one TMA box,
 //     the weights as 3-D TMA boxes, so that what lies past a segment's weights
 //     reads as zeros, not as its neighbour's;
-//   with a row list, warps 6-13 copy the rows instead, 16 bytes per cp.async
+//   with a row list, warps 10-17 copy the rows instead, 16 bytes per cp.async
 //     (a TMA gather of four rows takes about 85 cycles whatever the rows, 128 rows per 1.4 us,
 //     a third of the pace of the MMAs; the copies keep up with them);
 //   warp 1 issues the MMAs into one of two fp32 accumulators in tensor memory;
-//   warps 2-5 empty the other one: round once, transpose through shared memory,
-//     store whole 128-byte row pieces.  Rows past the segment's end are not stored.
+//   warps 2-9 empty the other one: round once, transpose through shared memory,
+//     store 64-byte row pieces (two warps for each quarter of the rows: four did not keep up
+//     with reductions of 512).  Rows past the segment's end are not stored.
 // Every output row is written once, so results are run-to-run identical.
 //
 // Every wait is bounded by the library's wait limit; one that runs out sets
@@ -27,7 +28,8 @@ namespace spc {
 
 namespace {
 
-constexpr int kThreads = 192;
+constexpr int kEpilogueWarps = 8;
+constexpr int kThreads = 64 + kEpilogueWarps * 32;
 constexpr int kGatherWarps = 8, kGatherThreads = kGatherWarps * 32;
 constexpr int kChunk = 64;  // reduction elements per stage: 128-byte rows
 constexpr uint64_t kDrainNs = 200000000ull;  // bound of the waits for a CTA's own copies and MMAs
@@ -41,7 +43,7 @@ struct Shape {
     static constexpr int kStage = kABytes + kBBytes;
     static constexpr int kStages = 196608 / kStage;     // 192 KB of stages
     static constexpr int kTmemCols = 2 * BN;
-    static constexpr int kStaging = 4 * 32 * 128;       // a 32-row x 128-byte box per epilogue warp
+    static constexpr int kStaging = kEpilogueWarps * 32 * 64;  // a 32-row x 64-byte box per epilogue warp
     static size_t smem(int segments)
     {
         return 1024 + (size_t)kStages * kStage + kStaging + 8 * (2 * kStages + 4) + 16 + 4 * ((size_t)segments + 3);
@@ -79,7 +81,7 @@ k_grouped_tc(GroupedArgs a, uint64_t wait_ns, const __grid_constant__ CUtensorMa
         }
         for (int b = 0; b < 2; ++b) {
             ptx::mbar_init(&acc_full[b], 1);
-            ptx::mbar_init(&acc_empty[b], 4 * CG);
+            ptx::mbar_init(&acc_empty[b], kEpilogueWarps * CG);
         }
         ptx::mbar_init_fence();
         ptx::prefetch_tmap(&map_in);
@@ -208,10 +210,10 @@ k_grouped_tc(GroupedArgs a, uint64_t wait_ns, const __grid_constant__ CUtensorMa
             for (int32_t t = first; t < tiles && ok; t += step, k = k_after) {
                 if (t + step < tiles) entries(t + step, after, k_after);
                 const uint8_t* src[4];
-                bool there[4];
+                bool there[4], inside[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const bool in = k.lo + r0 + 32 * j < k.hi && k.g >= 0;
+                    const bool in = inside[j] = k.lo + r0 + 32 * j < k.hi && k.g >= 0;
                     there[j] = in && entry[j] >= 0 && entry[j] < a.in_n;
                     if (in && !there[j]) set_status(a.status, SPC_ERR_ROW_INDEX);
                     src[j] = in_base + ((int64_t)(there[j] ? entry[j] : 0) * a.k + piece * 8) * 2;
@@ -223,11 +225,12 @@ k_grouped_tc(GroupedArgs a, uint64_t wait_ns, const __grid_constant__ CUtensorMa
                     if (it >= S::kStages) ok = ptx::mbar_wait(&empty[s], ((it / S::kStages) - 1) & 1, wait_ns);
                     if (!ok) break;
                     const uint32_t dst = ptx::smem_u32(smem + (size_t)s * S::kStage) + off;
-                    const bool inside = c * kChunk + piece * 8 < a.k;
+                    const bool column = c * kChunk + piece * 8 < a.k;
+                    // rows past the segment's end are not stored: whatever stands in the stage will do
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const bool take = there[j] && inside;
-                        ptx::cp_async16(dst + j * 32 * 128, take ? src[j] + (int64_t)c * kChunk * 2 : in_base, take ? 16u : 0u);
+                        const bool take = there[j] && column;
+                        if (inside[j]) ptx::cp_async16(dst + j * 32 * 128, take ? src[j] + (int64_t)c * kChunk * 2 : in_base, take ? 16u : 0u);
                     }
                     ptx::cp_async_arrive_noinc(&full[s]);
                 }
@@ -238,7 +241,7 @@ k_grouped_tc(GroupedArgs a, uint64_t wait_ns, const __grid_constant__ CUtensorMa
     } else {
         // --------------------------------------------------------- epilogue
         const int quarter = warp & 3;
-        uint8_t* box = staging + (warp - 2) * (32 * 128);
+        uint8_t* box = staging + (warp - 2) * (32 * 64);
         T* out = static_cast<T*>(a.out);
         uint32_t n = 0;
         for (int32_t t = first; t < tiles && ok; t += step) {
@@ -255,33 +258,31 @@ k_grouped_tc(GroupedArgs a, uint64_t wait_ns, const __grid_constant__ CUtensorMa
                 ++n;
             }
 #pragma unroll 1
-            for (int c = 0; c < BN / 64; ++c) {
-                const int n0 = k.col * BN + c * 64;
+            for (int c = (warp - 2) >> 2; c < BN / 32; c += kEpilogueWarps / 4) {
+                const int n0 = k.col * BN + c * 32;
                 if (n0 >= a.n) break;
-                uint32_t v[64];
+                uint32_t v[32];
                 if (k.g >= 0) {
-                    const uint32_t ta = tmem + ((uint32_t)(quarter * 32) << 16) + b * BN + c * 64;
-                    ptx::tmem_ld32(ta, *reinterpret_cast<uint32_t(*)[32]>(v));
-                    ptx::tmem_ld32(ta + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
+                    ptx::tmem_ld32(tmem + ((uint32_t)(quarter * 32) << 16) + b * BN + c * 32, v);
                     ptx::tmem_ld_wait();
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 64; ++j) v[j] = 0u;
+                    for (int j = 0; j < 32; ++j) v[j] = 0u;
                 }
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
+                for (int j = 0; j < 4; ++j) {
                     alignas(16) T o[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) o[i] = elem<T>::from_f32(__uint_as_float(v[j * 8 + i]));
-                    *reinterpret_cast<uint4*>(box + lane * 128 + ((j ^ (lane & 7)) << 4)) = *reinterpret_cast<uint4*>(o);
+                    *reinterpret_cast<uint4*>(box + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) = *reinterpret_cast<uint4*>(o);
                 }
                 __syncwarp();
-                const int piece = lane & 7;
+                const int piece = lane & 3;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int rr = j * 4 + (lane >> 3);
+                for (int j = 0; j < 4; ++j) {
+                    const int rr = j * 8 + (lane >> 2);
                     const int32_t to = __shfl_sync(FULL_MASK, row, rr);
-                    const uint4 w = *reinterpret_cast<const uint4*>(box + rr * 128 + ((piece ^ (rr & 7)) << 4));
+                    const uint4 w = *reinterpret_cast<const uint4*>(box + rr * 64 + ((piece ^ ((rr >> 1) & 3)) << 4));
                     if (to >= 0 && n0 + piece * 8 < a.n)
                         __stcs(reinterpret_cast<uint4*>(out + (int64_t)to * a.n + n0 + piece * 8), w);
                 }
@@ -354,11 +355,28 @@ spc_status launch(const GroupedArgs& a, cudaStream_t st)
 }
 
 template <typename T, int CG, int BN>
-spc_status pick(const GroupedArgs& a, cudaStream_t st)
+spc_status pick_operands(const GroupedArgs& a, cudaStream_t st)
 {
     if constexpr (CG == 1)
         if (a.in_rows) return a.w_transposed ? launch<T, CG, BN, false, true>(a, st) : launch<T, CG, BN, true, true>(a, st);
     return a.w_transposed ? launch<T, CG, BN, false, false>(a, st) : launch<T, CG, BN, true, false>(a, st);
+}
+
+// The tile.  256 x 256 by a pair of CTAs halves what each loads of the weights, but half a
+// tile of every segment is empty and its two epilogues have less time: it pays from about 2048 rows
+// a segment and reductions of 512 on (bf16, 16 segments of 2048, 1024 -> 4096: 186 us
+// against 199; one segment of 32,768: 168 against 186; 64 of 780, 1024 -> 256: 38 against 33; one of
+// 398,833, 128 -> 256: 75 against 59).  128 x 128 where 128 x 256 would leave columns empty or
+// make fewer tiles than there are SMs (398,833 x 128 -> 128: 40 us against 48; 8 segments of 256,
+// 512 -> 512: 7.8 against 9.1); a segment has a tile however few its rows, and few rows of many
+// segments run at the pace of the weights, better in wide tiles (32 rows of 64: 40 against 48).
+template <typename T>
+spc_status pick(const GroupedArgs& a, cudaStream_t st)
+{
+    const int64_t row_tiles = std::max<int64_t>(ceil_div(a.m, 128), std::min<int64_t>(a.m, a.segments));
+    if (a.n <= 128 || ceil_div(a.n, 256) * row_tiles < sm_count()) return pick_operands<T, 1, 128>(a, st);
+    if (!a.in_rows && a.k >= 512 && a.m / a.segments >= 2048) return pick_operands<T, 2, 256>(a, st);
+    return pick_operands<T, 1, 256>(a, st);
 }
 
 }  // namespace
@@ -372,8 +390,7 @@ bool grouped_tc_supported(int32_t k, int32_t n, int64_t in_n, spc_dtype dt)
 spc_status grouped_tc(const GroupedArgs& a, spc_dtype dt, cudaStream_t st)
 {
     if (ceil_div(a.n, 64) * (a.m / 128 + a.segments + 2) > INT32_MAX) return SPC_ERR_UNSUPPORTED;
-    if (dt == SPC_F16) return pick<__half, 1, 256>(a, st);
-    return pick<__nv_bfloat16, 1, 256>(a, st);
+    return dt == SPC_F16 ? pick<__half>(a, st) : pick<__nv_bfloat16>(a, st);
 }
 
 }  // namespace spc
