@@ -1,0 +1,1110 @@
+// group_norm.cuh -- group norm with an activation over the rows of each segment,
+// and its gradients; one translation unit per element type instantiates it.
+//
+// Both passes need sums over a segment before they can write a row, so each reads its
+// rows twice: a first kernel forms sums, a second applies them, walking its rows
+// backwards so that it meets the ones the first kernel read last while they are still in
+// L2.  One CTA per SM owns a run of consecutive positions in both.  A thread owns
+// V neighbouring channels (16 bytes where the row length allows) of every rt-th row, keeps
+// their parameters in registers and works on them in pairs (f32x2 instructions: the loops are
+// bound by issue slots before anything else).  The CTAs' sums over a segment
+// that several share go to the workspace, and every CTA that needs them
+// adds them in the order of the rows; a segment inside one CTA's run is finished there.
+//
+// Statistics: a thread sums d = x - p and d^2 around its own first value p, so a mean far
+// from zero costs no digits; threads, channels and CTAs are merged as (count, mean,
+// sum of squares around the mean), M2 = sum M2_i + sum n_i (mean_i - mean)^2.
+// Gradients: with dz = dy act'(z), sums of dz and dz (x - mean) per channel give dgamma,
+// dbeta and, weighted by gamma, the two means of a group; dx = A dz + B + D (x - mean).
+#pragma once
+
+#include <string.h>
+
+#include <type_traits>
+
+#include "layers.cuh"
+
+namespace spc {
+
+namespace {
+
+constexpr int kBlock = 256;      // of the kernels for very long rows
+constexpr int kThreads = 512;    // of the others
+constexpr int kUnroll = 4;       // rows of a thread in a group
+constexpr int kDepth = 3;        // groups in flight
+constexpr int kMinRows = 64;     // positions of a CTA, at least
+
+template <typename T, int V>
+struct alignas(sizeof(T) * V) Vec {
+    T e[V];
+};
+
+// ------------------------------------------------------------------ pairs of fp32
+struct F2 {
+    float x, y;
+};
+__device__ __forceinline__ uint64_t bits(F2 a)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
+    return r;
+}
+__device__ __forceinline__ F2 pair(uint64_t r)
+{
+    F2 a;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a.x), "=f"(a.y) : "l"(r));
+    return a;
+}
+__device__ __forceinline__ F2 both(float v) { return F2{v, v}; }
+__device__ __forceinline__ F2 add(F2 a, F2 b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
+    return pair(r);
+}
+__device__ __forceinline__ F2 mul(F2 a, F2 b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)));
+    return pair(r);
+}
+__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
+    return pair(r);
+}
+
+template <int V> constexpr int kPairs = (V + 1) / 2;  // a single channel is the first of a pair
+
+template <typename T, int V>
+__device__ __forceinline__ void unpack(const Vec<T, V>& v, F2 (&f)[kPairs<V>])
+{
+    if constexpr (V == 1) {
+        f[0] = F2{elem<T>::to_f32(v.e[0]), 0.f};
+    } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) f[j] = F2{elem<T>::to_f32(v.e[2 * j]), elem<T>::to_f32(v.e[2 * j + 1])};
+    } else {
+        uint32_t w[V / 2];
+        memcpy(w, v.e, sizeof(w));
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) {
+            if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+                f[j] = F2{__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u)};
+            } else {
+                __half2 h;
+                memcpy(&h, &w[j], 4);
+                const float2 g = __half22float2(h);
+                f[j] = F2{g.x, g.y};
+            }
+        }
+    }
+}
+
+template <typename T, int V>
+__device__ __forceinline__ Vec<T, V> pack(const F2 (&f)[kPairs<V>])
+{
+    Vec<T, V> v;
+    if constexpr (V == 1) {
+        v.e[0] = elem<T>::from_f32(f[0].x);
+    } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) {
+            v.e[2 * j] = elem<T>::from_f32(f[j].x);
+            v.e[2 * j + 1] = elem<T>::from_f32(f[j].y);
+        }
+    } else {
+        uint32_t w[V / 2];
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) {
+            if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(f[j].x, f[j].y);
+                memcpy(&w[j], &h, 4);
+            } else {
+                const __half2 h = __floats2half2_rn(f[j].x, f[j].y);
+                memcpy(&w[j], &h, 4);
+            }
+        }
+        memcpy(v.e, w, sizeof(w));
+    }
+    return v;
+}
+
+// A per-channel table as pairs.
+template <int V, typename F>
+__device__ __forceinline__ void gather_pairs(F2 (&f)[kPairs<V>], F value)
+{
+#pragma unroll
+    for (int j = 0; j < kPairs<V>; ++j) f[j] = F2{value(2 * j), 2 * j + 1 < V ? value(2 * j + 1) : 0.f};
+}
+
+// ------------------------------------------------------------------- activations
+// 1 / (1 + exp(-z)) with the hardware's exp2 and reciprocal: within 2^-19 for the |z| of a
+// normalised feature, a small part of the rounding of a 16-bit output (the exact functions cost
+// the 498,145 x 64 bf16 forward 95 us against 82, all else equal).
+__device__ __forceinline__ F2 sigmoid(F2 z)
+{
+    const F2 t = mul(z, both(-1.4426950408889634f));
+    F2 e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
+    e = add(e, both(1.f));
+    F2 s;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.x) : "f"(e.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.y) : "f"(e.y));
+    return s;
+}
+
+// SILU, or max(z, floor): floor 0 for RELU, -infinity for none (a NaN passes).
+template <bool SILU>
+__device__ __forceinline__ F2 activate(F2 z, float floor)
+{
+    if (SILU) return mul(z, sigmoid(z));
+    return F2{z.x < floor ? floor : z.x, z.y < floor ? floor : z.y};
+}
+
+// dy act'(z); least: the smallest z of slope 1 (RELU: the least positive number).
+template <bool SILU>
+__device__ __forceinline__ F2 through(F2 dy, F2 z, float least)
+{
+    if (SILU) {
+        const F2 s = sigmoid(z);
+        const F2 rest = fma(s, both(-1.f), both(1.f));
+        return mul(dy, mul(s, fma(z, rest, both(1.f))));
+    }
+    return F2{z.x < least ? 0.f : z.x != z.x ? z.x : dy.x, z.y < least ? 0.f : z.y != z.y ? z.y : dy.y};
+}
+__device__ __forceinline__ float floor_of(int act) { return act == SPC_ACT_RELU ? 0.f : -INFINITY; }
+__device__ __forceinline__ float least_of(int act) { return act == SPC_ACT_RELU ? __int_as_float(1) : -INFINITY; }
+
+// The same for the kernels that take one element at a time.
+__device__ __forceinline__ float activate(float z, int act)
+{
+    return act == SPC_ACT_SILU ? activate<true>(both(z), 0.f).x : activate<false>(both(z), floor_of(act)).x;
+}
+__device__ __forceinline__ float slope(float z, int act)
+{
+    return act == SPC_ACT_SILU ? through<true>(both(1.f), both(z), 0.f).x : through<false>(both(1.f), both(z), least_of(act)).x;
+}
+
+__device__ __forceinline__ float block_sum(float v)
+{
+    __shared__ float s[kBlock / 32];
+#pragma unroll
+    for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(FULL_MASK, v, d);
+    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
+    __syncthreads();
+    float t = 0.f;
+#pragma unroll
+    for (int w = 0; w < kBlock / 32; ++w) t += s[w];
+    __syncthreads();
+    return t;
+}
+
+// ------------------------------------------------- runs of consecutive positions
+// The offsets, in shared memory, inside [0, n]; what is out of range or order is reported.
+__device__ __forceinline__ void load_offsets(const NormArgs& a, int32_t* s_seg, bool report)
+{
+    for (int s = threadIdx.x; s <= a.segments; s += (int)blockDim.x) {
+        const int32_t v = __ldg(a.seg + s);
+        s_seg[s] = v < 0 ? 0 : (v > a.n ? (int32_t)a.n : v);
+        if (report && (v < 0 || v > a.n || (s < a.segments && __ldg(a.seg + s + 1) < v)))
+            set_status(a.status, SPC_ERR_ROW_INDEX);
+    }
+    __syncthreads();
+}
+
+// The last s with seg[s] <= r: the segment of position r, -1 before the first, `segments` from
+// the last offset on.
+__device__ __forceinline__ int find_segment(const int32_t* s_seg, int segments, int64_t r)
+{
+    int lo = 0, hi = segments + 1;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (s_seg[mid] > r) hi = mid;
+        else lo = mid + 1;
+    }
+    return lo - 1;
+}
+
+struct Run {
+    int s;           // segment, -1: none
+    int64_t lo, hi;  // its positions in this CTA's share
+};
+
+// The run that begins at position r of a share that ends at `end`.
+__device__ __forceinline__ Run run_at(const NormArgs& a, const int32_t* s_seg, int64_t r, int64_t end)
+{
+    Run k;
+    k.s = find_segment(s_seg, a.segments, r);
+    int64_t to = k.s >= a.segments ? a.n : s_seg[k.s + 1];
+    if (k.s >= a.segments) k.s = -1;
+    to = to > r ? to : r + 1;  // offsets out of order: still forward
+    k.lo = r;
+    k.hi = to < end ? to : end;
+    return k;
+}
+
+// The run that ends before position `end` of a share that begins at `begin`.
+__device__ __forceinline__ Run run_before(const NormArgs& a, const int32_t* s_seg, int64_t begin, int64_t end)
+{
+    Run k;
+    k.s = find_segment(s_seg, a.segments, end - 1);
+    int64_t from = k.s < 0 ? 0 : s_seg[k.s >= a.segments ? a.segments : k.s];
+    if (k.s >= a.segments) k.s = -1;
+    from = from < end ? from : end - 1;
+    k.hi = end;
+    k.lo = from > begin ? from : begin;
+    return k;
+}
+
+// Segment s over shares of `rows` positions: shares first .. last hold a part of it.
+struct Span {
+    int64_t lo, hi;
+    int first, last;
+    __device__ __forceinline__ Span(const int32_t* s_seg, int s, int64_t rows)
+    {
+        lo = s_seg[s];
+        hi = s_seg[s + 1] > lo ? s_seg[s + 1] : lo;
+        first = (int)(lo / rows);
+        last = hi > lo ? (int)((hi - 1) / rows) : first;
+    }
+    __device__ __forceinline__ int64_t count(int c, int64_t rows) const
+    {
+        const int64_t b = c * rows > lo ? c * rows : lo, e = (c + 1) * rows < hi ? (c + 1) * rows : hi;
+        return e - b;
+    }
+    // a share's part stands in its first slot if it begins with the share, else in its second
+    __device__ __forceinline__ int slot(int c, int64_t rows) const { return 2 * c + (c == first && lo > c * rows ? 1 : 0); }
+};
+
+// ------------------------------------------------------------ rows in flight
+// A thread's own vectors of every step-th position of a run of N tensors: asynchronous copies into
+// slots of shared memory that only this thread reads, kDepth groups of
+// kUnroll rows ahead of their use, so no barrier stands between memory and arithmetic.
+template <typename T, int V, int N>
+struct Stream {
+    static constexpr int kBytes = sizeof(T) * V;
+    static constexpr size_t kSmem = (size_t)kDepth * kUnroll * N * kThreads * kBytes;
+    const T* src[N];
+    const int32_t* order;
+    int32_t* status;
+    Vec<T, V>* slots;        // [kDepth * kUnroll][N][kThreads]
+    int32_t rows, c;
+    int32_t next, lo, hi;    // next position to ask for, of [lo, hi)
+    int32_t at, step;        // first position of the group in hand
+    int in, out;             // ring places
+    int32_t entry[kUnroll];  // rows of the group at `next`, -1: none
+
+    __device__ __forceinline__ Stream(const NormArgs& a, void* s)
+        : order(a.order), status(a.status), slots(static_cast<Vec<T, V>*>(s) + threadIdx.x), rows((int32_t)a.n), c(a.c)
+    {
+    }
+    __device__ __forceinline__ bool there(int32_t p) const { return (uint32_t)(p - lo) < (uint32_t)(hi - lo); }
+    __device__ __forceinline__ int32_t row_of(int32_t p) const { return !there(p) ? -1 : order ? __ldg(order + p) : p; }
+    __device__ __forceinline__ void ask()
+    {
+#pragma unroll
+        for (int q = 0; q < kUnroll; ++q) {
+            if ((uint32_t)entry[q] < (uint32_t)rows) {
+#pragma unroll
+                for (int t = 0; t < N; ++t) {
+                    Vec<T, V>* d = slots + ((in * kUnroll + q) * N + t) * kThreads;
+                    const T* g = src[t] + (int64_t)entry[q] * c;
+                    if constexpr (kBytes >= 4)
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(
+                                         (uint32_t)__cvta_generic_to_shared(d)), "l"(g), "n"(kBytes) : "memory");
+                    else
+                        *d = *reinterpret_cast<const Vec<T, V>*>(g);
+                }
+            } else if (entry[q] != -1 || (order && there(next + q * step))) {
+                set_status(status, SPC_ERR_ROW_INDEX);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        in = in + 1 == kDepth ? 0 : in + 1;
+        next += kUnroll * step;
+#pragma unroll
+        for (int q = 0; q < kUnroll; ++q) entry[q] = row_of(next + q * step);
+    }
+    // Starts on positions [lo, hi): from `first` on, `step` apart.
+    __device__ __forceinline__ void begin(int64_t first, int step_, int64_t lo_, int64_t hi_)
+    {
+        next = at = (int32_t)first;
+        step = step_;
+        lo = (int32_t)lo_;
+        hi = (int32_t)hi_;
+        in = out = 0;
+#pragma unroll
+        for (int q = 0; q < kUnroll; ++q) entry[q] = row_of(next + q * step);
+#pragma unroll
+        for (int d = 0; d < kDepth; ++d) ask();
+    }
+    __device__ __forceinline__ bool more() const { return there(at); }
+    __device__ __forceinline__ void wait() const { asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory"); }
+    // Row q of the group in hand, or -1.
+    __device__ __forceinline__ int32_t row(int q) const
+    {
+        const int32_t r = row_of(at + q * step);
+        return (uint32_t)r < (uint32_t)rows ? r : -1;
+    }
+    __device__ __forceinline__ void get(int q, int t, F2 (&f)[kPairs<V>]) const
+    {
+        unpack<T, V>(slots[((out * kUnroll + q) * N + t) * kThreads], f);
+    }
+    // The group in hand is done with: asks for the one kDepth groups on.
+    __device__ __forceinline__ void advance()
+    {
+        ask();
+        out = out + 1 == kDepth ? 0 : out + 1;
+        at += kUnroll * step;
+    }
+};
+
+// ------------------------------------------------------------------ column sums
+// Sums over the rt row threads of N values per channel: afterwards value k of channel ch
+// stands at column_at<V>(k, ch).  Planes of up to four channels keep the accesses whole.
+template <int V> constexpr int kPart = V >= 4 ? 4 : V;
+template <int V>
+__device__ __forceinline__ int column_at(int k, int ch)
+{
+    return ((k * (V / kPart<V>) + ch % V / kPart<V>) * kThreads + ch / V) * kPart<V> + ch % kPart<V>;
+}
+template <int V, int N>
+__device__ __forceinline__ void column_sums(const F2 (&v)[N][kPairs<V>], float* s, int tr, int rt, int vpr)
+{
+    constexpr int P = kPart<V>, H = V / P;
+    using W = Vec<float, P>;
+    W* w = reinterpret_cast<W*>(s);
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+            W u;
+#pragma unroll
+            for (int j = 0; j < P; ++j) {
+                const F2 f = v[k][(h * P + j) / 2];
+                u.e[j] = (h * P + j) % 2 ? f.y : f.x;
+            }
+            w[(k * H + h) * kThreads + threadIdx.x] = u;
+        }
+    int half = 1;
+    while (half < rt) half <<= 1;
+    for (half >>= 1; half; half >>= 1) {
+        __syncthreads();
+        if (tr < half && tr + half < rt)
+#pragma unroll
+            for (int k = 0; k < N * H; ++k) {
+                W a = w[k * kThreads + threadIdx.x];
+                const W b = w[k * kThreads + threadIdx.x + half * vpr];
+#pragma unroll
+                for (int j = 0; j < P; ++j) a.e[j] += b.e[j];
+                w[k * kThreads + threadIdx.x] = a;
+            }
+    }
+    __syncthreads();
+}
+
+__device__ __forceinline__ float warp_sum(float v)
+{
+#pragma unroll
+    for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(FULL_MASK, v, d);
+    return v;
+}
+
+// Of a pass's two kernels the second may be launched while the first still runs.
+__device__ __forceinline__ void wait_for_first_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// What the two kernels of a pass hand over.
+struct Ws {
+    float2* part;   // [2 shares][groups] sums over a shared segment's parts
+    float2* coef;   // [segments][groups] sums over the segments inside one share
+    float* total;   // [shares][2][c] sums over a share
+};
+
+// Thread tid's place: vector tv of every rt-th row from row tr on.
+template <int V>
+struct Place {
+    int vpr, rt, tr, tv, per, warp, lane;
+    int64_t begin, end;  // positions of this CTA
+    __device__ __forceinline__ Place(const NormArgs& a, int64_t rows)
+    {
+        const int tid = threadIdx.x;
+        vpr = a.c / V;
+        rt = kThreads / vpr;
+        tr = tid / vpr;
+        tv = tid % vpr;
+        per = a.c / a.groups;
+        warp = tid >> 5;
+        lane = tid & 31;
+        begin = blockIdx.x * rows;
+        end = begin + rows < a.n ? begin + rows : a.n;
+    }
+};
+
+// ------------------------------------------------------------------- statistics
+// part[slot][g] = (mean, M2) of a shared segment's part; whole segments end in mean, rstd.
+template <typename T, int V>
+__global__ void __launch_bounds__(kThreads, 1) k_norm_stats(NormArgs a, int64_t rows, Ws w)
+{
+    extern __shared__ __align__(16) uint8_t s_raw[];
+    using S = Stream<T, V, 1>;
+    float* s_sum = reinterpret_cast<float*>(s_raw);  // the slots, once a run's rows are in
+    float* s_mean = reinterpret_cast<float*>(s_raw + S::kSmem);
+    int32_t* s_seg = reinterpret_cast<int32_t*>(s_mean + a.c);
+    const Place<V> at(a, rows);
+    const bool works = at.tr < at.rt;
+    S in(a, s_raw);
+    in.src[0] = static_cast<const T*>(a.x) + at.tv * V;
+    load_offsets(a, s_seg, blockIdx.x == 0);
+    // empty segments are finished here, a block each in turn
+    for (int s = blockIdx.x; s < a.segments; s += gridDim.x)
+        if (s_seg[s] >= s_seg[s + 1])
+            for (int g = threadIdx.x; g < a.groups; g += kThreads) {
+                a.mean[(int64_t)s * a.groups + g] = 0.f;
+                a.rstd[(int64_t)s * a.groups + g] = 1.f / sqrtf(a.eps);
+            }
+    for (int64_t r0 = at.begin; r0 < at.end;) {
+        const Run k = run_at(a, s_seg, r0, at.end);
+        r0 = k.hi;
+        if (k.s < 0) continue;
+        F2 pivot[kPairs<V>], s1[kPairs<V>], s2[kPairs<V>], base[kPairs<V>];
+#pragma unroll
+        for (int j = 0; j < kPairs<V>; ++j) pivot[j] = s1[j] = s2[j] = base[j] = both(0.f);
+        int count = 0;
+        if (works) {
+            in.begin(k.lo + at.tr, at.rt, k.lo, k.hi);
+            // the run's first row, around which the threads' sums are brought together
+            const int64_t row0 = row_at(a.order, k.lo, a.n, nullptr);
+            if (row0 >= 0) unpack<T, V>(*reinterpret_cast<const Vec<T, V>*>(in.src[0] + row0 * a.c), base);
+            in.wait();
+            if (in.row(0) >= 0) in.get(0, 0, pivot);  // out of range: 0
+            F2 minus[kPairs<V>];
+#pragma unroll
+            for (int j = 0; j < kPairs<V>; ++j) minus[j] = F2{-pivot[j].x, -pivot[j].y};
+            for (; in.more(); in.advance()) {
+                in.wait();
+#pragma unroll
+                for (int q = 0; q < kUnroll; ++q)
+                    if (in.row(q) >= 0) {
+                        F2 f[kPairs<V>];
+                        in.get(q, 0, f);
+                        ++count;
+#pragma unroll
+                        for (int j = 0; j < kPairs<V>; ++j) {
+                            const F2 d = add(f[j], minus[j]);
+                            s1[j] = add(s1[j], d);
+                            s2[j] = fma(d, d, s2[j]);
+                        }
+                    }
+            }
+        }
+        // channel means around the run's first row, then squares around the channel means
+        const float n = (float)(k.hi - k.lo), mine = (float)count;
+        F2 v[1][kPairs<V>];
+#pragma unroll
+        for (int j = 0; j < kPairs<V>; ++j)
+            v[0][j] = F2{fmaf(mine, pivot[j].x - base[j].x, s1[j].x), fmaf(mine, pivot[j].y - base[j].y, s1[j].y)};
+        column_sums<V, 1>(v, s_sum, at.tr, at.rt, at.vpr);
+        if (at.tr == 0)
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float b = j % 2 ? base[j / 2].y : base[j / 2].x;
+                s_mean[at.tv * V + j] = b + s_sum[column_at<V>(0, at.tv * V + j)] / n;
+            }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kPairs<V>; ++j) v[0][j] = both(0.f);
+        if (works && count) {
+            auto square = [&](float p, float a1, float a2, int ch) -> float {
+                const float m = a1 / mine, d = (p - s_mean[ch]) + m, m2 = fmaf(-m, a1, a2);
+                return (m2 < 0.f ? 0.f : m2) + mine * d * d;
+            };
+#pragma unroll
+            for (int j = 0; j < kPairs<V>; ++j) {
+                v[0][j].x = square(pivot[j].x, s1[j].x, s2[j].x, at.tv * V + 2 * j);
+                if (2 * j + 1 < V) v[0][j].y = square(pivot[j].y, s1[j].y, s2[j].y, at.tv * V + 2 * j + 1);
+            }
+        }
+        column_sums<V, 1>(v, s_sum, at.tr, at.rt, at.vpr);
+        // channels to groups, a warp each
+        const Span span(s_seg, k.s, rows);
+        for (int g = at.warp; g < a.groups; g += kThreads / 32) {
+            const int ch0 = g * at.per;
+            const float first = s_mean[ch0];
+            float m = 0.f;
+            for (int j = at.lane; j < at.per; j += 32) m += s_mean[ch0 + j] - first;
+            const float mean = first + warp_sum(m) / (float)at.per;
+            float q = 0.f;
+            for (int j = at.lane; j < at.per; j += 32) {
+                const float d = s_mean[ch0 + j] - mean;
+                q += s_sum[column_at<V>(0, ch0 + j)] + n * d * d;
+            }
+            q = warp_sum(q);
+            if (at.lane == 0) {
+                if (span.first == span.last) {
+                    a.mean[(int64_t)k.s * a.groups + g] = mean;
+                    a.rstd[(int64_t)k.s * a.groups + g] = 1.f / sqrtf(q / (n * (float)at.per) + a.eps);
+                } else {
+                    w.part[(int64_t)span.slot(blockIdx.x, rows) * a.groups + g] = make_float2(mean, q);
+                }
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// (mean, rstd) of segment s into s_stat [groups], from the parts where several CTAs
+// share it; the CTA that holds its first position also writes them out.
+__device__ __forceinline__ void join_stats(const NormArgs& a, const int32_t* s_seg, int s, int64_t rows, const float2* part,
+                                           float2* s_stat)
+{
+    const Span span(s_seg, s, rows);
+    const int per = a.c / a.groups, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    __syncthreads();
+    for (int g = warp; g < a.groups; g += kThreads / 32) {
+        float mean, rstd;
+        if (span.first == span.last) {
+            mean = a.mean[(int64_t)s * a.groups + g];
+            rstd = a.rstd[(int64_t)s * a.groups + g];
+        } else {
+            constexpr int kKeep = 5;  // parts of a lane kept in registers: 160 CTAs
+            float2 v[kKeep];
+            float cnt[kKeep];
+#pragma unroll
+            for (int i = 0; i < kKeep; ++i) {
+                const int c = span.first + lane + 32 * i;
+                v[i] = make_float2(0.f, 0.f);
+                cnt[i] = 0.f;
+                if (c <= span.last) {
+                    v[i] = part[(int64_t)span.slot(c, rows) * a.groups + g];
+                    cnt[i] = (float)span.count(c, rows);
+                }
+            }
+            const float base = __shfl_sync(FULL_MASK, v[0].x, 0);
+            float m = 0.f;
+#pragma unroll
+            for (int i = 0; i < kKeep; ++i) m += cnt[i] > 0.f ? cnt[i] * (v[i].x - base) : 0.f;
+            for (int c = span.first + lane + 32 * kKeep; c <= span.last; c += 32)
+                m += (float)span.count(c, rows) * (part[(int64_t)span.slot(c, rows) * a.groups + g].x - base);
+            const float n = (float)(span.hi - span.lo);
+            mean = base + warp_sum(m) / n;
+            float q = 0.f;
+#pragma unroll
+            for (int i = 0; i < kKeep; ++i) {
+                const float d = v[i].x - mean;
+                q += cnt[i] > 0.f ? v[i].y + cnt[i] * (float)per * d * d : 0.f;
+            }
+            for (int c = span.first + lane + 32 * kKeep; c <= span.last; c += 32) {
+                const float2 u = part[(int64_t)span.slot(c, rows) * a.groups + g];
+                const float d = u.x - mean;
+                q += u.y + (float)span.count(c, rows) * (float)per * d * d;
+            }
+            rstd = 1.f / sqrtf(warp_sum(q) / (n * (float)per) + a.eps);
+            if (lane == 0 && (int)blockIdx.x == span.first) {
+                a.mean[(int64_t)s * a.groups + g] = mean;
+                a.rstd[(int64_t)s * a.groups + g] = rstd;
+            }
+        }
+        if (lane == 0) s_stat[g] = make_float2(mean, rstd);
+    }
+    __syncthreads();
+}
+
+template <typename T, int V, bool SILU>
+__global__ void __launch_bounds__(kThreads, 1) k_norm_apply(NormArgs a, int64_t rows, Ws w)
+{
+    extern __shared__ __align__(16) uint8_t s_raw[];
+    using S = Stream<T, V, 1>;
+    float2* s_stat = reinterpret_cast<float2*>(s_raw + S::kSmem);
+    int32_t* s_seg = reinterpret_cast<int32_t*>(s_stat + a.groups);
+    const Place<V> at(a, rows);
+    const bool works = at.tr < at.rt;
+    T* y = static_cast<T*>(a.out) + at.tv * V;
+    S in(a, s_raw);
+    in.src[0] = static_cast<const T*>(a.x) + at.tv * V;
+    load_offsets(a, s_seg, false);
+    const float floor = floor_of(a.act);
+    bool waited = false;
+    for (int64_t r0 = at.end; r0 > at.begin;) {
+        const Run k = run_before(a, s_seg, at.begin, r0);
+        r0 = k.lo;
+        if (k.s < 0) {
+            F2 zero[kPairs<V>];
+#pragma unroll
+            for (int j = 0; j < kPairs<V>; ++j) zero[j] = both(0.f);
+            if (works)
+                for (int64_t r = k.lo + at.tr; r < k.hi; r += at.rt) {
+                    const int64_t row = row_at(a.order, r, a.n, a.status);
+                    if (row >= 0) *reinterpret_cast<Vec<T, V>*>(y + row * a.c) = pack<T, V>(zero);
+                }
+            continue;
+        }
+        if (works) in.begin(k.hi - 1 - at.tr, -at.rt, k.lo, k.hi);  // on their way meanwhile
+        if (!waited) wait_for_first_kernel();
+        waited = true;
+        join_stats(a, s_seg, k.s, rows, w.part, s_stat);
+        if (!works) continue;
+        F2 minus[kPairs<V>], scale[kPairs<V>], shift[kPairs<V>];
+        gather_pairs<V>(scale, [&](int j) {
+            const int ch = at.tv * V + j;
+            return s_stat[ch / at.per].y * (a.gamma ? __ldg(a.gamma + ch) : 1.f);
+        });
+        // the mean is taken off first: a constant channel gives beta exactly
+        gather_pairs<V>(minus, [&](int j) { return -s_stat[(at.tv * V + j) / at.per].x; });
+        gather_pairs<V>(shift, [&](int j) { return a.beta ? __ldg(a.beta + at.tv * V + j) : 0.f; });
+        for (; in.more(); in.advance()) {
+            in.wait();
+#pragma unroll
+            for (int q = 0; q < kUnroll; ++q) {
+                const int32_t row = in.row(q);
+                if (row < 0) continue;
+                F2 f[kPairs<V>];
+                in.get(q, 0, f);
+#pragma unroll
+                for (int j = 0; j < kPairs<V>; ++j) f[j] = activate<SILU>(fma(add(f[j], minus[j]), scale[j], shift[j]), floor);
+                *reinterpret_cast<Vec<T, V>*>(y + (int64_t)row * a.c) = pack<T, V>(f);
+            }
+        }
+    }
+    if (!waited) wait_for_first_kernel();
+}
+
+// -------------------------------------------------------------------- gradients
+// Sums over the rows of this CTA: total[c][0] of dz and [1] of dz xh per channel, and per segment
+// and group (sum gamma dz, sum gamma dz xh): whole segments' in coef[s], parts in part[slot].
+template <typename T, int V, bool SILU>
+__global__ void __launch_bounds__(kThreads, 1) k_norm_bwd_sums(NormArgs a, int64_t rows, Ws w)
+{
+    extern __shared__ __align__(16) uint8_t s_raw[];
+    using S = Stream<T, V, 2>;
+    float* s_sum = reinterpret_cast<float*>(s_raw);  // the slots, once a run's rows are in
+    int32_t* s_seg = reinterpret_cast<int32_t*>(s_raw + S::kSmem);
+    const Place<V> at(a, rows);
+    const bool works = at.tr < at.rt;
+    S in(a, s_raw);
+    in.src[0] = static_cast<const T*>(a.x) + at.tv * V;
+    in.src[1] = static_cast<const T*>(a.dy) + at.tv * V;
+    load_offsets(a, s_seg, blockIdx.x == 0);
+    const float least = least_of(a.act);
+    float all[2][V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) all[0][j] = all[1][j] = 0.f;
+    for (int64_t r0 = at.begin; r0 < at.end;) {
+        const Run k = run_at(a, s_seg, r0, at.end);
+        r0 = k.hi;
+        if (k.s < 0) continue;
+        F2 minus[kPairs<V>], scale[kPairs<V>], shift[kPairs<V>], sum[2][kPairs<V>];
+#pragma unroll
+        for (int j = 0; j < kPairs<V>; ++j) sum[0][j] = sum[1][j] = both(0.f);
+        if (works) {
+            in.begin(k.lo + at.tr, at.rt, k.lo, k.hi);
+            const float* mean = a.mean + (int64_t)k.s * a.groups;
+            const float* rstd = a.rstd + (int64_t)k.s * a.groups;
+            gather_pairs<V>(minus, [&](int j) { return -__ldg(mean + (at.tv * V + j) / at.per); });
+            gather_pairs<V>(scale, [&](int j) {
+                const int ch = at.tv * V + j;
+                return __ldg(rstd + ch / at.per) * (a.gamma ? __ldg(a.gamma + ch) : 1.f);
+            });
+            gather_pairs<V>(shift, [&](int j) { return a.beta ? __ldg(a.beta + at.tv * V + j) : 0.f; });
+            for (; in.more(); in.advance()) {
+                in.wait();
+#pragma unroll
+                for (int q = 0; q < kUnroll; ++q) {
+                    if (in.row(q) < 0) continue;
+                    F2 f[kPairs<V>], d[kPairs<V>];
+                    in.get(q, 0, f);
+                    in.get(q, 1, d);
+#pragma unroll
+                    for (int j = 0; j < kPairs<V>; ++j) {
+                        const F2 e = add(f[j], minus[j]);
+                        const F2 dz = through<SILU>(d[j], fma(e, scale[j], shift[j]), least);
+                        sum[0][j] = add(sum[0][j], dz);
+                        sum[1][j] = fma(dz, e, sum[1][j]);
+                    }
+                }
+            }
+            F2 r[kPairs<V>];
+            gather_pairs<V>(r, [&](int j) { return __ldg(rstd + (at.tv * V + j) / at.per); });
+#pragma unroll
+            for (int j = 0; j < kPairs<V>; ++j) sum[1][j] = mul(sum[1][j], r[j]);
+        }
+        column_sums<V, 2>(sum, s_sum, at.tr, at.rt, at.vpr);
+        if (at.tr == 0)
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                all[0][j] += s_sum[column_at<V>(0, at.tv * V + j)];
+                all[1][j] += s_sum[column_at<V>(1, at.tv * V + j)];
+            }
+        const Span span(s_seg, k.s, rows);
+        for (int g = at.warp; g < a.groups; g += kThreads / 32) {
+            float m0 = 0.f, m1 = 0.f;
+            for (int j = at.lane; j < at.per; j += 32) {
+                const int ch = g * at.per + j;
+                const float u = a.gamma ? __ldg(a.gamma + ch) : 1.f;
+                m0 = fmaf(u, s_sum[column_at<V>(0, ch)], m0);
+                m1 = fmaf(u, s_sum[column_at<V>(1, ch)], m1);
+            }
+            m0 = warp_sum(m0);
+            m1 = warp_sum(m1);
+            if (at.lane == 0) {
+                if (span.first == span.last) w.coef[(int64_t)k.s * a.groups + g] = make_float2(m0, m1);
+                else w.part[(int64_t)span.slot(blockIdx.x, rows) * a.groups + g] = make_float2(m0, m1);
+            }
+        }
+        __syncthreads();
+    }
+    if (at.tr == 0)
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            w.total[(int64_t)blockIdx.x * 2 * a.c + at.tv * V + j] = all[0][j];
+            w.total[((int64_t)blockIdx.x * 2 + 1) * a.c + at.tv * V + j] = all[1][j];
+        }
+}
+
+template <typename T, int V, bool SILU>
+__global__ void __launch_bounds__(kThreads, 1) k_norm_bwd_apply(NormArgs a, int64_t rows, Ws w)
+{
+    extern __shared__ __align__(16) uint8_t s_raw[];
+    using S = Stream<T, V, 2>;
+    float2* s_stat = reinterpret_cast<float2*>(s_raw + S::kSmem);
+    int32_t* s_seg = reinterpret_cast<int32_t*>(s_stat + a.groups);
+    const Place<V> at(a, rows);
+    const bool works = at.tr < at.rt;
+    T* dx = static_cast<T*>(a.out) + at.tv * V;
+    S in(a, s_raw);
+    in.src[0] = static_cast<const T*>(a.x) + at.tv * V;
+    in.src[1] = static_cast<const T*>(a.dy) + at.tv * V;
+    load_offsets(a, s_seg, false);
+    const float least = least_of(a.act);
+    bool waited = false;
+    for (int64_t r0 = at.end; r0 > at.begin;) {
+        const Run k = run_before(a, s_seg, at.begin, r0);
+        r0 = k.lo;
+        if (k.s < 0) {
+            F2 zero[kPairs<V>];
+#pragma unroll
+            for (int j = 0; j < kPairs<V>; ++j) zero[j] = both(0.f);
+            if (works)
+                for (int64_t r = k.lo + at.tr; r < k.hi; r += at.rt) {
+                    const int64_t row = row_at(a.order, r, a.n, a.status);
+                    if (row >= 0) *reinterpret_cast<Vec<T, V>*>(dx + row * a.c) = pack<T, V>(zero);
+                }
+            continue;
+        }
+        if (works) in.begin(k.hi - 1 - at.tr, -at.rt, k.lo, k.hi);  // on their way meanwhile
+        if (!waited) wait_for_first_kernel();
+        waited = true;
+        const Span span(s_seg, k.s, rows);
+        __syncthreads();
+        for (int g = at.warp; g < a.groups; g += kThreads / 32) {
+            float2 m = make_float2(0.f, 0.f);
+            if (span.first == span.last) {
+                m = w.coef[(int64_t)k.s * a.groups + g];
+            } else {
+                for (int c = span.first + at.lane; c <= span.last; c += 32) {
+                    const float2 v = w.part[(int64_t)span.slot(c, rows) * a.groups + g];
+                    m.x += v.x;
+                    m.y += v.y;
+                }
+                m.x = warp_sum(m.x);
+                m.y = warp_sum(m.y);
+            }
+            const float n = (float)(span.hi - span.lo) * (float)at.per;
+            if (at.lane == 0) s_stat[g] = make_float2(m.x / n, m.y / n);
+        }
+        __syncthreads();
+        if (!works) continue;
+        F2 minus[kPairs<V>], scale[kPairs<V>], shift[kPairs<V>], lift[kPairs<V>], tilt[kPairs<V>];
+        const float* mean = a.mean + (int64_t)k.s * a.groups;
+        const float* rstd = a.rstd + (int64_t)k.s * a.groups;
+        gather_pairs<V>(minus, [&](int j) { return -__ldg(mean + (at.tv * V + j) / at.per); });
+        gather_pairs<V>(scale, [&](int j) {
+            const int ch = at.tv * V + j;
+            return __ldg(rstd + ch / at.per) * (a.gamma ? __ldg(a.gamma + ch) : 1.f);
+        });
+        gather_pairs<V>(shift, [&](int j) { return a.beta ? __ldg(a.beta + at.tv * V + j) : 0.f; });
+        gather_pairs<V>(lift, [&](int j) {
+            const int g = (at.tv * V + j) / at.per;
+            return -__ldg(rstd + g) * s_stat[g].x;
+        });
+        gather_pairs<V>(tilt, [&](int j) {
+            const int g = (at.tv * V + j) / at.per;
+            const float r = __ldg(rstd + g);
+            return -r * r * s_stat[g].y;
+        });
+        for (; in.more(); in.advance()) {
+            in.wait();
+#pragma unroll
+            for (int q = 0; q < kUnroll; ++q) {
+                const int32_t row = in.row(q);
+                if (row < 0) continue;
+                F2 f[kPairs<V>], d[kPairs<V>];
+                in.get(q, 0, f);
+                in.get(q, 1, d);
+#pragma unroll
+                for (int j = 0; j < kPairs<V>; ++j) {
+                    const F2 e = add(f[j], minus[j]);
+                    const F2 dz = through<SILU>(d[j], fma(e, scale[j], shift[j]), least);
+                    f[j] = fma(dz, scale[j], fma(e, tilt[j], lift[j]));
+                }
+                *reinterpret_cast<Vec<T, V>*>(dx + (int64_t)row * a.c) = pack<T, V>(f);
+            }
+        }
+    }
+    if (!waited) wait_for_first_kernel();
+    // dgamma and dbeta: a warp for each channel
+    if (a.dgamma || a.dbeta)
+        for (int ch = blockIdx.x * (kThreads / 32) + at.warp; ch < a.c; ch += gridDim.x * (kThreads / 32)) {
+            float s0 = 0.f, s1 = 0.f;
+            for (int c = at.lane; c < (int)gridDim.x; c += 32) {
+                s0 += w.total[(int64_t)c * 2 * a.c + ch];
+                s1 += w.total[((int64_t)c * 2 + 1) * a.c + ch];
+            }
+            s0 = warp_sum(s0);
+            s1 = warp_sum(s1);
+            if (at.lane == 0 && a.dbeta) a.dbeta[ch] = s0;
+            if (at.lane == 0 && a.dgamma) a.dgamma[ch] = s1;
+        }
+}
+
+// ------------------------------------------- rows of more than kThreads vectors
+// One block per (group, segment), then a thread per element.
+template <typename T>
+__global__ void __launch_bounds__(kBlock) k_norm_stats_wide(NormArgs a)
+{
+    const int g = blockIdx.x, s = blockIdx.y, per = a.c / a.groups;
+    int64_t lo, hi;
+    segment_bounds(a.seg, s, a.n, a.status, lo, hi);
+    const T* x = static_cast<const T*>(a.x);
+    const int64_t total = (hi - lo) * per;
+    const float count = (float)(total > 0 ? total : 1);
+    auto at = [&](int64_t e) -> float {
+        const int64_t row = row_at(a.order, lo + e / per, a.n, a.status);
+        return row < 0 ? 0.f : elem<T>::to_f32(x[row * a.c + g * per + e % per]);
+    };
+    float v = 0.f;
+    for (int64_t e = threadIdx.x; e < total; e += kBlock) v += at(e);
+    const float mean = block_sum(v) / count;
+    v = 0.f;
+    for (int64_t e = threadIdx.x; e < total; e += kBlock) {
+        const float d = at(e) - mean;
+        v += d * d;
+    }
+    const float var = block_sum(v) / count;
+    if (threadIdx.x == 0) {
+        a.mean[s * a.groups + g] = mean;
+        a.rstd[s * a.groups + g] = 1.f / sqrtf(var + a.eps);
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kBlock) k_norm_apply_wide(NormArgs a)
+{
+    const int64_t t = (int64_t)blockIdx.x * kBlock + threadIdx.x;
+    const int64_t r = t / a.c;
+    const int c = (int)(t % a.c);
+    if (r >= a.n) return;
+    const int64_t row = row_at(a.order, r, a.n, a.status);
+    if (row < 0) return;
+    const int s = segment_of(a.seg, a.segments, r);
+    float y = 0.f;
+    if (s >= 0 && s < a.segments) {
+        const int i = s * a.groups + c / (a.c / a.groups);
+        const float xh = (elem<T>::to_f32(static_cast<const T*>(a.x)[row * a.c + c]) - a.mean[i]) * a.rstd[i];
+        y = activate(xh * (a.gamma ? a.gamma[c] : 1.f) + (a.beta ? a.beta[c] : 0.f), a.act);
+    }
+    static_cast<T*>(a.out)[row * a.c + c] = elem<T>::from_f32(y);
+}
+
+// part[s][0][c] = sum of dz, part[s][1][c] = sum of dz xh over segment s
+template <typename T>
+__global__ void __launch_bounds__(kBlock) k_norm_bwd_sums_wide(NormArgs a, float* __restrict__ part)
+{
+    const int c = blockIdx.x, s = blockIdx.y;
+    const int i = s * a.groups + c / (a.c / a.groups);
+    int64_t lo, hi;
+    segment_bounds(a.seg, s, a.n, a.status, lo, hi);
+    const float mean = a.mean[i], rstd = a.rstd[i];
+    const float gamma = a.gamma ? a.gamma[c] : 1.f, beta = a.beta ? a.beta[c] : 0.f;
+    float s0 = 0.f, s1 = 0.f;
+    for (int64_t r = lo + threadIdx.x; r < hi; r += kBlock) {
+        const int64_t row = row_at(a.order, r, a.n, a.status);
+        if (row < 0) continue;
+        const float xh = (elem<T>::to_f32(static_cast<const T*>(a.x)[row * a.c + c]) - mean) * rstd;
+        const float dz = elem<T>::to_f32(static_cast<const T*>(a.dy)[row * a.c + c]) * slope(xh * gamma + beta, a.act);
+        s0 += dz;
+        s1 += dz * xh;
+    }
+    s0 = block_sum(s0);
+    s1 = block_sum(s1);
+    if (threadIdx.x == 0) {
+        part[(int64_t)s * 2 * a.c + c] = s0;
+        part[(int64_t)s * 2 * a.c + a.c + c] = s1;
+    }
+}
+
+__global__ void __launch_bounds__(kBlock) k_norm_bwd_params_wide(NormArgs a, const float* __restrict__ part)
+{
+    const int c = blockIdx.x * kBlock + threadIdx.x;
+    if (c >= a.c) return;
+    float s0 = 0.f, s1 = 0.f;
+    for (int s = 0; s < a.segments; ++s) {
+        s0 += part[(int64_t)s * 2 * a.c + c];
+        s1 += part[(int64_t)s * 2 * a.c + a.c + c];
+    }
+    if (a.dbeta) a.dbeta[c] = s0;
+    if (a.dgamma) a.dgamma[c] = s1;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kBlock) k_norm_bwd_apply_wide(NormArgs a, const float* __restrict__ part)
+{
+    const int64_t t = (int64_t)blockIdx.x * kBlock + threadIdx.x;
+    const int64_t r = t / a.c;
+    const int c = (int)(t % a.c), per = a.c / a.groups;
+    if (r >= a.n) return;
+    const int64_t row = row_at(a.order, r, a.n, a.status);
+    if (row < 0) return;
+    const int s = segment_of(a.seg, a.segments, r);
+    float dx = 0.f;
+    if (s >= 0 && s < a.segments) {
+        const int g = c / per, i = s * a.groups + g;
+        int64_t lo, hi;
+        segment_bounds(a.seg, s, a.n, a.status, lo, hi);
+        const float count = (float)((hi - lo) * per);
+        float m0 = 0.f, m1 = 0.f;
+        for (int j = g * per; j < (g + 1) * per; ++j) {
+            const float w = a.gamma ? a.gamma[j] : 1.f;
+            m0 += w * part[(int64_t)s * 2 * a.c + j];
+            m1 += w * part[(int64_t)s * 2 * a.c + a.c + j];
+        }
+        const float gamma = a.gamma ? a.gamma[c] : 1.f, beta = a.beta ? a.beta[c] : 0.f;
+        const float xh = (elem<T>::to_f32(static_cast<const T*>(a.x)[row * a.c + c]) - a.mean[i]) * a.rstd[i];
+        const float dz = elem<T>::to_f32(static_cast<const T*>(a.dy)[row * a.c + c]) * slope(xh * gamma + beta, a.act);
+        dx = a.rstd[i] * (gamma * dz - m0 / count - xh * (m1 / count));
+    }
+    static_cast<T*>(a.out)[row * a.c + c] = elem<T>::from_f32(dx);
+}
+
+template <typename T>
+spc_status fwd_wide(const NormArgs& a, cudaStream_t st)
+{
+    const int64_t blocks = ceil_div(a.n * a.c, kBlock);
+    if (blocks > INT32_MAX) return SPC_ERR_UNSUPPORTED;
+    k_norm_stats_wide<T><<<dim3(a.groups, a.segments), kBlock, 0, st>>>(a);
+    SPC_LAUNCH_CHECK();
+    if (a.n == 0) return SPC_OK;
+    k_norm_apply_wide<T><<<(unsigned)blocks, kBlock, 0, st>>>(a);
+    SPC_LAUNCH_CHECK();
+    return SPC_OK;
+}
+
+template <typename T>
+spc_status bwd_wide(const NormArgs& a, float* part, cudaStream_t st)
+{
+    const int64_t blocks = ceil_div(a.n * a.c, kBlock);
+    if (blocks > INT32_MAX) return SPC_ERR_UNSUPPORTED;
+    k_norm_bwd_sums_wide<T><<<dim3(a.c, a.segments), kBlock, 0, st>>>(a, part);
+    SPC_LAUNCH_CHECK();
+    if (a.dgamma || a.dbeta) {
+        k_norm_bwd_params_wide<<<(unsigned)ceil_div(a.c, kBlock), kBlock, 0, st>>>(a, part);
+        SPC_LAUNCH_CHECK();
+    }
+    if (a.n == 0) return SPC_OK;
+    k_norm_bwd_apply_wide<T><<<(unsigned)blocks, kBlock, 0, st>>>(a, part);
+    SPC_LAUNCH_CHECK();
+    return SPC_OK;
+}
+
+// ----------------------------------------------------------------------- launch
+// Channels of a thread: as many as divide the row and stand aligned in it.
+template <typename T>
+int vector_of(const NormArgs& a)
+{
+    const uintptr_t low = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.out) |
+                          reinterpret_cast<uintptr_t>(a.dy);
+    int v = 16 / (int)sizeof(T);
+    while (v > 1 && (a.c % v != 0 || (low & (v * sizeof(T) - 1)) != 0)) v /= 2;
+    return v;
+}
+
+int shares_of(int64_t n) { return (int)std::max<int64_t>(1, std::min<int64_t>(sm_count(), ceil_div(n, kMinRows))); }
+
+size_t carve(int64_t n, int32_t c, int32_t segments, int32_t groups, char* base, Ws* w)
+{
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        char* p = base ? base + off : nullptr;
+        off = align_up(off + bytes, 256);
+        return p;
+    };
+    const size_t shares = (size_t)shares_of(n);
+    char* part = take(sizeof(float2) * 2 * shares * groups);
+    char* coef = take(sizeof(float2) * (size_t)segments * groups);
+    char* total = take(sizeof(float) * 2 * shares * c);
+    if (w) *w = Ws{reinterpret_cast<float2*>(part), reinterpret_cast<float2*>(coef), reinterpret_cast<float*>(total)};
+    return off;
+}
+
+// second: the second kernel of a pass, which waits for the first one itself.
+template <typename K>
+spc_status launch(K* kernel, int shares, size_t smem, cudaStream_t st, const NormArgs& a, int64_t rows, const Ws& w,
+                  bool second)
+{
+    SPC_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)shares);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = second ? 1 : 0;
+    SPC_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, a, rows, w));
+    return SPC_OK;
+}
+
+template <typename T, int V, bool SILU>
+spc_status rows_pass(const NormArgs& a, const Ws& w, bool backward, cudaStream_t st)
+{
+    const int shares = shares_of(a.n);
+    const int64_t rows = std::max<int64_t>(1, ceil_div(a.n, shares));
+    const size_t offsets = sizeof(int32_t) * (a.segments + 1), stat = sizeof(float2) * a.groups;
+    if (backward) {
+        const size_t base = Stream<T, V, 2>::kSmem + offsets;
+        const spc_status s = launch(k_norm_bwd_sums<T, V, SILU>, shares, base, st, a, rows, w, false);
+        return s != SPC_OK ? s : launch(k_norm_bwd_apply<T, V, SILU>, shares, base + stat, st, a, rows, w, true);
+    }
+    const size_t base = Stream<T, V, 1>::kSmem + offsets;
+    const spc_status s = launch(k_norm_stats<T, V>, shares, base + sizeof(float) * a.c, st, a, rows, w, false);
+    return s != SPC_OK || a.n == 0 ? s : launch(k_norm_apply<T, V, SILU>, shares, base + stat, st, a, rows, w, true);
+}
+
+template <typename T, int V>
+spc_status rows_pass(const NormArgs& a, const Ws& w, bool backward, cudaStream_t st)
+{
+    return a.act == SPC_ACT_SILU ? rows_pass<T, V, true>(a, w, backward, st) : rows_pass<T, V, false>(a, w, backward, st);
+}
+
+template <typename T>
+spc_status norm_pass(const NormArgs& a, void* ws, bool backward, cudaStream_t st)
+{
+    const int v = vector_of<T>(a);
+    Ws w;
+    carve(a.n, a.c, a.segments, a.groups, static_cast<char*>(ws), &w);
+    if (a.c / v > kThreads) return backward ? bwd_wide<T>(a, static_cast<float*>(ws), st) : fwd_wide<T>(a, st);
+    if constexpr (sizeof(T) == 2)
+        if (v == 8) return rows_pass<T, 8>(a, w, backward, st);
+    if (v == 4) return rows_pass<T, 4>(a, w, backward, st);
+    if (v == 2) return rows_pass<T, 2>(a, w, backward, st);
+    return rows_pass<T, 1>(a, w, backward, st);
+}
+
+}  // namespace
+
+}  // namespace spc

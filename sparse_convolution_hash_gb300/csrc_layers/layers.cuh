@@ -31,8 +31,10 @@ struct NormArgs {
     float eps;
 };
 size_t group_norm_ws_bytes(int64_t n, int32_t c, int32_t segments, int32_t groups, spc_dtype dt);
-spc_status group_norm_fwd(const NormArgs& a, spc_dtype dt, void* ws, cudaStream_t st);
-spc_status group_norm_bwd(const NormArgs& a, spc_dtype dt, void* ws, cudaStream_t st);
+spc_status group_norm(const NormArgs& a, spc_dtype dt, void* ws, bool backward, cudaStream_t st);
+spc_status group_norm_f32(const NormArgs& a, void* ws, bool backward, cudaStream_t st);
+spc_status group_norm_f16(const NormArgs& a, void* ws, bool backward, cudaStream_t st);
+spc_status group_norm_bf16(const NormArgs& a, void* ws, bool backward, cudaStream_t st);
 
 // ------------------------------------------------------------------ dropout
 spc_status dropout(const void* x, const void* residual, int64_t n, double p, const uint64_t* rng,

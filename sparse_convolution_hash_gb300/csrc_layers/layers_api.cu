@@ -115,7 +115,7 @@ spc_status spc_group_norm_fwd(const void* x, const float* gamma, const float* be
     if (!(eps > 0.f) || isinf(eps)) return SPC_ERR_INVALID_ARG;
     const spc_status s = check_norm(a, dt, ws, ws_bytes);
     if (s != SPC_OK) return s;
-    return group_norm_fwd(a, dt, ws, static_cast<cudaStream_t>(stream));
+    return group_norm(a, dt, ws, false, static_cast<cudaStream_t>(stream));
 }
 
 spc_status spc_group_norm_bwd(const void* dy, const void* x, const float* gamma, const float* beta,
@@ -132,7 +132,7 @@ spc_status spc_group_norm_bwd(const void* dy, const void* x, const float* gamma,
     if (s != SPC_OK) return s;
     if (n > 0 && (!dy || !elem_aligned(dy, dt))) return SPC_ERR_INVALID_ARG;
     if (!aligned4(dgamma) || !aligned4(dbeta)) return SPC_ERR_INVALID_ARG;
-    return group_norm_bwd(a, dt, ws, static_cast<cudaStream_t>(stream));
+    return group_norm(a, dt, ws, true, static_cast<cudaStream_t>(stream));
 }
 
 spc_status spc_dropout_fwd(const void* x, const void* residual, int64_t n, double p,
