@@ -22,7 +22,9 @@
 
 #include <type_traits>
 
+#include "kernels.cuh"
 #include "layers.cuh"
+#include "ptx.cuh"
 
 namespace spc {
 
@@ -30,8 +32,7 @@ namespace {
 
 constexpr int kBlock = 256;      // of the kernels for very long rows
 constexpr int kThreads = 512;    // of the others
-constexpr int kUnroll = 4;       // rows of a thread in a group
-constexpr int kDepth = 3;        // groups in flight
+constexpr uint64_t kDrainNs = 200000000ull;  // bound of the wait for a CTA's own copies
 constexpr int kMinRows = 64;     // positions of a CTA, at least
 
 template <typename T, int V>
@@ -280,85 +281,168 @@ struct Span {
 };
 
 // ------------------------------------------------------------ rows in flight
-// A thread's own vectors of every step-th position of a run of N tensors: asynchronous copies into
-// slots of shared memory that only this thread reads, kDepth groups of
-// kUnroll rows ahead of their use, so no barrier stands between memory and arithmetic.
-template <typename T, int V, int N>
-struct Stream {
-    static constexpr int kBytes = sizeof(T) * V;
-    static constexpr size_t kSmem = (size_t)kDepth * kUnroll * N * kThreads * kBytes;
-    const T* src[N];
-    const int32_t* order;
-    int32_t* status;
-    Vec<T, V>* slots;        // [kDepth * kUnroll][N][kThreads]
-    int32_t rows, c;
-    int32_t next, lo, hi;    // next position to ask for, of [lo, hi)
-    int32_t at, step;        // first position of the group in hand
-    int in, out;             // ring places
-    int32_t entry[kUnroll];  // rows of the group at `next`, -1: none
+// Barrier of the threads that work on rows (the loading warp has its own way).
+__device__ __forceinline__ void sync_workers() { ptx::bar_sync_named(1, kThreads); }
 
-    __device__ __forceinline__ Stream(const NormArgs& a, void* s)
-        : order(a.order), status(a.status), slots(static_cast<Vec<T, V>*>(s) + threadIdx.x), rows((int32_t)a.n), c(a.c)
+// Rows in order (DENSE): a run is one contiguous piece of each of the N tensors.  A warp of its
+// own brings it in stages of kRowsOf rows a thread by bulk copies, kStages ahead of their use and on
+// into the next run, so neither addresses nor latencies cost the others anything.
+// Rows through a list, or not a multiple of 16 bytes: each thread loads its own.
+template <typename T, int V, int N, bool DENSE>
+struct Feed {
+    static constexpr int kRowsOf = DENSE ? 4 / N : 4;                        // rows of a thread per stage
+    static constexpr int kStage = kRowsOf * N * kThreads * (int)sizeof(T) * V;  // bytes
+    static constexpr int kStages = 5;
+    static constexpr size_t kSmem = DENSE ? (size_t)kStages * kStage + 2 * kStages * sizeof(uint64_t) : 0;
+    static constexpr int kBlockThreads = DENSE ? kThreads + 32 : kThreads;
+
+    const NormArgs& a;
+    const T* base[N];        // this thread's vector of row 0
+    uint8_t* stages;
+    uint64_t* full;
+    uint64_t* empty;
+    uint64_t wait_ns;
+    uint32_t it;             // stages used so far
+    int vpr, rt, tr;
+    int step;                // 1 forwards, -1 backwards
+    int64_t from, lo, hi;    // the run, and where it starts
+    bool ok;
+
+    __device__ __forceinline__ Feed(const NormArgs& args, void* smem, uint64_t limit, int vpr_, int rt_, int tr_)
+        : a(args), stages(static_cast<uint8_t*>(smem)), wait_ns(limit), it(0), vpr(vpr_), rt(rt_), tr(tr_), ok(true)
     {
+        full = reinterpret_cast<uint64_t*>(stages + (size_t)kStages * kStage);
+        empty = full + kStages;
+        if (DENSE && threadIdx.x == 0) {
+            for (int s = 0; s < kStages; ++s) {
+                ptx::mbar_init(&full[s], 1);
+                ptx::mbar_init(&empty[s], kThreads / 32);
+            }
+            ptx::mbar_init_fence();
+        }
     }
-    __device__ __forceinline__ bool there(int32_t p) const { return (uint32_t)(p - lo) < (uint32_t)(hi - lo); }
-    __device__ __forceinline__ int32_t row_of(int32_t p) const { return !there(p) ? -1 : order ? __ldg(order + p) : p; }
-    __device__ __forceinline__ void ask()
+    __device__ __forceinline__ int stage_rows() const { return kRowsOf * rt; }
+
+    // The loading thread: the run's stages in turn.
+    __device__ __forceinline__ void load(const Run& k, const T* const (&tensor)[N])
     {
+        const int64_t rows = stage_rows();
+        const uint32_t row_bytes = (uint32_t)a.c * (uint32_t)sizeof(T);
+        for (int64_t done = 0; done < k.hi - k.lo && ok; done += rows, ++it) {
+            const int s = it % kStages;
+            if (it >= kStages) ok = ptx::mbar_wait(&empty[s], ((it / kStages) - 1) & 1, wait_ns);
+            if (!ok) break;
+            const int64_t count = k.hi - k.lo - done < rows ? k.hi - k.lo - done : rows;
+            const int64_t r = step > 0 ? k.lo + done : k.hi - done - count;
+            ptx::mbar_arrive_expect_tx(&full[s], (uint32_t)(N * count) * row_bytes);
 #pragma unroll
-        for (int q = 0; q < kUnroll; ++q) {
-            if ((uint32_t)entry[q] < (uint32_t)rows) {
+            for (int t = 0; t < N; ++t)
+                asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                                 ptx::smem_u32(stages + (size_t)s * kStage + t * (kStage / N))),
+                             "l"(tensor[t] + r * a.c), "r"((uint32_t)count * row_bytes), "r"(ptx::smem_u32(&full[s]))
+                             : "memory");
+        }
+    }
+    // ... and at the end whatever it still has in flight.
+    __device__ __forceinline__ void drain()
+    {
+        if (!ok) set_status(a.status, SPC_ERR_TIMEOUT);
+        const uint32_t first = it > kStages ? it - kStages : 0;
+        for (uint32_t j = first; j < it; ++j) ptx::mbar_wait(&full[j % kStages], (j / kStages) & 1, kDrainNs);
+    }
+
+    // The working threads.
+    __device__ __forceinline__ void begin(const Run& k)
+    {
+        lo = k.lo;
+        hi = k.hi;
+    }
+    __device__ __forceinline__ void wait_full()
+    {
+        if (!DENSE || !ok) return;
+        const bool came = ptx::mbar_wait(&full[it % kStages], (it / kStages) & 1, wait_ns);
+        if (!came) set_status(a.status, SPC_ERR_TIMEOUT);
+        ok = came;
+    }
+    __device__ __forceinline__ const Vec<T, V>* slot(int q, int t) const
+    {
+        return reinterpret_cast<const Vec<T, V>*>(stages + (size_t)(it % kStages) * kStage + t * (kStage / N)) + q * rt * vpr + (int)threadIdx.x;
+    }
+    // This thread's first row of a run that goes forwards (0 where its entry is out of range) and
+    // the run's first one; nothing is used up.
+    __device__ __forceinline__ void first(F2 (&mine)[kPairs<V>], F2 (&lead)[kPairs<V>])
+    {
+        if constexpr (DENSE) {
+            wait_full();
+            if (lo + tr < hi) unpack<T, V>(*slot(0, 0), mine);
+            unpack<T, V>(*(slot(0, 0) - tr * vpr), lead);
+        } else {
+            const int64_t r0 = row_at(a.order, lo, a.n, nullptr), r1 = lo + tr < hi ? row_at(a.order, lo + tr, a.n, nullptr) : -1;
+            if (r0 >= 0) unpack<T, V>(*reinterpret_cast<const Vec<T, V>*>(base[0] + r0 * a.c), lead);
+            if (r1 >= 0) unpack<T, V>(*reinterpret_cast<const Vec<T, V>*>(base[0] + r1 * a.c), mine);
+        }
+    }
+    // body(values, row) for each of this thread's rows; every working thread calls it, `works`
+    // says whether it has rows at all.
+    template <typename B>
+    __device__ __forceinline__ void run(bool works, B body)
+    {
+        if constexpr (DENSE) {
+            const int64_t rows = stage_rows();
+            for (int64_t done = 0; done < hi - lo; done += rows, ++it) {
+                wait_full();
+                const int64_t left = hi - lo - done;
+                const int count = (int)(left < rows ? left : rows);
+                const int64_t r = (step > 0 ? lo + done : hi - done - count) + tr;
+                if (ok && works) {
+                    if (count == rows) {
+                        F2 f[kRowsOf][N][kPairs<V>];
 #pragma unroll
-                for (int t = 0; t < N; ++t) {
-                    Vec<T, V>* d = slots + ((in * kUnroll + q) * N + t) * kThreads;
-                    const T* g = src[t] + (int64_t)entry[q] * c;
-                    if constexpr (kBytes >= 4)
-                        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(
-                                         (uint32_t)__cvta_generic_to_shared(d)), "l"(g), "n"(kBytes) : "memory");
-                    else
-                        *d = *reinterpret_cast<const Vec<T, V>*>(g);
+                        for (int q = 0; q < kRowsOf; ++q)
+#pragma unroll
+                            for (int t = 0; t < N; ++t) unpack<T, V>(*slot(q, t), f[q][t]);
+#pragma unroll
+                        for (int q = 0; q < kRowsOf; ++q) body(f[q], r + q * rt);
+                    } else {
+                        for (int q = 0; q * rt + tr < count; ++q) {
+                            F2 f[N][kPairs<V>];
+#pragma unroll
+                            for (int t = 0; t < N; ++t) unpack<T, V>(*slot(q, t), f[t]);
+                            body(f, r + q * rt);
+                        }
+                    }
                 }
-            } else if (entry[q] != -1 || (order && there(next + q * step))) {
-                set_status(status, SPC_ERR_ROW_INDEX);
+                __syncwarp();
+                if ((threadIdx.x & 31) == 0) ptx::mbar_arrive(&empty[it % kStages]);
+            }
+        } else if (works) {
+            for (int64_t p = lo + tr; p < hi; p += kRowsOf * rt) {
+                int32_t row[kRowsOf];
+#pragma unroll
+                for (int q = 0; q < kRowsOf; ++q) {
+                    const int64_t at = p + q * rt;
+                    row[q] = at >= hi ? -1 : a.order ? __ldg(a.order + at) : (int32_t)at;
+                    if (at < hi && (row[q] < 0 || row[q] >= a.n)) {
+                        set_status(a.status, SPC_ERR_ROW_INDEX);
+                        row[q] = -1;
+                    }
+                }
+                Vec<T, V> v[kRowsOf][N];
+#pragma unroll
+                for (int q = 0; q < kRowsOf; ++q)
+                    if (row[q] >= 0)
+#pragma unroll
+                        for (int t = 0; t < N; ++t) v[q][t] = *reinterpret_cast<const Vec<T, V>*>(base[t] + (int64_t)row[q] * a.c);
+#pragma unroll
+                for (int q = 0; q < kRowsOf; ++q)
+                    if (row[q] >= 0) {
+                        F2 f[N][kPairs<V>];
+#pragma unroll
+                        for (int t = 0; t < N; ++t) unpack<T, V>(v[q][t], f[t]);
+                        body(f, row[q]);
+                    }
             }
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        in = in + 1 == kDepth ? 0 : in + 1;
-        next += kUnroll * step;
-#pragma unroll
-        for (int q = 0; q < kUnroll; ++q) entry[q] = row_of(next + q * step);
-    }
-    // Starts on positions [lo, hi): from `first` on, `step` apart.
-    __device__ __forceinline__ void begin(int64_t first, int step_, int64_t lo_, int64_t hi_)
-    {
-        next = at = (int32_t)first;
-        step = step_;
-        lo = (int32_t)lo_;
-        hi = (int32_t)hi_;
-        in = out = 0;
-#pragma unroll
-        for (int q = 0; q < kUnroll; ++q) entry[q] = row_of(next + q * step);
-#pragma unroll
-        for (int d = 0; d < kDepth; ++d) ask();
-    }
-    __device__ __forceinline__ bool more() const { return there(at); }
-    __device__ __forceinline__ void wait() const { asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory"); }
-    // Row q of the group in hand, or -1.
-    __device__ __forceinline__ int32_t row(int q) const
-    {
-        const int32_t r = row_of(at + q * step);
-        return (uint32_t)r < (uint32_t)rows ? r : -1;
-    }
-    __device__ __forceinline__ void get(int q, int t, F2 (&f)[kPairs<V>]) const
-    {
-        unpack<T, V>(slots[((out * kUnroll + q) * N + t) * kThreads], f);
-    }
-    // The group in hand is done with: asks for the one kDepth groups on.
-    __device__ __forceinline__ void advance()
-    {
-        ask();
-        out = out + 1 == kDepth ? 0 : out + 1;
-        at += kUnroll * step;
     }
 };
 
@@ -377,7 +461,7 @@ __device__ __forceinline__ void column_sums(const F2 (&v)[N][kPairs<V>], float* 
     constexpr int P = kPart<V>, H = V / P;
     using W = Vec<float, P>;
     W* w = reinterpret_cast<W*>(s);
-    __syncthreads();
+    sync_workers();
 #pragma unroll
     for (int k = 0; k < N; ++k)
 #pragma unroll
@@ -393,7 +477,7 @@ __device__ __forceinline__ void column_sums(const F2 (&v)[N][kPairs<V>], float* 
     int half = 1;
     while (half < rt) half <<= 1;
     for (half >>= 1; half; half >>= 1) {
-        __syncthreads();
+        sync_workers();
         if (tr < half && tr + half < rt)
 #pragma unroll
             for (int k = 0; k < N * H; ++k) {
@@ -404,7 +488,7 @@ __device__ __forceinline__ void column_sums(const F2 (&v)[N][kPairs<V>], float* 
                 w[k * kThreads + threadIdx.x] = a;
             }
     }
-    __syncthreads();
+    sync_workers();
 }
 
 __device__ __forceinline__ float warp_sum(float v)
@@ -446,19 +530,33 @@ struct Place {
 
 // ------------------------------------------------------------------- statistics
 // part[slot][g] = (mean, M2) of a shared segment's part; whole segments end in mean, rstd.
-template <typename T, int V>
-__global__ void __launch_bounds__(kThreads, 1) k_norm_stats(NormArgs a, int64_t rows, Ws w)
+template <typename T, int V, bool DENSE>
+__global__ void __launch_bounds__(Feed<T, V, 1, DENSE>::kBlockThreads, 1) k_norm_stats(NormArgs a, int64_t rows, Ws w, uint64_t wait_ns)
 {
     extern __shared__ __align__(16) uint8_t s_raw[];
-    using S = Stream<T, V, 1>;
-    float* s_sum = reinterpret_cast<float*>(s_raw);  // the slots, once a run's rows are in
-    float* s_mean = reinterpret_cast<float*>(s_raw + S::kSmem);
+    using S = Feed<T, V, 1, DENSE>;
+    float* s_sum = reinterpret_cast<float*>(s_raw + S::kSmem);
+    float* s_mean = s_sum + kThreads * V;
     int32_t* s_seg = reinterpret_cast<int32_t*>(s_mean + a.c);
     const Place<V> at(a, rows);
     const bool works = at.tr < at.rt;
-    S in(a, s_raw);
-    in.src[0] = static_cast<const T*>(a.x) + at.tv * V;
+    S in(a, s_raw, wait_ns, at.vpr, at.rt, at.tr);
+    const T* const tensor[1] = {static_cast<const T*>(a.x)};
+    in.step = 1;
+#pragma unroll
+    for (int t = 0; t < 1; ++t) in.base[t] = tensor[t] + at.tv * V;
     load_offsets(a, s_seg, blockIdx.x == 0);
+    if (DENSE && at.warp == kThreads / 32) {
+        if (at.lane == 0) {
+            for (int64_t r0 = at.begin; r0 < at.end;) {
+                const Run k = run_at(a, s_seg, r0, at.end);
+                r0 = k.hi;
+                if (k.s >= 0) in.load(k, tensor);
+            }
+            in.drain();
+        }
+        return;
+    }
     // empty segments are finished here, a block each in turn
     for (int s = blockIdx.x; s < a.segments; s += gridDim.x)
         if (s_seg[s] >= s_seg[s + 1])
@@ -470,51 +568,39 @@ __global__ void __launch_bounds__(kThreads, 1) k_norm_stats(NormArgs a, int64_t 
         const Run k = run_at(a, s_seg, r0, at.end);
         r0 = k.hi;
         if (k.s < 0) continue;
-        F2 pivot[kPairs<V>], s1[kPairs<V>], s2[kPairs<V>], base[kPairs<V>];
+        F2 pivot[1][kPairs<V>], s1[kPairs<V>], s2[kPairs<V>], lead[kPairs<V>];
 #pragma unroll
-        for (int j = 0; j < kPairs<V>; ++j) pivot[j] = s1[j] = s2[j] = base[j] = both(0.f);
+        for (int j = 0; j < kPairs<V>; ++j) pivot[0][j] = s1[j] = s2[j] = lead[j] = both(0.f);
         int count = 0;
-        if (works) {
-            in.begin(k.lo + at.tr, at.rt, k.lo, k.hi);
-            // the run's first row, around which the threads' sums are brought together
-            const int64_t row0 = row_at(a.order, k.lo, a.n, nullptr);
-            if (row0 >= 0) unpack<T, V>(*reinterpret_cast<const Vec<T, V>*>(in.src[0] + row0 * a.c), base);
-            in.wait();
-            if (in.row(0) >= 0) in.get(0, 0, pivot);  // out of range: 0
-            F2 minus[kPairs<V>];
+        in.begin(k);
+        // the run's first row is what the threads' sums are brought together around
+        if (works) in.first(pivot[0], lead);
+        F2 minus[kPairs<V>];
 #pragma unroll
-            for (int j = 0; j < kPairs<V>; ++j) minus[j] = F2{-pivot[j].x, -pivot[j].y};
-            for (; in.more(); in.advance()) {
-                in.wait();
+        for (int j = 0; j < kPairs<V>; ++j) minus[j] = F2{-pivot[0][j].x, -pivot[0][j].y};
+        in.run(works, [&](const F2 (&f)[1][kPairs<V>], int64_t) {
+            ++count;
 #pragma unroll
-                for (int q = 0; q < kUnroll; ++q)
-                    if (in.row(q) >= 0) {
-                        F2 f[kPairs<V>];
-                        in.get(q, 0, f);
-                        ++count;
-#pragma unroll
-                        for (int j = 0; j < kPairs<V>; ++j) {
-                            const F2 d = add(f[j], minus[j]);
-                            s1[j] = add(s1[j], d);
-                            s2[j] = fma(d, d, s2[j]);
-                        }
-                    }
+            for (int j = 0; j < kPairs<V>; ++j) {
+                const F2 d = add(f[0][j], minus[j]);
+                s1[j] = add(s1[j], d);
+                s2[j] = fma(d, d, s2[j]);
             }
-        }
+        });
         // channel means around the run's first row, then squares around the channel means
         const float n = (float)(k.hi - k.lo), mine = (float)count;
         F2 v[1][kPairs<V>];
 #pragma unroll
         for (int j = 0; j < kPairs<V>; ++j)
-            v[0][j] = F2{fmaf(mine, pivot[j].x - base[j].x, s1[j].x), fmaf(mine, pivot[j].y - base[j].y, s1[j].y)};
+            v[0][j] = F2{fmaf(mine, pivot[0][j].x - lead[j].x, s1[j].x), fmaf(mine, pivot[0][j].y - lead[j].y, s1[j].y)};
         column_sums<V, 1>(v, s_sum, at.tr, at.rt, at.vpr);
         if (at.tr == 0)
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const float b = j % 2 ? base[j / 2].y : base[j / 2].x;
+                const float b = j % 2 ? lead[j / 2].y : lead[j / 2].x;
                 s_mean[at.tv * V + j] = b + s_sum[column_at<V>(0, at.tv * V + j)] / n;
             }
-        __syncthreads();
+        sync_workers();
 #pragma unroll
         for (int j = 0; j < kPairs<V>; ++j) v[0][j] = both(0.f);
         if (works && count) {
@@ -524,8 +610,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_norm_stats(NormArgs a, int64_t 
             };
 #pragma unroll
             for (int j = 0; j < kPairs<V>; ++j) {
-                v[0][j].x = square(pivot[j].x, s1[j].x, s2[j].x, at.tv * V + 2 * j);
-                if (2 * j + 1 < V) v[0][j].y = square(pivot[j].y, s1[j].y, s2[j].y, at.tv * V + 2 * j + 1);
+                v[0][j].x = square(pivot[0][j].x, s1[j].x, s2[j].x, at.tv * V + 2 * j);
+                if (2 * j + 1 < V) v[0][j].y = square(pivot[0][j].y, s1[j].y, s2[j].y, at.tv * V + 2 * j + 1);
             }
         }
         column_sums<V, 1>(v, s_sum, at.tr, at.rt, at.vpr);
@@ -552,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_norm_stats(NormArgs a, int64_t 
                 }
             }
         }
-        __syncthreads();
+        sync_workers();
     }
 }
 
@@ -563,7 +649,7 @@ __device__ __forceinline__ void join_stats(const NormArgs& a, const int32_t* s_s
 {
     const Span span(s_seg, s, rows);
     const int per = a.c / a.groups, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    __syncthreads();
+    sync_workers();
     for (int g = warp; g < a.groups; g += kThreads / 32) {
         float mean, rstd;
         if (span.first == span.last) {
@@ -610,22 +696,36 @@ __device__ __forceinline__ void join_stats(const NormArgs& a, const int32_t* s_s
         }
         if (lane == 0) s_stat[g] = make_float2(mean, rstd);
     }
-    __syncthreads();
+    sync_workers();
 }
 
-template <typename T, int V, bool SILU>
-__global__ void __launch_bounds__(kThreads, 1) k_norm_apply(NormArgs a, int64_t rows, Ws w)
+template <typename T, int V, bool DENSE, bool SILU>
+__global__ void __launch_bounds__(Feed<T, V, 1, DENSE>::kBlockThreads, 1) k_norm_apply(NormArgs a, int64_t rows, Ws w, uint64_t wait_ns)
 {
     extern __shared__ __align__(16) uint8_t s_raw[];
-    using S = Stream<T, V, 1>;
+    using S = Feed<T, V, 1, DENSE>;
     float2* s_stat = reinterpret_cast<float2*>(s_raw + S::kSmem);
     int32_t* s_seg = reinterpret_cast<int32_t*>(s_stat + a.groups);
     const Place<V> at(a, rows);
     const bool works = at.tr < at.rt;
     T* y = static_cast<T*>(a.out) + at.tv * V;
-    S in(a, s_raw);
-    in.src[0] = static_cast<const T*>(a.x) + at.tv * V;
+    S in(a, s_raw, wait_ns, at.vpr, at.rt, at.tr);
+    const T* const tensor[1] = {static_cast<const T*>(a.x)};
+    in.step = -1;
+#pragma unroll
+    for (int t = 0; t < 1; ++t) in.base[t] = tensor[t] + at.tv * V;
     load_offsets(a, s_seg, false);
+    if (DENSE && at.warp == kThreads / 32) {
+        if (at.lane == 0) {
+            for (int64_t r0 = at.end; r0 > at.begin;) {
+                const Run k = run_before(a, s_seg, at.begin, r0);
+                r0 = k.lo;
+                if (k.s >= 0) in.load(k, tensor);
+            }
+            in.drain();
+        }
+        return;
+    }
     const float floor = floor_of(a.act);
     bool waited = false;
     for (int64_t r0 = at.end; r0 > at.begin;) {
@@ -642,11 +742,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_norm_apply(NormArgs a, int64_t 
                 }
             continue;
         }
-        if (works) in.begin(k.hi - 1 - at.tr, -at.rt, k.lo, k.hi);  // on their way meanwhile
+        in.begin(k);
         if (!waited) wait_for_first_kernel();
         waited = true;
         join_stats(a, s_seg, k.s, rows, w.part, s_stat);
-        if (!works) continue;
         F2 minus[kPairs<V>], scale[kPairs<V>], shift[kPairs<V>];
         gather_pairs<V>(scale, [&](int j) {
             const int ch = at.tv * V + j;
@@ -655,19 +754,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_norm_apply(NormArgs a, int64_t 
         // the mean is taken off first: a constant channel gives beta exactly
         gather_pairs<V>(minus, [&](int j) { return -s_stat[(at.tv * V + j) / at.per].x; });
         gather_pairs<V>(shift, [&](int j) { return a.beta ? __ldg(a.beta + at.tv * V + j) : 0.f; });
-        for (; in.more(); in.advance()) {
-            in.wait();
+        in.run(works, [&](F2 (&f)[1][kPairs<V>], int64_t row) {
 #pragma unroll
-            for (int q = 0; q < kUnroll; ++q) {
-                const int32_t row = in.row(q);
-                if (row < 0) continue;
-                F2 f[kPairs<V>];
-                in.get(q, 0, f);
-#pragma unroll
-                for (int j = 0; j < kPairs<V>; ++j) f[j] = activate<SILU>(fma(add(f[j], minus[j]), scale[j], shift[j]), floor);
-                *reinterpret_cast<Vec<T, V>*>(y + (int64_t)row * a.c) = pack<T, V>(f);
-            }
-        }
+            for (int j = 0; j < kPairs<V>; ++j) f[0][j] = activate<SILU>(fma(add(f[0][j], minus[j]), scale[j], shift[j]), floor);
+            *reinterpret_cast<Vec<T, V>*>(y + row * a.c) = pack<T, V>(f[0]);
+        });
     }
     if (!waited) wait_for_first_kernel();
 }
@@ -675,19 +766,32 @@ __global__ void __launch_bounds__(kThreads, 1) k_norm_apply(NormArgs a, int64_t 
 // -------------------------------------------------------------------- gradients
 // Sums over the rows of this CTA: total[c][0] of dz and [1] of dz xh per channel, and per segment
 // and group (sum gamma dz, sum gamma dz xh): whole segments' in coef[s], parts in part[slot].
-template <typename T, int V, bool SILU>
-__global__ void __launch_bounds__(kThreads, 1) k_norm_bwd_sums(NormArgs a, int64_t rows, Ws w)
+template <typename T, int V, bool DENSE, bool SILU>
+__global__ void __launch_bounds__(Feed<T, V, 2, DENSE>::kBlockThreads, 1) k_norm_bwd_sums(NormArgs a, int64_t rows, Ws w, uint64_t wait_ns)
 {
     extern __shared__ __align__(16) uint8_t s_raw[];
-    using S = Stream<T, V, 2>;
-    float* s_sum = reinterpret_cast<float*>(s_raw);  // the slots, once a run's rows are in
-    int32_t* s_seg = reinterpret_cast<int32_t*>(s_raw + S::kSmem);
+    using S = Feed<T, V, 2, DENSE>;
+    float* s_sum = reinterpret_cast<float*>(s_raw + S::kSmem);
+    int32_t* s_seg = reinterpret_cast<int32_t*>(s_sum + 2 * kThreads * V);
     const Place<V> at(a, rows);
     const bool works = at.tr < at.rt;
-    S in(a, s_raw);
-    in.src[0] = static_cast<const T*>(a.x) + at.tv * V;
-    in.src[1] = static_cast<const T*>(a.dy) + at.tv * V;
+    S in(a, s_raw, wait_ns, at.vpr, at.rt, at.tr);
+    const T* const tensor[2] = {static_cast<const T*>(a.x), static_cast<const T*>(a.dy)};
+    in.step = 1;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) in.base[t] = tensor[t] + at.tv * V;
     load_offsets(a, s_seg, blockIdx.x == 0);
+    if (DENSE && at.warp == kThreads / 32) {
+        if (at.lane == 0) {
+            for (int64_t r0 = at.begin; r0 < at.end;) {
+                const Run k = run_at(a, s_seg, r0, at.end);
+                r0 = k.hi;
+                if (k.s >= 0) in.load(k, tensor);
+            }
+            in.drain();
+        }
+        return;
+    }
     const float least = least_of(a.act);
     float all[2][V];
 #pragma unroll
@@ -699,33 +803,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_norm_bwd_sums(NormArgs a, int64
         F2 minus[kPairs<V>], scale[kPairs<V>], shift[kPairs<V>], sum[2][kPairs<V>];
 #pragma unroll
         for (int j = 0; j < kPairs<V>; ++j) sum[0][j] = sum[1][j] = both(0.f);
-        if (works) {
-            in.begin(k.lo + at.tr, at.rt, k.lo, k.hi);
-            const float* mean = a.mean + (int64_t)k.s * a.groups;
-            const float* rstd = a.rstd + (int64_t)k.s * a.groups;
-            gather_pairs<V>(minus, [&](int j) { return -__ldg(mean + (at.tv * V + j) / at.per); });
-            gather_pairs<V>(scale, [&](int j) {
-                const int ch = at.tv * V + j;
-                return __ldg(rstd + ch / at.per) * (a.gamma ? __ldg(a.gamma + ch) : 1.f);
-            });
-            gather_pairs<V>(shift, [&](int j) { return a.beta ? __ldg(a.beta + at.tv * V + j) : 0.f; });
-            for (; in.more(); in.advance()) {
-                in.wait();
+        in.begin(k);
+        const float* mean = a.mean + (int64_t)k.s * a.groups;
+        const float* rstd = a.rstd + (int64_t)k.s * a.groups;
+        gather_pairs<V>(minus, [&](int j) { return works ? -__ldg(mean + (at.tv * V + j) / at.per) : 0.f; });
+        gather_pairs<V>(scale, [&](int j) {
+            const int ch = at.tv * V + j;
+            return works ? __ldg(rstd + ch / at.per) * (a.gamma ? __ldg(a.gamma + ch) : 1.f) : 0.f;
+        });
+        gather_pairs<V>(shift, [&](int j) { return works && a.beta ? __ldg(a.beta + at.tv * V + j) : 0.f; });
+        in.run(works, [&](const F2 (&f)[2][kPairs<V>], int64_t) {
 #pragma unroll
-                for (int q = 0; q < kUnroll; ++q) {
-                    if (in.row(q) < 0) continue;
-                    F2 f[kPairs<V>], d[kPairs<V>];
-                    in.get(q, 0, f);
-                    in.get(q, 1, d);
-#pragma unroll
-                    for (int j = 0; j < kPairs<V>; ++j) {
-                        const F2 e = add(f[j], minus[j]);
-                        const F2 dz = through<SILU>(d[j], fma(e, scale[j], shift[j]), least);
-                        sum[0][j] = add(sum[0][j], dz);
-                        sum[1][j] = fma(dz, e, sum[1][j]);
-                    }
-                }
+            for (int j = 0; j < kPairs<V>; ++j) {
+                const F2 e = add(f[0][j], minus[j]);
+                const F2 dz = through<SILU>(f[1][j], fma(e, scale[j], shift[j]), least);
+                sum[0][j] = add(sum[0][j], dz);
+                sum[1][j] = fma(dz, e, sum[1][j]);
             }
+        });
+        if (works) {
             F2 r[kPairs<V>];
             gather_pairs<V>(r, [&](int j) { return __ldg(rstd + (at.tv * V + j) / at.per); });
 #pragma unroll
@@ -754,7 +850,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_norm_bwd_sums(NormArgs a, int64
                 else w.part[(int64_t)span.slot(blockIdx.x, rows) * a.groups + g] = make_float2(m0, m1);
             }
         }
-        __syncthreads();
+        sync_workers();
     }
     if (at.tr == 0)
 #pragma unroll
@@ -764,20 +860,33 @@ __global__ void __launch_bounds__(kThreads, 1) k_norm_bwd_sums(NormArgs a, int64
         }
 }
 
-template <typename T, int V, bool SILU>
-__global__ void __launch_bounds__(kThreads, 1) k_norm_bwd_apply(NormArgs a, int64_t rows, Ws w)
+template <typename T, int V, bool DENSE, bool SILU>
+__global__ void __launch_bounds__(Feed<T, V, 2, DENSE>::kBlockThreads, 1) k_norm_bwd_apply(NormArgs a, int64_t rows, Ws w, uint64_t wait_ns)
 {
     extern __shared__ __align__(16) uint8_t s_raw[];
-    using S = Stream<T, V, 2>;
+    using S = Feed<T, V, 2, DENSE>;
     float2* s_stat = reinterpret_cast<float2*>(s_raw + S::kSmem);
     int32_t* s_seg = reinterpret_cast<int32_t*>(s_stat + a.groups);
     const Place<V> at(a, rows);
     const bool works = at.tr < at.rt;
     T* dx = static_cast<T*>(a.out) + at.tv * V;
-    S in(a, s_raw);
-    in.src[0] = static_cast<const T*>(a.x) + at.tv * V;
-    in.src[1] = static_cast<const T*>(a.dy) + at.tv * V;
+    S in(a, s_raw, wait_ns, at.vpr, at.rt, at.tr);
+    const T* const tensor[2] = {static_cast<const T*>(a.x), static_cast<const T*>(a.dy)};
+    in.step = -1;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) in.base[t] = tensor[t] + at.tv * V;
     load_offsets(a, s_seg, false);
+    if (DENSE && at.warp == kThreads / 32) {
+        if (at.lane == 0) {
+            for (int64_t r0 = at.end; r0 > at.begin;) {
+                const Run k = run_before(a, s_seg, at.begin, r0);
+                r0 = k.lo;
+                if (k.s >= 0) in.load(k, tensor);
+            }
+            in.drain();
+        }
+        return;
+    }
     const float least = least_of(a.act);
     bool waited = false;
     for (int64_t r0 = at.end; r0 > at.begin;) {
@@ -794,11 +903,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_norm_bwd_apply(NormArgs a, int6
                 }
             continue;
         }
-        if (works) in.begin(k.hi - 1 - at.tr, -at.rt, k.lo, k.hi);  // on their way meanwhile
+        in.begin(k);
         if (!waited) wait_for_first_kernel();
         waited = true;
         const Span span(s_seg, k.s, rows);
-        __syncthreads();
+        sync_workers();
         for (int g = at.warp; g < a.groups; g += kThreads / 32) {
             float2 m = make_float2(0.f, 0.f);
             if (span.first == span.last) {
@@ -815,8 +924,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_norm_bwd_apply(NormArgs a, int6
             const float n = (float)(span.hi - span.lo) * (float)at.per;
             if (at.lane == 0) s_stat[g] = make_float2(m.x / n, m.y / n);
         }
-        __syncthreads();
-        if (!works) continue;
+        sync_workers();
         F2 minus[kPairs<V>], scale[kPairs<V>], shift[kPairs<V>], lift[kPairs<V>], tilt[kPairs<V>];
         const float* mean = a.mean + (int64_t)k.s * a.groups;
         const float* rstd = a.rstd + (int64_t)k.s * a.groups;
@@ -835,24 +943,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_norm_bwd_apply(NormArgs a, int6
             const float r = __ldg(rstd + g);
             return -r * r * s_stat[g].y;
         });
-        for (; in.more(); in.advance()) {
-            in.wait();
+        in.run(works, [&](F2 (&f)[2][kPairs<V>], int64_t row) {
 #pragma unroll
-            for (int q = 0; q < kUnroll; ++q) {
-                const int32_t row = in.row(q);
-                if (row < 0) continue;
-                F2 f[kPairs<V>], d[kPairs<V>];
-                in.get(q, 0, f);
-                in.get(q, 1, d);
-#pragma unroll
-                for (int j = 0; j < kPairs<V>; ++j) {
-                    const F2 e = add(f[j], minus[j]);
-                    const F2 dz = through<SILU>(d[j], fma(e, scale[j], shift[j]), least);
-                    f[j] = fma(dz, scale[j], fma(e, tilt[j], lift[j]));
-                }
-                *reinterpret_cast<Vec<T, V>*>(dx + (int64_t)row * a.c) = pack<T, V>(f);
+            for (int j = 0; j < kPairs<V>; ++j) {
+                const F2 e = add(f[0][j], minus[j]);
+                const F2 dz = through<SILU>(f[1][j], fma(e, scale[j], shift[j]), least);
+                f[0][j] = fma(dz, scale[j], fma(e, tilt[j], lift[j]));
             }
-        }
+            *reinterpret_cast<Vec<T, V>*>(dx + row * a.c) = pack<T, V>(f[0]);
+        });
     }
     if (!waited) wait_for_first_kernel();
     // dgamma and dbeta: a warp for each channel
@@ -1051,13 +1150,13 @@ size_t carve(int64_t n, int32_t c, int32_t segments, int32_t groups, char* base,
 
 // second: the second kernel of a pass, which waits for the first one itself.
 template <typename K>
-spc_status launch(K* kernel, int shares, size_t smem, cudaStream_t st, const NormArgs& a, int64_t rows, const Ws& w,
+spc_status launch(K* kernel, int shares, int threads, size_t smem, cudaStream_t st, const NormArgs& a, int64_t rows, const Ws& w,
                   bool second)
 {
     SPC_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)shares);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -1065,30 +1164,40 @@ spc_status launch(K* kernel, int shares, size_t smem, cudaStream_t st, const Nor
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = second ? 1 : 0;
-    SPC_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, a, rows, w));
+    SPC_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, a, rows, w, wait_limit_ns()));
     return SPC_OK;
 }
 
-template <typename T, int V, bool SILU>
+template <typename T, int V, bool DENSE, bool SILU>
 spc_status rows_pass(const NormArgs& a, const Ws& w, bool backward, cudaStream_t st)
 {
     const int shares = shares_of(a.n);
     const int64_t rows = std::max<int64_t>(1, ceil_div(a.n, shares));
     const size_t offsets = sizeof(int32_t) * (a.segments + 1), stat = sizeof(float2) * a.groups;
     if (backward) {
-        const size_t base = Stream<T, V, 2>::kSmem + offsets;
-        const spc_status s = launch(k_norm_bwd_sums<T, V, SILU>, shares, base, st, a, rows, w, false);
-        return s != SPC_OK ? s : launch(k_norm_bwd_apply<T, V, SILU>, shares, base + stat, st, a, rows, w, true);
+        using F = Feed<T, V, 2, DENSE>;
+        const size_t base = F::kSmem + offsets;
+        const spc_status s = launch(k_norm_bwd_sums<T, V, DENSE, SILU>, shares, F::kBlockThreads,
+                                    base + sizeof(float) * 2 * kThreads * V, st, a, rows, w, false);
+        return s != SPC_OK ? s : launch(k_norm_bwd_apply<T, V, DENSE, SILU>, shares, F::kBlockThreads, base + stat, st, a, rows, w, true);
     }
-    const size_t base = Stream<T, V, 1>::kSmem + offsets;
-    const spc_status s = launch(k_norm_stats<T, V>, shares, base + sizeof(float) * a.c, st, a, rows, w, false);
-    return s != SPC_OK || a.n == 0 ? s : launch(k_norm_apply<T, V, SILU>, shares, base + stat, st, a, rows, w, true);
+    using F = Feed<T, V, 1, DENSE>;
+    const size_t base = F::kSmem + offsets;
+    const spc_status s = launch(k_norm_stats<T, V, DENSE>, shares, F::kBlockThreads,
+                                base + sizeof(float) * (kThreads * V + a.c), st, a, rows, w, false);
+    return s != SPC_OK || a.n == 0
+               ? s
+               : launch(k_norm_apply<T, V, DENSE, SILU>, shares, F::kBlockThreads, base + stat, st, a, rows, w, true);
 }
 
 template <typename T, int V>
 spc_status rows_pass(const NormArgs& a, const Ws& w, bool backward, cudaStream_t st)
 {
-    return a.act == SPC_ACT_SILU ? rows_pass<T, V, true>(a, w, backward, st) : rows_pass<T, V, false>(a, w, backward, st);
+    const bool silu = a.act == SPC_ACT_SILU;
+    // the form for rows in order exists for whole 16-byte vectors; the other takes any
+    if constexpr (V * sizeof(T) == 16)
+        if (!a.order) return silu ? rows_pass<T, V, true, true>(a, w, backward, st) : rows_pass<T, V, true, false>(a, w, backward, st);
+    return silu ? rows_pass<T, V, false, true>(a, w, backward, st) : rows_pass<T, V, false, false>(a, w, backward, st);
 }
 
 template <typename T>
