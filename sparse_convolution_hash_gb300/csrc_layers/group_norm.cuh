@@ -143,18 +143,19 @@ __device__ __forceinline__ void gather_pairs(F2 (&f)[kPairs<V>], F value)
 // ------------------------------------------------------------------- activations
 // 1 / (1 + exp(-z)) with the hardware's exp2 and reciprocal: within 2^-19 for the |z| of a
 // normalised feature, a small part of the rounding of a 16-bit output (the exact functions cost
-// the 498,145 x 64 bf16 forward 95 us against 82, all else equal).
+// the 498,145 x 64 bf16 forward 95 us against 82, all else equal).  The special-function unit has a
+// quarter of the rate that this needs, so the pair shares one reciprocal, 1 / a = b / (a b);
+// exp is held to 2^57 for that, where the sigmoid is 0 to 17 digits.
 __device__ __forceinline__ F2 sigmoid(F2 z)
 {
     const F2 t = mul(z, both(-1.4426950408889634f));
     F2 e;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(fminf(t.x, 57.f)));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(fminf(t.y, 57.f)));
     e = add(e, both(1.f));
-    F2 s;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.x) : "f"(e.x));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.y) : "f"(e.y));
-    return s;
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(e.x * e.y));
+    return mul(both(r), F2{e.y, e.x});
 }
 
 // SILU, or max(z, floor): floor 0 for RELU, -infinity for none (a NaN passes).
@@ -292,7 +293,7 @@ template <typename T, int V, int N, bool DENSE>
 struct Feed {
     static constexpr int kRowsOf = DENSE ? 4 / N : 4;                        // rows of a thread per stage
     static constexpr int kStage = kRowsOf * N * kThreads * (int)sizeof(T) * V;  // bytes
-    static constexpr int kStages = 5;
+    static constexpr int kStages = 6 - N;
     static constexpr size_t kSmem = DENSE ? (size_t)kStages * kStage + 2 * kStages * sizeof(uint64_t) : 0;
     static constexpr int kBlockThreads = DENSE ? kThreads + 32 : kThreads;
 
@@ -447,49 +448,94 @@ struct Feed {
 };
 
 // ------------------------------------------------------------------ column sums
-// Sums over the rt row threads of N values per channel: afterwards value k of channel ch
-// stands at column_at<V>(k, ch).  Planes of up to four channels keep the accesses whole.
-template <int V> constexpr int kPart = V >= 4 ? 4 : V;
-template <int V>
-__device__ __forceinline__ int column_at(int k, int ch)
-{
-    return ((k * (V / kPart<V>) + ch % V / kPart<V>) * kThreads + ch / V) * kPart<V> + ch % kPart<V>;
-}
-template <int V, int N>
-__device__ __forceinline__ void column_sums(const F2 (&v)[N][kPairs<V>], float* s, int tr, int rt, int vpr)
-{
-    constexpr int P = kPart<V>, H = V / P;
-    using W = Vec<float, P>;
-    W* w = reinterpret_cast<W*>(s);
-    sync_workers();
-#pragma unroll
-    for (int k = 0; k < N; ++k)
-#pragma unroll
-        for (int h = 0; h < H; ++h) {
-            W u;
-#pragma unroll
-            for (int j = 0; j < P; ++j) {
-                const F2 f = v[k][(h * P + j) / 2];
-                u.e[j] = (h * P + j) % 2 ? f.y : f.x;
-            }
-            w[(k * H + h) * kThreads + threadIdx.x] = u;
-        }
-    int half = 1;
-    while (half < rt) half <<= 1;
-    for (half >>= 1; half; half >>= 1) {
-        sync_workers();
-        if (tr < half && tr + half < rt)
-#pragma unroll
-            for (int k = 0; k < N * H; ++k) {
-                W a = w[k * kThreads + threadIdx.x];
-                const W b = w[k * kThreads + threadIdx.x + half * vpr];
-#pragma unroll
-                for (int j = 0; j < P; ++j) a.e[j] += b.e[j];
-                w[k * kThreads + threadIdx.x] = a;
-            }
+// A sum that carries the rounding errors of its additions along (Knuth's two-sum).
+struct Exact {
+    float s = 0.f, e = 0.f;
+    __device__ __forceinline__ void add(float v)
+    {
+        const float t = s + v, z = t - s;
+        e += (s - (t - z)) + (v - z);
+        s = t;
     }
+    __device__ __forceinline__ float value() const { return e == e ? s + e : s; }  // s itself once it is not finite
+};
+
+// Sums over the rt row threads of N values per channel, into s_out [N][c].  The threads
+// lay their values out by row and channel; each then adds a stretch of one channel's rows, and
+// the stretches are added in turn: two short steps whatever c is.  The additions are exact to
+// twice the digits, so that a mean hardly depends on how rows were dealt out to threads.  s: kSums<V, N> floats.
+template <int V, int N> constexpr int kSums = N * kThreads * (V + 1);
+template <int V, int N>
+__device__ __forceinline__ void column_sums(const F2 (&v)[N][kPairs<V>], float* s, float* s_out, int c, int tr, int tv, int rt)
+{
+    constexpr int P = V >= 4 ? 4 : V;
+    using W = Vec<float, P>;
+    const int plane = rt * c;
+    if (tr < rt)
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+#pragma unroll
+            for (int h = 0; h < V / P; ++h) {
+                W u;
+#pragma unroll
+                for (int j = 0; j < P; ++j) {
+                    const F2 f = v[k][(h * P + j) / 2];
+                    u.e[j] = (h * P + j) % 2 ? f.y : f.x;
+                }
+                *reinterpret_cast<W*>(s + k * plane + tr * c + tv * V + h * P) = u;
+            }
+    sync_workers();
+    if (c >= kThreads) {
+        for (int ch = threadIdx.x; ch < c; ch += kThreads)
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                Exact t;
+                for (int r = 0; r < rt; ++r) t.add(s[k * plane + r * c + ch]);
+                s_out[k * c + ch] = t.value();
+            }
+        sync_workers();
+        return;
+    }
+    const int parts = kThreads / c, len = (rt + parts - 1) / parts;
+    const int part = (int)threadIdx.x / c, ch = (int)threadIdx.x % c;
+    float* s_part = s + N * plane;  // [N][parts][c]
+    if (part < parts)
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            Exact t;
+            const int to = (part + 1) * len < rt ? (part + 1) * len : rt;
+#pragma unroll 4
+            for (int r = part * len; r < to; ++r) t.add(s[k * plane + r * c + ch]);
+            s_part[(k * parts + part) * c + ch] = t.value();
+        }
+    sync_workers();
+    if ((int)threadIdx.x < c)
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            Exact t;
+#pragma unroll 4
+            for (int q = 0; q < parts; ++q) t.add(s_part[(k * parts + q) * c + ch]);
+            s_out[k * c + ch] = t.value();
+        }
     sync_workers();
 }
+
+// Calls f(g, j0, step) for every group: a thread for itself, or a warp's lanes together where
+// groups are wide; `sum` then adds up what f gathered.
+constexpr int kNarrow = 16;
+__device__ __forceinline__ float warp_sum(float v);
+__device__ __forceinline__ float group_sum(float v, int per) { return per <= kNarrow ? v : warp_sum(v); }
+struct GroupLoop {
+    int g, step, lane, lanes;
+    __device__ __forceinline__ explicit GroupLoop(int per)
+    {
+        const bool narrow = per <= kNarrow;
+        g = narrow ? threadIdx.x : threadIdx.x >> 5;
+        step = narrow ? kThreads : kThreads / 32;
+        lane = narrow ? 0 : threadIdx.x & 31;
+        lanes = narrow ? 1 : 32;
+    }
+};
 
 __device__ __forceinline__ float warp_sum(float v)
 {
@@ -536,8 +582,9 @@ __global__ void __launch_bounds__(Feed<T, V, 1, DENSE>::kBlockThreads, 1) k_norm
     extern __shared__ __align__(16) uint8_t s_raw[];
     using S = Feed<T, V, 1, DENSE>;
     float* s_sum = reinterpret_cast<float*>(s_raw + S::kSmem);
-    float* s_mean = s_sum + kThreads * V;
-    int32_t* s_seg = reinterpret_cast<int32_t*>(s_mean + a.c);
+    float* s_mean = s_sum + kSums<V, 1>;  // channel means, and sums of squares around them
+    float* s_m2 = s_mean + a.c;
+    int32_t* s_seg = reinterpret_cast<int32_t*>(s_m2 + a.c);
     const Place<V> at(a, rows);
     const bool works = at.tr < at.rt;
     S in(a, s_raw, wait_ns, at.vpr, at.rt, at.tr);
@@ -588,17 +635,17 @@ __global__ void __launch_bounds__(Feed<T, V, 1, DENSE>::kBlockThreads, 1) k_norm
             }
         });
         // channel means around the run's first row, then squares around the channel means
-        const float n = (float)(k.hi - k.lo), mine = (float)count;
+        const float n = (float)(int)(k.hi - k.lo), mine = (float)count;
         F2 v[1][kPairs<V>];
 #pragma unroll
         for (int j = 0; j < kPairs<V>; ++j)
             v[0][j] = F2{fmaf(mine, pivot[0][j].x - lead[j].x, s1[j].x), fmaf(mine, pivot[0][j].y - lead[j].y, s1[j].y)};
-        column_sums<V, 1>(v, s_sum, at.tr, at.rt, at.vpr);
+        column_sums<V, 1>(v, s_sum, s_mean, a.c, at.tr, at.tv, at.rt);
         if (at.tr == 0)
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 const float b = j % 2 ? lead[j / 2].y : lead[j / 2].x;
-                s_mean[at.tv * V + j] = b + s_sum[column_at<V>(0, at.tv * V + j)] / n;
+                s_mean[at.tv * V + j] = b + s_mean[at.tv * V + j] / n;
             }
         sync_workers();
 #pragma unroll
@@ -614,22 +661,23 @@ __global__ void __launch_bounds__(Feed<T, V, 1, DENSE>::kBlockThreads, 1) k_norm
                 if (2 * j + 1 < V) v[0][j].y = square(pivot[0][j].y, s1[j].y, s2[j].y, at.tv * V + 2 * j + 1);
             }
         }
-        column_sums<V, 1>(v, s_sum, at.tr, at.rt, at.vpr);
-        // channels to groups, a warp each
+        column_sums<V, 1>(v, s_sum, s_m2, a.c, at.tr, at.tv, at.rt);
+        // channels to groups
         const Span span(s_seg, k.s, rows);
-        for (int g = at.warp; g < a.groups; g += kThreads / 32) {
+        const GroupLoop way(at.per);
+        for (int g = way.g; g < a.groups; g += way.step) {
             const int ch0 = g * at.per;
-            const float first = s_mean[ch0];
+            const float lead0 = s_mean[ch0];
             float m = 0.f;
-            for (int j = at.lane; j < at.per; j += 32) m += s_mean[ch0 + j] - first;
-            const float mean = first + warp_sum(m) / (float)at.per;
+            for (int j = way.lane; j < at.per; j += way.lanes) m += s_mean[ch0 + j] - lead0;
+            const float mean = lead0 + group_sum(m, at.per) / (float)at.per;
             float q = 0.f;
-            for (int j = at.lane; j < at.per; j += 32) {
+            for (int j = way.lane; j < at.per; j += way.lanes) {
                 const float d = s_mean[ch0 + j] - mean;
-                q += s_sum[column_at<V>(0, ch0 + j)] + n * d * d;
+                q += s_m2[ch0 + j] + n * d * d;
             }
-            q = warp_sum(q);
-            if (at.lane == 0) {
+            q = group_sum(q, at.per);
+            if (way.lane == 0) {
                 if (span.first == span.last) {
                     a.mean[(int64_t)k.s * a.groups + g] = mean;
                     a.rstd[(int64_t)k.s * a.groups + g] = 1.f / sqrtf(q / (n * (float)at.per) + a.eps);
@@ -642,59 +690,73 @@ __global__ void __launch_bounds__(Feed<T, V, 1, DENSE>::kBlockThreads, 1) k_norm
     }
 }
 
+// Sixteen lanes join the parts of a group; sums over them.
+constexpr int kJoin = 16;
+__device__ __forceinline__ float join_sum(float v)
+{
+#pragma unroll
+    for (int d = kJoin / 2; d; d >>= 1) v += __shfl_xor_sync(FULL_MASK, v, d);
+    return v;
+}
+
 // (mean, rstd) of segment s into s_stat [groups], from the parts where several CTAs
 // share it; the CTA that holds its first position also writes them out.
 __device__ __forceinline__ void join_stats(const NormArgs& a, const int32_t* s_seg, int s, int64_t rows, const float2* part,
                                            float2* s_stat)
 {
     const Span span(s_seg, s, rows);
-    const int per = a.c / a.groups, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int per = a.c / a.groups, lane = threadIdx.x % kJoin;
     sync_workers();
-    for (int g = warp; g < a.groups; g += kThreads / 32) {
-        float mean, rstd;
+    // all lanes of a warp go round as often: the shuffles are the warp's
+    for (int g0 = 0; g0 < a.groups; g0 += kThreads / kJoin) {
+        const int g = g0 + (int)threadIdx.x / kJoin;
+        const bool real = g < a.groups;
+        float mean = 0.f, rstd = 0.f;
         if (span.first == span.last) {
-            mean = a.mean[(int64_t)s * a.groups + g];
-            rstd = a.rstd[(int64_t)s * a.groups + g];
+            if (real && lane == 0) {
+                mean = a.mean[(int64_t)s * a.groups + g];
+                rstd = a.rstd[(int64_t)s * a.groups + g];
+            }
         } else {
-            constexpr int kKeep = 5;  // parts of a lane kept in registers: 160 CTAs
+            constexpr int kKeep = 10;  // parts of a lane kept in registers: 160 CTAs
             float2 v[kKeep];
             float cnt[kKeep];
 #pragma unroll
             for (int i = 0; i < kKeep; ++i) {
-                const int c = span.first + lane + 32 * i;
+                const int c = span.first + lane + kJoin * i;
                 v[i] = make_float2(0.f, 0.f);
                 cnt[i] = 0.f;
-                if (c <= span.last) {
+                if (real && c <= span.last) {
                     v[i] = part[(int64_t)span.slot(c, rows) * a.groups + g];
-                    cnt[i] = (float)span.count(c, rows);
+                    cnt[i] = (float)(int)span.count(c, rows);
                 }
             }
-            const float base = __shfl_sync(FULL_MASK, v[0].x, 0);
+            const float base = __shfl_sync(FULL_MASK, v[0].x, (int)threadIdx.x & 16);
             float m = 0.f;
 #pragma unroll
             for (int i = 0; i < kKeep; ++i) m += cnt[i] > 0.f ? cnt[i] * (v[i].x - base) : 0.f;
-            for (int c = span.first + lane + 32 * kKeep; c <= span.last; c += 32)
-                m += (float)span.count(c, rows) * (part[(int64_t)span.slot(c, rows) * a.groups + g].x - base);
-            const float n = (float)(span.hi - span.lo);
-            mean = base + warp_sum(m) / n;
+            for (int c = span.first + lane + kJoin * kKeep; real && c <= span.last; c += kJoin)
+                m += (float)(int)span.count(c, rows) * (part[(int64_t)span.slot(c, rows) * a.groups + g].x - base);
+            const float n = (float)(int)(span.hi - span.lo);
+            mean = base + join_sum(m) / n;
             float q = 0.f;
 #pragma unroll
             for (int i = 0; i < kKeep; ++i) {
                 const float d = v[i].x - mean;
                 q += cnt[i] > 0.f ? v[i].y + cnt[i] * (float)per * d * d : 0.f;
             }
-            for (int c = span.first + lane + 32 * kKeep; c <= span.last; c += 32) {
+            for (int c = span.first + lane + kJoin * kKeep; real && c <= span.last; c += kJoin) {
                 const float2 u = part[(int64_t)span.slot(c, rows) * a.groups + g];
                 const float d = u.x - mean;
-                q += u.y + (float)span.count(c, rows) * (float)per * d * d;
+                q += u.y + (float)(int)span.count(c, rows) * (float)per * d * d;
             }
-            rstd = 1.f / sqrtf(warp_sum(q) / (n * (float)per) + a.eps);
-            if (lane == 0 && (int)blockIdx.x == span.first) {
+            rstd = 1.f / sqrtf(join_sum(q) / (n * (float)per) + a.eps);
+            if (real && lane == 0 && (int)blockIdx.x == span.first) {
                 a.mean[(int64_t)s * a.groups + g] = mean;
                 a.rstd[(int64_t)s * a.groups + g] = rstd;
             }
         }
-        if (lane == 0) s_stat[g] = make_float2(mean, rstd);
+        if (real && lane == 0) s_stat[g] = make_float2(mean, rstd);
     }
     sync_workers();
 }
@@ -772,7 +834,8 @@ __global__ void __launch_bounds__(Feed<T, V, 2, DENSE>::kBlockThreads, 1) k_norm
     extern __shared__ __align__(16) uint8_t s_raw[];
     using S = Feed<T, V, 2, DENSE>;
     float* s_sum = reinterpret_cast<float*>(s_raw + S::kSmem);
-    int32_t* s_seg = reinterpret_cast<int32_t*>(s_sum + 2 * kThreads * V);
+    float* s_dz = s_sum + kSums<V, 2>;  // [2][c]
+    int32_t* s_seg = reinterpret_cast<int32_t*>(s_dz + 2 * a.c);
     const Place<V> at(a, rows);
     const bool works = at.tr < at.rt;
     S in(a, s_raw, wait_ns, at.vpr, at.rt, at.tr);
@@ -827,25 +890,26 @@ __global__ void __launch_bounds__(Feed<T, V, 2, DENSE>::kBlockThreads, 1) k_norm
 #pragma unroll
             for (int j = 0; j < kPairs<V>; ++j) sum[1][j] = mul(sum[1][j], r[j]);
         }
-        column_sums<V, 2>(sum, s_sum, at.tr, at.rt, at.vpr);
+        column_sums<V, 2>(sum, s_sum, s_dz, a.c, at.tr, at.tv, at.rt);
         if (at.tr == 0)
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                all[0][j] += s_sum[column_at<V>(0, at.tv * V + j)];
-                all[1][j] += s_sum[column_at<V>(1, at.tv * V + j)];
+                all[0][j] += s_dz[at.tv * V + j];
+                all[1][j] += s_dz[a.c + at.tv * V + j];
             }
         const Span span(s_seg, k.s, rows);
-        for (int g = at.warp; g < a.groups; g += kThreads / 32) {
+        const GroupLoop way(at.per);
+        for (int g = way.g; g < a.groups; g += way.step) {
             float m0 = 0.f, m1 = 0.f;
-            for (int j = at.lane; j < at.per; j += 32) {
+            for (int j = way.lane; j < at.per; j += way.lanes) {
                 const int ch = g * at.per + j;
                 const float u = a.gamma ? __ldg(a.gamma + ch) : 1.f;
-                m0 = fmaf(u, s_sum[column_at<V>(0, ch)], m0);
-                m1 = fmaf(u, s_sum[column_at<V>(1, ch)], m1);
+                m0 = fmaf(u, s_dz[ch], m0);
+                m1 = fmaf(u, s_dz[a.c + ch], m1);
             }
-            m0 = warp_sum(m0);
-            m1 = warp_sum(m1);
-            if (at.lane == 0) {
+            m0 = group_sum(m0, at.per);
+            m1 = group_sum(m1, at.per);
+            if (way.lane == 0) {
                 if (span.first == span.last) w.coef[(int64_t)k.s * a.groups + g] = make_float2(m0, m1);
                 else w.part[(int64_t)span.slot(blockIdx.x, rows) * a.groups + g] = make_float2(m0, m1);
             }
@@ -908,21 +972,24 @@ __global__ void __launch_bounds__(Feed<T, V, 2, DENSE>::kBlockThreads, 1) k_norm
         waited = true;
         const Span span(s_seg, k.s, rows);
         sync_workers();
-        for (int g = at.warp; g < a.groups; g += kThreads / 32) {
+        for (int g0 = 0; g0 < a.groups; g0 += kThreads / kJoin) {
+            const int g = g0 + (int)threadIdx.x / kJoin, lane = threadIdx.x % kJoin;
+            const bool real = g < a.groups;
             float2 m = make_float2(0.f, 0.f);
             if (span.first == span.last) {
-                m = w.coef[(int64_t)k.s * a.groups + g];
+                if (real && lane == 0) m = w.coef[(int64_t)k.s * a.groups + g];
             } else {
-                for (int c = span.first + at.lane; c <= span.last; c += 32) {
+#pragma unroll 10
+                for (int c = span.first + lane; real && c <= span.last; c += kJoin) {
                     const float2 v = w.part[(int64_t)span.slot(c, rows) * a.groups + g];
                     m.x += v.x;
                     m.y += v.y;
                 }
-                m.x = warp_sum(m.x);
-                m.y = warp_sum(m.y);
+                m.x = join_sum(m.x);
+                m.y = join_sum(m.y);
             }
-            const float n = (float)(span.hi - span.lo) * (float)at.per;
-            if (at.lane == 0) s_stat[g] = make_float2(m.x / n, m.y / n);
+            const float n = (float)(int)(span.hi - span.lo) * (float)at.per;
+            if (real && lane == 0) s_stat[g] = make_float2(m.x / n, m.y / n);
         }
         sync_workers();
         F2 minus[kPairs<V>], scale[kPairs<V>], shift[kPairs<V>], lift[kPairs<V>], tilt[kPairs<V>];
@@ -1178,13 +1245,13 @@ spc_status rows_pass(const NormArgs& a, const Ws& w, bool backward, cudaStream_t
         using F = Feed<T, V, 2, DENSE>;
         const size_t base = F::kSmem + offsets;
         const spc_status s = launch(k_norm_bwd_sums<T, V, DENSE, SILU>, shares, F::kBlockThreads,
-                                    base + sizeof(float) * 2 * kThreads * V, st, a, rows, w, false);
+                                    base + sizeof(float) * (kSums<V, 2> + 2 * a.c), st, a, rows, w, false);
         return s != SPC_OK ? s : launch(k_norm_bwd_apply<T, V, DENSE, SILU>, shares, F::kBlockThreads, base + stat, st, a, rows, w, true);
     }
     using F = Feed<T, V, 1, DENSE>;
     const size_t base = F::kSmem + offsets;
     const spc_status s = launch(k_norm_stats<T, V, DENSE>, shares, F::kBlockThreads,
-                                base + sizeof(float) * (kThreads * V + a.c), st, a, rows, w, false);
+                                base + sizeof(float) * (kSums<V, 1> + 2 * a.c), st, a, rows, w, false);
     return s != SPC_OK || a.n == 0
                ? s
                : launch(k_norm_apply<T, V, DENSE, SILU>, shares, F::kBlockThreads, base + stat, st, a, rows, w, true);
