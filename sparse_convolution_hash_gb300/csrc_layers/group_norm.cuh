@@ -233,6 +233,10 @@ __device__ __forceinline__ int find_segment(const int32_t* s_seg, int segments, 
 struct Run {
     int s;           // segment, -1: none
     int64_t lo, hi;  // its positions in this CTA's share
+    // Whether the share [begin, end) holds all of the segment.
+    __device__ __forceinline__ bool whole(const int32_t* s_seg) const { return lo == s_seg[s] && hi >= s_seg[s + 1]; }
+    // Where its part goes: a share's first slot if it begins with the share, else its second.
+    __device__ __forceinline__ int slot(int64_t begin) const { return 2 * (int)blockIdx.x + (lo > begin ? 1 : 0); }
 };
 
 // The run that begins at position r of a share that ends at `end`.
@@ -269,8 +273,8 @@ struct Span {
     {
         lo = s_seg[s];
         hi = s_seg[s + 1] > lo ? s_seg[s + 1] : lo;
-        first = (int)(lo / rows);
-        last = hi > lo ? (int)((hi - 1) / rows) : first;
+        first = (int)((uint32_t)lo / (uint32_t)rows);
+        last = hi > lo ? (int)((uint32_t)(hi - 1) / (uint32_t)rows) : first;
     }
     __device__ __forceinline__ int64_t count(int c, int64_t rows) const
     {
@@ -460,68 +464,79 @@ struct Exact {
     __device__ __forceinline__ float value() const { return e == e ? s + e : s; }  // s itself once it is not finite
 };
 
+// Values from, from + stride, ... (count of them), eight loads at a time.  The additions are
+// exact to twice the digits, so that a mean hardly depends on how rows were dealt out to threads.
+__device__ __forceinline__ float stretch(const float* from, int stride, int count)
+{
+    Exact all;
+    for (int r = 0; r < count; r += 8) {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = r + i < count ? from[(r + i) * stride] : 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) all.add(v[i]);
+    }
+    return all.value();
+}
+
 // Sums over the rt row threads of N values per channel, into s_out [N][c].  The threads
 // lay their values out by row and channel; each then adds a stretch of one channel's rows, and
-// the stretches are added in turn: two short steps whatever c is.  The additions are exact to
-// twice the digits, so that a mean hardly depends on how rows were dealt out to threads.  s: kSums<V, N> floats.
+// the stretches are added in turn: two short steps whatever c is, with their indexes worked
+// out once.  s: kSums<V, N> floats.
 template <int V, int N> constexpr int kSums = N * kThreads * (V + 1);
+struct Columns {
+    int c, rt, parts, len, part, ch;
+    __device__ __forceinline__ Columns(int c_, int rt_) : c(c_), rt(rt_)
+    {
+        parts = c < kThreads ? kThreads / c : 1;
+        len = (rt + parts - 1) / parts;
+        part = (int)threadIdx.x / c;
+        ch = (int)threadIdx.x - part * c;
+    }
+};
 template <int V, int N>
-__device__ __forceinline__ void column_sums(const F2 (&v)[N][kPairs<V>], float* s, float* s_out, int c, int tr, int tv, int rt)
+__device__ __forceinline__ void column_sums(const Columns& k, const F2 (&v)[N][kPairs<V>], float* s, float* s_out, int tr, int tv)
 {
     constexpr int P = V >= 4 ? 4 : V;
     using W = Vec<float, P>;
-    const int plane = rt * c;
-    if (tr < rt)
+    const int plane = k.rt * k.c;
+    if (tr < k.rt)
 #pragma unroll
-        for (int k = 0; k < N; ++k)
+        for (int n = 0; n < N; ++n)
 #pragma unroll
             for (int h = 0; h < V / P; ++h) {
                 W u;
 #pragma unroll
                 for (int j = 0; j < P; ++j) {
-                    const F2 f = v[k][(h * P + j) / 2];
+                    const F2 f = v[n][(h * P + j) / 2];
                     u.e[j] = (h * P + j) % 2 ? f.y : f.x;
                 }
-                *reinterpret_cast<W*>(s + k * plane + tr * c + tv * V + h * P) = u;
+                *reinterpret_cast<W*>(s + n * plane + tr * k.c + tv * V + h * P) = u;
             }
     sync_workers();
-    if (c >= kThreads) {
-        for (int ch = threadIdx.x; ch < c; ch += kThreads)
+    if (k.parts == 1) {
+        for (int ch = threadIdx.x; ch < k.c; ch += kThreads)
 #pragma unroll
-            for (int k = 0; k < N; ++k) {
-                Exact t;
-                for (int r = 0; r < rt; ++r) t.add(s[k * plane + r * c + ch]);
-                s_out[k * c + ch] = t.value();
-            }
+            for (int n = 0; n < N; ++n) s_out[n * k.c + ch] = stretch(s + n * plane + ch, k.c, k.rt);
         sync_workers();
         return;
     }
-    const int parts = kThreads / c, len = (rt + parts - 1) / parts;
-    const int part = (int)threadIdx.x / c, ch = (int)threadIdx.x % c;
     float* s_part = s + N * plane;  // [N][parts][c]
-    if (part < parts)
+    if (k.part < k.parts) {
+        const int r0 = k.part * k.len, left = k.rt - r0, count = left < k.len ? left : k.len;
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-            Exact t;
-            const int to = (part + 1) * len < rt ? (part + 1) * len : rt;
-#pragma unroll 4
-            for (int r = part * len; r < to; ++r) t.add(s[k * plane + r * c + ch]);
-            s_part[(k * parts + part) * c + ch] = t.value();
-        }
+        for (int n = 0; n < N; ++n)
+            s_part[(n * k.parts + k.part) * k.c + k.ch] = stretch(s + n * plane + r0 * k.c + k.ch, k.c, count);
+    }
     sync_workers();
-    if ((int)threadIdx.x < c)
+    if ((int)threadIdx.x < k.c)
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-            Exact t;
-#pragma unroll 4
-            for (int q = 0; q < parts; ++q) t.add(s_part[(k * parts + q) * c + ch]);
-            s_out[k * c + ch] = t.value();
-        }
+        for (int n = 0; n < N; ++n)
+            s_out[n * k.c + (int)threadIdx.x] = stretch(s_part + n * k.parts * k.c + (int)threadIdx.x, k.c, k.parts);
     sync_workers();
 }
 
-// Calls f(g, j0, step) for every group: a thread for itself, or a warp's lanes together where
-// groups are wide; `sum` then adds up what f gathered.
+// Who sums up a group: a thread for itself, or a warp's lanes together where groups are wide.
 constexpr int kNarrow = 16;
 __device__ __forceinline__ float warp_sum(float v);
 __device__ __forceinline__ float group_sum(float v, int per) { return per <= kNarrow ? v : warp_sum(v); }
@@ -558,6 +573,7 @@ struct Ws {
 template <int V>
 struct Place {
     int vpr, rt, tr, tv, per, warp, lane;
+    int group[V];        // of each of its channels
     int64_t begin, end;  // positions of this CTA
     __device__ __forceinline__ Place(const NormArgs& a, int64_t rows)
     {
@@ -569,6 +585,15 @@ struct Place {
         per = a.c / a.groups;
         warp = tid >> 5;
         lane = tid & 31;
+        int g = tv * V / per, r = tv * V - g * per;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            group[j] = g;
+            if (++r == per) {
+                r = 0;
+                ++g;
+            }
+        }
         begin = blockIdx.x * rows;
         end = begin + rows < a.n ? begin + rows : a.n;
     }
@@ -604,6 +629,7 @@ __global__ void __launch_bounds__(Feed<T, V, 1, DENSE>::kBlockThreads, 1) k_norm
         }
         return;
     }
+    const Columns columns(a.c, at.rt);
     // empty segments are finished here, a block each in turn
     for (int s = blockIdx.x; s < a.segments; s += gridDim.x)
         if (s_seg[s] >= s_seg[s + 1])
@@ -640,7 +666,7 @@ __global__ void __launch_bounds__(Feed<T, V, 1, DENSE>::kBlockThreads, 1) k_norm
 #pragma unroll
         for (int j = 0; j < kPairs<V>; ++j)
             v[0][j] = F2{fmaf(mine, pivot[0][j].x - lead[j].x, s1[j].x), fmaf(mine, pivot[0][j].y - lead[j].y, s1[j].y)};
-        column_sums<V, 1>(v, s_sum, s_mean, a.c, at.tr, at.tv, at.rt);
+        column_sums<V, 1>(columns, v, s_sum, s_mean, at.tr, at.tv);
         if (at.tr == 0)
 #pragma unroll
             for (int j = 0; j < V; ++j) {
@@ -651,8 +677,9 @@ __global__ void __launch_bounds__(Feed<T, V, 1, DENSE>::kBlockThreads, 1) k_norm
 #pragma unroll
         for (int j = 0; j < kPairs<V>; ++j) v[0][j] = both(0.f);
         if (works && count) {
+            const float inverse = 1.f / mine;
             auto square = [&](float p, float a1, float a2, int ch) -> float {
-                const float m = a1 / mine, d = (p - s_mean[ch]) + m, m2 = fmaf(-m, a1, a2);
+                const float m = a1 * inverse, d = (p - s_mean[ch]) + m, m2 = fmaf(-m, a1, a2);
                 return (m2 < 0.f ? 0.f : m2) + mine * d * d;
             };
 #pragma unroll
@@ -661,9 +688,10 @@ __global__ void __launch_bounds__(Feed<T, V, 1, DENSE>::kBlockThreads, 1) k_norm
                 if (2 * j + 1 < V) v[0][j].y = square(pivot[0][j].y, s1[j].y, s2[j].y, at.tv * V + 2 * j + 1);
             }
         }
-        column_sums<V, 1>(v, s_sum, s_m2, a.c, at.tr, at.tv, at.rt);
+        column_sums<V, 1>(columns, v, s_sum, s_m2, at.tr, at.tv);
         // channels to groups
-        const Span span(s_seg, k.s, rows);
+        const bool whole = k.whole(s_seg);
+        const int slot = k.slot(at.begin);
         const GroupLoop way(at.per);
         for (int g = way.g; g < a.groups; g += way.step) {
             const int ch0 = g * at.per;
@@ -678,11 +706,11 @@ __global__ void __launch_bounds__(Feed<T, V, 1, DENSE>::kBlockThreads, 1) k_norm
             }
             q = group_sum(q, at.per);
             if (way.lane == 0) {
-                if (span.first == span.last) {
+                if (whole) {
                     a.mean[(int64_t)k.s * a.groups + g] = mean;
                     a.rstd[(int64_t)k.s * a.groups + g] = 1.f / sqrtf(q / (n * (float)at.per) + a.eps);
                 } else {
-                    w.part[(int64_t)span.slot(blockIdx.x, rows) * a.groups + g] = make_float2(mean, q);
+                    w.part[(int64_t)slot * a.groups + g] = make_float2(mean, q);
                 }
             }
         }
@@ -699,64 +727,63 @@ __device__ __forceinline__ float join_sum(float v)
     return v;
 }
 
+// The parts of a shared segment, as their shares left them.
+struct Parts {
+    const float2* at;        // part of share `first`, group 0
+    int first, last, groups;
+    int odd;                 // the first part stands in its share's second slot
+    float rows, rows_first, rows_last;
+    __device__ __forceinline__ Parts(const Span& span, const float2* part, int64_t rows_, int groups_)
+        : first(span.first), last(span.last), groups(groups_)
+    {
+        const int slot = span.slot(first, rows_);
+        odd = slot & 1;
+        at = part + (int64_t)slot * groups;
+        rows = (float)(int)rows_;
+        rows_first = (float)(int)span.count(first, rows_);
+        rows_last = (float)(int)span.count(last, rows_);
+    }
+    // Part of share first + i.
+    __device__ __forceinline__ float2 get(int i, int g) const { return at[(2 * i - (i ? odd : 0)) * groups + g]; }
+    __device__ __forceinline__ int count() const { return last - first + 1; }
+    __device__ __forceinline__ float rows_of(int i) const { return i == 0 ? rows_first : first + i == last ? rows_last : rows; }
+};
+
 // (mean, rstd) of segment s into s_stat [groups], from the parts where several CTAs
-// share it; the CTA that holds its first position also writes them out.
+// share it; the CTA that holds its first position also writes them out.  Parts are taken around the
+// first one's mean: their means lie close together, so one pass over them will do.
 __device__ __forceinline__ void join_stats(const NormArgs& a, const int32_t* s_seg, int s, int64_t rows, const float2* part,
                                            float2* s_stat)
 {
     const Span span(s_seg, s, rows);
-    const int per = a.c / a.groups, lane = threadIdx.x % kJoin;
+    const int lane = threadIdx.x % kJoin;
+    const float per = (float)(a.c / a.groups);
     sync_workers();
     // all lanes of a warp go round as often: the shuffles are the warp's
     for (int g0 = 0; g0 < a.groups; g0 += kThreads / kJoin) {
-        const int g = g0 + (int)threadIdx.x / kJoin;
-        const bool real = g < a.groups;
-        float mean = 0.f, rstd = 0.f;
-        if (span.first == span.last) {
-            if (real && lane == 0) {
-                mean = a.mean[(int64_t)s * a.groups + g];
-                rstd = a.rstd[(int64_t)s * a.groups + g];
+        const int g = g0 + (int)threadIdx.x / kJoin, gr = g < a.groups ? g : 0;
+        float mean = a.mean[(int64_t)s * a.groups + gr], rstd = a.rstd[(int64_t)s * a.groups + gr];
+        if (span.first != span.last) {
+            const Parts parts(span, part, rows, a.groups);
+            const float base = parts.get(0, gr).x;
+            float m = 0.f, q = 0.f;
+#pragma unroll 5
+            for (int i = lane; i < parts.count(); i += kJoin) {
+                const float2 v = parts.get(i, gr);
+                const float n = parts.rows_of(i), d = v.x - base;
+                m = fmaf(n, d, m);
+                q += fmaf(n * per, d * d, v.y);
             }
-        } else {
-            constexpr int kKeep = 10;  // parts of a lane kept in registers: 160 CTAs
-            float2 v[kKeep];
-            float cnt[kKeep];
-#pragma unroll
-            for (int i = 0; i < kKeep; ++i) {
-                const int c = span.first + lane + kJoin * i;
-                v[i] = make_float2(0.f, 0.f);
-                cnt[i] = 0.f;
-                if (real && c <= span.last) {
-                    v[i] = part[(int64_t)span.slot(c, rows) * a.groups + g];
-                    cnt[i] = (float)(int)span.count(c, rows);
-                }
-            }
-            const float base = __shfl_sync(FULL_MASK, v[0].x, (int)threadIdx.x & 16);
-            float m = 0.f;
-#pragma unroll
-            for (int i = 0; i < kKeep; ++i) m += cnt[i] > 0.f ? cnt[i] * (v[i].x - base) : 0.f;
-            for (int c = span.first + lane + kJoin * kKeep; real && c <= span.last; c += kJoin)
-                m += (float)(int)span.count(c, rows) * (part[(int64_t)span.slot(c, rows) * a.groups + g].x - base);
-            const float n = (float)(int)(span.hi - span.lo);
-            mean = base + join_sum(m) / n;
-            float q = 0.f;
-#pragma unroll
-            for (int i = 0; i < kKeep; ++i) {
-                const float d = v[i].x - mean;
-                q += cnt[i] > 0.f ? v[i].y + cnt[i] * (float)per * d * d : 0.f;
-            }
-            for (int c = span.first + lane + kJoin * kKeep; real && c <= span.last; c += kJoin) {
-                const float2 u = part[(int64_t)span.slot(c, rows) * a.groups + g];
-                const float d = u.x - mean;
-                q += u.y + (float)(int)span.count(c, rows) * (float)per * d * d;
-            }
-            rstd = 1.f / sqrtf(join_sum(q) / (n * (float)per) + a.eps);
-            if (real && lane == 0 && (int)blockIdx.x == span.first) {
+            const float n = (float)(int)(span.hi - span.lo), shift = join_sum(m) / n;
+            mean = base + shift;
+            q = fmaf(-n * per * shift, shift, join_sum(q));
+            rstd = 1.f / sqrtf((q < 0.f ? 0.f : q) / (n * per) + a.eps);
+            if (g < a.groups && lane == 0 && (int)blockIdx.x == span.first) {
                 a.mean[(int64_t)s * a.groups + g] = mean;
                 a.rstd[(int64_t)s * a.groups + g] = rstd;
             }
         }
-        if (real && lane == 0) s_stat[g] = make_float2(mean, rstd);
+        if (g < a.groups && lane == 0) s_stat[g] = make_float2(mean, rstd);
     }
     sync_workers();
 }
@@ -788,6 +815,9 @@ __global__ void __launch_bounds__(Feed<T, V, 1, DENSE>::kBlockThreads, 1) k_norm
         }
         return;
     }
+    F2 gamma[kPairs<V>], beta[kPairs<V>];
+    gather_pairs<V>(gamma, [&](int j) { return works && a.gamma ? __ldg(a.gamma + at.tv * V + j) : 1.f; });
+    gather_pairs<V>(beta, [&](int j) { return works && a.beta ? __ldg(a.beta + at.tv * V + j) : 0.f; });
     const float floor = floor_of(a.act);
     bool waited = false;
     for (int64_t r0 = at.end; r0 > at.begin;) {
@@ -808,17 +838,17 @@ __global__ void __launch_bounds__(Feed<T, V, 1, DENSE>::kBlockThreads, 1) k_norm
         if (!waited) wait_for_first_kernel();
         waited = true;
         join_stats(a, s_seg, k.s, rows, w.part, s_stat);
-        F2 minus[kPairs<V>], scale[kPairs<V>], shift[kPairs<V>];
+        F2 minus[kPairs<V>], scale[kPairs<V>];
         gather_pairs<V>(scale, [&](int j) {
-            const int ch = at.tv * V + j;
-            return s_stat[ch / at.per].y * (a.gamma ? __ldg(a.gamma + ch) : 1.f);
+            return s_stat[at.group[j]].y;
         });
+#pragma unroll
+        for (int j = 0; j < kPairs<V>; ++j) scale[j] = mul(scale[j], gamma[j]);
         // the mean is taken off first: a constant channel gives beta exactly
-        gather_pairs<V>(minus, [&](int j) { return -s_stat[(at.tv * V + j) / at.per].x; });
-        gather_pairs<V>(shift, [&](int j) { return a.beta ? __ldg(a.beta + at.tv * V + j) : 0.f; });
+        gather_pairs<V>(minus, [&](int j) { return -s_stat[at.group[j]].x; });
         in.run(works, [&](F2 (&f)[1][kPairs<V>], int64_t row) {
 #pragma unroll
-            for (int j = 0; j < kPairs<V>; ++j) f[0][j] = activate<SILU>(fma(add(f[0][j], minus[j]), scale[j], shift[j]), floor);
+            for (int j = 0; j < kPairs<V>; ++j) f[0][j] = activate<SILU>(fma(add(f[0][j], minus[j]), scale[j], beta[j]), floor);
             *reinterpret_cast<Vec<T, V>*>(y + row * a.c) = pack<T, V>(f[0]);
         });
     }
@@ -855,6 +885,10 @@ __global__ void __launch_bounds__(Feed<T, V, 2, DENSE>::kBlockThreads, 1) k_norm
         }
         return;
     }
+    const Columns columns(a.c, at.rt);
+    F2 gamma[kPairs<V>], beta[kPairs<V>];
+    gather_pairs<V>(gamma, [&](int j) { return works && a.gamma ? __ldg(a.gamma + at.tv * V + j) : 1.f; });
+    gather_pairs<V>(beta, [&](int j) { return works && a.beta ? __ldg(a.beta + at.tv * V + j) : 0.f; });
     const float least = least_of(a.act);
     float all[2][V];
 #pragma unroll
@@ -863,41 +897,42 @@ __global__ void __launch_bounds__(Feed<T, V, 2, DENSE>::kBlockThreads, 1) k_norm
         const Run k = run_at(a, s_seg, r0, at.end);
         r0 = k.hi;
         if (k.s < 0) continue;
-        F2 minus[kPairs<V>], scale[kPairs<V>], shift[kPairs<V>], sum[2][kPairs<V>];
+        F2 minus[kPairs<V>], scale[kPairs<V>], sum[2][kPairs<V>];
 #pragma unroll
         for (int j = 0; j < kPairs<V>; ++j) sum[0][j] = sum[1][j] = both(0.f);
         in.begin(k);
         const float* mean = a.mean + (int64_t)k.s * a.groups;
         const float* rstd = a.rstd + (int64_t)k.s * a.groups;
-        gather_pairs<V>(minus, [&](int j) { return works ? -__ldg(mean + (at.tv * V + j) / at.per) : 0.f; });
+        gather_pairs<V>(minus, [&](int j) { return works ? -__ldg(mean + at.group[j]) : 0.f; });
         gather_pairs<V>(scale, [&](int j) {
-            const int ch = at.tv * V + j;
-            return works ? __ldg(rstd + ch / at.per) * (a.gamma ? __ldg(a.gamma + ch) : 1.f) : 0.f;
+            return works ? __ldg(rstd + at.group[j]) : 0.f;
         });
-        gather_pairs<V>(shift, [&](int j) { return works && a.beta ? __ldg(a.beta + at.tv * V + j) : 0.f; });
+#pragma unroll
+        for (int j = 0; j < kPairs<V>; ++j) scale[j] = mul(scale[j], gamma[j]);
         in.run(works, [&](const F2 (&f)[2][kPairs<V>], int64_t) {
 #pragma unroll
             for (int j = 0; j < kPairs<V>; ++j) {
                 const F2 e = add(f[0][j], minus[j]);
-                const F2 dz = through<SILU>(f[1][j], fma(e, scale[j], shift[j]), least);
+                const F2 dz = through<SILU>(f[1][j], fma(e, scale[j], beta[j]), least);
                 sum[0][j] = add(sum[0][j], dz);
                 sum[1][j] = fma(dz, e, sum[1][j]);
             }
         });
         if (works) {
             F2 r[kPairs<V>];
-            gather_pairs<V>(r, [&](int j) { return __ldg(rstd + (at.tv * V + j) / at.per); });
+            gather_pairs<V>(r, [&](int j) { return __ldg(rstd + at.group[j]); });
 #pragma unroll
             for (int j = 0; j < kPairs<V>; ++j) sum[1][j] = mul(sum[1][j], r[j]);
         }
-        column_sums<V, 2>(sum, s_sum, s_dz, a.c, at.tr, at.tv, at.rt);
+        column_sums<V, 2>(columns, sum, s_sum, s_dz, at.tr, at.tv);
         if (at.tr == 0)
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 all[0][j] += s_dz[at.tv * V + j];
                 all[1][j] += s_dz[a.c + at.tv * V + j];
             }
-        const Span span(s_seg, k.s, rows);
+        const bool whole = k.whole(s_seg);
+        const int slot = k.slot(at.begin);
         const GroupLoop way(at.per);
         for (int g = way.g; g < a.groups; g += way.step) {
             float m0 = 0.f, m1 = 0.f;
@@ -910,8 +945,8 @@ __global__ void __launch_bounds__(Feed<T, V, 2, DENSE>::kBlockThreads, 1) k_norm
             m0 = group_sum(m0, at.per);
             m1 = group_sum(m1, at.per);
             if (way.lane == 0) {
-                if (span.first == span.last) w.coef[(int64_t)k.s * a.groups + g] = make_float2(m0, m1);
-                else w.part[(int64_t)span.slot(blockIdx.x, rows) * a.groups + g] = make_float2(m0, m1);
+                if (whole) w.coef[(int64_t)k.s * a.groups + g] = make_float2(m0, m1);
+                else w.part[(int64_t)slot * a.groups + g] = make_float2(m0, m1);
             }
         }
         sync_workers();
@@ -951,6 +986,9 @@ __global__ void __launch_bounds__(Feed<T, V, 2, DENSE>::kBlockThreads, 1) k_norm
         }
         return;
     }
+    F2 gamma[kPairs<V>], beta[kPairs<V>];
+    gather_pairs<V>(gamma, [&](int j) { return works && a.gamma ? __ldg(a.gamma + at.tv * V + j) : 1.f; });
+    gather_pairs<V>(beta, [&](int j) { return works && a.beta ? __ldg(a.beta + at.tv * V + j) : 0.f; });
     const float least = least_of(a.act);
     bool waited = false;
     for (int64_t r0 = at.end; r0 > at.begin;) {
@@ -979,9 +1017,10 @@ __global__ void __launch_bounds__(Feed<T, V, 2, DENSE>::kBlockThreads, 1) k_norm
             if (span.first == span.last) {
                 if (real && lane == 0) m = w.coef[(int64_t)k.s * a.groups + g];
             } else {
-#pragma unroll 10
-                for (int c = span.first + lane; real && c <= span.last; c += kJoin) {
-                    const float2 v = w.part[(int64_t)span.slot(c, rows) * a.groups + g];
+                const Parts parts(span, w.part, rows, a.groups);
+#pragma unroll 5
+                for (int i = lane; i < parts.count(); i += kJoin) {
+                    const float2 v = parts.get(i, real ? g : 0);
                     m.x += v.x;
                     m.y += v.y;
                 }
@@ -992,21 +1031,21 @@ __global__ void __launch_bounds__(Feed<T, V, 2, DENSE>::kBlockThreads, 1) k_norm
             if (real && lane == 0) s_stat[g] = make_float2(m.x / n, m.y / n);
         }
         sync_workers();
-        F2 minus[kPairs<V>], scale[kPairs<V>], shift[kPairs<V>], lift[kPairs<V>], tilt[kPairs<V>];
+        F2 minus[kPairs<V>], scale[kPairs<V>], lift[kPairs<V>], tilt[kPairs<V>];
         const float* mean = a.mean + (int64_t)k.s * a.groups;
         const float* rstd = a.rstd + (int64_t)k.s * a.groups;
-        gather_pairs<V>(minus, [&](int j) { return -__ldg(mean + (at.tv * V + j) / at.per); });
+        gather_pairs<V>(minus, [&](int j) { return -__ldg(mean + at.group[j]); });
         gather_pairs<V>(scale, [&](int j) {
-            const int ch = at.tv * V + j;
-            return __ldg(rstd + ch / at.per) * (a.gamma ? __ldg(a.gamma + ch) : 1.f);
+            return works ? __ldg(rstd + at.group[j]) : 0.f;
         });
-        gather_pairs<V>(shift, [&](int j) { return a.beta ? __ldg(a.beta + at.tv * V + j) : 0.f; });
+#pragma unroll
+        for (int j = 0; j < kPairs<V>; ++j) scale[j] = mul(scale[j], gamma[j]);
         gather_pairs<V>(lift, [&](int j) {
-            const int g = (at.tv * V + j) / at.per;
+            const int g = at.group[j];
             return -__ldg(rstd + g) * s_stat[g].x;
         });
         gather_pairs<V>(tilt, [&](int j) {
-            const int g = (at.tv * V + j) / at.per;
+            const int g = at.group[j];
             const float r = __ldg(rstd + g);
             return -r * r * s_stat[g].y;
         });
@@ -1014,7 +1053,7 @@ __global__ void __launch_bounds__(Feed<T, V, 2, DENSE>::kBlockThreads, 1) k_norm
 #pragma unroll
             for (int j = 0; j < kPairs<V>; ++j) {
                 const F2 e = add(f[0][j], minus[j]);
-                const F2 dz = through<SILU>(f[1][j], fma(e, scale[j], shift[j]), least);
+                const F2 dz = through<SILU>(f[1][j], fma(e, scale[j], beta[j]), least);
                 f[0][j] = fma(dz, scale[j], fma(e, tilt[j], lift[j]));
             }
             *reinterpret_cast<Vec<T, V>*>(dx + row * a.c) = pack<T, V>(f[0]);
