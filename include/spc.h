@@ -601,7 +601,8 @@ SPC_API spc_status spc_dropout_bwd(const void* dy, int64_t n, double p, const ui
  *         segment give rows of zeros (and add nothing to dW).
  *  dw     [segments, cin, cout] fp32 out, overwritten (zeros for an empty segment).
  *  status device int32 sticky error word, or NULL (also SPC_ERR_TIMEOUT).
- *  ws     spc_grouped_workspace_size(...) bytes, 256-byte aligned; serves all three.
+ *  ws     spc_grouped_workspace_size(...) bytes, 256-byte aligned, for spc_grouped_wgrad
+ *         (0 where it needs none); the other two use none.
  *  x, dy, w and the result must be 16-byte aligned.  Results are run-to-run
  *  bit-identical.
  *  Kernels: tcgen05 tensor cores for fp16 / bf16 with cin and cout multiples of 8,

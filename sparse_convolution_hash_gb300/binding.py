@@ -79,6 +79,8 @@ _GP = ctypes.POINTER(Geom)
 def lib():
     """The loaded libspc.so (raises SpcLibraryMissing if it was never built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -177,13 +179,14 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _stream(device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+    # the raw handle, without the Stream object that torch.cuda.current_stream builds around it
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _cuda(t: torch.Tensor, name: str) -> torch.Tensor:
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    return t.contiguous()
+    return t if t.is_contiguous() else t.contiguous()
 
 
 def _workspace(nbytes: int, device) -> torch.Tensor:
@@ -537,31 +540,45 @@ def spc_conv_wgrad(x: torch.Tensor, dy: torch.Tensor, imap: Optional[torch.Tenso
     return dw
 
 
-def _int_list(t: Optional[torch.Tensor], name: str) -> Optional[torch.Tensor]:
-    """An int32 index list on the device (offsets, row orders), or None."""
-    return None if t is None else _cuda(t, name).to(torch.int32)
+# The layers between convolutions.  Their calls can be shorter than a few microseconds on the
+# device, so what does not need a tensor operation here does not get one.
+
+def _typed(t: torch.Tensor, dtype, name: str) -> torch.Tensor:
+    """A contiguous CUDA tensor of the given type."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype is not dtype:
+        t = t.to(dtype)
+    return t if t.is_contiguous() else t.contiguous()
 
 
-def _values(t: torch.Tensor, name: str, like: Optional[torch.Tensor] = None) -> torch.Tensor:
-    """A feature tensor of a supported type, or of `like`'s type."""
+def _values(t: torch.Tensor, name: str) -> torch.Tensor:
+    """A feature tensor of a supported type."""
     t = _cuda(t, name)
-    if like is not None:
-        return t.to(like.dtype)
     if t.dtype not in _DTYPES:
         raise ValueError(f"{name} must be float32, float16 or bfloat16, not {t.dtype}")
     return t
 
 
-def _shape(t: Optional[torch.Tensor], shape, name: str):
-    if t is not None and tuple(t.shape) != tuple(shape):
+def _expect(t: torch.Tensor, shape, name: str):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _optional(t: Optional[torch.Tensor], dtype, shape, name: str):
+    """(tensor, pointer) of an optional argument."""
+    if t is None:
+        return None, None
+    t = _typed(t, dtype, name)
+    _expect(t, shape, name)
+    return t, t.data_ptr()
 
 
 def _result(out: Optional[torch.Tensor], shape, dtype, device, name: str) -> torch.Tensor:
     """The caller's output buffer, checked, or a new one."""
     if out is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    if tuple(out.shape) != tuple(shape) or out.dtype != dtype or out.device != device or not out.is_contiguous():
+    if out.shape != shape or out.dtype is not dtype or out.device != device or not out.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
     return out
 
@@ -578,32 +595,23 @@ def spc_row_segments(ids: torch.Tensor, segments: int, with_order: bool = True,
         raise ValueError("ids must have one dimension")
     if not ids.is_cuda:
         raise ValueError("ids must be a CUDA tensor")
-    ids = ids.to(torch.int32)
+    if ids.dtype is not torch.int32:
+        ids = ids.to(torch.int32)
     n, dev = ids.shape[0], ids.device
-    if n > 1 and ids.stride(0) < 1:
-        ids = ids.contiguous()
+    stride = ids.stride(0) if n > 1 else 1
+    if stride < 1:
+        ids, stride = ids.contiguous(), 1
     seg = _result(out, (segments + 1,), torch.int32, dev, "out")
     if with_order:
         order = _result(order, (n,), torch.int32, dev, "order")
-    nbytes = int(lib().spc_row_segments_workspace_size(n, segments))
+    L = lib()
+    nbytes = L.spc_row_segments_workspace_size(n, segments)
     if ws is None or ws.numel() < nbytes:
         ws = _workspace(nbytes, dev)
-    code = lib().spc_row_segments(_ptr(ids), ids.stride(0) if n > 1 else 1, n, segments, _ptr(seg),
-                                  _ptr(order) if with_order else None, _ptr(ws), ws.numel(), _stream(dev))
+    code = L.spc_row_segments(ids.data_ptr(), stride, n, segments, seg.data_ptr(),
+                              order.data_ptr() if with_order else None, ws.data_ptr(), ws.numel(), _stream(dev))
     _check(code, "spc_row_segments")
     return seg, (order if with_order else None)
-
-
-def _norm_ws(ws, x, segments, groups):
-    n, c = x.shape
-    nbytes = int(lib().spc_group_norm_workspace_size(n, c, segments, groups, _DTYPES[x.dtype]))
-    return _workspace(nbytes, x.device) if ws is None or ws.numel() < nbytes else ws
-
-
-def _affine(t, c, name):
-    t = None if t is None else _cuda(t, name).to(torch.float32)
-    _shape(t, (c,), name)
-    return t
 
 
 def spc_group_norm_fwd(x: torch.Tensor, gamma: Optional[torch.Tensor], beta: Optional[torch.Tensor],
@@ -618,17 +626,22 @@ def spc_group_norm_fwd(x: torch.Tensor, gamma: Optional[torch.Tensor], beta: Opt
     pass `out`, `mean`, `rstd` and `ws` to call without allocating."""
     x = _values(x, "x")
     n, c = x.shape
-    seg, order = _int_list(seg, "seg"), _int_list(order, "order")
+    dev, dt = x.device, _DTYPES[x.dtype]
+    seg = _typed(seg, torch.int32, "seg")
     segments = seg.shape[0] - 1
-    _shape(order, (n,), "order")
-    gamma, beta = _affine(gamma, c, "gamma"), _affine(beta, c, "beta")
-    y = _result(out, (n, c), x.dtype, x.device, "out")
-    mean = _result(mean, (segments, groups), torch.float32, x.device, "mean")
-    rstd = _result(rstd, (segments, groups), torch.float32, x.device, "rstd")
-    ws = _norm_ws(ws, x, segments, groups)
-    code = lib().spc_group_norm_fwd(_ptr(x), _ptr(gamma), _ptr(beta), _ptr(seg), _ptr(order), segments, n, c,
-                                    groups, eps, act, _DTYPES[x.dtype], _ptr(y), _ptr(mean), _ptr(rstd),
-                                    _ptr(status), _ptr(ws), ws.numel(), _stream(x.device))
+    order, order_p = _optional(order, torch.int32, (n,), "order")
+    gamma, gamma_p = _optional(gamma, torch.float32, (c,), "gamma")
+    beta, beta_p = _optional(beta, torch.float32, (c,), "beta")
+    y = _result(out, (n, c), x.dtype, dev, "out")
+    mean = _result(mean, (segments, groups), torch.float32, dev, "mean")
+    rstd = _result(rstd, (segments, groups), torch.float32, dev, "rstd")
+    L = lib()
+    nbytes = L.spc_group_norm_workspace_size(n, c, segments, groups, dt)
+    if ws is None or ws.numel() < nbytes:
+        ws = _workspace(nbytes, dev)
+    code = L.spc_group_norm_fwd(x.data_ptr(), gamma_p, beta_p, seg.data_ptr(), order_p, segments, n, c, groups,
+                                eps, act, dt, y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _ptr(status),
+                                ws.data_ptr(), ws.numel(), _stream(dev))
     _check(code, "spc_group_norm_fwd")
     return y, mean, rstd
 
@@ -641,30 +654,34 @@ def spc_group_norm_bwd(dy: torch.Tensor, x: torch.Tensor, gamma: Optional[torch.
     """Gradients of spc_group_norm_fwd: (dx [n, C], dgamma [C] fp32, dbeta [C] fp32).
     `mean` and `rstd` come from the forward call."""
     x = _values(x, "x")
-    dy = _values(dy, "dy", x)
     n, c = x.shape
-    _shape(dy, (n, c), "dy")
-    seg, order = _int_list(seg, "seg"), _int_list(order, "order")
+    dev, dt = x.device, _DTYPES[x.dtype]
+    dy = _typed(dy, x.dtype, "dy")
+    _expect(dy, (n, c), "dy")
+    seg = _typed(seg, torch.int32, "seg")
     segments = seg.shape[0] - 1
-    _shape(order, (n,), "order")
-    gamma, beta = _affine(gamma, c, "gamma"), _affine(beta, c, "beta")
-    mean, rstd = _cuda(mean, "mean").to(torch.float32), _cuda(rstd, "rstd").to(torch.float32)
-    _shape(mean, (segments, groups), "mean")
-    _shape(rstd, (segments, groups), "rstd")
-    dx = _result(out, (n, c), x.dtype, x.device, "out")
-    params = torch.empty((2, c), dtype=torch.float32, device=x.device)
-    ws = _norm_ws(ws, x, segments, groups)
-    code = lib().spc_group_norm_bwd(_ptr(dy), _ptr(x), _ptr(gamma), _ptr(beta), _ptr(mean), _ptr(rstd),
-                                    _ptr(seg), _ptr(order), segments, n, c, groups, act, _DTYPES[x.dtype],
-                                    _ptr(dx), params.data_ptr(), params.data_ptr() + 4 * c, _ptr(status),
-                                    _ptr(ws), ws.numel(), _stream(x.device))
+    order, order_p = _optional(order, torch.int32, (n,), "order")
+    gamma, gamma_p = _optional(gamma, torch.float32, (c,), "gamma")
+    beta, beta_p = _optional(beta, torch.float32, (c,), "beta")
+    mean, mean_p = _optional(mean, torch.float32, (segments, groups), "mean")
+    rstd, rstd_p = _optional(rstd, torch.float32, (segments, groups), "rstd")
+    dx = _result(out, (n, c), x.dtype, dev, "out")
+    dgamma = torch.empty(c, dtype=torch.float32, device=dev)
+    dbeta = torch.empty(c, dtype=torch.float32, device=dev)
+    L = lib()
+    nbytes = L.spc_group_norm_workspace_size(n, c, segments, groups, dt)
+    if ws is None or ws.numel() < nbytes:
+        ws = _workspace(nbytes, dev)
+    code = L.spc_group_norm_bwd(dy.data_ptr(), x.data_ptr(), gamma_p, beta_p, mean_p, rstd_p, seg.data_ptr(),
+                                order_p, segments, n, c, groups, act, dt, dx.data_ptr(), dgamma.data_ptr(),
+                                dbeta.data_ptr(), _ptr(status), ws.data_ptr(), ws.numel(), _stream(dev))
     _check(code, "spc_group_norm_bwd")
-    return dx, params[0], params[1]
+    return dx, dgamma, dbeta
 
 
 def _rng(rng: torch.Tensor) -> torch.Tensor:
     rng = _cuda(rng, "rng")
-    if rng.dtype not in (torch.int64, torch.uint64) or rng.numel() != 2:
+    if (rng.dtype is not torch.int64 and rng.dtype is not torch.uint64) or rng.numel() != 2:
         raise ValueError("rng must hold two 64-bit integers: seed and offset")
     return rng
 
@@ -675,12 +692,11 @@ def spc_dropout_fwd(x: torch.Tensor, p: float, rng: torch.Tensor,
     """y = residual + (x / (1 - p) where kept, else 0).  `rng` [2] int64 on the device holds
     seed and offset; the mask is computed from them and the element's index, never stored."""
     x = _values(x, "x")
-    res = _values(residual, "residual", x) if residual is not None else None
-    _shape(res, x.shape, "residual")
+    residual, residual_p = _optional(residual, x.dtype, x.shape, "residual")
     rng = _rng(rng)
-    y = _result(out, x.shape, x.dtype, x.device, "out")
-    code = lib().spc_dropout_fwd(_ptr(x), _ptr(res), x.numel(), p, _ptr(rng), _DTYPES[x.dtype],
-                                 _ptr(y), _stream(x.device))
+    y = torch.empty_like(x) if out is None else _result(out, x.shape, x.dtype, x.device, "out")
+    code = lib().spc_dropout_fwd(x.data_ptr(), residual_p, x.numel(), p, rng.data_ptr(), _DTYPES[x.dtype],
+                                 y.data_ptr(), _stream(x.device))
     _check(code, "spc_dropout_fwd")
     return y
 
@@ -690,25 +706,30 @@ def spc_dropout_bwd(dy: torch.Tensor, p: float, rng: torch.Tensor,
     """dx = dy / (1 - p) where the forward call with this rng and p kept the element, else 0."""
     dy = _values(dy, "dy")
     rng = _rng(rng)
-    dx = _result(out, dy.shape, dy.dtype, dy.device, "out")
-    code = lib().spc_dropout_bwd(_ptr(dy), dy.numel(), p, _ptr(rng), _DTYPES[dy.dtype], _ptr(dx),
+    dx = torch.empty_like(dy) if out is None else _result(out, dy.shape, dy.dtype, dy.device, "out")
+    code = lib().spc_dropout_bwd(dy.data_ptr(), dy.numel(), p, rng.data_ptr(), _DTYPES[dy.dtype], dx.data_ptr(),
                                  _stream(dy.device))
     _check(code, "spc_dropout_bwd")
     return dx
 
 
-def _grouped(seg, x_rows, y_rows, rows):
-    """Offsets, row lists and the number of positions (a list's length, else the operand's rows)."""
-    seg, x_rows, y_rows = _int_list(seg, "seg"), _int_list(x_rows, "x_rows"), _int_list(y_rows, "y_rows")
-    m = x_rows.shape[0] if x_rows is not None else y_rows.shape[0] if y_rows is not None else rows
-    _shape(x_rows, (m,), "x_rows")
-    _shape(y_rows, (m,), "y_rows")
-    return seg, x_rows, y_rows, m
+def _positions(x_rows, y_rows, rows: int):
+    """Row lists with their pointers, and the number of positions (a list's length, else the operand's rows)."""
+    m = rows
+    if x_rows is not None:
+        m = x_rows.shape[0]
+    elif y_rows is not None:
+        m = y_rows.shape[0]
+    x_rows, x_p = _optional(x_rows, torch.int32, (m,), "x_rows")
+    y_rows, y_p = _optional(y_rows, torch.int32, (m,), "y_rows")
+    return x_rows, x_p, y_rows, y_p, m
 
 
-def _grouped_ws(ws, segments, m, cin, cout, like):
-    nbytes = int(lib().spc_grouped_workspace_size(segments, m, cin, cout, _DTYPES[like.dtype]))
-    return _workspace(nbytes, like.device) if nbytes and (ws is None or ws.numel() < nbytes) else ws
+def _grouped_ws(ws, segments, m, cin, cout, dt, device):
+    nbytes = lib().spc_grouped_workspace_size(segments, m, cin, cout, dt)
+    if nbytes and (ws is None or ws.numel() < nbytes):
+        ws = _workspace(nbytes, device)
+    return (ws, ws.data_ptr(), ws.numel()) if ws is not None else (None, None, 0)
 
 
 def spc_grouped_fwd(x: torch.Tensor, w: torch.Tensor, seg: torch.Tensor,
@@ -718,16 +739,17 @@ def spc_grouped_fwd(x: torch.Tensor, w: torch.Tensor, seg: torch.Tensor,
     """y[y_rows[r]] = x[x_rows[r]] W[g] for the positions r of each segment (expert) g:
     w [segments, cin, cout]; returns y [m, cout].  A list left out means row r at position r."""
     x = _values(x, "x")
-    w = _values(w, "w", x)
+    w = _typed(w, x.dtype, "w")
     segments, cin, cout = w.shape
-    _shape(x, (x.shape[0], cin), "x")
-    seg, x_rows, y_rows, m = _grouped(seg, x_rows, y_rows, x.shape[0])
-    _shape(seg, (segments + 1,), "seg")
-    y = _result(out, (m, cout), x.dtype, x.device, "out")
-    ws = _grouped_ws(ws, segments, m, cin, cout, x)
-    code = lib().spc_grouped_fwd(_ptr(x), _ptr(w), _ptr(seg), _ptr(x_rows), _ptr(y_rows), segments,
-                                 x.shape[0], m, cin, cout, _DTYPES[x.dtype], _ptr(y), _ptr(status),
-                                 _ptr(ws), 0 if ws is None else ws.numel(), _stream(x.device))
+    n_x, dev, dt = x.shape[0], x.device, _DTYPES[x.dtype]
+    _expect(x, (n_x, cin), "x")
+    seg = _typed(seg, torch.int32, "seg")
+    _expect(seg, (segments + 1,), "seg")
+    x_rows, x_p, y_rows, y_p, m = _positions(x_rows, y_rows, n_x)
+    y = _result(out, (m, cout), x.dtype, dev, "out")
+    ws_p, ws_n = (None, 0) if ws is None else (ws.data_ptr(), ws.numel())  # only the gradient by w needs one
+    code = lib().spc_grouped_fwd(x.data_ptr(), w.data_ptr(), seg.data_ptr(), x_p, y_p, segments, n_x, m, cin, cout,
+                                 dt, y.data_ptr(), _ptr(status), ws_p, ws_n, _stream(dev))
     _check(code, "spc_grouped_fwd")
     return y
 
@@ -739,16 +761,17 @@ def spc_grouped_dgrad(dy: torch.Tensor, w: torch.Tensor, seg: torch.Tensor,
     """dx[x_rows[r]] = dy[y_rows[r]] W[g]^T; returns dx [m, cin].  Where the forward's x_rows
     repeat rows, pass the list of slots instead and sum a row's slots."""
     dy = _values(dy, "dy")
-    w = _values(w, "w", dy)
+    w = _typed(w, dy.dtype, "w")
     segments, cin, cout = w.shape
-    _shape(dy, (dy.shape[0], cout), "dy")
-    seg, x_rows, y_rows, m = _grouped(seg, x_rows, y_rows, dy.shape[0])
-    _shape(seg, (segments + 1,), "seg")
-    dx = _result(out, (m, cin), dy.dtype, dy.device, "out")
-    ws = _grouped_ws(ws, segments, m, cin, cout, dy)
-    code = lib().spc_grouped_dgrad(_ptr(dy), _ptr(w), _ptr(seg), _ptr(x_rows), _ptr(y_rows), segments,
-                                   dy.shape[0], m, cin, cout, _DTYPES[dy.dtype], _ptr(dx), _ptr(status),
-                                   _ptr(ws), 0 if ws is None else ws.numel(), _stream(dy.device))
+    n_y, dev, dt = dy.shape[0], dy.device, _DTYPES[dy.dtype]
+    _expect(dy, (n_y, cout), "dy")
+    seg = _typed(seg, torch.int32, "seg")
+    _expect(seg, (segments + 1,), "seg")
+    x_rows, x_p, y_rows, y_p, m = _positions(x_rows, y_rows, n_y)
+    dx = _result(out, (m, cin), dy.dtype, dev, "out")
+    ws_p, ws_n = (None, 0) if ws is None else (ws.data_ptr(), ws.numel())  # only the gradient by w needs one
+    code = lib().spc_grouped_dgrad(dy.data_ptr(), w.data_ptr(), seg.data_ptr(), x_p, y_p, segments, n_y, m, cin, cout,
+                                   dt, dx.data_ptr(), _ptr(status), ws_p, ws_n, _stream(dev))
     _check(code, "spc_grouped_dgrad")
     return dx
 
@@ -760,15 +783,15 @@ def spc_grouped_wgrad(x: torch.Tensor, dy: torch.Tensor, seg: torch.Tensor,
     """dW[g] = sum over the positions r of segment g of x[x_rows[r]]^T dy[y_rows[r]],
     float32 [segments, cin, cout]."""
     x = _values(x, "x")
-    dy = _values(dy, "dy", x)
-    cin, cout = x.shape[1], dy.shape[1]
-    seg, x_rows, y_rows, m = _grouped(seg, x_rows, y_rows, max(x.shape[0], dy.shape[0]))
+    dy = _typed(dy, x.dtype, "dy")
+    (n_x, cin), (n_y, cout) = x.shape, dy.shape
+    dev, dt = x.device, _DTYPES[x.dtype]
+    seg = _typed(seg, torch.int32, "seg")
     segments = seg.shape[0] - 1
-    dw = _result(out, (segments, cin, cout), torch.float32, x.device, "out")
-    ws = _grouped_ws(ws, segments, m, cin, cout, x)
-    code = lib().spc_grouped_wgrad(_ptr(x), _ptr(dy), _ptr(seg), _ptr(x_rows), _ptr(y_rows), segments,
-                                   x.shape[0], dy.shape[0], m, cin, cout, _DTYPES[x.dtype], _ptr(dw),
-                                   _ptr(status), _ptr(ws), 0 if ws is None else ws.numel(),
-                                   _stream(x.device))
+    x_rows, x_p, y_rows, y_p, m = _positions(x_rows, y_rows, max(n_x, n_y))
+    dw = _result(out, (segments, cin, cout), torch.float32, dev, "out")
+    ws, ws_p, ws_n = _grouped_ws(ws, segments, m, cin, cout, dt, dev)
+    code = lib().spc_grouped_wgrad(x.data_ptr(), dy.data_ptr(), seg.data_ptr(), x_p, y_p, segments, n_x, n_y, m, cin,
+                                   cout, dt, dw.data_ptr(), _ptr(status), ws_p, ws_n, _stream(dev))
     _check(code, "spc_grouped_wgrad")
     return dw

@@ -1257,11 +1257,12 @@ size_t carve(int64_t n, int32_t c, int32_t segments, int32_t groups, char* base,
 }
 
 // second: the second kernel of a pass, which waits for the first one itself.
-template <typename K>
-spc_status launch(K* kernel, int shares, int threads, size_t smem, cudaStream_t st, const NormArgs& a, int64_t rows, const Ws& w,
+template <auto KERNEL>
+spc_status launch(int shares, int threads, size_t smem, cudaStream_t st, const NormArgs& a, int64_t rows, const Ws& w,
                   bool second)
 {
-    SPC_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+    const spc_status allowed = allow_smem<KERNEL>();
+    if (allowed != SPC_OK) return allowed;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)shares);
     cfg.blockDim = dim3((unsigned)threads);
@@ -1272,7 +1273,7 @@ spc_status launch(K* kernel, int shares, int threads, size_t smem, cudaStream_t 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = second ? 1 : 0;
-    SPC_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, a, rows, w, wait_limit_ns()));
+    SPC_CUDA_TRY(cudaLaunchKernelEx(&cfg, KERNEL, a, rows, w, wait_limit_ns()));
     return SPC_OK;
 }
 
@@ -1285,17 +1286,17 @@ spc_status rows_pass(const NormArgs& a, const Ws& w, bool backward, cudaStream_t
     if (backward) {
         using F = Feed<T, V, 2, DENSE>;
         const size_t base = F::kSmem + offsets;
-        const spc_status s = launch(k_norm_bwd_sums<T, V, DENSE, SILU>, shares, F::kBlockThreads,
+        const spc_status s = launch<k_norm_bwd_sums<T, V, DENSE, SILU>>(shares, F::kBlockThreads,
                                     base + sizeof(float) * (kSums<V, 2> + 2 * a.c), st, a, rows, w, false);
-        return s != SPC_OK ? s : launch(k_norm_bwd_apply<T, V, DENSE, SILU>, shares, F::kBlockThreads, base + stat, st, a, rows, w, true);
+        return s != SPC_OK ? s : launch<k_norm_bwd_apply<T, V, DENSE, SILU>>(shares, F::kBlockThreads, base + stat, st, a, rows, w, true);
     }
     using F = Feed<T, V, 1, DENSE>;
     const size_t base = F::kSmem + offsets;
-    const spc_status s = launch(k_norm_stats<T, V, DENSE>, shares, F::kBlockThreads,
+    const spc_status s = launch<k_norm_stats<T, V, DENSE>>(shares, F::kBlockThreads,
                                 base + sizeof(float) * (kSums<V, 1> + 2 * a.c), st, a, rows, w, false);
     return s != SPC_OK || a.n == 0
                ? s
-               : launch(k_norm_apply<T, V, DENSE, SILU>, shares, F::kBlockThreads, base + stat, st, a, rows, w, true);
+               : launch<k_norm_apply<T, V, DENSE, SILU>>(shares, F::kBlockThreads, base + stat, st, a, rows, w, true);
 }
 
 template <typename T, int V>

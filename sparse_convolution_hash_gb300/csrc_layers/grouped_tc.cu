@@ -335,7 +335,8 @@ spc_status launch(const GroupedArgs& a, cudaStream_t st)
     if (!w_ok) return SPC_ERR_CUDA;
     auto* kernel = k_grouped_tc<T, CG, BN, BMN, GATHER>;
     const size_t smem = S::smem(a.segments);
-    SPC_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+    const spc_status allowed = allow_smem<k_grouped_tc<T, CG, BN, BMN, GATHER>>();
+    if (allowed != SPC_OK) return allowed;
     const int64_t most = (a.m / S::kRows + a.segments + 2) * ceil_div(a.n, BN);
     const int groups = (int)std::min<int64_t>(sm_count() / CG, most);
     cudaLaunchConfig_t cfg = {};

@@ -569,7 +569,8 @@ spc_status launch(const GroupedWgradArgs& a, float* part, cudaStream_t st)
         return SPC_ERR_CUDA;
     auto* kernel = k_grouped_wgrad_tc<T, BN, GATHER>;
     const size_t smem = S::smem(a.segments);
-    SPC_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+    const spc_status allowed = allow_smem<k_grouped_wgrad_tc<T, BN, GATHER>>();
+    if (allowed != SPC_OK) return allowed;
     const int parts = grouped_wgrad_parts();
     Join* joins = reinterpret_cast<Join*>(part + (int64_t)parts * 2 * kTileM * 256);
     kernel<<<parts, GATHER ? kThreads + kGatherThreads : kThreads, smem, st>>>(a, part, joins, wait_limit_ns(), mx, my);

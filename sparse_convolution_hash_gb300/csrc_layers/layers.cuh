@@ -3,6 +3,8 @@
 // Argument validation happens in layers_api.cu before these are called.
 #pragma once
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace spc {
@@ -75,6 +77,25 @@ size_t grouped_wgrad_tc_ws_bytes();
 bool grouped_wgrad_tc_supported(const GroupedWgradArgs& a, spc_dtype dt);
 spc_status grouped_wgrad_tc(const GroupedWgradArgs& a, spc_dtype dt, void* ws, cudaStream_t st);
 spc_status grouped_wgrad_simt(const GroupedWgradArgs& a, spc_dtype dt, cudaStream_t st);
+
+// Lets a kernel ask for as much dynamic shared memory as an SM has; set once per device, as every
+// setting costs the host about as much as a launch.
+constexpr int kMostSmem = 227 * 1024;
+template <auto KERNEL>
+spc_status allow_smem()
+{
+    static std::atomic<bool> done[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SPC_ERR_CUDA;
+    if (!done[dev].load(std::memory_order_relaxed)) {
+        cudaFuncAttributes at;
+        SPC_CUDA_TRY(cudaFuncGetAttributes(&at, KERNEL));
+        SPC_CUDA_TRY(cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                          kMostSmem - (int)at.sharedSizeBytes));
+        done[dev].store(true, std::memory_order_relaxed);
+    }
+    return SPC_OK;
+}
 
 // ------------------------------------------------------------ device helpers
 // Segment s as positions [lo, hi) inside [0, n): offsets out of range or out of

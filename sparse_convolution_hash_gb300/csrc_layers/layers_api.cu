@@ -54,7 +54,7 @@ spc_status check_dropout(const void* x, int64_t n, double p, const uint64_t* rng
 spc_status check_grouped(const void* a, const void* b, const void* out, const int32_t* seg,
                          const int32_t* a_rows, const int32_t* b_rows, int32_t segments,
                          int64_t n_a, int64_t n_b, int64_t m, int32_t cin, int32_t cout,
-                         spc_dtype dt, const void* ws, size_t ws_bytes)
+                         spc_dtype dt)
 {
     if (!dtype_ok(dt) || !segments_ok(segments) || m < 0 || n_a < 0 || n_b < 0 || cin < 1 || cout < 1)
         return SPC_ERR_INVALID_ARG;
@@ -62,8 +62,6 @@ spc_status check_grouped(const void* a, const void* b, const void* out, const in
     if ((!a_rows && n_a < m) || (!b_rows && n_b < m)) return SPC_ERR_INVALID_ARG;
     if (!aligned16(a) || !aligned16(b) || !aligned16(out)) return SPC_ERR_INVALID_ARG;
     if (m > INT32_MAX - 1 || n_a > INT32_MAX - 1 || n_b > INT32_MAX - 1) return SPC_ERR_UNSUPPORTED;
-    const size_t need = spc_grouped_workspace_size(segments, m, cin, cout, dt);
-    if (need && (!ws || !aligned256(ws) || ws_bytes < need)) return SPC_ERR_WORKSPACE;
     return SPC_OK;
 }
 
@@ -164,8 +162,9 @@ spc_status spc_grouped_fwd(const void* x, const void* w, const int32_t* seg, con
                            int32_t cin, int32_t cout, spc_dtype dt, void* y, int32_t* status,
                            void* ws, size_t ws_bytes, void* stream)
 {
-    const spc_status s = check_grouped(x, w, y, seg, x_rows, y_rows, segments, n_x, m, m, cin, cout,
-                                       dt, ws, ws_bytes);
+    const spc_status s = check_grouped(x, w, y, seg, x_rows, y_rows, segments, n_x, m, m, cin, cout, dt);
+    (void)ws;
+    (void)ws_bytes;
     if (s != SPC_OK) return s;
     if (m == 0) return SPC_OK;
     if (!w || !y || (n_x > 0 && !x)) return SPC_ERR_INVALID_ARG;
@@ -178,8 +177,9 @@ spc_status spc_grouped_dgrad(const void* dy, const void* w, const int32_t* seg,
                              int64_t n_y, int64_t m, int32_t cin, int32_t cout, spc_dtype dt,
                              void* dx, int32_t* status, void* ws, size_t ws_bytes, void* stream)
 {
-    const spc_status s = check_grouped(dy, w, dx, seg, x_rows, y_rows, segments, m, n_y, m, cin, cout,
-                                       dt, ws, ws_bytes);
+    const spc_status s = check_grouped(dy, w, dx, seg, x_rows, y_rows, segments, m, n_y, m, cin, cout, dt);
+    (void)ws;
+    (void)ws_bytes;
     if (s != SPC_OK) return s;
     if (m == 0) return SPC_OK;
     if (!w || !dx || (n_y > 0 && !dy)) return SPC_ERR_INVALID_ARG;
@@ -194,10 +194,11 @@ spc_status spc_grouped_wgrad(const void* x, const void* dy, const int32_t* seg,
                              spc_dtype dt, float* dw, int32_t* status, void* ws, size_t ws_bytes,
                              void* stream)
 {
-    const spc_status s = check_grouped(x, dy, dw, seg, x_rows, y_rows, segments, n_x, n_y, m, cin,
-                                       cout, dt, ws, ws_bytes);
+    const spc_status s = check_grouped(x, dy, dw, seg, x_rows, y_rows, segments, n_x, n_y, m, cin, cout, dt);
     if (s != SPC_OK) return s;
     if (!dw || (n_x > 0 && !x) || (n_y > 0 && !dy)) return SPC_ERR_INVALID_ARG;
+    const size_t need = spc_grouped_workspace_size(segments, m, cin, cout, dt);
+    if (need && (!ws || !aligned256(ws) || ws_bytes < need)) return SPC_ERR_WORKSPACE;
     const GroupedWgradArgs a{x, dy, seg, x_rows, y_rows, dw, status, n_x, n_y, m, segments, cin, cout};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return grouped_wgrad_tc_supported(a, dt) ? grouped_wgrad_tc(a, dt, ws, st) : grouped_wgrad_simt(a, dt, st);

@@ -145,9 +145,8 @@ spc_status row_segments(const int32_t* ids, int64_t id_stride, int64_t n, int32_
     const int blocks = (int)std::max<int64_t>(1, ceil_div(n, rows));
     int32_t* counts = static_cast<int32_t*>(ws);
     const size_t place_smem = sizeof(int32_t) * (size_t)bins * (1 + kWarps);
-    if (place_smem > 48 * 1024)
-        SPC_CUDA_TRY(cudaFuncSetAttribute(k_seg_place, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                          (int)place_smem));
+    const spc_status allowed = allow_smem<k_seg_place>();
+    if (allowed != SPC_OK) return allowed;
     k_seg_count<<<blocks, kBlock, sizeof(int32_t) * bins, st>>>(ids, id_stride, n, segments, rows, counts);
     SPC_LAUNCH_CHECK();
     k_seg_place<<<order ? blocks : 1, kBlock, place_smem, st>>>(ids, id_stride, n, segments, rows, blocks,
