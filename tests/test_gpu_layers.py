@@ -58,7 +58,8 @@ def close(got, want, bound, what=""):
 # -------------------------------------------------------------------- segments
 @pytest.mark.parametrize("kind", ["random", "sorted", "one", "out"])
 @pytest.mark.parametrize("n,segments", [(1, 1), (2, 5), (31, 2), (257, 1024), (1024, 3), (5000, 64),
-                                        (40001, 300), (160001, 2), (300000, 255), (70000, 1024)])
+                                        (40001, 300), (160001, 2), (300000, 255), (70000, 1024),
+                                        (16384, 70), (16385, 70), (700001, 5), (640000, 1024)])
 def test_row_segments(n, segments, kind):
     g = np.random.default_rng(n + segments)
     ids = make_ids(g, n, segments, kind)
