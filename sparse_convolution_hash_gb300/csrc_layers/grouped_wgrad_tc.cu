@@ -2,8 +2,8 @@
 // on the 5th-generation tensor cores, fp32 result.
 //
 // The reduction runs over rows, so both operands are MN-major: a row of a stage
-// is 64 channels (M or N) of one reduction index, and a tile is 128 input x BN output
-// channels.  Segments differ in length and there may be fewer tiles than SMs,
+// is 64 channels (M or N) of one reduction index, and a tile is 128 CG input x BN
+// output channels.  Segments differ in length and there may be fewer tiles than SMs,
 // so the work is cut by units of 64 rows of one tile: all units of all tiles in a row, in equal
 // shares, one for each CTA.  A tile inside one share is written to dW as it
 // is; the parts of the others go to the workspace and a second kernel adds them in the
@@ -13,7 +13,12 @@
 // rows by cp.async, warp 1 issues the MMAs into one of two accumulators and
 // first clears the rows of a last, partial unit past the segment's end (they hold the
 // next segment's rows: a zero weight would not do, as 0 x NaN is NaN), warps 2-5 store
-// the other accumulator.  Every wait is bounded (SPC_ERR_TIMEOUT).
+// the other accumulator.  A pair of CTAs (CG = 2) shares a 256 x 256 tile: each loads its half of the
+// channels of both operands, warp 1 of the second reports its stages ready to the first, whose
+// warp 1 issues for both.
+// One CTA's 128 x 256 x 64 unit takes 1,080 cycles where its MMAs alone would take 512: it writes
+// and reads 96 KB of shared memory, 768 cycles at 128 bytes each.
+// Every wait is bounded (SPC_ERR_TIMEOUT).
 #include "kernels.cuh"
 #include "layers.cuh"
 #include "tc2.cuh"
@@ -26,23 +31,25 @@ namespace {
 constexpr int kThreads = 192;
 constexpr int kGatherThreads = 256;
 constexpr int kUnit = 64;    // rows of a unit
-constexpr int kTileM = 128;  // input channels of a tile
+constexpr int kHalfM = 128;  // input channels of a CTA's part of a tile
 constexpr int kJoinRows = 4;
 constexpr int kMaxParts = 192;  // CTAs at most: one thread of the smaller block plans for each
 constexpr int kAtom = kUnit * 128;  // 64 rows x 64 channels
 constexpr uint64_t kDrainNs = 200000000ull;
 
-template <int BN>
+template <int CG, int BN>
 struct Shape {
-    static constexpr int kABytes = kTileM / 64 * kAtom;
-    static constexpr int kBBytes = BN / 64 * kAtom;
+    static constexpr int kTileM = kHalfM * CG;
+    static constexpr int kHalfN = BN / CG;  // output channels that a CTA loads
+    static constexpr int kABytes = kHalfM / 64 * kAtom;
+    static constexpr int kBBytes = kHalfN / 64 * kAtom;
     static constexpr int kStage = kABytes + kBBytes;
     static constexpr int kStages = 196608 / kStage;
     static constexpr int kTmemCols = 2 * BN;
     static constexpr int kStaging = 4 * 32 * 128;
     static size_t smem(int segments)
     {
-        return 1024 + (size_t)kStages * kStage + kStaging + 8 * (2 * kStages + 4) + 16 + 4 * (2 * (size_t)segments + 1);
+        return 1024 + (size_t)kStages * kStage + kStaging + 8 * (3 * kStages + 4) + 16 + 4 * (2 * (size_t)segments + 1);
     }
 };
 
@@ -272,34 +279,38 @@ __device__ __forceinline__ Join join_of(const Walk& walk, int c)
     return j;
 }
 
-template <typename T, int BN, bool GATHER>
+template <typename T, int CG, int BN, bool GATHER>
 __global__ void __launch_bounds__(GATHER ? kThreads + kGatherThreads : kThreads, 1)
 k_grouped_wgrad_tc(GroupedWgradArgs a, float* __restrict__ part, Join* __restrict__ joins, uint64_t wait_ns,
                    const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_dy)
 {
-    using S = Shape<BN>;
+    using S = Shape<CG, BN>;
     constexpr int kAll = GATHER ? kThreads + kGatherThreads : kThreads;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     uint8_t* staging = smem + (size_t)S::kStages * S::kStage;
     uint64_t* full = reinterpret_cast<uint64_t*>(staging + S::kStaging);
     uint64_t* empty = full + S::kStages;
-    uint64_t* acc_full = empty + S::kStages;
+    uint64_t* peer = empty + S::kStages;  // the second CTA's stages, reported to the first
+    uint64_t* acc_full = peer + S::kStages;
     uint64_t* acc_empty = acc_full + 2;
     uint32_t* s_ctrl = reinterpret_cast<uint32_t*>(acc_empty + 2);
     int32_t* s_start = reinterpret_cast<int32_t*>(s_ctrl + 4);
     int32_t* s_list = s_start + a.segments + 1;
     __shared__ Plan plan;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t rank = CG == 2 ? ptx::cluster_rank() : 0;
+    const int me = blockIdx.x / CG;  // pair
 
     if (tid == 0) {
         for (int s = 0; s < S::kStages; ++s) {
             ptx::mbar_init(&full[s], GATHER ? kGatherThreads : 1);
             ptx::mbar_init(&empty[s], 1);
+            ptx::mbar_init(&peer[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
             ptx::mbar_init(&acc_full[b], 1);
-            ptx::mbar_init(&acc_empty[b], 4);
+            ptx::mbar_init(&acc_empty[b], 4 * CG);
         }
         ptx::mbar_init_fence();
         if (!GATHER) {
@@ -307,15 +318,16 @@ k_grouped_wgrad_tc(GroupedWgradArgs a, float* __restrict__ part, Join* __restric
             ptx::prefetch_tmap(&map_dy);
         }
     }
-    if (warp == 1) ptx::tmem_alloc_cg<1>(s_ctrl, S::kTmemCols);
-    const int cols = (a.cout + BN - 1) / BN, tiles = (a.cin + kTileM - 1) / kTileM * cols;
-    make_plan(a.seg, a.segments, a.m, tiles, gridDim.x, s_start, s_list, &plan, blockIdx.x == 0 ? a.status : nullptr, tid, kAll);
+    if (warp == 1) ptx::tmem_alloc_cg<CG>(s_ctrl, S::kTmemCols);
+    const int cols = (a.cout + BN - 1) / BN, tiles = (a.cin + S::kTileM - 1) / S::kTileM * cols;
+    make_plan(a.seg, a.segments, a.m, tiles, gridDim.x / CG, s_start, s_list, &plan, blockIdx.x == 0 ? a.status : nullptr, tid, kAll);
     ptx::tc_fence_before();
-    __syncthreads();
+    if constexpr (CG == 2) ptx::cluster_sync();
+    else __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = s_ctrl[0];
     Walk walk{s_start, s_list, a.seg, &plan, a.m, a.segments, tiles, 0, 0, 0, 0, 0};
-    walk.reset(blockIdx.x);
+    walk.reset(me);
     bool ok = true;
     if (blockIdx.x == 0 && tid < plan.parts && plan.first[tid + 1] > plan.first[tid]) joins[plan.id[tid]] = join_of(walk, tid);
     if (blockIdx.x == 0 && tid >= 1 && tid <= plan.parts) {  // numbers that no share has
@@ -330,7 +342,7 @@ k_grouped_wgrad_tc(GroupedWgradArgs a, float* __restrict__ part, Join* __restric
             while (walk.more() && ok) {
                 const Piece p = walk.next();
                 if (p.lo == p.hi) continue;
-                const int c0 = p.tile / cols * kTileM, n0 = p.tile % cols * BN;
+                const int c0 = p.tile / cols * S::kTileM + rank * kHalfM, n0 = p.tile % cols * BN + rank * S::kHalfN;
                 for (int k = p.k0; k < p.k1; ++k, ++it) {
                     const int s = it % S::kStages;
                     if (it >= S::kStages) ok = ptx::mbar_wait(&empty[s], ((it / S::kStages) - 1) & 1, wait_ns);
@@ -339,9 +351,9 @@ k_grouped_wgrad_tc(GroupedWgradArgs a, float* __restrict__ part, Join* __restric
                     const int32_t row = (int32_t)(p.lo + (int64_t)k * kUnit);
                     ptx::mbar_arrive_expect_tx(&full[s], S::kStage);
 #pragma unroll
-                    for (int j = 0; j < kTileM / 64; ++j) ptx::tma_load2d<1>(base + j * kAtom, &map_x, c0 + 64 * j, row, bar);
+                    for (int j = 0; j < kHalfM / 64; ++j) ptx::tma_load2d<1>(base + j * kAtom, &map_x, c0 + 64 * j, row, bar);
 #pragma unroll
-                    for (int j = 0; j < BN / 64; ++j)
+                    for (int j = 0; j < S::kHalfN / 64; ++j)
                         ptx::tma_load2d<1>(base + S::kABytes + j * kAtom, &map_dy, n0 + 64 * j, row, bar);
                 }
             }
@@ -351,13 +363,15 @@ k_grouped_wgrad_tc(GroupedWgradArgs a, float* __restrict__ part, Join* __restric
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------- MMAs
-        const uint32_t idesc = ptx::idesc_make(Fmt<T>::v, kTileM, BN) | (1u << 15) | (1u << 16);
+        const uint32_t idesc = ptx::idesc_make(Fmt<T>::v, S::kTileM, BN) | (1u << 15) | (1u << 16);
         uint32_t it = 0, n = 0;
         while (walk.more() && ok) {
             const Piece p = walk.next();
             if (p.lo == p.hi) continue;
             const uint32_t b = n & 1;
-            if (n >= 2) ok = __all_sync(FULL_MASK, ptx::mbar_wait(&acc_empty[b], ((n >> 1) - 1) & 1, wait_ns));
+            if (n >= 2 && rank == 0)
+                ok = __all_sync(FULL_MASK, CG == 2 ? ptx::mbar_wait_cluster(&acc_empty[b], ((n >> 1) - 1) & 1, wait_ns)
+                                                   : ptx::mbar_wait(&acc_empty[b], ((n >> 1) - 1) & 1, wait_ns));
             if (!ok) break;
             ptx::tc_fence_after();
             const uint32_t d = tmem + b * BN;
@@ -370,26 +384,35 @@ k_grouped_wgrad_tc(GroupedWgradArgs a, float* __restrict__ part, Join* __restric
                 if (!GATHER && left < kUnit) {
                     for (int e = (int)left * 8 + lane; e < kUnit * 8; e += 32)
 #pragma unroll
-                        for (int j = 0; j < kTileM / 64 + BN / 64; ++j)
+                        for (int j = 0; j < kHalfM / 64 + S::kHalfN / 64; ++j)
                             *reinterpret_cast<uint4*>(stage + j * kAtom + e * 16) = make_uint4(0, 0, 0, 0);
                     ptx::fence_proxy_async_smem();
                     __syncwarp();
                 }
+                if (GATHER) ptx::fence_proxy_async_smem();
+                if (CG == 2 && rank == 1) {
+                    if (lane == 0) ptx::mbar_arrive_cluster(ptx::map_rank(ptx::smem_u32(&peer[s]), 0));
+                    __syncwarp();
+                    continue;
+                }
+                if (CG == 2) {
+                    ok = __all_sync(FULL_MASK, ptx::mbar_wait_cluster(&peer[s], (it / S::kStages) & 1, wait_ns));
+                    if (!ok) break;
+                }
                 if (lane == 0) {
-                    if (GATHER) ptx::fence_proxy_async_smem();
                     ptx::tc_fence_after();
                     const uint32_t base = ptx::smem_u32(stage);
                     const uint64_t ad = ptx::desc_mn_sw128(base, kAtom), bd = ptx::desc_mn_sw128(base + S::kABytes, kAtom);
 #pragma unroll
                     for (int q = 0; q < kUnit / 16; ++q)
-                        ptx::mma_f16<1>(d, ad + (uint64_t)(q * (2048 >> 4)), bd + (uint64_t)(q * (2048 >> 4)), idesc,
+                        ptx::mma_f16<CG>(d, ad + (uint64_t)(q * (2048 >> 4)), bd + (uint64_t)(q * (2048 >> 4)), idesc,
                                         k != p.k0 || q != 0);
-                    ptx::mma_commit(&empty[s]);
+                    ptx::mma_commit_cg<CG>(&empty[s]);
                 }
                 __syncwarp();
             }
             if (!ok) break;
-            if (lane == 0) ptx::mma_commit(&acc_full[b]);
+            if (lane == 0 && rank == 0) ptx::mma_commit_cg<CG>(&acc_full[b]);
             ++n;
         }
         if (!ok && lane == 0) set_status(a.status, SPC_ERR_TIMEOUT);
@@ -406,7 +429,8 @@ k_grouped_wgrad_tc(GroupedWgradArgs a, float* __restrict__ part, Join* __restric
             while (walk.more() && ok) {
                 const Piece p = walk.next();
                 if (p.lo == p.hi) continue;
-                const int c0 = p.tile / cols * kTileM + piece * 8, n0 = p.tile % cols * BN + piece * 8;
+                const int c0 = p.tile / cols * S::kTileM + rank * kHalfM + piece * 8;
+                const int n0 = p.tile % cols * BN + rank * S::kHalfN + piece * 8;
                 // the list entries of thread e's two reduction indices of unit k, read one
                 // unit ahead and checked when they are used
                 auto entries = [&](int k, int32_t (&xe)[2], int32_t (&ye)[2]) {
@@ -438,13 +462,13 @@ k_grouped_wgrad_tc(GroupedWgradArgs a, float* __restrict__ part, Join* __restric
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
 #pragma unroll
-                        for (int q = 0; q < kTileM / 64; ++q) {
+                        for (int q = 0; q < kHalfM / 64; ++q) {
                             const bool take = xr[j] >= 0 && c0 + 64 * q < a.cin;
                             ptx::cp_async16(dst + q * kAtom + j * 32 * 128, take ? x + (xr[j] * a.cin + c0 + 64 * q) * 2 : x,
                                             take ? 16u : 0u);
                         }
 #pragma unroll
-                        for (int q = 0; q < BN / 64; ++q) {
+                        for (int q = 0; q < S::kHalfN / 64; ++q) {
                             const bool take = yr[j] >= 0 && n0 + 64 * q < a.cout;
                             ptx::cp_async16(dst + S::kABytes + q * kAtom + j * 32 * 128,
                                             take ? dy + (yr[j] * a.cout + n0 + 64 * q) * 2 : dy, take ? 16u : 0u);
@@ -473,7 +497,7 @@ k_grouped_wgrad_tc(GroupedWgradArgs a, float* __restrict__ part, Join* __restric
                 ptx::tc_fence_after();
                 ++n;
             }
-            const int c0 = p.tile / cols * kTileM + quarter * 32, n0 = p.tile % cols * BN;
+            const int c0 = p.tile / cols * S::kTileM + rank * kHalfM + quarter * 32, n0 = p.tile % cols * BN;
             // a whole tile goes to dW, a part to this CTA's first or last slot
             float* dst;
             int64_t pitch;
@@ -484,7 +508,7 @@ k_grouped_wgrad_tc(GroupedWgradArgs a, float* __restrict__ part, Join* __restric
                 rows = a.cin - c0;
                 width = a.cout - n0;
             } else {
-                dst = part + ((int64_t)plan.id[blockIdx.x] * 2 + p.slot) * (kTileM * BN) + quarter * 32 * BN;
+                dst = part + ((int64_t)plan.id[me] * 2 + p.slot) * (S::kTileM * BN) + ((int)rank * kHalfM + quarter * 32) * BN;
                 pitch = BN;
                 rows = 32;
                 width = BN;
@@ -517,34 +541,39 @@ k_grouped_wgrad_tc(GroupedWgradArgs a, float* __restrict__ part, Join* __restric
             if (some) {
                 ptx::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(&acc_empty[b]);
+                if (lane == 0) {
+                    if constexpr (CG == 2) ptx::mbar_arrive_cluster(ptx::map_rank(ptx::smem_u32(&acc_empty[b]), 0));
+                    else ptx::mbar_arrive(&acc_empty[b]);
+                }
             }
         }
         if (!ok && lane == 0) set_status(a.status, SPC_ERR_TIMEOUT);
     }
     __syncwarp();
     ptx::tc_fence_before();
-    __syncthreads();
+    if constexpr (CG == 2) ptx::cluster_sync();
+    else __syncthreads();
     if (warp == 1) {
         ptx::tc_fence_after();
-        ptx::tmem_dealloc_cg<1>(tmem, S::kTmemCols);
+        ptx::tmem_dealloc_cg<CG>(tmem, S::kTmemCols);
     }
 }
 
 // Block (c, q): rows kJoinRows q .. of the tile that share c's plan names become the sum
 // of its parts, in the order of the shares.
-template <int BN>
+template <int TM, int BN>
 __global__ void __launch_bounds__(kJoinRows * BN / 4)
 k_grouped_wgrad_join(GroupedWgradArgs a, const float* __restrict__ part, const Join* __restrict__ joins)
 {
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the parts were still coming
     const int c = blockIdx.x;
     const Join j = joins[c];
     if (j.more == 0) return;
     const int cols = (a.cout + BN - 1) / BN;
     const int r = blockIdx.y * kJoinRows + threadIdx.x / (BN / 4), n = threadIdx.x % (BN / 4) * 4;
-    const int row = j.tile / cols * kTileM + r, col = j.tile % cols * BN + n;
+    const int row = j.tile / cols * TM + r, col = j.tile % cols * BN + n;
     if (row >= a.cin || col >= a.cout) return;
-    constexpr int64_t kSlot = kTileM * BN;
+    constexpr int64_t kSlot = TM * BN;
     const float* src = part + r * BN + n;
     float4 s = __ldcs(reinterpret_cast<const float4*>(src + ((int64_t)c * 2 + j.slot) * kSlot));
     src += (int64_t)(c + 1) * 2 * kSlot;
@@ -559,41 +588,63 @@ k_grouped_wgrad_join(GroupedWgradArgs a, const float* __restrict__ part, const J
     *reinterpret_cast<float4*>(a.dw + ((int64_t)j.g * a.cin + row) * a.cout + col) = s;
 }
 
-template <typename T, int BN, bool GATHER>
+template <typename T, int CG, int BN, bool GATHER>
 spc_status launch(const GroupedWgradArgs& a, float* part, cudaStream_t st)
 {
-    using S = Shape<BN>;
+    using S = Shape<CG, BN>;
     CUtensorMap mx, my;
     if (!tmap_2d(&mx, Fmt<T>::t, 2, a.x, (uint64_t)a.cin, (uint64_t)a.n_x, 64, kUnit, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !tmap_2d(&my, Fmt<T>::t, 2, a.dy, (uint64_t)a.cout, (uint64_t)a.n_y, 64, kUnit, CU_TENSOR_MAP_SWIZZLE_128B))
         return SPC_ERR_CUDA;
-    auto* kernel = k_grouped_wgrad_tc<T, BN, GATHER>;
-    const size_t smem = S::smem(a.segments);
-    const spc_status allowed = allow_smem<k_grouped_wgrad_tc<T, BN, GATHER>>();
+    const spc_status allowed = allow_smem<k_grouped_wgrad_tc<T, CG, BN, GATHER>>();
     if (allowed != SPC_OK) return allowed;
-    const int parts = grouped_wgrad_parts();
-    Join* joins = reinterpret_cast<Join*>(part + (int64_t)parts * 2 * kTileM * 256);
-    kernel<<<parts, GATHER ? kThreads + kGatherThreads : kThreads, smem, st>>>(a, part, joins, wait_limit_ns(), mx, my);
-    SPC_LAUNCH_CHECK();
-    k_grouped_wgrad_join<BN><<<dim3(parts, kTileM / kJoinRows), kJoinRows * BN / 4, 0, st>>>(a, part, joins);
-    SPC_LAUNCH_CHECK();
+    const int parts = grouped_wgrad_ctas() / CG;
+    Join* joins = reinterpret_cast<Join*>(part + (int64_t)grouped_wgrad_ctas() * 2 * kHalfM * 256);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(parts * CG));
+    cfg.blockDim = dim3(GATHER ? kThreads + kGatherThreads : kThreads);
+    cfg.dynamicSmemBytes = S::smem(a.segments);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = CG;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = CG == 2 ? 1 : 0;
+    SPC_CUDA_TRY(cudaLaunchKernelEx(&cfg, k_grouped_wgrad_tc<T, CG, BN, GATHER>, a, part, joins, wait_limit_ns(), mx, my));
+    cfg.gridDim = dim3((unsigned)parts, S::kTileM / kJoinRows);
+    cfg.blockDim = dim3(kJoinRows * BN / 4);
+    cfg.dynamicSmemBytes = 0;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = 1;
+    SPC_CUDA_TRY(cudaLaunchKernelEx(&cfg, k_grouped_wgrad_join<S::kTileM, BN>, a, (const float*)part, (const Join*)joins));
     return SPC_OK;
 }
 
-template <typename T, int BN>
+// The tile.  Listed rows: a pair's 256 x 256 where both sides fill it, as every row copied then
+// serves twice the multiplications (bf16, 8 segments of 4096, 512 x 2048: 118 us against 126; 16 of
+// 2048, 1024 x 4096: 369 against 401).  Rows in order: one CTA's 128 x 256, which TMA
+// feeds better alone (71 us against 164 and 221 against 551 by pairs).  128 x 128 where there are no more
+// output channels (398,833 rows of 128 x 128: 60 us).
+template <typename T>
 spc_status pick(const GroupedWgradArgs& a, float* part, cudaStream_t st)
 {
-    return a.x_rows || a.y_rows ? launch<T, BN, true>(a, part, st) : launch<T, BN, false>(a, part, st);
+    const bool gather = a.x_rows || a.y_rows;
+    if (gather && a.cin > 128 && a.cout > 128) return launch<T, 2, 256, true>(a, part, st);
+    if (a.cout > 128) return gather ? launch<T, 1, 256, true>(a, part, st) : launch<T, 1, 256, false>(a, part, st);
+    return gather ? launch<T, 1, 128, true>(a, part, st) : launch<T, 1, 128, false>(a, part, st);
 }
 
 }  // namespace
 
-int grouped_wgrad_parts() { return std::min(sm_count(), kMaxParts); }
+int grouped_wgrad_ctas() { return std::min(sm_count(), kMaxParts) / 2 * 2; }
 
-// Two parts of a tile for each CTA.
+// Two parts of a tile for each CTA, and the joins.
 size_t grouped_wgrad_tc_ws_bytes()
 {
-    return align_up((sizeof(float) * 2 * kTileM * 256 + sizeof(Join)) * (size_t)grouped_wgrad_parts(), 256);
+    return align_up((sizeof(float) * 2 * kHalfM * 256 + sizeof(Join)) * (size_t)grouped_wgrad_ctas(), 256);
 }
 
 bool grouped_wgrad_tc_supported(const GroupedWgradArgs& a, spc_dtype dt)
@@ -604,8 +655,7 @@ bool grouped_wgrad_tc_supported(const GroupedWgradArgs& a, spc_dtype dt)
 spc_status grouped_wgrad_tc(const GroupedWgradArgs& a, spc_dtype dt, void* ws, cudaStream_t st)
 {
     float* part = static_cast<float*>(ws);
-    if (dt == SPC_F16) return a.cout <= 128 ? pick<__half, 128>(a, part, st) : pick<__half, 256>(a, part, st);
-    return a.cout <= 128 ? pick<__nv_bfloat16, 128>(a, part, st) : pick<__nv_bfloat16, 256>(a, part, st);
+    return dt == SPC_F16 ? pick<__half>(a, part, st) : pick<__nv_bfloat16>(a, part, st);
 }
 
 }  // namespace spc
