@@ -556,3 +556,68 @@ def test_binding_checks_of_shapes_and_types():
                                           y_rows=torch.arange(10, dtype=torch.int32, device=d))):
         with pytest.raises((spc.SpcError, ValueError)):
             f()
+
+
+def test_wait_limit_ends_the_pipelined_layers_with_a_status():
+    """With a limit of 0 a wait whose phase is not complete gives up at once: the kernels report
+    it, free what they hold and return, and the same calls work again afterwards."""
+    d = dev()
+    x = torch.randn(6000, 512, device=d, dtype=torch.bfloat16)
+    w = torch.randn(2, 512, 512, device=d, dtype=torch.bfloat16)
+    seg = torch.tensor([0, 2500, 6000], dtype=torch.int32, device=d)
+    rows = torch.randperm(6000, device=d).to(torch.int32)
+    calls = [lambda st: spc.spc_grouped_fwd(x, w, seg, status=st),
+             lambda st: spc.spc_grouped_fwd(x, w, seg, x_rows=rows, status=st),
+             lambda st: spc.spc_grouped_dgrad(x, w, seg, status=st),
+             lambda st: spc.spc_grouped_wgrad(x, x, seg, status=st),
+             lambda st: spc.spc_grouped_wgrad(x, x, seg, x_rows=rows, y_rows=rows, status=st),
+             lambda st: spc.spc_group_norm_fwd(x, None, None, seg, 32, status=st)[0],
+             lambda st: spc.spc_group_norm_bwd(x, x, None, None, torch.zeros(2, 32, device=d), torch.ones(2, 32, device=d),
+                                               seg, 32, status=st)[0]]
+    want = [f(None).clone() for f in calls]
+    old = spc.spc_get_wait_limit_ns()
+    try:
+        spc.spc_set_wait_limit_ns(0)
+        for f in calls:
+            st = spc.new_status(d)
+            f(st)
+            torch.cuda.synchronize()
+            assert int(st) == 9  # SPC_ERR_TIMEOUT
+    finally:
+        spc.spc_set_wait_limit_ns(old)
+    for f, y in zip(calls, want):
+        st = spc.new_status(d)
+        assert torch.equal(f(st), y)
+        spc.check_status(st)
+
+
+def test_layers_past_32_bits():
+    """More than 2^31 (and 2^32) elements: rows at the end are addressed as rows at the start."""
+    d = dev()
+    c = 512
+    n = 2 ** 32 // c + 4097
+    x = torch.zeros(n, c, device=d, dtype=torch.bfloat16)
+    tail = torch.randn(3000, c, device=d).to(torch.bfloat16)
+    x[-3000:] = tail
+    seg = torch.tensor([0, n - 3000, n], dtype=torch.int32, device=d)
+    y, mean, rstd = spc.spc_group_norm_fwd(x, None, None, seg, 32, act=2)
+    small = torch.tensor([0, 3000], dtype=torch.int32, device=d)
+    want, mean_w, rstd_w = spc.spc_group_norm_fwd(tail, None, None, small, 32, act=2)
+    assert torch.allclose(mean[1], mean_w[0], atol=1e-6) and torch.allclose(rstd[1], rstd_w[0], rtol=1e-5)
+    assert torch.allclose(y[-3000:].float(), want.float(), rtol=2 ** -7, atol=2 ** -7)
+    assert float(y[: n - 3000: 65537].abs().max()) == 0
+    dx, dg, db = spc.spc_group_norm_bwd(x, x, None, None, mean, rstd, seg, 32, act=2, out=y)
+    dx_w, dg_w, db_w = spc.spc_group_norm_bwd(tail, tail, None, None, mean_w, rstd_w, small, 32, act=2)
+    assert torch.allclose(dx[-3000:].float(), dx_w.float(), rtol=2 ** -6, atol=2 ** -6)
+    # the rows of zeros add nothing: xh = 0 there and dy = 0
+    assert torch.allclose(dg, dg_w, rtol=1e-3, atol=1e-2) and torch.allclose(db, db_w, rtol=1e-3, atol=1e-2)
+    del y, dx
+    w = torch.randn(2, c, 64, device=d).to(torch.bfloat16)
+    z = spc.spc_grouped_fwd(x, w, seg)
+    assert torch.equal(z[-3000:], spc.spc_grouped_fwd(tail, w[1:].contiguous(), small))
+    dw = spc.spc_grouped_wgrad(x, z, seg)
+    dw_w = spc.spc_grouped_wgrad(tail, z[-3000:].contiguous(), small)
+    assert float(dw[0].abs().max()) == 0
+    assert torch.allclose(dw[1], dw_w[0], rtol=1e-4, atol=1e-2)
+    back = spc.spc_grouped_dgrad(z, w, seg, out=x)
+    assert torch.equal(back[-3000:], spc.spc_grouped_dgrad(z[-3000:].contiguous(), w[1:].contiguous(), small))
