@@ -602,14 +602,15 @@ SPC_API spc_status spc_dropout_bwd(const void* dy, int64_t n, double p, const ui
  *  dw     [segments, cin, cout] fp32 out, overwritten (zeros for an empty segment).
  *  status device int32 sticky error word, or NULL (also SPC_ERR_TIMEOUT).
  *  ws     spc_grouped_workspace_size(...) bytes, 256-byte aligned, for spc_grouped_wgrad
- *         (0 where it needs none); the other two use none.
+ *         (0 where it needs none; listed: a row list is given, whose rows it may bring
+ *         into order there first); the other two use none.
  *  x, dy, w and the result must be 16-byte aligned.  Results are run-to-run
  *  bit-identical.
  *  Kernels: tcgen05 tensor cores for fp16 / bf16 with cin and cout multiples of 8,
  *  else a tiled CUDA-core kernel (fp32 in full fp32 multiplies).
  */
 SPC_API size_t spc_grouped_workspace_size(int32_t segments, int64_t m, int32_t cin, int32_t cout,
-                                          spc_dtype dt);
+                                          spc_dtype dt, int32_t listed);
 SPC_API spc_status spc_grouped_fwd(const void* x, const void* w, const int32_t* seg,
                                    const int32_t* x_rows, const int32_t* y_rows, int32_t segments,
                                    int64_t n_x, int64_t m, int32_t cin, int32_t cout, spc_dtype dt,

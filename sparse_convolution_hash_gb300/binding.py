@@ -157,7 +157,7 @@ def lib():
             L.spc_dropout_fwd.restype = _i32
             L.spc_dropout_bwd.argtypes = [_p, _i64, ctypes.c_double, _p, _i32, _p, _p]
             L.spc_dropout_bwd.restype = _i32
-            L.spc_grouped_workspace_size.argtypes = [_i32, _i64, _i32, _i32, _i32]
+            L.spc_grouped_workspace_size.argtypes = [_i32, _i64, _i32, _i32, _i32, _i32]
             L.spc_grouped_workspace_size.restype = _sz
             for f in (L.spc_grouped_fwd, L.spc_grouped_dgrad):
                 f.argtypes = [_p, _p, _p, _p, _p, _i32, _i64, _i64, _i32, _i32, _i32, _p, _p, _p, _sz, _p]
@@ -725,8 +725,8 @@ def _positions(x_rows, y_rows, rows: int):
     return x_rows, x_p, y_rows, y_p, m
 
 
-def _grouped_ws(ws, segments, m, cin, cout, dt, device):
-    nbytes = lib().spc_grouped_workspace_size(segments, m, cin, cout, dt)
+def _grouped_ws(ws, segments, m, cin, cout, dt, listed, device):
+    nbytes = lib().spc_grouped_workspace_size(segments, m, cin, cout, dt, listed)
     if nbytes and (ws is None or ws.numel() < nbytes):
         ws = _workspace(nbytes, device)
     return (ws, ws.data_ptr(), ws.numel()) if ws is not None else (None, None, 0)
@@ -790,7 +790,7 @@ def spc_grouped_wgrad(x: torch.Tensor, dy: torch.Tensor, seg: torch.Tensor,
     segments = seg.shape[0] - 1
     x_rows, x_p, y_rows, y_p, m = _positions(x_rows, y_rows, max(n_x, n_y))
     dw = _result(out, (segments, cin, cout), torch.float32, dev, "out")
-    ws, ws_p, ws_n = _grouped_ws(ws, segments, m, cin, cout, dt, dev)
+    ws, ws_p, ws_n = _grouped_ws(ws, segments, m, cin, cout, dt, x_p is not None or y_p is not None, dev)
     code = lib().spc_grouped_wgrad(x.data_ptr(), dy.data_ptr(), seg.data_ptr(), x_p, y_p, segments, n_x, n_y, m, cin,
                                    cout, dt, dw.data_ptr(), _ptr(status), ws_p, ws_n, _stream(dev))
     _check(code, "spc_grouped_wgrad")

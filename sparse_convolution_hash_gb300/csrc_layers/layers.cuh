@@ -71,9 +71,7 @@ struct GroupedWgradArgs {
 spc_status grouped_simt(const GroupedArgs& a, spc_dtype dt, cudaStream_t st);
 bool grouped_tc_supported(int32_t k, int32_t n, int64_t in_n, spc_dtype dt);
 spc_status grouped_tc(const GroupedArgs& a, spc_dtype dt, cudaStream_t st);
-// CTAs of the tensor-core gradient by the weights: the workspace has two parts of a tile for each.
-int grouped_wgrad_ctas();
-size_t grouped_wgrad_tc_ws_bytes();
+size_t grouped_wgrad_tc_ws_bytes(int64_t m, int32_t cin, int32_t cout, bool listed);
 bool grouped_wgrad_tc_supported(const GroupedWgradArgs& a, spc_dtype dt);
 spc_status grouped_wgrad_tc(const GroupedWgradArgs& a, spc_dtype dt, void* ws, cudaStream_t st);
 spc_status grouped_wgrad_simt(const GroupedWgradArgs& a, spc_dtype dt, cudaStream_t st);

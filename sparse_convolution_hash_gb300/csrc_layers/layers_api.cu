@@ -150,11 +150,12 @@ spc_status spc_dropout_bwd(const void* dy, int64_t n, double p, const uint64_t* 
     return dropout(dy, nullptr, n, p, rng, dt, dx, static_cast<cudaStream_t>(stream));
 }
 
-size_t spc_grouped_workspace_size(int32_t segments, int64_t m, int32_t cin, int32_t cout, spc_dtype dt)
+size_t spc_grouped_workspace_size(int32_t segments, int64_t m, int32_t cin, int32_t cout, spc_dtype dt,
+                                  int32_t listed)
 {
     if (!segments_ok(segments) || m < 0 || cin < 1 || cout < 1 || !dtype_ok(dt)) return 0;
-    // the gradient by the weights on tensor cores keeps parts of tiles there
-    return dt == SPC_F32 || cin % 8 || cout % 8 ? 0 : grouped_wgrad_tc_ws_bytes();
+    // the gradient by the weights on tensor cores keeps parts of tiles there, and listed rows in order
+    return dt == SPC_F32 || cin % 8 || cout % 8 ? 0 : grouped_wgrad_tc_ws_bytes(m, cin, cout, listed != 0);
 }
 
 spc_status spc_grouped_fwd(const void* x, const void* w, const int32_t* seg, const int32_t* x_rows,
@@ -197,7 +198,7 @@ spc_status spc_grouped_wgrad(const void* x, const void* dy, const int32_t* seg,
     const spc_status s = check_grouped(x, dy, dw, seg, x_rows, y_rows, segments, n_x, n_y, m, cin, cout, dt);
     if (s != SPC_OK) return s;
     if (!dw || (n_x > 0 && !x) || (n_y > 0 && !dy)) return SPC_ERR_INVALID_ARG;
-    const size_t need = spc_grouped_workspace_size(segments, m, cin, cout, dt);
+    const size_t need = spc_grouped_workspace_size(segments, m, cin, cout, dt, x_rows || y_rows);
     if (need && (!ws || !aligned256(ws) || ws_bytes < need)) return SPC_ERR_WORKSPACE;
     const GroupedWgradArgs a{x, dy, seg, x_rows, y_rows, dw, status, n_x, n_y, m, segments, cin, cout};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
