@@ -74,7 +74,8 @@ spc_status grouped_tc(const GroupedArgs& a, spc_dtype dt, cudaStream_t st);
 size_t grouped_wgrad_tc_ws_bytes(int64_t m, int32_t cin, int32_t cout, bool listed);
 bool grouped_wgrad_tc_supported(const GroupedWgradArgs& a, spc_dtype dt);
 spc_status grouped_wgrad_tc(const GroupedWgradArgs& a, spc_dtype dt, void* ws, cudaStream_t st);
-spc_status grouped_wgrad_simt(const GroupedWgradArgs& a, spc_dtype dt, cudaStream_t st);
+size_t grouped_wgrad_simt_ws_bytes(int32_t segments, int64_t m, int32_t cin, int32_t cout);
+spc_status grouped_wgrad_simt(const GroupedWgradArgs& a, spc_dtype dt, void* ws, cudaStream_t st);
 
 // Lets a kernel ask for as much dynamic shared memory as an SM has; set once per device, as every
 // setting costs the host about as much as a launch.

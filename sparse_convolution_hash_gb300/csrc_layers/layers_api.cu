@@ -154,8 +154,11 @@ size_t spc_grouped_workspace_size(int32_t segments, int64_t m, int32_t cin, int3
                                   int32_t listed)
 {
     if (!segments_ok(segments) || m < 0 || cin < 1 || cout < 1 || !dtype_ok(dt)) return 0;
-    // the gradient by the weights on tensor cores keeps parts of tiles there, and listed rows in order
-    return dt == SPC_F32 || cin % 8 || cout % 8 ? 0 : grouped_wgrad_tc_ws_bytes(m, cin, cout, listed != 0);
+    // the gradient by the weights keeps parts of sums there (on tensor cores parts of tiles, and listed
+    // rows in order)
+    const size_t simt = grouped_wgrad_simt_ws_bytes(segments, m, cin, cout);
+    if (dt == SPC_F32 || cin % 8 || cout % 8) return simt;
+    return std::max(simt, grouped_wgrad_tc_ws_bytes(m, cin, cout, listed != 0));
 }
 
 spc_status spc_grouped_fwd(const void* x, const void* w, const int32_t* seg, const int32_t* x_rows,
@@ -202,7 +205,7 @@ spc_status spc_grouped_wgrad(const void* x, const void* dy, const int32_t* seg,
     if (need && (!ws || !aligned256(ws) || ws_bytes < need)) return SPC_ERR_WORKSPACE;
     const GroupedWgradArgs a{x, dy, seg, x_rows, y_rows, dw, status, n_x, n_y, m, segments, cin, cout};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return grouped_wgrad_tc_supported(a, dt) ? grouped_wgrad_tc(a, dt, ws, st) : grouped_wgrad_simt(a, dt, st);
+    return grouped_wgrad_tc_supported(a, dt) ? grouped_wgrad_tc(a, dt, ws, st) : grouped_wgrad_simt(a, dt, ws, st);
 }
 
 }  // extern "C"
