@@ -4,10 +4,10 @@
 // The reduction runs over rows, so both operands are MN-major: a row of a stage
 // is 64 channels (M or N) of one reduction index, and a tile is 128 input x BN
 // output channels.  Segments differ in length and there may be fewer tiles than SMs,
-// so the work is cut by units of 64 rows of one tile: all units of all tiles in a row, in equal
-// shares, one for each CTA.  A tile inside one share is written to dW as it
-// is; the parts of the others go to the workspace and a second kernel adds them in the
-// order of the rows: no atomics, run-to-run identical.
+// so whole tiles go round the CTAs as far as they fill them evenly and the rest is cut by units
+// of 64 rows (Plan).  A whole tile is written to dW as it is; the parts of the others go to the
+// workspace and a second kernel adds them in the order of the rows: no atomics, run-to-run
+// identical.
 //
 // The tensor core truncates where it adds to an accumulator, so sums over long segments would
 // drift (4096 rows: 5 10^-6 of the result).  An accumulator takes 512 rows; eight warps then add it,
@@ -17,8 +17,9 @@
 // rows by cp.async, warp 1 issues the MMAs into one of two accumulators and
 // first clears the rows of a last, partial unit past the segment's end (they hold the
 // next segment's rows: a zero weight would not do, as 0 x NaN is NaN).
-// A 128 x 256 x 64 unit takes about 1,000 cycles where its MMAs alone would take 512: with its
-// copies it moves 96 KB through shared memory, 768 cycles at 128 bytes each, and 48 KB from L2.
+// Wide tiles are bound by what comes from L2 (one CTA's 128 x 256 x 64 unit: 48 KB), so two CTAs
+// that hold the same output channels make a pair: each loads half of dy's columns into
+// both (TMA multicast) and a stage is free when both have used it; all else is the CTA's own.
 // Every wait is bounded (SPC_ERR_TIMEOUT).
 #include "kernels.cuh"
 #include "layers.cuh"
@@ -35,6 +36,7 @@ constexpr int kGatherThreads = 256;
 constexpr int kUnit = 64;    // rows of a unit
 constexpr int kFlush = 8;    // units that an accumulator in tensor memory sums up
 constexpr int kTileM = 128;  // input channels of a tile
+constexpr int kSplitFrom = 24;
 constexpr int kJoinRows = 4;
 constexpr int kMaxParts = 192;  // CTAs at most: one thread of the smaller block plans for each
 constexpr int kAtom = kUnit * 128;  // 64 rows x 64 channels
@@ -73,17 +75,17 @@ struct Piece {
 // the longer ones after them.  The tiles of that list in turn: the first `waves` x CTAs
 // are whole tiles, tile c + i CTAs for CTA c, so that neighbouring tiles read the same
 // rows at the same time; the units of the tiles after them go to the CTAs in
-// contiguous shares, each as long as evens out what its whole tiles took.
+// contiguous shares, each as long as evens out what its whole tiles took.  Where no tile is
+// longer than kSplitFrom units all of them stay whole: a cut costs two parts of 128 KB written and
+// read again, as much as 20 units or so (4,096 rows of 8 segments, 512 x 2048: 25 us
+// against 33).
 struct Plan {
-    int32_t waves;
+    int64_t whole;               // tiles that stay whole
+    int32_t longest;             // units of the longest tile
     int32_t parts;               // CTAs
     int64_t base;                // first unit of the shares
     int64_t first[kMaxParts + 1];  // share c: units base + first[c] .. base + first[c + 1)
     int32_t id[kMaxParts];       // number of CTA c among those that have a share
-    int64_t sum;
-    int32_t count;
-    int64_t warp_sum[32];
-    int32_t warp_count[32];
 };
 
 struct Walk {
@@ -110,13 +112,14 @@ struct Walk {
         u = begin = plan->base + plan->first[c];
         end = plan->base + plan->first[c + 1];
     }
-    __device__ __forceinline__ bool more() const { return wave < plan->waves || u < end; }
+    __device__ __forceinline__ int64_t tile_of(int w) const { return c + (int64_t)w * plan->parts; }
+    __device__ __forceinline__ bool more() const { return tile_of(wave) < plan->whole || u < end; }
     __device__ __forceinline__ Piece next()
     {
         Piece p;
-        if (wave < plan->waves) {
-            const int64_t t = c + (int64_t)wave * plan->parts;
-            const int32_t j = (int32_t)(t / tiles);
+        if (tile_of(wave) < plan->whole) {
+            const int64_t t = tile_of(wave);
+            const int32_t j = (int32_t)((uint32_t)t / (uint32_t)tiles);
             piece(p, j, (int32_t)(t - (int64_t)j * tiles));
             p.k0 = p.slot = 0;
             p.k1 = p.units;
@@ -151,112 +154,151 @@ struct Walk {
     }
 };
 
-// Inclusive sum over the block; every thread calls it.
 template <typename V>
-__device__ __forceinline__ V block_scan(V v, V* s_warp, int tid, int threads, V& total)
+__device__ __forceinline__ V warp_add(V v)
 {
-    const int lane = tid & 31, warp = tid >> 5;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(FULL_MASK, v, d);
+    return v;
+}
+template <typename V>
+__device__ __forceinline__ V warp_before(V v, int lane)  // the sum of the lanes below
+{
+    const V own = v;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
         const V u = __shfl_up_sync(FULL_MASK, v, d);
         if (lane >= d) v += u;
     }
-    __syncthreads();
-    if (lane == 31) s_warp[warp] = v;
-    __syncthreads();
-    total = 0;
-    for (int w = 0; w < threads / 32; ++w) {
-        if (w < warp) v += s_warp[w];
-        total += s_warp[w];
-    }
-    return v;
+    return v - own;
 }
 
-// Fills the list, its unit sums [segments + 1] and the plan; every thread of the block calls it.
-__device__ __forceinline__ void make_plan(const int32_t* seg, int segments, int64_t m, int tiles, int parts,
-                                          int32_t* s_start, int32_t* s_list, int32_t* s_units, Plan* plan, int32_t* status,
-                                          int tid,
-                                          int threads)
+// The whole tiles and the shares, by one warp; a lane speaks for kMaxParts / 32 CTAs in a row.
+__device__ __forceinline__ void share_out(Plan* plan, const int32_t* s_start, int segments, int tiles, int parts, int shorter,
+                                          int64_t total, int lane)
 {
-    int64_t all = 0, t64;
-    for (int g = tid; g < segments; g += threads) {
-        int64_t a, b;
-        segment_bounds(seg, g, m, status, a, b);
-        s_units[g] = b > a ? (int32_t)((b - a + kUnit - 1) / kUnit) : 1;
-        all += s_units[g];
-    }
-    block_scan<int64_t>(all, plan->warp_sum, tid, threads, t64);
-    const int64_t total = t64 * tiles, even = total / parts;
-    int32_t listed = 0, shorter = 0, t32;
-    for (int pass = 0; pass < 2; ++pass)
-        for (int g0 = 0; g0 < segments; g0 += threads) {
-            const int g = g0 + tid;
-            const bool mine = g < segments && (s_units[g] <= even) == (pass == 0);
-            const int32_t at = block_scan<int32_t>(mine ? 1 : 0, plan->warp_count, tid, threads, t32);
-            if (mine) s_list[listed + at - 1] = g;
-            listed += t32;
-            if (pass == 0) shorter += t32;
-        }
-    __syncthreads();
-    int32_t carry = 0;
-    for (int j0 = 0; j0 < segments; j0 += threads) {
-        const int j = j0 + tid;
-        const int32_t units = j < segments ? s_units[s_list[j]] : 0;
-        const int32_t at = block_scan<int32_t>(units, plan->warp_count, tid, threads, t32);
-        if (j < segments) s_start[j + 1] = carry + at;
-        carry += t32;
-    }
-    if (tid == 0) s_start[0] = 0;
-    __syncthreads();
-    // whole waves: all there are, less one where too little would be left to even out
-    int32_t waves = (int32_t)((int64_t)shorter * tiles / parts);
+    constexpr int P = kMaxParts / 32;
     auto unit_of_tile = [&](int64_t t) -> int64_t {
-        const int32_t j = (int32_t)(t / tiles);
+        const int32_t j = (int32_t)((uint32_t)t / (uint32_t)tiles);
         if (j >= segments) return total;
         return (int64_t)s_start[j] * tiles + (t - (int64_t)j * tiles) * (s_start[j + 1] - s_start[j]);
     };
+    // whole waves: all there are, less one where too little would be left to even out
+    int32_t waves = (int32_t)((int64_t)shorter * tiles / parts);
     if (waves > 0 && (total - unit_of_tile((int64_t)waves * parts)) * 8 < total / waves) --waves;
-    const int64_t base = unit_of_tile((int64_t)waves * parts), rest = total - base;
-    int64_t took = 0;
-    if (tid < parts)
-        for (int i = 0; i < waves; ++i) {
-            const int32_t j = (int32_t)((tid + (int64_t)i * parts) / tiles);
-            took += s_start[j + 1] - s_start[j];
-        }
+    const bool all_whole = plan->longest <= kSplitFrom;
+    const int64_t whole = all_whole ? (int64_t)segments * tiles : (int64_t)waves * parts;
+    const int64_t base = unit_of_tile(whole), rest = total - base;
+    int64_t took[P];
+    bool below[P];
+#pragma unroll
+    for (int q = 0; q < P; ++q) {
+        const int c = lane * P + q;
+        took[q] = 0;
+        below[q] = c < parts && rest > 0;
+        if (below[q])
+            for (int i = 0; i < waves; ++i) {
+                const uint32_t j = (uint32_t)(c + i * parts) / (uint32_t)tiles;
+                took[q] += s_start[j + 1] - s_start[j];
+            }
+    }
     // the level to which the shares fill every CTA that is below it
-    bool below = tid < parts;
-    int64_t level = 0, extra = 0, rank = 0;
-    for (int round = 0; round < 8; ++round) {
-        int64_t sum;
-        int32_t n;
-        block_scan<int64_t>(below ? took : 0, plan->warp_sum, tid, threads, sum);
-        const int32_t at = block_scan<int32_t>(below ? 1 : 0, plan->warp_count, tid, threads, n);
-        rank = at - 1;
-        level = (rest + sum) / n;
-        extra = (rest + sum) - level * n;
-        const bool still = below && took <= level;
-        int32_t kept;
-        block_scan<int32_t>(still ? 1 : 0, plan->warp_count, tid, threads, kept);
-        if (kept == n) break;
-        if (round < 7) below = still;
+    int64_t level = 0, extra = 0;
+    for (int round = 0; round < 8 && rest > 0; ++round) {
+        int64_t sum = 0;
+        int32_t n = 0;
+#pragma unroll
+        for (int q = 0; q < P; ++q)
+            if (below[q]) {
+                sum += took[q];
+                ++n;
+            }
+        sum = warp_add(sum) + rest;
+        n = warp_add(n);
+        level = sum / n;
+        extra = sum - level * n;
+        bool above = false;
+#pragma unroll
+        for (int q = 0; q < P; ++q) above |= below[q] && took[q] > level;
+        if (!__any_sync(FULL_MASK, above) || round == 7) break;
+#pragma unroll
+        for (int q = 0; q < P; ++q) below[q] = below[q] && took[q] <= level;
     }
-    int64_t share = below ? level - took + (rank < extra ? 1 : 0) : 0;
-    if (share < 0) share = 0;
-    int64_t sum;
-    int32_t n;
-    const int64_t to = block_scan<int64_t>(share, plan->warp_sum, tid, threads, sum);
-    const int32_t at = block_scan<int32_t>(share > 0 ? 1 : 0, plan->warp_count, tid, threads, n);
-    if (tid < parts) {
-        plan->first[tid + 1] = tid == parts - 1 || to > rest ? rest : to;
-        plan->id[tid] = at - 1;
+    int32_t mine = 0;
+#pragma unroll
+    for (int q = 0; q < P; ++q) mine += below[q];
+    int32_t rank = warp_before(mine, lane);
+    int64_t share[P], sum = 0;
+    int32_t some = 0;
+#pragma unroll
+    for (int q = 0; q < P; ++q) {
+        share[q] = below[q] ? level - took[q] + (rank++ < extra ? 1 : 0) : 0;
+        if (share[q] < 0) share[q] = 0;
+        sum += share[q];
+        some += share[q] > 0;
     }
-    if (tid == 0) {
+    int64_t to = warp_before(sum, lane);
+    int32_t id = warp_before(some, lane);
+#pragma unroll
+    for (int q = 0; q < P; ++q) {
+        const int c = lane * P + q;
+        to += share[q];
+        if (c < parts) {
+            plan->first[c + 1] = c == parts - 1 || to > rest ? rest : to;
+            plan->id[c] = share[q] > 0 ? id : id - 1;
+        }
+        id += share[q] > 0;
+    }
+    if (lane == 0) {
         plan->first[0] = 0;
-        plan->waves = waves;
+        plan->whole = whole;
         plan->parts = parts;
         plan->base = base;
     }
-    __syncthreads();
+}
+
+// Fills the list, its unit sums [segments + 1] and the plan; one warp does it all, which
+// spares a dozen barriers of the block.
+__device__ __forceinline__ void make_plan(const int32_t* seg, int segments, int64_t m, int tiles, int parts,
+                                          int32_t* s_start, int32_t* s_list, int32_t* s_units, Plan* plan, int32_t* status,
+                                          int lane)
+{
+    int64_t all = 0;
+    int32_t longest = 0;
+    for (int g = lane; g < segments; g += 32) {
+        int64_t a, b;
+        segment_bounds(seg, g, m, status, a, b);
+        const int32_t units = b > a ? (int32_t)((b - a + kUnit - 1) / kUnit) : 1;
+        s_units[g] = units;
+        all += units;
+        longest = longest > units ? longest : units;
+    }
+    const int64_t total = warp_add(all) * tiles, even = total / parts;
+    longest = __reduce_max_sync(FULL_MASK, longest);
+    __syncwarp();
+    int32_t listed = 0, shorter = 0, carry = 0;
+    for (int pass = 0; pass < 2; ++pass)
+        for (int g0 = 0; g0 < segments; g0 += 32) {
+            const int g = g0 + lane;
+            const int32_t units = g < segments ? s_units[g] : 0;
+            const bool mine = g < segments && (units <= even) == (pass == 0);
+            const unsigned who = __ballot_sync(FULL_MASK, mine);
+            const int32_t at = listed + __popc(who & ((1u << lane) - 1u)), own = mine ? units : 0;
+            const int32_t before = carry + warp_before(own, lane);
+            if (mine) {
+                s_list[at] = g;
+                s_start[at] = before;
+            }
+            listed += __popc(who);
+            carry = __shfl_sync(FULL_MASK, before + own, 31);
+            if (pass == 0) shorter = listed;
+        }
+    if (lane == 0) {
+        s_start[segments] = carry;
+        plan->longest = longest;
+    }
+    __syncwarp();
+    share_out(plan, s_start, segments, tiles, parts, shorter, total, lane);
 }
 
 // The tile that starts in the share of a CTA and ends in a later one: its parts are slot `slot`
@@ -281,13 +323,12 @@ __device__ __forceinline__ Join join_of(const Walk& walk, int c)
     return j;
 }
 
-template <typename T, int BN, bool GATHER>
+template <typename T, int BN, bool GATHER, bool PAIR>
 __global__ void __launch_bounds__(GATHER ? kThreads + kGatherThreads : kThreads, 1)
 k_grouped_wgrad_tc(GroupedWgradArgs a, float* __restrict__ part, Join* __restrict__ joins, uint64_t wait_ns,
                    const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_dy)
 {
     using S = Shape<BN>;
-    constexpr int kAll = GATHER ? kThreads + kGatherThreads : kThreads;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     uint8_t* staging = smem + (size_t)S::kStages * S::kStage;
@@ -300,11 +341,14 @@ k_grouped_wgrad_tc(GroupedWgradArgs a, float* __restrict__ part, Join* __restric
     int32_t* s_list = s_start + a.segments + 1;
     __shared__ Plan plan;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    constexpr int kWide = PAIR ? 2 * kTileM : kTileM;  // input channels of a planned tile
+    constexpr int kCtas = PAIR ? 2 : 1;
+    const int rank = PAIR ? (int)ptx::cluster_rank() : 0, me = (int)blockIdx.x / kCtas;
 
     if (tid == 0) {
         for (int s = 0; s < S::kStages; ++s) {
             ptx::mbar_init(&full[s], GATHER ? kGatherThreads : 1);
-            ptx::mbar_init(&empty[s], 1);
+            ptx::mbar_init(&empty[s], kCtas);
         }
         for (int b = 0; b < 2; ++b) {
             ptx::mbar_init(&acc_full[b], 1);
@@ -317,14 +361,17 @@ k_grouped_wgrad_tc(GroupedWgradArgs a, float* __restrict__ part, Join* __restric
         }
     }
     if (warp == 1) ptx::tmem_alloc_cg<1>(s_ctrl, S::kTmemCols);
-    const int cols = (a.cout + BN - 1) / BN, tiles = (a.cin + kTileM - 1) / kTileM * cols;
-    make_plan(a.seg, a.segments, a.m, tiles, gridDim.x, s_start, s_list, s_list + a.segments, &plan, blockIdx.x == 0 ? a.status : nullptr, tid, kAll);
+    const int cols = (a.cout + BN - 1) / BN, tiles = (a.cin + kWide - 1) / kWide * cols;
+    if (warp == 0)
+        make_plan(a.seg, a.segments, a.m, tiles, gridDim.x / kCtas, s_start, s_list, s_list + a.segments, &plan,
+                  blockIdx.x == 0 ? a.status : nullptr, lane);
     ptx::tc_fence_before();
-    __syncthreads();
+    if constexpr (PAIR) ptx::cluster_sync();
+    else __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = s_ctrl[0];
     Walk walk{s_start, s_list, a.seg, &plan, a.m, a.segments, tiles, 0, 0, 0, 0, 0};
-    walk.reset(blockIdx.x);
+    walk.reset(me);
     bool ok = true;
     if (blockIdx.x == 0 && tid < plan.parts && plan.first[tid + 1] > plan.first[tid]) joins[plan.id[tid]] = join_of(walk, tid);
     if (blockIdx.x == 0 && tid >= 1 && tid <= plan.parts) {  // numbers that no share has
@@ -339,7 +386,7 @@ k_grouped_wgrad_tc(GroupedWgradArgs a, float* __restrict__ part, Join* __restric
             while (walk.more() && ok) {
                 const Piece p = walk.next();
                 if (p.lo == p.hi) continue;
-                const int c0 = p.tile / cols * kTileM, n0 = p.tile % cols * BN;
+                const int c0 = p.tile / cols * kWide + rank * kTileM, n0 = p.tile % cols * BN;
                 for (int k = p.k0; k < p.k1; ++k, ++it) {
                     const int s = it % S::kStages;
                     if (it >= S::kStages) ok = ptx::mbar_wait(&empty[s], ((it / S::kStages) - 1) & 1, wait_ns);
@@ -350,8 +397,11 @@ k_grouped_wgrad_tc(GroupedWgradArgs a, float* __restrict__ part, Join* __restric
 #pragma unroll
                     for (int j = 0; j < kTileM / 64; ++j) ptx::tma_load2d<1>(base + j * kAtom, &map_x, c0 + 64 * j, row, bar);
 #pragma unroll
-                    for (int j = 0; j < BN / 64; ++j)
-                        ptx::tma_load2d<1>(base + S::kABytes + j * kAtom, &map_dy, n0 + 64 * j, row, bar);
+                    for (int j = 0; j < BN / 64; ++j) {
+                        const uint32_t to = base + S::kABytes + j * kAtom;
+                        if constexpr (!PAIR) ptx::tma_load2d<1>(to, &map_dy, n0 + 64 * j, row, bar);
+                        else if (j / (BN / 128) == rank) ptx::tma_load2d_both(to, &map_dy, n0 + 64 * j, row, bar);
+                    }
                 }
             }
             if (!ok) set_status(a.status, SPC_ERR_TIMEOUT);
@@ -394,12 +444,13 @@ k_grouped_wgrad_tc(GroupedWgradArgs a, float* __restrict__ part, Join* __restric
                         for (int q = 0; q < kUnit / 16; ++q)
                             ptx::mma_f16<1>(d, ad + (uint64_t)(q * (2048 >> 4)), bd + (uint64_t)(q * (2048 >> 4)), idesc,
                                             k != k0 || q != 0);
-                        ptx::mma_commit_cg<1>(&empty[s]);
+                        if constexpr (PAIR) ptx::mma_commit_both(&empty[s]);
+                        else ptx::mma_commit(&empty[s]);
                     }
                     __syncwarp();
                 }
                 if (!ok) break;
-                if (lane == 0) ptx::mma_commit_cg<1>(&acc_full[b]);
+                if (lane == 0) ptx::mma_commit(&acc_full[b]);
             }
         }
         if (!ok && lane == 0) set_status(a.status, SPC_ERR_TIMEOUT);
@@ -416,7 +467,7 @@ k_grouped_wgrad_tc(GroupedWgradArgs a, float* __restrict__ part, Join* __restric
             while (walk.more() && ok) {
                 const Piece p = walk.next();
                 if (p.lo == p.hi) continue;
-                const int c0 = p.tile / cols * kTileM + piece * 8;
+                const int c0 = p.tile / cols * kWide + rank * kTileM + piece * 8;
                 const int n0 = p.tile % cols * BN + piece * 8;
                 // the list entries of thread e's two reduction indices of unit k, read one
                 // unit ahead and checked when they are used
@@ -499,7 +550,7 @@ k_grouped_wgrad_tc(GroupedWgradArgs a, float* __restrict__ part, Join* __restric
                 if (lane == 0) ptx::mbar_arrive(&acc_empty[b]);
             }
             if (!ok) break;
-            const int c0 = p.tile / cols * kTileM + quarter * 32;
+            const int c0 = p.tile / cols * kWide + rank * kTileM + quarter * 32;
             const int n0 = p.tile % cols * BN + half * S::kWarpCols;
             // a whole tile goes to dW, a part to this CTA's first or last slot
             float* dst;
@@ -511,8 +562,8 @@ k_grouped_wgrad_tc(GroupedWgradArgs a, float* __restrict__ part, Join* __restric
                 rows = a.cin - c0;
                 width = a.cout - n0;
             } else {
-                dst = part + ((int64_t)plan.id[blockIdx.x] * 2 + p.slot) * (kTileM * BN) +
-                      quarter * 32 * BN + half * S::kWarpCols;
+                dst = part + ((int64_t)plan.id[me] * 2 + p.slot) * (kWide * BN) +
+                      (rank * kTileM + quarter * 32) * BN + half * S::kWarpCols;
                 pitch = BN;
                 rows = 32;
                 width = S::kWarpCols;
@@ -539,7 +590,8 @@ k_grouped_wgrad_tc(GroupedWgradArgs a, float* __restrict__ part, Join* __restric
     }
     __syncwarp();
     ptx::tc_fence_before();
-    __syncthreads();
+    if constexpr (PAIR) ptx::cluster_sync();
+    else __syncthreads();
     if (warp == 1) {
         ptx::tc_fence_after();
         ptx::tmem_dealloc_cg<1>(tmem, S::kTmemCols);
@@ -548,7 +600,7 @@ k_grouped_wgrad_tc(GroupedWgradArgs a, float* __restrict__ part, Join* __restric
 
 // Block (c, q): rows kJoinRows q .. of the tile that share c's plan names become the sum
 // of its parts, in the order of the shares.
-template <int BN>
+template <int BN, int WIDE>
 __global__ void __launch_bounds__(kJoinRows * BN / 4)
 k_grouped_wgrad_join(GroupedWgradArgs a, const float* __restrict__ part, const Join* __restrict__ joins)
 {
@@ -558,9 +610,9 @@ k_grouped_wgrad_join(GroupedWgradArgs a, const float* __restrict__ part, const J
     if (j.more == 0) return;
     const int cols = (a.cout + BN - 1) / BN;
     const int r = blockIdx.y * kJoinRows + threadIdx.x / (BN / 4), n = threadIdx.x % (BN / 4) * 4;
-    const int row = j.tile / cols * kTileM + r, col = j.tile % cols * BN + n;
+    const int row = j.tile / cols * WIDE + r, col = j.tile % cols * BN + n;
     if (row >= a.cin || col >= a.cout) return;
-    constexpr int64_t kSlot = kTileM * BN;
+    constexpr int64_t kSlot = WIDE * BN;
     const float* src = part + r * BN + n;
     float4 s = __ldcs(reinterpret_cast<const float4*>(src + ((int64_t)c * 2 + j.slot) * kSlot));
     src += (int64_t)(c + 1) * 2 * kSlot;
@@ -575,7 +627,7 @@ k_grouped_wgrad_join(GroupedWgradArgs a, const float* __restrict__ part, const J
     *reinterpret_cast<float4*>(a.dw + ((int64_t)j.g * a.cin + row) * a.cout + col) = s;
 }
 
-int grouped_wgrad_ctas() { return std::min(sm_count(), kMaxParts); }
+int grouped_wgrad_ctas() { return std::min(sm_count(), kMaxParts) / 2 * 2; }
 
 // Two parts of a tile for each CTA, and the joins.
 size_t parts_bytes()
@@ -583,7 +635,7 @@ size_t parts_bytes()
     return align_up((sizeof(float) * 2 * kTileM * 256 + sizeof(Join)) * (size_t)grouped_wgrad_ctas(), 256);
 }
 
-template <typename T, int BN, bool GATHER>
+template <typename T, int BN, bool GATHER, bool PAIR>
 spc_status launch(const GroupedWgradArgs& a, float* part, cudaStream_t st)
 {
     using S = Shape<BN>;
@@ -591,25 +643,31 @@ spc_status launch(const GroupedWgradArgs& a, float* part, cudaStream_t st)
     if (!tmap_2d(&mx, Fmt<T>::t, 2, a.x, (uint64_t)a.cin, (uint64_t)a.n_x, 64, kUnit, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !tmap_2d(&my, Fmt<T>::t, 2, a.dy, (uint64_t)a.cout, (uint64_t)a.n_y, 64, kUnit, CU_TENSOR_MAP_SWIZZLE_128B))
         return SPC_ERR_CUDA;
-    const spc_status allowed = allow_smem<k_grouped_wgrad_tc<T, BN, GATHER>>();
+    const spc_status allowed = allow_smem<k_grouped_wgrad_tc<T, BN, GATHER, PAIR>>();
     if (allowed != SPC_OK) return allowed;
-    const int parts = grouped_wgrad_ctas();
-    Join* joins = reinterpret_cast<Join*>(part + (int64_t)parts * 2 * kTileM * 256);
+    const int parts = PAIR ? grouped_wgrad_ctas() / 2 : grouped_wgrad_ctas();
+    Join* joins = reinterpret_cast<Join*>(part + (int64_t)grouped_wgrad_ctas() * 2 * kTileM * 256);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)parts);
+    cfg.gridDim = dim3((unsigned)(PAIR ? 2 * parts : parts));
     cfg.blockDim = dim3(GATHER ? kThreads + kGatherThreads : kThreads);
     cfg.dynamicSmemBytes = S::smem(a.segments);
     cfg.stream = st;
-    SPC_CUDA_TRY(cudaLaunchKernelEx(&cfg, k_grouped_wgrad_tc<T, BN, GATHER>, a, part, joins, wait_limit_ns(), mx, my));
-    cfg.gridDim = dim3((unsigned)parts, kTileM / kJoinRows);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = PAIR ? 1 : 0;
+    SPC_CUDA_TRY(cudaLaunchKernelEx(&cfg, k_grouped_wgrad_tc<T, BN, GATHER, PAIR>, a, part, joins, wait_limit_ns(), mx, my));
+    constexpr int kWide = PAIR ? 2 * kTileM : kTileM;
+    cfg.gridDim = dim3((unsigned)parts, kWide / kJoinRows);
     cfg.blockDim = dim3(kJoinRows * BN / 4);
     cfg.dynamicSmemBytes = 0;
-    cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
     cfg.numAttrs = 1;
-    SPC_CUDA_TRY(cudaLaunchKernelEx(&cfg, k_grouped_wgrad_join<BN>, a, (const float*)part, (const Join*)joins));
+    SPC_CUDA_TRY(cudaLaunchKernelEx(&cfg, k_grouped_wgrad_join<BN, kWide>, a, (const float*)part, (const Join*)joins));
     return SPC_OK;
 }
 
@@ -641,7 +699,7 @@ spc_status bring(const void* from, const int32_t* list, int64_t rows, int64_t m,
     return SPC_OK;
 }
 
-// Listed rows of wide operands are brought into order first: a tile row (column) of weights would copy
+// Listed rows of wide operands are brought into order first: every tile row (column) of weights would copy
 // each of them again (bf16, 8 segments of 4096, 512 x 2048: 129 us against 194 by copies in the
 // kernel; 398,833 rows of 128 x 128, where each is copied once: 75 in the kernel).  128 x 128 tiles where 128 x 256
 // would be empty by half.
@@ -650,7 +708,9 @@ bool brings_rows(int32_t cin, int32_t cout) { return cin > kTileM && cout > kTil
 template <typename T>
 spc_status pick(GroupedWgradArgs a, float* part, cudaStream_t st)
 {
-    if ((a.x_rows || a.y_rows) && !brings_rows(a.cin, a.cout)) return launch<T, 128, true>(a, part, st);
+    // tiles are counted in 31 bits
+    if (ceil_div(a.cin, 128) * ceil_div(a.cout, 128) * a.segments > INT32_MAX) return SPC_ERR_UNSUPPORTED;
+    if ((a.x_rows || a.y_rows) && !brings_rows(a.cin, a.cout)) return launch<T, 128, true, false>(a, part, st);
     if (a.x_rows || a.y_rows) {
         uint8_t* x = reinterpret_cast<uint8_t*>(part) + parts_bytes();
         uint8_t* dy = x + align_up((size_t)a.m * a.cin * 2, 256);
@@ -668,7 +728,8 @@ spc_status pick(GroupedWgradArgs a, float* part, cudaStream_t st)
         }
         a.x_rows = a.y_rows = nullptr;
     }
-    return a.cout > 128 ? launch<T, 256, false>(a, part, st) : launch<T, 128, false>(a, part, st);
+    if (a.cout <= 128) return launch<T, 128, false, false>(a, part, st);
+    return a.cin > kTileM ? launch<T, 256, false, true>(a, part, st) : launch<T, 256, false, false>(a, part, st);
 }
 
 }  // namespace

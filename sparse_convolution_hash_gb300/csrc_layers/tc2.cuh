@@ -36,24 +36,6 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr)
     asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
-// mbar_wait for a barrier on which another CTA of the cluster arrives.
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, uint64_t limit_ns)
-{
-    const uint64_t t0 = globaltimer();
-    while (true) {
-        uint32_t done;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(done)
-            : "r"(smem_u32(bar)), "r"(parity)
-            : "memory");
-        if (done) return true;
-        if (globaltimer() - t0 >= limit_ns) return false;
-    }
-}
-
 // TMA loads that complete on an mbarrier named by its cluster address (for a
 // CTA pair, the leader's).
 template <int CG>
@@ -67,6 +49,14 @@ __device__ __forceinline__ void tma_load2d(uint32_t dst, const void* tmap, int32
         asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
                      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(tmap), "r"(x), "r"(y), "r"(bar)
                      : "memory");
+}
+
+// The same box into every CTA of a pair, at the same offset, completing on each one's barrier.
+__device__ __forceinline__ void tma_load2d_both(uint32_t dst, const void* tmap, int32_t x, int32_t y, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
+                 " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst), "l"(tmap), "r"(x), "r"(y), "r"(bar), "h"((uint16_t)3)
+                 : "memory");
 }
 
 template <int CG>
@@ -133,6 +123,14 @@ __device__ __forceinline__ void mma_commit_cg(uint64_t* bar)
         asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
                      " [%0], %1;" ::"r"(smem_u32(bar)), "h"((uint16_t)3)
                      : "memory");
+}
+
+// One CTA's MMAs, reported to both CTAs of a pair.
+__device__ __forceinline__ void mma_commit_both(uint64_t* bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+                 " [%0], %1;" ::"r"(smem_u32(bar)), "h"((uint16_t)3)
+                 : "memory");
 }
 
 }  // namespace ptx

@@ -374,7 +374,8 @@ GROUPED = [  # m, cin, cout, segments, keys, slots (0: rows in grouped order)
     (257, 128, 64, 4, "out", 1), (512, 64, 136, 2, "one", 2), (600, 200, 128, 7, "random", 2),
     (777, 100, 72, 5, "out", 0), (1000, 33, 65, 9, "random", 2), (64, 256, 512, 64, "random", 2),
     (1500, 256, 264, 3, "random", 1), (900, 72, 1000, 40, "out", 2), (300, 520, 40, 2, "random", 0),
-    (16, 1024, 256, 100, "random", 2), (129, 8, 24, 200, "random", 0), (2600, 128, 384, 2, "one", 1)]
+    (16, 1024, 256, 100, "random", 2), (129, 8, 24, 200, "random", 0), (2600, 128, 384, 2, "one", 1),
+    (9000, 264, 264, 3, "random", 0), (9000, 136, 264, 2, "one", 2), (12000, 64, 520, 4, "sorted", 0)]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
