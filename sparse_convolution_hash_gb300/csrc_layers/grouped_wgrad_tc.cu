@@ -11,7 +11,7 @@
 //
 // The tensor core truncates where it adds to an accumulator, so sums over long segments would
 // drift (4096 rows: 5 10^-6 of the result).  An accumulator takes 512 rows; eight warps then add it,
-// rounding, to the piece's sums in their registers while the other one fills (6 10^-7).
+// rounding, to the piece's sums in their registers while the other one fills (5 10^-7).
 //
 // In a CTA, as in the forward: warp 0 loads dense rows by TMA, eight more copy listed
 // rows by cp.async, warp 1 issues the MMAs into one of two accumulators and
