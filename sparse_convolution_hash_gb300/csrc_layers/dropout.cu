@@ -59,10 +59,10 @@ struct Rule {
 
 // Whole 16-byte vectors, kVectors of them in flight a thread, a block's neighbours together;
 // nothing but the vectors is read or written.  The generator's 20 wide multiplications for four
-// elements stand against 16 to 48 bytes: 398,833 x 128 bf16 with a residual takes 44 us with one of the ten
-// rounds and 54 with all (66 before the key schedule went to the uniform registers).
-// Two vectors and blocks of 128 hide most of it (one: 69, four: 58).
-constexpr int kVectors = 2;
+// elements stand against 16 to 48 bytes: 398,833 x 128 bf16 with a residual takes 48.5 us (6.3 TB/s)
+// and 44 with one of the ten rounds.  Four vectors hide most of it (two: 52, eight: 50; two and the key
+// schedule in every lane: 56).  498,145 x 64 fp16: 30 us, with two vectors 33.
+constexpr int kVectors = 4;
 template <typename T, bool RESIDUAL, bool ANY>
 __global__ void __launch_bounds__(kBlock)
 k_dropout(const T* x, const T* residual, int64_t n, Rule k, const uint64_t* __restrict__ rng, T* y)
