@@ -52,8 +52,8 @@ __device__ __forceinline__ void gather_pairs(F2 (&f)[kPairs<V>], F value)
 
 // ------------------------------------------------------------------- activations
 // 1 / (1 + exp(-z)) with the hardware's exp2 and reciprocal: within 2^-19 for the |z| of a
-// normalised feature, a small part of the rounding of a 16-bit output (the exact functions cost
-// the 498,145 x 64 bf16 forward 95 us against 82, all else equal).  The special-function unit has a
+// normalised feature, a small part of the rounding of a 16-bit output (with the exact functions
+// 498,145 x 64 bf16 takes 73 us forward for 37.5 and 185 for 63 in its gradients, repeated calls).  The special-function unit has a
 // quarter of the rate that this needs, so the pair shares one reciprocal, 1 / a = b / (a b);
 // exp is held to 2^57 for that, where the sigmoid is 0 to 17 digits.
 __device__ __forceinline__ F2 sigmoid(F2 z)
