@@ -20,8 +20,8 @@
 // Large inputs run at the pace of memory (498,145 x 64 bf16, 4 samples, SILU: forward 42.5 us,
 // gradients 66, reading rows twice).  With few rows every instruction is run once and costs
 // about 10 cycles whatever it does, so the code around the loops over rows is kept short: sums and
-// statistics go through the same code in turn, short runs take one row body (2,000 x 16 fp32, against
-// those unrolled: forward 9.1 us for 9.5, gradients 9.6 for 10.8).
+// statistics go through the same code in turn, short runs take one row body (2,000 x 16 fp32: with that
+// unrolled forward 9.5 us for 9.1, gradients 10.8 for 9.6; a launch beside the kernel before: 8.7 and 8.8).
 #pragma once
 
 #include "kernels.cuh"
@@ -519,8 +519,9 @@ __device__ __forceinline__ float warp_sum(float v)
     return v;
 }
 
-// Of a pass's two kernels the second may be launched while the first still runs.
-__device__ __forceinline__ void wait_for_first_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Both kernels of a pass may be launched while what stands before them in the stream still runs; they wait
+// for it here, the first before it touches memory, the second where it needs the first one's sums.
+__device__ __forceinline__ void wait_for_kernel_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // What the two kernels of a pass hand over.
 struct Ws {
@@ -577,6 +578,7 @@ __global__ void __launch_bounds__(Feed<T, V, 1, DENSE>::kBlockThreads, 1) k_norm
     in.step = 1;
 #pragma unroll
     for (int t = 0; t < 1; ++t) in.base[t] = tensor[t] + at.tv * V;
+    wait_for_kernel_before();
     in.ahead(at.begin, at.end, tensor);
     load_offsets(a, s_seg, blockIdx.x == 0);
     if (DENSE && at.warp == kThreads / 32) {
@@ -799,7 +801,7 @@ __global__ void __launch_bounds__(Feed<T, V, 1, DENSE>::kBlockThreads, 1) k_norm
             continue;
         }
         in.begin(k);
-        if (!waited) wait_for_first_kernel();
+        if (!waited) wait_for_kernel_before();
         waited = true;
         join_stats(a, s_seg, k.s, rows, w.part, s_stat);
         F2 minus[kPairs<V>], scale[kPairs<V>];
@@ -816,7 +818,7 @@ __global__ void __launch_bounds__(Feed<T, V, 1, DENSE>::kBlockThreads, 1) k_norm
             *reinterpret_cast<Vec<T, V>*>(y + row * a.c) = pack<T, V>(f[0]);
         });
     }
-    if (!waited) wait_for_first_kernel();
+    if (!waited) wait_for_kernel_before();
 }
 
 // -------------------------------------------------------------------- gradients
@@ -837,6 +839,7 @@ __global__ void __launch_bounds__(Feed<T, V, 2, DENSE>::kBlockThreads, 1) k_norm
     in.step = 1;
 #pragma unroll
     for (int t = 0; t < 2; ++t) in.base[t] = tensor[t] + at.tv * V;
+    wait_for_kernel_before();
     in.ahead(at.begin, at.end, tensor);
     load_offsets(a, s_seg, blockIdx.x == 0);
     if (DENSE && at.warp == kThreads / 32) {
@@ -972,7 +975,7 @@ __global__ void __launch_bounds__(Feed<T, V, 2, DENSE>::kBlockThreads, 1) k_norm
             continue;
         }
         in.begin(k);
-        if (!waited) wait_for_first_kernel();
+        if (!waited) wait_for_kernel_before();
         waited = true;
         const Span span(s_seg, k.s, rows);
         sync_workers();
@@ -1025,7 +1028,7 @@ __global__ void __launch_bounds__(Feed<T, V, 2, DENSE>::kBlockThreads, 1) k_norm
             *reinterpret_cast<Vec<T, V>*>(dx + row * a.c) = pack<T, V>(f[0]);
         });
     }
-    if (!waited) wait_for_first_kernel();
+    if (!waited) wait_for_kernel_before();
     // dgamma and dbeta: a warp for each channel
     if (a.dgamma || a.dbeta)
         for (int ch = blockIdx.x * (kThreads / 32) + at.warp; ch < a.c; ch += gridDim.x * (kThreads / 32)) {
@@ -1220,10 +1223,8 @@ size_t carve(int64_t n, int32_t c, int32_t segments, int32_t groups, char* base,
     return off;
 }
 
-// second: the second kernel of a pass, which waits for the first one itself.
 template <auto KERNEL>
-spc_status launch(int shares, int threads, size_t smem, cudaStream_t st, const NormArgs& a, int64_t rows, const Ws& w,
-                  bool second)
+spc_status launch(int shares, int threads, size_t smem, cudaStream_t st, const NormArgs& a, int64_t rows, const Ws& w)
 {
     const spc_status allowed = allow_smem<KERNEL>();
     if (allowed != SPC_OK) return allowed;
@@ -1236,7 +1237,7 @@ spc_status launch(int shares, int threads, size_t smem, cudaStream_t st, const N
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = second ? 1 : 0;
+    cfg.numAttrs = 1;
     SPC_CUDA_TRY(cudaLaunchKernelEx(&cfg, KERNEL, a, rows, w, wait_limit_ns()));
     return SPC_OK;
 }
@@ -1251,16 +1252,16 @@ spc_status rows_pass(const NormArgs& a, const Ws& w, bool backward, cudaStream_t
         using F = Feed<T, V, 2, DENSE>;
         const size_t base = F::kSmem + offsets;
         const spc_status s = launch<k_norm_bwd_sums<T, V, DENSE, SILU>>(shares, F::kBlockThreads,
-                                    base + sizeof(float) * (kSums<V, 2> + 2 * a.c), st, a, rows, w, false);
-        return s != SPC_OK ? s : launch<k_norm_bwd_apply<T, V, DENSE, SILU>>(shares, F::kBlockThreads, base + stat, st, a, rows, w, true);
+                                    base + sizeof(float) * (kSums<V, 2> + 2 * a.c), st, a, rows, w);
+        return s != SPC_OK ? s : launch<k_norm_bwd_apply<T, V, DENSE, SILU>>(shares, F::kBlockThreads, base + stat, st, a, rows, w);
     }
     using F = Feed<T, V, 1, DENSE>;
     const size_t base = F::kSmem + offsets;
     const spc_status s = launch<k_norm_stats<T, V, DENSE>>(shares, F::kBlockThreads,
-                                base + sizeof(float) * (kSums<V, 1> + 2 * a.c), st, a, rows, w, false);
+                                base + sizeof(float) * (kSums<V, 1> + 2 * a.c), st, a, rows, w);
     return s != SPC_OK || a.n == 0
                ? s
-               : launch<k_norm_apply<T, V, DENSE, SILU>>(shares, F::kBlockThreads, base + stat, st, a, rows, w, true);
+               : launch<k_norm_apply<T, V, DENSE, SILU>>(shares, F::kBlockThreads, base + stat, st, a, rows, w);
 }
 
 template <typename T, int V>
