@@ -519,10 +519,6 @@ __device__ __forceinline__ float warp_sum(float v)
     return v;
 }
 
-// Both kernels of a pass may be launched while what stands before them in the stream still runs; they wait
-// for it here, the first before it touches memory, the second where it needs the first one's sums.
-__device__ __forceinline__ void wait_for_kernel_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // What the two kernels of a pass hand over.
 struct Ws {
     float2* part;   // [2 shares][groups] sums over a shared segment's parts
@@ -1233,9 +1229,8 @@ spc_status launch(int shares, int threads, size_t smem, cudaStream_t st, const N
     cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    // the first kernel of a pass waits before it touches memory, the second where it needs the first one's sums
+    cudaLaunchAttribute attr[1] = {beside_the_kernel_before()};
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     SPC_CUDA_TRY(cudaLaunchKernelEx(&cfg, KERNEL, a, rows, w, wait_limit_ns()));

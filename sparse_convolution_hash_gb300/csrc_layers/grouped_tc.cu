@@ -89,6 +89,7 @@ k_grouped_tc(GroupedArgs a, uint64_t wait_ns, const __grid_constant__ CUtensorMa
     }
     if (warp == 1) ptx::tmem_alloc_cg<CG>(s_ctrl, S::kTmemCols);
     const int cols = (a.n + BN - 1) / BN;
+    wait_for_kernel_before();
     const int32_t tiles = tile_starts(a.seg, a.segments, a.m, S::kRows, cols, s_start,
                                       blockIdx.x == 0 ? a.status : nullptr, tid, kAll);
     ptx::tc_fence_before();
@@ -344,13 +345,13 @@ spc_status launch(const GroupedArgs& a, cudaStream_t st)
     cfg.blockDim = dim3(GATHER ? kThreads + kGatherThreads : kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = CG;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2] = {beside_the_kernel_before()};
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = CG == 2 ? 1 : 0;
+    cfg.numAttrs = CG == 2 ? 2 : 1;
     SPC_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, a, wait_limit_ns(), map_in, map_w));
     return SPC_OK;
 }

@@ -362,6 +362,7 @@ k_grouped_wgrad_tc(GroupedWgradArgs a, float* __restrict__ part, Join* __restric
     }
     if (warp == 1) ptx::tmem_alloc_cg<1>(s_ctrl, S::kTmemCols);
     const int cols = (a.cout + BN - 1) / BN, tiles = (a.cin + kWide - 1) / kWide * cols;
+    wait_for_kernel_before();
     if (warp == 0)
         make_plan(a.seg, a.segments, a.m, tiles, gridDim.x / kCtas, s_start, s_list, s_list + a.segments, &plan,
                   blockIdx.x == 0 ? a.status : nullptr, lane);
@@ -604,7 +605,7 @@ template <int BN, int WIDE>
 __global__ void __launch_bounds__(kJoinRows * BN / 4)
 k_grouped_wgrad_join(GroupedWgradArgs a, const float* __restrict__ part, const Join* __restrict__ joins)
 {
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the parts were still coming
+    wait_for_kernel_before();  // launched while the parts were still coming
     const int c = blockIdx.x;
     const Join j = joins[c];
     if (j.more == 0) return;
@@ -652,20 +653,18 @@ spc_status launch(const GroupedWgradArgs& a, float* part, cudaStream_t st)
     cfg.blockDim = dim3(GATHER ? kThreads + kGatherThreads : kThreads);
     cfg.dynamicSmemBytes = S::smem(a.segments);
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2] = {beside_the_kernel_before()};
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = PAIR ? 1 : 0;
+    cfg.numAttrs = PAIR ? 2 : 1;
     SPC_CUDA_TRY(cudaLaunchKernelEx(&cfg, k_grouped_wgrad_tc<T, BN, GATHER, PAIR>, a, part, joins, wait_limit_ns(), mx, my));
     constexpr int kWide = PAIR ? 2 * kTileM : kTileM;
     cfg.gridDim = dim3((unsigned)parts, kWide / kJoinRows);
     cfg.blockDim = dim3(kJoinRows * BN / 4);
     cfg.dynamicSmemBytes = 0;
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.numAttrs = 1;
     SPC_CUDA_TRY(cudaLaunchKernelEx(&cfg, k_grouped_wgrad_join<BN, kWide>, a, (const float*)part, (const Join*)joins));
     return SPC_OK;

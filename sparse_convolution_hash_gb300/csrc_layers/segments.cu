@@ -331,9 +331,7 @@ spc_status row_segments(const int32_t* ids, int64_t id_stride, int64_t n, int32_
     cfg.blockDim = dim3(kBlock);
     cfg.dynamicSmemBytes = sizeof(int32_t) * (size_t)bins * (2 + kWarps);
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchAttribute attr[1] = {beside_the_kernel_before()};
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     SPC_CUDA_TRY(cudaLaunchKernelEx(&cfg, keep ? k_seg_place<true> : k_seg_place<false>, ids, id_stride, n, (int)segments,
