@@ -69,6 +69,7 @@ k_dropout(const T* x, const T* residual, int64_t n, Rule k, const uint64_t* __re
 {
     constexpr int E = 16 / sizeof(T);
     using P = Vec<T, E>;
+    wait_for_kernel_before();
     const Keys keys(rng);
     const int64_t vectors = n / E, first = (int64_t)blockIdx.x * (kBlock * kVectors) + threadIdx.x;
     P v[kVectors], r[kVectors];
@@ -120,6 +121,7 @@ template <typename T, bool ANY>
 __global__ void __launch_bounds__(kBlock)
 k_dropout_unaligned(const T* x, const T* residual, int64_t n, Rule k, const uint64_t* __restrict__ rng, T* y)
 {
+    wait_for_kernel_before();
     const Keys keys(rng);
     const int64_t q = (int64_t)blockIdx.x * kBlock + threadIdx.x;
     if (q * 4 >= n) return;
@@ -144,10 +146,15 @@ spc_status launch(const void* xv, const void* rv, int64_t n, const Rule& k, cons
     const int64_t blocks = whole ? std::max<int64_t>(1, ceil_div(n / (16 / (int64_t)sizeof(T)), kBlock * kVectors))
                                  : ceil_div(ceil_div(n, 4), kBlock);
     if (blocks > INT32_MAX) return SPC_ERR_UNSUPPORTED;
-    if (!whole) k_dropout_unaligned<T, ANY><<<(unsigned)blocks, kBlock, 0, st>>>(x, r, n, k, rng, y);
-    else if (r) k_dropout<T, true, ANY><<<(unsigned)blocks, kBlock, 0, st>>>(x, r, n, k, rng, y);
-    else k_dropout<T, false, ANY><<<(unsigned)blocks, kBlock, 0, st>>>(x, r, n, k, rng, y);
-    SPC_LAUNCH_CHECK();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(kBlock);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1] = {beside_the_kernel_before()};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    auto* kernel = !whole ? k_dropout_unaligned<T, ANY> : r ? k_dropout<T, true, ANY> : k_dropout<T, false, ANY>;
+    SPC_CUDA_TRY(cudaLaunchKernelEx(&cfg, kernel, x, r, n, k, rng, y));
     return SPC_OK;
 }
 
