@@ -27,7 +27,7 @@ struct Keys {
     uint32_t k0, k1, c2, c3;
     __device__ __forceinline__ explicit Keys(const uint64_t* rng)
     {
-        const uint64_t seed = __ldg(rng), offset = __ldg(rng + 1);
+        const uint64_t seed = fetch(rng), offset = fetch(rng + 1);
         k0 = __reduce_or_sync(FULL_MASK, (uint32_t)seed);
         k1 = __reduce_or_sync(FULL_MASK, (uint32_t)(seed >> 32));
         c2 = __reduce_or_sync(FULL_MASK, (uint32_t)offset);
@@ -65,7 +65,7 @@ struct Rule {
 constexpr int kVectors = 4;
 template <typename T, bool RESIDUAL, bool ANY>
 __global__ void __launch_bounds__(kBlock)
-k_dropout(const T* x, const T* residual, int64_t n, Rule k, const uint64_t* __restrict__ rng, T* y)
+k_dropout(const T* x, const T* residual, int64_t n, Rule k, const uint64_t* rng, T* y)
 {
     constexpr int E = 16 / sizeof(T);
     using P = Vec<T, E>;
@@ -119,7 +119,7 @@ k_dropout(const T* x, const T* residual, int64_t n, Rule k, const uint64_t* __re
 // Tensors off a 16-byte boundary: four elements a thread, one by one.
 template <typename T, bool ANY>
 __global__ void __launch_bounds__(kBlock)
-k_dropout_unaligned(const T* x, const T* residual, int64_t n, Rule k, const uint64_t* __restrict__ rng, T* y)
+k_dropout_unaligned(const T* x, const T* residual, int64_t n, Rule k, const uint64_t* rng, T* y)
 {
     wait_for_kernel_before();
     const Keys keys(rng);

@@ -119,9 +119,9 @@ __device__ __forceinline__ float block_sum(float v)
 __device__ __forceinline__ void load_offsets(const NormArgs& a, int32_t* s_seg, bool report)
 {
     for (int s = threadIdx.x; s <= a.segments; s += (int)blockDim.x) {
-        const int32_t v = __ldg(a.seg + s);
+        const int32_t v = fetch(a.seg + s);
         s_seg[s] = v < 0 ? 0 : (v > a.n ? (int32_t)a.n : v);
-        if (report && (v < 0 || v > a.n || (s < a.segments && __ldg(a.seg + s + 1) < v)))
+        if (report && (v < 0 || v > a.n || (s < a.segments && fetch(a.seg + s + 1) < v)))
             set_status(a.status, SPC_ERR_ROW_INDEX);
     }
     __syncthreads();
@@ -292,7 +292,7 @@ struct Feed {
     __device__ __forceinline__ void list_rows(int64_t p)
     {
 #pragma unroll
-        for (int q = 0; q < kRowsOf; ++q, p += rt) next[q] = p >= hi ? -1 : a.order ? __ldg(a.order + p) : (int32_t)p;
+        for (int q = 0; q < kRowsOf; ++q, p += rt) next[q] = p >= hi ? -1 : a.order ? fetch(a.order + p) : (int32_t)p;
     }
     __device__ __forceinline__ void wait_full()
     {
@@ -778,8 +778,8 @@ __global__ void __launch_bounds__(Feed<T, V, 1, DENSE>::kBlockThreads, 1) k_norm
         return;
     }
     F2 gamma[kPairs<V>], beta[kPairs<V>];
-    gather_pairs<V>(gamma, [&](int j) { return works && a.gamma ? __ldg(a.gamma + at.tv * V + j) : 1.f; });
-    gather_pairs<V>(beta, [&](int j) { return works && a.beta ? __ldg(a.beta + at.tv * V + j) : 0.f; });
+    gather_pairs<V>(gamma, [&](int j) { return works && a.gamma ? fetch(a.gamma + at.tv * V + j) : 1.f; });
+    gather_pairs<V>(beta, [&](int j) { return works && a.beta ? fetch(a.beta + at.tv * V + j) : 0.f; });
     const float floor = floor_of(a.act);
     bool waited = false;
     for (int64_t r0 = at.end; r0 > at.begin;) {
@@ -851,8 +851,8 @@ __global__ void __launch_bounds__(Feed<T, V, 2, DENSE>::kBlockThreads, 1) k_norm
     }
     const Columns columns(a.c, at.rt);
     F2 gamma[kPairs<V>], beta[kPairs<V>];
-    gather_pairs<V>(gamma, [&](int j) { return works && a.gamma ? __ldg(a.gamma + at.tv * V + j) : 1.f; });
-    gather_pairs<V>(beta, [&](int j) { return works && a.beta ? __ldg(a.beta + at.tv * V + j) : 0.f; });
+    gather_pairs<V>(gamma, [&](int j) { return works && a.gamma ? fetch(a.gamma + at.tv * V + j) : 1.f; });
+    gather_pairs<V>(beta, [&](int j) { return works && a.beta ? fetch(a.beta + at.tv * V + j) : 0.f; });
     const float least = least_of(a.act);
     float all[2][V];
 #pragma unroll
@@ -867,9 +867,9 @@ __global__ void __launch_bounds__(Feed<T, V, 2, DENSE>::kBlockThreads, 1) k_norm
         in.begin(k);
         const float* mean = a.mean + (int64_t)k.s * a.groups;
         const float* rstd = a.rstd + (int64_t)k.s * a.groups;
-        gather_pairs<V>(minus, [&](int j) { return works ? -__ldg(mean + at.group[j]) : 0.f; });
+        gather_pairs<V>(minus, [&](int j) { return works ? -fetch(mean + at.group[j]) : 0.f; });
         gather_pairs<V>(scale, [&](int j) {
-            return works ? __ldg(rstd + at.group[j]) : 0.f;
+            return works ? fetch(rstd + at.group[j]) : 0.f;
         });
 #pragma unroll
         for (int j = 0; j < kPairs<V>; ++j) scale[j] = mul(scale[j], gamma[j]);
@@ -884,7 +884,7 @@ __global__ void __launch_bounds__(Feed<T, V, 2, DENSE>::kBlockThreads, 1) k_norm
         });
         if (works) {
             F2 r[kPairs<V>];
-            gather_pairs<V>(r, [&](int j) { return __ldg(rstd + at.group[j]); });
+            gather_pairs<V>(r, [&](int j) { return fetch(rstd + at.group[j]); });
 #pragma unroll
             for (int j = 0; j < kPairs<V>; ++j) sum[1][j] = mul(sum[1][j], r[j]);
         }
@@ -902,7 +902,7 @@ __global__ void __launch_bounds__(Feed<T, V, 2, DENSE>::kBlockThreads, 1) k_norm
             float m0 = 0.f, m1 = 0.f;
             for (int j = way.lane; j < at.per; j += way.lanes) {
                 const int ch = g * at.per + j;
-                const float u = a.gamma ? __ldg(a.gamma + ch) : 1.f;
+                const float u = a.gamma ? fetch(a.gamma + ch) : 1.f;
                 m0 = fmaf(u, s_dz[ch], m0);
                 m1 = fmaf(u, s_dz[a.c + ch], m1);
             }
@@ -952,8 +952,8 @@ __global__ void __launch_bounds__(Feed<T, V, 2, DENSE>::kBlockThreads, 1) k_norm
         return;
     }
     F2 gamma[kPairs<V>], beta[kPairs<V>];
-    gather_pairs<V>(gamma, [&](int j) { return works && a.gamma ? __ldg(a.gamma + at.tv * V + j) : 1.f; });
-    gather_pairs<V>(beta, [&](int j) { return works && a.beta ? __ldg(a.beta + at.tv * V + j) : 0.f; });
+    gather_pairs<V>(gamma, [&](int j) { return works && a.gamma ? fetch(a.gamma + at.tv * V + j) : 1.f; });
+    gather_pairs<V>(beta, [&](int j) { return works && a.beta ? fetch(a.beta + at.tv * V + j) : 0.f; });
     const float least = least_of(a.act);
     bool waited = false;
     for (int64_t r0 = at.end; r0 > at.begin;) {
@@ -999,19 +999,19 @@ __global__ void __launch_bounds__(Feed<T, V, 2, DENSE>::kBlockThreads, 1) k_norm
         F2 minus[kPairs<V>], scale[kPairs<V>], lift[kPairs<V>], tilt[kPairs<V>];
         const float* mean = a.mean + (int64_t)k.s * a.groups;
         const float* rstd = a.rstd + (int64_t)k.s * a.groups;
-        gather_pairs<V>(minus, [&](int j) { return -__ldg(mean + at.group[j]); });
+        gather_pairs<V>(minus, [&](int j) { return -fetch(mean + at.group[j]); });
         gather_pairs<V>(scale, [&](int j) {
-            return works ? __ldg(rstd + at.group[j]) : 0.f;
+            return works ? fetch(rstd + at.group[j]) : 0.f;
         });
 #pragma unroll
         for (int j = 0; j < kPairs<V>; ++j) scale[j] = mul(scale[j], gamma[j]);
         gather_pairs<V>(lift, [&](int j) {
             const int g = at.group[j];
-            return -__ldg(rstd + g) * s_stat[g].x;
+            return -fetch(rstd + g) * s_stat[g].x;
         });
         gather_pairs<V>(tilt, [&](int j) {
             const int g = at.group[j];
-            const float r = __ldg(rstd + g);
+            const float r = fetch(rstd + g);
             return -r * r * s_stat[g].y;
         });
         in.run(works, [&](F2 (&f)[2][kPairs<V>], int64_t row) {

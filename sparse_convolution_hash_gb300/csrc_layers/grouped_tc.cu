@@ -202,7 +202,7 @@ k_grouped_tc(GroupedArgs a, uint64_t wait_ns, const __grid_constant__ CUtensorMa
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int64_t p = k.lo + r0 + 32 * j;
-                    v[j] = p < k.hi && k.g >= 0 ? __ldg(a.in_rows + p) : -1;
+                    v[j] = p < k.hi && k.g >= 0 ? fetch(a.in_rows + p) : -1;
                 }
             };
             int32_t entry[4] = {-1, -1, -1, -1}, after[4];

@@ -25,11 +25,11 @@ struct TileWalk {
     __device__ __forceinline__ void bounds(int entry, int64_t& lo, int64_t& hi) const
     {
         if (entry == 0) {
-            const int64_t f = __ldg(seg);
+            const int64_t f = fetch(seg);
             lo = 0;
             hi = f < 0 ? 0 : (f > m ? m : f);
         } else if (entry > segments) {
-            const int64_t f = __ldg(seg + segments);
+            const int64_t f = fetch(seg + segments);
             lo = f < 0 ? 0 : (f > m ? m : f);
             hi = m;
         } else {
@@ -75,12 +75,12 @@ __device__ __forceinline__ int32_t tile_starts(const int32_t* seg, int segments,
         const int v = v0 + tid;
         int64_t a = 0, b = 0;
         if (v == 0) {
-            const int64_t f = __ldg(seg);
+            const int64_t f = fetch(seg);
             b = f < 0 ? 0 : (f > m ? m : f);
         } else if (v <= segments) {
             segment_bounds(seg, v - 1, m, status, a, b);
         } else if (v == segments + 1) {
-            const int64_t f = __ldg(seg + segments);
+            const int64_t f = fetch(seg + segments);
             a = f < 0 ? 0 : (f > m ? m : f);
             b = m;
         }

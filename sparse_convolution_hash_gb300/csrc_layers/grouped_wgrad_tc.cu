@@ -477,8 +477,8 @@ k_grouped_wgrad_tc(GroupedWgradArgs a, float* __restrict__ part, Join* __restric
                     for (int j = 0; j < 2; ++j) {
                         const int64_t r = p.lo + (int64_t)k * kUnit + r0 + 32 * j;
                         const bool in = k < p.k1 && r < p.hi;
-                        xe[j] = !in ? -1 : a.x_rows ? __ldg(a.x_rows + r) : (int32_t)r;
-                        ye[j] = !in ? -1 : a.y_rows ? __ldg(a.y_rows + r) : (int32_t)r;
+                        xe[j] = !in ? -1 : a.x_rows ? fetch(a.x_rows + r) : (int32_t)r;
+                        ye[j] = !in ? -1 : a.y_rows ? fetch(a.y_rows + r) : (int32_t)r;
                     }
                 };
                 int32_t xe[2], ye[2], xn[2], yn[2];
@@ -603,7 +603,7 @@ k_grouped_wgrad_tc(GroupedWgradArgs a, float* __restrict__ part, Join* __restric
 // of its parts, in the order of the shares.
 template <int BN, int WIDE>
 __global__ void __launch_bounds__(kJoinRows * BN / 4)
-k_grouped_wgrad_join(GroupedWgradArgs a, const float* __restrict__ part, const Join* __restrict__ joins)
+k_grouped_wgrad_join(GroupedWgradArgs a, const float* part, const Join* joins)
 {
     wait_for_kernel_before();  // launched while the parts were still coming
     const int c = blockIdx.x;
@@ -615,11 +615,11 @@ k_grouped_wgrad_join(GroupedWgradArgs a, const float* __restrict__ part, const J
     if (row >= a.cin || col >= a.cout) return;
     constexpr int64_t kSlot = WIDE * BN;
     const float* src = part + r * BN + n;
-    float4 s = __ldcs(reinterpret_cast<const float4*>(src + ((int64_t)c * 2 + j.slot) * kSlot));
+    float4 s = fetch(reinterpret_cast<const float4*>(src + ((int64_t)c * 2 + j.slot) * kSlot));
     src += (int64_t)(c + 1) * 2 * kSlot;
 #pragma unroll 8
     for (int q = 0; q < j.more; ++q) {
-        const float4 v = __ldcs(reinterpret_cast<const float4*>(src + q * 2 * kSlot));
+        const float4 v = fetch(reinterpret_cast<const float4*>(src + q * 2 * kSlot));
         s.x += v.x;
         s.y += v.y;
         s.z += v.z;
@@ -680,13 +680,13 @@ k_bring_rows(const uint4* __restrict__ from, const int32_t* __restrict__ list, i
     const int lane = threadIdx.x & 31;
     const int64_t r = (int64_t)blockIdx.x * kBringWarps + (threadIdx.x >> 5);
     if (r >= m) return;
-    const int32_t i = __ldg(list + r);
+    const int32_t i = fetch(list + r);
     const bool good = i >= 0 && i < rows;
     if (!good) set_status(status, SPC_ERR_ROW_INDEX);
     const uint4* src = from + (good ? i : 0) * (int64_t)words;
     uint4* dst = to + r * words;
 #pragma unroll 4
-    for (int w = lane; w < words; w += 32) dst[w] = good ? __ldg(src + w) : make_uint4(0, 0, 0, 0);
+    for (int w = lane; w < words; w += 32) dst[w] = good ? fetch(src + w) : make_uint4(0, 0, 0, 0);
 }
 
 spc_status bring(const void* from, const int32_t* list, int64_t rows, int64_t m, int32_t c, void* to, int32_t* status, cudaStream_t st)

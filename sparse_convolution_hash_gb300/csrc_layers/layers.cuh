@@ -107,6 +107,10 @@ inline cudaLaunchAttribute beside_the_kernel_before()
     return at;
 }
 __device__ __forceinline__ void wait_for_kernel_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Such kernels read what others wrote by ordinary loads: one through the read-only path might be
+// moved ahead of the wait.
+template <typename T>
+__device__ __forceinline__ T fetch(const T* p) { return *p; }
 
 // ------------------------------------------------------------ device helpers
 // Segment s as positions [lo, hi) inside [0, n): offsets out of range or out of
@@ -114,7 +118,7 @@ __device__ __forceinline__ void wait_for_kernel_before() { asm volatile("griddep
 __device__ __forceinline__ void segment_bounds(const int32_t* seg, int s, int64_t n, int32_t* status,
                                                int64_t& lo, int64_t& hi)
 {
-    const int64_t a = __ldg(seg + s), b = __ldg(seg + s + 1);
+    const int64_t a = fetch(seg + s), b = fetch(seg + s + 1);
     lo = a < 0 ? 0 : (a > n ? n : a);
     hi = b < lo ? lo : (b > n ? n : b);
     if (lo != a || hi != b) set_status(status, SPC_ERR_ROW_INDEX);
@@ -127,7 +131,7 @@ __device__ __forceinline__ int segment_of(const int32_t* seg, int segments, int6
     int lo = 0, hi = segments + 1;  // first index with seg[index] > r
     while (lo < hi) {
         const int mid = (lo + hi) >> 1;
-        if (__ldg(seg + mid) > r) hi = mid;
+        if (fetch(seg + mid) > r) hi = mid;
         else lo = mid + 1;
     }
     return lo - 1;
@@ -137,7 +141,7 @@ __device__ __forceinline__ int segment_of(const int32_t* seg, int segments, int6
 __device__ __forceinline__ int64_t row_at(const int32_t* list, int64_t r, int64_t rows, int32_t* status)
 {
     if (!list) return r;
-    const int32_t i = __ldg(list + r);
+    const int32_t i = fetch(list + r);
     if (i < 0 || i >= rows) {
         set_status(status, SPC_ERR_ROW_INDEX);
         return -1;
