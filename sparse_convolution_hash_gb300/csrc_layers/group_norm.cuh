@@ -17,11 +17,11 @@
 // Gradients: with dz = dy act'(z), sums of dz and dz (x - mean) per channel give dgamma,
 // dbeta and, weighted by gamma, the two means of a group; dx = A dz + B + D (x - mean).
 //
-// Large inputs run at the pace of memory (498,145 x 64 bf16, 4 samples, SILU: forward 42.5 us,
-// gradients 66, reading rows twice).  With few rows every instruction is run once and costs
+// Large inputs run at the pace of memory (498,145 x 64 bf16, 4 samples, SILU: forward 41 us,
+// gradients 65, reading rows twice).  With few rows every instruction is run once and costs
 // about 10 cycles whatever it does, so the code around the loops over rows is kept short: sums and
 // statistics go through the same code in turn, short runs take one row body (2,000 x 16 fp32: with that
-// unrolled forward 9.5 us for 9.1, gradients 10.8 for 9.6; a launch beside the kernel before: 8.7 and 8.8).
+// unrolled forward 9.5 us for 9.1, gradients 10.8 for 9.6; a launch beside the kernel before: 8.8 and 9.2).
 #pragma once
 
 #include "kernels.cuh"

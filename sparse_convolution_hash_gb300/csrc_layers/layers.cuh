@@ -98,7 +98,7 @@ spc_status allow_smem()
 
 // Launch attribute of a kernel that may be set up while the one before it in the stream ends; it touches no
 // memory of others before wait_for_kernel_before() (grouped forward, 2,048 rows in 8 segments, 512 x 512 bf16,
-// repeated: 7.4 us against 7.9; 2,000 x 16 fp32 group norm 8.7 against 9.1).
+// repeated: 7.4 us against 7.9; 2,000 x 16 fp32 group norm 8.8 against 9.1).
 inline cudaLaunchAttribute beside_the_kernel_before()
 {
     cudaLaunchAttribute at;
