@@ -103,6 +103,7 @@ def main():
     coords = torch.from_numpy(w["coords"]).to(dev)
     scene = Scene(coords, w["batch"], w["shape"])
     block = ExpertBlock(channels=64, hidden=256, experts=8, groups=16, p=0.1, dtype=torch.bfloat16, device=dev)
+    torch.manual_seed(0)
     x, dy = w["x"].to(dev), torch.randn(coords.shape[0], 64, device=dev).to(torch.bfloat16)
     rng = torch.tensor([1234, 0], device=dev)
     start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
