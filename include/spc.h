@@ -560,12 +560,13 @@ SPC_API spc_status spc_group_norm_bwd(const void* dy, const void* x, const float
                                       int32_t* status, void* ws, size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------ dropout
- * spc_dropout_fwd -- y[i] = residual[i] + (keep(i) ? x[i] / (1 - p) : 0), one
- * rounding to dt.  The mask is a function of the element's index and is never
- * stored: word i % 4 of the block (i / 4) of the counter-based generator
- * Philox4x32-10 (Salmon, Moraes, Dror, Shaw: "Parallel random numbers: as easy as
- * 1, 2, 3", SC 2011) with key = rng[0] and counter = (i / 4, rng[1]), low words
- * first; element i is kept when its word >= round(p 2^32).
+ * spc_dropout_fwd -- y[i] = residual[i] + (keep(i) ? x[i] / (1 - p) : 0): the product
+ * with 1 / (1 - p) and the sum are rounded to fp32, then once to dt.  The mask is a
+ * function of the element's index and is never stored: word i % 4 of the block
+ * (i / 4) of the counter-based generator Philox4x32-10 (Salmon, Moraes, Dror, Shaw:
+ * "Parallel random numbers: as easy as 1, 2, 3", SC 2011) with key = rng[0] and
+ * counter = (i / 4, rng[1]), low words first; element i is kept when its
+ * word >= round(p 2^32).
  *
  *  rng       [2] uint64 on the DEVICE: seed and offset.  A graph that holds the call draws
  *            a new mask at every replay in which the caller advanced the offset.

@@ -6,6 +6,9 @@
 // Feistel exchange of their halves, and two round keys that advance by the
 // published constants.  Four elements share one block, so a thread owns whole
 // groups of four.
+//
+// The product with 1 / (1 - p) and the sum with the residual are each rounded to fp32, in every form
+// of the kernel, so that an element's bits do not depend on which side of a 16-byte boundary it stands.
 #include <math.h>
 
 #include "layers.cuh"
@@ -97,7 +100,9 @@ k_dropout(const T* x, const T* residual, int64_t n, Rule k, const uint64_t* rng,
                 F2 e = f[2 * h + j];
                 e.x = ANY && w.w[2 * j] <= k.last ? 0.f : e.x;
                 e.y = ANY && w.w[2 * j + 1] <= k.last ? 0.f : e.y;
-                f[2 * h + j] = RESIDUAL ? fma(e, both(k.scale), g[2 * h + j]) : mul(e, both(k.scale));
+                // the products one by one: a product of pairs and a sum of pairs would be made one instruction
+                e = F2{__fmul_rn(e.x, k.scale), __fmul_rn(e.y, k.scale)};
+                f[2 * h + j] = RESIDUAL ? add(e, g[2 * h + j]) : e;
             }
         }
         reinterpret_cast<P*>(y)[i] = pack<T, E>(f);
@@ -109,9 +114,8 @@ k_dropout(const T* x, const T* residual, int64_t n, Rule k, const uint64_t* rng,
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             if (t + j < n) {
-                float f = ANY && w.w[j] <= k.last ? 0.f : elem<T>::to_f32(x[t + j]) * k.scale;
-                if (RESIDUAL) f += elem<T>::to_f32(residual[t + j]);
-                y[t + j] = elem<T>::from_f32(f);
+                const float f = ANY && w.w[j] <= k.last ? 0.f : __fmul_rn(elem<T>::to_f32(x[t + j]), k.scale);
+                y[t + j] = elem<T>::from_f32(RESIDUAL ? __fadd_rn(f, elem<T>::to_f32(residual[t + j])) : f);
             }
     }
 }
@@ -130,9 +134,8 @@ k_dropout_unaligned(const T* x, const T* residual, int64_t n, Rule k, const uint
     for (int j = 0; j < 4; ++j) {
         const int64_t i = q * 4 + j;
         if (i >= n) break;
-        float f = ANY && w.w[j] <= k.last ? 0.f : elem<T>::to_f32(x[i]) * k.scale;
-        if (residual) f += elem<T>::to_f32(residual[i]);
-        y[i] = elem<T>::from_f32(f);
+        const float f = ANY && w.w[j] <= k.last ? 0.f : __fmul_rn(elem<T>::to_f32(x[i]), k.scale);
+        y[i] = elem<T>::from_f32(residual ? __fadd_rn(f, elem<T>::to_f32(residual[i])) : f);
     }
 }
 

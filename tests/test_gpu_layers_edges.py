@@ -1,0 +1,56 @@
+"""The layers between convolutions where a kernel changes its way: the last bit of dropout at either
+alignment, parts of a segment that one row fills, the tiles of CTA pairs and of long rows, empty lists,
+keys and row lists of wider types, views off a 16-byte boundary, very long rows.
+
+Bounds are those of test_gpu_layers.py where nothing else is said."""
+
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import layers_ref as ref
+import sparse_convolution_hash_gb300 as spc
+from gpu_util import DT, dev
+from sparse_convolution_hash_gb300 import binding
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    import __graft_entry__
+
+    __graft_entry__.build()
+
+
+def to_dev(a):
+    if a is None:
+        return None
+    return (torch.from_numpy(np.ascontiguousarray(a)) if isinstance(a, np.ndarray) else a).to(dev())
+
+
+def close(got, want, bound, what=""):
+    got = got.double().cpu()
+    bad = ~((got - want).abs() <= bound)
+    assert not bad.any(), f"{what}: {int(bad.sum())} elements off, worst {((got - want).abs() - bound).max():.3g}"
+
+
+# --------------------------------------------------------------------- dropout
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("n,skip", [(40003, 0), (40003, 1)])
+def test_dropout_is_a_product_and_a_sum_in_fp32(n, skip, dtype, residual):
+    """Every element has the bits of x s in fp32, s = 1 / (1 - p) in fp32, plus the residual in fp32,
+    rounded to the type: in whole vectors, in the last partial one and off a 16-byte boundary."""
+    g = np.random.default_rng(n + skip)
+    x = to_dev(torch.from_numpy(g.standard_normal(n + skip)).to(DT[dtype]))[skip:]
+    res = to_dev(torch.from_numpy(g.standard_normal(n + skip)).to(DT[dtype]))[skip:]
+    p, seed, offset = 0.1, 0x1234567890ABCDEF, 7
+    y = spc.spc_dropout_fwd(x, p, to_dev(torch.tensor([seed, offset])), residual=res if residual else None)
+    keep = torch.from_numpy(ref.dropout_words(seed, offset, 0, n) >= np.uint64(round(p * 2 ** 32)))
+    want = torch.where(keep, x.cpu().float() * torch.tensor(1 / (1 - p), dtype=torch.float32), torch.zeros(()))
+    if residual:
+        want = want + res.cpu().float()
+    assert torch.equal(y.cpu(), want.to(DT[dtype]))
