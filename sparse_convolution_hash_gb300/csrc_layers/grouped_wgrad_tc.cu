@@ -17,10 +17,8 @@
 // rows by cp.async, warp 1 issues the MMAs into one of two accumulators and
 // first clears the rows of a last, partial unit past the segment's end (they hold the
 // next segment's rows: a zero weight would not do, as 0 x NaN is NaN).
-// Wide tiles are bound by what comes from L2 (one CTA's 128 x 256 x 64 unit: 48 KB), so two CTAs
-// that hold the same output channels make a pair: each loads half of dy's columns into
-// both (TMA multicast) and a stage is free when both have used it; all else is the CTA's own.
-// Every wait is bounded (SPC_ERR_TIMEOUT).
+// Wide tiles are bound by what comes from L2 (a 128 x 256 x 64 unit: 48 KB).  Every wait is bounded
+// (SPC_ERR_TIMEOUT).
 #include "kernels.cuh"
 #include "layers.cuh"
 #include "tc2.cuh"
@@ -323,7 +321,7 @@ __device__ __forceinline__ Join join_of(const Walk& walk, int c)
     return j;
 }
 
-template <typename T, int BN, bool GATHER, bool PAIR>
+template <typename T, int BN, bool GATHER>
 __global__ void __launch_bounds__(GATHER ? kThreads + kGatherThreads : kThreads, 1)
 k_grouped_wgrad_tc(GroupedWgradArgs a, float* __restrict__ part, Join* __restrict__ joins, uint64_t wait_ns,
                    const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_dy)
@@ -341,14 +339,12 @@ k_grouped_wgrad_tc(GroupedWgradArgs a, float* __restrict__ part, Join* __restric
     int32_t* s_list = s_start + a.segments + 1;
     __shared__ Plan plan;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    constexpr int kWide = PAIR ? 2 * kTileM : kTileM;  // input channels of a planned tile
-    constexpr int kCtas = PAIR ? 2 : 1;
-    const int rank = PAIR ? (int)ptx::cluster_rank() : 0, me = (int)blockIdx.x / kCtas;
+    const int me = (int)blockIdx.x;
 
     if (tid == 0) {
         for (int s = 0; s < S::kStages; ++s) {
             ptx::mbar_init(&full[s], GATHER ? kGatherThreads : 1);
-            ptx::mbar_init(&empty[s], kCtas);
+            ptx::mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
             ptx::mbar_init(&acc_full[b], 1);
@@ -361,14 +357,13 @@ k_grouped_wgrad_tc(GroupedWgradArgs a, float* __restrict__ part, Join* __restric
         }
     }
     if (warp == 1) ptx::tmem_alloc_cg<1>(s_ctrl, S::kTmemCols);
-    const int cols = (a.cout + BN - 1) / BN, tiles = (a.cin + kWide - 1) / kWide * cols;
+    const int cols = (a.cout + BN - 1) / BN, tiles = (a.cin + kTileM - 1) / kTileM * cols;
     wait_for_kernel_before();
     if (warp == 0)
-        make_plan(a.seg, a.segments, a.m, tiles, gridDim.x / kCtas, s_start, s_list, s_list + a.segments, &plan,
+        make_plan(a.seg, a.segments, a.m, tiles, gridDim.x, s_start, s_list, s_list + a.segments, &plan,
                   blockIdx.x == 0 ? a.status : nullptr, lane);
     ptx::tc_fence_before();
-    if constexpr (PAIR) ptx::cluster_sync();
-    else __syncthreads();
+    __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = s_ctrl[0];
     Walk walk{s_start, s_list, a.seg, &plan, a.m, a.segments, tiles, 0, 0, 0, 0, 0};
@@ -387,7 +382,7 @@ k_grouped_wgrad_tc(GroupedWgradArgs a, float* __restrict__ part, Join* __restric
             while (walk.more() && ok) {
                 const Piece p = walk.next();
                 if (p.lo == p.hi) continue;
-                const int c0 = p.tile / cols * kWide + rank * kTileM, n0 = p.tile % cols * BN;
+                const int c0 = p.tile / cols * kTileM, n0 = p.tile % cols * BN;
                 for (int k = p.k0; k < p.k1; ++k, ++it) {
                     const int s = it % S::kStages;
                     if (it >= S::kStages) ok = ptx::mbar_wait(&empty[s], ((it / S::kStages) - 1) & 1, wait_ns);
@@ -398,11 +393,8 @@ k_grouped_wgrad_tc(GroupedWgradArgs a, float* __restrict__ part, Join* __restric
 #pragma unroll
                     for (int j = 0; j < kTileM / 64; ++j) ptx::tma_load2d<1>(base + j * kAtom, &map_x, c0 + 64 * j, row, bar);
 #pragma unroll
-                    for (int j = 0; j < BN / 64; ++j) {
-                        const uint32_t to = base + S::kABytes + j * kAtom;
-                        if constexpr (!PAIR) ptx::tma_load2d<1>(to, &map_dy, n0 + 64 * j, row, bar);
-                        else if (j / (BN / 128) == rank) ptx::tma_load2d_both(to, &map_dy, n0 + 64 * j, row, bar);
-                    }
+                    for (int j = 0; j < BN / 64; ++j)
+                        ptx::tma_load2d<1>(base + S::kABytes + j * kAtom, &map_dy, n0 + 64 * j, row, bar);
                 }
             }
             if (!ok) set_status(a.status, SPC_ERR_TIMEOUT);
@@ -445,8 +437,7 @@ k_grouped_wgrad_tc(GroupedWgradArgs a, float* __restrict__ part, Join* __restric
                         for (int q = 0; q < kUnit / 16; ++q)
                             ptx::mma_f16<1>(d, ad + (uint64_t)(q * (2048 >> 4)), bd + (uint64_t)(q * (2048 >> 4)), idesc,
                                             k != k0 || q != 0);
-                        if constexpr (PAIR) ptx::mma_commit_both(&empty[s]);
-                        else ptx::mma_commit(&empty[s]);
+                        ptx::mma_commit(&empty[s]);
                     }
                     __syncwarp();
                 }
@@ -468,7 +459,7 @@ k_grouped_wgrad_tc(GroupedWgradArgs a, float* __restrict__ part, Join* __restric
             while (walk.more() && ok) {
                 const Piece p = walk.next();
                 if (p.lo == p.hi) continue;
-                const int c0 = p.tile / cols * kWide + rank * kTileM + piece * 8;
+                const int c0 = p.tile / cols * kTileM + piece * 8;
                 const int n0 = p.tile % cols * BN + piece * 8;
                 // the list entries of thread e's two reduction indices of unit k, read one
                 // unit ahead and checked when they are used
@@ -551,7 +542,7 @@ k_grouped_wgrad_tc(GroupedWgradArgs a, float* __restrict__ part, Join* __restric
                 if (lane == 0) ptx::mbar_arrive(&acc_empty[b]);
             }
             if (!ok) break;
-            const int c0 = p.tile / cols * kWide + rank * kTileM + quarter * 32;
+            const int c0 = p.tile / cols * kTileM + quarter * 32;
             const int n0 = p.tile % cols * BN + half * S::kWarpCols;
             // a whole tile goes to dW, a part to this CTA's first or last slot
             float* dst;
@@ -563,8 +554,7 @@ k_grouped_wgrad_tc(GroupedWgradArgs a, float* __restrict__ part, Join* __restric
                 rows = a.cin - c0;
                 width = a.cout - n0;
             } else {
-                dst = part + ((int64_t)plan.id[me] * 2 + p.slot) * (kWide * BN) +
-                      (rank * kTileM + quarter * 32) * BN + half * S::kWarpCols;
+                dst = part + ((int64_t)plan.id[me] * 2 + p.slot) * (kTileM * BN) + quarter * 32 * BN + half * S::kWarpCols;
                 pitch = BN;
                 rows = 32;
                 width = S::kWarpCols;
@@ -591,8 +581,7 @@ k_grouped_wgrad_tc(GroupedWgradArgs a, float* __restrict__ part, Join* __restric
     }
     __syncwarp();
     ptx::tc_fence_before();
-    if constexpr (PAIR) ptx::cluster_sync();
-    else __syncthreads();
+    __syncthreads();
     if (warp == 1) {
         ptx::tc_fence_after();
         ptx::tmem_dealloc_cg<1>(tmem, S::kTmemCols);
@@ -601,7 +590,7 @@ k_grouped_wgrad_tc(GroupedWgradArgs a, float* __restrict__ part, Join* __restric
 
 // Block (c, q): rows kJoinRows q .. of the tile that share c's plan names become the sum
 // of its parts, in the order of the shares.
-template <int BN, int WIDE>
+template <int BN>
 __global__ void __launch_bounds__(kJoinRows * BN / 4)
 k_grouped_wgrad_join(GroupedWgradArgs a, const float* part, const Join* joins)
 {
@@ -611,9 +600,9 @@ k_grouped_wgrad_join(GroupedWgradArgs a, const float* part, const Join* joins)
     if (j.more == 0) return;
     const int cols = (a.cout + BN - 1) / BN;
     const int r = blockIdx.y * kJoinRows + threadIdx.x / (BN / 4), n = threadIdx.x % (BN / 4) * 4;
-    const int row = j.tile / cols * WIDE + r, col = j.tile % cols * BN + n;
+    const int row = j.tile / cols * kTileM + r, col = j.tile % cols * BN + n;
     if (row >= a.cin || col >= a.cout) return;
-    constexpr int64_t kSlot = WIDE * BN;
+    constexpr int64_t kSlot = kTileM * BN;
     const float* src = part + r * BN + n;
     float4 s = fetch(reinterpret_cast<const float4*>(src + ((int64_t)c * 2 + j.slot) * kSlot));
     src += (int64_t)(c + 1) * 2 * kSlot;
@@ -628,7 +617,7 @@ k_grouped_wgrad_join(GroupedWgradArgs a, const float* part, const Join* joins)
     *reinterpret_cast<float4*>(a.dw + ((int64_t)j.g * a.cin + row) * a.cout + col) = s;
 }
 
-int grouped_wgrad_ctas() { return std::min(sm_count(), kMaxParts) / 2 * 2; }
+int grouped_wgrad_ctas() { return std::min(sm_count(), kMaxParts); }
 
 // Two parts of a tile for each CTA, and the joins.
 size_t parts_bytes()
@@ -636,7 +625,7 @@ size_t parts_bytes()
     return align_up((sizeof(float) * 2 * kTileM * 256 + sizeof(Join)) * (size_t)grouped_wgrad_ctas(), 256);
 }
 
-template <typename T, int BN, bool GATHER, bool PAIR>
+template <typename T, int BN, bool GATHER>
 spc_status launch(const GroupedWgradArgs& a, float* part, cudaStream_t st)
 {
     using S = Shape<BN>;
@@ -644,29 +633,23 @@ spc_status launch(const GroupedWgradArgs& a, float* part, cudaStream_t st)
     if (!tmap_2d(&mx, Fmt<T>::t, 2, a.x, (uint64_t)a.cin, (uint64_t)a.n_x, 64, kUnit, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !tmap_2d(&my, Fmt<T>::t, 2, a.dy, (uint64_t)a.cout, (uint64_t)a.n_y, 64, kUnit, CU_TENSOR_MAP_SWIZZLE_128B))
         return SPC_ERR_CUDA;
-    const spc_status allowed = allow_smem<k_grouped_wgrad_tc<T, BN, GATHER, PAIR>>();
+    const spc_status allowed = allow_smem<k_grouped_wgrad_tc<T, BN, GATHER>>();
     if (allowed != SPC_OK) return allowed;
-    const int parts = PAIR ? grouped_wgrad_ctas() / 2 : grouped_wgrad_ctas();
-    Join* joins = reinterpret_cast<Join*>(part + (int64_t)grouped_wgrad_ctas() * 2 * kTileM * 256);
+    const int parts = grouped_wgrad_ctas();
+    Join* joins = reinterpret_cast<Join*>(part + (int64_t)parts * 2 * kTileM * 256);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(PAIR ? 2 * parts : parts));
+    cfg.gridDim = dim3((unsigned)parts);
     cfg.blockDim = dim3(GATHER ? kThreads + kGatherThreads : kThreads);
     cfg.dynamicSmemBytes = S::smem(a.segments);
     cfg.stream = st;
-    cudaLaunchAttribute attr[2] = {beside_the_kernel_before()};
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = 2;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[1] = {beside_the_kernel_before()};
     cfg.attrs = attr;
-    cfg.numAttrs = PAIR ? 2 : 1;
-    SPC_CUDA_TRY(cudaLaunchKernelEx(&cfg, k_grouped_wgrad_tc<T, BN, GATHER, PAIR>, a, part, joins, wait_limit_ns(), mx, my));
-    constexpr int kWide = PAIR ? 2 * kTileM : kTileM;
-    cfg.gridDim = dim3((unsigned)parts, kWide / kJoinRows);
+    cfg.numAttrs = 1;
+    SPC_CUDA_TRY(cudaLaunchKernelEx(&cfg, k_grouped_wgrad_tc<T, BN, GATHER>, a, part, joins, wait_limit_ns(), mx, my));
+    cfg.gridDim = dim3((unsigned)parts, kTileM / kJoinRows);
     cfg.blockDim = dim3(kJoinRows * BN / 4);
     cfg.dynamicSmemBytes = 0;
-    cfg.numAttrs = 1;
-    SPC_CUDA_TRY(cudaLaunchKernelEx(&cfg, k_grouped_wgrad_join<BN, kWide>, a, (const float*)part, (const Join*)joins));
+    SPC_CUDA_TRY(cudaLaunchKernelEx(&cfg, k_grouped_wgrad_join<BN>, a, (const float*)part, (const Join*)joins));
     return SPC_OK;
 }
 
@@ -709,7 +692,7 @@ spc_status pick(GroupedWgradArgs a, float* part, cudaStream_t st)
 {
     // tiles are counted in 31 bits
     if (ceil_div(a.cin, 128) * ceil_div(a.cout, 128) * a.segments > INT32_MAX) return SPC_ERR_UNSUPPORTED;
-    if ((a.x_rows || a.y_rows) && !brings_rows(a.cin, a.cout)) return launch<T, 128, true, false>(a, part, st);
+    if ((a.x_rows || a.y_rows) && !brings_rows(a.cin, a.cout)) return launch<T, 128, true>(a, part, st);
     if (a.x_rows || a.y_rows) {
         uint8_t* x = reinterpret_cast<uint8_t*>(part) + parts_bytes();
         uint8_t* dy = x + align_up((size_t)a.m * a.cin * 2, 256);
@@ -727,8 +710,7 @@ spc_status pick(GroupedWgradArgs a, float* part, cudaStream_t st)
         }
         a.x_rows = a.y_rows = nullptr;
     }
-    if (a.cout <= 128) return launch<T, 128, false, false>(a, part, st);
-    return a.cin > kTileM ? launch<T, 256, false, true>(a, part, st) : launch<T, 256, false, false>(a, part, st);
+    return a.cout <= 128 ? launch<T, 128, false>(a, part, st) : launch<T, 256, false>(a, part, st);
 }
 
 }  // namespace

@@ -51,14 +51,6 @@ __device__ __forceinline__ void tma_load2d(uint32_t dst, const void* tmap, int32
                      : "memory");
 }
 
-// The same box into every CTA of a pair, at the same offset, completing on each one's barrier.
-__device__ __forceinline__ void tma_load2d_both(uint32_t dst, const void* tmap, int32_t x, int32_t y, uint32_t bar)
-{
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster"
-                 " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst), "l"(tmap), "r"(x), "r"(y), "r"(bar), "h"((uint16_t)3)
-                 : "memory");
-}
-
 template <int CG>
 __device__ __forceinline__ void tma_load3d(uint32_t dst, const void* tmap, int32_t x, int32_t y, int32_t z,
                                            uint32_t bar)
@@ -123,14 +115,6 @@ __device__ __forceinline__ void mma_commit_cg(uint64_t* bar)
         asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
                      " [%0], %1;" ::"r"(smem_u32(bar)), "h"((uint16_t)3)
                      : "memory");
-}
-
-// One CTA's MMAs, reported to both CTAs of a pair.
-__device__ __forceinline__ void mma_commit_both(uint64_t* bar)
-{
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-                 " [%0], %1;" ::"r"(smem_u32(bar)), "h"((uint16_t)3)
-                 : "memory");
 }
 
 }  // namespace ptx
