@@ -54,3 +54,29 @@ def test_dropout_is_a_product_and_a_sum_in_fp32(n, skip, dtype, residual):
     if residual:
         want = want + res.cpu().float()
     assert torch.equal(y.cpu(), want.to(DT[dtype]))
+
+
+# ------------------------------------------------------------------ group norm
+def share_rows(n):
+    """Positions that one CTA of the group norm owns: one CTA for each SM, 64 positions at least."""
+    shares = max(1, min(torch.cuda.get_device_properties(dev()).multi_processor_count, -(-n // 64)))
+    return -(-n // shares)
+
+
+@pytest.mark.parametrize("first", [0.0, 1100.0])
+@pytest.mark.parametrize("n", [40000, 498145])
+def test_group_norm_segment_that_starts_on_a_last_position(n, first):
+    """The first part of the second segment is one row, far from the others at 1000 +- 1: the parts
+    join without losing the variance's digits."""
+    g = np.random.default_rng(0)
+    x = torch.from_numpy(1000 + g.standard_normal((n, 16))).float()
+    cut = share_rows(n) - 1
+    x[cut] = first
+    seg = np.array([0, cut, n], np.int32)
+    y_r, mean_r, rstd_r, _ = ref.norm_fwd(x, None, None, seg, None, 4, 1e-5, "none")
+    y, mean, rstd = spc.spc_group_norm_fwd(to_dev(x), None, None, to_dev(seg), 4)
+    # as for one segment with such a first row: the values' distances from the mean are exact to
+    # 1000 e / spread and 1e-4 covers that and the sums around pivots
+    assert float((rstd.double().cpu() / rstd_r - 1).abs().max()) < 1e-4
+    assert float((mean.double().cpu() / mean_r - 1).abs().max()) < 1e-6
+    assert float((y.double().cpu() - y_r).norm() / y_r.norm()) < 1e-3
