@@ -3,7 +3,10 @@ the arithmetic of their kernels that runs as plain host code."""
 
 import glob
 import os
+import shutil
+import subprocess
 
+import numpy as np
 import pytest
 
 from sparse_convolution_hash_gb300 import build as libbuild
@@ -19,3 +22,62 @@ def test_no_load_fills_several_ctas():
             text = fh.read()
         for piece in text.split("cp.async.bulk")[1:]:
             assert "multi" + "cast" not in piece.split('"')[0], f
+
+
+# ------------------------------------------- the plan of the gradient by the weights
+@pytest.fixture(scope="module")
+def plan_check(tmp_path_factory):
+    """tests/wgrad_plan_check.cpp, built with the host compiler: lines of cases to lines of findings."""
+    cxx = shutil.which("g++")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(libbuild.nvcc())), "include")
+    if cxx is None or not os.path.exists(os.path.join(cuda, "cuda_runtime.h")):
+        pytest.skip("needs g++ and the CUDA headers")
+    exe = str(tmp_path_factory.mktemp("plan") / "wgrad_plan_check")
+    subprocess.run([cxx, "-std=c++20", "-O2", "-pthread", "-I", cuda, "-I", libbuild.INCLUDE, "-I", libbuild.CSRC,
+                    "-I", libbuild.CSRC_LAYERS, os.path.join(os.path.dirname(__file__), "wgrad_plan_check.cpp"),
+                    "-o", exe], check=True)
+
+    def run(cases):
+        text = "".join(f"{len(seg) - 1} {m} {tiles} {parts} {' '.join(map(str, seg))}\n" for m, tiles, parts, seg in cases)
+        out = subprocess.run([exe], input=text, capture_output=True, text=True, timeout=300, check=True).stdout
+        return out.split("\n")[:-1]
+
+    return run
+
+
+def offsets(units):
+    return [64 * sum(units[:i]) for i in range(len(units) + 1)]
+
+
+# Tiles of a segment, CTAs, and 64-row units of each segment whose whole tiles fill the CTAs to levels that
+# differ by orders of magnitude.
+STEEP = [
+    (94, 152, [1688, 57, 46711, 291, 2112, 2, 181, 489, 91, 449, 5, 1, 1053, 729, 6, 1296, 20691, 6238, 13, 1137,
+      6, 134, 381, 391, 98835, 47, 1816, 2181, 52, 41006, 1, 1774, 268, 1, 19, 366, 130, 170, 4161, 21, 175542, 3,
+      6525, 1555, 21, 29, 22, 4794, 26588, 2840, 428, 574, 2, 11, 2]),
+    (105, 100, [113, 133690, 3, 17301, 12, 75, 2, 2518, 173, 23, 11346, 6, 1702, 136892, 4842930, 48720, 499, 10,
+      6, 38, 249, 348, 1, 223, 497, 633, 3237, 253, 3, 16, 16, 146187, 3710, 601, 1194, 47, 256, 1, 140, 24, 52,
+      54043, 3173, 6185, 415, 43930, 19307, 1631, 5, 63, 1732, 1260098, 16863, 32, 65136, 243, 109, 2, 3, 2, 1]),
+]
+
+
+@pytest.mark.parametrize("tiles,parts,units", STEEP)
+def test_weight_gradient_plan_of_steep_segments(plan_check, tiles, parts, units):
+    seg = offsets(units)
+    assert [f.split(" ")[0] for f in plan_check([(seg[-1], tiles, parts, seg)])] == ["ok"]
+
+
+def test_weight_gradient_plan_of_many_splits(plan_check):
+    """Rows of every skew, with and without cut tiles, one CTA and more than there are tiles."""
+    g = np.random.default_rng(0)
+    cases = []
+    for i in range(120):
+        segments = int(g.integers(1, 200)) if i % 6 else 1024
+        m, tiles = int(np.exp(g.uniform(0, 16))), int(np.exp(g.uniform(0, 4)))
+        w = np.exp(g.uniform(0, 4) * g.standard_normal(segments))
+        seg = np.concatenate([[0], np.cumsum(g.multinomial(m, w / w.sum()))]) + int(g.integers(0, 100))
+        cases.append((m + 150, tiles, int(g.choice([1, 2, 16, 76, 152, 152, 192])), seg.tolist()))
+    found = plan_check(cases)
+    assert len(found) == len(cases)
+    assert [f for f in found if not f.startswith("ok")] == []
+    assert sum(f != "ok (0, 0)" for f in found) > 20  # tiles were cut
