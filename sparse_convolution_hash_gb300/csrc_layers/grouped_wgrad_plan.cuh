@@ -31,6 +31,7 @@ struct Piece {
 // read again, as much as 20 units or so (4,096 rows of 8 segments, 512 x 2048: 25 us
 // against 33).
 struct Plan {
+    int64_t m;                   // positions, 0 where the offsets cannot be used
     int64_t whole;               // tiles that stay whole
     int32_t longest;             // units of the longest tile
     int32_t parts;               // CTAs
@@ -44,7 +45,6 @@ struct Walk {
     const int32_t* list;   // segment j of the list
     const int32_t* seg;
     const Plan* plan;
-    int64_t m;
     int32_t segments, tiles;  // tiles of one segment
     int32_t wave, c;
     int64_t u, begin, end;
@@ -54,7 +54,7 @@ struct Walk {
         p.g = list[j];
         p.tile = tile;
         p.units = start[j + 1] - start[j];
-        segment_bounds(seg, p.g, m, nullptr, p.lo, p.hi);
+        segment_bounds(seg, p.g, plan->m, nullptr, p.lo, p.hi);
     }
     __device__ __forceinline__ void reset(int32_t cta)
     {
@@ -225,9 +225,19 @@ __device__ __forceinline__ void make_plan(const int32_t* seg, int segments, int6
         all += units;
         longest = longest > units ? longest : units;
     }
-    const int64_t total = warp_add(all) * tiles, even = total / parts;
+    all = warp_add(all);
     longest = __reduce_max_sync(FULL_MASK, longest);
     __syncwarp();
+    if (all > INT32_MAX) {
+        // only offsets out of order, which were reported, name that many: each segment is taken as empty, as
+        // the sums of units below have 31 bits
+        for (int g = lane; g < segments; g += 32) s_units[g] = 1;
+        all = segments;
+        longest = 1;
+        m = 0;
+        __syncwarp();
+    }
+    const int64_t total = all * tiles, even = total / parts;
     int32_t listed = 0, shorter = 0, carry = 0;
     for (int pass = 0; pass < 2; ++pass)
         for (int g0 = 0; g0 < segments; g0 += 32) {
@@ -248,6 +258,7 @@ __device__ __forceinline__ void make_plan(const int32_t* seg, int segments, int6
     if (lane == 0) {
         s_start[segments] = carry;
         plan->longest = longest;
+        plan->m = m;
     }
     __syncwarp();
     share_out(plan, s_start, segments, tiles, parts, shorter, total, lane);

@@ -102,7 +102,7 @@ k_grouped_wgrad_tc(GroupedWgradArgs a, float* __restrict__ part, Join* __restric
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = s_ctrl[0];
-    Walk walk{s_start, s_list, a.seg, &plan, a.m, a.segments, tiles, 0, 0, 0, 0, 0};
+    Walk walk{s_start, s_list, a.seg, &plan, a.segments, tiles, 0, 0, 0, 0, 0};
     walk.reset(me);
     bool ok = true;
     if (blockIdx.x == 0 && tid < plan.parts) write_join(walk, tid, joins);

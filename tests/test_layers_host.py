@@ -81,3 +81,12 @@ def test_weight_gradient_plan_of_many_splits(plan_check):
     assert len(found) == len(cases)
     assert [f for f in found if not f.startswith("ok")] == []
     assert sum(f != "ok (0, 0)" for f in found) > 20  # tiles were cut
+
+
+@pytest.mark.parametrize("segments,m,tiles", [(1024, 2 ** 31 - 2, 1), (1024, 300000000, 3), (200, 2 ** 31 - 2, 1),
+                                              (1024, 2 ** 28 + 999, 2), (1024, 100000, 5)])
+def test_weight_gradient_plan_of_offsets_out_of_order(plan_check, segments, m, tiles):
+    """Offsets that go back and forth name every row hundreds of times: reported, and no piece or join
+    leaves the tensors however many units that is."""
+    seg = [0 if i % 2 == 0 else m for i in range(segments + 1)]
+    assert plan_check([(m, tiles, 152, seg)])[0].startswith("ok") and plan_check([(m, tiles, 152, seg)])[0].endswith(", 10)")

@@ -96,7 +96,7 @@ static std::string check(int segments, int64_t m, int tiles, int parts, const st
         segment_bounds(seg.data(), g, m, nullptr, lo, hi);
         want[g] = hi > lo ? (hi - lo + kUnit - 1) / kUnit : 1;
     }
-    Walk walk{start.data(), list.data(), seg.data(), &plan, m, segments, tiles, 0, 0, 0, 0, 0};
+    Walk walk{start.data(), list.data(), seg.data(), &plan, segments, tiles, 0, 0, 0, 0, 0};
     std::map<int64_t, Span> cut;  // by place: number of the share, slot
     const int64_t most = (int64_t)segments * tiles + 2 * parts;
     for (int c = 0; c < parts; ++c) {
