@@ -326,7 +326,7 @@ template <int BN>
 __global__ void __launch_bounds__(kJoinRows * BN / 4)
 k_grouped_wgrad_join(GroupedWgradArgs a, const float* part, const Join* joins)
 {
-    wait_for_kernel_before();  // launched while the parts were still coming
+    wait_for_kernel_before();  // set up while the blocks that write the parts end
     const int c = blockIdx.x;
     const Join j = joins[c];
     if (j.more == 0) return;
@@ -406,7 +406,6 @@ k_bring_rows(const uint4* __restrict__ from, const int32_t* __restrict__ list, i
 
 spc_status bring(const void* from, const int32_t* list, int64_t rows, int64_t m, int32_t c, void* to, int32_t* status, cudaStream_t st)
 {
-    if (m == 0) return SPC_OK;
     k_bring_rows<<<(unsigned)ceil_div(m, kBringWarps), kBringWarps * 32, 0, st>>>(
         static_cast<const uint4*>(from), list, rows, m, c / 8, static_cast<uint4*>(to), status);
     SPC_LAUNCH_CHECK();
@@ -457,7 +456,8 @@ size_t grouped_wgrad_tc_ws_bytes(int64_t m, int32_t cin, int32_t cout, bool list
 
 bool grouped_wgrad_tc_supported(const GroupedWgradArgs& a, spc_dtype dt)
 {
-    return (dt == SPC_F16 || dt == SPC_BF16) && a.cin % 8 == 0 && a.cout % 8 == 0 && a.n_x > 0 && a.n_y > 0;
+    // an empty tensor has no tensor map
+    return (dt == SPC_F16 || dt == SPC_BF16) && a.cin % 8 == 0 && a.cout % 8 == 0 && a.m > 0 && a.n_x > 0 && a.n_y > 0;
 }
 
 spc_status grouped_wgrad_tc(const GroupedWgradArgs& a, spc_dtype dt, void* ws, cudaStream_t st)

@@ -80,3 +80,25 @@ def test_group_norm_segment_that_starts_on_a_last_position(n, first):
     assert float((rstd.double().cpu() / rstd_r - 1).abs().max()) < 1e-4
     assert float((mean.double().cpu() / mean_r - 1).abs().max()) < 1e-6
     assert float((y.double().cpu() - y_r).norm() / y_r.norm()) < 1e-3
+
+
+# ------------------------------------------------------------- grouped products
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("cin,cout", [(64, 64), (256, 256), (33, 40)])
+def test_grouped_weight_gradient_of_no_positions(cin, cout, dtype):
+    """m = 0 with row lists (which are not NULL) and operands that have rows: dW is zeros."""
+    d, L = dev(), binding.lib()
+    x, dy = torch.randn(7, cin, device=d).to(DT[dtype]), torch.randn(5, cout, device=d).to(DT[dtype])
+    rows = torch.zeros(8, dtype=torch.int32, device=d)
+    seg = torch.zeros(4, dtype=torch.int32, device=d)
+    dw = torch.full((3, cin, cout), 7.0, device=d)
+    dt = {"f32": 0, "f16": 1, "bf16": 2}[dtype]
+    need = L.spc_grouped_workspace_size(3, 0, cin, cout, dt, 1)
+    ws = torch.empty(max(need, 256), dtype=torch.uint8, device=d)
+    st = spc.new_status(d)
+    p = lambda t: ctypes.c_void_p(t.data_ptr())
+    code = L.spc_grouped_wgrad(p(x), p(dy), p(seg), p(rows), p(rows), 3, 7, 5, 0, cin, cout, dt, p(dw), p(st), p(ws),
+                               ws.numel(), ctypes.c_void_p(torch.cuda.current_stream(d).cuda_stream))
+    assert code == 0, binding.spc_status_string(code)
+    spc.check_status(st)
+    assert float(dw.abs().max()) == 0
