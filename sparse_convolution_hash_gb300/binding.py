@@ -543,12 +543,22 @@ def spc_conv_wgrad(x: torch.Tensor, dy: torch.Tensor, imap: Optional[torch.Tenso
 # The layers between convolutions.  Their calls can be shorter than a few microseconds on the
 # device, so what does not need a tensor operation here does not get one.
 
+def _int32(t: torch.Tensor, name: str) -> torch.Tensor:
+    """Whole numbers as int32.  One that 32 bits do not hold becomes the nearest that they do, which is out of
+    every range here as the number itself is (its low half might not be)."""
+    if t.is_floating_point() or t.is_complex():
+        raise ValueError(f"{name} must hold whole numbers, not {t.dtype}")
+    if t.dtype is torch.uint32 or t.dtype is torch.uint64:
+        t = t.to(torch.int64)  # from 2^63 on: below zero
+    return (t.clamp(-2 ** 31, 2 ** 31 - 1) if t.dtype is torch.int64 else t).to(torch.int32)
+
+
 def _typed(t: torch.Tensor, dtype, name: str) -> torch.Tensor:
     """A contiguous CUDA tensor of the given type."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype is not dtype:
-        t = t.to(dtype)
+        t = _int32(t, name) if dtype is torch.int32 else t.to(dtype)
     return t if t.is_contiguous() else t.contiguous()
 
 
@@ -596,7 +606,7 @@ def spc_row_segments(ids: torch.Tensor, segments: int, with_order: bool = True,
     if not ids.is_cuda:
         raise ValueError("ids must be a CUDA tensor")
     if ids.dtype is not torch.int32:
-        ids = ids.to(torch.int32)
+        ids = _int32(ids, "ids")
     n, dev = ids.shape[0], ids.device
     stride = ids.stride(0) if n > 1 else 1
     if stride < 1:

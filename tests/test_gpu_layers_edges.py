@@ -102,3 +102,44 @@ def test_grouped_weight_gradient_of_no_positions(cin, cout, dtype):
     assert code == 0, binding.spc_status_string(code)
     spc.check_status(st)
     assert float(dw.abs().max()) == 0
+
+
+# ----------------------------------------------- keys and row lists of other types
+def test_keys_and_lists_of_wider_types_keep_their_values():
+    """A key or row number that 32 bits do not hold is out of range, not its low half."""
+    d = dev()
+    wide = torch.tensor([2 ** 32, 1, -1, 2 ** 32 + 1, 0, 2 ** 31, 1 - 2 ** 32, -2 ** 63, 2 ** 63 - 1], device=d)
+    seg, order = spc.spc_row_segments(wide, 2)
+    assert seg.tolist() == [0, 1, 2] and order.tolist() == [4, 1, 0, 2, 3, 5, 6, 7, 8]
+    for dt in (torch.uint8, torch.int16, torch.int64, torch.uint32, torch.uint64):
+        seg, order = spc.spc_row_segments(torch.tensor([1, 0, 2, 1], device=d).to(dt), 2)
+        assert seg.tolist() == [0, 1, 3] and order.tolist() == [1, 0, 3, 2]
+    high = torch.tensor([1, -2], device=d).view(torch.uint64)  # 2^64 - 2
+    assert spc.spc_row_segments(high, 2)[0].tolist() == [0, 0, 1]
+    x = torch.randn(6, 16, device=d)
+    w = torch.randn(1, 16, 8, device=d)
+    seg = torch.tensor([0, 6], device=d)  # offsets of 64 bits are read as they are
+    rows = torch.arange(6, device=d)
+    want = spc.spc_grouped_fwd(x, w, seg)
+    assert torch.equal(spc.spc_grouped_fwd(x, w, seg, x_rows=rows, y_rows=rows), want)
+    rows[3] = 2 ** 32 + 3
+    for f in (lambda st: spc.spc_grouped_fwd(x, w, seg, x_rows=rows, status=st),
+              lambda st: spc.spc_grouped_wgrad(x, want, seg, y_rows=rows, status=st),
+              lambda st: spc.spc_group_norm_fwd(x, None, None, seg, 4, order=rows, status=st),
+              lambda st: spc.spc_grouped_fwd(x, w, torch.tensor([0, 2 ** 32 + 6], device=d), status=st)):
+        st = spc.new_status(d)
+        f(st)
+        assert int(st) == 10
+
+
+def test_keys_and_lists_are_whole_numbers():
+    d = dev()
+    x = torch.randn(6, 16, device=d)
+    w = torch.randn(1, 16, 8, device=d)
+    seg = torch.tensor([0, 6], dtype=torch.int32, device=d)
+    for f in (lambda: spc.spc_row_segments(torch.tensor([0.5, 1.0], device=d), 2),
+              lambda: spc.spc_grouped_fwd(x, w, seg.float()),
+              lambda: spc.spc_grouped_fwd(x, w, seg, x_rows=torch.zeros(6, device=d)),
+              lambda: spc.spc_group_norm_fwd(x, None, None, seg, 4, order=torch.zeros(6, device=d))):
+        with pytest.raises(ValueError):
+            f()
