@@ -605,7 +605,9 @@ SPC_API spc_status spc_dropout_bwd(const void* dy, int64_t n, double p, const ui
  *  ws     spc_grouped_workspace_size(...) bytes, 256-byte aligned, for spc_grouped_wgrad
  *         (0 where it needs none; listed: a row list is given, whose rows it may bring
  *         into order there first); the other two use none.
- *  x, dy, w and the result must be 16-byte aligned.  Results are run-to-run
+ *  x, dy, w and the result start on a 16-byte boundary where the tensor cores take the
+ *  product, else on one of four elements where cin and cout are multiples of 4, else on
+ *  an element's: slices of the first axis always do.  Results are run-to-run
  *  bit-identical.
  *  Kernels: tcgen05 tensor cores for fp16 / bf16 with cin and cout multiples of 8,
  *  else a tiled CUDA-core kernel (fp32 in full fp32 multiplies).

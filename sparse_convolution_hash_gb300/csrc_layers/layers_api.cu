@@ -49,6 +49,15 @@ spc_status check_dropout(const void* x, int64_t n, double p, const uint64_t* rng
     return SPC_OK;
 }
 
+// The boundary that a grouped product's tensors start on: what its kernel moves at once.  Tensor cores: 16
+// bytes; CUDA cores: four elements where every row is a multiple of that, else one.
+size_t grouped_boundary(int32_t cin, int32_t cout, spc_dtype dt)
+{
+    const size_t e = dt == SPC_F32 ? 4 : 2;
+    if (dt != SPC_F32 && cin % 8 == 0 && cout % 8 == 0) return 16;
+    return cin % 4 == 0 && cout % 4 == 0 ? 4 * e : e;
+}
+
 // What the three grouped products ask of their arguments; `rows` of each operand
 // must reach m when its row list is absent.
 spc_status check_grouped(const void* a, const void* b, const void* out, const int32_t* seg,
@@ -60,7 +69,8 @@ spc_status check_grouped(const void* a, const void* b, const void* out, const in
         return SPC_ERR_INVALID_ARG;
     if (!seg || !aligned4(seg) || !aligned4(a_rows) || !aligned4(b_rows)) return SPC_ERR_INVALID_ARG;
     if ((!a_rows && n_a < m) || (!b_rows && n_b < m)) return SPC_ERR_INVALID_ARG;
-    if (!aligned16(a) || !aligned16(b) || !aligned16(out)) return SPC_ERR_INVALID_ARG;
+    const uintptr_t low = reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b) | reinterpret_cast<uintptr_t>(out);
+    if (low % grouped_boundary(cin, cout, dt) != 0) return SPC_ERR_INVALID_ARG;
     if (m > INT32_MAX - 1 || n_a > INT32_MAX - 1 || n_b > INT32_MAX - 1) return SPC_ERR_UNSUPPORTED;
     return SPC_OK;
 }
@@ -200,7 +210,7 @@ spc_status spc_grouped_wgrad(const void* x, const void* dy, const int32_t* seg,
 {
     const spc_status s = check_grouped(x, dy, dw, seg, x_rows, y_rows, segments, n_x, n_y, m, cin, cout, dt);
     if (s != SPC_OK) return s;
-    if (!dw || (n_x > 0 && !x) || (n_y > 0 && !dy)) return SPC_ERR_INVALID_ARG;
+    if (!dw || !aligned4(dw) || (n_x > 0 && !x) || (n_y > 0 && !dy)) return SPC_ERR_INVALID_ARG;
     const size_t need = spc_grouped_workspace_size(segments, m, cin, cout, dt, x_rows || y_rows);
     if (need && (!ws || !aligned256(ws) || ws_bytes < need)) return SPC_ERR_WORKSPACE;
     const GroupedWgradArgs a{x, dy, seg, x_rows, y_rows, dw, status, n_x, n_y, m, segments, cin, cout};

@@ -143,3 +143,22 @@ def test_keys_and_lists_are_whole_numbers():
               lambda: spc.spc_group_norm_fwd(x, None, None, seg, 4, order=torch.zeros(6, device=d))):
         with pytest.raises(ValueError):
             f()
+
+
+# ------------------------------------------------ views off a 16-byte boundary
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("cin,cout", [(33, 65), (36, 20), (33, 8), (8, 33)])
+def test_grouped_products_of_rows_that_start_anywhere(cin, cout, dtype):
+    """Slices of the first axis start on their rows' own boundary: odd rows on an element's, rows of a
+    multiple of four on four elements'.  The products are those of aligned copies."""
+    g = torch.Generator().manual_seed(cin + cout)
+    mk = lambda *s: torch.randn(*s, generator=g).to(DT[dtype]).to(dev())[1:]
+    x, dy, w = mk(301, cin), mk(301, cout), mk(4, cin, cout)
+    seg = to_dev(np.array([0, 100, 100, 290], np.int32))
+    y = torch.empty(301, cout, device=dev(), dtype=DT[dtype])[1:]
+    dx = torch.empty(301, cin, device=dev(), dtype=DT[dtype])[1:]
+    dw = torch.empty(4, cin, cout, device=dev())[1:]
+    c = lambda t: t.clone()
+    assert torch.equal(spc.spc_grouped_fwd(x, w, seg, out=y), spc.spc_grouped_fwd(c(x), c(w), seg))
+    assert torch.equal(spc.spc_grouped_dgrad(dy, w, seg, out=dx), spc.spc_grouped_dgrad(c(dy), c(w), seg))
+    assert torch.equal(spc.spc_grouped_wgrad(x, dy, seg, out=dw), spc.spc_grouped_wgrad(c(x), c(dy), seg))

@@ -1,6 +1,7 @@
 """The layers between convolutions, checked on the CPU: what their sources may hold, and
 the arithmetic of their kernels that runs as plain host code."""
 
+import ctypes
 import glob
 import os
 import shutil
@@ -9,6 +10,7 @@ import subprocess
 import numpy as np
 import pytest
 
+from sparse_convolution_hash_gb300 import binding
 from sparse_convolution_hash_gb300 import build as libbuild
 
 
@@ -90,3 +92,23 @@ def test_weight_gradient_plan_of_offsets_out_of_order(plan_check, segments, m, t
     leaves the tensors however many units that is."""
     seg = [0 if i % 2 == 0 else m for i in range(segments + 1)]
     assert plan_check([(m, tiles, 152, seg)])[0].startswith("ok") and plan_check([(m, tiles, 152, seg)])[0].endswith(", 10)")
+
+
+# ----------------------------------------------------------------- refusals
+def test_grouped_products_refuse_tensors_off_their_boundary():
+    """16 bytes on tensor cores, four elements where rows are a multiple of four, else an element."""
+    libbuild.build()
+    L, P = binding.lib(), ctypes.c_void_p
+
+    def codes(shift, c, dt):
+        for at in range(3):
+            p = [P(256), P(256), P(256)]
+            p[at] = P(256 + shift)
+            for f in (L.spc_grouped_fwd, L.spc_grouped_dgrad):
+                yield f(p[0], p[1], P(256), None, None, 2, 4, 4, c, c, dt, p[2], None, None, 0, None)
+            yield L.spc_grouped_wgrad(p[0], p[1], P(256), None, None, 2, 4, 4, 4, c, c, dt, p[2], None, P(256), 1 << 40, None)
+
+    f32, f16, bf16 = 0, 1, 2
+    for shift, c, dt in ((8, 8, f16), (8, 64, bf16), (4, 8, f32), (8, 4, f32), (4, 4, f16), (2, 12, bf16), (2, 33, f32),
+                         (1, 33, f16), (3, 5, bf16)):
+        assert set(codes(shift, c, dt)) == {1}, (shift, c, dt)
