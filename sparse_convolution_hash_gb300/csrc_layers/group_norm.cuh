@@ -1058,15 +1058,16 @@ __global__ void __launch_bounds__(kBlock) k_norm_stats_wide(NormArgs a)
         const int64_t row = row_at(a.order, lo + e / per, a.n, a.status);
         return row < 0 ? 0.f : elem<T>::to_f32(x[row * a.c + g * per + e % per]);
     };
-    float v = 0.f;
-    for (int64_t e = threadIdx.x; e < total; e += kBlock) v += at(e);
-    const float mean = block_sum(v) / count;
-    v = 0.f;
+    // a thread's sums are long (a 256th of the group): around the group's first value, carrying their rounding
+    const float pivot = total > 0 ? at(0) : 0.f;
+    Exact sum, squares;
+    for (int64_t e = threadIdx.x; e < total; e += kBlock) sum.add(at(e) - pivot);
+    const float mean = pivot + block_sum(sum.value()) / count;
     for (int64_t e = threadIdx.x; e < total; e += kBlock) {
         const float d = at(e) - mean;
-        v += d * d;
+        squares.add(d * d);
     }
-    const float var = block_sum(v) / count;
+    const float var = block_sum(squares.value()) / count;
     if (threadIdx.x == 0) {
         a.mean[s * a.groups + g] = mean;
         a.rstd[s * a.groups + g] = 1.f / sqrtf(var + a.eps);

@@ -162,3 +162,23 @@ def test_grouped_products_of_rows_that_start_anywhere(cin, cout, dtype):
     assert torch.equal(spc.spc_grouped_fwd(x, w, seg, out=y), spc.spc_grouped_fwd(c(x), c(w), seg))
     assert torch.equal(spc.spc_grouped_dgrad(dy, w, seg, out=dx), spc.spc_grouped_dgrad(c(dy), c(w), seg))
     assert torch.equal(spc.spc_grouped_wgrad(x, dy, seg, out=dw), spc.spc_grouped_wgrad(c(x), c(dy), seg))
+
+
+# ------------------------------------------------------------- very long rows
+@pytest.mark.parametrize("c,groups", [(1026, 2), (1026, 513)])
+def test_group_norm_of_very_long_rows_far_from_zero(c, groups):
+    """Rows of more than 512 vectors at 1000.3 +- 0.01: a sum of the values themselves would take the
+    same side at every rounding and move the mean by many spreads."""
+    n = 20000
+    g = np.random.default_rng(2)
+    x = torch.from_numpy(1000.3 + 0.01 * g.standard_normal((n, c))).float()
+    seg = np.array([0, n - 700, n], np.int32)
+    _, mean_r, rstd_r, _ = ref.norm_fwd(x, None, None, seg, None, groups, 1e-12, "none")
+    y, mean, rstd = spc.spc_group_norm_fwd(to_dev(x), None, None, to_dev(seg), groups, eps=1e-12)
+    # the mean is rounded to fp32 (2^-24 relative, 6e-5 here) after sums around a pivot that lose
+    # less than as much again; squares around it are off by (1e-4 / 0.01)^2 of the variance
+    assert float((mean.double().cpu() / mean_r - 1).abs().max()) < 2 * ref.EPS32
+    assert float((rstd.double().cpu() / rstd_r - 1).abs().max()) < 2e-4
+    y_r = ((x.double() - mean.double().cpu().repeat_interleave(c // groups, 1)[(torch.arange(n) >= n - 700).long()])
+           * rstd_r.repeat_interleave(c // groups, 1)[(torch.arange(n) >= n - 700).long()])
+    assert float((y.double().cpu() - y_r).norm() / y_r.norm()) < 1e-3
