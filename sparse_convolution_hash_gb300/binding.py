@@ -584,6 +584,24 @@ def _optional(t: Optional[torch.Tensor], dtype, shape, name: str):
     return t, t.data_ptr()
 
 
+def _status(t: Optional[torch.Tensor]):
+    """The pointer of a status word, which kernels write to."""
+    if t is None:
+        return None
+    if not t.is_cuda or t.dtype is not torch.int32 or t.numel() < 1:
+        raise ValueError("status must be an int32 CUDA tensor of one element")
+    return t.data_ptr()
+
+
+def _room(ws: Optional[torch.Tensor], nbytes: int, device) -> torch.Tensor:
+    """The caller's workspace where it is large enough, or a new one."""
+    if ws is None:
+        return _workspace(nbytes, device)
+    if not ws.is_cuda or not ws.is_contiguous():
+        raise ValueError("ws must be a contiguous CUDA tensor")
+    return ws if ws.numel() >= nbytes else _workspace(nbytes, device)
+
+
 def _result(out: Optional[torch.Tensor], shape, dtype, device, name: str) -> torch.Tensor:
     """The caller's output buffer, checked, or a new one."""
     if out is None:
@@ -616,8 +634,7 @@ def spc_row_segments(ids: torch.Tensor, segments: int, with_order: bool = True,
         order = _result(order, (n,), torch.int32, dev, "order")
     L = lib()
     nbytes = L.spc_row_segments_workspace_size(n, segments)
-    if ws is None or ws.numel() < nbytes:
-        ws = _workspace(nbytes, dev)
+    ws = _room(ws, nbytes, dev)
     code = L.spc_row_segments(ids.data_ptr(), stride, n, segments, seg.data_ptr(),
                               order.data_ptr() if with_order else None, ws.data_ptr(), ws.numel(), _stream(dev))
     _check(code, "spc_row_segments")
@@ -647,10 +664,9 @@ def spc_group_norm_fwd(x: torch.Tensor, gamma: Optional[torch.Tensor], beta: Opt
     rstd = _result(rstd, (segments, groups), torch.float32, dev, "rstd")
     L = lib()
     nbytes = L.spc_group_norm_workspace_size(n, c, segments, groups, dt)
-    if ws is None or ws.numel() < nbytes:
-        ws = _workspace(nbytes, dev)
+    ws = _room(ws, nbytes, dev)
     code = L.spc_group_norm_fwd(x.data_ptr(), gamma_p, beta_p, seg.data_ptr(), order_p, segments, n, c, groups,
-                                eps, act, dt, y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _ptr(status),
+                                eps, act, dt, y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _status(status),
                                 ws.data_ptr(), ws.numel(), _stream(dev))
     _check(code, "spc_group_norm_fwd")
     return y, mean, rstd
@@ -680,11 +696,10 @@ def spc_group_norm_bwd(dy: torch.Tensor, x: torch.Tensor, gamma: Optional[torch.
     dbeta = torch.empty(c, dtype=torch.float32, device=dev)
     L = lib()
     nbytes = L.spc_group_norm_workspace_size(n, c, segments, groups, dt)
-    if ws is None or ws.numel() < nbytes:
-        ws = _workspace(nbytes, dev)
+    ws = _room(ws, nbytes, dev)
     code = L.spc_group_norm_bwd(dy.data_ptr(), x.data_ptr(), gamma_p, beta_p, mean_p, rstd_p, seg.data_ptr(),
                                 order_p, segments, n, c, groups, act, dt, dx.data_ptr(), dgamma.data_ptr(),
-                                dbeta.data_ptr(), _ptr(status), ws.data_ptr(), ws.numel(), _stream(dev))
+                                dbeta.data_ptr(), _status(status), ws.data_ptr(), ws.numel(), _stream(dev))
     _check(code, "spc_group_norm_bwd")
     return dx, dgamma, dbeta
 
@@ -737,9 +752,10 @@ def _positions(x_rows, y_rows, rows: int):
 
 def _grouped_ws(ws, segments, m, cin, cout, dt, listed, device):
     nbytes = lib().spc_grouped_workspace_size(segments, m, cin, cout, dt, listed)
-    if nbytes and (ws is None or ws.numel() < nbytes):
-        ws = _workspace(nbytes, device)
-    return (ws, ws.data_ptr(), ws.numel()) if ws is not None else (None, None, 0)
+    if not nbytes and ws is None:
+        return None, None, 0
+    ws = _room(ws, nbytes, device)
+    return ws, ws.data_ptr(), ws.numel()
 
 
 def spc_grouped_fwd(x: torch.Tensor, w: torch.Tensor, seg: torch.Tensor,
@@ -757,9 +773,9 @@ def spc_grouped_fwd(x: torch.Tensor, w: torch.Tensor, seg: torch.Tensor,
     _expect(seg, (segments + 1,), "seg")
     x_rows, x_p, y_rows, y_p, m = _positions(x_rows, y_rows, n_x)
     y = _result(out, (m, cout), x.dtype, dev, "out")
-    ws_p, ws_n = (None, 0) if ws is None else (ws.data_ptr(), ws.numel())  # only the gradient by w needs one
+    ws_p, ws_n = (None, 0) if ws is None else (_room(ws, 0, dev).data_ptr(), ws.numel())  # only the gradient by w needs one
     code = lib().spc_grouped_fwd(x.data_ptr(), w.data_ptr(), seg.data_ptr(), x_p, y_p, segments, n_x, m, cin, cout,
-                                 dt, y.data_ptr(), _ptr(status), ws_p, ws_n, _stream(dev))
+                                 dt, y.data_ptr(), _status(status), ws_p, ws_n, _stream(dev))
     _check(code, "spc_grouped_fwd")
     return y
 
@@ -779,9 +795,9 @@ def spc_grouped_dgrad(dy: torch.Tensor, w: torch.Tensor, seg: torch.Tensor,
     _expect(seg, (segments + 1,), "seg")
     x_rows, x_p, y_rows, y_p, m = _positions(x_rows, y_rows, n_y)
     dx = _result(out, (m, cin), dy.dtype, dev, "out")
-    ws_p, ws_n = (None, 0) if ws is None else (ws.data_ptr(), ws.numel())  # only the gradient by w needs one
+    ws_p, ws_n = (None, 0) if ws is None else (_room(ws, 0, dev).data_ptr(), ws.numel())  # only the gradient by w needs one
     code = lib().spc_grouped_dgrad(dy.data_ptr(), w.data_ptr(), seg.data_ptr(), x_p, y_p, segments, n_y, m, cin, cout,
-                                   dt, dx.data_ptr(), _ptr(status), ws_p, ws_n, _stream(dev))
+                                   dt, dx.data_ptr(), _status(status), ws_p, ws_n, _stream(dev))
     _check(code, "spc_grouped_dgrad")
     return dx
 
@@ -802,6 +818,6 @@ def spc_grouped_wgrad(x: torch.Tensor, dy: torch.Tensor, seg: torch.Tensor,
     dw = _result(out, (segments, cin, cout), torch.float32, dev, "out")
     ws, ws_p, ws_n = _grouped_ws(ws, segments, m, cin, cout, dt, x_p is not None or y_p is not None, dev)
     code = lib().spc_grouped_wgrad(x.data_ptr(), dy.data_ptr(), seg.data_ptr(), x_p, y_p, segments, n_x, n_y, m, cin,
-                                   cout, dt, dw.data_ptr(), _ptr(status), ws_p, ws_n, _stream(dev))
+                                   cout, dt, dw.data_ptr(), _status(status), ws_p, ws_n, _stream(dev))
     _check(code, "spc_grouped_wgrad")
     return dw

@@ -182,3 +182,27 @@ def test_group_norm_of_very_long_rows_far_from_zero(c, groups):
     y_r = ((x.double() - mean.double().cpu().repeat_interleave(c // groups, 1)[(torch.arange(n) >= n - 700).long()])
            * rstd_r.repeat_interleave(c // groups, 1)[(torch.arange(n) >= n - 700).long()])
     assert float((y.double().cpu() - y_r).norm() / y_r.norm()) < 1e-3
+
+
+# ------------------------------------------------------- where buffers have to be
+def test_status_words_and_workspaces_are_on_the_device():
+    d = dev()
+    x = torch.randn(10, 16, device=d)
+    seg = torch.tensor([0, 10], dtype=torch.int32, device=d)
+    w = torch.randn(1, 16, 8, device=d)
+    dy = torch.randn(10, 8, device=d)
+    m = torch.zeros(1, 4, device=d)
+    host, host_ws = torch.zeros(1, dtype=torch.int32), torch.empty(1 << 20, dtype=torch.uint8)
+    calls = [lambda **k: spc.spc_group_norm_fwd(x, None, None, seg, 4, **k),
+             lambda **k: spc.spc_group_norm_bwd(x, x, None, None, m, m + 1, seg, 4, **k),
+             lambda **k: spc.spc_grouped_fwd(x, w, seg, **k), lambda **k: spc.spc_grouped_dgrad(dy, w, seg, **k),
+             lambda **k: spc.spc_grouped_wgrad(x, dy, seg, **k)]
+    for f in calls:
+        for bad in (host, torch.zeros(1, device=d), torch.zeros(0, dtype=torch.int32, device=d)):
+            with pytest.raises(ValueError):
+                f(status=bad)
+        for bad in (host_ws, torch.zeros(1, dtype=torch.uint8, device=d).expand(1 << 20)):
+            with pytest.raises(ValueError):
+                f(ws=bad)
+    with pytest.raises(ValueError):
+        spc.spc_row_segments(seg, 2, ws=host_ws)
