@@ -206,3 +206,119 @@ def test_status_words_and_workspaces_are_on_the_device():
                 f(ws=bad)
     with pytest.raises(ValueError):
         spc.spc_row_segments(seg, 2, ws=host_ws)
+
+
+# ---------------------------------------------------- tiles that long segments take
+def ragged(segments, m, x_rows, y_rows, dtype, cin, cout, seed=0):
+    g = np.random.default_rng(seed + m + cin + cout)
+    x = torch.from_numpy(g.standard_normal((m, cin))).to(DT[dtype])
+    dy = torch.from_numpy(g.standard_normal((m, cout))).to(DT[dtype])
+    w = torch.from_numpy(g.standard_normal((segments, cin, cout)) / np.sqrt(cin)).to(DT[dtype])
+    perm = lambda: g.permutation(m).astype(np.int32)
+    return x, dy, w, perm() if x_rows else None, perm() if y_rows else None
+
+
+def check_products(x, dy, w, seg, x_rows, y_rows, dtype, wgrad=False):
+    """Forward, gradient by the input and (on request) by the weights against float64, twice the same."""
+    m, cin, cout = x.shape[0], x.shape[1], dy.shape[1]
+    u, st = ref.U[DT[dtype]], spc.new_status(dev())
+    lists = dict(x_rows=to_dev(x_rows), y_rows=to_dev(y_rows), status=st)
+    f = lambda: spc.spc_grouped_fwd(to_dev(x), to_dev(w), to_dev(seg), **lists)
+    y = f()
+    want, mag = ref.grouped_fwd(x, w, seg, x_rows, y_rows, m)
+    close(y, want, 1.01 * u * want.abs() + cin * 2.0 ** -23 * mag * 1.01 + 2.0 ** -25 * (mag > 0), "y")
+    assert torch.equal(y, f())
+    f = lambda: spc.spc_grouped_dgrad(to_dev(dy), to_dev(w), to_dev(seg), **lists)
+    dx = f()
+    want, mag = ref.grouped_fwd(dy, w.transpose(1, 2), seg, y_rows, x_rows, m)
+    close(dx, want, 1.01 * u * want.abs() + cout * 2.0 ** -23 * mag * 1.01 + 2.0 ** -25 * (mag > 0), "dx")
+    assert torch.equal(dx, f())
+    if wgrad:
+        f = lambda: spc.spc_grouped_wgrad(to_dev(x), to_dev(dy), to_dev(seg), **lists)
+        dw = f()
+        want, mag = ref.grouped_wgrad(x, dy, seg, x_rows, y_rows)
+        close(dw, want, torch.from_numpy(np.diff(seg).astype(np.float64))[:, None, None] * 2.0 ** -23 * mag, "dw")
+        assert torch.equal(dw, f())
+    spc.check_status(st)
+
+
+# offsets with rows of no segment on both sides, an empty segment, one shorter than a CTA's 128 rows
+# (the second CTA of a pair has none), and a last tile of 74 rows
+LONG = np.array([40, 6000, 6000, 6100, 8990], np.int32)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("m,cin,cout,seg", [
+    (9000, 520, 520, LONG),                                              # pairs both ways, columns 520 = 2 x 256 + 8
+    (10500, 512, 264, np.array([0, 5000, 10500], np.int32)),             # pairs forward; dgrad: K of 264, no pairs
+    (10500, 264, 512, np.array([3, 4100, 4101, 4101, 10499], np.int32)),  # pairs in dgrad; a segment of one row
+    (12800, 1024, 512, np.array([0, 2560, 5120, 7680, 10240, 12800], np.int32))])  # whole tiles, deep K
+def test_grouped_products_of_long_dense_segments(m, cin, cout, seg, dtype):
+    check_products(*ragged(len(seg) - 1, m, False, False, dtype, cin, cout)[:3], seg, None, None, dtype, wgrad=True)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("cin,cout", [(520, 520), (264, 1024)])
+def test_grouped_products_of_long_listed_segments(cin, cout, dtype):
+    """128 x 256 tiles with rows through lists, forward and gradient by the input."""
+    x, dy, w, xr, yr = ragged(4, 9000, True, True, dtype, cin, cout)
+    check_products(x, dy, w, LONG, xr, yr, dtype, wgrad=True)
+
+
+@pytest.mark.parametrize("listed", [False, True])
+@pytest.mark.parametrize("cin,cout", [(33, 385), (36, 388)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_grouped_products_in_large_cuda_core_tiles(dtype, cin, cout, listed):
+    """128 x 128 tiles on CUDA cores (two for each SM), values one by one and four at a time."""
+    m, seg = 26000, np.array([5, 9000, 9000, 9100, 25999], np.int32)
+    x, dy, w, xr, yr = ragged(4, m, listed, listed, dtype, cin, cout)
+    st = spc.new_status(dev())
+    y = spc.spc_grouped_fwd(to_dev(x), to_dev(w), to_dev(seg), x_rows=to_dev(xr), y_rows=to_dev(yr), status=st)
+    want, mag = ref.grouped_fwd(x, w, seg, xr, yr, m)
+    u = ref.U[DT[dtype]]
+    close(y, want, 1.01 * u * want.abs() + cin * 2.0 ** -23 * mag * 1.01 + 2.0 ** -25 * (mag > 0), "y")
+    # the gradient by the input of the mirrored shape has as many columns
+    x, dy, w, xr, yr = ragged(4, m, listed, listed, dtype, cout, cin)
+    dx = spc.spc_grouped_dgrad(to_dev(dy), to_dev(w), to_dev(seg), x_rows=to_dev(xr), y_rows=to_dev(yr), status=st)
+    want, mag = ref.grouped_fwd(dy, w.transpose(1, 2), seg, yr, xr, m)
+    close(dx, want, 1.01 * u * want.abs() + cin * 2.0 ** -23 * mag * 1.01 + 2.0 ** -25 * (mag > 0), "dx")
+    spc.check_status(st)
+
+
+@pytest.mark.parametrize("listed", [False, True])
+@pytest.mark.parametrize("cin,cout", [(129, 257), (132, 260)])
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+def test_grouped_weight_gradient_in_large_cuda_core_tiles(dtype, cin, cout, listed):
+    segments, m = 52, 900
+    g = np.random.default_rng(cin)
+    seg = np.sort(g.integers(0, m + 1, segments + 1)).astype(np.int32)
+    x, dy, w, xr, yr = ragged(segments, m, listed, listed, dtype, cin, cout)
+    check_products(x, dy, w, seg, xr, yr, dtype, wgrad=True)
+
+
+def test_wait_limit_ends_products_of_long_segments_with_a_status():
+    """As for the other shapes: with a limit of 0 the pair kernels give up, report it and return, and
+    the same calls work again afterwards."""
+    d = dev()
+    x = torch.randn(9000, 520, device=d, dtype=torch.bfloat16)
+    w = torch.randn(4, 520, 520, device=d, dtype=torch.bfloat16)
+    seg, rows = to_dev(LONG), torch.randperm(9000, device=d).to(torch.int32)
+    calls = [lambda st: spc.spc_grouped_fwd(x, w, seg, status=st), lambda st: spc.spc_grouped_dgrad(x, w, seg, status=st),
+             lambda st: spc.spc_grouped_dgrad(x, w, seg, y_rows=rows, status=st),
+             lambda st: spc.spc_grouped_wgrad(x, x, seg, status=st),
+             lambda st: spc.spc_grouped_wgrad(x, x, seg, x_rows=rows, y_rows=rows, status=st)]
+    want = [f(None).clone() for f in calls]
+    old = spc.spc_get_wait_limit_ns()
+    try:
+        spc.spc_set_wait_limit_ns(0)
+        for f in calls:
+            st = spc.new_status(d)
+            f(st)
+            torch.cuda.synchronize()
+            assert int(st) == 9  # SPC_ERR_TIMEOUT
+    finally:
+        spc.spc_set_wait_limit_ns(old)
+    for f, y in zip(calls, want):
+        st = spc.new_status(d)
+        assert torch.equal(f(st), y)
+        spc.check_status(st)
