@@ -1,3 +1,4 @@
+import gc
 import os
 import sys
 
@@ -27,3 +28,11 @@ def pytest_collection_modifyitems(config, items):
     for it in items:
         if "gpu" in it.keywords:
             it.add_marker(skip)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _collected():
+    """What earlier tests left in reference cycles (an exception holds its frames' tensors) is freed
+    before a module begins, not while one of its tests counts memory."""
+    gc.collect()
+    yield
