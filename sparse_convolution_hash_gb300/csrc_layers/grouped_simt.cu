@@ -6,6 +6,11 @@
 // chunk is on its way into registers while this one is multiplied, two columns per f32x2
 // instruction.  Segment sizes are known on the device only, so the grid covers the most row
 // tiles there can be (one partial tile per segment) and each block finds its segment in `seg`.
+//
+// 8,000 fp32 rows in 4 segments, 256 -> 1024: 144 us, 29 TFLOP/s.  The large tile's 130 registers leave one block of
+// eight warps an SM, two a scheduler, and they wait for shared memory a third of the time: the FMA pipe is
+// active 46%.  A segment of few rows pays for a whole 64-row tile (16 rows of 64 segments, 1024 -> 4096: 226 us, 77%
+// of the shared-memory pipe).  A value's terms are added in one fp32 chain, or one per split of the rows.
 #include "layers.cuh"
 #include "pairs.cuh"
 

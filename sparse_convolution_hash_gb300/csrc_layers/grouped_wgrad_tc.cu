@@ -413,7 +413,7 @@ spc_status bring(const void* from, const int32_t* list, int64_t rows, int64_t m,
 }
 
 // Listed rows of wide operands are brought into order first: every tile row (column) of weights would copy
-// each of them again (bf16, 8 segments of 4096, 512 x 2048: 129 us against 194 by copies in the
+// each of them again (bf16, 8 segments of 4096, 512 x 2048: 134 us against 194 by copies in the
 // kernel; 398,833 rows of 128 x 128, where each is copied once: 75 in the kernel).  128 x 128 tiles where 128 x 256
 // would be empty by half.
 bool brings_rows(int32_t cin, int32_t cout) { return cin > kTileM && cout > kTileM; }
