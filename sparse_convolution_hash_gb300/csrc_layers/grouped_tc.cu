@@ -87,9 +87,11 @@ k_grouped_tc(GroupedArgs a, uint64_t wait_ns, const __grid_constant__ CUtensorMa
         ptx::prefetch_tmap(&map_in);
         ptx::prefetch_tmap(&map_w);
     }
+    // tensor memory only after the wait: a kernel before this one that lets it start early may still have to
+    // allocate its own, and neither would end
+    wait_for_kernel_before();
     if (warp == 1) ptx::tmem_alloc_cg<CG>(s_ctrl, S::kTmemCols);
     const int cols = (a.n + BN - 1) / BN;
-    wait_for_kernel_before();
     const int32_t tiles = tile_starts(a.seg, a.segments, a.m, S::kRows, cols, s_start,
                                       blockIdx.x == 0 ? a.status : nullptr, tid, kAll);
     ptx::tc_fence_before();

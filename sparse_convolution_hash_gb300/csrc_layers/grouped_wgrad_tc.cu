@@ -92,9 +92,9 @@ k_grouped_wgrad_tc(GroupedWgradArgs a, float* __restrict__ part, Join* __restric
             ptx::prefetch_tmap(&map_dy);
         }
     }
+    wait_for_kernel_before();  // before tensor memory, as in the forward
     if (warp == 1) ptx::tmem_alloc_cg<1>(s_ctrl, S::kTmemCols);
     const int cols = (a.cout + BN - 1) / BN, tiles = (a.cin + kTileM - 1) / kTileM * cols;
-    wait_for_kernel_before();
     if (warp == 0)
         make_plan(a.seg, a.segments, a.m, tiles, gridDim.x, s_start, s_list, s_list + a.segments, &plan,
                   blockIdx.x == 0 ? a.status : nullptr, lane);

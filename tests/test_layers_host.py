@@ -26,6 +26,19 @@ def test_no_load_fills_several_ctas():
             assert "multi" + "cast" not in piece.split('"')[0], f
 
 
+def test_tensor_memory_is_taken_after_the_wait():
+    """A kernel set up beside the one before it holds no tensor memory while it waits: the other may still
+    have blocks to start that need some."""
+    kernels = 0
+    for f in glob.glob(os.path.join(libbuild.CSRC_LAYERS, "*.cu")):
+        with open(f, encoding="utf-8") as fh:
+            for body in fh.read().split("__global__")[1:]:
+                if "tmem_alloc" in body:
+                    kernels += 1
+                    assert 0 <= body.find("wait_for_kernel_before();") < body.find("tmem_alloc"), f
+    assert kernels == 2
+
+
 # ------------------------------------------- the plan of the gradient by the weights
 @pytest.fixture(scope="module")
 def plan_check(tmp_path_factory):
