@@ -516,8 +516,9 @@ SPC_API spc_status spc_row_segments(const int32_t* ids, int64_t id_stride, int64
  * and the group's channels, rstd = 1 / sqrt(variance + eps), and
  *   y = act(gamma (x - mean) rstd + beta).
  * Sums run in fp32 around a pivot near the mean, merged in a fixed order: results are
- * run-to-run bit-identical.   SILU and its slope take the sigmoid from the hardware's
- * exp2 and reciprocal for every dt, fp32 among them: within 2^-19 relative for |z| up to 16.  An empty segment has mean 0 and variance 0; the
+ * run-to-run bit-identical.  SILU and its slope take the sigmoid from the hardware's
+ * exp2 and reciprocal for every dt, fp32 among them: within 2^-19 relative for |z|
+ * up to 16.  An empty segment has mean 0 and variance 0; the
  * rows of no segment give zeros.
  *
  *  x      [n, c] of dtype dt.      y [n, c] of dtype dt out (may be x itself).

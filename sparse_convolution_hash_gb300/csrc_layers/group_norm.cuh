@@ -18,7 +18,7 @@
 // dbeta and, weighted by gamma, the two means of a group; dx = A dz + B + D (x - mean).
 //
 // Large inputs take 2.2 times what one reading of their rows would (498,145 x 64 bf16, 4 samples, SILU: forward
-// 42 us, gradients 65).  With few rows every instruction is run once and costs
+// 40 us, gradients 64).  With few rows every instruction is run once and costs
 // about 10 cycles whatever it does, so the code around the loops over rows is kept short: sums and
 // statistics go through the same code in turn, short runs take one row body (2,000 x 16 fp32: with that
 // unrolled forward 9.5 us for 9.1, gradients 10.8 for 9.6; a launch beside the kernel before: 8.8 and 9.2).
@@ -714,10 +714,11 @@ struct Parts {
 };
 
 // (mean, rstd) of segment s into s_stat [groups], from the parts where several CTAs
-// share it; the CTA that holds its first position also writes them out.  Means are summed around one of
-// the longest parts', then squares around the joint mean in a second pass over the parts (10 of a lane):
-// a part of one row far from the others would cost a single pass around it the variance's digits (40,000 rows
-// of 1000 +- 1, such a row of 0: rstd off by 2e-3).  498,145 x 64 bf16 38.2 us, with the single pass 37.4.
+// share it; the CTA that holds its first position also writes them out.  Parts are taken around the first one's
+// mean p: M2 = sum (M2_i + n_i (mean_i - p)^2) - n (mean - p)^2.  Their means lie close together as a rule; where
+// the difference would cancel more than a sixteenth (a first part of one row far from the others cost the
+// rstd of 40,000 rows of 1000 +- 1 2e-3), a second pass takes squares around the joint mean.  (A second pass
+// at all times: 498,145 x 64 bf16 38.2 us for 37.4.)
 __device__ __forceinline__ void join_stats(const NormArgs& a, const int32_t* s_seg, int s, int64_t rows, const float2* part,
                                            float2* s_stat)
 {
@@ -731,18 +732,39 @@ __device__ __forceinline__ void join_stats(const NormArgs& a, const int32_t* s_s
         float mean = a.mean[(int64_t)s * a.groups + gr], rstd = a.rstd[(int64_t)s * a.groups + gr];
         if (span.first != span.last) {
             const Parts parts(span, part, rows, a.groups);
-            const float base = parts.get(parts.longest(), gr).x, n = (float)(int)(span.hi - span.lo);
+            const float base = parts.get(0, gr).x;
             float m = 0.f, q = 0.f;
-#pragma unroll 5
-            for (int i = lane; i < parts.count(); i += kJoin) m = fmaf(parts.rows_of(i), parts.get(i, gr).x - base, m);
-            mean = base + join_sum(m) / n;
 #pragma unroll 5
             for (int i = lane; i < parts.count(); i += kJoin) {
                 const float2 v = parts.get(i, gr);
-                const float d = v.x - mean;
-                q += fmaf(parts.rows_of(i) * per, d * d, v.y);
+                const float n = parts.rows_of(i), d = v.x - base;
+                m = fmaf(n, d, m);
+                q += fmaf(n * per, d * d, v.y);
             }
-            rstd = 1.f / sqrtf(join_sum(q) / (n * per) + a.eps);
+            const float n = (float)(int)(span.hi - span.lo), shift = join_sum(m) / n;
+            mean = base + shift;
+            q = join_sum(q);
+            const bool near = n * per * shift * shift <= 0.0625f * q;
+            q = fmaf(-n * per * shift, shift, q);
+            if (!__all_sync(FULL_MASK, near)) {
+                // around the mean of one of the longest parts, then around the joint mean
+                const float middle = parts.get(parts.longest(), gr).x;
+                float m2 = 0.f, q2 = 0.f;
+#pragma unroll 1
+                for (int i = lane; i < parts.count(); i += kJoin) m2 = fmaf(parts.rows_of(i), parts.get(i, gr).x - middle, m2);
+                const float joint = middle + join_sum(m2) / n;
+#pragma unroll 1
+                for (int i = lane; i < parts.count(); i += kJoin) {
+                    const float2 v = parts.get(i, gr);
+                    const float d = v.x - joint;
+                    q2 += fmaf(parts.rows_of(i) * per, d * d, v.y);
+                }
+                q2 = join_sum(q2);
+                // a group that was near keeps its sums: they do not depend on its neighbours'
+                mean = near ? mean : joint;
+                q = near ? q : q2;
+            }
+            rstd = 1.f / sqrtf((q < 0.f ? 0.f : q) / (n * per) + a.eps);
             if (g < a.groups && lane == 0 && (int)blockIdx.x == span.first) {
                 a.mean[(int64_t)s * a.groups + g] = mean;
                 a.rstd[(int64_t)s * a.groups + g] = rstd;
