@@ -9,7 +9,10 @@
  *     gradient (dfilter) as implicit GEMMs over that map;
  *   - the layers that stand between convolutions: group norm with an activation
  *     per sample, dropout, and products of rows with the weight of their expert,
- *     each with its gradients, over rows grouped into segments.
+ *     each with its gradients, over rows grouped into segments;
+ *   - what a transformer block over the same rows needs besides: layer norm, rotary
+ *     positions from the voxels' coordinates, attention within segments and the
+ *     choice of experts, each with its gradient.
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -85,6 +88,9 @@ typedef enum { SPC_PREC_EXACT = 0, SPC_PREC_TF32 = 1 } spc_precision;
 /* Activation of the fused forward epilogue (spc_conv_fwd_fused: NONE and RELU)
  * and of group norm (all three; SILU is z / (1 + exp(-z))). */
 typedef enum { SPC_ACT_NONE = 0, SPC_ACT_RELU = 1, SPC_ACT_SILU = 2 } spc_activation;
+
+/* What a logit is worth in spc_route_fwd. */
+typedef enum { SPC_SCORE_SOFTMAX = 0, SPC_SCORE_SIGMOID = 1 } spc_score;
 
 /* How spc_conv_dgrad reads its map argument. */
 typedef enum {
@@ -632,6 +638,150 @@ SPC_API spc_status spc_grouped_wgrad(const void* x, const void* dy, const int32_
                                      const int32_t* x_rows, const int32_t* y_rows, int32_t segments,
                                      int64_t n_x, int64_t n_y, int64_t m, int32_t cin, int32_t cout,
                                      spc_dtype dt, float* dw, int32_t* status, void* ws,
+                                     size_t ws_bytes, void* stream);
+
+/* --------------------------------------------------------------- layer norm
+ * spc_layer_norm_fwd -- per row: mean and variance (divided by c) of its channels,
+ * rstd = 1 / sqrt(variance + eps), y = gamma (x - mean) rstd + beta.  The variance is
+ * summed around the mean, in fp32.
+ *
+ *  x      [n, c] of dtype dt.      y [n, c] of dtype dt out (may be x itself).
+ *  gamma, beta  [c] fp32, or NULL (1 and 0).      eps > 0.
+ *  mean, rstd   [n] fp32 out (what the backward pass reads).
+ *  Rows of any length; they are held in registers up to 16,384 (16-bit) or 8,192 channels, and
+ *  read in 16-byte words when x and y are 16-byte aligned and c is a multiple of 16 bytes,
+ *  else element by element.
+ */
+SPC_API spc_status spc_layer_norm_fwd(const void* x, const float* gamma, const float* beta, int64_t n,
+                                      int32_t c, float eps, spc_dtype dt, void* y, float* mean,
+                                      float* rstd, void* stream);
+
+/* spc_layer_norm_bwd -- the gradients: with xh = (x - mean) rstd and u = gamma dy,
+ *   dx = rstd (u - mean_c(u) - xh mean_c(u xh)),  dgamma = sum over rows of dy xh,
+ *   dbeta = sum over rows of dy.
+ * Sums run in fp32 in a fixed order: results are run-to-run bit-identical.
+ *
+ *  mean, rstd     [n] fp32 from the forward pass.
+ *  dx             [n, c] of dtype dt out (may be dy or x itself).
+ *  dgamma, dbeta  [c] fp32 out, or NULL (zeros where n = 0).
+ *  ws  spc_layer_norm_workspace_size(n, c) bytes, 256-byte aligned (only the backward pass needs one).
+ */
+SPC_API size_t spc_layer_norm_workspace_size(int64_t n, int32_t c);
+SPC_API spc_status spc_layer_norm_bwd(const void* dy, const void* x, const float* gamma,
+                                      const float* mean, const float* rstd, int64_t n, int32_t c,
+                                      spc_dtype dt, void* dx, float* dgamma, float* dbeta, void* ws,
+                                      size_t ws_bytes, void* stream);
+
+/* --------------------------------------------------------- rotary positions
+ * spc_rope_fwd -- turns pairs of channels of each head by angles that grow with the voxel's
+ * cell on one axis: of a head's d channels, pair i is (2 i, 2 i + 1); the first pairs[0]
+ * pairs belong to z, the next pairs[1] to y, the next pairs[2] to x, and pair i of an axis at
+ * cell p turns by p steps[i]:
+ *   y_2i = x_2i cos - x_2i+1 sin,   y_2i+1 = x_2i sin + x_2i+1 cos.
+ * Channels past those pairs are copied.  spc_rope_bwd turns back (the gradient).
+ *
+ *  x      n rows of [heads, d] of dtype dt, a row ldx elements after the one before it
+ *         (ldx >= heads d: the queries' and keys' part of a projection's rows is read in place).
+ *  coords [n, 4] int32 rows (b, z, y, x), 16-byte aligned; any cell, negative ones too.
+ *  pairs  host [3], sum <= d / 2 and <= 128.
+ *  steps  host [sum of pairs]: the turn from one cell to the next, 2^64 to a full turn, so
+ *         that angles are exact at every cell; spc_rope_steps writes
+ *         base^(-j / pairs[a]) radians for pair j of axis a.
+ *  y      n rows of dtype dt out, ldy elements apart (may be x itself with ldy = ldx).
+ */
+SPC_API spc_status spc_rope_steps(const int32_t pairs[3], double base, uint64_t* steps);
+SPC_API spc_status spc_rope_fwd(const void* x, int64_t ldx, const int32_t* coords,
+                                const int32_t pairs[3], const uint64_t* steps, int64_t n,
+                                int32_t heads, int32_t d, spc_dtype dt, void* y, int64_t ldy,
+                                void* stream);
+SPC_API spc_status spc_rope_bwd(const void* dy, int64_t lddy, const int32_t* coords,
+                                const int32_t pairs[3], const uint64_t* steps, int64_t n,
+                                int32_t heads, int32_t d, spc_dtype dt, void* dx, int64_t lddx,
+                                void* stream);
+
+/* ------------------------------------------------------- routing to experts
+ * spc_route_fwd -- for each token the top_k experts and their weights.  With p the softmax
+ * over the token's logits or the sigmoid of each, and c = p + bias:
+ *   - of `groups` equal groups of neighbouring experts the top_groups with the largest
+ *     sum of their two best c (of the one, where a group has one) are kept;
+ *   - of the kept groups' experts the top_k largest c are chosen, largest first;
+ *   - expert's weight  gate = scale p, or with renorm  scale p / (sum of the chosen p).
+ * The bias counts in the choice only.  Equal c go to the lowest expert, equal groups to the
+ * lowest group.  The choice is that of c in 64 bits (without bias and groups: of the logits).
+ * An expert whose logit is -inf or NaN, or whose bias is NaN or -inf, is not available; where fewer than top_k
+ * are left the rest of a token's slots hold expert -1 (which spc_row_segments puts last) and gate 0.
+ *
+ *  logits  [n, experts] of dtype dt; experts 1 .. SPC_MAX_SEGMENTS.
+ *  bias    [experts] fp32 or NULL.
+ *  top_k   1 .. SPC_MAX_TOP_K, at most top_groups experts / groups.
+ *  groups  divides experts (1: no groups); top_groups 1 .. groups.
+ *  expert  [n, top_k] int32 out.     gate [n, top_k] fp32 out.
+ */
+#define SPC_MAX_TOP_K 32
+
+SPC_API spc_status spc_route_fwd(const void* logits, const float* bias, int64_t n, int32_t experts,
+                                 int32_t top_k, spc_score score, int32_t groups, int32_t top_groups,
+                                 int32_t renorm, float scale, spc_dtype dt, int32_t* expert,
+                                 float* gate, void* stream);
+
+/* spc_route_bwd -- the gradient by the logits for the forward's choice (which, as the bias, has none):
+ *  dgate   [n, top_k] fp32.      expert [n, top_k] int32 from the forward pass (slots of -1 add
+ *          nothing; other numbers outside [0, experts) are skipped and set SPC_ERR_ROW_INDEX).
+ *  dlogits [n, experts] of dtype dt out; must not be logits itself.
+ *  status  device int32 sticky error word, or NULL.
+ */
+SPC_API spc_status spc_route_bwd(const float* dgate, const void* logits, const int32_t* expert,
+                                 int64_t n, int32_t experts, int32_t top_k, spc_score score,
+                                 int32_t renorm, float scale, spc_dtype dt, void* dlogits,
+                                 int32_t* status, void* stream);
+
+/* ---------------------------------------------------------------- attention
+ * spc_attention_fwd -- each query attends to the keys of its own segment:
+ *   s = scale q k^T,  p = softmax(s) over the segment's keys,  o = p v,
+ *   lse = log(sum of exp(s)).
+ * seg_q and seg_k (as above, any number of segments) hold the rows of each segment among the queries and the
+ * keys; pass the same array for attention of rows among themselves.  Rows of the same
+ * head are independent of other segments' values, NaN and infinities among them.  A query without keys
+ * (an empty segment, rows outside all segments, scores all -inf) gives o = 0 and lse = -inf.
+ *
+ *  q      nq rows of [hq, d]; k, v  nk rows of [hk, d], of dtype dt; rows ldq, ldk, ldv elements
+ *         apart (slices of one projection are read in place).  hk divides hq: query head h
+ *         reads key head h / (hq / hk).  d 1 .. 128.
+ *  scale  > 0, finite.
+ *  o      nq rows of [hq, d] of dtype dt out, ldo apart.     lse [nq, hq] fp32 out.
+ *  status device int32 sticky error word, or NULL (SPC_ERR_ROW_INDEX, SPC_ERR_TIMEOUT).
+ *  ws     spc_attention_workspace_size(..., backward = 0) bytes, 256-byte aligned (0: none needed).
+ *  Probabilities are rounded to dt before the product with v on tensor cores; sums and the softmax
+ *  are fp32.  Results are run-to-run bit-identical.
+ *  Kernels: tcgen05 tensor cores for fp16 / bf16 with d a multiple of 8 and rows and
+ *  tensors on 16-byte boundaries, else CUDA cores in fp32.
+ */
+SPC_API size_t spc_attention_workspace_size(int64_t nq, int64_t nk, int32_t segments, int32_t hq,
+                                            int32_t hk, int32_t d, spc_dtype dt, int32_t backward);
+SPC_API spc_status spc_attention_fwd(const void* q, int64_t ldq, const void* k, int64_t ldk,
+                                     const void* v, int64_t ldv, const int32_t* seg_q,
+                                     const int32_t* seg_k, int32_t segments, int64_t nq, int64_t nk,
+                                     int32_t hq, int32_t hk, int32_t d, float scale, spc_dtype dt,
+                                     void* o, int64_t ldo, float* lse, int32_t* status, void* ws,
+                                     size_t ws_bytes, void* stream);
+
+/* spc_attention_bwd -- the gradients, with the probabilities computed again from lse:
+ *   delta = sum over d of dout o,  ds = p (dout v^T - delta),
+ *   dq = scale ds k,  dk = scale ds^T q,  dv = p^T dout,
+ * dk and dv summed over the query heads that share a key head.  Rows of no segment give zeros.  p and ds are
+ * rounded to dt before their products on tensor cores.  No atomics: results are run-to-run bit-identical.
+ *
+ *  o, lse  from the forward pass.    dout rows of [hq, d], lddo apart.
+ *  dq, dk, dv  rows of dtype dt out, lddq, lddk, lddv apart; they overlap no argument nor one another.
+ *  ws  spc_attention_workspace_size(..., backward = 1) bytes, 256-byte aligned.
+ */
+SPC_API spc_status spc_attention_bwd(const void* dout, int64_t lddo, const void* q, int64_t ldq,
+                                     const void* k, int64_t ldk, const void* v, int64_t ldv,
+                                     const void* o, int64_t ldo, const float* lse,
+                                     const int32_t* seg_q, const int32_t* seg_k, int32_t segments,
+                                     int64_t nq, int64_t nk, int32_t hq, int32_t hk, int32_t d,
+                                     float scale, spc_dtype dt, void* dq, int64_t lddq, void* dk,
+                                     int64_t lddk, void* dv, int64_t lddv, int32_t* status, void* ws,
                                      size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus

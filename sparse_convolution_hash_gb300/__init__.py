@@ -1,7 +1,8 @@
 """GB300-native sparse 3-D convolution: indice maps, strided output sets and
 implicit-GEMM conv forward / dinput / dfilter, and the layers between convolutions
-(group norm with activation, dropout, products grouped by expert), behind the C
-ABI of libspc.so.
+(group norm with activation, dropout, products grouped by expert; layer norm, rotary
+positions, attention within segments, the choice of experts), behind the C ABI of
+libspc.so.
 
 ``binding`` holds the Python functions, named after the C entry points; the
 library is built in-tree by ``build.build()``.
@@ -35,6 +36,18 @@ from .binding import (  # noqa: F401
     spc_grouped_fwd,
     spc_grouped_dgrad,
     spc_grouped_wgrad,
+    SPC_MAX_TOP_K,
+    SPC_SCORE_SIGMOID,
+    SPC_SCORE_SOFTMAX,
+    spc_layer_norm_fwd,
+    spc_layer_norm_bwd,
+    spc_rope_steps,
+    spc_rope_fwd,
+    spc_rope_bwd,
+    spc_route_fwd,
+    spc_route_bwd,
+    spc_attention_fwd,
+    spc_attention_bwd,
     spc_conv_inverse,
     spc_map_row_order,
     spc_maxpool_fwd,

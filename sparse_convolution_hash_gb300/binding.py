@@ -29,6 +29,8 @@ STATUS_NAMES = {
 SPC_F32, SPC_F16, SPC_BF16 = 0, 1, 2
 SPC_PREC_EXACT, SPC_PREC_TF32 = 0, 1
 SPC_MAP_TRANSPOSED, SPC_MAP_SUBM_MIRROR = 0, 1
+SPC_SCORE_SOFTMAX, SPC_SCORE_SIGMOID = 0, 1
+SPC_MAX_TOP_K = 32
 
 _DTYPES = {torch.float32: SPC_F32, torch.float16: SPC_F16, torch.bfloat16: SPC_BF16}
 
@@ -165,6 +167,25 @@ def lib():
             L.spc_grouped_wgrad.argtypes = [_p, _p, _p, _p, _p, _i32, _i64, _i64, _i64, _i32, _i32, _i32,
                                             _p, _p, _p, _sz, _p]
             L.spc_grouped_wgrad.restype = _i32
+            L.spc_layer_norm_workspace_size.argtypes = [_i64, _i32]
+            L.spc_layer_norm_workspace_size.restype = _sz
+            L.spc_layer_norm_fwd.argtypes = [_p, _p, _p, _i64, _i32, _f, _i32, _p, _p, _p, _p]
+            L.spc_layer_norm_bwd.argtypes = [_p, _p, _p, _p, _p, _i64, _i32, _i32, _p, _p, _p, _p, _sz, _p]
+            L.spc_rope_steps.argtypes = [_I3, ctypes.c_double, _p]
+            L.spc_rope_fwd.argtypes = [_p, _i64, _p, _I3, _p, _i64, _i32, _i32, _i32, _p, _i64, _p]
+            L.spc_rope_bwd.argtypes = L.spc_rope_fwd.argtypes
+            L.spc_route_fwd.argtypes = [_p, _p, _i64, _i32, _i32, _i32, _i32, _i32, _i32, _f, _i32, _p, _p, _p]
+            L.spc_route_bwd.argtypes = [_p, _p, _p, _i64, _i32, _i32, _i32, _i32, _f, _i32, _p, _p, _p]
+            L.spc_attention_workspace_size.argtypes = [_i64, _i64, _i32, _i32, _i32, _i32, _i32, _i32]
+            L.spc_attention_workspace_size.restype = _sz
+            L.spc_attention_fwd.argtypes = [_p, _i64, _p, _i64, _p, _i64, _p, _p, _i32, _i64, _i64, _i32, _i32, _i32,
+                                            _f, _i32, _p, _i64, _p, _p, _p, _sz, _p]
+            L.spc_attention_bwd.argtypes = [_p, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _p, _p, _i32, _i64,
+                                            _i64, _i32, _i32, _i32, _f, _i32, _p, _i64, _p, _i64, _p, _i64, _p, _p,
+                                            _sz, _p]
+            for f in (L.spc_layer_norm_fwd, L.spc_layer_norm_bwd, L.spc_rope_steps, L.spc_rope_fwd, L.spc_rope_bwd,
+                      L.spc_route_fwd, L.spc_route_bwd, L.spc_attention_fwd, L.spc_attention_bwd):
+                f.restype = _i32
             _lib = L
     return _lib
 
@@ -821,3 +842,273 @@ def spc_grouped_wgrad(x: torch.Tensor, dy: torch.Tensor, seg: torch.Tensor,
                                    cout, dt, dw.data_ptr(), _status(status), ws_p, ws_n, _stream(dev))
     _check(code, "spc_grouped_wgrad")
     return dw
+
+
+# A transformer block's layers.  Their tensors lie on one device, whichever is current.
+
+def _one_device(dev, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+
+
+def _launch(dev, f, *args):
+    """Calls a C entry with `dev` as the current device and its current stream as the last argument."""
+    if torch._C._cuda_getDevice() == dev.index:
+        return f(*args, _stream(dev))
+    with torch.cuda.device(dev):
+        return f(*args, _stream(dev))
+
+
+def _matrix(t: torch.Tensor, name: str) -> torch.Tensor:
+    t = _values(t, name)
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions")
+    return t
+
+
+def _head_rows(t: torch.Tensor, name: str):
+    """(tensor, elements from row to row) of rows [heads, d]; what is not laid out so is copied."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have shape [rows, heads, channels]")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in _DTYPES:
+        raise ValueError(f"{name} must be float32, float16 or bfloat16, not {t.dtype}")
+    n, heads, d = t.shape
+    ld, between, step = t.stride()
+    if n > 1 and ld < heads * d or heads > 1 and between != d or d > 1 and step != 1:
+        t, ld = t.contiguous(), heads * d
+    return t, ld if n > 1 else heads * d
+
+
+def _head_result(out: Optional[torch.Tensor], shape, dtype, device, name: str):
+    """(tensor, elements from row to row) of a caller's output, checked, or of a new one."""
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device), shape[1] * shape[2]
+    if out.shape != shape or out.dtype is not dtype or out.device != device:
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} on {device}")
+    laid, ld = _head_rows(out, name)
+    if laid is not out:
+        raise ValueError(f"{name}'s rows must hold their heads' channels one after the other")
+    return out, ld
+
+
+def spc_layer_norm_fwd(x: torch.Tensor, gamma: Optional[torch.Tensor], beta: Optional[torch.Tensor], eps: float = 1e-5,
+                       out: Optional[torch.Tensor] = None, mean: Optional[torch.Tensor] = None,
+                       rstd: Optional[torch.Tensor] = None):
+    """y = gamma (x - mean) rstd + beta with the statistics of each row of x [n, C]: returns (y, mean [n],
+    rstd [n]).  Pass `out`, `mean` and `rstd` to call without allocating."""
+    x = _matrix(x, "x")
+    n, c = x.shape
+    dev = x.device
+    gamma, gamma_p = _optional(gamma, torch.float32, (c,), "gamma")
+    beta, beta_p = _optional(beta, torch.float32, (c,), "beta")
+    _one_device(dev, gamma=gamma, beta=beta)
+    y = _result(out, (n, c), x.dtype, dev, "out")
+    mean = _result(mean, (n,), torch.float32, dev, "mean")
+    rstd = _result(rstd, (n,), torch.float32, dev, "rstd")
+    code = _launch(dev, lib().spc_layer_norm_fwd, x.data_ptr(), gamma_p, beta_p, n, c, eps, _DTYPES[x.dtype], y.data_ptr(),
+                   mean.data_ptr(), rstd.data_ptr())
+    _check(code, "spc_layer_norm_fwd")
+    return y, mean, rstd
+
+
+def spc_layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, gamma: Optional[torch.Tensor], mean: torch.Tensor,
+                       rstd: torch.Tensor, out: Optional[torch.Tensor] = None, dgamma: Optional[torch.Tensor] = None,
+                       dbeta: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None):
+    """Gradients of spc_layer_norm_fwd: (dx [n, C], dgamma [C] fp32, dbeta [C] fp32).  `mean` and `rstd` come from
+    the forward call."""
+    x = _matrix(x, "x")
+    n, c = x.shape
+    dev = x.device
+    dy = _typed(dy, x.dtype, "dy")
+    _expect(dy, (n, c), "dy")
+    gamma, gamma_p = _optional(gamma, torch.float32, (c,), "gamma")
+    mean, mean_p = _optional(mean, torch.float32, (n,), "mean")
+    rstd, rstd_p = _optional(rstd, torch.float32, (n,), "rstd")
+    _one_device(dev, dy=dy, gamma=gamma, mean=mean, rstd=rstd, ws=ws)
+    dx = _result(out, (n, c), x.dtype, dev, "out")
+    dgamma = _result(dgamma, (c,), torch.float32, dev, "dgamma")
+    dbeta = _result(dbeta, (c,), torch.float32, dev, "dbeta")
+    L = lib()
+    ws = _room(ws, _launch_size(dev, L.spc_layer_norm_workspace_size, n, c), dev)
+    code = _launch(dev, L.spc_layer_norm_bwd, dy.data_ptr(), x.data_ptr(), gamma_p, mean_p, rstd_p, n, c, _DTYPES[x.dtype],
+                   dx.data_ptr(), dgamma.data_ptr(), dbeta.data_ptr(), ws.data_ptr(), ws.numel())
+    _check(code, "spc_layer_norm_bwd")
+    return dx, dgamma, dbeta
+
+
+def _launch_size(dev, f, *args) -> int:
+    """A workspace's size, which may depend on the device."""
+    if torch._C._cuda_getDevice() == dev.index:
+        return f(*args)
+    with torch.cuda.device(dev):
+        return f(*args)
+
+
+def _three(pairs) -> tuple:
+    t = tuple(int(p) for p in pairs)
+    if len(t) != 3 or min(t) < 0:
+        raise ValueError("pairs must hold the number of turned pairs of channels for z, y and x")
+    return t
+
+
+def spc_rope_steps(pairs: Sequence[int], base: float = 10000.0) -> torch.Tensor:
+    """Steps of spc_rope_fwd for base^(-j / pairs[axis]) radians a cell, j = 0 .. pairs[axis] - 1: a CPU tensor
+    [sum(pairs)] int64, 2^64 to a full turn.  Computed once, kept by the caller."""
+    pairs = _three(pairs)
+    steps = torch.empty(sum(pairs), dtype=torch.int64)
+    _check(lib().spc_rope_steps(_I3(*pairs), base, steps.data_ptr() if sum(pairs) else None), "spc_rope_steps")
+    return steps
+
+
+def _rope(name: str, x: torch.Tensor, coords: torch.Tensor, steps: torch.Tensor, pairs, out):
+    x, ldx = _head_rows(x, "x")
+    n, heads, d = x.shape
+    dev = x.device
+    pairs = _three(pairs)
+    if not coords.is_cuda or coords.dtype is not torch.int32:
+        raise ValueError("coords must be an int32 CUDA tensor")
+    _expect(coords, (n, 4), "coords")
+    coords = coords if coords.is_contiguous() else coords.contiguous()
+    if steps.is_cuda or steps.dtype is not torch.int64 or not steps.is_contiguous():
+        raise ValueError("steps must be a contiguous int64 CPU tensor (spc_rope_steps)")
+    _expect(steps, (sum(pairs),), "steps")
+    _one_device(dev, coords=coords)
+    y, ldy = _head_result(out, (n, heads, d), x.dtype, dev, "out")
+    code = _launch(dev, getattr(lib(), name), x.data_ptr(), ldx, coords.data_ptr(), _I3(*pairs),
+                   steps.data_ptr() if sum(pairs) else None, n, heads, d, _DTYPES[x.dtype], y.data_ptr(), ldy)
+    _check(code, name)
+    return y
+
+
+def spc_rope_fwd(x: torch.Tensor, coords: torch.Tensor, steps: torch.Tensor, pairs: Sequence[int],
+                 out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Rotary positions: pairs (2i, 2i + 1) of the channels of each head of x [n, heads, d] turned by the voxel's
+    cell times the pair's step, the first pairs[0] pairs by z, the next pairs[1] by y, the next pairs[2] by x of
+    coords [n, 4] int32 (b, z, y, x); the rest is copied.  A slice of a projection's rows (qkv[:, :2 * heads]) is
+    read in place; `out` may be such a slice, or x itself."""
+    return _rope("spc_rope_fwd", x, coords, steps, pairs, out)
+
+
+def spc_rope_bwd(dy: torch.Tensor, coords: torch.Tensor, steps: torch.Tensor, pairs: Sequence[int],
+                 out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The gradient of spc_rope_fwd: the same turns backwards."""
+    return _rope("spc_rope_bwd", dy, coords, steps, pairs, out)
+
+
+def spc_route_fwd(logits: torch.Tensor, top_k: int, score: int = SPC_SCORE_SOFTMAX, bias: Optional[torch.Tensor] = None,
+                  groups: int = 1, top_groups: int = 1, renorm: bool = True, scale: float = 1.0,
+                  expert: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None):
+    """The top_k experts of each token and their weights: (expert [n, top_k] int32, gate [n, top_k] fp32), best first.
+    logits [n, experts]; `bias` [experts] counts in the choice only; of `groups` groups of neighbouring experts the
+    top_groups best are kept (by the sum of their two best); `renorm` divides the weights by their sum.  A slot
+    for which no expert is available (logits of -inf or NaN) holds -1 and weight 0."""
+    logits = _matrix(logits, "logits")
+    n, experts = logits.shape
+    dev = logits.device
+    bias, bias_p = _optional(bias, torch.float32, (experts,), "bias")
+    _one_device(dev, bias=bias)
+    expert = _result(expert, (n, top_k), torch.int32, dev, "expert")
+    gate = _result(gate, (n, top_k), torch.float32, dev, "gate")
+    code = _launch(dev, lib().spc_route_fwd, logits.data_ptr(), bias_p, n, experts, top_k, score, groups, top_groups, bool(renorm),
+                   scale, _DTYPES[logits.dtype], expert.data_ptr(), gate.data_ptr())
+    _check(code, "spc_route_fwd")
+    return expert, gate
+
+
+def spc_route_bwd(dgate: torch.Tensor, logits: torch.Tensor, expert: torch.Tensor, score: int = SPC_SCORE_SOFTMAX,
+                  renorm: bool = True, scale: float = 1.0, out: Optional[torch.Tensor] = None,
+                  status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The gradient of spc_route_fwd's weights by the logits, [n, experts] of their type, for the experts that the
+    forward call chose."""
+    logits = _matrix(logits, "logits")
+    n, experts = logits.shape
+    dev = logits.device
+    expert = _typed(expert, torch.int32, "expert")
+    if expert.dim() != 2:
+        raise ValueError("expert must have shape [n, top_k]")
+    top_k = expert.shape[1]
+    _expect(expert, (n, top_k), "expert")
+    dgate = _typed(dgate, torch.float32, "dgate")
+    _expect(dgate, (n, top_k), "dgate")
+    _one_device(dev, expert=expert, dgate=dgate, status=status)
+    dlogits = _result(out, (n, experts), logits.dtype, dev, "out")
+    code = _launch(dev, lib().spc_route_bwd, dgate.data_ptr(), logits.data_ptr(), expert.data_ptr(), n, experts, top_k, score,
+                   bool(renorm), scale, _DTYPES[logits.dtype], dlogits.data_ptr(), _status(status))
+    _check(code, "spc_route_bwd")
+    return dlogits
+
+
+def _attention_args(q, k, v, seg, seg_k, scale):
+    q, ldq = _head_rows(q, "q")
+    (nq, hq, d), dev = q.shape, q.device
+    k, ldk = _head_rows(k if k.dtype is q.dtype else k.to(q.dtype), "k")
+    nk, hk = k.shape[:2]
+    _expect(k, (nk, hk, d), "k")
+    v, ldv = _head_rows(v if v.dtype is q.dtype else v.to(q.dtype), "v")
+    _expect(v, (nk, hk, d), "v")
+    seg = _typed(seg, torch.int32, "seg")
+    if seg.dim() != 1 or seg.shape[0] < 2:
+        raise ValueError("seg must hold segments + 1 offsets")
+    if seg_k is None:
+        if nk != nq:
+            raise ValueError("without seg_k there are as many keys as queries")
+        seg_k = seg
+    else:
+        seg_k = _typed(seg_k, torch.int32, "seg_k")
+        _expect(seg_k, seg.shape, "seg_k")
+    _one_device(dev, k=k, v=v, seg=seg, seg_k=seg_k)
+    return q, ldq, k, ldk, v, ldv, seg, seg_k, nq, nk, hq, hk, d, d ** -0.5 if scale is None else scale, dev
+
+
+def spc_attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seg: torch.Tensor,
+                      seg_k: Optional[torch.Tensor] = None, scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                      lse: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                      ws: Optional[torch.Tensor] = None):
+    """Attention of each query to the keys of its own segment: (o [nq, hq, d], lse [nq, hq] fp32).
+
+    q [nq, hq, d]; k, v [nk, hk, d], hk dividing hq (query head h reads key head h // (hq // hk)); slices of a
+    projection's rows are read in place.  `seg` [segments + 1] int32 holds the offsets of the queries'
+    segments, `seg_k` those of the keys (None: the same rows).  scale None: d^-0.5.  A query without keys
+    gives 0 and lse -inf.  Pass `out`, `lse` and `ws` to call without allocating."""
+    q, ldq, k, ldk, v, ldv, seg, seg_k, nq, nk, hq, hk, d, scale, dev = _attention_args(q, k, v, seg, seg_k, scale)
+    _one_device(dev, ws=ws, status=status)
+    o, ldo = _head_result(out, (nq, hq, d), q.dtype, dev, "out")
+    lse = _result(lse, (nq, hq), torch.float32, dev, "lse")
+    L, dt, segments = lib(), _DTYPES[q.dtype], seg.shape[0] - 1
+    nbytes = _launch_size(dev, L.spc_attention_workspace_size, nq, nk, segments, hq, hk, d, dt, 0)
+    if nbytes or ws is not None:
+        ws = _room(ws, nbytes, dev)
+    code = _launch(dev, L.spc_attention_fwd, q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, seg.data_ptr(),
+                   seg_k.data_ptr(), segments, nq, nk, hq, hk, d, scale, dt, o.data_ptr(), ldo, lse.data_ptr(),
+                   _status(status), _ptr(ws), 0 if ws is None else ws.numel())
+    _check(code, "spc_attention_fwd")
+    return o, lse
+
+
+def spc_attention_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
+                      lse: torch.Tensor, seg: torch.Tensor, seg_k: Optional[torch.Tensor] = None,
+                      scale: Optional[float] = None, dq: Optional[torch.Tensor] = None, dk: Optional[torch.Tensor] = None,
+                      dv: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                      ws: Optional[torch.Tensor] = None):
+    """Gradients of spc_attention_fwd: (dq [nq, hq, d], dk, dv [nk, hk, d]).  `o` and `lse` come from the forward
+    call.  `dq`, `dk` and `dv` may be slices of one gradient of the projection's rows."""
+    q, ldq, k, ldk, v, ldv, seg, seg_k, nq, nk, hq, hk, d, scale, dev = _attention_args(q, k, v, seg, seg_k, scale)
+    dout, lddo = _head_rows(dout if dout.dtype is q.dtype else dout.to(q.dtype), "dout")
+    _expect(dout, (nq, hq, d), "dout")
+    o, ldo = _head_rows(o if o.dtype is q.dtype else o.to(q.dtype), "o")
+    _expect(o, (nq, hq, d), "o")
+    lse, lse_p = _optional(lse, torch.float32, (nq, hq), "lse")
+    _one_device(dev, dout=dout, o=o, lse=lse, ws=ws, status=status)
+    dq, lddq = _head_result(dq, (nq, hq, d), q.dtype, dev, "dq")
+    dk, lddk = _head_result(dk, (nk, hk, d), q.dtype, dev, "dk")
+    dv, lddv = _head_result(dv, (nk, hk, d), q.dtype, dev, "dv")
+    L, dt, segments = lib(), _DTYPES[q.dtype], seg.shape[0] - 1
+    ws = _room(ws, _launch_size(dev, L.spc_attention_workspace_size, nq, nk, segments, hq, hk, d, dt, 1), dev)
+    code = _launch(dev, L.spc_attention_bwd, dout.data_ptr(), lddo, q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv,
+                   o.data_ptr(), ldo, lse_p, seg.data_ptr(), seg_k.data_ptr(), segments, nq, nk, hq, hk, d, scale, dt,
+                   dq.data_ptr(), lddq, dk.data_ptr(), lddk, dv.data_ptr(), lddv, _status(status), ws.data_ptr(), ws.numel())
+    _check(code, "spc_attention_bwd")
+    return dq, dk, dv

@@ -1,0 +1,265 @@
+// attention.cu -- attention over segments: which kernels take a call, how it is split, and the small kernels around
+// the large ones: the joins of split results and the backward pass' row sums.
+#include "attention.cuh"
+#include "pairs.cuh"
+
+namespace spc {
+
+namespace {
+
+constexpr int kBlock = 256;
+
+// Splits along the other axis: few tiles leave SMs idle, so each tile's walk is cut until there are two blocks an
+// SM, in shares of at least `least` rows of an axis of n_other.
+int splits_for(int64_t n, int32_t segments, int64_t heads, int64_t n_other, int rows, int least)
+{
+    const int64_t tiles = std::max<int64_t>(1, std::max<int64_t>(ceil_div(n, rows), std::min<int64_t>(n, segments))) * heads;
+    const int64_t wanted = 2 * (int64_t)sm_count() / tiles;
+    return (int)std::max<int64_t>(1, std::min<int64_t>(wanted, ceil_div(n_other, least)));
+}
+
+constexpr int kTileRows = 64, kLeastShare = 256;
+
+struct Layout {
+    int32_t splits, splits_kv;
+    size_t part, part_lse, part_kv, delta, most, bytes;
+};
+
+Layout layout(int64_t nq, int64_t nk, int32_t segments, int32_t hq, int32_t hk, int32_t d, bool backward)
+{
+    Layout l = {};
+    l.splits = splits_for(nq, segments, hq, nk, kTileRows, kLeastShare);
+    l.splits_kv = backward ? splits_for(nk, segments, hk, nq * (hq / hk), kTileRows, kLeastShare) : 1;
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t here = at;
+        at += align_up(bytes, 256);
+        return here;
+    };
+    const size_t rows = (size_t)nq * hq;
+    if (l.splits > 1) {
+        l.part = take(rows * l.splits * d * 4);
+        l.part_lse = take(backward ? 0 : rows * l.splits * 4);
+    }
+    if (backward) {
+        if (l.splits_kv > 1) l.part_kv = take((size_t)nk * hk * d * 4 * 2 * l.splits_kv);
+        l.delta = take(rows * 4);
+        l.most = take(16);
+    }
+    l.bytes = at;
+    return l;
+}
+
+// o and lse from the splits': weights exp(lse_z - lse).  A warp to a row and head.
+template <typename T>
+__global__ void __launch_bounds__(kBlock)
+k_attn_join(AttnArgs a)
+{
+    wait_for_kernel_before();
+    const int64_t i = (int64_t)blockIdx.x * (kBlock / 32) + threadIdx.x / 32, rows = a.nq * a.hq;
+    const int lane = threadIdx.x & 31;
+    if (i >= rows) return;
+    float most = -INFINITY;
+    for (int z = lane; z < a.splits; z += 32) most = fmaxf(most, fetch(a.part_lse + z * rows + i));
+#pragma unroll
+    for (int o = 16; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(FULL_MASK, most, o));
+    float total = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
+    // an infinite or NaN sum is one split's: its weight is 1, so that it reaches the result
+    for (int z = 0; z < a.splits; ++z) {
+        const float l = fetch(a.part_lse + z * rows + i);
+        if (l == -INFINITY) continue;
+        const float w = l == most ? 1.f : expf(l - most);
+        total += w;
+        const float* from = a.part + (z * rows + i) * a.d;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (lane + 32 * j < a.d) v[j] = fmaf(w, fetch(from + lane + 32 * j), v[j]);
+    }
+    const int64_t row = i / a.hq, head = i - row * a.hq;
+    T* to = static_cast<T*>(a.o) + row * a.ldo + head * a.d;
+    const float inv = total > 0.f || total != total ? 1.f / total : 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (lane + 32 * j < a.d) to[lane + 32 * j] = elem<T>::from_f32(v[j] * inv);
+    if (lane == 0) a.lse[i] = total > 0.f || total != total ? most + logf(total) : -INFINITY;
+}
+
+// Sums of the splits' gradients in order; rows of `width` values, at `ld` in the result.
+template <typename T>
+__global__ void __launch_bounds__(kBlock)
+k_attn_sum(const float* part, int splits, int64_t rows, int width, T* to, int64_t ld)
+{
+    wait_for_kernel_before();
+    const int64_t i = (int64_t)blockIdx.x * kBlock + threadIdx.x, all = rows * width;
+    if (i >= all) return;
+    float s = 0.f;
+    for (int z = 0; z < splits; ++z) s += fetch(part + z * all + i);
+    const int64_t row = i / width;
+    to[row * ld + (i - row * width)] = elem<T>::from_f32(s);
+}
+
+// delta = sum of do o over a head's channels: eight lanes to a row and head.  fp16 also takes the
+// largest norm of a row of do (for the scale of ds, see the gradient kernels).
+template <typename T, bool MOST>
+__global__ void __launch_bounds__(kBlock)
+k_attn_delta(AttnArgs a)
+{
+    wait_for_kernel_before();
+    const int64_t i = ((int64_t)blockIdx.x * kBlock + threadIdx.x) / 8, rows = a.nq * a.hq;
+    const int lane = threadIdx.x & 7;
+    float s = 0.f, most = 0.f;
+    if (i < rows) {
+        const int64_t row = i / a.hq, head = i - row * a.hq;
+        const T* o = static_cast<const T*>(a.o) + row * a.ldo + head * a.d;
+        const T* g = static_cast<const T*>(a.dout) + row * a.lddo + head * a.d;
+        constexpr int V = 16 / sizeof(T);
+        if (a.d % V == 0 && a.ldo % V == 0 && a.lddo % V == 0 && ((uintptr_t)a.o | (uintptr_t)a.dout) % 16 == 0) {
+            for (int c = lane * V; c < a.d; c += 8 * V) {
+                const Vec<T, V> x = *reinterpret_cast<const Vec<T, V>*>(o + c), y = *reinterpret_cast<const Vec<T, V>*>(g + c);
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const float u = elem<T>::to_f32(y.e[j]);
+                    s = fmaf(elem<T>::to_f32(x.e[j]), u, s);
+                    if (MOST) most = fmaf(u, u, most);
+                }
+            }
+        } else {
+            for (int c = lane; c < a.d; c += 8) {
+                const float u = elem<T>::to_f32(g[c]);
+                s = fmaf(elem<T>::to_f32(o[c]), u, s);
+                if (MOST) most = fmaf(u, u, most);
+            }
+        }
+    }
+#pragma unroll
+    for (int o = 4; o; o >>= 1) {
+        s += __shfl_xor_sync(FULL_MASK, s, o);
+        if (MOST) most += __shfl_xor_sync(FULL_MASK, most, o);
+    }
+    if (i < rows && lane == 0) a.delta[i] = s;
+    if (MOST) {
+        // non-negative floats are ordered as their bits are; the largest does not depend on the order
+        const uint32_t b = __reduce_max_sync(FULL_MASK, __float_as_uint(most));
+        if ((threadIdx.x & 31) == 0) atomicMax(a.most, b);
+    }
+}
+
+// fp16: the largest norm of a row of v.
+__global__ void __launch_bounds__(kBlock)
+k_attn_most_v(AttnArgs a)
+{
+    wait_for_kernel_before();
+    const int64_t i = ((int64_t)blockIdx.x * kBlock + threadIdx.x) / 8, rows = a.nk * a.hk;
+    const int lane = threadIdx.x & 7;
+    float most = 0.f;
+    if (i < rows) {
+        const int64_t row = i / a.hk, head = i - row * a.hk;
+        const __half* v = static_cast<const __half*>(a.v) + row * a.ldv + head * a.d;
+        for (int c = lane * 8; c < a.d; c += 64) {
+            const Vec<__half, 8> x = *reinterpret_cast<const Vec<__half, 8>*>(v + c);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) most = fmaf(__half2float(x.e[j]), __half2float(x.e[j]), most);
+        }
+    }
+#pragma unroll
+    for (int o = 4; o; o >>= 1) most += __shfl_xor_sync(FULL_MASK, most, o);
+    const uint32_t b = __reduce_max_sync(FULL_MASK, __float_as_uint(most));
+    if ((threadIdx.x & 31) == 0) atomicMax(a.most + 1, b);
+}
+
+template <typename T>
+spc_status join_fwd(const AttnArgs& a, cudaStream_t st)
+{
+    const int64_t blocks = ceil_div(a.nq * a.hq, kBlock / 32);
+    if (blocks > INT32_MAX) return SPC_ERR_UNSUPPORTED;
+    return attn_start_kernel<k_attn_join<T>>(dim3((unsigned)blocks), kBlock, 0, st, a);
+}
+
+template <typename T>
+spc_status sum(const float* part, int splits, int64_t rows, int width, void* to, int64_t ld, cudaStream_t st)
+{
+    const int64_t blocks = ceil_div(rows * width, kBlock);
+    if (blocks > INT32_MAX) return SPC_ERR_UNSUPPORTED;
+    return attn_start_kernel<k_attn_sum<T>>(dim3((unsigned)blocks), kBlock, 0, st, part, splits, rows, width, static_cast<T*>(to), ld);
+}
+
+template <typename T>
+spc_status join_bwd(const AttnArgs& a, cudaStream_t st)
+{
+    spc_status s = SPC_OK;
+    if (a.splits > 1) s = sum<T>(a.part, a.splits, a.nq, a.hq * a.d, a.dq, a.lddq, st);
+    if (s == SPC_OK && a.splits_kv > 1) {
+        const int64_t all = a.nk * a.hk * a.d;
+        s = sum<T>(a.part_kv, a.splits_kv, a.nk, a.hk * a.d, a.dk, a.lddk, st);
+        if (s == SPC_OK) s = sum<T>(a.part_kv + all * a.splits_kv, a.splits_kv, a.nk, a.hk * a.d, a.dv, a.lddv, st);
+    }
+    return s;
+}
+
+template <typename T>
+spc_status row_sums(const AttnArgs& a, bool most, cudaStream_t st)
+{
+    const int64_t blocks = ceil_div(a.nq * a.hq * 8, kBlock);
+    if (blocks == 0) return SPC_OK;
+    if (blocks > INT32_MAX) return SPC_ERR_UNSUPPORTED;
+    if constexpr (std::is_same<T, __half>::value) {
+        if (most) {
+            SPC_CUDA_TRY(cudaMemsetAsync(a.most, 0, 8, st));
+            const int64_t kv = ceil_div(a.nk * a.hk * 8, kBlock);
+            if (kv > INT32_MAX) return SPC_ERR_UNSUPPORTED;
+            spc_status s = attn_start_kernel<k_attn_most_v>(dim3((unsigned)kv), kBlock, 0, st, a);
+            return s != SPC_OK ? s : attn_start_kernel<k_attn_delta<T, true>>(dim3((unsigned)blocks), kBlock, 0, st, a);
+        }
+    }
+    return attn_start_kernel<k_attn_delta<T, false>>(dim3((unsigned)blocks), kBlock, 0, st, a);
+}
+
+}  // namespace
+
+size_t attention_ws_bytes(int64_t nq, int64_t nk, int32_t segments, int32_t hq, int32_t hk, int32_t d, bool backward)
+{
+    return layout(nq, nk, segments, hq, hk, d, backward).bytes;
+}
+
+void attention_plan(AttnArgs& a, void* ws, bool backward)
+{
+    const Layout l = layout(a.nq, a.nk, a.segments, a.hq, a.hk, a.d, backward);
+    uint8_t* base = static_cast<uint8_t*>(ws);
+    a.splits = l.splits;
+    a.splits_kv = l.splits_kv;
+    a.part = reinterpret_cast<float*>(base + l.part);
+    a.part_lse = reinterpret_cast<float*>(base + l.part_lse);
+    a.part_kv = reinterpret_cast<float*>(base + l.part_kv);
+    a.delta = reinterpret_cast<float*>(base + l.delta);
+    a.most = reinterpret_cast<uint32_t*>(base + l.most);
+}
+
+spc_status attention_fwd(const AttnArgs& a, spc_dtype dt, cudaStream_t st)
+{
+    if (a.nq == 0) return SPC_OK;
+    const spc_status s = attention_tc_supported(a, dt, false) ? attention_fwd_tc(a, dt, st) : attention_fwd_simt(a, dt, st);
+    if (s != SPC_OK || a.splits == 1) return s;
+    switch (dt) {
+    case SPC_F32: return join_fwd<float>(a, st);
+    case SPC_F16: return join_fwd<__half>(a, st);
+    default: return join_fwd<__nv_bfloat16>(a, st);
+    }
+}
+
+spc_status attention_bwd(const AttnArgs& a, spc_dtype dt, cudaStream_t st)
+{
+    if (a.nq == 0 && a.nk == 0) return SPC_OK;
+    const bool tc = attention_tc_supported(a, dt, true);
+    spc_status s = dt == SPC_F32   ? row_sums<float>(a, tc, st)
+                   : dt == SPC_F16 ? row_sums<__half>(a, tc, st)
+                                   : row_sums<__nv_bfloat16>(a, tc, st);
+    if (s == SPC_OK) s = tc ? attention_bwd_tc(a, dt, st) : attention_bwd_simt(a, dt, st);
+    if (s != SPC_OK) return s;
+    switch (dt) {
+    case SPC_F32: return join_bwd<float>(a, st);
+    case SPC_F16: return join_bwd<__half>(a, st);
+    default: return join_bwd<__nv_bfloat16>(a, st);
+    }
+}
+
+}  // namespace spc

@@ -1,0 +1,535 @@
+// layer_norm.cu -- y = gamma (x - mean) rstd + beta with the statistics of each row, and its gradients.
+//
+// A row is held in registers by a group of L threads (a part of a warp, a warp, or several warps), K vectors of V
+// channels to a thread (neighbours read as 16 bytes, or, where rows do not start on such a boundary, channels L
+// apart read one by one), so it is read once: the mean, then the sum of
+// squares around it, then the result.  In the backward pass a block keeps its channels for all of its rows,
+// so the sums over the rows (dgamma, dbeta) also stay in registers; a block's groups join in shared memory and
+// the blocks in a second, small kernel, always in the same order.
+//
+// Bound by memory: 16 operations stand against 4 to 8 bytes an element.  What has to be right is the number
+// of bytes in flight, so a group works on R rows at once.
+#include "layers.cuh"
+#include "pairs.cuh"
+
+namespace spc {
+
+namespace {
+
+constexpr int kFwdBlock = 256, kWideFwdBlock = 512;
+constexpr int kBwdBlock = 512;
+constexpr int kLongBlock = 512;
+constexpr int kJoinCols = 32, kJoinRows = 16;
+
+__device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// Sums of N values over the L threads of a group, in every thread.  Groups of more than a warp meet at a named
+// barrier and pass their warps' sums through `box` (16 warps x N floats, double-buffered by `turn`).
+template <int N>
+__device__ __forceinline__ void group_sum(float (&v)[N], int L, float* box, int turn)
+{
+    for (int o = min(L, 32) >> 1; o; o >>= 1) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] += __shfl_xor_sync(FULL_MASK, v[j], o);
+    }
+    if (L > 32) {
+        const int warp = threadIdx.x >> 5, warps = L >> 5, group = threadIdx.x / L;
+        float* at = box + turn * (16 * N);
+        if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+            for (int j = 0; j < N; ++j) at[warp * N + j] = v[j];
+        }
+        asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(L) : "memory");
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = 0.f;
+        for (int w = group * warps; w < (group + 1) * warps; ++w) {
+#pragma unroll
+            for (int j = 0; j < N; ++j) v[j] += at[w * N + j];
+        }
+    }
+}
+
+// Which channels a thread holds: element j of its vector k.
+template <int V, bool WHOLE>
+struct Place {
+    int t, L, c;
+    __device__ __forceinline__ int at(int k, int j) const { return WHOLE ? (t + k * L) * V + j : (k * V + j) * L + t; }
+    __device__ __forceinline__ bool in(int k, int j) const { return at(k, j) < c; }
+};
+
+template <typename T, int V, bool WHOLE>
+__device__ __forceinline__ void load_row(const T* row, const Place<V, WHOLE>& w, int k, Vec<T, V>& v)
+{
+    if constexpr (WHOLE) {
+        if (w.in(k, 0)) v = *reinterpret_cast<const Vec<T, V>*>(row + w.at(k, 0));
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            if (w.in(k, j)) v.e[j] = row[w.at(k, j)];
+    }
+}
+
+// As pairs, zeros where the row has ended (or there is no row).
+template <typename T, int V, bool WHOLE>
+__device__ __forceinline__ void spread(const Vec<T, V>& v, const Place<V, WHOLE>& w, int k, bool there, F2 (&f)[V / 2])
+{
+    unpack<T, V>(v, f);
+#pragma unroll
+    for (int j = 0; j < V / 2; ++j) {
+        f[j].x = there && w.in(k, 2 * j) ? f[j].x : 0.f;
+        f[j].y = there && w.in(k, 2 * j + 1) ? f[j].y : 0.f;
+    }
+}
+
+template <typename T, int V, bool WHOLE>
+__device__ __forceinline__ void store_row(T* row, const Place<V, WHOLE>& w, int k, const F2 (&f)[V / 2])
+{
+    const Vec<T, V> v = pack<T, V>(f);
+    if constexpr (WHOLE) {
+        if (w.in(k, 0)) *reinterpret_cast<Vec<T, V>*>(row + w.at(k, 0)) = v;
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            if (w.in(k, j)) row[w.at(k, j)] = v.e[j];
+    }
+}
+
+template <int V, bool WHOLE>
+__device__ __forceinline__ void load_affine(const float* p, float other, const Place<V, WHOLE>& w, int k, F2 (&f)[V / 2])
+{
+#pragma unroll
+    for (int j = 0; j < V / 2; ++j) {
+        f[j].x = p && w.in(k, 2 * j) ? fetch(p + w.at(k, 2 * j)) : other;
+        f[j].y = p && w.in(k, 2 * j + 1) ? fetch(p + w.at(k, 2 * j + 1)) : other;
+    }
+}
+
+// R rows of a group at a time.
+template <typename T, int V, int K, int R, int BLOCK, bool WHOLE>
+__global__ void __launch_bounds__(BLOCK)
+k_layer_norm(LayerNormArgs a, int L)
+{
+    constexpr int H = V / 2;
+    __shared__ float box[2 * 16 * R];
+    wait_for_kernel_before();
+    let_next_kernel_start();
+    const Place<V, WHOLE> w{(int)threadIdx.x & (L - 1), L, a.c};
+    const int groups = BLOCK / L;
+    const int64_t row0 = ((int64_t)blockIdx.x * groups + threadIdx.x / L) * R;
+    const T* x = static_cast<const T*>(a.x);
+    Vec<T, V> raw[R][K];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (row0 + r < a.n) load_row<T, V, WHOLE>(x + (row0 + r) * a.c, w, k, raw[r][k]);
+    }
+    F2 f[R][K][H];
+    float sum[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        F2 s{0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            spread<T, V, WHOLE>(raw[r][k], w, k, row0 + r < a.n, f[r][k]);
+#pragma unroll
+            for (int j = 0; j < H; ++j) s = add(s, f[r][k][j]);
+        }
+        sum[r] = s.x + s.y;
+    }
+    group_sum<R>(sum, L, box, 0);
+    const float inv = 1.f / (float)a.c;
+    float mean[R], sq[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        mean[r] = sum[r] * inv;
+        F2 s{0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+#pragma unroll
+            for (int j = 0; j < H; ++j) {
+                f[r][k][j] = add(f[r][k][j], both(-mean[r]));
+                if (!w.in(k, 2 * j)) f[r][k][j].x = 0.f;
+                if (!w.in(k, 2 * j + 1)) f[r][k][j].y = 0.f;
+                s = fma(f[r][k][j], f[r][k][j], s);
+            }
+        }
+        sq[r] = s.x + s.y;
+    }
+    group_sum<R>(sq, L, box, 1);
+    T* y = static_cast<T*>(a.out);
+    float rstd[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        rstd[r] = 1.f / sqrtf(sq[r] * inv + a.eps);
+        if (w.t == 0 && row0 + r < a.n) {
+            a.mean[row0 + r] = mean[r];
+            a.rstd[row0 + r] = rstd[r];
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        F2 ga[H], be[H];
+        load_affine<V, WHOLE>(a.gamma, 1.f, w, k, ga);
+        load_affine<V, WHOLE>(a.beta, 0.f, w, k, be);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if (row0 + r >= a.n) break;
+#pragma unroll
+            for (int j = 0; j < H; ++j) f[r][k][j] = fma(mul(f[r][k][j], both(rstd[r])), ga[j], be[j]);
+            store_row<T, V, WHOLE>(y + (row0 + r) * a.c, w, k, f[r][k]);
+        }
+    }
+}
+
+// Persistent: a group takes R rows, the next R rows are read while these are worked on.
+// part [blocks][2][c]: each block's sums of dy xh and of dy.
+template <typename T, int V, int K, int R, bool WHOLE>
+__global__ void __launch_bounds__(kBwdBlock, 1)
+k_layer_norm_grad(LayerNormArgs a, int L, float* part)
+{
+    constexpr int H = V / 2;
+    extern __shared__ float joint[];  // [units][2][c]
+    __shared__ float box[2 * 16 * 2 * R];
+    wait_for_kernel_before();
+    let_next_kernel_start();
+    const Place<V, WHOLE> w{(int)threadIdx.x & (L - 1), L, a.c};
+    const int groups = kBwdBlock / L;
+    const T* x = static_cast<const T*>(a.x);
+    const T* dy = static_cast<const T*>(a.dy);
+    T* dx = static_cast<T*>(a.out);
+    const float inv = 1.f / (float)a.c;
+    F2 ga[K][H], dg[K][H], db[K][H];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        load_affine<V, WHOLE>(a.gamma, 1.f, w, k, ga[k]);
+#pragma unroll
+        for (int j = 0; j < H; ++j) dg[k][j] = db[k][j] = F2{0.f, 0.f};
+    }
+    Vec<T, V> xr[R][K], dr[R][K];
+    float mr[R], sr[R];
+    auto load = [&](int64_t row0) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const bool there = row0 + r < a.n;
+            mr[r] = there ? fetch(a.mean + row0 + r) : 0.f;
+            sr[r] = there ? fetch(a.rstd + row0 + r) : 0.f;
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (there) {
+                    load_row<T, V, WHOLE>(x + (row0 + r) * a.c, w, k, xr[r][k]);
+                    load_row<T, V, WHOLE>(dy + (row0 + r) * a.c, w, k, dr[r][k]);
+                }
+        }
+    };
+    const int64_t step = (int64_t)gridDim.x * groups * R;
+    // every group of a block makes the same number of turns, so that groups which share a warp's shuffles stay together
+    const int64_t first = (int64_t)blockIdx.x * groups * R;
+    const int64_t mine = (threadIdx.x / L) * R;
+    int turn = 0;
+    if (first < a.n) load(first + mine);
+    for (int64_t base = first; base < a.n; base += step) {
+        const int64_t row0 = base + mine;
+        F2 xh[R][K][H], u[R][K][H];
+        float s[2 * R], rs[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            F2 p{0.f, 0.f}, q{0.f, 0.f};
+            const bool there = row0 + r < a.n;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                F2 g[H];
+                spread<T, V, WHOLE>(xr[r][k], w, k, there, xh[r][k]);
+                spread<T, V, WHOLE>(dr[r][k], w, k, there, g);
+#pragma unroll
+                for (int j = 0; j < H; ++j) {
+                    // past the row's end dy is 0, and so is everything that this thread adds
+                    xh[r][k][j] = mul(add(xh[r][k][j], both(-mr[r])), both(sr[r]));
+                    if (!w.in(k, 2 * j)) xh[r][k][j].x = 0.f;
+                    if (!w.in(k, 2 * j + 1)) xh[r][k][j].y = 0.f;
+                    dg[k][j] = fma(g[j], xh[r][k][j], dg[k][j]);
+                    db[k][j] = add(db[k][j], g[j]);
+                    u[r][k][j] = mul(g[j], ga[k][j]);
+                    p = add(p, u[r][k][j]);
+                    q = fma(u[r][k][j], xh[r][k][j], q);
+                }
+            }
+            s[2 * r] = p.x + p.y;
+            s[2 * r + 1] = q.x + q.y;
+            rs[r] = sr[r];
+        }
+        if (base + step < a.n) load(base + step + mine);
+        group_sum<2 * R>(s, L, box, turn);
+        turn ^= 1;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if (row0 + r >= a.n) break;
+            const F2 am = both(-s[2 * r] * inv), bm = both(-s[2 * r + 1] * inv);
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+#pragma unroll
+                for (int j = 0; j < H; ++j) u[r][k][j] = mul(add(fma(xh[r][k][j], bm, u[r][k][j]), am), both(rs[r]));
+                store_row<T, V, WHOLE>(dx + (row0 + r) * a.c, w, k, u[r][k]);
+            }
+        }
+    }
+    // groups that share a warp first, then the units (warps, or groups of several) of the block
+    for (int o = L; o < 32; o <<= 1) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+#pragma unroll
+            for (int j = 0; j < H; ++j) {
+                dg[k][j].x += __shfl_xor_sync(FULL_MASK, dg[k][j].x, o);
+                dg[k][j].y += __shfl_xor_sync(FULL_MASK, dg[k][j].y, o);
+                db[k][j].x += __shfl_xor_sync(FULL_MASK, db[k][j].x, o);
+                db[k][j].y += __shfl_xor_sync(FULL_MASK, db[k][j].y, o);
+            }
+        }
+    }
+    const int width = max(L, 32), units = kBwdBlock / width, unit = threadIdx.x / width;
+    if ((threadIdx.x & (width - 1)) < L) {
+        float* at = joint + (int64_t)unit * 2 * a.c;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                if (w.in(k, j)) {
+                    at[w.at(k, j)] = j & 1 ? dg[k][j / 2].y : dg[k][j / 2].x;
+                    at[a.c + w.at(k, j)] = j & 1 ? db[k][j / 2].y : db[k][j / 2].x;
+                }
+        }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * a.c; i += kBwdBlock) {
+        float s = 0.f;
+        for (int u = 0; u < units; ++u) s += joint[(int64_t)u * 2 * a.c + i];
+        part[(int64_t)blockIdx.x * 2 * a.c + i] = s;
+    }
+}
+
+// dgamma and dbeta: the blocks' sums, each thread a sixteenth of them, then those in order.
+__global__ void __launch_bounds__(kJoinCols * kJoinRows)
+k_layer_norm_join(const float* part, int blocks, int c, float* dgamma, float* dbeta)
+{
+    __shared__ float box[kJoinRows][kJoinCols + 1];
+    wait_for_kernel_before();
+    const int col = blockIdx.x * kJoinCols + threadIdx.x % kJoinCols, row = threadIdx.x / kJoinCols;
+    float s = 0.f;
+    if (col < 2 * c)
+        for (int b = row; b < blocks; b += kJoinRows) s += fetch(part + (int64_t)b * 2 * c + col);
+    box[row][threadIdx.x % kJoinCols] = s;
+    __syncthreads();
+    if (row == 0 && col < 2 * c) {
+        s = 0.f;
+#pragma unroll
+        for (int r = 0; r < kJoinRows; ++r) s += box[r][threadIdx.x];
+        float* out = col < c ? dgamma : dbeta;
+        if (out) out[col < c ? col : col - c] = s;
+    }
+}
+
+// ------------------------------------------------------------- rows that registers do not hold
+__device__ __forceinline__ float block_sum(float v, float* box)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(FULL_MASK, v, o);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) box[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kLongBlock / 32; ++w) v += box[w];
+    return v;
+}
+
+// A block to a row, which it reads three times.
+template <typename T>
+__global__ void __launch_bounds__(kLongBlock)
+k_layer_norm_long(LayerNormArgs a)
+{
+    __shared__ float box[kLongBlock / 32];
+    wait_for_kernel_before();
+    const int64_t row = blockIdx.x;
+    const T* x = static_cast<const T*>(a.x) + row * a.c;
+    T* y = static_cast<T*>(a.out) + row * a.c;
+    float s = 0.f;
+    for (int i = threadIdx.x; i < a.c; i += kLongBlock) s += elem<T>::to_f32(x[i]);
+    const float mean = block_sum(s, box) / (float)a.c;
+    s = 0.f;
+    for (int i = threadIdx.x; i < a.c; i += kLongBlock) {
+        const float d = elem<T>::to_f32(x[i]) - mean;
+        s = fmaf(d, d, s);
+    }
+    const float rstd = 1.f / sqrtf(block_sum(s, box) / (float)a.c + a.eps);
+    for (int i = threadIdx.x; i < a.c; i += kLongBlock) {
+        const float z = (elem<T>::to_f32(x[i]) - mean) * rstd * (a.gamma ? fetch(a.gamma + i) : 1.f);
+        y[i] = elem<T>::from_f32(z + (a.beta ? fetch(a.beta + i) : 0.f));
+    }
+    if (threadIdx.x == 0) {
+        a.mean[row] = mean;
+        a.rstd[row] = rstd;
+    }
+}
+
+// Sums over a share of the rows, a thread to a channel (before dx, which may take dy's or x's place).
+template <typename T>
+__global__ void __launch_bounds__(kLongBlock)
+k_layer_norm_long_sums(LayerNormArgs a, float* part)
+{
+    wait_for_kernel_before();
+    const int64_t c = (int64_t)blockIdx.x * kLongBlock + threadIdx.x;
+    if (c >= a.c) return;
+    const int64_t share = (a.n + gridDim.y - 1) / gridDim.y, lo = share * blockIdx.y, hi = min(lo + share, a.n);
+    float g = 0.f, b = 0.f;
+    for (int64_t r = lo; r < hi; ++r) {
+        const float d = elem<T>::to_f32(static_cast<const T*>(a.dy)[r * a.c + c]);
+        const float xh = (elem<T>::to_f32(static_cast<const T*>(a.x)[r * a.c + c]) - fetch(a.mean + r)) * fetch(a.rstd + r);
+        g = fmaf(d, xh, g);
+        b += d;
+    }
+    part[(int64_t)blockIdx.y * 2 * a.c + c] = g;
+    part[(int64_t)blockIdx.y * 2 * a.c + a.c + c] = b;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kLongBlock)
+k_layer_norm_long_grad(LayerNormArgs a)
+{
+    __shared__ float box[kLongBlock / 32];
+    wait_for_kernel_before();
+    const int64_t row = blockIdx.x;
+    const T* x = static_cast<const T*>(a.x) + row * a.c;
+    const T* dy = static_cast<const T*>(a.dy) + row * a.c;
+    T* dx = static_cast<T*>(a.out) + row * a.c;
+    const float mean = fetch(a.mean + row), rstd = fetch(a.rstd + row);
+    float p = 0.f, q = 0.f;
+    for (int i = threadIdx.x; i < a.c; i += kLongBlock) {
+        const float u = elem<T>::to_f32(dy[i]) * (a.gamma ? fetch(a.gamma + i) : 1.f);
+        p += u;
+        q = fmaf(u, (elem<T>::to_f32(x[i]) - mean) * rstd, q);
+    }
+    p = block_sum(p, box) / (float)a.c;
+    q = block_sum(q, box) / (float)a.c;
+    for (int i = threadIdx.x; i < a.c; i += kLongBlock) {
+        const float u = elem<T>::to_f32(dy[i]) * (a.gamma ? fetch(a.gamma + i) : 1.f);
+        const float xh = (elem<T>::to_f32(x[i]) - mean) * rstd;
+        dx[i] = elem<T>::from_f32(rstd * (u - p - xh * q));
+    }
+}
+
+// ---------------------------------------------------------------------- host
+template <auto KERNEL, typename... A>
+spc_status start(dim3 grid, int block, size_t smem, cudaStream_t st, A... args)
+{
+    if (smem > 48 * 1024) {
+        const spc_status s = allow_smem<KERNEL>();
+        if (s != SPC_OK) return s;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1] = {beside_the_kernel_before()};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    SPC_CUDA_TRY(cudaLaunchKernelEx(&cfg, KERNEL, args...));
+    return SPC_OK;
+}
+
+int pow2_at_least(int64_t v)
+{
+    int p = 1;
+    while (p < v) p <<= 1;
+    return p;
+}
+
+// Threads to a row: as many as hold it with K vectors each.
+int lanes_for(int c, int per_thread) { return pow2_at_least(ceil_div(c, per_thread)); }
+
+template <typename T, int V, int K, int R, int BLOCK, bool WHOLE>
+spc_status fwd(const LayerNormArgs& a, cudaStream_t st)
+{
+    const int L = lanes_for(a.c, V * K);
+    const int64_t blocks = ceil_div(a.n, (int64_t)(BLOCK / L) * R);
+    if (blocks > INT32_MAX) return SPC_ERR_UNSUPPORTED;
+    return start<k_layer_norm<T, V, K, R, BLOCK, WHOLE>>(dim3((unsigned)blocks), BLOCK, 0, st, a, L);
+}
+
+// Rows that a warp holds with one vector a thread are taken four at once, with two vectors two at once; longer
+// rows take four vectors a thread and as many warps as they need.
+template <typename T, bool WHOLE>
+spc_status fwd_any(const LayerNormArgs& a, cudaStream_t st)
+{
+    constexpr int V = 16 / (int)sizeof(T);
+    if (a.c <= 32 * V) return fwd<T, V, 1, 4, kFwdBlock, WHOLE>(a, st);
+    if (a.c <= 64 * V) return fwd<T, V, 2, 2, kFwdBlock, WHOLE>(a, st);
+    if (a.c <= 4 * V * kWideFwdBlock) return fwd<T, V, 4, 1, kWideFwdBlock, WHOLE>(a, st);
+    if (a.n > INT32_MAX) return SPC_ERR_UNSUPPORTED;
+    return start<k_layer_norm_long<T>>(dim3((unsigned)a.n), kLongBlock, 0, st, a);
+}
+
+constexpr int kMostLongShares = 256, kBwdPer = 16;  // channels of a thread in the backward pass, at most
+
+template <typename T, int V, int K, int R, bool WHOLE>
+spc_status bwd(const LayerNormArgs& a, float* part, int* blocks, cudaStream_t st)
+{
+    const int L = lanes_for(a.c, V * K), units = kBwdBlock / std::max(L, 32);
+    *blocks = (int)std::min<int64_t>(sm_count(), ceil_div(a.n, (int64_t)(kBwdBlock / L) * R));
+    return start<k_layer_norm_grad<T, V, K, R, WHOLE>>(dim3((unsigned)*blocks), kBwdBlock, (size_t)units * 2 * a.c * 4, st, a, L,
+                                                       part);
+}
+
+template <typename T, bool WHOLE>
+spc_status bwd_any(const LayerNormArgs& a, float* part, cudaStream_t st)
+{
+    constexpr int V = 16 / (int)sizeof(T), K = kBwdPer / V;
+    int blocks = 0;
+    spc_status s = SPC_OK;
+    if (a.n > 0) {
+        if (a.c <= 32 * V) {
+            s = bwd<T, V, 1, 2, WHOLE>(a, part, &blocks, st);
+        } else if (a.c <= kBwdPer * kBwdBlock) {
+            s = bwd<T, V, K, 1, WHOLE>(a, part, &blocks, st);
+        } else {
+            if (a.n > INT32_MAX) return SPC_ERR_UNSUPPORTED;
+            blocks = (int)std::min<int64_t>(kMostLongShares, a.n);
+            s = start<k_layer_norm_long_sums<T>>(dim3((unsigned)ceil_div(a.c, kLongBlock), (unsigned)blocks), kLongBlock, 0, st,
+                                                 a, part);
+            if (s == SPC_OK) s = start<k_layer_norm_long_grad<T>>(dim3((unsigned)a.n), kLongBlock, 0, st, a);
+        }
+    }
+    if (s != SPC_OK || (!a.dgamma && !a.dbeta)) return s;
+    return start<k_layer_norm_join>(dim3((unsigned)ceil_div(2 * (int64_t)a.c, kJoinCols)), kJoinCols * kJoinRows, 0, st,
+                                    (const float*)part, blocks, (int)a.c, a.dgamma, a.dbeta);
+}
+
+template <typename T>
+spc_status any(const LayerNormArgs& a, float* part, bool backward, cudaStream_t st)
+{
+    // 16-byte vectors where rows and tensors start on such a boundary
+    const bool whole = a.c % (16 / (int)sizeof(T)) == 0 && aligned16(a.x) && aligned16(a.out) && aligned16(a.dy);
+    if (backward) return whole ? bwd_any<T, true>(a, part, st) : bwd_any<T, false>(a, part, st);
+    return whole ? fwd_any<T, true>(a, st) : fwd_any<T, false>(a, st);
+}
+
+}  // namespace
+
+size_t layer_norm_ws_bytes(int64_t n, int32_t c)
+{
+    const int64_t most = c <= kBwdPer * kBwdBlock ? sm_count() : kMostLongShares;
+    return align_up((size_t)std::min<int64_t>(most, std::max<int64_t>(n, 1)) * 2 * c * 4, 256);
+}
+
+spc_status layer_norm(const LayerNormArgs& a, spc_dtype dt, void* ws, bool backward, cudaStream_t st)
+{
+    if (!backward && a.n == 0) return SPC_OK;
+    float* part = static_cast<float*>(ws);
+    switch (dt) {
+    case SPC_F32: return any<float>(a, part, backward, st);
+    case SPC_F16: return any<__half>(a, part, backward, st);
+    default: return any<__nv_bfloat16>(a, part, backward, st);
+    }
+}
+
+}  // namespace spc
