@@ -9,27 +9,35 @@ namespace {
 
 constexpr int kBlock = 256;
 
-// Splits along the other axis: few tiles leave SMs idle, so each tile's walk is cut until there are two blocks an
-// SM, in shares of at least `least` rows of an axis of n_other.
-int splits_for(int64_t n, int32_t segments, int64_t heads, int64_t n_other, int rows, int least)
+// Splits along the other axis: few tiles leave SMs idle, so each tile's walk is cut until there are `blocks` for
+// every SM, in shares of at least `least` rows of an axis of n_other.
+int splits_for(int64_t n, int32_t segments, int64_t heads, int64_t n_other, int rows, int least, int blocks)
 {
     const int64_t tiles = std::max<int64_t>(1, std::max<int64_t>(ceil_div(n, rows), std::min<int64_t>(n, segments))) * heads;
-    const int64_t wanted = 2 * (int64_t)sm_count() / tiles;
+    const int64_t wanted = blocks * (int64_t)sm_count() / tiles;
     return (int)std::max<int64_t>(1, std::min<int64_t>(wanted, ceil_div(n_other, least)));
 }
 
-constexpr int kTileRows = 64, kLeastShare = 256;
+constexpr int kSimtRows = 64, kLeastShare = 256;
+
+bool wide_enough(int32_t d, spc_dtype dt) { return dt != SPC_F32 && d % 8 == 0; }
 
 struct Layout {
     int32_t splits, splits_kv;
     size_t part, part_lse, part_kv, delta, most, bytes;
 };
 
-Layout layout(int64_t nq, int64_t nk, int32_t segments, int32_t hq, int32_t hk, int32_t d, bool backward)
+Layout layout(int64_t nq, int64_t nk, int32_t segments, int32_t hq, int32_t hk, int32_t d, spc_dtype dt, bool backward)
 {
     Layout l = {};
-    l.splits = splits_for(nq, segments, hq, nk, kTileRows, kLeastShare);
-    l.splits_kv = backward ? splits_for(nk, segments, hk, nq * (hq / hk), kTileRows, kLeastShare) : 1;
+    const bool tc = wide_enough(d, dt);
+    if (tc && !backward) {
+        const AttnShape f = attn_shape(nq, segments, hq, hk);
+        l.splits = splits_for(nq, segments, hq / f.heads, nk, f.positions * f.tiles, kLeastShare, f.tiles == 2 ? 1 : 2);
+    } else {
+        l.splits = splits_for(nq, segments, hq, nk, kSimtRows, kLeastShare, 2);
+    }
+    l.splits_kv = backward ? splits_for(nk, segments, hk, nq * (hq / hk), kSimtRows, kLeastShare, 2) : 1;
     size_t at = 0;
     auto take = [&](size_t bytes) {
         const size_t here = at;
@@ -216,14 +224,40 @@ spc_status row_sums(const AttnArgs& a, bool most, cudaStream_t st)
 
 }  // namespace
 
-size_t attention_ws_bytes(int64_t nq, int64_t nk, int32_t segments, int32_t hq, int32_t hk, int32_t d, bool backward)
+// The query heads of a tile: as many of those that share a key head as divide them and leave a tile two positions.
+// Two tiles to a block where a segment has rows for them and the halved number of blocks still fills the SMs.
+AttnShape attn_shape(int64_t nq, int32_t segments, int32_t hq, int32_t hk)
 {
-    return layout(nq, nk, segments, hq, hk, d, backward).bytes;
+    AttnShape f;
+    const int per = hq / hk;
+    f.heads = 1;
+    for (int g = 2; g <= std::min(per, 64); ++g)
+        if (per % g == 0) f.heads = g;
+    f.positions = 128 / f.heads;
+    const bool long_enough = nq / segments >= 2 * f.positions - f.positions / 2;
+    const int64_t blocks = ceil_div(nq, 2 * f.positions) * (hq / f.heads);
+    f.tiles = long_enough && blocks >= sm_count() ? 2 : 1;
+    return f;
 }
 
-void attention_plan(AttnArgs& a, void* ws, bool backward)
+bool attention_tc_supported(const AttnArgs& a, spc_dtype dt, bool backward)
 {
-    const Layout l = layout(a.nq, a.nk, a.segments, a.hq, a.hk, a.d, backward);
+    const uintptr_t low = reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v) |
+                          reinterpret_cast<uintptr_t>(a.o);
+    // TMA rows start on 16-byte boundaries; an empty tensor has no map
+    if (!wide_enough(a.d, dt) || a.nq == 0 || a.nk == 0 || low % 16 || (a.ldq | a.ldk | a.ldv | a.ldo) % 8) return false;
+    if (backward) return false;
+    return true;
+}
+
+size_t attention_ws_bytes(int64_t nq, int64_t nk, int32_t segments, int32_t hq, int32_t hk, int32_t d, spc_dtype dt, bool backward)
+{
+    return layout(nq, nk, segments, hq, hk, d, dt, backward).bytes;
+}
+
+void attention_plan(AttnArgs& a, spc_dtype dt, void* ws, bool backward)
+{
+    const Layout l = layout(a.nq, a.nk, a.segments, a.hq, a.hk, a.d, dt, backward);
     uint8_t* base = static_cast<uint8_t*>(ws);
     a.splits = l.splits;
     a.splits_kv = l.splits_kv;
@@ -237,7 +271,8 @@ void attention_plan(AttnArgs& a, void* ws, bool backward)
 spc_status attention_fwd(const AttnArgs& a, spc_dtype dt, cudaStream_t st)
 {
     if (a.nq == 0) return SPC_OK;
-    const spc_status s = attention_tc_supported(a, dt, false) ? attention_fwd_tc(a, dt, st) : attention_fwd_simt(a, dt, st);
+    spc_status s = attention_tc_supported(a, dt, false) ? attention_fwd_tc(a, dt, st) : SPC_ERR_UNSUPPORTED;
+    if (s == SPC_ERR_UNSUPPORTED) s = attention_fwd_simt(a, dt, st);  // strides that no tensor map holds, too
     if (s != SPC_OK || a.splits == 1) return s;
     switch (dt) {
     case SPC_F32: return join_fwd<float>(a, st);

@@ -101,10 +101,17 @@ __device__ __forceinline__ void attn_share(int64_t lo, int64_t hi, int per, int 
 }
 
 // ---------------------------------------------------------------- host side
+// How the tensor-core forward kernel lays out queries: `heads` of the query heads that share a key head stand in
+// one tile of 128 rows with `positions` positions, and a block has `tiles` such tiles.
+struct AttnShape {
+    int heads, positions, tiles;
+};
+AttnShape attn_shape(int64_t nq, int32_t segments, int32_t hq, int32_t hk);
+
 // Kernels for 16-bit heads of a multiple of 8 channels, up to 128, on 16-byte boundaries.
 bool attention_tc_supported(const AttnArgs& a, spc_dtype dt, bool backward);
-size_t attention_ws_bytes(int64_t nq, int64_t nk, int32_t segments, int32_t hq, int32_t hk, int32_t d, bool backward);
-void attention_plan(AttnArgs& a, void* ws, bool backward);
+size_t attention_ws_bytes(int64_t nq, int64_t nk, int32_t segments, int32_t hq, int32_t hk, int32_t d, spc_dtype dt, bool backward);
+void attention_plan(AttnArgs& a, spc_dtype dt, void* ws, bool backward);
 spc_status attention_fwd(const AttnArgs& a, spc_dtype dt, cudaStream_t st);
 spc_status attention_bwd(const AttnArgs& a, spc_dtype dt, cudaStream_t st);
 

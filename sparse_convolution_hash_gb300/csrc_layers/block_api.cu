@@ -162,7 +162,7 @@ size_t spc_attention_workspace_size(int64_t nq, int64_t nk, int32_t segments, in
                                     int32_t backward)
 {
     if (nq < 0 || nk < 0 || segments < 1 || hq < 1 || hk < 1 || hq % hk != 0 || d < 1 || d > 128 || !dtype_ok(dt)) return 0;
-    return attention_ws_bytes(nq, nk, segments, hq, hk, d, backward != 0);
+    return attention_ws_bytes(nq, nk, segments, hq, hk, d, dt, backward != 0);
 }
 
 spc_status spc_attention_fwd(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv,
@@ -176,9 +176,9 @@ spc_status spc_attention_fwd(const void* q, int64_t ldq, const void* k, int64_t 
     a.o = o, a.ldo = ldo, a.lse = lse, a.status = status;
     const spc_status s = check_attention(a, dt, false);
     if (s != SPC_OK) return s;
-    const size_t need = attention_ws_bytes(nq, nk, segments, hq, hk, d, false);
+    const size_t need = attention_ws_bytes(nq, nk, segments, hq, hk, d, dt, false);
     if (need && (!ws || !on(ws, 256) || ws_bytes < need)) return SPC_ERR_WORKSPACE;
-    attention_plan(a, ws, false);
+    attention_plan(a, dt, ws, false);
     return attention_fwd(a, dt, static_cast<cudaStream_t>(stream));
 }
 
@@ -195,9 +195,9 @@ spc_status spc_attention_bwd(const void* dout, int64_t lddo, const void* q, int6
     a.dout = dout, a.lddo = lddo, a.dq = dq, a.lddq = lddq, a.dk = dk, a.lddk = lddk, a.dv = dv, a.lddv = lddv;
     const spc_status s = check_attention(a, dt, true);
     if (s != SPC_OK) return s;
-    const size_t need = attention_ws_bytes(nq, nk, segments, hq, hk, d, true);
+    const size_t need = attention_ws_bytes(nq, nk, segments, hq, hk, d, dt, true);
     if (need && (!ws || !on(ws, 256) || ws_bytes < need)) return SPC_ERR_WORKSPACE;
-    attention_plan(a, ws, true);
+    attention_plan(a, dt, ws, true);
     return attention_bwd(a, dt, static_cast<cudaStream_t>(stream));
 }
 
