@@ -24,7 +24,7 @@ bool wide_enough(int32_t d, spc_dtype dt) { return dt != SPC_F32 && d % 8 == 0; 
 
 struct Layout {
     int32_t splits, splits_kv;
-    size_t part, part_lse, part_kv, delta, most, bytes;
+    size_t part, part_lse, part_kv, lse2, delta, most, bytes;
 };
 
 Layout layout(int64_t nq, int64_t nk, int32_t segments, int32_t hq, int32_t hk, int32_t d, spc_dtype dt, bool backward)
@@ -51,6 +51,7 @@ Layout layout(int64_t nq, int64_t nk, int32_t segments, int32_t hq, int32_t hk, 
     }
     if (backward) {
         if (l.splits_kv > 1) l.part_kv = take((size_t)nk * hk * d * 4 * 2 * l.splits_kv);
+        l.lse2 = take(rows * 4);
         l.delta = take(rows * 4);
         l.most = take(16);
     }
@@ -106,7 +107,7 @@ k_attn_sum(const float* part, int splits, int64_t rows, int width, T* to, int64_
     to[row * ld + (i - row * width)] = elem<T>::from_f32(s);
 }
 
-// delta = sum of do o over a head's channels: eight lanes to a row and head.  fp16 also takes the
+// minus the sum of do o over a head's channels, and minus lse to base 2: eight lanes to a row and head.  fp16 also takes the
 // largest norm of a row of do (for the scale of ds, see the gradient kernels).
 template <typename T, bool MOST>
 __global__ void __launch_bounds__(kBlock)
@@ -144,10 +145,16 @@ k_attn_delta(AttnArgs a)
         s += __shfl_xor_sync(FULL_MASK, s, o);
         if (MOST) most += __shfl_xor_sync(FULL_MASK, most, o);
     }
-    if (i < rows && lane == 0) a.delta[i] = s;
+    if (i < rows && lane == 0) {
+        const int64_t row = i / a.hq, head = i - row * a.hq;
+        const float lse = fetch(a.lse + i);
+        a.delta[head * a.nq + row] = -s;
+        a.lse2[head * a.nq + row] = lse == -INFINITY ? -INFINITY : -lse * 1.44269504088896340736f;
+    }
     if (MOST) {
-        // non-negative floats are ordered as their bits are; the largest does not depend on the order
-        const uint32_t b = __reduce_max_sync(FULL_MASK, __float_as_uint(most));
+        // non-negative floats are ordered as their bits are; the largest does not depend on the order.  Rows that are
+        // not finite have no say (their results are not either)
+        const uint32_t b = __reduce_max_sync(FULL_MASK, most < INFINITY ? __float_as_uint(most) : 0u);
         if ((threadIdx.x & 31) == 0) atomicMax(a.most, b);
     }
 }
@@ -171,7 +178,7 @@ k_attn_most_v(AttnArgs a)
     }
 #pragma unroll
     for (int o = 4; o; o >>= 1) most += __shfl_xor_sync(FULL_MASK, most, o);
-    const uint32_t b = __reduce_max_sync(FULL_MASK, __float_as_uint(most));
+    const uint32_t b = __reduce_max_sync(FULL_MASK, most < INFINITY ? __float_as_uint(most) : 0u);
     if ((threadIdx.x & 31) == 0) atomicMax(a.most + 1, b);
 }
 
@@ -246,8 +253,10 @@ bool attention_tc_supported(const AttnArgs& a, spc_dtype dt, bool backward)
                           reinterpret_cast<uintptr_t>(a.o);
     // TMA rows start on 16-byte boundaries; an empty tensor has no map
     if (!wide_enough(a.d, dt) || a.nq == 0 || a.nk == 0 || low % 16 || (a.ldq | a.ldk | a.ldv | a.ldo) % 8) return false;
-    if (backward) return false;
-    return true;
+    if (!backward) return true;
+    const uintptr_t back = reinterpret_cast<uintptr_t>(a.dout) | reinterpret_cast<uintptr_t>(a.dq) | reinterpret_cast<uintptr_t>(a.dk) |
+                           reinterpret_cast<uintptr_t>(a.dv);
+    return back % 16 == 0 && (a.lddo | a.lddq | a.lddk | a.lddv) % 8 == 0;
 }
 
 size_t attention_ws_bytes(int64_t nq, int64_t nk, int32_t segments, int32_t hq, int32_t hk, int32_t d, spc_dtype dt, bool backward)
@@ -264,6 +273,7 @@ void attention_plan(AttnArgs& a, spc_dtype dt, void* ws, bool backward)
     a.part = reinterpret_cast<float*>(base + l.part);
     a.part_lse = reinterpret_cast<float*>(base + l.part_lse);
     a.part_kv = reinterpret_cast<float*>(base + l.part_kv);
+    a.lse2 = reinterpret_cast<float*>(base + l.lse2);
     a.delta = reinterpret_cast<float*>(base + l.delta);
     a.most = reinterpret_cast<uint32_t*>(base + l.most);
 }
@@ -288,7 +298,9 @@ spc_status attention_bwd(const AttnArgs& a, spc_dtype dt, cudaStream_t st)
     spc_status s = dt == SPC_F32   ? row_sums<float>(a, tc, st)
                    : dt == SPC_F16 ? row_sums<__half>(a, tc, st)
                                    : row_sums<__nv_bfloat16>(a, tc, st);
-    if (s == SPC_OK) s = tc ? attention_bwd_tc(a, dt, st) : attention_bwd_simt(a, dt, st);
+    if (s != SPC_OK) return s;
+    s = tc ? attention_bwd_tc(a, dt, st) : SPC_ERR_UNSUPPORTED;
+    if (s == SPC_ERR_UNSUPPORTED) s = attention_bwd_simt(a, dt, st);
     if (s != SPC_OK) return s;
     switch (dt) {
     case SPC_F32: return join_bwd<float>(a, st);

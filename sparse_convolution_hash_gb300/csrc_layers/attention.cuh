@@ -39,8 +39,9 @@ struct AttnArgs {
     float* part;              // [splits][nq][hq][d]: o (with part_lse) or dq
     float* part_lse;          // [splits][nq][hq]
     float* part_kv;           // [2][splits_kv][nk][hk][d]: dk, dv
-    float* delta;             // [nq][hq]: sum of do o
-    uint32_t* most;           // fp16: bits of the largest |do| and |v| rows' norms
+    float* lse2;              // [hq][nq]: minus lse, to base 2 (-inf for a query without keys: no probability)
+    float* delta;             // [hq][nq]: minus the sum of do o
+    uint32_t* most;           // fp16: bits of the largest squared norms of a row of do and of v
 };
 
 inline int64_t attn_slots(int64_t n, int32_t segments, int32_t rows) { return n / rows + segments + 2; }
@@ -123,7 +124,7 @@ spc_status attention_bwd_tc(const AttnArgs& a, spc_dtype dt, cudaStream_t st);
 template <auto KERNEL, typename... A>
 spc_status attn_start_kernel(dim3 grid, int block, size_t smem, cudaStream_t st, A... args)
 {
-    if (smem > 48 * 1024) {
+    if (smem > 32 * 1024) {  // 48 KB with the static part need no leave
         const spc_status s = allow_smem<KERNEL>();
         if (s != SPC_OK) return s;
     }

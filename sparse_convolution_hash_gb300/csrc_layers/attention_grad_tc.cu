@@ -1,0 +1,430 @@
+// attention_grad_tc.cu -- the gradients of attention over segments on the 5th-generation tensor cores: two kernels,
+// each of which keeps 128 rows of one side and walks over the other side's rows 64 at a time.
+//   dk, dv   keeps keys: S^T = K Q^T and dP^T = V dO^T, then dV += P^T dO and dK += dS^T Q;
+//   dq       keeps queries: S = Q K^T and dP = dO V^T, then dQ += dS K;
+// with P = exp(S - lse) and dS = P (dP - delta), written as 16 bits in the place of S and dP, a thread to a lane.
+// Seven products where five would do, were dq summed across blocks; but then its bits would hang on their order.
+//
+// Two steps are in work at any time, each with four warps and a quarter of tensor memory: while one's
+// probabilities are taken, the other's products run.
+//
+// fp16: P is kept times 2^14 and dS times a power of two for which the largest possible value, |P| <= 1 times
+// 2 max|do| max|v|, stays below 2^14, so small probabilities and gradients keep their digits.
+//
+// Waits are bounded as in the forward kernel.
+#include "attention_tc.cuh"
+
+namespace spc {
+
+namespace {
+
+constexpr int kStep = 64;  // rows of the streamed side
+
+template <int D>
+struct Shape {
+    static constexpr int kBoxes = D / 64;
+    static constexpr int kKept = 128 * 128 * kBoxes;      // bytes of the 128 rows that a block keeps
+    static constexpr int kHalf = kStep * 128 * kBoxes;    // bytes of a step's rows of one operand
+    static constexpr int kStage = 2 * kHalf;
+    static constexpr int kStages = D == 128 ? 4 : 6;
+    static constexpr int kThreads = 384;
+    static constexpr int kBars = 3 * kStages + 7;
+    static constexpr size_t kSmem = 1024 + 2 * (size_t)kKept + (size_t)kStages * (kStage + 2 * kStep * 4) + 8 * kBars + 16;
+};
+
+struct Scales {
+    float up;      // log2 of P's factor
+    float ds;      // factor of dS beside P's
+    float back_p;  // what undoes them in the sums of P and dS
+    float back_ds;
+};
+
+template <typename T>
+__device__ __forceinline__ Scales scales(const AttnArgs& a)
+{
+    if constexpr (!std::is_same<T, __half>::value) return Scales{0.f, 1.f, 1.f, 1.f};
+    else {
+        // do and v have these norms at most, and delta is a mean of such products
+        const float most = 2.f * sqrtf(__uint_as_float(fetch(a.most))) * sqrtf(__uint_as_float(fetch(a.most + 1)));
+        int e = 0;
+        if (most > 0.f && most < 3e38f) frexpf(most, &e);
+        e = min(max(e, -100), 100);
+        return Scales{14.f, ldexpf(1.f, -e), 0x1p-14f, ldexpf(1.f, e - 14)};
+    }
+}
+
+// 32 columns of probabilities and their gradients, as 16-bit pairs.  lse2 and delta of each column, or (COLUMN false)
+// one pair for the lane.
+template <typename T>
+__device__ __forceinline__ void grad32(const uint32_t (&s)[32], const uint32_t (&dp)[32], F2 c, const F2 (&minus_lse)[16], const F2 (&minus_delta)[16],
+                                       F2 ds_scale, uint32_t (&p)[16], uint32_t (&ds)[16])
+{
+#pragma unroll
+    for (int y = 0; y < 16; ++y) {
+        F2 e = fma(F2{__uint_as_float(s[2 * y]), __uint_as_float(s[2 * y + 1])}, c, minus_lse[y]);
+        e = F2{ptx::ex2(e.x), ptx::ex2(e.y)};
+        F2 g = add(F2{__uint_as_float(dp[2 * y]), __uint_as_float(dp[2 * y + 1])}, minus_delta[y]);
+        p[y] = pack2<T>(e.x, e.y);
+        if constexpr (std::is_same<T, __half>::value) g = mul(g, ds_scale);
+        g = mul(g, e);
+        ds[y] = pack2<T>(g.x, g.y);
+    }
+}
+
+// A row of `width` channels from tensor memory, 32 columns from x on in steps of `stride`, to T or fp32 parts.
+template <typename T>
+__device__ __forceinline__ void store_row(uint32_t at, int x0, int stride, int d, float mul, bool there, T* out, float* part)
+{
+#pragma unroll 1
+    for (int x = x0; x < d; x += stride) {
+        uint32_t v[32];
+        ptx::tmem_ld32(at + x, v);
+        ptx::tmem_ld_wait();
+        if (!there) continue;
+        if (part) {
+#pragma unroll
+            for (int y = 0; y < 32; y += 4)
+                if (x + y < d)
+                    *reinterpret_cast<float4*>(part + x + y) = make_float4(__uint_as_float(v[y]) * mul, __uint_as_float(v[y + 1]) * mul,
+                                                                           __uint_as_float(v[y + 2]) * mul, __uint_as_float(v[y + 3]) * mul);
+        } else {
+#pragma unroll
+            for (int y = 0; y < 32; y += 8) {
+                uint4 w;
+                w.x = pack2<T>(__uint_as_float(v[y]) * mul, __uint_as_float(v[y + 1]) * mul);
+                w.y = pack2<T>(__uint_as_float(v[y + 2]) * mul, __uint_as_float(v[y + 3]) * mul);
+                w.z = pack2<T>(__uint_as_float(v[y + 4]) * mul, __uint_as_float(v[y + 5]) * mul);
+                w.w = pack2<T>(__uint_as_float(v[y + 6]) * mul, __uint_as_float(v[y + 7]) * mul);
+                if (x + y < d) *reinterpret_cast<uint4*>(out + x + y) = w;
+            }
+        }
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void store_zeros(int x0, int stride, int d, bool there, T* out, float* part)
+{
+    if (!there) return;
+    for (int x = x0; x < d; x += stride)
+        for (int y = x; y < min(x + 32, d); y += 8) {
+            if (part) {
+                *reinterpret_cast<float4*>(part + y) = make_float4(0.f, 0.f, 0.f, 0.f);
+                *reinterpret_cast<float4*>(part + y + 4) = make_float4(0.f, 0.f, 0.f, 0.f);
+            } else {
+                *reinterpret_cast<uint4*>(out + y) = make_uint4(0u, 0u, 0u, 0u);
+            }
+        }
+}
+
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// KEYS: the kernel of dk and dv (keeps keys, walks over the queries of every head that shares them), else of dq.
+// grid: slots of 128 rows, heads of the kept side, splits
+template <typename T, int D, bool KEYS>
+__global__ void __launch_bounds__(Shape<D>::kThreads, 1)
+k_attn_grad_tc(AttnArgs a, uint64_t wait_ns, const __grid_constant__ CUtensorMap kept1, const __grid_constant__ CUtensorMap kept2,
+               const __grid_constant__ CUtensorMap step1, const __grid_constant__ CUtensorMap step2)
+{
+    using S = Shape<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    uint8_t* ring = smem + 2 * S::kKept;
+    float* stats = reinterpret_cast<float*>(ring + (size_t)S::kStages * S::kStage);  // [stages][2][kStep]: -lse log2 e, -delta
+    uint64_t* full = reinterpret_cast<uint64_t*>(stats + S::kStages * 2 * kStep);
+    uint64_t* empty = full + S::kStages;
+    uint64_t* ready = empty + S::kStages;
+    uint64_t* kept_full = ready + S::kStages;
+    uint64_t* drain = kept_full + 1;
+    uint64_t* s_full = drain + 1;
+    uint64_t* p_full = s_full + 2;
+    uint64_t* o_full = p_full + 2;
+    uint32_t* s_ctrl = reinterpret_cast<uint32_t*>(o_full + 1);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    wait_for_kernel_before();
+    const int32_t* seg = KEYS ? a.seg_k : a.seg_q;
+    const int64_t rows = KEYS ? a.nk : a.nq;
+    if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) attn_check(seg, a.segments, rows, a.status, tid, S::kThreads);
+    AttnTile t;
+    if (!attn_tile(seg, KEYS ? a.seg_q : a.seg_k, a.segments, rows, KEYS ? a.nq : a.nk, 128, blockIdx.x, t)) return;
+    const int per = a.hq / a.hk;
+    const int kept_head = blockIdx.y, splits = KEYS ? a.splits_kv : a.splits;
+    // steps [from, to) of all: KEYS, those of every query head, one head after the other
+    const int64_t steps_each = (t.hi - t.lo + kStep - 1) / kStep, all = steps_each * (KEYS ? per : 1);
+    const int64_t from = all * blockIdx.z / splits, to = all * (blockIdx.z + 1) / splits;
+    const int n = (int)(to - from);
+    auto step_head = [&](int j) { return KEYS ? kept_head * per + (int)((from + j) / steps_each) : kept_head / per; };
+    auto step_row = [&](int j) { return t.lo + (KEYS ? (from + j) % steps_each : from + j) * kStep; };
+
+    if (tid == 0) {
+        for (int s = 0; s < S::kStages; ++s) {
+            ptx::mbar_init(&full[s], 1);
+            ptx::mbar_init(&empty[s], 1);
+            ptx::mbar_init(&ready[s], 32);
+        }
+        ptx::mbar_init(kept_full, 1);
+        ptx::mbar_init(drain, 1);
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(&s_full[i], 1);
+            ptx::mbar_init(&p_full[i], 4);
+        }
+        ptx::mbar_init(o_full, 1);
+        ptx::mbar_init_fence();
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(s_ctrl, 512);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = s_ctrl[0], kept_base = ptx::smem_u32(smem), ring_base = ptx::smem_u32(ring);
+    // tensor memory: step buffers of 128 columns (S, dP), then the sums: dv and dk, or dq
+    const uint32_t sum1 = tmem + 256, sum2 = tmem + 256 + D;
+    bool ok = true;
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ loads
+        if (lane == 0 && n > 0) {
+            ptx::mbar_arrive_expect_tx(kept_full, 2 * S::kKept);
+            for (int b = 0; b < S::kBoxes; ++b) {
+                ptx::tma_load3d<1>(kept_base + b * 16384, &kept1, b * 64, kept_head, (int32_t)t.row, ptx::smem_u32(kept_full));
+                ptx::tma_load3d<1>(kept_base + S::kKept + b * 16384, &kept2, b * 64, kept_head, (int32_t)t.row, ptx::smem_u32(kept_full));
+            }
+            int it = 0;
+            for (; it < n; ++it) {
+                const int s = it % S::kStages;
+                if (it >= S::kStages) ok = ptx::mbar_wait(&empty[s], (it / S::kStages - 1) & 1, wait_ns);
+                if (!ok) break;
+                const uint32_t base = ring_base + (uint32_t)s * S::kStage, bar = ptx::smem_u32(&full[s]);
+                ptx::mbar_arrive_expect_tx(&full[s], S::kStage);
+                const int head = step_head(it), row = (int)step_row(it);
+                for (int b = 0; b < S::kBoxes; ++b) {
+                    ptx::tma_load3d<1>(base + b * (kStep * 128), &step1, b * 64, head, row, bar);
+                    ptx::tma_load3d<1>(base + S::kHalf + b * (kStep * 128), &step2, b * 64, head, row, bar);
+                }
+            }
+            if (!ok) set_status(a.status, SPC_ERR_TIMEOUT);
+            // what is in flight has to land before the block's shared memory goes
+            ptx::mbar_wait(kept_full, 0, kAttnDrainNs);
+            for (int j = it > S::kStages ? it - S::kStages : 0; j < it; ++j)
+                ptx::mbar_wait(&full[j % S::kStages], (j / S::kStages) & 1, kAttnDrainNs);
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------- MMAs
+        if (lane == 0 && n > 0) {
+            const int steps = (a.d + 15) / 16;
+            const uint32_t id_s = ptx::idesc_make(AttnFmt<T>::v, 128, kStep);
+            const uint32_t id_o = ptx::idesc_make(AttnFmt<T>::v, 128, steps * 16) | 1u << 16;
+            auto scores = [&](int j) {
+                const int s = j % S::kStages;
+                const uint32_t parity = (j / S::kStages) & 1;
+                ok = ptx::mbar_wait(&full[s], parity, wait_ns) && (!KEYS || ptx::mbar_wait(&ready[s], parity, wait_ns));
+                if (!ok) return;
+                ptx::tc_fence_after();
+                const uint32_t base = ring_base + (uint32_t)s * S::kStage, d = tmem + (j & 1) * 128;
+                attn_mma_ss(d, kept_base, 16384, base, kStep * 128, id_s, steps);
+                attn_mma_ss(d + 64, kept_base + S::kKept, 16384, base + S::kHalf, kStep * 128, id_s, steps);
+                ptx::mma_commit(&s_full[j & 1]);
+            };
+            ok = ptx::mbar_wait(kept_full, 0, wait_ns);
+            if (ok) scores(0);
+            if (ok && n > 1) scores(1);
+            for (int j = 0; j < n && ok; ++j) {
+                const int s = j % S::kStages;
+                ok = ptx::mbar_wait(&p_full[j & 1], (j >> 1) & 1, wait_ns);
+                if (!ok) break;
+                ptx::tc_fence_after();
+                const uint32_t base = ring_base + (uint32_t)s * S::kStage, p = tmem + (j & 1) * 128;
+                const uint64_t d1 = ptx::desc_mn_sw128(base, kStep * 128), d2 = ptx::desc_mn_sw128(base + S::kHalf, kStep * 128);
+#pragma unroll
+                for (int q = 0; q < kStep / 16; ++q) {
+                    if (KEYS) ptx::mma_f16_ts(sum1, p + q * 8, d2 + q * 128, id_o, (j | q) != 0);  // dV += P^T dO
+                }
+#pragma unroll
+                for (int q = 0; q < kStep / 16; ++q)  // dK += dS^T Q, dQ += dS K
+                    ptx::mma_f16_ts(KEYS ? sum2 : sum1, p + 64 + q * 8, d1 + q * 128, id_o, (j | q) != 0);
+                ptx::mma_commit(&empty[s]);
+                if (j + 2 < n) scores(j + 2);
+            }
+            if (ok) ptx::mma_commit(o_full);
+            else set_status(a.status, SPC_ERR_TIMEOUT);
+            ptx::mma_commit(drain);
+            ptx::mbar_wait(drain, 0, kAttnDrainNs);
+        }
+    } else if (warp == 2) {
+        // ------------------------------- the queries' log-sums and row sums, and rows past the segment's end
+        if (KEYS) {
+            int it = 0;
+            for (; it < n; ++it) {
+                const int s = it % S::kStages;
+                if (it >= S::kStages) ok = __all_sync(FULL_MASK, ptx::mbar_wait(&empty[s], (it / S::kStages - 1) & 1, wait_ns));
+                if (!ok) break;
+                const int64_t row = step_row(it), at = (int64_t)step_head(it) * a.nq + row;
+                const int valid = (int)min((int64_t)kStep, t.hi - row);
+                float* to_s = stats + s * 2 * kStep;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int i = lane + 32 * x;
+                    if (i < valid) {
+                        cp_async4(ptx::smem_u32(to_s + i), a.lse2 + at + i);
+                        cp_async4(ptx::smem_u32(to_s + kStep + i), a.delta + at + i);
+                    }
+                }
+                if (valid == kStep) {
+                    ptx::cp_async_arrive_noinc(&ready[s]);
+                } else {
+                    for (int i = valid + lane; i < kStep; i += 32) {
+                        to_s[i] = -INFINITY;  // no probability
+                        to_s[kStep + i] = 0.f;
+                    }
+                    ok = __all_sync(FULL_MASK, ptx::mbar_wait(&full[s], (it / S::kStages) & 1, wait_ns));
+                    if (!ok) break;
+                    const uint32_t base = ring_base + (uint32_t)s * S::kStage;
+                    attn_clear_rows<S::kBoxes>(base, kStep, valid, lane, 32);
+                    attn_clear_rows<S::kBoxes>(base + S::kHalf, kStep, valid, lane, 32);
+                    ptx::cp_async_wait_all();
+                    ptx::mbar_arrive(&ready[s]);
+                }
+            }
+            if (!ok && lane == 0) set_status(a.status, SPC_ERR_TIMEOUT);
+            ptx::cp_async_wait_all();
+        }
+    } else if (warp >= 4) {
+        // ------------------------------------------- probabilities, their gradients, results
+        const int b = (warp - 4) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+        const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+        const uint32_t s_at = tmem + lanes + b * 128;
+        const Scales sc = scales<T>(a);
+        const float c = a.scale * kLog2e;
+        const int64_t row = t.row + r;
+        const bool there = row < t.end;
+        float my_lse = -INFINITY, my_delta = 0.f;
+        if (!KEYS && there) {
+            my_lse = fetch(a.lse2 + (int64_t)kept_head * a.nq + row) + sc.up;
+            my_delta = fetch(a.delta + (int64_t)kept_head * a.nq + row);
+        }
+        for (int j = b; j < n; j += 2) {
+            const int s = j % S::kStages;
+            ok = ptx::mbar_wait(&s_full[b], (j >> 1) & 1, wait_ns);
+            if (KEYS) ok = ok && ptx::mbar_wait(&ready[s], (j / S::kStages) & 1, wait_ns);
+            ok = __all_sync(FULL_MASK, ok);
+            if (!ok) break;
+            ptx::tc_fence_after();
+            const float* st = stats + s * 2 * kStep;
+            const int64_t left = KEYS ? kStep : t.hi - step_row(j);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                uint32_t sv[32], dp[32], p[16], ds[16];
+                ptx::tmem_ld32(s_at + x * 32, sv);
+                ptx::tmem_ld32(s_at + 64 + x * 32, dp);
+                F2 ml[16], md[16];
+                if (KEYS) {
+#pragma unroll
+                    for (int y = 0; y < 8; ++y) {
+                        const float4 l4 = *reinterpret_cast<const float4*>(st + x * 32 + 4 * y), d4 = *reinterpret_cast<const float4*>(st + kStep + x * 32 + 4 * y);
+                        ml[2 * y] = F2{l4.x, l4.y};
+                        ml[2 * y + 1] = F2{l4.z, l4.w};
+                        if constexpr (std::is_same<T, __half>::value) {
+                            ml[2 * y] = add(ml[2 * y], both(sc.up));
+                            ml[2 * y + 1] = add(ml[2 * y + 1], both(sc.up));
+                        }
+                        md[2 * y] = F2{d4.x, d4.y};
+                        md[2 * y + 1] = F2{d4.z, d4.w};
+                    }
+                } else {
+#pragma unroll
+                    for (int y = 0; y < 16; ++y) {
+                        ml[y] = both(my_lse);
+                        md[y] = both(my_delta);
+                    }
+                }
+                ptx::tmem_ld_wait();
+                grad32<T>(sv, dp, both(c), ml, md, both(sc.ds), p, ds);
+                if (!KEYS && left < kStep) {
+#pragma unroll
+                    for (int y = 0; y < 16; ++y) {
+                        const int at = x * 32 + 2 * y;
+                        ds[y] &= (at < left ? 0x0000ffffu : 0u) | (at + 1 < left ? 0xffff0000u : 0u);
+                    }
+                }
+                // in the place of columns that have been read: 16 columns for every 32
+                if (KEYS) ptx::tmem_st16(s_at + x * 16, p);
+                ptx::tmem_st16(s_at + 64 + x * 16, ds);
+            }
+            ptx::tmem_st_wait();
+            if (!KEYS && left < kStep) {
+                ok = __all_sync(FULL_MASK, ptx::mbar_wait(&full[s], (j / S::kStages) & 1, wait_ns));
+                if (!ok) break;
+                attn_clear_rows<S::kBoxes>(ring_base + (uint32_t)s * S::kStage, kStep, (int)left, r, 128);
+            }
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&p_full[b]);
+        }
+        if (ok && n > 0) ok = __all_sync(FULL_MASK, ptx::mbar_wait(o_full, 0, wait_ns));
+        ptx::tc_fence_after();
+        if (!ok && lane == 0) set_status(a.status, SPC_ERR_TIMEOUT);
+        if (ok) {
+            if (KEYS) {
+                // the first four warps dv, the others dk
+                const int64_t width = (int64_t)a.hk * a.d, off = row * width + (int64_t)kept_head * a.d, one = a.nk * width;
+                T* out = b == 0 ? static_cast<T*>(a.dv) + row * a.lddv + (int64_t)kept_head * a.d
+                                : static_cast<T*>(a.dk) + row * a.lddk + (int64_t)kept_head * a.d;
+                float* part = splits > 1 ? a.part_kv + ((b == 0 ? splits : 0) + blockIdx.z) * one + off : nullptr;
+                if (n > 0) store_row<T>((b == 0 ? sum1 : sum2) + lanes, 0, 32, a.d, b == 0 ? sc.back_p : sc.back_ds * a.scale, there, out, part);
+                else store_zeros<T>(0, 32, a.d, there, out, part);
+            } else {
+                T* out = static_cast<T*>(a.dq) + row * a.lddq + (int64_t)kept_head * a.d;
+                float* part = splits > 1 ? a.part + ((blockIdx.z * a.nq + row) * a.hq + kept_head) * a.d : nullptr;
+                if (n > 0) store_row<T>(sum1 + lanes, 32 * b, 64, a.d, sc.back_ds * a.scale, there, out, part);
+                else store_zeros<T>(32 * b, 64, a.d, there, out, part);
+            }
+        }
+    }
+    __syncwarp();
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, 512);
+    }
+}
+
+template <typename T, int D, bool KEYS>
+spc_status launch(const AttnArgs& a, cudaStream_t st)
+{
+    using S = Shape<D>;
+    CUtensorMap q, g, k, v;
+    const int box_q = KEYS ? kStep : 128, box_k = KEYS ? 128 : kStep;
+    if (!attn_tmap<T>(&q, a.q, a.ldq, a.nq, a.hq, a.d, 1, box_q) || !attn_tmap<T>(&g, a.dout, a.lddo, a.nq, a.hq, a.d, 1, box_q) ||
+        !attn_tmap<T>(&k, a.k, a.ldk, a.nk, a.hk, a.d, 1, box_k) || !attn_tmap<T>(&v, a.v, a.ldv, a.nk, a.hk, a.d, 1, box_k))
+        return SPC_ERR_UNSUPPORTED;
+    const int64_t slots = attn_slots(KEYS ? a.nk : a.nq, a.segments, 128);
+    if (slots > INT32_MAX) return SPC_ERR_UNSUPPORTED;
+    const spc_status s = allow_smem<k_attn_grad_tc<T, D, KEYS>>();
+    if (s != SPC_OK) return s;
+    const dim3 grid((unsigned)slots, (unsigned)(KEYS ? a.hk : a.hq), (unsigned)(KEYS ? a.splits_kv : a.splits));
+    return KEYS ? attn_start_kernel<k_attn_grad_tc<T, D, KEYS>>(grid, S::kThreads, S::kSmem, st, a, wait_limit_ns(), k, v, q, g)
+                : attn_start_kernel<k_attn_grad_tc<T, D, KEYS>>(grid, S::kThreads, S::kSmem, st, a, wait_limit_ns(), q, g, k, v);
+}
+
+template <typename T, int D>
+spc_status both_kernels(const AttnArgs& a, cudaStream_t st)
+{
+    const spc_status s = launch<T, D, true>(a, st);
+    return s != SPC_OK ? s : launch<T, D, false>(a, st);
+}
+
+}  // namespace
+
+spc_status attention_bwd_tc(const AttnArgs& a, spc_dtype dt, cudaStream_t st)
+{
+    if (dt == SPC_F16) return a.d <= 64 ? both_kernels<__half, 64>(a, st) : both_kernels<__half, 128>(a, st);
+    return a.d <= 64 ? both_kernels<__nv_bfloat16, 64>(a, st) : both_kernels<__nv_bfloat16, 128>(a, st);
+}
+
+}  // namespace spc

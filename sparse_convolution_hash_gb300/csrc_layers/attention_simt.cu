@@ -225,13 +225,13 @@ __device__ __forceinline__ void tile_grad(const AttnArgs& a, const Mat<DP>& q, c
     for (int i = 0; i < 4; ++i) {
         const int64_t r = row + 4 * ty + i;
         const bool there = r < row_end;
-        const float lse = there ? fetch(a.lse + r * a.hq + head) : -INFINITY, delta = there ? fetch(a.delta + r * a.hq + head) : 0.f;
+        const float lse = there ? fetch(a.lse2 + head * a.nq + r) : -INFINITY, delta = there ? fetch(a.delta + head * a.nq + r) : 0.f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const bool in = there && key + tx + 16 * j < key_end && lse != -INFINITY;
-            const float e = in ? exp2f(s[i][j] * to_log2 - lse * kLog2e) : 0.f;
+            const float e = in ? exp2f(s[i][j] * to_log2 + lse) : 0.f;
             if (!BY_Q) p->v[4 * ty + i][tx + 16 * j] = e;
-            ds.v[4 * ty + i][tx + 16 * j] = in ? e * (dp[i][j] - delta) : 0.f;
+            ds.v[4 * ty + i][tx + 16 * j] = in ? e * (dp[i][j] + delta) : 0.f;
         }
     }
 }

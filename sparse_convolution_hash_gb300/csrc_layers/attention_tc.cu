@@ -320,6 +320,4 @@ spc_status attention_fwd_tc(const AttnArgs& a, spc_dtype dt, cudaStream_t st)
     return dt == SPC_F16 ? typed<__half>(a, f, st) : typed<__nv_bfloat16>(a, f, st);
 }
 
-spc_status attention_bwd_tc(const AttnArgs&, spc_dtype, cudaStream_t) { return SPC_ERR_UNSUPPORTED; }
-
 }  // namespace spc

@@ -421,7 +421,7 @@ k_layer_norm_long_grad(LayerNormArgs a)
 template <auto KERNEL, typename... A>
 spc_status start(dim3 grid, int block, size_t smem, cudaStream_t st, A... args)
 {
-    if (smem > 48 * 1024) {
+    if (smem > 32 * 1024) {  // 48 KB with the static part need no leave
         const spc_status s = allow_smem<KERNEL>();
         if (s != SPC_OK) return s;
     }

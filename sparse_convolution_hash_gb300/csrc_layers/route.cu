@@ -437,7 +437,7 @@ spc_status start(const A& a, size_t smem, bool whole, cudaStream_t st)
     const int L = lanes_for(a.experts);
     const int64_t blocks = ceil_div(a.n, (int64_t)(kBlock / 32) * (32 / L));
     if (blocks > INT32_MAX) return SPC_ERR_UNSUPPORTED;
-    if (smem > 48 * 1024) {
+    if (smem > 32 * 1024) {  // 48 KB with the static part need no leave
         const spc_status s = allow_smem<KERNEL>();
         if (s != SPC_OK) return s;
     }

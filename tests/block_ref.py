@@ -173,7 +173,10 @@ def attention_fwd(q, k, v, seg, seg_k, scale, rounded):
             near = 2 * off + (2 * m + 64) * E + 2.0 ** -20
             lb[a, h] = near + 4 * E * lse[a, h].abs()
             size = p @ v[b, g].abs()
-            ob[a, h] = size * (near + (m + 64) * 2 * E + (u if rounded else 0.0))[:, None]
+            if rounded and t is torch.float16:
+                # the largest probability is kept as 2^7 or more, the smallest ones as multiples of 2^-24
+                ob[a, h] += 2.0 ** -32 * v[b, g].abs().sum(0)
+            ob[a, h] += size * (near + (m + 64) * 2 * E + (u if rounded else 0.0))[:, None]
     return (o, lse), (ob * (1 + u) + rounding(o, t) + 2.0 ** -30, lb)
 
 
@@ -200,6 +203,11 @@ def attention_bwd(dout, q, k, v, o, lse, seg, seg_k, scale, rounded):
             dpb = (d + 4) * 2 * E * (dout[a, h].abs() @ v[b, g].abs().T + (dout[a, h] * o[a, h]).abs().sum(1, keepdim=True))
             dsb = ds.abs() * (r + off + 4 * E) + p * dpb * (1 + off)
             pb = p * (r + off)
+            if rounded and t is torch.float16:
+                # p is kept times 2^14 and ds times 2^14 / 2^e with 2^(e - 1) <= 2 max|do| max|v|, the smallest as
+                # multiples of 2^-24
+                pb = pb + 2.0 ** -39
+                dsb = dsb + 2.0 ** -38 * 2 * dout.norm(dim=2).max() * v.norm(dim=2).max()
             grow = lambda count: (count * (hq // hk) + 64) * 2 * E  # noqa: E731
             out[0][a, h] += scale * ds @ k[b, g]
             bound[0][a, h] += scale * (dsb + grow(m) * ds.abs()) @ k[b, g].abs()

@@ -45,7 +45,7 @@ def close(got, want, bound, what=""):
 
 # ------------------------------------------------------------------ layer norm
 NORM = [(1, 1), (1, 16), (3, 8), (2000, 16), (513, 64), (77, 33), (300, 40), (129, 127), (65, 200), (1025, 96), (40, 260), (33, 512),
-        (21, 520), (17, 1000), (50, 1024), (9, 1027), (7, 2048), (5, 4001), (12, 4096), (3, 9000), (4, 8192), (2, 20000), (0, 24),
+        (21, 520), (17, 1000), (50, 1024), (9, 1027), (7, 2048), (30, 384), (5, 4001), (12, 4096), (3, 9000), (4, 8192), (2, 20000), (0, 24),
         (40000, 24), (20000, 7)]
 
 
