@@ -26,9 +26,9 @@ struct Shape {
     static constexpr int kKept = 128 * 128 * kBoxes;      // bytes of the 128 rows that a block keeps
     static constexpr int kHalf = kStep * 128 * kBoxes;    // bytes of a step's rows of one operand
     static constexpr int kStage = 2 * kHalf;
-    static constexpr int kStages = D == 128 ? 4 : 6;
+    static constexpr int kStages = 4;
     static constexpr int kThreads = 384;
-    static constexpr int kBars = 3 * kStages + 7;
+    static constexpr int kBars = 2 * kStages + 7;
     static constexpr size_t kSmem = 1024 + 2 * (size_t)kKept + (size_t)kStages * (kStage + 2 * kStep * 4) + 8 * kBars + 16;
 };
 
@@ -134,8 +134,7 @@ k_attn_grad_tc(AttnArgs a, uint64_t wait_ns, const __grid_constant__ CUtensorMap
     uint8_t* ring = smem + 2 * S::kKept;
     float* stats = reinterpret_cast<float*>(ring + (size_t)S::kStages * S::kStage);  // [stages][2][kStep]: -lse log2 e, -delta
     uint64_t* full = reinterpret_cast<uint64_t*>(stats + S::kStages * 2 * kStep);
-    uint64_t* empty = full + S::kStages;
-    uint64_t* ready = empty + S::kStages;
+    uint64_t* ready = full + S::kStages;
     uint64_t* kept_full = ready + S::kStages;
     uint64_t* drain = kept_full + 1;
     uint64_t* s_full = drain + 1;
@@ -162,7 +161,6 @@ k_attn_grad_tc(AttnArgs a, uint64_t wait_ns, const __grid_constant__ CUtensorMap
     if (tid == 0) {
         for (int s = 0; s < S::kStages; ++s) {
             ptx::mbar_init(&full[s], 1);
-            ptx::mbar_init(&empty[s], 1);
             ptx::mbar_init(&ready[s], 32);
         }
         ptx::mbar_init(kept_full, 1);
@@ -185,29 +183,45 @@ k_attn_grad_tc(AttnArgs a, uint64_t wait_ns, const __grid_constant__ CUtensorMap
     // tensor memory: step buffers of 128 columns (S, dP), then the sums: dv and dk, or dq
     const uint32_t sum1 = tmem + 256, sum2 = tmem + 256 + D;
     bool ok = true;
+    // Until step it's stage may be written: the products that read it before come ahead of the scores of step it - 2, which
+    // no step's loads may pass.  Called for every step from the second on, as a parity tells a phase from its neighbours only.
+    static_assert(S::kStages == 4, "");
+    auto stage_free = [&](int it) { return attn_wait(&s_full[it & 1], ((it - 2) >> 1) & 1, wait_ns); };
 
     if (warp == 0) {
         // ------------------------------------------------------------ loads
-        if (lane == 0 && n > 0) {
-            ptx::mbar_arrive_expect_tx(kept_full, 2 * S::kKept);
-            for (int b = 0; b < S::kBoxes; ++b) {
-                ptx::tma_load3d<1>(kept_base + b * 16384, &kept1, b * 64, kept_head, (int32_t)t.row, ptx::smem_u32(kept_full));
-                ptx::tma_load3d<1>(kept_base + S::kKept + b * 16384, &kept2, b * 64, kept_head, (int32_t)t.row, ptx::smem_u32(kept_full));
-            }
-            int it = 0;
-            for (; it < n; ++it) {
-                const int s = it % S::kStages;
-                if (it >= S::kStages) ok = ptx::mbar_wait(&empty[s], (it / S::kStages - 1) & 1, wait_ns);
-                if (!ok) break;
-                const uint32_t base = ring_base + (uint32_t)s * S::kStage, bar = ptx::smem_u32(&full[s]);
-                ptx::mbar_arrive_expect_tx(&full[s], S::kStage);
-                const int head = step_head(it), row = (int)step_row(it);
+        if (n > 0) {
+            if (attn_elect()) {
+                ptx::mbar_arrive_expect_tx(kept_full, 2 * S::kKept);
+#pragma unroll
                 for (int b = 0; b < S::kBoxes; ++b) {
-                    ptx::tma_load3d<1>(base + b * (kStep * 128), &step1, b * 64, head, row, bar);
-                    ptx::tma_load3d<1>(base + S::kHalf + b * (kStep * 128), &step2, b * 64, head, row, bar);
+                    ptx::tma_load3d<1>(kept_base + b * 16384, &kept1, b * 64, kept_head, (int32_t)t.row, ptx::smem_u32(kept_full));
+                    ptx::tma_load3d<1>(kept_base + S::kKept + b * 16384, &kept2, b * 64, kept_head, (int32_t)t.row, ptx::smem_u32(kept_full));
                 }
             }
-            if (!ok) set_status(a.status, SPC_ERR_TIMEOUT);
+            __syncwarp();
+            int it = 0, head = step_head(0), row = (int)step_row(0);
+            for (; it < n; ++it) {
+                const int s = it % S::kStages;
+                if (it >= 2) ok = stage_free(it);
+                if (!ok) break;
+                if (attn_elect()) {
+                    const uint32_t base = ring_base + (uint32_t)s * S::kStage, bar = ptx::smem_u32(&full[s]);
+                    ptx::mbar_arrive_expect_tx(&full[s], S::kStage);
+#pragma unroll
+                    for (int b = 0; b < S::kBoxes; ++b) {
+                        ptx::tma_load3d<1>(base + b * (kStep * 128), &step1, b * 64, head, row, bar);
+                        ptx::tma_load3d<1>(base + S::kHalf + b * (kStep * 128), &step2, b * 64, head, row, bar);
+                    }
+                }
+                __syncwarp();
+                row += kStep;
+                if (KEYS && row >= t.hi) {
+                    row = (int)t.lo;
+                    ++head;
+                }
+            }
+            if (!ok && lane == 0) set_status(a.status, SPC_ERR_TIMEOUT);
             // what is in flight has to land before the block's shared memory goes
             ptx::mbar_wait(kept_full, 0, kAttnDrainNs);
             for (int j = it > S::kStages ? it - S::kStages : 0; j < it; ++j)
@@ -215,55 +229,66 @@ k_attn_grad_tc(AttnArgs a, uint64_t wait_ns, const __grid_constant__ CUtensorMap
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------- MMAs
-        if (lane == 0 && n > 0) {
+        if (n > 0) {
             const int steps = (a.d + 15) / 16;
             const uint32_t id_s = ptx::idesc_make(AttnFmt<T>::v, 128, kStep);
             const uint32_t id_o = ptx::idesc_make(AttnFmt<T>::v, 128, steps * 16) | 1u << 16;
-            auto scores = [&](int j) {
+            const uint64_t kept_desc = ptx::desc_k_sw128(kept_base), k_desc = ptx::desc_k_sw128(ring_base);
+            const uint64_t mn_desc = ptx::desc_mn_sw128(ring_base, kStep * 128);
+            auto there = [&](int j) {
                 const int s = j % S::kStages;
                 const uint32_t parity = (j / S::kStages) & 1;
-                ok = ptx::mbar_wait(&full[s], parity, wait_ns) && (!KEYS || ptx::mbar_wait(&ready[s], parity, wait_ns));
-                if (!ok) return;
-                ptx::tc_fence_after();
-                const uint32_t base = ring_base + (uint32_t)s * S::kStage, d = tmem + (j & 1) * 128;
-                attn_mma_ss(d, kept_base, 16384, base, kStep * 128, id_s, steps);
-                attn_mma_ss(d + 64, kept_base + S::kKept, 16384, base + S::kHalf, kStep * 128, id_s, steps);
+                return attn_wait(&full[s], parity, wait_ns) && (!KEYS || attn_wait(&ready[s], parity, wait_ns));
+            };
+            auto scores = [&](int j) {  // by one lane
+                const uint64_t b = k_desc + j % S::kStages * (S::kStage >> 4);
+                const uint32_t d = tmem + (j & 1) * 128;
+                attn_mma_ss<D / 16>(d, kept_desc, 16384, b, kStep * 128, id_s, steps);
+                attn_mma_ss<D / 16>(d + 64, kept_desc + (S::kKept >> 4), 16384, b + (S::kHalf >> 4), kStep * 128, id_s, steps);
                 ptx::mma_commit(&s_full[j & 1]);
             };
-            ok = ptx::mbar_wait(kept_full, 0, wait_ns);
-            if (ok) scores(0);
-            if (ok && n > 1) scores(1);
+            ok = attn_wait(kept_full, 0, wait_ns);
+            for (int j = 0; j < min(n, 2) && ok; ++j) {
+                ok = there(j);
+                ptx::tc_fence_after();
+                if (ok && attn_elect()) scores(j);
+                __syncwarp();
+            }
             for (int j = 0; j < n && ok; ++j) {
-                const int s = j % S::kStages;
-                ok = ptx::mbar_wait(&p_full[j & 1], (j >> 1) & 1, wait_ns);
+                if (j + 2 < n) ok = there(j + 2);
+                if (ok) ok = attn_wait(&p_full[j & 1], (j >> 1) & 1, wait_ns);
                 if (!ok) break;
                 ptx::tc_fence_after();
-                const uint32_t base = ring_base + (uint32_t)s * S::kStage, p = tmem + (j & 1) * 128;
-                const uint64_t d1 = ptx::desc_mn_sw128(base, kStep * 128), d2 = ptx::desc_mn_sw128(base + S::kHalf, kStep * 128);
+                if (attn_elect()) {
+                    const uint32_t p = tmem + (j & 1) * 128;
+                    const uint64_t d1 = mn_desc + j % S::kStages * (S::kStage >> 4), d2 = d1 + (S::kHalf >> 4);
+                    if (KEYS) {
 #pragma unroll
-                for (int q = 0; q < kStep / 16; ++q) {
-                    if (KEYS) ptx::mma_f16_ts(sum1, p + q * 8, d2 + q * 128, id_o, (j | q) != 0);  // dV += P^T dO
+                        for (int q = 0; q < kStep / 16; ++q) ptx::mma_f16_ts(sum1, p + q * 8, d2 + q * 128, id_o, q > 0 || j > 0);  // dV += P^T dO
+                    }
+#pragma unroll
+                    for (int q = 0; q < kStep / 16; ++q)  // dK += dS^T Q, dQ += dS K
+                        ptx::mma_f16_ts(KEYS ? sum2 : sum1, p + 64 + q * 8, d1 + q * 128, id_o, q > 0 || j > 0);
+                    if (j + 2 < n) scores(j + 2);
+                    else if (j + 1 == n) ptx::mma_commit(o_full);
                 }
-#pragma unroll
-                for (int q = 0; q < kStep / 16; ++q)  // dK += dS^T Q, dQ += dS K
-                    ptx::mma_f16_ts(KEYS ? sum2 : sum1, p + 64 + q * 8, d1 + q * 128, id_o, (j | q) != 0);
-                ptx::mma_commit(&empty[s]);
-                if (j + 2 < n) scores(j + 2);
+                __syncwarp();
             }
-            if (ok) ptx::mma_commit(o_full);
-            else set_status(a.status, SPC_ERR_TIMEOUT);
-            ptx::mma_commit(drain);
+            if (!ok && lane == 0) set_status(a.status, SPC_ERR_TIMEOUT);
+            if (attn_elect()) ptx::mma_commit(drain);
+            __syncwarp();
             ptx::mbar_wait(drain, 0, kAttnDrainNs);
         }
     } else if (warp == 2) {
         // ------------------------------- the queries' log-sums and row sums, and rows past the segment's end
         if (KEYS) {
-            int it = 0;
-            for (; it < n; ++it) {
+            int64_t row = n > 0 ? step_row(0) : 0;
+            int head = n > 0 ? step_head(0) : 0;
+            for (int it = 0; it < n; ++it) {
                 const int s = it % S::kStages;
-                if (it >= S::kStages) ok = __all_sync(FULL_MASK, ptx::mbar_wait(&empty[s], (it / S::kStages - 1) & 1, wait_ns));
+                if (it >= 2) ok = stage_free(it);
                 if (!ok) break;
-                const int64_t row = step_row(it), at = (int64_t)step_head(it) * a.nq + row;
+                const int64_t at = (int64_t)head * a.nq + row;
                 const int valid = (int)min((int64_t)kStep, t.hi - row);
                 float* to_s = stats + s * 2 * kStep;
 #pragma unroll
@@ -281,13 +306,18 @@ k_attn_grad_tc(AttnArgs a, uint64_t wait_ns, const __grid_constant__ CUtensorMap
                         to_s[i] = -INFINITY;  // no probability
                         to_s[kStep + i] = 0.f;
                     }
-                    ok = __all_sync(FULL_MASK, ptx::mbar_wait(&full[s], (it / S::kStages) & 1, wait_ns));
+                    ok = attn_wait(&full[s], (it / S::kStages) & 1, wait_ns);
                     if (!ok) break;
                     const uint32_t base = ring_base + (uint32_t)s * S::kStage;
                     attn_clear_rows<S::kBoxes>(base, kStep, valid, lane, 32);
                     attn_clear_rows<S::kBoxes>(base + S::kHalf, kStep, valid, lane, 32);
                     ptx::cp_async_wait_all();
                     ptx::mbar_arrive(&ready[s]);
+                }
+                row += kStep;
+                if (row >= t.hi) {
+                    row = t.lo;
+                    ++head;
                 }
             }
             if (!ok && lane == 0) set_status(a.status, SPC_ERR_TIMEOUT);
@@ -309,9 +339,8 @@ k_attn_grad_tc(AttnArgs a, uint64_t wait_ns, const __grid_constant__ CUtensorMap
         }
         for (int j = b; j < n; j += 2) {
             const int s = j % S::kStages;
-            ok = ptx::mbar_wait(&s_full[b], (j >> 1) & 1, wait_ns);
-            if (KEYS) ok = ok && ptx::mbar_wait(&ready[s], (j / S::kStages) & 1, wait_ns);
-            ok = __all_sync(FULL_MASK, ok);
+            ok = attn_wait(&s_full[b], (j >> 1) & 1, wait_ns);
+            if (KEYS && ok) ok = attn_wait(&ready[s], (j / S::kStages) & 1, wait_ns);
             if (!ok) break;
             ptx::tc_fence_after();
             const float* st = stats + s * 2 * kStep;
@@ -357,7 +386,7 @@ k_attn_grad_tc(AttnArgs a, uint64_t wait_ns, const __grid_constant__ CUtensorMap
             }
             ptx::tmem_st_wait();
             if (!KEYS && left < kStep) {
-                ok = __all_sync(FULL_MASK, ptx::mbar_wait(&full[s], (j / S::kStages) & 1, wait_ns));
+                ok = attn_wait(&full[s], (j / S::kStages) & 1, wait_ns);
                 if (!ok) break;
                 attn_clear_rows<S::kBoxes>(ring_base + (uint32_t)s * S::kStage, kStep, (int)left, r, 128);
             }
@@ -365,7 +394,7 @@ k_attn_grad_tc(AttnArgs a, uint64_t wait_ns, const __grid_constant__ CUtensorMap
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&p_full[b]);
         }
-        if (ok && n > 0) ok = __all_sync(FULL_MASK, ptx::mbar_wait(o_full, 0, wait_ns));
+        if (ok && n > 0) ok = attn_wait(o_full, 0, wait_ns);
         ptx::tc_fence_after();
         if (!ok && lane == 0) set_status(a.status, SPC_ERR_TIMEOUT);
         if (ok) {

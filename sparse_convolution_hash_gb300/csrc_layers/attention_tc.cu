@@ -1,11 +1,12 @@
 // attention_tc.cu -- the forward pass of attention over segments on the 5th-generation tensor cores.
 //
 // A block keeps TILES tiles of 128 query rows (the positions of a segment, and the query heads that share a key head
-// beside one another, so that keys are read once for all of them) and walks over the segment's keys 128 at a time:
+// beside one another, so that keys are read once for all of them) and walks over the segment's keys 64 at a time:
 //   warp 0 loads the queries once and keys and values in turn into a ring of stages (TMA);
 //   warp 1 issues S = Q K^T into tensor memory and O += P V with P from tensor memory;
 //   four warps for each tile take S, a thread to a row: running maximum, exponentials, P as 16 bits in the place of S.
-// With two tiles the products of one run while the other's exponentials are taken.  O stays in tensor memory; it is
+// S has two buffers a tile, so the next scores are there when a tile's exponentials are done, and with two tiles the
+// products of one run while the other's exponentials are taken.  O stays in tensor memory; it is
 // rescaled only when a row's maximum has grown by more than 2^8, so almost never after the first tiles
 // (sums and P carry the same factor, which the end divides out).
 //
@@ -17,18 +18,20 @@ namespace spc {
 
 namespace {
 
-constexpr int kKeys = 128;       // keys of a tile
+constexpr int kKeys = 64;        // keys of a step
 constexpr float kLazy = 8.f;     // a maximum may grow by this much (log2) before sums are rescaled
 
 template <int D, int TILES>
 struct Shape {
     static constexpr int kBoxes = D / 64;
-    static constexpr int kTile = 128 * 128 * kBoxes;          // bytes of 128 rows
-    static constexpr int kStages = TILES == 2 ? (D == 128 ? 4 : 8) : (D == 128 ? 2 : 5);
+    static constexpr int kTile = 128 * 128 * kBoxes;          // bytes of a tile's queries
+    static constexpr int kPart = kKeys * 128 * kBoxes;        // bytes of a step's keys, or values
+    static constexpr int kStage = 2 * kPart;                  // the values of a step, the keys of the next but one
+    static constexpr int kStages = TILES == 1 && D == 128 ? 2 : 4;
     static constexpr int kThreads = 64 + 128 * TILES;
-    static constexpr int kCols = TILES == 2 ? 512 : 256;      // tensor memory
-    static constexpr int kBars = 2 * kStages + 2 + 3 * TILES;
-    static constexpr size_t kSmem = 1024 + (size_t)(TILES + kStages) * kTile + 8 * kBars + 16;
+    static constexpr int kCols = TILES == 2 ? 512 : 256;      // tensor memory: 128 of scores and D of sums a tile
+    static constexpr int kBars = 2 * kStages + 2 + 6 * TILES;
+    static constexpr size_t kSmem = 1024 + (size_t)TILES * kTile + (size_t)kStages * kStage + 8 * kBars + 16;
 };
 
 struct Packing {
@@ -44,15 +47,17 @@ k_attn_tc(AttnArgs a, Packing pk, uint64_t wait_ns, const __grid_constant__ CUte
     using S = Shape<D, TILES>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    // a stage: the values of a step, then the keys of the next but one (the last two begin with those of steps 0 and 1)
     uint8_t* ring = smem + TILES * S::kTile;
-    uint64_t* full = reinterpret_cast<uint64_t*>(ring + (size_t)S::kStages * S::kTile);
+    uint64_t* full = reinterpret_cast<uint64_t*>(ring + (size_t)S::kStages * S::kStage);
     uint64_t* empty = full + S::kStages;
     uint64_t* q_full = empty + S::kStages;
     uint64_t* drain = q_full + 1;
-    uint64_t* s_full = drain + 1;
-    uint64_t* p_full = s_full + TILES;
-    uint64_t* o_full = p_full + TILES;
-    uint32_t* s_ctrl = reinterpret_cast<uint32_t*>(o_full + TILES);
+    uint64_t* s_full = drain + 1;             // [tile][buffer]: the scores of a step, and the sums of the one two before
+    uint64_t* p_full = s_full + 2 * TILES;    // [tile][buffer]
+    uint64_t* o_last = p_full + 2 * TILES;    // [tile]: the sums of the last step but one
+    uint64_t* o_done = o_last + TILES;        // [tile]: and of the last one
+    uint32_t* s_ctrl = reinterpret_cast<uint32_t*>(o_done + TILES);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     wait_for_kernel_before();
@@ -76,11 +81,11 @@ k_attn_tc(AttnArgs a, Packing pk, uint64_t wait_ns, const __grid_constant__ CUte
         }
         ptx::mbar_init(q_full, 1);
         ptx::mbar_init(drain, 1);
-        for (int i = 0; i < TILES; ++i) {
+        for (int i = 0; i < 2 * TILES; ++i) {
             ptx::mbar_init(&s_full[i], 1);
             ptx::mbar_init(&p_full[i], 4);
-            ptx::mbar_init(&o_full[i], 1);
         }
+        for (int i = 0; i < 2 * TILES; ++i) ptx::mbar_init(&o_last[i], 1);
         ptx::mbar_init_fence();
     }
     if (warp == 1) {
@@ -94,70 +99,89 @@ k_attn_tc(AttnArgs a, Packing pk, uint64_t wait_ns, const __grid_constant__ CUte
     const uint32_t q_base = ptx::smem_u32(smem), ring_base = ptx::smem_u32(ring);
     bool ok = true;
 
+
     if (warp == 0) {
         // ------------------------------------------------------------ loads
-        if (lane == 0 && n > 0) {
-            const uint32_t bytes = (uint32_t)pk.heads * pk.positions * 128;
-            ptx::mbar_arrive_expect_tx(q_full, bytes * S::kBoxes * tiles);
-            for (int i = 0; i < tiles; ++i)
+        if (n > 0) {
+            auto load = [&](uint32_t to, const CUtensorMap* map, int step, uint64_t* bar) {
+#pragma unroll
                 for (int b = 0; b < S::kBoxes; ++b)
-                    ptx::tma_load3d<1>(q_base + i * S::kTile + b * 16384, &map_q, b * 64, head0, (int32_t)(t.row + i * pk.positions),
-                                       ptx::smem_u32(q_full));
-            int it = 0;
-            for (int j = 0; j < 2 * n && ok; ++j, ++it) {
-                const int s = it % S::kStages;
-                if (it >= S::kStages) ok = ptx::mbar_wait(&empty[s], (it / S::kStages - 1) & 1, wait_ns);
-                if (!ok) break;
-                ptx::mbar_arrive_expect_tx(&full[s], S::kTile);
-                for (int b = 0; b < S::kBoxes; ++b)
-                    ptx::tma_load3d<1>(ring_base + s * S::kTile + b * 16384, j & 1 ? &map_v : &map_k, b * 64, kv,
-                                       (int32_t)(lo + (int64_t)(j >> 1) * kKeys), ptx::smem_u32(&full[s]));
+                    ptx::tma_load3d<1>(to + b * (kKeys * 128), map, b * 64, kv, (int32_t)lo + step * kKeys, ptx::smem_u32(bar));
+            };
+            if (attn_elect()) {
+                ptx::mbar_arrive_expect_tx(q_full, (uint32_t)pk.heads * pk.positions * 128 * S::kBoxes * tiles + S::kPart * min(n, 2));
+                for (int i = 0; i < tiles; ++i)
+                    for (int b = 0; b < S::kBoxes; ++b)
+                        ptx::tma_load3d<1>(q_base + i * S::kTile + b * 16384, &map_q, b * 64, head0, (int32_t)(t.row + i * pk.positions),
+                                           ptx::smem_u32(q_full));
+                for (int j = 0; j < min(n, 2); ++j) load(ring_base + (S::kStages - 2 + j) * S::kStage + S::kPart, &map_k, j, q_full);
             }
-            if (!ok) set_status(a.status, SPC_ERR_TIMEOUT);
+            __syncwarp();
+            int j = 0;
+            for (; j < n; ++j) {
+                // freed once for each step that used it, and the last two by the scores of steps 0 and 1 besides
+                const int s = j % S::kStages, freed = j / S::kStages + (s >= S::kStages - 2);
+                if (freed > 0) ok = attn_wait(&empty[s], (freed - 1) & 1, wait_ns);
+                if (!ok) break;
+                if (attn_elect()) {
+                    const uint32_t to = ring_base + s * S::kStage;
+                    ptx::mbar_arrive_expect_tx(&full[s], j + 2 < n ? S::kStage : S::kPart);
+                    load(to, &map_v, j, &full[s]);
+                    if (j + 2 < n) load(to + S::kPart, &map_k, j + 2, &full[s]);
+                }
+                __syncwarp();
+            }
+            if (!ok && lane == 0) set_status(a.status, SPC_ERR_TIMEOUT);
             // what is in flight has to land before the block's shared memory goes
             ptx::mbar_wait(q_full, 0, kAttnDrainNs);
-            for (int j = it > S::kStages ? it - S::kStages : 0; j < it; ++j)
-                ptx::mbar_wait(&full[j % S::kStages], (j / S::kStages) & 1, kAttnDrainNs);
+            for (int i = max(j - S::kStages, 0); i < j; ++i) ptx::mbar_wait(&full[i % S::kStages], (i / S::kStages) & 1, kAttnDrainNs);
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------- MMAs
-        if (lane == 0 && n > 0) {
+        if (n > 0) {
             const int steps = (a.d + 15) / 16;
             const uint32_t id_s = ptx::idesc_make(AttnFmt<T>::v, 128, kKeys);
             const uint32_t id_o = ptx::idesc_make(AttnFmt<T>::v, 128, steps * 16) | 1u << 16;
-            auto stage = [&](int it) { return ring_base + (uint32_t)(it % S::kStages) * S::kTile; };
-            auto arrived = [&](int it) { return ptx::mbar_wait(&full[it % S::kStages], (it / S::kStages) & 1, wait_ns); };
-            auto scores = [&](int i, int j) {
-                attn_mma_ss(tmem + i * 128, q_base + i * S::kTile, 16384, stage(2 * j), 16384, id_s, steps);
-                ptx::mma_commit(&s_full[i]);
-                if (i == tiles - 1) ptx::mma_commit(&empty[2 * j % S::kStages]);
+            const uint64_t q_desc = ptx::desc_k_sw128(q_base);
+            const uint64_t k_desc = ptx::desc_k_sw128(ring_base + S::kPart), v_desc = ptx::desc_mn_sw128(ring_base, kKeys * 128);
+            auto scores = [&](int i, int j) {  // by one lane
+                const uint64_t keys = k_desc + (j + S::kStages - 2) % S::kStages * (S::kStage >> 4);
+                attn_mma_ss<D / 16>(tmem + i * 128 + (j & 1) * 64, q_desc + i * (S::kTile >> 4), 16384, keys, kKeys * 128, id_s, steps);
+                ptx::mma_commit(&s_full[2 * i + (j & 1)]);
             };
-            ok = ptx::mbar_wait(q_full, 0, wait_ns) && arrived(0);
+            ok = attn_wait(q_full, 0, wait_ns);
             ptx::tc_fence_after();
-            for (int i = 0; i < tiles && ok; ++i) scores(i, 0);
+            if (ok && attn_elect())
+                for (int j = 0; j < min(n, 2); ++j) {
+                    for (int i = 0; i < tiles; ++i) scores(i, j);
+                    ptx::mma_commit(&empty[S::kStages - 2 + j]);
+                }
+            __syncwarp();
             for (int j = 0; j < n && ok; ++j) {
-                ok = arrived(2 * j + 1);
-                const uint64_t vd = ptx::desc_mn_sw128(stage(2 * j + 1), 16384);
-                for (int i = 0; i < tiles && ok; ++i) {
-                    ok = ptx::mbar_wait(&p_full[i], j & 1, wait_ns);
+                const int s = j % S::kStages;
+                ok = attn_wait(&full[s], (j / S::kStages) & 1, wait_ns);
+#pragma unroll
+                for (int i = 0; i < TILES; ++i) {
+                    if (i >= tiles || !ok) break;
+                    ok = attn_wait(&p_full[2 * i + (j & 1)], (j >> 1) & 1, wait_ns);
                     if (!ok) break;
                     ptx::tc_fence_after();
+                    if (attn_elect()) {
 #pragma unroll
-                    for (int q = 0; q < kKeys / 16; ++q)
-                        ptx::mma_f16_ts(tmem + TILES * 128 + i * D, tmem + i * 128 + q * 8, vd + q * 128, id_o, (j | q) != 0);
-                    if (i == tiles - 1) ptx::mma_commit(&empty[(2 * j + 1) % S::kStages]);
-                    if (j + 1 < n) {
-                        if (i == 0) ok = arrived(2 * j + 2);
-                        if (!ok) break;
-                        ptx::tc_fence_after();
-                        scores(i, j + 1);
-                    } else {
-                        ptx::mma_commit(&o_full[i]);
+                        for (int q = 0; q < kKeys / 16; ++q)
+                            ptx::mma_f16_ts(tmem + TILES * 128 + i * D, tmem + i * 128 + (j & 1) * 64 + q * 8,
+                                            v_desc + s * (S::kStage >> 4) + q * 128, id_o, q > 0 || j > 0);
+                        // in the place of P, which the products before have read by then
+                        if (j + 2 < n) scores(i, j + 2);
+                        else ptx::mma_commit(j + 2 == n ? &o_last[i] : &o_done[i]);
+                        if (i == tiles - 1) ptx::mma_commit(&empty[s]);
                     }
+                    __syncwarp();
                 }
             }
-            if (!ok) set_status(a.status, SPC_ERR_TIMEOUT);
-            ptx::mma_commit(drain);
+            if (!ok && lane == 0) set_status(a.status, SPC_ERR_TIMEOUT);
+            if (attn_elect()) ptx::mma_commit(drain);
+            __syncwarp();
             ptx::mbar_wait(drain, 0, kAttnDrainNs);
         }
     } else {
@@ -171,24 +195,25 @@ k_attn_tc(AttnArgs a, Packing pk, uint64_t wait_ns, const __grid_constant__ CUte
             constexpr float kUp = std::is_same<T, __half>::value ? 7.f : 0.f;
             float m = -INFINITY, l = 0.f;
             for (int j = 0; j < n; ++j) {
-                ok = __all_sync(FULL_MASK, ptx::mbar_wait(&s_full[i], j & 1, wait_ns));
+                ok = attn_wait(&s_full[2 * i + (j & 1)], (j >> 1) & 1, wait_ns);
                 if (!ok) break;
                 ptx::tc_fence_after();
-                uint32_t v[4][32];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) ptx::tmem_ld32(s_at + x * 32, v[x]);
+                const uint32_t at = s_at + (j & 1) * 64;
+                uint32_t v[2][32];
+                ptx::tmem_ld32(at, v[0]);
+                ptx::tmem_ld32(at + 32, v[1]);
                 ptx::tmem_ld_wait();
                 const int valid = (int)min((int64_t)kKeys, hi - lo - (int64_t)j * kKeys);
                 if (valid < kKeys) {
 #pragma unroll
-                    for (int x = 0; x < 128; ++x)
+                    for (int x = 0; x < kKeys; ++x)
                         if (x >= valid) v[x >> 5][x & 31] = 0xff800000u;
                 }
                 float most[4] = {m, m, m, m};
 #pragma unroll
-                for (int x = 0; x < 32; ++x) {
+                for (int x = 0; x < 16; ++x) {
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) most[y] = fmaxf(most[y], __uint_as_float(v[y][x]));
+                    for (int y = 0; y < 4; ++y) most[y] = fmaxf(most[y], __uint_as_float(v[y >> 1][2 * x + (y & 1)]));
                 }
                 const float top = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
                 const bool grow = (top - m) * c > kLazy;  // false where both are -inf
@@ -197,45 +222,45 @@ k_attn_tc(AttnArgs a, Packing pk, uint64_t wait_ns, const __grid_constant__ CUte
                     if (grow) m = top;
                     l *= shrink;
                     if (j > 0) {
+                        // the sums of step j - 1
+                        ok = j + 1 < n ? attn_wait(&s_full[2 * i + ((j + 1) & 1)], ((j + 1) >> 1) & 1, wait_ns) : attn_wait(&o_last[i], 0, wait_ns);
+                        if (!ok) break;
+                        ptx::tc_fence_after();
 #pragma unroll 1
-                        for (int x = 0; x < D; x += 16) {
-                            uint32_t o[16];
-                            ptx::tmem_ld16(o_at + x, o);
+                        for (int x = 0; x < D; x += 32) {
+                            uint32_t o[32];
+                            ptx::tmem_ld32(o_at + x, o);
                             ptx::tmem_ld_wait();
 #pragma unroll
-                            for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * shrink);
-                            ptx::tmem_st16(o_at + x, o);
+                            for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * shrink);
+                            ptx::tmem_st32(o_at + x, o);
                         }
                     }
                 }
                 const F2 base = both(m == -INFINITY ? 0.f : kUp - m * c), cc = both(c);
                 F2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
+                uint32_t p[32];
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    uint32_t p[16];
-#pragma unroll
-                    for (int y = 0; y < 16; ++y) {
-                        F2 e = fma(F2{__uint_as_float(v[x][2 * y]), __uint_as_float(v[x][2 * y + 1])}, cc, base);
-                        e = F2{ptx::ex2(e.x), ptx::ex2(e.y)};
-                        sum[y & 1] = add(sum[y & 1], e);
-                        p[y] = pack2<T>(e.x, e.y);
-                    }
-                    ptx::tmem_st16(s_at + x * 16, p);
+                for (int y = 0; y < 32; ++y) {
+                    F2 e = fma(F2{__uint_as_float(v[y >> 4][2 * (y & 15)]), __uint_as_float(v[y >> 4][2 * (y & 15) + 1])}, cc, base);
+                    e = F2{ptx::ex2(e.x), ptx::ex2(e.y)};
+                    sum[y & 1] = add(sum[y & 1], e);
+                    p[y] = pack2<T>(e.x, e.y);
                 }
-                ptx::tmem_st_wait();
+                ptx::tmem_st32(at, p);
                 sum[0] = add(sum[0], sum[1]);
                 l += sum[0].x + sum[0].y;
+                ptx::tmem_st_wait();
                 if (i == 0 && valid < kKeys) {
-                    const int it = 2 * j + 1;
-                    ok = __all_sync(FULL_MASK, ptx::mbar_wait(&full[it % S::kStages], (it / S::kStages) & 1, wait_ns));
+                    ok = attn_wait(&full[j % S::kStages], (j / S::kStages) & 1, wait_ns);
                     if (!ok) break;
-                    attn_clear_rows<S::kBoxes>(ring_base + (uint32_t)(it % S::kStages) * S::kTile, kKeys, valid, r, 128);
+                    attn_clear_rows<S::kBoxes>(ring_base + (uint32_t)(j % S::kStages) * S::kStage, kKeys, valid, r, 128);
                 }
                 ptx::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(&p_full[i]);
+                if (lane == 0) ptx::mbar_arrive(&p_full[2 * i + (j & 1)]);
             }
-            if (ok && n > 0) ok = __all_sync(FULL_MASK, ptx::mbar_wait(&o_full[i], 0, wait_ns));
+            if (ok && n > 0) ok = attn_wait(&o_done[i], 0, wait_ns);
             ptx::tc_fence_after();
             if (!ok && lane == 0) set_status(a.status, SPC_ERR_TIMEOUT);
             const int pos = r / pk.heads;

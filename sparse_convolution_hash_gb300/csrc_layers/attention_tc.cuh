@@ -94,16 +94,28 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi)
     return w;
 }
 
-// A product of rows of D channels in shared memory, both K-major: boxes of 64 channels lie `a_box` / `b_box` bytes
-// apart.  `steps` of 16 channels.
-__device__ __forceinline__ void attn_mma_ss(uint32_t d, uint32_t a, uint32_t a_box, uint32_t b, uint32_t b_box, uint32_t idesc, int steps)
+// The tensor warps run their loops as whole warps and elect a lane where they issue: what a loop computes then stays in
+// uniform registers, from which products and copies take their operands.  With a loop of one lane each product took
+// about 100 cycles to issue, and the products, not the exponentials, set the pace (d = 64: 385 TFLOP/s).
+__device__ __forceinline__ bool attn_elect()
+{
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
+}
+__device__ __forceinline__ bool attn_wait(uint64_t* bar, uint32_t parity, uint64_t wait_ns)
+{
+    return __all_sync(FULL_MASK, ptx::mbar_wait(bar, parity, wait_ns));
+}
+
+// A product of rows of up to 128 channels in shared memory, both K-major, by one lane; boxes of 64 channels lie a_box / b_box
+// bytes apart.  a, b: descriptors of the first box; `steps` of 16 channels, at most MOST.
+template <int MOST>
+__device__ __forceinline__ void attn_mma_ss(uint32_t d, uint64_t a, uint32_t a_box, uint64_t b, uint32_t b_box, uint32_t idesc, int steps)
 {
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-        if (q >= steps) break;
-        ptx::mma_f16<1>(d, ptx::desc_k_sw128(a + (q >> 2) * a_box) + 2 * (q & 3), ptx::desc_k_sw128(b + (q >> 2) * b_box) + 2 * (q & 3),
-                        idesc, q != 0);
-    }
+    for (int q = 0; q < MOST; ++q)
+        if (q < steps) ptx::mma_f16<1>(d, a + (q >> 2) * (a_box >> 4) + 2 * (q & 3), b + (q >> 2) * (b_box >> 4) + 2 * (q & 3), idesc, q != 0);
 }
 
 // Zeroes the rows [from, rows) of a tile in shared memory (NB boxes of `rows` lines of 128 bytes): what belongs to

@@ -83,22 +83,70 @@ __device__ __forceinline__ S score_of(float l, bool sigmoid, float most, S sum)
 }
 
 struct RouteShared {
-    int32_t* expert;   // [rows][k] of this warp
-    float* logit;      // [rows][k]
-    double* c;         // [rows][experts], groups only
-    double* best;      // [rows][groups]
+    int32_t* expert;   // [k] of this row
+    float* logit;      // [k]
+    void* c;           // [experts], then [groups], of the scores' type; groups only
 };
+
+// Scores as words that are ordered as they are (the least word for -inf and NaN, which are never chosen).
+__device__ __forceinline__ uint32_t order_of(float v)
+{
+    const uint32_t b = __float_as_uint(v + 0.f);  // one zero
+    return v > -INFINITY ? b ^ (b >> 31 ? 0xffffffffu : 0x80000000u) : 0u;
+}
+__device__ __forceinline__ float value_of(uint32_t w) { return w ? __uint_as_float(w >> 31 ? w ^ 0x80000000u : ~w) : -INFINITY; }
+
+__device__ __forceinline__ uint32_t lanes_most(uint32_t v, int L)
+{
+    if (L == 32) return __reduce_max_sync(FULL_MASK, v);
+    return lanes_max(v, L);
+}
+
+// The best of the lanes' values: (value, expert, logit), ties to the lowest expert; expert kNone where none is left.
+template <int C>
+__device__ __forceinline__ void best_of_lanes(float& top, int& e, float& l, int lane, int L)
+{
+    const uint32_t key = order_of(top), most = lanes_most(key, L);
+    const bool mine = key == most && e != kNone;
+    int winner;
+    if constexpr (C == 1) {  // lanes hold ascending experts
+        const uint32_t at = (threadIdx.x & 31) - lane, votes = __ballot_sync(FULL_MASK, mine) >> at;
+        winner = __ffs(L == 32 ? votes : votes & ((1u << L) - 1)) - 1;
+    } else {
+        const uint32_t least = ~lanes_most(~(mine ? (uint32_t)e : (uint32_t)kNone), L);
+        const uint32_t votes = __ballot_sync(FULL_MASK, mine && (uint32_t)e == least);
+        winner = __ffs(votes) - 1;
+    }
+    const int from = max(winner, 0);
+    e = __shfl_sync(FULL_MASK, e, from, L);
+    l = __shfl_sync(FULL_MASK, l, from, L);
+    top = value_of(most);
+    if (winner < 0) e = kNone;
+}
+template <int C>
+__device__ __forceinline__ void best_of_lanes(double& top, int& e, float& l, int, int L)
+{
+    for (int o = L >> 1; o; o >>= 1) {
+        const double v = __shfl_xor_sync(FULL_MASK, top, o);
+        const int other = __shfl_xor_sync(FULL_MASK, e, o);
+        const float z = __shfl_xor_sync(FULL_MASK, l, o);
+        if (v > top || (v == top && other < e)) {
+            top = v;
+            e = other;
+            l = z;
+        }
+    }
+}
 
 // The row's k best, written to sh.expert and sh.logit by its lane 0.  S: the type that scores are compared in
 // (BY_LOGIT: the logits, exactly).  Returns whether two neighbours, or the border of the kept groups, lie
-// within the error of S.
+// within the error of S: scores are off by `rel` of themselves, none is above p_most.
 template <typename S, bool BY_LOGIT, int C>
-__device__ __forceinline__ bool choose(const RouteArgs& a, const float (&l)[C][kPer], int lane, int L, int sub, const RouteShared& sh)
+__device__ __forceinline__ bool choose(const RouteArgs& a, const float (&l)[C][kPer], int lane, int L, const RouteShared& sh)
 {
     const S kLow = -INFINITY;
-    const S rel = a.score == SPC_SCORE_SIGMOID ? (S)0x1p-20 : (S)0x1p-16;
     bool near = false;
-    S c[C][kPer];
+    S c[C][kPer], off = 0;
     if constexpr (BY_LOGIT) {
 #pragma unroll
         for (int i = 0; i < C; ++i) {
@@ -115,18 +163,20 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&l)[C][k
         }
         most = lanes_max(most, L);
         const S sum = sigmoid ? (S)1 : exp_sum<S>(l, most, L);
+        off = sigmoid ? (S)0x1p-20 : (S)0x1p-16 / sum;
 #pragma unroll
         for (int i = 0; i < C; ++i) {
 #pragma unroll
             for (int j = 0; j < kPer; ++j) {
                 const int e = (i * L + lane) * kPer + j;
                 c[i][j] = l[i][j] > -INFINITY ? score_of<S>(l[i][j], sigmoid, most, sum) + (a.bias ? (S)fetch(a.bias + e) : (S)0) : kLow;
+                if (!(c[i][j] > kLow)) c[i][j] = kLow;  // a bias of NaN
             }
         }
         if (a.groups > 1) {
             // a group's score: the sum of its two best (its only one's, where it has one)
-            double* row = sh.c + (int64_t)sub * a.experts;
-            double* best = sh.best + (int64_t)sub * a.groups;
+            S* row = static_cast<S*>(sh.c);
+            S* best = row + a.experts;
             const int size = a.experts / a.groups;
             __syncwarp();
 #pragma unroll
@@ -134,31 +184,37 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&l)[C][k
 #pragma unroll
                 for (int j = 0; j < kPer; ++j) {
                     const int e = (i * L + lane) * kPer + j;
-                    if (e < a.experts) row[e] = (double)c[i][j];
+                    if (e < a.experts) row[e] = c[i][j];
                 }
             }
             __syncwarp();
-            for (int g = lane; g < a.groups; g += L) {
+            // with fewer groups than lanes several lanes read a group, neighbours side by side
+            const int share = a.groups >= L ? 1 : 1 << (31 - __clz(L / a.groups));
+            for (int g0 = 0; g0 < a.groups; g0 += L / share) {
+                const int g = g0 + lane / share;
                 S first = kLow, second = kLow;
-                for (int e = g * size; e < (g + 1) * size; ++e) {
-                    const S v = (S)row[e];
-                    if (v > first) {
-                        second = first;
-                        first = v;
-                    } else if (v > second) {
-                        second = v;
+                if (g < a.groups) {
+                    for (int e = lane & (share - 1); e < size; e += share) {
+                        const S v = row[g * size + e], low = min(v, first);
+                        first = max(v, first);
+                        second = max(second, low);
                     }
                 }
-                best[g] = (double)(second > kLow ? first + second : first);
+                for (int o = 1; o < share; o <<= 1) {
+                    const S v = __shfl_xor_sync(FULL_MASK, first, o), w = __shfl_xor_sync(FULL_MASK, second, o);
+                    second = max(max(second, w), min(first, v));
+                    first = max(first, v);
+                }
+                if (g < a.groups && (lane & (share - 1)) == 0) best[g] = second > kLow ? first + second : first;
             }
             __syncwarp();
             S least_kept = INFINITY, best_left = kLow;
-            uint32_t kept_mask = 0;  // of this lane's groups, the first 32 (1,024 groups on 32 lanes)
+            uint32_t kept_mask = 0;  // of this lane's groups: 1,024 groups on 32 lanes are 32
             for (int g = lane, q = 0; g < a.groups; g += L, ++q) {
-                const S mine = (S)best[g];
+                const S mine = best[g];
                 int better = 0;
                 for (int o = 0; o < a.groups; ++o) {
-                    const S other = (S)best[o];
+                    const S other = best[o];
                     better += other > mine || (other == mine && o < g);
                 }
                 const bool keep = better < a.top_groups && mine > kLow;
@@ -169,16 +225,21 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&l)[C][k
             least_kept = -lanes_max(-least_kept, L);
             best_left = lanes_max(best_left, L);
             if (best_left > kLow && least_kept < INFINITY)
-                near = least_kept - best_left <= 2 * rel + (S)0x1p-21 * (fabs(least_kept) + fabs(best_left));
+                near = least_kept - best_left <= 4 * off + (S)0x1p-21 * (fabs(least_kept) + fabs(best_left));
             __syncwarp();
-            for (int g = lane, q = 0; g < a.groups; g += L, ++q) best[g] = kept_mask >> q & 1 ? 1.0 : 0.0;
+            for (int g = lane, q = 0; g < a.groups; g += L, ++q) best[g] = kept_mask >> q & 1 ? (S)1 : (S)0;
             __syncwarp();
 #pragma unroll
             for (int i = 0; i < C; ++i) {
+                // the group of each expert, by counting on from the first one's
+                int e = (i * L + lane) * kPer, g = e / size, in = e - g * size;
 #pragma unroll
-                for (int j = 0; j < kPer; ++j) {
-                    const int e = (i * L + lane) * kPer + j;
-                    if (e < a.experts && best[e / size] == 0.0) c[i][j] = kLow;
+                for (int j = 0; j < kPer; ++j, ++e) {
+                    if (e < a.experts && best[g] == (S)0) c[i][j] = kLow;
+                    if (++in == size) {
+                        in = 0;
+                        ++g;
+                    }
                 }
             }
         }
@@ -189,47 +250,34 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&l)[C][k
     // one round more than asked for shows the gap to the first that is left out
     const int rounds = BY_LOGIT ? a.top_k : a.top_k + 1;
     for (int r = 0; r < rounds; ++r) {
-        S mine = kLow;
-        int e_mine = kNone;
-        float l_mine = 0.f;
+        S top = kLow;
+        int e_top = kNone;
+        float l_top = 0.f;
 #pragma unroll
         for (int i = 0; i < C; ++i) {
 #pragma unroll
             for (int j = 0; j < kPer; ++j)
-                if (c[i][j] > mine) {
-                    mine = c[i][j];
-                    e_mine = (i * L + lane) * kPer + j;
-                    l_mine = l[i][j];
+                if (c[i][j] > top) {
+                    top = c[i][j];
+                    e_top = (i * L + lane) * kPer + j;
+                    l_top = l[i][j];
                 }
         }
-        S top = mine;
-        int e_top = e_mine;
-        float l_top = l_mine;
-        for (int o = L >> 1; o; o >>= 1) {
-            const S v = __shfl_xor_sync(FULL_MASK, top, o);
-            const int e = __shfl_xor_sync(FULL_MASK, e_top, o);
-            const float z = __shfl_xor_sync(FULL_MASK, l_top, o);
-            if (v > top || (v == top && e < e_top)) {
-                top = v;
-                e_top = e;
-                l_top = z;
-            }
-        }
+        best_of_lanes<C>(top, e_top, l_top, lane, L);
         const bool found = e_top != kNone;
-        if (!BY_LOGIT && r > 0 && found && before_e >= 0) {
+        if (!BY_LOGIT && r > 0 && found && before - top <= 2 * off + (S)0x1p-21 * (fabs(before) + fabs(top))) {
+            // equal logits and biases are a tie in any arithmetic
             const float b0 = a.bias ? fetch(a.bias + before_e) : 0.f, b1 = a.bias ? fetch(a.bias + e_top) : 0.f;
-            const S p0 = before - (S)b0, p1 = top - (S)b1;
-            if (!(before_l == l_top && b0 == b1))
-                near |= before - top <= rel * max(fabs(p0), fabs(p1)) + (S)0x1p-22 * (fabs(before) + fabs(top) + fabs((S)b0) + fabs((S)b1));
+            near |= !(before_l == l_top && b0 == b1);
         }
         before = top;
         before_l = l_top;
-        before_e = found ? e_top : -1;
+        before_e = found ? e_top : 0;
         if (r < a.top_k && lane == 0) {
-            sh.expert[sub * a.top_k + r] = found ? e_top : -1;
-            sh.logit[sub * a.top_k + r] = l_top;
+            sh.expert[r] = found ? e_top : -1;
+            sh.logit[r] = l_top;
         }
-        if (e_mine == e_top) {
+        if (found && e_top / kPer % L == lane) {
 #pragma unroll
             for (int i = 0; i < C; ++i) {
 #pragma unroll
@@ -241,30 +289,63 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&l)[C][k
     return near;
 }
 
+// An expert's weight from its logit: its score, or its share of the chosen ones' scores.
+struct Weights {
+    float most, total;
+    bool sigmoid;
+    __device__ __forceinline__ float of(float l) const { return score_of<float>(l, sigmoid, most, 1.f) / total; }
+};
+
+// most and sum: of the whole row (softmax without renorm).  Lanes take the chosen experts in turn.
+__device__ __forceinline__ Weights weights_of(const RouteShared& sh, int k, bool sigmoid, bool renorm, float most, float sum, int lane, int L)
+{
+    Weights w{most, sum, sigmoid};
+    if (!renorm) return w;
+    w.most = -INFINITY;
+    for (int r = lane; r < k; r += L)
+        if (sh.expert[r] >= 0) w.most = fmaxf(w.most, sh.logit[r]);
+    w.most = lanes_max(w.most, L);
+    auto add_up = [&]() {
+        float s = 0.f;
+        for (int r = lane; r < k; r += L)
+            if (sh.expert[r] >= 0) s += score_of<float>(sh.logit[r], w.sigmoid, w.most, 1.f);
+        return lanes_sum(s, L);
+    };
+    w.total = add_up();
+    if (sigmoid) {
+        // scores that fp32 does not hold: sigmoid(l) is exp(l) there, to the last bit
+        const bool tiny = w.total < 1e-30f;
+        if (__any_sync(FULL_MASK, tiny)) {
+            w.sigmoid = !tiny;
+            const float total = add_up();
+            if (tiny) w.total = total;
+        }
+    }
+    return w;
+}
+
 template <typename T, int C>
 __global__ void __launch_bounds__(kBlock)
 k_route(RouteArgs a, int L, bool whole)
 {
     extern __shared__ double room[];
     wait_for_kernel_before();
-    const int lane = threadIdx.x & (L - 1), sub = (threadIdx.x & 31) / L, rows = 32 / L, warp = threadIdx.x >> 5;
-    const int64_t row = ((int64_t)blockIdx.x * (kBlock / 32) + warp) * rows + sub, at = min(row, a.n - 1);
+    const int lane = threadIdx.x & (L - 1), rows = kBlock / L, mine = threadIdx.x / L;
+    const int64_t row = (int64_t)blockIdx.x * rows + mine, at = min(row, a.n - 1);
     RouteShared sh;
-    const int grouped = a.groups > 1 ? rows * (a.experts + a.groups) : 0;
-    double* mine = room + warp * grouped;
-    sh.c = mine;
-    sh.best = mine + (grouped ? rows * a.experts : 0);
-    sh.logit = reinterpret_cast<float*>(room + (kBlock / 32) * grouped) + warp * 2 * rows * a.top_k;
-    sh.expert = reinterpret_cast<int32_t*>(sh.logit + rows * a.top_k);
+    const int grouped = a.groups > 1 ? a.experts + a.groups : 0;
+    sh.c = room + mine * grouped;
+    sh.logit = reinterpret_cast<float*>(room + rows * grouped) + mine * 2 * a.top_k;
+    sh.expert = reinterpret_cast<int32_t*>(sh.logit + a.top_k);
     float l[C][kPer];
     load_logits<T, C>(static_cast<const T*>(a.logits) + at * a.experts, a.experts, lane, L, whole, l);
     if (!a.bias && a.groups == 1) {
-        choose<float, true, C>(a, l, lane, L, sub, sh);
+        choose<float, true, C>(a, l, lane, L, sh);
     } else {
-        const bool near = choose<float, false, C>(a, l, lane, L, sub, sh);
+        const bool near = choose<float, false, C>(a, l, lane, L, sh);
         if (__any_sync(FULL_MASK, near)) {
             __syncwarp();
-            choose<double, false, C>(a, l, lane, L, sub, sh);
+            choose<double, false, C>(a, l, lane, L, sh);
         }
     }
     float most = -INFINITY, sum = 1.f;
@@ -279,37 +360,11 @@ k_route(RouteArgs a, int L, bool whole)
         sum = exp_sum<float>(l, most, L);
     }
     __syncwarp();
+    const Weights w = weights_of(sh, a.top_k, sigmoid, a.renorm, most, sum, lane, L);
     if (row >= a.n) return;
-    const int32_t* expert = sh.expert + sub * a.top_k;
-    const float* logit = sh.logit + sub * a.top_k;
-    float total = 1.f;
-    bool tiny = false;
-    if (a.renorm) {
-        total = 0.f;
-        if (!sigmoid) {
-            for (int r = 0; r < a.top_k; ++r)
-                if (expert[r] >= 0) most = fmaxf(most, logit[r]);
-        }
-        for (int r = 0; r < a.top_k; ++r)
-            if (expert[r] >= 0) total += score_of<float>(logit[r], sigmoid, most, 1.f);
-        // scores that fp32 does not hold: sigmoid(l) is exp(l) there, to the last bit
-        tiny = sigmoid && total < 1e-30f;
-        if (tiny) {
-            for (int r = 0; r < a.top_k; ++r)
-                if (expert[r] >= 0) most = fmaxf(most, logit[r]);
-            total = 0.f;
-            for (int r = 0; r < a.top_k; ++r)
-                if (expert[r] >= 0) total += expf(logit[r] - most);
-        }
-    }
     for (int r = lane; r < a.top_k; r += L) {
-        float g = 0.f;
-        if (expert[r] >= 0) {
-            g = score_of<float>(logit[r], sigmoid && !tiny, most, sum);
-            if (a.renorm) g = g / total;
-        }
-        a.expert[row * a.top_k + r] = expert[r];
-        a.gate[row * a.top_k + r] = g * a.scale;
+        a.expert[row * a.top_k + r] = sh.expert[r];
+        a.gate[row * a.top_k + r] = sh.expert[r] >= 0 ? w.of(sh.logit[r]) * a.scale : 0.f;
     }
 }
 
@@ -321,15 +376,27 @@ __global__ void __launch_bounds__(kBlock)
 k_route_grad(RouteGradArgs a, int L, bool whole)
 {
     wait_for_kernel_before();
-    const int lane = threadIdx.x & (L - 1), sub = (threadIdx.x & 31) / L, rows = 32 / L, warp = threadIdx.x >> 5;
-    const int64_t row = ((int64_t)blockIdx.x * (kBlock / 32) + warp) * rows + sub, at = min(row, a.n - 1);
+    extern __shared__ double room[];
+    const int lane = threadIdx.x & (L - 1), rows = kBlock / L, mine = threadIdx.x / L;
+    const int64_t row = (int64_t)blockIdx.x * rows + mine, at = min(row, a.n - 1);
     const T* logits = static_cast<const T*>(a.logits) + at * a.experts;
-    const int32_t* expert = a.expert + at * a.top_k;
-    const float* dgate = a.dgate + at * a.top_k;
     const bool sigmoid = a.score == SPC_SCORE_SIGMOID;
+    RouteShared sh;
+    sh.logit = reinterpret_cast<float*>(room) + mine * 2 * a.top_k;
+    sh.expert = reinterpret_cast<int32_t*>(sh.logit + a.top_k);
+    // the chosen experts' logits, -1 where there is none
+    for (int r = lane; r < a.top_k; r += L) {
+        int e = fetch(a.expert + at * a.top_k + r);
+        if (e < -1 || e >= a.experts) set_status(a.status, SPC_ERR_ROW_INDEX);
+        float l = e >= 0 && e < a.experts ? elem<T>::to_f32(fetch(logits + e)) : -INFINITY;
+        l = l > -INFINITY ? fminf(l, 3.402823466e38f) : -INFINITY;
+        sh.logit[r] = l;
+        sh.expert[r] = l > -INFINITY ? e : -1;
+    }
     float dl[C][kPer];
     float most = -INFINITY, sum = 1.f;
-    if (!sigmoid && !a.renorm) {
+    const bool full = !sigmoid && !a.renorm;
+    if (full) {
         load_logits<T, C>(logits, a.experts, lane, L, whole, dl);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
@@ -337,72 +404,46 @@ k_route_grad(RouteGradArgs a, int L, bool whole)
             for (int j = 0; j < kPer; ++j) most = fmaxf(most, dl[c][j]);
         }
         most = lanes_max(most, L);
-        sum = exp_sum<float>(dl, most, L);
-    }
-    // logit of the r-th chosen expert, -inf where there is none
-    auto chosen = [&](int r, int& e) {
-        e = fetch(expert + r);
-        if (e < 0 || e >= a.experts) {
-            if (e != -1) set_status(a.status, SPC_ERR_ROW_INDEX);
-            e = -1;
-            return -INFINITY;
-        }
-        const float l = elem<T>::to_f32(fetch(logits + e));
-        if (!(l > -INFINITY)) e = -1;
-        return l > -INFINITY ? fminf(l, 3.402823466e38f) : -INFINITY;
-    };
-    int e;
-    float total = 1.f, dot = 0.f;
-    bool tiny = false;
-    if (a.renorm) {
-        float largest = -INFINITY;
-        total = 0.f;
-        for (int r = 0; r < a.top_k; ++r) largest = fmaxf(largest, chosen(r, e));
-        most = largest;
-        for (int r = 0; r < a.top_k; ++r) {
-            const float l = chosen(r, e);
-            if (e >= 0) total += score_of<float>(l, sigmoid, most, 1.f);
-        }
-        tiny = sigmoid && total < 1e-30f;
-        if (tiny) {
-            total = 0.f;
-            for (int r = 0; r < a.top_k; ++r) {
-                const float l = chosen(r, e);
-                if (e >= 0) total += expf(l - most);
+        // exponentials stand in for the logits from here on
+        float s = 0.f;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) {
+                dl[c][j] = dl[c][j] > -INFINITY ? expf(dl[c][j] - most) : 0.f;
+                s += dl[c][j];
             }
         }
+        sum = lanes_sum(s, L);
     }
-    if (a.renorm || !sigmoid) {
-        for (int r = 0; r < a.top_k; ++r) {
-            const float l = chosen(r, e);
-            if (e >= 0) dot += score_of<float>(l, sigmoid && !tiny, most, sum) / total * fetch(dgate + r);
-        }
+    __syncwarp();
+    const Weights w = weights_of(sh, a.top_k, sigmoid, a.renorm, most, sum, lane, L);
+    float dot = 0.f;
+    for (int r = lane; r < a.top_k; r += L)
+        if (sh.expert[r] >= 0) dot += w.of(sh.logit[r]) * fetch(a.dgate + at * a.top_k + r);
+    dot = a.renorm || !sigmoid ? lanes_sum(dot, L) : 0.f;
+    const float rest = full && sum > 0.f ? -a.scale * dot / sum : 0.f;  // sum 0: no expert is available
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) dl[c][j] = full ? rest * dl[c][j] : 0.f;
     }
-    if (!sigmoid && !a.renorm) {
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-#pragma unroll
-            for (int j = 0; j < kPer; ++j)
-                dl[c][j] = dl[c][j] > -INFINITY ? -a.scale * dot * score_of<float>(dl[c][j], false, most, sum) : 0.f;
-        }
-    } else {
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-#pragma unroll
-            for (int j = 0; j < kPer; ++j) dl[c][j] = 0.f;
-        }
+    __syncwarp();
+    // what the chosen ones add, in the place of their logits
+    for (int r = lane; r < a.top_k; r += L) {
+        const float l = sh.logit[r];
+        const float g = w.of(l) * (sigmoid ? 1.f / (1.f + expf(l)) : 1.f);
+        sh.logit[r] = a.scale * g * (fetch(a.dgate + at * a.top_k + r) - (a.renorm ? dot : 0.f));
     }
+    __syncwarp();
     for (int r = 0; r < a.top_k; ++r) {
-        const float l = chosen(r, e);
-        if (e < 0 || (e / kPer) % L != lane) continue;
-        float g = score_of<float>(l, sigmoid && !tiny, most, sum) / total;
-        if (sigmoid) g *= 1.f / (1.f + expf(l));
-        const float d = a.scale * g * (fetch(dgate + r) - (a.renorm ? dot : 0.f));
+        const int e = sh.expert[r];
+        if (e < 0 || e / kPer % L != lane) continue;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
 #pragma unroll
             for (int j = 0; j < kPer; ++j)
-                if ((c * L + lane) * kPer + j == e) dl[c][j] += d;
+                if ((c * L + lane) * kPer + j == e) dl[c][j] += sh.logit[r];
         }
     }
     if (row >= a.n) return;
@@ -435,7 +476,7 @@ template <auto KERNEL, typename A>
 spc_status start(const A& a, size_t smem, bool whole, cudaStream_t st)
 {
     const int L = lanes_for(a.experts);
-    const int64_t blocks = ceil_div(a.n, (int64_t)(kBlock / 32) * (32 / L));
+    const int64_t blocks = ceil_div(a.n, (int64_t)(kBlock / L));
     if (blocks > INT32_MAX) return SPC_ERR_UNSUPPORTED;
     if (smem > 32 * 1024) {  // 48 KB with the static part need no leave
         const spc_status s = allow_smem<KERNEL>();
@@ -457,8 +498,8 @@ template <typename T>
 spc_status fwd(const RouteArgs& a, cudaStream_t st)
 {
     const bool whole = a.experts % kPer == 0 && aligned16(a.logits);
-    const int warps = kBlock / 32, rows = 32 / lanes_for(a.experts);
-    const size_t smem = (size_t)warps * rows * ((a.groups > 1 ? 8 * (size_t)(a.experts + a.groups) : 0) + 8 * (size_t)a.top_k);
+    const size_t rows = kBlock / lanes_for(a.experts);
+    const size_t smem = rows * ((a.groups > 1 ? 8 * (size_t)(a.experts + a.groups) : 0) + 8 * (size_t)a.top_k);
     return a.experts <= 256 ? start<k_route<T, 1>>(a, smem, whole, st) : start<k_route<T, 4>>(a, smem, whole, st);
 }
 
@@ -466,7 +507,8 @@ template <typename T>
 spc_status bwd(const RouteGradArgs& a, cudaStream_t st)
 {
     const bool whole = a.experts % kPer == 0 && aligned16(a.logits) && aligned16(a.dlogits);
-    return a.experts <= 256 ? start<k_route_grad<T, 1>>(a, 0, whole, st) : start<k_route_grad<T, 4>>(a, 0, whole, st);
+    const size_t smem = 8 * (size_t)(kBlock / lanes_for(a.experts)) * a.top_k;
+    return a.experts <= 256 ? start<k_route_grad<T, 1>>(a, smem, whole, st) : start<k_route_grad<T, 4>>(a, smem, whole, st);
 }
 
 }  // namespace

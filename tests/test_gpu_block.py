@@ -179,7 +179,7 @@ def test_route_near_ties(score, groups, kept):
 def test_route_masked_and_extreme_logits(score, renorm, biased):
     inf, nan = math.inf, math.nan
     rows = [[-inf] * 8, [nan] * 8, [-inf, nan, 1, -inf, nan, -inf, -inf, -inf], [inf, 1, inf, 0, -1, -inf, nan, 3],
-            [-300, -301, -302, -500, -inf, -700, -650, -310], [3e38, -3e38, 0, 1, 2, 3, 4, 5], [0] * 8, [90, 100, 110, 88, -88, -90, 0, 1]]
+            [-300, -301, -302, -500, -inf, -700, -650, -310], [3e38, -3e38, 0, 1, 2, 3, 4, 5], [0.0, -0.0] * 4, [-0.0, 0.0] * 4, [90, 100, 110, 88, -88, -90, 0, 1]]
     logits = torch.tensor(rows, dtype=torch.float32)
     bias = torch.linspace(0.5, -0.5, 8) if biased else None
     kind = spc.SPC_SCORE_SIGMOID if score == "sigmoid" else spc.SPC_SCORE_SOFTMAX
@@ -187,7 +187,7 @@ def test_route_masked_and_extreme_logits(score, renorm, biased):
     got, w = spc.spc_route_fwd(to(logits), 3, score=kind, bias=to(bias), renorm=renorm)
     assert torch.equal(got.cpu(), expert)
     close(w, gate, bound + 1e-30)
-    dgate = torch.linspace(-1, 1, 24).view(8, 3)
+    dgate = torch.linspace(-1, 1, 27).view(9, 3)
     want, bound = ref.route_bwd(dgate, logits, expert, score, renorm, 1.0)
     close(spc.spc_route_bwd(to(dgate), to(logits), got, score=kind, renorm=renorm), want, bound + 1e-30)
 
@@ -241,8 +241,10 @@ def on_cores(dtype, d):
 def run_attention(q, k, v, dout, seg, seg_k, dtype, scale=None, st=None):
     t_seg = torch.tensor(seg, dtype=torch.int32, device=dev())
     t_seg_k = None if seg_k is seg else torch.tensor(seg_k, dtype=torch.int32, device=dev())
+    st = spc.new_status(dev()) if st is None else st
     o, lse = spc.spc_attention_fwd(to(q), to(k), to(v), t_seg, seg_k=t_seg_k, scale=scale, status=st)
     grads = spc.spc_attention_bwd(to(dout), to(q), to(k), to(v), o, lse, t_seg, seg_k=t_seg_k, scale=scale, status=st)
+    spc.check_status(st)
     return o, lse, grads
 
 
