@@ -3,7 +3,8 @@
 // A block keeps TILES tiles of 128 query rows (the positions of a segment, and the query heads that share a key head
 // beside one another, so that keys are read once for all of them) and walks over the segment's keys 64 at a time:
 //   warp 0 loads the queries once and keys and values in turn into a ring of stages (TMA);
-//   warp 1 issues S = Q K^T into tensor memory and O += P V with P from tensor memory;
+//   a warp for each tile issues S = Q K^T into tensor memory and O += P V with P from tensor memory (a warp's waits
+//     queue up behind its own products, so one warp for two tiles left the tensor cores idle half of the time);
 //   four warps for each tile take S, a thread to a row: running maximum, exponentials, P as 16 bits in the place of S.
 // S has two buffers a tile, so the next scores are there when a tile's exponentials are done, and with two tiles the
 // products of one run while the other's exponentials are taken.  O stays in tensor memory; it is
@@ -28,9 +29,10 @@ struct Shape {
     static constexpr int kPart = kKeys * 128 * kBoxes;        // bytes of a step's keys, or values
     static constexpr int kStage = 2 * kPart;                  // the values of a step, the keys of the next but one
     static constexpr int kStages = TILES == 1 && D == 128 ? 2 : 4;
-    static constexpr int kThreads = 64 + 128 * TILES;
+    static constexpr int kSoftmax = TILES == 2 ? 4 : 2;       // the first of four softmax warps a tile
+    static constexpr int kThreads = 32 * kSoftmax + 128 * TILES;
     static constexpr int kCols = TILES == 2 ? 512 : 256;      // tensor memory: 128 of scores and D of sums a tile
-    static constexpr int kBars = 2 * kStages + 2 + 6 * TILES;
+    static constexpr int kBars = 2 * kStages + 1 + 7 * TILES;
     static constexpr size_t kSmem = 1024 + (size_t)TILES * kTile + (size_t)kStages * kStage + 8 * kBars + 16;
 };
 
@@ -53,7 +55,7 @@ k_attn_tc(AttnArgs a, Packing pk, uint64_t wait_ns, const __grid_constant__ CUte
     uint64_t* empty = full + S::kStages;
     uint64_t* q_full = empty + S::kStages;
     uint64_t* drain = q_full + 1;
-    uint64_t* s_full = drain + 1;             // [tile][buffer]: the scores of a step, and the sums of the one two before
+    uint64_t* s_full = drain + TILES;             // [tile][buffer]: the scores of a step, and the sums of the one two before
     uint64_t* p_full = s_full + 2 * TILES;    // [tile][buffer]
     uint64_t* o_last = p_full + 2 * TILES;    // [tile]: the sums of the last step but one
     uint64_t* o_done = o_last + TILES;        // [tile]: and of the last one
@@ -77,10 +79,10 @@ k_attn_tc(AttnArgs a, Packing pk, uint64_t wait_ns, const __grid_constant__ CUte
     if (tid == 0) {
         for (int s = 0; s < S::kStages; ++s) {
             ptx::mbar_init(&full[s], 1);
-            ptx::mbar_init(&empty[s], 1);
+            ptx::mbar_init(&empty[s], tiles);
         }
         ptx::mbar_init(q_full, 1);
-        ptx::mbar_init(drain, 1);
+        for (int i = 0; i < TILES; ++i) ptx::mbar_init(&drain[i], 1);
         for (int i = 0; i < 2 * TILES; ++i) {
             ptx::mbar_init(&s_full[i], 1);
             ptx::mbar_init(&p_full[i], 4);
@@ -136,57 +138,53 @@ k_attn_tc(AttnArgs a, Packing pk, uint64_t wait_ns, const __grid_constant__ CUte
             ptx::mbar_wait(q_full, 0, kAttnDrainNs);
             for (int i = max(j - S::kStages, 0); i < j; ++i) ptx::mbar_wait(&full[i % S::kStages], (i / S::kStages) & 1, kAttnDrainNs);
         }
-    } else if (warp == 1) {
+    } else if (warp <= TILES) {
         // ------------------------------------------------------------- MMAs
-        if (n > 0) {
+        const int i = warp - 1;
+        if (n > 0 && i < tiles) {
             const int steps = (a.d + 15) / 16;
             const uint32_t id_s = ptx::idesc_make(AttnFmt<T>::v, 128, kKeys);
             const uint32_t id_o = ptx::idesc_make(AttnFmt<T>::v, 128, steps * 16) | 1u << 16;
-            const uint64_t q_desc = ptx::desc_k_sw128(q_base);
+            const uint64_t q_desc = ptx::desc_k_sw128(q_base + i * S::kTile);
             const uint64_t k_desc = ptx::desc_k_sw128(ring_base + S::kPart), v_desc = ptx::desc_mn_sw128(ring_base, kKeys * 128);
-            auto scores = [&](int i, int j) {  // by one lane
+            const uint32_t s_at = tmem + i * 128, o_at = tmem + TILES * 128 + i * D;
+            auto scores = [&](int j) {  // by one lane
                 const uint64_t keys = k_desc + (j + S::kStages - 2) % S::kStages * (S::kStage >> 4);
-                attn_mma_ss<D / 16>(tmem + i * 128 + (j & 1) * 64, q_desc + i * (S::kTile >> 4), 16384, keys, kKeys * 128, id_s, steps);
+                attn_mma_ss<D / 16>(s_at + (j & 1) * 64, q_desc, 16384, keys, kKeys * 128, id_s, steps);
                 ptx::mma_commit(&s_full[2 * i + (j & 1)]);
             };
             ok = attn_wait(q_full, 0, wait_ns);
             ptx::tc_fence_after();
             if (ok && attn_elect())
                 for (int j = 0; j < min(n, 2); ++j) {
-                    for (int i = 0; i < tiles; ++i) scores(i, j);
+                    scores(j);
                     ptx::mma_commit(&empty[S::kStages - 2 + j]);
                 }
             __syncwarp();
             for (int j = 0; j < n && ok; ++j) {
                 const int s = j % S::kStages;
-                ok = attn_wait(&full[s], (j / S::kStages) & 1, wait_ns);
+                ok = attn_wait(&full[s], (j / S::kStages) & 1, wait_ns) && attn_wait(&p_full[2 * i + (j & 1)], (j >> 1) & 1, wait_ns);
+                if (!ok) break;
+                ptx::tc_fence_after();
+                if (attn_elect()) {
 #pragma unroll
-                for (int i = 0; i < TILES; ++i) {
-                    if (i >= tiles || !ok) break;
-                    ok = attn_wait(&p_full[2 * i + (j & 1)], (j >> 1) & 1, wait_ns);
-                    if (!ok) break;
-                    ptx::tc_fence_after();
-                    if (attn_elect()) {
-#pragma unroll
-                        for (int q = 0; q < kKeys / 16; ++q)
-                            ptx::mma_f16_ts(tmem + TILES * 128 + i * D, tmem + i * 128 + (j & 1) * 64 + q * 8,
-                                            v_desc + s * (S::kStage >> 4) + q * 128, id_o, q > 0 || j > 0);
-                        // in the place of P, which the products before have read by then
-                        if (j + 2 < n) scores(i, j + 2);
-                        else ptx::mma_commit(j + 2 == n ? &o_last[i] : &o_done[i]);
-                        if (i == tiles - 1) ptx::mma_commit(&empty[s]);
-                    }
-                    __syncwarp();
+                    for (int q = 0; q < kKeys / 16; ++q)
+                        ptx::mma_f16_ts(o_at, s_at + (j & 1) * 64 + q * 8, v_desc + s * (S::kStage >> 4) + q * 128, id_o, q > 0 || j > 0);
+                    // in the place of P, which the products before have read by then
+                    if (j + 2 < n) scores(j + 2);
+                    else ptx::mma_commit(j + 2 == n ? &o_last[i] : &o_done[i]);
+                    ptx::mma_commit(&empty[s]);
                 }
+                __syncwarp();
             }
             if (!ok && lane == 0) set_status(a.status, SPC_ERR_TIMEOUT);
-            if (attn_elect()) ptx::mma_commit(drain);
+            if (attn_elect()) ptx::mma_commit(&drain[i]);
             __syncwarp();
-            ptx::mbar_wait(drain, 0, kAttnDrainNs);
+            ptx::mbar_wait(&drain[i], 0, kAttnDrainNs);
         }
-    } else {
+    } else if (warp >= S::kSoftmax) {
         // ---------------------------------------------------------- softmax
-        const int i = (warp - 2) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+        const int i = (warp - S::kSoftmax) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
         if (i < tiles) {
             const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
             const uint32_t s_at = tmem + lanes + i * 128, o_at = tmem + lanes + TILES * 128 + i * D;
@@ -251,7 +249,7 @@ k_attn_tc(AttnArgs a, Packing pk, uint64_t wait_ns, const __grid_constant__ CUte
                 sum[0] = add(sum[0], sum[1]);
                 l += sum[0].x + sum[0].y;
                 ptx::tmem_st_wait();
-                if (i == 0 && valid < kKeys) {
+                if (valid < kKeys) {  // by each tile's warps: its own products wait for them alone
                     ok = attn_wait(&full[j % S::kStages], (j / S::kStages) & 1, wait_ns);
                     if (!ok) break;
                     attn_clear_rows<S::kBoxes>(ring_base + (uint32_t)(j % S::kStages) * S::kStage, kKeys, valid, r, 128);
