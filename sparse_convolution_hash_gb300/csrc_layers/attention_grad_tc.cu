@@ -28,7 +28,7 @@ struct Shape {
     static constexpr int kStage = 2 * kHalf;
     static constexpr int kStages = 4;
     static constexpr int kThreads = 384;
-    static constexpr int kBars = 2 * kStages + 7;
+    static constexpr int kBars = 3 * kStages + 10;
     static constexpr size_t kSmem = 1024 + 2 * (size_t)kKept + (size_t)kStages * (kStage + 2 * kStep * 4) + 8 * kBars + 16;
 };
 
@@ -134,12 +134,14 @@ k_attn_grad_tc(AttnArgs a, uint64_t wait_ns, const __grid_constant__ CUtensorMap
     uint8_t* ring = smem + 2 * S::kKept;
     float* stats = reinterpret_cast<float*>(ring + (size_t)S::kStages * S::kStage);  // [stages][2][kStep]: -lse log2 e, -delta
     uint64_t* full = reinterpret_cast<uint64_t*>(stats + S::kStages * 2 * kStep);
-    uint64_t* ready = full + S::kStages;
+    uint64_t* empty = full + S::kStages;
+    uint64_t* ready = empty + S::kStages;
     uint64_t* kept_full = ready + S::kStages;
-    uint64_t* drain = kept_full + 1;
-    uint64_t* s_full = drain + 1;
-    uint64_t* p_full = s_full + 2;
-    uint64_t* o_full = p_full + 2;
+    uint64_t* drain = kept_full + 1;   // of the two warps that issue
+    uint64_t* s_full = drain + 2;      // [buffer]: S and dP of a step
+    uint64_t* p_full = s_full + 2;     // [buffer]: P and dS
+    uint64_t* sum_full = p_full + 2;   // [buffer]: the sums with them
+    uint64_t* o_full = sum_full + 2;   // all sums
     uint32_t* s_ctrl = reinterpret_cast<uint32_t*>(o_full + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -161,11 +163,13 @@ k_attn_grad_tc(AttnArgs a, uint64_t wait_ns, const __grid_constant__ CUtensorMap
     if (tid == 0) {
         for (int s = 0; s < S::kStages; ++s) {
             ptx::mbar_init(&full[s], 1);
+            ptx::mbar_init(&empty[s], 1);
             ptx::mbar_init(&ready[s], 32);
         }
         ptx::mbar_init(kept_full, 1);
-        ptx::mbar_init(drain, 1);
         for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(&drain[i], 1);
+            ptx::mbar_init(&sum_full[i], 1);
             ptx::mbar_init(&s_full[i], 1);
             ptx::mbar_init(&p_full[i], 4);
         }
@@ -183,11 +187,6 @@ k_attn_grad_tc(AttnArgs a, uint64_t wait_ns, const __grid_constant__ CUtensorMap
     // tensor memory: step buffers of 128 columns (S, dP), then the sums: dv and dk, or dq
     const uint32_t sum1 = tmem + 256, sum2 = tmem + 256 + D;
     bool ok = true;
-    // Until step it's stage may be written: the products that read it before come ahead of the scores of step it - 2, which
-    // no step's loads may pass.  Called for every step from the second on, as a parity tells a phase from its neighbours only.
-    static_assert(S::kStages == 4, "");
-    auto stage_free = [&](int it) { return attn_wait(&s_full[it & 1], ((it - 2) >> 1) & 1, wait_ns); };
-
     if (warp == 0) {
         // ------------------------------------------------------------ loads
         if (n > 0) {
@@ -203,7 +202,7 @@ k_attn_grad_tc(AttnArgs a, uint64_t wait_ns, const __grid_constant__ CUtensorMap
             int it = 0, head = step_head(0), row = (int)step_row(0);
             for (; it < n; ++it) {
                 const int s = it % S::kStages;
-                if (it >= 2) ok = stage_free(it);
+                if (it >= S::kStages) ok = attn_wait(&empty[s], (it / S::kStages - 1) & 1, wait_ns);
                 if (!ok) break;
                 if (attn_elect()) {
                     const uint32_t base = ring_base + (uint32_t)s * S::kStage, bar = ptx::smem_u32(&full[s]);
@@ -227,57 +226,63 @@ k_attn_grad_tc(AttnArgs a, uint64_t wait_ns, const __grid_constant__ CUtensorMap
             for (int j = it > S::kStages ? it - S::kStages : 0; j < it; ++j)
                 ptx::mbar_wait(&full[j % S::kStages], (j / S::kStages) & 1, kAttnDrainNs);
         }
-    } else if (warp == 1) {
-        // ------------------------------------------------------------- MMAs
+    } else if (warp == 1 || warp == 3) {
+        // -------------------- MMAs: S and dP by one warp, the sums by another, as a warp's waits queue up behind its own
         if (n > 0) {
             const int steps = (a.d + 15) / 16;
-            const uint32_t id_s = ptx::idesc_make(AttnFmt<T>::v, 128, kStep);
-            const uint32_t id_o = ptx::idesc_make(AttnFmt<T>::v, 128, steps * 16) | 1u << 16;
-            const uint64_t kept_desc = ptx::desc_k_sw128(kept_base), k_desc = ptx::desc_k_sw128(ring_base);
-            const uint64_t mn_desc = ptx::desc_mn_sw128(ring_base, kStep * 128);
-            auto there = [&](int j) {
-                const int s = j % S::kStages;
-                const uint32_t parity = (j / S::kStages) & 1;
-                return attn_wait(&full[s], parity, wait_ns) && (!KEYS || attn_wait(&ready[s], parity, wait_ns));
-            };
-            auto scores = [&](int j) {  // by one lane
-                const uint64_t b = k_desc + j % S::kStages * (S::kStage >> 4);
-                const uint32_t d = tmem + (j & 1) * 128;
-                attn_mma_ss<D / 16>(d, kept_desc, 16384, b, kStep * 128, id_s, steps);
-                attn_mma_ss<D / 16>(d + 64, kept_desc + (S::kKept >> 4), 16384, b + (S::kHalf >> 4), kStep * 128, id_s, steps);
-                ptx::mma_commit(&s_full[j & 1]);
-            };
-            ok = attn_wait(kept_full, 0, wait_ns);
-            for (int j = 0; j < min(n, 2) && ok; ++j) {
-                ok = there(j);
-                ptx::tc_fence_after();
-                if (ok && attn_elect()) scores(j);
-                __syncwarp();
-            }
-            for (int j = 0; j < n && ok; ++j) {
-                if (j + 2 < n) ok = there(j + 2);
-                if (ok) ok = attn_wait(&p_full[j & 1], (j >> 1) & 1, wait_ns);
-                if (!ok) break;
-                ptx::tc_fence_after();
-                if (attn_elect()) {
-                    const uint32_t p = tmem + (j & 1) * 128;
-                    const uint64_t d1 = mn_desc + j % S::kStages * (S::kStage >> 4), d2 = d1 + (S::kHalf >> 4);
-                    if (KEYS) {
-#pragma unroll
-                        for (int q = 0; q < kStep / 16; ++q) ptx::mma_f16_ts(sum1, p + q * 8, d2 + q * 128, id_o, q > 0 || j > 0);  // dV += P^T dO
+            if (warp == 1) {
+                const uint32_t idesc = ptx::idesc_make(AttnFmt<T>::v, 128, kStep);
+                const uint64_t kept_desc = ptx::desc_k_sw128(kept_base), k_desc = ptx::desc_k_sw128(ring_base);
+                ok = attn_wait(kept_full, 0, wait_ns);
+                for (int j = 0; j < n && ok; ++j) {
+                    const int s = j % S::kStages;
+                    const uint32_t parity = (j / S::kStages) & 1;
+                    ok = attn_wait(&full[s], parity, wait_ns) && (!KEYS || attn_wait(&ready[s], parity, wait_ns));
+                    // in the place of P and dS, once the sums of step j - 2 have them
+                    if (ok && j >= 2) ok = attn_wait(&sum_full[j & 1], ((j - 2) >> 1) & 1, wait_ns);
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    if (attn_elect()) {
+                        const uint64_t b = k_desc + s * (S::kStage >> 4);
+                        const uint32_t d = tmem + (j & 1) * 128;
+                        attn_mma_ss<D / 16>(d, kept_desc, 16384, b, kStep * 128, idesc, steps);
+                        attn_mma_ss<D / 16>(d + 64, kept_desc + (S::kKept >> 4), 16384, b + (S::kHalf >> 4), kStep * 128, idesc, steps);
+                        ptx::mma_commit(&s_full[j & 1]);
                     }
-#pragma unroll
-                    for (int q = 0; q < kStep / 16; ++q)  // dK += dS^T Q, dQ += dS K
-                        ptx::mma_f16_ts(KEYS ? sum2 : sum1, p + 64 + q * 8, d1 + q * 128, id_o, q > 0 || j > 0);
-                    if (j + 2 < n) scores(j + 2);
-                    else if (j + 1 == n) ptx::mma_commit(o_full);
+                    __syncwarp();
                 }
-                __syncwarp();
+            } else {
+                const uint32_t idesc = ptx::idesc_make(AttnFmt<T>::v, 128, steps * 16) | 1u << 16;
+                const uint64_t mn_desc = ptx::desc_mn_sw128(ring_base, kStep * 128);
+                for (int j = 0; j < n && ok; ++j) {
+                    const int s = j % S::kStages;
+                    const uint32_t parity = (j / S::kStages) & 1;
+                    ok = attn_wait(&full[s], parity, wait_ns) && (!KEYS || attn_wait(&ready[s], parity, wait_ns)) &&
+                         attn_wait(&p_full[j & 1], (j >> 1) & 1, wait_ns);
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    if (attn_elect()) {
+                        const uint32_t p = tmem + (j & 1) * 128;
+                        const uint64_t d1 = mn_desc + s * (S::kStage >> 4), d2 = d1 + (S::kHalf >> 4);
+                        if (KEYS) {
+#pragma unroll
+                            for (int q = 0; q < kStep / 16; ++q) ptx::mma_f16_ts(sum1, p + q * 8, d2 + q * 128, idesc, q > 0 || j > 0);  // dV += P^T dO
+                        }
+#pragma unroll
+                        for (int q = 0; q < kStep / 16; ++q)  // dK += dS^T Q, dQ += dS K
+                            ptx::mma_f16_ts(KEYS ? sum2 : sum1, p + 64 + q * 8, d1 + q * 128, idesc, q > 0 || j > 0);
+                        ptx::mma_commit(&sum_full[j & 1]);
+                        ptx::mma_commit(&empty[s]);
+                        if (j + 1 == n) ptx::mma_commit(o_full);
+                    }
+                    __syncwarp();
+                }
             }
             if (!ok && lane == 0) set_status(a.status, SPC_ERR_TIMEOUT);
-            if (attn_elect()) ptx::mma_commit(drain);
+            uint64_t* mine = &drain[warp >> 1];
+            if (attn_elect()) ptx::mma_commit(mine);
             __syncwarp();
-            ptx::mbar_wait(drain, 0, kAttnDrainNs);
+            ptx::mbar_wait(mine, 0, kAttnDrainNs);
         }
     } else if (warp == 2) {
         // ------------------------------- the queries' log-sums and row sums, and rows past the segment's end
@@ -286,7 +291,7 @@ k_attn_grad_tc(AttnArgs a, uint64_t wait_ns, const __grid_constant__ CUtensorMap
             int head = n > 0 ? step_head(0) : 0;
             for (int it = 0; it < n; ++it) {
                 const int s = it % S::kStages;
-                if (it >= 2) ok = stage_free(it);
+                if (it >= S::kStages) ok = attn_wait(&empty[s], (it / S::kStages - 1) & 1, wait_ns);
                 if (!ok) break;
                 const int64_t at = (int64_t)head * a.nq + row;
                 const int valid = (int)min((int64_t)kStep, t.hi - row);

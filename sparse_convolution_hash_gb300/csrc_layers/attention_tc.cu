@@ -2,10 +2,11 @@
 //
 // A block keeps TILES tiles of 128 query rows (the positions of a segment, and the query heads that share a key head
 // beside one another, so that keys are read once for all of them) and walks over the segment's keys 64 at a time:
-//   warp 0 loads the queries once and keys and values in turn into a ring of stages (TMA);
-//   a warp for each tile issues S = Q K^T into tensor memory and O += P V with P from tensor memory (a warp's waits
-//     queue up behind its own products, so one warp for two tiles left the tensor cores idle half of the time);
-//   four warps for each tile take S, a thread to a row: running maximum, exponentials, P as 16 bits in the place of S.
+//   four warps for each tile take S, a thread to a row: running maximum, exponentials, P as 16 bits in the place of S;
+//   a warp loads the queries once and keys and values into a ring of stages (TMA);
+//   two warps for each tile issue S = Q K^T into tensor memory, and O += P V with P from tensor memory.  A warp's waits
+//     queue up behind its own products: one warp for all of them left the tensor cores idle half of the time
+//     (32,768 rows in 2 samples, 8 heads of 128: 2,005 us), a warp for each tile a third of it at d = 64.
 // S has two buffers a tile, so the next scores are there when a tile's exponentials are done, and with two tiles the
 // products of one run while the other's exponentials are taken.  O stays in tensor memory; it is
 // rescaled only when a row's maximum has grown by more than 2^8, so almost never after the first tiles
@@ -29,10 +30,10 @@ struct Shape {
     static constexpr int kPart = kKeys * 128 * kBoxes;        // bytes of a step's keys, or values
     static constexpr int kStage = 2 * kPart;                  // the values of a step, the keys of the next but one
     static constexpr int kStages = TILES == 1 && D == 128 ? 2 : 4;
-    static constexpr int kSoftmax = TILES == 2 ? 4 : 2;       // the first of four softmax warps a tile
-    static constexpr int kThreads = 32 * kSoftmax + 128 * TILES;
+    static constexpr int kLoad = 4 * TILES;                   // the warp that loads; after it those that issue
+    static constexpr int kThreads = 32 * (kLoad + 1 + 2 * TILES);
     static constexpr int kCols = TILES == 2 ? 512 : 256;      // tensor memory: 128 of scores and D of sums a tile
-    static constexpr int kBars = 2 * kStages + 1 + 7 * TILES;
+    static constexpr int kBars = 3 * kStages + 1 + 8 * TILES;
     static constexpr size_t kSmem = 1024 + (size_t)TILES * kTile + (size_t)kStages * kStage + 8 * kBars + 16;
 };
 
@@ -52,14 +53,14 @@ k_attn_tc(AttnArgs a, Packing pk, uint64_t wait_ns, const __grid_constant__ CUte
     // a stage: the values of a step, then the keys of the next but one (the last two begin with those of steps 0 and 1)
     uint8_t* ring = smem + TILES * S::kTile;
     uint64_t* full = reinterpret_cast<uint64_t*>(ring + (size_t)S::kStages * S::kStage);
-    uint64_t* empty = full + S::kStages;
-    uint64_t* q_full = empty + S::kStages;
-    uint64_t* drain = q_full + 1;
-    uint64_t* s_full = drain + TILES;             // [tile][buffer]: the scores of a step, and the sums of the one two before
-    uint64_t* p_full = s_full + 2 * TILES;    // [tile][buffer]
-    uint64_t* o_last = p_full + 2 * TILES;    // [tile]: the sums of the last step but one
-    uint64_t* o_done = o_last + TILES;        // [tile]: and of the last one
-    uint32_t* s_ctrl = reinterpret_cast<uint32_t*>(o_done + TILES);
+    uint64_t* k_empty = full + S::kStages;
+    uint64_t* v_empty = k_empty + S::kStages;
+    uint64_t* q_full = v_empty + S::kStages;
+    uint64_t* drain = q_full + 1;             // [tile][2]
+    uint64_t* s_full = drain + 2 * TILES;     // [tile][buffer]: the scores of a step
+    uint64_t* p_full = s_full + 2 * TILES;    // [tile][buffer]: its probabilities
+    uint64_t* o_full = p_full + 2 * TILES;    // [tile][buffer]: the sums with them
+    uint32_t* s_ctrl = reinterpret_cast<uint32_t*>(o_full + 2 * TILES);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     wait_for_kernel_before();
@@ -79,18 +80,19 @@ k_attn_tc(AttnArgs a, Packing pk, uint64_t wait_ns, const __grid_constant__ CUte
     if (tid == 0) {
         for (int s = 0; s < S::kStages; ++s) {
             ptx::mbar_init(&full[s], 1);
-            ptx::mbar_init(&empty[s], tiles);
+            ptx::mbar_init(&k_empty[s], tiles);
+            ptx::mbar_init(&v_empty[s], tiles);
         }
         ptx::mbar_init(q_full, 1);
-        for (int i = 0; i < TILES; ++i) ptx::mbar_init(&drain[i], 1);
         for (int i = 0; i < 2 * TILES; ++i) {
+            ptx::mbar_init(&drain[i], 1);
             ptx::mbar_init(&s_full[i], 1);
             ptx::mbar_init(&p_full[i], 4);
+            ptx::mbar_init(&o_full[i], 1);
         }
-        for (int i = 0; i < 2 * TILES; ++i) ptx::mbar_init(&o_last[i], 1);
         ptx::mbar_init_fence();
     }
-    if (warp == 1) {
+    if (warp == S::kLoad) {
         ptx::tmem_alloc(s_ctrl, S::kCols);
         ptx::tmem_relinquish();
     }
@@ -102,7 +104,7 @@ k_attn_tc(AttnArgs a, Packing pk, uint64_t wait_ns, const __grid_constant__ CUte
     bool ok = true;
 
 
-    if (warp == 0) {
+    if (warp == S::kLoad) {
         // ------------------------------------------------------------ loads
         if (n > 0) {
             auto load = [&](uint32_t to, const CUtensorMap* map, int step, uint64_t* bar) {
@@ -121,9 +123,10 @@ k_attn_tc(AttnArgs a, Packing pk, uint64_t wait_ns, const __grid_constant__ CUte
             __syncwarp();
             int j = 0;
             for (; j < n; ++j) {
-                // freed once for each step that used it, and the last two by the scores of steps 0 and 1 besides
-                const int s = j % S::kStages, freed = j / S::kStages + (s >= S::kStages - 2);
-                if (freed > 0) ok = attn_wait(&empty[s], (freed - 1) & 1, wait_ns);
+                // freed once for each step that used it, and the keys' part of the last two by steps 0 and 1 besides
+                const int s = j % S::kStages, round = j / S::kStages, keys = round + (s >= S::kStages - 2);
+                if (round > 0) ok = attn_wait(&v_empty[s], (round - 1) & 1, wait_ns);
+                if (keys > 0 && ok) ok = attn_wait(&k_empty[s], (keys - 1) & 1, wait_ns);
                 if (!ok) break;
                 if (attn_elect()) {
                     const uint32_t to = ring_base + s * S::kStage;
@@ -138,53 +141,58 @@ k_attn_tc(AttnArgs a, Packing pk, uint64_t wait_ns, const __grid_constant__ CUte
             ptx::mbar_wait(q_full, 0, kAttnDrainNs);
             for (int i = max(j - S::kStages, 0); i < j; ++i) ptx::mbar_wait(&full[i % S::kStages], (i / S::kStages) & 1, kAttnDrainNs);
         }
-    } else if (warp <= TILES) {
+    } else if (warp > S::kLoad) {
         // ------------------------------------------------------------- MMAs
-        const int i = warp - 1;
+        const int i = (warp - S::kLoad - 1) >> 1;
+        const bool scores = (warp - S::kLoad) & 1;
         if (n > 0 && i < tiles) {
             const int steps = (a.d + 15) / 16;
-            const uint32_t id_s = ptx::idesc_make(AttnFmt<T>::v, 128, kKeys);
-            const uint32_t id_o = ptx::idesc_make(AttnFmt<T>::v, 128, steps * 16) | 1u << 16;
-            const uint64_t q_desc = ptx::desc_k_sw128(q_base + i * S::kTile);
-            const uint64_t k_desc = ptx::desc_k_sw128(ring_base + S::kPart), v_desc = ptx::desc_mn_sw128(ring_base, kKeys * 128);
             const uint32_t s_at = tmem + i * 128, o_at = tmem + TILES * 128 + i * D;
-            auto scores = [&](int j) {  // by one lane
-                const uint64_t keys = k_desc + (j + S::kStages - 2) % S::kStages * (S::kStage >> 4);
-                attn_mma_ss<D / 16>(s_at + (j & 1) * 64, q_desc, 16384, keys, kKeys * 128, id_s, steps);
-                ptx::mma_commit(&s_full[2 * i + (j & 1)]);
-            };
-            ok = attn_wait(q_full, 0, wait_ns);
-            ptx::tc_fence_after();
-            if (ok && attn_elect())
-                for (int j = 0; j < min(n, 2); ++j) {
-                    scores(j);
-                    ptx::mma_commit(&empty[S::kStages - 2 + j]);
+            if (scores) {
+                const uint32_t idesc = ptx::idesc_make(AttnFmt<T>::v, 128, kKeys);
+                const uint64_t q_desc = ptx::desc_k_sw128(q_base + i * S::kTile), k_desc = ptx::desc_k_sw128(ring_base + S::kPart);
+                ok = attn_wait(q_full, 0, wait_ns);
+                for (int j = 0; j < n && ok; ++j) {
+                    const int s = (j + S::kStages - 2) % S::kStages;
+                    // in the place of P, once the sums of step j - 2 have it
+                    if (j >= 2)
+                        ok = attn_wait(&full[s], ((j - 2) / S::kStages) & 1, wait_ns) && attn_wait(&o_full[2 * i + (j & 1)], ((j - 2) >> 1) & 1, wait_ns);
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    if (attn_elect()) {
+                        attn_mma_ss<D / 16>(s_at + (j & 1) * 64, q_desc, 16384, k_desc + s * (S::kStage >> 4), kKeys * 128, idesc, steps);
+                        ptx::mma_commit(&s_full[2 * i + (j & 1)]);
+                        ptx::mma_commit(&k_empty[s]);
+                    }
+                    __syncwarp();
                 }
-            __syncwarp();
-            for (int j = 0; j < n && ok; ++j) {
-                const int s = j % S::kStages;
-                ok = attn_wait(&full[s], (j / S::kStages) & 1, wait_ns) && attn_wait(&p_full[2 * i + (j & 1)], (j >> 1) & 1, wait_ns);
-                if (!ok) break;
-                ptx::tc_fence_after();
-                if (attn_elect()) {
+            } else {
+                const uint32_t idesc = ptx::idesc_make(AttnFmt<T>::v, 128, steps * 16) | 1u << 16;
+                const uint64_t v_desc = ptx::desc_mn_sw128(ring_base, kKeys * 128);
+                for (int j = 0; j < n && ok; ++j) {
+                    const int s = j % S::kStages;
+                    ok = attn_wait(&full[s], (j / S::kStages) & 1, wait_ns) && attn_wait(&p_full[2 * i + (j & 1)], (j >> 1) & 1, wait_ns);
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    if (attn_elect()) {
 #pragma unroll
-                    for (int q = 0; q < kKeys / 16; ++q)
-                        ptx::mma_f16_ts(o_at, s_at + (j & 1) * 64 + q * 8, v_desc + s * (S::kStage >> 4) + q * 128, id_o, q > 0 || j > 0);
-                    // in the place of P, which the products before have read by then
-                    if (j + 2 < n) scores(j + 2);
-                    else ptx::mma_commit(j + 2 == n ? &o_last[i] : &o_done[i]);
-                    ptx::mma_commit(&empty[s]);
+                        for (int q = 0; q < kKeys / 16; ++q)
+                            ptx::mma_f16_ts(o_at, s_at + (j & 1) * 64 + q * 8, v_desc + s * (S::kStage >> 4) + q * 128, idesc, q > 0 || j > 0);
+                        ptx::mma_commit(&o_full[2 * i + (j & 1)]);
+                        ptx::mma_commit(&v_empty[s]);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
             }
             if (!ok && lane == 0) set_status(a.status, SPC_ERR_TIMEOUT);
-            if (attn_elect()) ptx::mma_commit(&drain[i]);
+            uint64_t* mine = &drain[2 * i + scores];
+            if (attn_elect()) ptx::mma_commit(mine);
             __syncwarp();
-            ptx::mbar_wait(&drain[i], 0, kAttnDrainNs);
+            ptx::mbar_wait(mine, 0, kAttnDrainNs);
         }
-    } else if (warp >= S::kSoftmax) {
+    } else {
         // ---------------------------------------------------------- softmax
-        const int i = (warp - S::kSoftmax) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+        const int i = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
         if (i < tiles) {
             const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
             const uint32_t s_at = tmem + lanes + i * 128, o_at = tmem + lanes + TILES * 128 + i * D;
@@ -220,8 +228,8 @@ k_attn_tc(AttnArgs a, Packing pk, uint64_t wait_ns, const __grid_constant__ CUte
                     if (grow) m = top;
                     l *= shrink;
                     if (j > 0) {
-                        // the sums of step j - 1
-                        ok = j + 1 < n ? attn_wait(&s_full[2 * i + ((j + 1) & 1)], ((j + 1) >> 1) & 1, wait_ns) : attn_wait(&o_last[i], 0, wait_ns);
+                        // the sums of step j - 1 (the scores of step j - 1 showed those of step j - 3, so the parity is not mistaken)
+                        ok = attn_wait(&o_full[2 * i + ((j - 1) & 1)], ((j - 1) >> 1) & 1, wait_ns);
                         if (!ok) break;
                         ptx::tc_fence_after();
 #pragma unroll 1
@@ -258,7 +266,7 @@ k_attn_tc(AttnArgs a, Packing pk, uint64_t wait_ns, const __grid_constant__ CUte
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(&p_full[2 * i + (j & 1)]);
             }
-            if (ok && n > 0) ok = attn_wait(&o_done[i], 0, wait_ns);
+            if (ok && n > 0) ok = attn_wait(&o_full[2 * i + ((n - 1) & 1)], ((n - 1) >> 1) & 1, wait_ns);
             ptx::tc_fence_after();
             if (!ok && lane == 0) set_status(a.status, SPC_ERR_TIMEOUT);
             const int pos = r / pk.heads;
@@ -306,7 +314,7 @@ k_attn_tc(AttnArgs a, Packing pk, uint64_t wait_ns, const __grid_constant__ CUte
     __syncwarp();
     ptx::tc_fence_before();
     __syncthreads();
-    if (warp == 1) {
+    if (warp == S::kLoad) {
         ptx::tc_fence_after();
         ptx::tmem_dealloc(tmem, S::kCols);
     }
