@@ -217,11 +217,12 @@ k_attn_tc(AttnArgs a, Packing pk, uint64_t wait_ns, const __grid_constant__ CUte
                 }
                 float most[4] = {m, m, m, m};
 #pragma unroll
-                for (int x = 0; x < 16; ++x) {
+                for (int x = 0; x < 8; ++x) {
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) most[y] = fmaxf(most[y], __uint_as_float(v[y >> 1][2 * x + (y & 1)]));
+                    for (int y = 0; y < 4; ++y)
+                        most[y] = ptx::max3(most[y], __uint_as_float(v[y >> 1][4 * x + 2 * (y & 1)]), __uint_as_float(v[y >> 1][4 * x + 2 * (y & 1) + 1]));
                 }
-                const float top = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
+                const float top = fmaxf(ptx::max3(most[0], most[1], most[2]), most[3]);
                 const bool grow = (top - m) * c > kLazy;  // false where both are -inf
                 if (__any_sync(FULL_MASK, grow)) {
                     const float shrink = grow ? ptx::ex2((m - top) * c) : 1.f;
