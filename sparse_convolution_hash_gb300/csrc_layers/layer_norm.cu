@@ -57,27 +57,17 @@ struct Place {
     __device__ __forceinline__ bool in(int k, int j) const { return at(k, j) < c; }
 };
 
+// Zeros where the row has ended, or there is no row: they add nothing to any sum.
 template <typename T, int V, bool WHOLE>
-__device__ __forceinline__ void load_row(const T* row, const Place<V, WHOLE>& w, int k, Vec<T, V>& v)
+__device__ __forceinline__ void load_row(const T* row, const Place<V, WHOLE>& w, int k, bool there, Vec<T, V>& v)
 {
     if constexpr (WHOLE) {
-        if (w.in(k, 0)) v = *reinterpret_cast<const Vec<T, V>*>(row + w.at(k, 0));
+        uint4 bits = make_uint4(0u, 0u, 0u, 0u);
+        if (there && w.in(k, 0)) bits = *reinterpret_cast<const uint4*>(row + w.at(k, 0));
+        memcpy(&v, &bits, 16);
     } else {
 #pragma unroll
-        for (int j = 0; j < V; ++j)
-            if (w.in(k, j)) v.e[j] = row[w.at(k, j)];
-    }
-}
-
-// As pairs, zeros where the row has ended (or there is no row).
-template <typename T, int V, bool WHOLE>
-__device__ __forceinline__ void spread(const Vec<T, V>& v, const Place<V, WHOLE>& w, int k, bool there, F2 (&f)[V / 2])
-{
-    unpack<T, V>(v, f);
-#pragma unroll
-    for (int j = 0; j < V / 2; ++j) {
-        f[j].x = there && w.in(k, 2 * j) ? f[j].x : 0.f;
-        f[j].y = there && w.in(k, 2 * j + 1) ? f[j].y : 0.f;
+        for (int j = 0; j < V; ++j) v.e[j] = there && w.in(k, j) ? row[w.at(k, j)] : elem<T>::from_f32(0.f);
     }
 }
 
@@ -122,7 +112,7 @@ k_layer_norm(LayerNormArgs a, int L)
     for (int r = 0; r < R; ++r) {
 #pragma unroll
         for (int k = 0; k < K; ++k)
-            if (row0 + r < a.n) load_row<T, V, WHOLE>(x + (row0 + r) * a.c, w, k, raw[r][k]);
+            load_row<T, V, WHOLE>(x + (row0 + r) * a.c, w, k, row0 + r < a.n, raw[r][k]);
     }
     F2 f[R][K][H];
     float sum[R];
@@ -131,7 +121,7 @@ k_layer_norm(LayerNormArgs a, int L)
         F2 s{0.f, 0.f};
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            spread<T, V, WHOLE>(raw[r][k], w, k, row0 + r < a.n, f[r][k]);
+            unpack<T, V>(raw[r][k], f[r][k]);
 #pragma unroll
             for (int j = 0; j < H; ++j) s = add(s, f[r][k][j]);
         }
@@ -149,9 +139,10 @@ k_layer_norm(LayerNormArgs a, int L)
 #pragma unroll
             for (int j = 0; j < H; ++j) {
                 f[r][k][j] = add(f[r][k][j], both(-mean[r]));
-                if (!w.in(k, 2 * j)) f[r][k][j].x = 0.f;
-                if (!w.in(k, 2 * j + 1)) f[r][k][j].y = 0.f;
-                s = fma(f[r][k][j], f[r][k][j], s);
+                F2 d = f[r][k][j];
+                if (!w.in(k, 2 * j)) d.x = 0.f;
+                if (!w.in(k, 2 * j + 1)) d.y = 0.f;
+                s = fma(d, d, s);
             }
         }
         sq[r] = s.x + s.y;
@@ -215,11 +206,10 @@ k_layer_norm_grad(LayerNormArgs a, int L, float* part)
             mr[r] = there ? fetch(a.mean + row0 + r) : 0.f;
             sr[r] = there ? fetch(a.rstd + row0 + r) : 0.f;
 #pragma unroll
-            for (int k = 0; k < K; ++k)
-                if (there) {
-                    load_row<T, V, WHOLE>(x + (row0 + r) * a.c, w, k, xr[r][k]);
-                    load_row<T, V, WHOLE>(dy + (row0 + r) * a.c, w, k, dr[r][k]);
-                }
+            for (int k = 0; k < K; ++k) {
+                load_row<T, V, WHOLE>(x + (row0 + r) * a.c, w, k, there, xr[r][k]);
+                load_row<T, V, WHOLE>(dy + (row0 + r) * a.c, w, k, there, dr[r][k]);
+            }
         }
     };
     const int64_t step = (int64_t)gridDim.x * groups * R;
@@ -235,18 +225,15 @@ k_layer_norm_grad(LayerNormArgs a, int L, float* part)
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             F2 p{0.f, 0.f}, q{0.f, 0.f};
-            const bool there = row0 + r < a.n;
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 F2 g[H];
-                spread<T, V, WHOLE>(xr[r][k], w, k, there, xh[r][k]);
-                spread<T, V, WHOLE>(dr[r][k], w, k, there, g);
+                unpack<T, V>(xr[r][k], xh[r][k]);
+                unpack<T, V>(dr[r][k], g);
 #pragma unroll
                 for (int j = 0; j < H; ++j) {
                     // past the row's end dy is 0, and so is everything that this thread adds
                     xh[r][k][j] = mul(add(xh[r][k][j], both(-mr[r])), both(sr[r]));
-                    if (!w.in(k, 2 * j)) xh[r][k][j].x = 0.f;
-                    if (!w.in(k, 2 * j + 1)) xh[r][k][j].y = 0.f;
                     dg[k][j] = fma(g[j], xh[r][k][j], dg[k][j]);
                     db[k][j] = add(db[k][j], g[j]);
                     u[r][k][j] = mul(g[j], ga[k][j]);
@@ -464,6 +451,7 @@ spc_status fwd_any(const LayerNormArgs& a, cudaStream_t st)
     constexpr int V = 16 / (int)sizeof(T);
     if (a.c <= 32 * V) return fwd<T, V, 1, 4, kFwdBlock, WHOLE>(a, st);
     if (a.c <= 64 * V) return fwd<T, V, 2, 2, kFwdBlock, WHOLE>(a, st);
+    if (a.c <= 4 * V * kFwdBlock) return fwd<T, V, 4, 1, kFwdBlock, WHOLE>(a, st);
     if (a.c <= 4 * V * kWideFwdBlock) return fwd<T, V, 4, 1, kWideFwdBlock, WHOLE>(a, st);
     if (a.n > INT32_MAX) return SPC_ERR_UNSUPPORTED;
     return start<k_layer_norm_long<T>>(dim3((unsigned)a.n), kLongBlock, 0, st, a);
@@ -487,8 +475,10 @@ spc_status bwd_any(const LayerNormArgs& a, float* part, cudaStream_t st)
     int blocks = 0;
     spc_status s = SPC_OK;
     if (a.n > 0) {
-        if (a.c <= 32 * V) {
+        if (WHOLE && a.c <= 32 * V) {
             s = bwd<T, V, 1, 2, WHOLE>(a, part, &blocks, st);
+        } else if (!WHOLE && a.c <= V * kBwdBlock) {
+            s = bwd<T, V, 1, 1, WHOLE>(a, part, &blocks, st);  // addresses and bounds of single channels take registers
         } else if (a.c <= kBwdPer * kBwdBlock) {
             s = bwd<T, V, K, 1, WHOLE>(a, part, &blocks, st);
         } else {

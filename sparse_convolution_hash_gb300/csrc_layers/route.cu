@@ -1,13 +1,14 @@
 // route.cu -- the experts of each token and their weights, and the gradient by the logits.
 //
-// A row of logits lies in the registers of L lanes (4 to 32), eight neighbouring experts to a lane and chunk.
-// The best is taken k times: each lane's own best, then the best of the lanes by shuffles, ties to the lowest
-// expert.  Without a bias and groups the logits themselves are compared, which is exact.  With them the scores
-// decide, p + bias, and fp32 is not enough for the last digit: the row's choice is made in fp32, and where two
-// neighbours of the result lie closer than fp32's error (about one row in a hundred or fewer), made again in
+// A row of logits lies in the registers of L lanes (4 to 32), eight neighbouring experts to a lane (beyond 256
+// experts four such chunks).  Each lane sorts its eight once; then the best of the lanes' firsts is taken k times and
+// its lane moves up, so a round costs a reduction and a few moves whatever the number of experts.  Without a bias and groups
+// the logits themselves are compared, which is exact; 16-bit ones are sorted together with their expert in one word.
+// With a bias or groups the scores decide, p + bias, and fp32 is not enough for the last digit: the row's choice is made in fp32, and where
+// two neighbours of the result lie closer than fp32's error (about one row in a hundred or fewer), made again in
 // 64 bits.  The choice is therefore that of the formula in 64 bits, whatever the order of the sums.
 //
-// Bound by instructions: a row of 64 experts in 16 bits is 128 bytes.
+// Bound by instructions: a row of 64 experts in 16 bits is 128 bytes and some 200 instructions.
 #include <math.h>
 
 #include "layers.cuh"
@@ -24,23 +25,25 @@ constexpr int kNone = INT32_MAX;
 __device__ __forceinline__ float exp_of(float x) { return expf(x); }
 __device__ __forceinline__ double exp_of(double x) { return exp(x); }
 
-template <typename S>
-__device__ __forceinline__ S lanes_sum(S v, int L)
+template <int L, typename S>
+__device__ __forceinline__ S lanes_sum(S v)
 {
+#pragma unroll
     for (int o = L >> 1; o; o >>= 1) v += __shfl_xor_sync(FULL_MASK, v, o);
     return v;
 }
-template <typename S>
-__device__ __forceinline__ S lanes_max(S v, int L)
+template <int L, typename S>
+__device__ __forceinline__ S lanes_max(S v)
 {
+#pragma unroll
     for (int o = L >> 1; o; o >>= 1) v = max(v, __shfl_xor_sync(FULL_MASK, v, o));
     return v;
 }
 
 // Logits of a row, -inf where there is no expert, and for one that is not available (-inf, NaN); +inf counts as
 // the largest finite number, so that differences exist.
-template <typename T, int C>
-__device__ __forceinline__ void load_logits(const T* row, int experts, int lane, int L, bool whole, float (&l)[C][kPer])
+template <typename T, int C, int L>
+__device__ __forceinline__ void load_logits(const T* row, int experts, int lane, bool whole, float (&l)[C][kPer])
 {
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -63,8 +66,8 @@ __device__ __forceinline__ void load_logits(const T* row, int experts, int lane,
 }
 
 // Sum over the row of exp(l - most), `most` its largest logit (-inf: no expert is available).
-template <typename S, int C>
-__device__ __forceinline__ S exp_sum(const float (&l)[C][kPer], float most, int L)
+template <typename S, int C, int L>
+__device__ __forceinline__ S exp_sum(const float (&l)[C][kPer], float most)
 {
     S s = 0;
 #pragma unroll
@@ -73,7 +76,7 @@ __device__ __forceinline__ S exp_sum(const float (&l)[C][kPer], float most, int 
         for (int j = 0; j < kPer; ++j)
             if (l[c][j] > -INFINITY) s += exp_of((S)l[c][j] - (S)most);
     }
-    return lanes_sum(s, L);
+    return lanes_sum<L>(s);
 }
 
 template <typename S>
@@ -81,6 +84,13 @@ __device__ __forceinline__ S score_of(float l, bool sigmoid, float most, S sum)
 {
     return sigmoid ? (S)1 / ((S)1 + exp_of(-(S)l)) : exp_of((S)l - (S)most) / sum;
 }
+
+// For the choice in fp32: off by less than 2^-21 (sigmoid) or 2^-18 of the largest score.
+__device__ __forceinline__ float rough_score(float l, bool sigmoid, float most, float sum)
+{
+    return sigmoid ? __fdividef(1.f, 1.f + __expf(fminf(-l, 88.f))) : __fdividef(__expf(l - most), sum);
+}
+__device__ __forceinline__ double rough_score(float l, bool sigmoid, float most, double sum) { return score_of<double>(l, sigmoid, most, sum); }
 
 struct RouteShared {
     int32_t* expert;   // [k] of this row
@@ -96,24 +106,25 @@ __device__ __forceinline__ uint32_t order_of(float v)
 }
 __device__ __forceinline__ float value_of(uint32_t w) { return w ? __uint_as_float(w >> 31 ? w ^ 0x80000000u : ~w) : -INFINITY; }
 
-__device__ __forceinline__ uint32_t lanes_most(uint32_t v, int L)
+template <int L>
+__device__ __forceinline__ uint32_t lanes_most(uint32_t v)
 {
-    if (L == 32) return __reduce_max_sync(FULL_MASK, v);
-    return lanes_max(v, L);
+    if constexpr (L == 32) return __reduce_max_sync(FULL_MASK, v);
+    else return lanes_max<L>(v);
 }
 
 // The best of the lanes' values: (value, expert, logit), ties to the lowest expert; expert kNone where none is left.
-template <int C>
-__device__ __forceinline__ void best_of_lanes(float& top, int& e, float& l, int lane, int L)
+template <int C, int L>
+__device__ __forceinline__ void best_of_lanes(float& top, int& e, float& l, int lane)
 {
-    const uint32_t key = order_of(top), most = lanes_most(key, L);
+    const uint32_t key = order_of(top), most = lanes_most<L>(key);
     const bool mine = key == most && e != kNone;
     int winner;
     if constexpr (C == 1) {  // lanes hold ascending experts
         const uint32_t at = (threadIdx.x & 31) - lane, votes = __ballot_sync(FULL_MASK, mine) >> at;
-        winner = __ffs(L == 32 ? votes : votes & ((1u << L) - 1)) - 1;
+        winner = __ffs(L == 32 ? votes : votes & ((1u << (L & 31)) - 1)) - 1;
     } else {
-        const uint32_t least = ~lanes_most(~(mine ? (uint32_t)e : (uint32_t)kNone), L);
+        const uint32_t least = ~lanes_most<L>(~(mine ? (uint32_t)e : (uint32_t)kNone));
         const uint32_t votes = __ballot_sync(FULL_MASK, mine && (uint32_t)e == least);
         winner = __ffs(votes) - 1;
     }
@@ -123,9 +134,10 @@ __device__ __forceinline__ void best_of_lanes(float& top, int& e, float& l, int 
     top = value_of(most);
     if (winner < 0) e = kNone;
 }
-template <int C>
-__device__ __forceinline__ void best_of_lanes(double& top, int& e, float& l, int, int L)
+template <int C, int L>
+__device__ __forceinline__ void best_of_lanes(double& top, int& e, float& l, int)
 {
+#pragma unroll
     for (int o = L >> 1; o; o >>= 1) {
         const double v = __shfl_xor_sync(FULL_MASK, top, o);
         const int other = __shfl_xor_sync(FULL_MASK, e, o);
@@ -138,15 +150,89 @@ __device__ __forceinline__ void best_of_lanes(double& top, int& e, float& l, int
     }
 }
 
+// ---- a lane's eight in falling order.  Words of 64 bits: order_of(value), then the larger for the lower expert; of 32
+// bits, for 16-bit logits: their order in the high half.  0: not available.
+__device__ __forceinline__ uint64_t rank_of(float v, int e)
+{
+    const uint32_t w = order_of(v);
+    return w ? (uint64_t)w << 32 | (0xffffffffu - (uint32_t)e) : 0ull;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t rank16(T v, int e)
+{
+    constexpr uint32_t kInf = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
+    uint16_t h;
+    memcpy(&h, &v, 2);
+    uint32_t b = h == 0x8000u ? 0u : h;
+    const bool there = (b & 0x7fffu) <= kInf && b != (0x8000u | kInf);
+    b = b & 0x8000u ? ~b & 0xffffu : b | 0x8000u;
+    return there ? b << 16 | (0xffffu - (uint32_t)e) : 0u;
+}
+template <typename T>
+__device__ __forceinline__ float logit16(uint32_t word)
+{
+    const uint32_t b = word >> 16;
+    const uint16_t h = (uint16_t)(b & 0x8000u ? b & 0x7fffu : ~b);
+    T v;
+    memcpy(&v, &h, 2);
+    return fminf(elem<T>::to_f32(v), 3.402823466e38f);
+}
+
+template <typename W>
+__device__ __forceinline__ void sort8(W (&v)[8])
+{
+    // Batcher's odd-even merging network
+    constexpr int kA[19] = {0, 2, 4, 6, 0, 1, 4, 5, 1, 5, 0, 1, 2, 3, 2, 3, 1, 3, 5};
+    constexpr int kB[19] = {1, 3, 5, 7, 2, 3, 6, 7, 2, 6, 4, 5, 6, 7, 4, 5, 2, 4, 6};
+#pragma unroll
+    for (int x = 0; x < 19; ++x) {
+        const W a = v[kA[x]], b = v[kB[x]];
+        v[kA[x]] = max(a, b);
+        v[kB[x]] = min(a, b);
+    }
+}
+
+// The best of the lanes' firsts (0: none is left), which its lane drops; e: its expert.
+template <int L>
+__device__ __forceinline__ uint32_t take_best(uint32_t (&v)[8], int, int& e)
+{
+    const uint32_t most = lanes_most<L>(v[0]);  // no two are equal but 0
+    e = 0xffff - (int)(most & 0xffffu);
+    if (v[0] == most) {
+#pragma unroll
+        for (int j = 0; j < 7; ++j) v[j] = v[j + 1];
+        v[7] = 0u;
+    }
+    return most;
+}
+template <int L>
+__device__ __forceinline__ uint32_t take_best(uint64_t (&v)[8], int lane, int& e)
+{
+    const uint32_t most = lanes_most<L>((uint32_t)(v[0] >> 32));
+    // lanes hold ascending experts, so the lowest lane has the lowest of equal ones
+    const uint32_t at = (threadIdx.x & 31) - lane, votes = __ballot_sync(FULL_MASK, (uint32_t)(v[0] >> 32) == most) >> at;
+    const int winner = __ffs(votes) - 1;
+    e = (int)(0xffffffffu - __shfl_sync(FULL_MASK, (uint32_t)v[0], winner, L));
+    if (lane == winner) {
+#pragma unroll
+        for (int j = 0; j < 7; ++j) v[j] = v[j + 1];
+        v[7] = 0ull;
+    }
+    return most;
+}
+
 // The row's k best, written to sh.expert and sh.logit by its lane 0.  S: the type that scores are compared in
 // (BY_LOGIT: the logits, exactly).  Returns whether two neighbours, or the border of the kept groups, lie
-// within the error of S: scores are off by `rel` of themselves, none is above p_most.
-template <typename S, bool BY_LOGIT, int C>
-__device__ __forceinline__ bool choose(const RouteArgs& a, const float (&l)[C][kPer], int lane, int L, const RouteShared& sh)
+// within the error of S: scores are off by 2^-20, or 2^-16 of the largest one (softmax), at most.
+template <typename T, typename S, bool BY_LOGIT, int C, int L>
+__device__ __forceinline__ bool choose(const RouteArgs& a, const T* row, const float (&l)[C][kPer], int lane, const RouteShared& sh)
 {
     const S kLow = -INFINITY;
     bool near = false;
     S c[C][kPer], off = 0;
+    // groups of whole lanes, a power of two of them: no shared memory
+    const int spread = a.experts / a.groups / kPer;
+    const bool in_lanes = C == 1 && sizeof(S) == 4 && a.experts == a.groups * spread * kPer && (spread & (spread - 1)) == 0;
     if constexpr (BY_LOGIT) {
 #pragma unroll
         for (int i = 0; i < C; ++i) {
@@ -161,22 +247,22 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&l)[C][k
 #pragma unroll
             for (int j = 0; j < kPer; ++j) most = fmaxf(most, l[i][j]);
         }
-        most = lanes_max(most, L);
-        const S sum = sigmoid ? (S)1 : exp_sum<S>(l, most, L);
+        most = lanes_max<L>(most);
+        const S sum = sigmoid ? (S)1 : exp_sum<S, C, L>(l, most);
         off = sigmoid ? (S)0x1p-20 : (S)0x1p-16 / sum;
 #pragma unroll
         for (int i = 0; i < C; ++i) {
 #pragma unroll
             for (int j = 0; j < kPer; ++j) {
                 const int e = (i * L + lane) * kPer + j;
-                c[i][j] = l[i][j] > -INFINITY ? score_of<S>(l[i][j], sigmoid, most, sum) + (a.bias ? (S)fetch(a.bias + e) : (S)0) : kLow;
+                c[i][j] = l[i][j] > -INFINITY ? rough_score(l[i][j], sigmoid, most, sum) + (a.bias ? (S)fetch(a.bias + e) : (S)0) : kLow;
                 if (!(c[i][j] > kLow)) c[i][j] = kLow;  // a bias of NaN
             }
         }
-        if (a.groups > 1) {
+        if (a.groups > 1 && !in_lanes) {
             // a group's score: the sum of its two best (its only one's, where it has one)
-            S* row = static_cast<S*>(sh.c);
-            S* best = row + a.experts;
+            S* by = static_cast<S*>(sh.c);
+            S* best = by + a.experts;
             const int size = a.experts / a.groups;
             __syncwarp();
 #pragma unroll
@@ -184,7 +270,7 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&l)[C][k
 #pragma unroll
                 for (int j = 0; j < kPer; ++j) {
                     const int e = (i * L + lane) * kPer + j;
-                    if (e < a.experts) row[e] = c[i][j];
+                    if (e < a.experts) by[e] = c[i][j];
                 }
             }
             __syncwarp();
@@ -195,7 +281,7 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&l)[C][k
                 S first = kLow, second = kLow;
                 if (g < a.groups) {
                     for (int e = lane & (share - 1); e < size; e += share) {
-                        const S v = row[g * size + e], low = min(v, first);
+                        const S v = by[g * size + e], low = min(v, first);
                         first = max(v, first);
                         second = max(second, low);
                     }
@@ -222,8 +308,8 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&l)[C][k
                 else best_left = max(best_left, mine);
                 if (keep) kept_mask |= 1u << q;
             }
-            least_kept = -lanes_max(-least_kept, L);
-            best_left = lanes_max(best_left, L);
+            least_kept = -lanes_max<L>(-least_kept);
+            best_left = lanes_max<L>(best_left);
             if (best_left > kLow && least_kept < INFINITY)
                 near = least_kept - best_left <= 4 * off + (S)0x1p-21 * (fabs(least_kept) + fabs(best_left));
             __syncwarp();
@@ -244,49 +330,132 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const float (&l)[C][k
             }
         }
     }
+    const int rounds = BY_LOGIT ? a.top_k : a.top_k + 1;  // one more than asked for shows the gap to the first that is left out
     S before = 0;
-    float before_l = 0.f;
-    int before_e = -1;
-    // one round more than asked for shows the gap to the first that is left out
-    const int rounds = BY_LOGIT ? a.top_k : a.top_k + 1;
-    for (int r = 0; r < rounds; ++r) {
-        S top = kLow;
-        int e_top = kNone;
-        float l_top = 0.f;
+    int before_e = 0;
+    auto logit_at = [&](int e) { return fminf(elem<T>::to_f32(fetch(row + e)), 3.402823466e38f); };
+    // equal logits and biases are a tie in any arithmetic
+    auto too_near = [&](S top, int e) {
+        if (!(before - top <= 2 * off + (S)0x1p-21 * (fabs(before) + fabs(top)))) return false;
+        const float b0 = a.bias ? fetch(a.bias + before_e) : 0.f, b1 = a.bias ? fetch(a.bias + e) : 0.f;
+        return !(logit_at(before_e) == logit_at(e) && b0 == b1);
+    };
+    if constexpr (C == 1 && sizeof(S) == 4) {
+        uint64_t v[kPer];
 #pragma unroll
-        for (int i = 0; i < C; ++i) {
+        for (int j = 0; j < kPer; ++j) v[j] = rank_of(c[0][j], lane * kPer + j);
+        sort8(v);
+        if (!BY_LOGIT && a.groups > 1 && in_lanes) {
+            // a group's score: the sum of its two best (its only one's, where it has one)
+            S first = value_of((uint32_t)(v[0] >> 32)), second = value_of((uint32_t)(v[1] >> 32));
+            for (int o = 1; o < spread; o <<= 1) {
+                const S x = __shfl_xor_sync(FULL_MASK, first, o), y = __shfl_xor_sync(FULL_MASK, second, o);
+                second = max(max(second, y), min(first, x));
+                first = max(first, x);
+            }
+            const S best = second > kLow ? first + second : first;
+            const int mine = lane / spread;
+            int better = 0;
+            for (int g = 0; g < a.groups; ++g) {
+                const S other = __shfl_sync(FULL_MASK, best, g * spread, L);
+                better += other > best || (other == best && g < mine);
+            }
+            const bool there = lane * kPer < a.experts && best > kLow, keep = there && better < a.top_groups;
+            const S least_kept = -lanes_max<L>(keep ? -best : kLow), best_left = lanes_max<L>(there && !keep ? best : kLow);
+            if (best_left > kLow && least_kept < INFINITY)
+                near = least_kept - best_left <= 4 * off + (S)0x1p-21 * (fabs(least_kept) + fabs(best_left));
+            if (!keep) {
 #pragma unroll
-            for (int j = 0; j < kPer; ++j)
-                if (c[i][j] > top) {
-                    top = c[i][j];
-                    e_top = (i * L + lane) * kPer + j;
-                    l_top = l[i][j];
-                }
+                for (int j = 0; j < kPer; ++j) v[j] = 0ull;
+            }
         }
-        best_of_lanes<C>(top, e_top, l_top, lane, L);
-        const bool found = e_top != kNone;
-        if (!BY_LOGIT && r > 0 && found && before - top <= 2 * off + (S)0x1p-21 * (fabs(before) + fabs(top))) {
-            // equal logits and biases are a tie in any arithmetic
-            const float b0 = a.bias ? fetch(a.bias + before_e) : 0.f, b1 = a.bias ? fetch(a.bias + e_top) : 0.f;
-            near |= !(before_l == l_top && b0 == b1);
+        for (int r = 0; r < rounds; ++r) {
+            int e;
+            const uint32_t most = take_best<L>(v, lane, e);
+            const S top = value_of(most);
+            if (!BY_LOGIT) {
+                if (r > 0 && most) near |= too_near(top, e);
+                before = top;
+                before_e = most ? e : 0;
+            }
+            if (r < a.top_k && lane == 0) {
+                sh.expert[r] = most ? e : -1;
+                if (BY_LOGIT) sh.logit[r] = top;
+            }
         }
-        before = top;
-        before_l = l_top;
-        before_e = found ? e_top : 0;
-        if (r < a.top_k && lane == 0) {
-            sh.expert[r] = found ? e_top : -1;
-            sh.logit[r] = l_top;
-        }
-        if (found && e_top / kPer % L == lane) {
+    } else {
+        for (int r = 0; r < rounds; ++r) {
+            S top = kLow;
+            int e_top = kNone;
+            float l_top = 0.f;
 #pragma unroll
             for (int i = 0; i < C; ++i) {
 #pragma unroll
                 for (int j = 0; j < kPer; ++j)
-                    if ((i * L + lane) * kPer + j == e_top) c[i][j] = kLow;
+                    if (c[i][j] > top) {
+                        top = c[i][j];
+                        e_top = (i * L + lane) * kPer + j;
+                        l_top = l[i][j];
+                    }
+            }
+            best_of_lanes<C, L>(top, e_top, l_top, lane);
+            const bool found = e_top != kNone;
+            if (!BY_LOGIT && sizeof(S) == 4 && r > 0 && found) near |= too_near(top, e_top);
+            before = top;
+            before_e = found ? e_top : 0;
+            if (r < a.top_k && lane == 0) {
+                sh.expert[r] = found ? e_top : -1;
+                if (BY_LOGIT) sh.logit[r] = l_top;
+            }
+            if (found && e_top / kPer % L == lane) {
+#pragma unroll
+                for (int i = 0; i < C; ++i) {
+#pragma unroll
+                    for (int j = 0; j < kPer; ++j)
+                        if ((i * L + lane) * kPer + j == e_top) c[i][j] = kLow;
+                }
             }
         }
     }
+    if (!BY_LOGIT) {
+        __syncwarp();
+        for (int r = lane; r < a.top_k; r += L) sh.logit[r] = sh.expert[r] >= 0 ? logit_at(sh.expert[r]) : 0.f;
+    }
     return near;
+}
+
+// 16-bit logits by themselves: expert and logit in one word.
+template <typename T, int L>
+__device__ __forceinline__ void choose16(const RouteArgs& a, const T* row, int lane, bool whole, const RouteShared& sh)
+{
+    uint32_t v[kPer];
+    const int e0 = lane * kPer;
+    if (whole && e0 < a.experts) {
+        const Vec<T, kPer> raw = *reinterpret_cast<const Vec<T, kPer>*>(row + e0);
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) v[j] = rank16(raw.e[j], e0 + j);
+    } else {
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) v[j] = e0 + j < a.experts ? rank16(fetch(row + e0 + j), e0 + j) : 0u;
+    }
+    sort8(v);
+    for (int r = 0; r < a.top_k; ++r) {
+        int e;
+        const uint32_t most = take_best<L>(v, lane, e);
+        if (lane == 0) {
+            sh.expert[r] = most ? e : -1;
+            sh.logit[r] = logit16<T>(most);
+        }
+    }
+}
+
+// The same choice in 64 bits, for the rows that need it.
+template <typename T, int C, int L>
+__device__ __noinline__ void choose_exactly(const RouteArgs& a, const T* row, int lane, bool whole, const RouteShared& sh)
+{
+    float l[C][kPer];
+    load_logits<T, C, L>(row, a.experts, lane, whole, l);
+    choose<T, double, false, C, L>(a, row, l, lane, sh);
 }
 
 // An expert's weight from its logit: its score, or its share of the chosen ones' scores.
@@ -297,19 +466,20 @@ struct Weights {
 };
 
 // most and sum: of the whole row (softmax without renorm).  Lanes take the chosen experts in turn.
-__device__ __forceinline__ Weights weights_of(const RouteShared& sh, int k, bool sigmoid, bool renorm, float most, float sum, int lane, int L)
+template <int L>
+__device__ __forceinline__ Weights weights_of(const RouteShared& sh, int k, bool sigmoid, bool renorm, float most, float sum, int lane)
 {
     Weights w{most, sum, sigmoid};
     if (!renorm) return w;
     w.most = -INFINITY;
     for (int r = lane; r < k; r += L)
         if (sh.expert[r] >= 0) w.most = fmaxf(w.most, sh.logit[r]);
-    w.most = lanes_max(w.most, L);
+    w.most = lanes_max<L>(w.most);
     auto add_up = [&]() {
         float s = 0.f;
         for (int r = lane; r < k; r += L)
             if (sh.expert[r] >= 0) s += score_of<float>(sh.logit[r], w.sigmoid, w.most, 1.f);
-        return lanes_sum(s, L);
+        return lanes_sum<L>(s);
     };
     w.total = add_up();
     if (sigmoid) {
@@ -324,9 +494,9 @@ __device__ __forceinline__ Weights weights_of(const RouteShared& sh, int k, bool
     return w;
 }
 
-template <typename T, int C>
+template <typename T, int C, int L>
 __global__ void __launch_bounds__(kBlock)
-k_route(RouteArgs a, int L, bool whole)
+k_route(RouteArgs a, bool whole)
 {
     extern __shared__ double room[];
     wait_for_kernel_before();
@@ -337,30 +507,38 @@ k_route(RouteArgs a, int L, bool whole)
     sh.c = room + mine * grouped;
     sh.logit = reinterpret_cast<float*>(room + rows * grouped) + mine * 2 * a.top_k;
     sh.expert = reinterpret_cast<int32_t*>(sh.logit + a.top_k);
-    float l[C][kPer];
-    load_logits<T, C>(static_cast<const T*>(a.logits) + at * a.experts, a.experts, lane, L, whole, l);
-    if (!a.bias && a.groups == 1) {
-        choose<float, true, C>(a, l, lane, L, sh);
-    } else {
-        const bool near = choose<float, false, C>(a, l, lane, L, sh);
-        if (__any_sync(FULL_MASK, near)) {
-            __syncwarp();
-            choose<double, false, C>(a, l, lane, L, sh);
+    const T* logits = static_cast<const T*>(a.logits) + at * a.experts;
+    const bool sigmoid = a.score == SPC_SCORE_SIGMOID, by_logit = !a.bias && a.groups == 1, all = !sigmoid && !a.renorm;
+    float most = -INFINITY, sum = 1.f;
+    bool chosen = false;
+    if constexpr (sizeof(T) == 2 && C == 1) {
+        if (by_logit) {
+            choose16<T, L>(a, logits, lane, whole, sh);
+            chosen = true;
         }
     }
-    float most = -INFINITY, sum = 1.f;
-    const bool sigmoid = a.score == SPC_SCORE_SIGMOID;
-    if (!sigmoid && !a.renorm) {
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-#pragma unroll
-            for (int j = 0; j < kPer; ++j) most = fmaxf(most, l[c][j]);
+    if (!chosen || all) {
+        float l[C][kPer];
+        load_logits<T, C, L>(logits, a.experts, lane, whole, l);
+        if (chosen) {
+        } else if (by_logit) {
+            choose<T, float, true, C, L>(a, logits, l, lane, sh);
+        } else if (__any_sync(FULL_MASK, choose<T, float, false, C, L>(a, logits, l, lane, sh))) {
+            __syncwarp();
+            choose_exactly<T, C, L>(a, logits, lane, whole, sh);
         }
-        most = lanes_max(most, L);
-        sum = exp_sum<float>(l, most, L);
+        if (all) {
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) most = fmaxf(most, l[c][j]);
+            }
+            most = lanes_max<L>(most);
+            sum = exp_sum<float, C, L>(l, most);
+        }
     }
     __syncwarp();
-    const Weights w = weights_of(sh, a.top_k, sigmoid, a.renorm, most, sum, lane, L);
+    const Weights w = weights_of<L>(sh, a.top_k, sigmoid, a.renorm, most, sum, lane);
     if (row >= a.n) return;
     for (int r = lane; r < a.top_k; r += L) {
         a.expert[row * a.top_k + r] = sh.expert[r];
@@ -371,9 +549,9 @@ k_route(RouteArgs a, int L, bool whole)
 // With s the scale, G the chosen experts and p the scores:
 //   softmax  dl_e = p_e ([e in G] s dg_e - sum_G s dg p),           sigmoid  dl_e = [e in G] s dg_e p_e (1 - p_e)
 // and with weights g = p / sum_G p:  dl_e = [e in G] s g_e (dg_e - sum_G g dg), times (1 - p_e) for sigmoid.
-template <typename T, int C>
+template <typename T, int C, int L>
 __global__ void __launch_bounds__(kBlock)
-k_route_grad(RouteGradArgs a, int L, bool whole)
+k_route_grad(RouteGradArgs a, bool whole)
 {
     wait_for_kernel_before();
     extern __shared__ double room[];
@@ -397,13 +575,13 @@ k_route_grad(RouteGradArgs a, int L, bool whole)
     float most = -INFINITY, sum = 1.f;
     const bool full = !sigmoid && !a.renorm;
     if (full) {
-        load_logits<T, C>(logits, a.experts, lane, L, whole, dl);
+        load_logits<T, C, L>(logits, a.experts, lane, whole, dl);
 #pragma unroll
         for (int c = 0; c < C; ++c) {
 #pragma unroll
             for (int j = 0; j < kPer; ++j) most = fmaxf(most, dl[c][j]);
         }
-        most = lanes_max(most, L);
+        most = lanes_max<L>(most);
         // exponentials stand in for the logits from here on
         float s = 0.f;
 #pragma unroll
@@ -414,14 +592,14 @@ k_route_grad(RouteGradArgs a, int L, bool whole)
                 s += dl[c][j];
             }
         }
-        sum = lanes_sum(s, L);
+        sum = lanes_sum<L>(s);
     }
     __syncwarp();
-    const Weights w = weights_of(sh, a.top_k, sigmoid, a.renorm, most, sum, lane, L);
+    const Weights w = weights_of<L>(sh, a.top_k, sigmoid, a.renorm, most, sum, lane);
     float dot = 0.f;
     for (int r = lane; r < a.top_k; r += L)
         if (sh.expert[r] >= 0) dot += w.of(sh.logit[r]) * fetch(a.dgate + at * a.top_k + r);
-    dot = a.renorm || !sigmoid ? lanes_sum(dot, L) : 0.f;
+    dot = a.renorm || !sigmoid ? lanes_sum<L>(dot) : 0.f;
     const float rest = full && sum > 0.f ? -a.scale * dot / sum : 0.f;  // sum 0: no expert is available
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -473,9 +651,8 @@ k_route_grad(RouteGradArgs a, int L, bool whole)
 int lanes_for(int experts) { return experts <= 32 ? 4 : experts <= 64 ? 8 : experts <= 128 ? 16 : 32; }
 
 template <auto KERNEL, typename A>
-spc_status start(const A& a, size_t smem, bool whole, cudaStream_t st)
+spc_status start(const A& a, int L, size_t smem, bool whole, cudaStream_t st)
 {
-    const int L = lanes_for(a.experts);
     const int64_t blocks = ceil_div(a.n, (int64_t)(kBlock / L));
     if (blocks > INT32_MAX) return SPC_ERR_UNSUPPORTED;
     if (smem > 32 * 1024) {  // 48 KB with the static part need no leave
@@ -490,7 +667,7 @@ spc_status start(const A& a, size_t smem, bool whole, cudaStream_t st)
     cudaLaunchAttribute attr[1] = {beside_the_kernel_before()};
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    SPC_CUDA_TRY(cudaLaunchKernelEx(&cfg, KERNEL, a, L, whole));
+    SPC_CUDA_TRY(cudaLaunchKernelEx(&cfg, KERNEL, a, whole));
     return SPC_OK;
 }
 
@@ -498,17 +675,30 @@ template <typename T>
 spc_status fwd(const RouteArgs& a, cudaStream_t st)
 {
     const bool whole = a.experts % kPer == 0 && aligned16(a.logits);
-    const size_t rows = kBlock / lanes_for(a.experts);
-    const size_t smem = rows * ((a.groups > 1 ? 8 * (size_t)(a.experts + a.groups) : 0) + 8 * (size_t)a.top_k);
-    return a.experts <= 256 ? start<k_route<T, 1>>(a, smem, whole, st) : start<k_route<T, 4>>(a, smem, whole, st);
+    const int L = lanes_for(a.experts);
+    const size_t smem = (size_t)(kBlock / L) * ((a.groups > 1 ? 8 * (size_t)(a.experts + a.groups) : 0) + 8 * (size_t)a.top_k);
+    if (a.experts > 256) return start<k_route<T, 4, 32>>(a, L, smem, whole, st);
+    switch (L) {
+    case 4: return start<k_route<T, 1, 4>>(a, L, smem, whole, st);
+    case 8: return start<k_route<T, 1, 8>>(a, L, smem, whole, st);
+    case 16: return start<k_route<T, 1, 16>>(a, L, smem, whole, st);
+    default: return start<k_route<T, 1, 32>>(a, L, smem, whole, st);
+    }
 }
 
 template <typename T>
 spc_status bwd(const RouteGradArgs& a, cudaStream_t st)
 {
     const bool whole = a.experts % kPer == 0 && aligned16(a.logits) && aligned16(a.dlogits);
-    const size_t smem = 8 * (size_t)(kBlock / lanes_for(a.experts)) * a.top_k;
-    return a.experts <= 256 ? start<k_route_grad<T, 1>>(a, smem, whole, st) : start<k_route_grad<T, 4>>(a, smem, whole, st);
+    const int L = lanes_for(a.experts);
+    const size_t smem = 8 * (size_t)(kBlock / L) * a.top_k;
+    if (a.experts > 256) return start<k_route_grad<T, 4, 32>>(a, L, smem, whole, st);
+    switch (L) {
+    case 4: return start<k_route_grad<T, 1, 4>>(a, L, smem, whole, st);
+    case 8: return start<k_route_grad<T, 1, 8>>(a, L, smem, whole, st);
+    case 16: return start<k_route_grad<T, 1, 16>>(a, L, smem, whole, st);
+    default: return start<k_route_grad<T, 1, 32>>(a, L, smem, whole, st);
+    }
 }
 
 }  // namespace
