@@ -5,8 +5,10 @@
 // with P = exp(S - lse) and dS = P (dP - delta), written as 16 bits in the place of S and dP, a thread to a lane.
 // Seven products where five would do, were dq summed across blocks; but then its bits would hang on their order.
 //
-// Two steps are in work at any time, each with four warps and a quarter of tensor memory: while one's
-// probabilities are taken, the other's products run.
+// BUFS steps are in work at any time, each with four warps and 128 columns of tensor memory: while one's
+// probabilities are taken, the others' products run.  Three where heads of up to 64 channels leave the columns, two beyond;
+// one where the walk is a few steps long, so that two blocks share an SM and one's first loads and last
+// stores run beside the other's steps.
 //
 // fp16: P is kept times 2^14 and dS times a power of two for which the largest possible value, |P| <= 1 times
 // 2 max|do| max|v|, stays below 2^14, so small probabilities and gradients keep their digits.
@@ -18,17 +20,20 @@ namespace spc {
 
 namespace {
 
-constexpr int kStep = 64;  // rows of the streamed side
+constexpr int kStep = 64;       // rows of the streamed side
+constexpr int kShortWalk = 12;  // steps up to which one buffer a block and two blocks an SM are faster
 
-template <int D>
+template <int D, int BUFS>
 struct Shape {
     static constexpr int kBoxes = D / 64;
     static constexpr int kKept = 128 * 128 * kBoxes;      // bytes of the 128 rows that a block keeps
     static constexpr int kHalf = kStep * 128 * kBoxes;    // bytes of a step's rows of one operand
     static constexpr int kStage = 2 * kHalf;
-    static constexpr int kStages = 4;
-    static constexpr int kThreads = 384;
-    static constexpr int kBars = 3 * kStages + 10;
+    static constexpr int kStages = BUFS == 3 ? 6 : 4;
+    static constexpr int kThreads = 128 + 128 * BUFS;
+    static constexpr int kCols = BUFS == 1 ? 256 : 512;   // tensor memory
+    static constexpr int kBars = 3 * kStages + 4 + 3 * BUFS;
+    static_assert(BUFS * 128 + 2 * D <= kCols, "");
     static constexpr size_t kSmem = 1024 + 2 * (size_t)kKept + (size_t)kStages * (kStage + 2 * kStep * 4) + 8 * kBars + 16;
 };
 
@@ -53,14 +58,13 @@ __device__ __forceinline__ Scales scales(const AttnArgs& a)
     }
 }
 
-// 32 columns of probabilities and their gradients, as 16-bit pairs.  lse2 and delta of each column, or (COLUMN false)
-// one pair for the lane.
+// 16 columns of probabilities and their gradients, as 16-bit pairs.
 template <typename T>
-__device__ __forceinline__ void grad32(const uint32_t (&s)[32], const uint32_t (&dp)[32], F2 c, const F2 (&minus_lse)[16], const F2 (&minus_delta)[16],
-                                       F2 ds_scale, uint32_t (&p)[16], uint32_t (&ds)[16])
+__device__ __forceinline__ void grad16(const uint32_t (&s)[16], const uint32_t (&dp)[16], F2 c, const F2 (&minus_lse)[8], const F2 (&minus_delta)[8],
+                                       F2 ds_scale, uint32_t (&p)[8], uint32_t (&ds)[8])
 {
 #pragma unroll
-    for (int y = 0; y < 16; ++y) {
+    for (int y = 0; y < 8; ++y) {
         F2 e = fma(F2{__uint_as_float(s[2 * y]), __uint_as_float(s[2 * y + 1])}, c, minus_lse[y]);
         e = F2{ptx::ex2(e.x), ptx::ex2(e.y)};
         F2 g = add(F2{__uint_as_float(dp[2 * y]), __uint_as_float(dp[2 * y + 1])}, minus_delta[y]);
@@ -123,12 +127,12 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src)
 
 // KEYS: the kernel of dk and dv (keeps keys, walks over the queries of every head that shares them), else of dq.
 // grid: slots of 128 rows, heads of the kept side, splits
-template <typename T, int D, bool KEYS>
-__global__ void __launch_bounds__(Shape<D>::kThreads, 1)
+template <typename T, int D, int BUFS, bool KEYS>
+__global__ void __launch_bounds__(Shape<D, BUFS>::kThreads, BUFS == 1 ? 2 : 1)
 k_attn_grad_tc(AttnArgs a, uint64_t wait_ns, const __grid_constant__ CUtensorMap kept1, const __grid_constant__ CUtensorMap kept2,
                const __grid_constant__ CUtensorMap step1, const __grid_constant__ CUtensorMap step2)
 {
-    using S = Shape<D>;
+    using S = Shape<D, BUFS>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     uint8_t* ring = smem + 2 * S::kKept;
@@ -138,10 +142,10 @@ k_attn_grad_tc(AttnArgs a, uint64_t wait_ns, const __grid_constant__ CUtensorMap
     uint64_t* ready = empty + S::kStages;
     uint64_t* kept_full = ready + S::kStages;
     uint64_t* drain = kept_full + 1;   // of the two warps that issue
-    uint64_t* s_full = drain + 2;      // [buffer]: S and dP of a step
-    uint64_t* p_full = s_full + 2;     // [buffer]: P and dS
-    uint64_t* sum_full = p_full + 2;   // [buffer]: the sums with them
-    uint64_t* o_full = sum_full + 2;   // all sums
+    uint64_t* s_full = drain + 2;          // [buffer]: S and dP of a step
+    uint64_t* p_full = s_full + BUFS;      // [buffer]: P and dS
+    uint64_t* sum_full = p_full + BUFS;    // [buffer]: the sums with them
+    uint64_t* o_full = sum_full + BUFS;    // all sums
     uint32_t* s_ctrl = reinterpret_cast<uint32_t*>(o_full + 1);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -167,8 +171,9 @@ k_attn_grad_tc(AttnArgs a, uint64_t wait_ns, const __grid_constant__ CUtensorMap
             ptx::mbar_init(&ready[s], 32);
         }
         ptx::mbar_init(kept_full, 1);
-        for (int i = 0; i < 2; ++i) {
-            ptx::mbar_init(&drain[i], 1);
+        ptx::mbar_init(&drain[0], 1);
+        ptx::mbar_init(&drain[1], 1);
+        for (int i = 0; i < BUFS; ++i) {
             ptx::mbar_init(&sum_full[i], 1);
             ptx::mbar_init(&s_full[i], 1);
             ptx::mbar_init(&p_full[i], 4);
@@ -177,7 +182,7 @@ k_attn_grad_tc(AttnArgs a, uint64_t wait_ns, const __grid_constant__ CUtensorMap
         ptx::mbar_init_fence();
     }
     if (warp == 1) {
-        ptx::tmem_alloc(s_ctrl, 512);
+        ptx::tmem_alloc(s_ctrl, S::kCols);
         ptx::tmem_relinquish();
     }
     ptx::tc_fence_before();
@@ -185,7 +190,7 @@ k_attn_grad_tc(AttnArgs a, uint64_t wait_ns, const __grid_constant__ CUtensorMap
     ptx::tc_fence_after();
     const uint32_t tmem = s_ctrl[0], kept_base = ptx::smem_u32(smem), ring_base = ptx::smem_u32(ring);
     // tensor memory: step buffers of 128 columns (S, dP), then the sums: dv and dk, or dq
-    const uint32_t sum1 = tmem + 256, sum2 = tmem + 256 + D;
+    const uint32_t sum1 = tmem + BUFS * 128, sum2 = sum1 + D;
     bool ok = true;
     if (warp == 0) {
         // ------------------------------------------------------------ loads
@@ -238,16 +243,17 @@ k_attn_grad_tc(AttnArgs a, uint64_t wait_ns, const __grid_constant__ CUtensorMap
                     const int s = j % S::kStages;
                     const uint32_t parity = (j / S::kStages) & 1;
                     ok = attn_wait(&full[s], parity, wait_ns) && (!KEYS || attn_wait(&ready[s], parity, wait_ns));
-                    // in the place of P and dS, once the sums of step j - 2 have them
-                    if (ok && j >= 2) ok = attn_wait(&sum_full[j & 1], ((j - 2) >> 1) & 1, wait_ns);
+                    // in the place of P and dS, once the sums of step j - BUFS have them
+                    const int b = j % BUFS;
+                    if (ok && j >= BUFS) ok = attn_wait(&sum_full[b], (j / BUFS - 1) & 1, wait_ns);
                     if (!ok) break;
                     ptx::tc_fence_after();
                     if (attn_elect()) {
-                        const uint64_t b = k_desc + s * (S::kStage >> 4);
-                        const uint32_t d = tmem + (j & 1) * 128;
-                        attn_mma_ss<D / 16>(d, kept_desc, 16384, b, kStep * 128, idesc, steps);
-                        attn_mma_ss<D / 16>(d + 64, kept_desc + (S::kKept >> 4), 16384, b + (S::kHalf >> 4), kStep * 128, idesc, steps);
-                        ptx::mma_commit(&s_full[j & 1]);
+                        const uint64_t rows = k_desc + s * (S::kStage >> 4);
+                        const uint32_t d = tmem + b * 128;
+                        attn_mma_ss<D / 16>(d, kept_desc, 16384, rows, kStep * 128, idesc, steps);
+                        attn_mma_ss<D / 16>(d + 64, kept_desc + (S::kKept >> 4), 16384, rows + (S::kHalf >> 4), kStep * 128, idesc, steps);
+                        ptx::mma_commit(&s_full[b]);
                     }
                     __syncwarp();
                 }
@@ -255,14 +261,14 @@ k_attn_grad_tc(AttnArgs a, uint64_t wait_ns, const __grid_constant__ CUtensorMap
                 const uint32_t idesc = ptx::idesc_make(AttnFmt<T>::v, 128, steps * 16) | 1u << 16;
                 const uint64_t mn_desc = ptx::desc_mn_sw128(ring_base, kStep * 128);
                 for (int j = 0; j < n && ok; ++j) {
-                    const int s = j % S::kStages;
+                    const int s = j % S::kStages, b = j % BUFS;
                     const uint32_t parity = (j / S::kStages) & 1;
                     ok = attn_wait(&full[s], parity, wait_ns) && (!KEYS || attn_wait(&ready[s], parity, wait_ns)) &&
-                         attn_wait(&p_full[j & 1], (j >> 1) & 1, wait_ns);
+                         attn_wait(&p_full[b], (j / BUFS) & 1, wait_ns);
                     if (!ok) break;
                     ptx::tc_fence_after();
                     if (attn_elect()) {
-                        const uint32_t p = tmem + (j & 1) * 128;
+                        const uint32_t p = tmem + b * 128;
                         const uint64_t d1 = mn_desc + s * (S::kStage >> 4), d2 = d1 + (S::kHalf >> 4);
                         if (KEYS) {
 #pragma unroll
@@ -271,7 +277,7 @@ k_attn_grad_tc(AttnArgs a, uint64_t wait_ns, const __grid_constant__ CUtensorMap
 #pragma unroll
                         for (int q = 0; q < kStep / 16; ++q)  // dK += dS^T Q, dQ += dS K
                             ptx::mma_f16_ts(KEYS ? sum2 : sum1, p + 64 + q * 8, d1 + q * 128, idesc, q > 0 || j > 0);
-                        ptx::mma_commit(&sum_full[j & 1]);
+                        ptx::mma_commit(&sum_full[b]);
                         ptx::mma_commit(&empty[s]);
                         if (j + 1 == n) ptx::mma_commit(o_full);
                     }
@@ -342,24 +348,25 @@ k_attn_grad_tc(AttnArgs a, uint64_t wait_ns, const __grid_constant__ CUtensorMap
             my_lse = fetch(a.lse2 + (int64_t)kept_head * a.nq + row) + sc.up;
             my_delta = fetch(a.delta + (int64_t)kept_head * a.nq + row);
         }
-        for (int j = b; j < n; j += 2) {
+        for (int j = b; j < n; j += BUFS) {
             const int s = j % S::kStages;
-            ok = attn_wait(&s_full[b], (j >> 1) & 1, wait_ns);
+            ok = attn_wait(&s_full[b], (j / BUFS) & 1, wait_ns);
             if (KEYS && ok) ok = attn_wait(&ready[s], (j / S::kStages) & 1, wait_ns);
             if (!ok) break;
             ptx::tc_fence_after();
             const float* st = stats + s * 2 * kStep;
             const int64_t left = KEYS ? kStep : t.hi - step_row(j);
+            uint32_t sv[2][16], dp[2][16];
+            ptx::tmem_ld16(s_at, sv[0]);
+            ptx::tmem_ld16(s_at + 64, dp[0]);
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                uint32_t sv[32], dp[32], p[16], ds[16];
-                ptx::tmem_ld32(s_at + x * 32, sv);
-                ptx::tmem_ld32(s_at + 64 + x * 32, dp);
-                F2 ml[16], md[16];
+            for (int x = 0; x < 4; ++x) {
+                uint32_t p[8], ds[8];
+                F2 ml[8], md[8];
                 if (KEYS) {
 #pragma unroll
-                    for (int y = 0; y < 8; ++y) {
-                        const float4 l4 = *reinterpret_cast<const float4*>(st + x * 32 + 4 * y), d4 = *reinterpret_cast<const float4*>(st + kStep + x * 32 + 4 * y);
+                    for (int y = 0; y < 4; ++y) {
+                        const float4 l4 = *reinterpret_cast<const float4*>(st + x * 16 + 4 * y), d4 = *reinterpret_cast<const float4*>(st + kStep + x * 16 + 4 * y);
                         ml[2 * y] = F2{l4.x, l4.y};
                         ml[2 * y + 1] = F2{l4.z, l4.w};
                         if constexpr (std::is_same<T, __half>::value) {
@@ -371,23 +378,27 @@ k_attn_grad_tc(AttnArgs a, uint64_t wait_ns, const __grid_constant__ CUtensorMap
                     }
                 } else {
 #pragma unroll
-                    for (int y = 0; y < 16; ++y) {
+                    for (int y = 0; y < 8; ++y) {
                         ml[y] = both(my_lse);
                         md[y] = both(my_delta);
                     }
                 }
                 ptx::tmem_ld_wait();
-                grad32<T>(sv, dp, both(c), ml, md, both(sc.ds), p, ds);
+                if (x < 3) {  // the next columns while these are worked on
+                    ptx::tmem_ld16(s_at + (x + 1) * 16, sv[(x + 1) & 1]);
+                    ptx::tmem_ld16(s_at + 64 + (x + 1) * 16, dp[(x + 1) & 1]);
+                }
+                grad16<T>(sv[x & 1], dp[x & 1], both(c), ml, md, both(sc.ds), p, ds);
                 if (!KEYS && left < kStep) {
 #pragma unroll
-                    for (int y = 0; y < 16; ++y) {
-                        const int at = x * 32 + 2 * y;
+                    for (int y = 0; y < 8; ++y) {
+                        const int at = x * 16 + 2 * y;
                         ds[y] &= (at < left ? 0x0000ffffu : 0u) | (at + 1 < left ? 0xffff0000u : 0u);
                     }
                 }
-                // in the place of columns that have been read: 16 columns for every 32
-                if (KEYS) ptx::tmem_st16(s_at + x * 16, p);
-                ptx::tmem_st16(s_at + 64 + x * 16, ds);
+                // in the place of columns that have been read: 8 columns for every 16
+                if (KEYS) ptx::tmem_st8(s_at + x * 8, p);
+                ptx::tmem_st8(s_at + 64 + x * 8, ds);
             }
             ptx::tmem_st_wait();
             if (!KEYS && left < kStep) {
@@ -404,18 +415,21 @@ k_attn_grad_tc(AttnArgs a, uint64_t wait_ns, const __grid_constant__ CUtensorMap
         if (!ok && lane == 0) set_status(a.status, SPC_ERR_TIMEOUT);
         if (ok) {
             if (KEYS) {
-                // the first four warps dv, the others dk
+                // the first four warps dv, the next ones dk
                 const int64_t width = (int64_t)a.hk * a.d, off = row * width + (int64_t)kept_head * a.d, one = a.nk * width;
-                T* out = b == 0 ? static_cast<T*>(a.dv) + row * a.lddv + (int64_t)kept_head * a.d
-                                : static_cast<T*>(a.dk) + row * a.lddk + (int64_t)kept_head * a.d;
-                float* part = splits > 1 ? a.part_kv + ((b == 0 ? splits : 0) + blockIdx.z) * one + off : nullptr;
-                if (n > 0) store_row<T>((b == 0 ? sum1 : sum2) + lanes, 0, 32, a.d, b == 0 ? sc.back_p : sc.back_ds * a.scale, there, out, part);
-                else store_zeros<T>(0, 32, a.d, there, out, part);
-            } else {
+                for (int which = b; which < 2; which += BUFS == 1 ? 1 : 2) {
+                    T* out = which == 0 ? static_cast<T*>(a.dv) + row * a.lddv + (int64_t)kept_head * a.d
+                                        : static_cast<T*>(a.dk) + row * a.lddk + (int64_t)kept_head * a.d;
+                    float* part = splits > 1 ? a.part_kv + ((which == 0 ? splits : 0) + blockIdx.z) * one + off : nullptr;
+                    if (n > 0) store_row<T>((which == 0 ? sum1 : sum2) + lanes, 0, 32, a.d, which == 0 ? sc.back_p : sc.back_ds * a.scale, there, out, part);
+                    else store_zeros<T>(0, 32, a.d, there, out, part);
+                }
+            } else if (b < 2) {
                 T* out = static_cast<T*>(a.dq) + row * a.lddq + (int64_t)kept_head * a.d;
                 float* part = splits > 1 ? a.part + ((blockIdx.z * a.nq + row) * a.hq + kept_head) * a.d : nullptr;
-                if (n > 0) store_row<T>(sum1 + lanes, 32 * b, 64, a.d, sc.back_ds * a.scale, there, out, part);
-                else store_zeros<T>(32 * b, 64, a.d, there, out, part);
+                constexpr int kStride = BUFS == 1 ? 32 : 64;
+                if (n > 0) store_row<T>(sum1 + lanes, 32 * b, kStride, a.d, sc.back_ds * a.scale, there, out, part);
+                else store_zeros<T>(32 * b, kStride, a.d, there, out, part);
             }
         }
     }
@@ -424,14 +438,14 @@ k_attn_grad_tc(AttnArgs a, uint64_t wait_ns, const __grid_constant__ CUtensorMap
     __syncthreads();
     if (warp == 1) {
         ptx::tc_fence_after();
-        ptx::tmem_dealloc(tmem, 512);
+        ptx::tmem_dealloc(tmem, S::kCols);
     }
 }
 
-template <typename T, int D, bool KEYS>
+template <typename T, int D, int BUFS, bool KEYS>
 spc_status launch(const AttnArgs& a, cudaStream_t st)
 {
-    using S = Shape<D>;
+    using S = Shape<D, BUFS>;
     CUtensorMap q, g, k, v;
     const int box_q = KEYS ? kStep : 128, box_k = KEYS ? 128 : kStep;
     if (!attn_tmap<T>(&q, a.q, a.ldq, a.nq, a.hq, a.d, 1, box_q) || !attn_tmap<T>(&g, a.dout, a.lddo, a.nq, a.hq, a.d, 1, box_q) ||
@@ -439,26 +453,35 @@ spc_status launch(const AttnArgs& a, cudaStream_t st)
         return SPC_ERR_UNSUPPORTED;
     const int64_t slots = attn_slots(KEYS ? a.nk : a.nq, a.segments, 128);
     if (slots > INT32_MAX) return SPC_ERR_UNSUPPORTED;
-    const spc_status s = allow_smem<k_attn_grad_tc<T, D, KEYS>>();
+    const spc_status s = allow_smem<k_attn_grad_tc<T, D, BUFS, KEYS>>();
     if (s != SPC_OK) return s;
     const dim3 grid((unsigned)slots, (unsigned)(KEYS ? a.hk : a.hq), (unsigned)(KEYS ? a.splits_kv : a.splits));
-    return KEYS ? attn_start_kernel<k_attn_grad_tc<T, D, KEYS>>(grid, S::kThreads, S::kSmem, st, a, wait_limit_ns(), k, v, q, g)
-                : attn_start_kernel<k_attn_grad_tc<T, D, KEYS>>(grid, S::kThreads, S::kSmem, st, a, wait_limit_ns(), q, g, k, v);
+    if (KEYS) return attn_start_kernel<k_attn_grad_tc<T, D, BUFS, KEYS>>(grid, S::kThreads, S::kSmem, st, a, wait_limit_ns(), k, v, q, g);
+    return attn_start_kernel<k_attn_grad_tc<T, D, BUFS, KEYS>>(grid, S::kThreads, S::kSmem, st, a, wait_limit_ns(), q, g, k, v);
 }
 
-template <typename T, int D>
+template <typename T, bool KEYS>
+spc_status pick(const AttnArgs& a, cudaStream_t st)
+{
+    if (a.d > 64) return launch<T, 128, 2, KEYS>(a, st);
+    // steps of a block's walk, were all segments alike
+    const int64_t steps = KEYS ? ceil_div(a.nq, (int64_t)a.segments * kStep) * (a.hq / a.hk) / a.splits_kv
+                               : ceil_div(a.nk, (int64_t)a.segments * kStep) / a.splits;
+    return steps <= kShortWalk ? launch<T, 64, 1, KEYS>(a, st) : launch<T, 64, 3, KEYS>(a, st);
+}
+
+template <typename T>
 spc_status both_kernels(const AttnArgs& a, cudaStream_t st)
 {
-    const spc_status s = launch<T, D, true>(a, st);
-    return s != SPC_OK ? s : launch<T, D, false>(a, st);
+    const spc_status s = pick<T, true>(a, st);
+    return s != SPC_OK ? s : pick<T, false>(a, st);
 }
 
 }  // namespace
 
 spc_status attention_bwd_tc(const AttnArgs& a, spc_dtype dt, cudaStream_t st)
 {
-    if (dt == SPC_F16) return a.d <= 64 ? both_kernels<__half, 64>(a, st) : both_kernels<__half, 128>(a, st);
-    return a.d <= 64 ? both_kernels<__nv_bfloat16, 64>(a, st) : both_kernels<__nv_bfloat16, 128>(a, st);
+    return dt == SPC_F16 ? both_kernels<__half>(a, st) : both_kernels<__nv_bfloat16>(a, st);
 }
 
 }  // namespace spc
