@@ -1,5 +1,6 @@
-"""Build libspc.so from the CUDA sources in csrc/ (maps, convolutions, pooling) and
-csrc_layers/ (the layers between convolutions) with nvcc, in-tree.
+"""Build libspc.so from the CUDA sources in csrc/ (maps, convolutions, pooling),
+csrc_layers/ (the layers between convolutions) and csrc_block/ (a transformer block's
+layers) with nvcc, in-tree.
 
 The library is compiled for sm_103a only (one -gencode), one object per
 translation unit in parallel, then linked into a shared library with the CUDA
@@ -19,6 +20,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 CSRC_LAYERS = os.path.join(HERE, "csrc_layers")
+CSRC_BLOCK = os.path.join(HERE, "csrc_block")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libspc.so")
@@ -36,12 +38,12 @@ def nvcc() -> str:
 
 
 def sources():
-    return sorted(glob.glob(os.path.join(CSRC, "*.cu"))) + sorted(glob.glob(os.path.join(CSRC_LAYERS, "*.cu")))
+    return [f for d in (CSRC, CSRC_LAYERS, CSRC_BLOCK) for f in sorted(glob.glob(os.path.join(d, "*.cu")))]
 
 
 def _deps():
     return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) \
-        + glob.glob(os.path.join(CSRC_LAYERS, "*.cuh")) \
+        + glob.glob(os.path.join(CSRC_LAYERS, "*.cuh")) + glob.glob(os.path.join(CSRC_BLOCK, "*.cuh")) \
         + glob.glob(os.path.join(INCLUDE, "*.h")) \
         + [os.path.abspath(__file__)]
 
@@ -63,7 +65,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
 
     def compile_one(src):
         obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
-        cmd = [cc, *ARCH, *FLAGS, "-I", INCLUDE, "-I", CSRC, "-I", CSRC_LAYERS, "-c", src, "-o", obj]
+        cmd = [cc, *ARCH, *FLAGS, "-I", INCLUDE, "-I", CSRC, "-I", CSRC_LAYERS, "-I", CSRC_BLOCK, "-c", src, "-o", obj]
         if verbose:
             print(" ".join(cmd), flush=True)
         r = subprocess.run(cmd, capture_output=True, text=True)

@@ -7,6 +7,7 @@
 #include <math.h>
 
 #include "attention.cuh"
+#include "block.cuh"
 
 using namespace spc;
 

@@ -9,7 +9,7 @@
 //
 // Bound by memory: 16 operations stand against 4 to 8 bytes an element.  What has to be right is the number
 // of bytes in flight, so a group works on R rows at once.
-#include "layers.cuh"
+#include "block.cuh"
 #include "pairs.cuh"
 
 namespace spc {

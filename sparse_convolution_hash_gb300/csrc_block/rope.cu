@@ -7,7 +7,7 @@
 // heads, several in flight: one sine and cosine for `heads` pairs, and memory is what bounds it.
 #include <math.h>
 
-#include "layers.cuh"
+#include "block.cuh"
 #include "pairs.cuh"
 
 namespace spc {

@@ -11,7 +11,7 @@
 // Bound by instructions: a row of 64 experts in 16 bits is 128 bytes and some 200 instructions.
 #include <math.h>
 
-#include "layers.cuh"
+#include "block.cuh"
 #include "pairs.cuh"
 
 namespace spc {
