@@ -748,7 +748,7 @@ SPC_API spc_status spc_route_bwd(const float* dgate, const void* logits, const i
  *         apart (slices of one projection are read in place).  hk divides hq: query head h
  *         reads key head h / (hq / hk).  d 1 .. 128.
  *  scale  > 0, finite.
- *  o      nq rows of [hq, d] of dtype dt out, ldo apart.     lse [nq, hq] fp32 out.
+ *  o      nq rows of [hq, d] of dtype dt out, ldo apart; it overlaps no argument.     lse [nq, hq] fp32 out.
  *  status device int32 sticky error word, or NULL (SPC_ERR_ROW_INDEX, SPC_ERR_TIMEOUT).
  *  ws     spc_attention_workspace_size(..., backward = 0) bytes, 256-byte aligned (0: none needed).
  *  Probabilities are rounded to dt before the product with v on tensor cores; sums and the softmax

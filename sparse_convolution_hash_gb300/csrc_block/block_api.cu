@@ -58,6 +58,15 @@ spc_status check_route(const void* logits, int64_t n, int32_t experts, int32_t t
     return experts > SPC_MAX_SEGMENTS || top_k > SPC_MAX_TOP_K ? SPC_ERR_UNSUPPORTED : SPC_OK;
 }
 
+// Whether a result starts where an argument (or another result) does.
+template <size_t N>
+bool among(const void* result, const void* const (&others)[N])
+{
+    for (const void* p : others)
+        if (result && result == p) return true;
+    return false;
+}
+
 spc_status check_attention(const AttnArgs& a, spc_dtype dt, bool backward)
 {
     if (!dtype_ok(dt) || a.nq < 0 || a.nk < 0 || a.segments < 1 || a.hq < 1 || a.hk < 1 || a.d < 1) return SPC_ERR_INVALID_ARG;
@@ -74,6 +83,10 @@ spc_status check_attention(const AttnArgs& a, spc_dtype dt, bool backward)
         if (!rows_ok(a.dout, a.nq, dt) || !rows_ok(a.dq, a.nq, dt) || !rows_ok(a.dk, a.nk, dt) || !rows_ok(a.dv, a.nk, dt))
             return SPC_ERR_INVALID_ARG;
     }
+    if (!backward && among(a.o, {a.q, a.k, a.v})) return SPC_ERR_INVALID_ARG;
+    if (backward && (among(a.dq, {a.q, a.k, a.v, a.o, a.dout, a.dk, a.dv}) || among(a.dk, {a.q, a.k, a.v, a.o, a.dout, a.dv}) ||
+                     among(a.dv, {a.q, a.k, a.v, a.o, a.dout})))
+        return SPC_ERR_INVALID_ARG;
     if (a.d > 128 || a.hq > 65535 || a.nq > INT32_MAX - 1 || a.nk > INT32_MAX - 1 || a.segments > INT32_MAX - 4) return SPC_ERR_UNSUPPORTED;
     return SPC_OK;
 }
