@@ -11,6 +11,7 @@ built, loading raises ``SpcLibraryMissing``.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 from typing import Optional, Sequence
@@ -846,10 +847,17 @@ def spc_grouped_wgrad(x: torch.Tensor, dy: torch.Tensor, seg: torch.Tensor,
 
 # A transformer block's layers.  Their tensors lie on one device, whichever is current.
 
-def _one_device(dev, **tensors):
-    for name, t in tensors.items():
+def _one_device(dev, *tensors):
+    for t in tensors:
         if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+            raise ValueError(f"a tensor of shape {tuple(t.shape)} is on {t.device}, expected {dev}")
+
+
+def _two_results(a, b, shape, dev, names):
+    """Two fp32 results of one shape: the caller's, checked, or new ones (in one allocation where both are)."""
+    if a is None and b is None:
+        return torch.empty((2, *shape), dtype=torch.float32, device=dev).unbind(0)
+    return _result(a, shape, torch.float32, dev, names[0]), _result(b, shape, torch.float32, dev, names[1])
 
 
 def _launch(dev, f, *args):
@@ -904,10 +912,9 @@ def spc_layer_norm_fwd(x: torch.Tensor, gamma: Optional[torch.Tensor], beta: Opt
     dev = x.device
     gamma, gamma_p = _optional(gamma, torch.float32, (c,), "gamma")
     beta, beta_p = _optional(beta, torch.float32, (c,), "beta")
-    _one_device(dev, gamma=gamma, beta=beta)
+    _one_device(dev, gamma, beta)
     y = _result(out, (n, c), x.dtype, dev, "out")
-    mean = _result(mean, (n,), torch.float32, dev, "mean")
-    rstd = _result(rstd, (n,), torch.float32, dev, "rstd")
+    mean, rstd = _two_results(mean, rstd, (n,), dev, ("mean", "rstd"))
     code = _launch(dev, lib().spc_layer_norm_fwd, x.data_ptr(), gamma_p, beta_p, n, c, eps, _DTYPES[x.dtype], y.data_ptr(),
                    mean.data_ptr(), rstd.data_ptr())
     _check(code, "spc_layer_norm_fwd")
@@ -927,10 +934,9 @@ def spc_layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, gamma: Optional[torch.
     gamma, gamma_p = _optional(gamma, torch.float32, (c,), "gamma")
     mean, mean_p = _optional(mean, torch.float32, (n,), "mean")
     rstd, rstd_p = _optional(rstd, torch.float32, (n,), "rstd")
-    _one_device(dev, dy=dy, gamma=gamma, mean=mean, rstd=rstd, ws=ws)
+    _one_device(dev, dy, gamma, mean, rstd, ws)
     dx = _result(out, (n, c), x.dtype, dev, "out")
-    dgamma = _result(dgamma, (c,), torch.float32, dev, "dgamma")
-    dbeta = _result(dbeta, (c,), torch.float32, dev, "dbeta")
+    dgamma, dbeta = _two_results(dgamma, dbeta, (c,), dev, ("dgamma", "dbeta"))
     L = lib()
     ws = _room(ws, _launch_size(dev, L.spc_layer_norm_workspace_size, n, c), dev)
     code = _launch(dev, L.spc_layer_norm_bwd, dy.data_ptr(), x.data_ptr(), gamma_p, mean_p, rstd_p, n, c, _DTYPES[x.dtype],
@@ -947,38 +953,40 @@ def _launch_size(dev, f, *args) -> int:
         return f(*args)
 
 
-def _three(pairs) -> tuple:
+@functools.lru_cache(maxsize=64)
+def _three(pairs: tuple):
+    """(C array, sum) of the numbers of turned pairs of channels for z, y and x."""
     t = tuple(int(p) for p in pairs)
     if len(t) != 3 or min(t) < 0:
         raise ValueError("pairs must hold the number of turned pairs of channels for z, y and x")
-    return t
+    return _I3(*t), sum(t)
 
 
 def spc_rope_steps(pairs: Sequence[int], base: float = 10000.0) -> torch.Tensor:
     """Steps of spc_rope_fwd for base^(-j / pairs[axis]) radians a cell, j = 0 .. pairs[axis] - 1: a CPU tensor
     [sum(pairs)] int64, 2^64 to a full turn.  Computed once, kept by the caller."""
-    pairs = _three(pairs)
-    steps = torch.empty(sum(pairs), dtype=torch.int64)
-    _check(lib().spc_rope_steps(_I3(*pairs), base, steps.data_ptr() if sum(pairs) else None), "spc_rope_steps")
+    counts, turned = _three(tuple(pairs))
+    steps = torch.empty(turned, dtype=torch.int64)
+    _check(lib().spc_rope_steps(counts, base, steps.data_ptr() if turned else None), "spc_rope_steps")
     return steps
 
 
-def _rope(name: str, x: torch.Tensor, coords: torch.Tensor, steps: torch.Tensor, pairs, out):
+def _rope(f, name: str, x: torch.Tensor, coords: torch.Tensor, steps: torch.Tensor, pairs, out):
     x, ldx = _head_rows(x, "x")
     n, heads, d = x.shape
     dev = x.device
-    pairs = _three(pairs)
+    counts, turned = _three(tuple(pairs))
     if not coords.is_cuda or coords.dtype is not torch.int32:
         raise ValueError("coords must be an int32 CUDA tensor")
     _expect(coords, (n, 4), "coords")
     coords = coords if coords.is_contiguous() else coords.contiguous()
     if steps.is_cuda or steps.dtype is not torch.int64 or not steps.is_contiguous():
         raise ValueError("steps must be a contiguous int64 CPU tensor (spc_rope_steps)")
-    _expect(steps, (sum(pairs),), "steps")
-    _one_device(dev, coords=coords)
+    _expect(steps, (turned,), "steps")
+    _one_device(dev, coords)
     y, ldy = _head_result(out, (n, heads, d), x.dtype, dev, "out")
-    code = _launch(dev, getattr(lib(), name), x.data_ptr(), ldx, coords.data_ptr(), _I3(*pairs),
-                   steps.data_ptr() if sum(pairs) else None, n, heads, d, _DTYPES[x.dtype], y.data_ptr(), ldy)
+    code = _launch(dev, f, x.data_ptr(), ldx, coords.data_ptr(), counts, steps.data_ptr() if turned else None, n, heads, d,
+                   _DTYPES[x.dtype], y.data_ptr(), ldy)
     _check(code, name)
     return y
 
@@ -989,13 +997,13 @@ def spc_rope_fwd(x: torch.Tensor, coords: torch.Tensor, steps: torch.Tensor, pai
     cell times the pair's step, the first pairs[0] pairs by z, the next pairs[1] by y, the next pairs[2] by x of
     coords [n, 4] int32 (b, z, y, x); the rest is copied.  A slice of a projection's rows (qkv[:, :2 * heads]) is
     read in place; `out` may be such a slice, or x itself."""
-    return _rope("spc_rope_fwd", x, coords, steps, pairs, out)
+    return _rope(lib().spc_rope_fwd, "spc_rope_fwd", x, coords, steps, pairs, out)
 
 
 def spc_rope_bwd(dy: torch.Tensor, coords: torch.Tensor, steps: torch.Tensor, pairs: Sequence[int],
                  out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The gradient of spc_rope_fwd: the same turns backwards."""
-    return _rope("spc_rope_bwd", dy, coords, steps, pairs, out)
+    return _rope(lib().spc_rope_bwd, "spc_rope_bwd", dy, coords, steps, pairs, out)
 
 
 def spc_route_fwd(logits: torch.Tensor, top_k: int, score: int = SPC_SCORE_SOFTMAX, bias: Optional[torch.Tensor] = None,
@@ -1009,7 +1017,7 @@ def spc_route_fwd(logits: torch.Tensor, top_k: int, score: int = SPC_SCORE_SOFTM
     n, experts = logits.shape
     dev = logits.device
     bias, bias_p = _optional(bias, torch.float32, (experts,), "bias")
-    _one_device(dev, bias=bias)
+    _one_device(dev, bias)
     expert = _result(expert, (n, top_k), torch.int32, dev, "expert")
     gate = _result(gate, (n, top_k), torch.float32, dev, "gate")
     code = _launch(dev, lib().spc_route_fwd, logits.data_ptr(), bias_p, n, experts, top_k, score, groups, top_groups, bool(renorm),
@@ -1033,7 +1041,7 @@ def spc_route_bwd(dgate: torch.Tensor, logits: torch.Tensor, expert: torch.Tenso
     _expect(expert, (n, top_k), "expert")
     dgate = _typed(dgate, torch.float32, "dgate")
     _expect(dgate, (n, top_k), "dgate")
-    _one_device(dev, expert=expert, dgate=dgate, status=status)
+    _one_device(dev, expert, dgate, status)
     dlogits = _result(out, (n, experts), logits.dtype, dev, "out")
     code = _launch(dev, lib().spc_route_bwd, dgate.data_ptr(), logits.data_ptr(), expert.data_ptr(), n, experts, top_k, score,
                    bool(renorm), scale, _DTYPES[logits.dtype], dlogits.data_ptr(), _status(status))
@@ -1059,7 +1067,7 @@ def _attention_args(q, k, v, seg, seg_k, scale):
     else:
         seg_k = _typed(seg_k, torch.int32, "seg_k")
         _expect(seg_k, seg.shape, "seg_k")
-    _one_device(dev, k=k, v=v, seg=seg, seg_k=seg_k)
+    _one_device(dev, k, v, seg, seg_k)
     return q, ldq, k, ldk, v, ldv, seg, seg_k, nq, nk, hq, hk, d, d ** -0.5 if scale is None else scale, dev
 
 
@@ -1074,7 +1082,7 @@ def spc_attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seg: to
     segments, `seg_k` those of the keys (None: the same rows).  scale None: d^-0.5.  A query without keys
     gives 0 and lse -inf.  Pass `out`, `lse` and `ws` to call without allocating."""
     q, ldq, k, ldk, v, ldv, seg, seg_k, nq, nk, hq, hk, d, scale, dev = _attention_args(q, k, v, seg, seg_k, scale)
-    _one_device(dev, ws=ws, status=status)
+    _one_device(dev, ws, status)
     o, ldo = _head_result(out, (nq, hq, d), q.dtype, dev, "out")
     lse = _result(lse, (nq, hq), torch.float32, dev, "lse")
     L, dt, segments = lib(), _DTYPES[q.dtype], seg.shape[0] - 1
@@ -1101,7 +1109,7 @@ def spc_attention_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: t
     o, ldo = _head_rows(o if o.dtype is q.dtype else o.to(q.dtype), "o")
     _expect(o, (nq, hq, d), "o")
     lse, lse_p = _optional(lse, torch.float32, (nq, hq), "lse")
-    _one_device(dev, dout=dout, o=o, lse=lse, ws=ws, status=status)
+    _one_device(dev, dout, o, lse, ws, status)
     dq, lddq = _head_result(dq, (nq, hq, d), q.dtype, dev, "dq")
     dk, lddk = _head_result(dk, (nk, hk, d), q.dtype, dev, "dk")
     dv, lddv = _head_result(dv, (nk, hk, d), q.dtype, dev, "dv")

@@ -59,38 +59,62 @@ Layout layout(int64_t nq, int64_t nk, int32_t segments, int32_t hq, int32_t hk, 
     return l;
 }
 
-// o and lse from the splits': weights exp(lse_z - lse).  A warp to a row and head.
+// o and lse from the splits': weights exp(lse_z - lse).  A block to a row and head; its warps take the splits in turn, each
+// with a maximum and sum of its own, and join in order (a warp alone waits for memory once for every split: 24 us for
+// the 38 splits of 4 queries, 8 heads).
+constexpr int kJoinWarps = 8;
 template <typename T>
-__global__ void __launch_bounds__(kBlock)
+__global__ void __launch_bounds__(32 * kJoinWarps)
 k_attn_join(AttnArgs a)
 {
+    __shared__ float box[kJoinWarps][4 * 32], tops[kJoinWarps], totals[kJoinWarps];
     wait_for_kernel_before();
-    const int64_t i = (int64_t)blockIdx.x * (kBlock / 32) + threadIdx.x / 32, rows = a.nq * a.hq;
-    const int lane = threadIdx.x & 31;
-    if (i >= rows) return;
+    const int64_t i = blockIdx.x, rows = a.nq * a.hq;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     float most = -INFINITY;
-    for (int z = lane; z < a.splits; z += 32) most = fmaxf(most, fetch(a.part_lse + z * rows + i));
+    for (int z = warp + kJoinWarps * lane; z < a.splits; z += 32 * kJoinWarps) most = fmaxf(most, fetch(a.part_lse + z * rows + i));
 #pragma unroll
     for (int o = 16; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(FULL_MASK, most, o));
     float total = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
     // an infinite or NaN sum is one split's: its weight is 1, so that it reaches the result
-    for (int z = 0; z < a.splits; ++z) {
+#pragma unroll 4
+    for (int z = warp; z < a.splits; z += kJoinWarps) {
         const float l = fetch(a.part_lse + z * rows + i);
-        if (l == -INFINITY) continue;
-        const float w = l == most ? 1.f : expf(l - most);
-        total += w;
         const float* from = a.part + (z * rows + i) * a.d;
+        float x[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (lane + 32 * j < a.d) v[j] = fmaf(w, fetch(from + lane + 32 * j), v[j]);
+        for (int j = 0; j < 4; ++j) x[j] = lane + 32 * j < a.d ? fetch(from + lane + 32 * j) : 0.f;
+        const bool there = l != -INFINITY;  // a split without keys has written no sums
+        const float w = !there ? 0.f : l == most ? 1.f : expf(l - most);
+        total += w;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = there ? fmaf(w, x[j], v[j]) : v[j];
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) box[warp][32 * j + lane] = v[j];
+    if (lane == 0) {
+        tops[warp] = most;
+        totals[warp] = total;
+    }
+    __syncthreads();
+    const int c = threadIdx.x;
+    if (c >= 128) return;
+    most = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) most = fmaxf(most, tops[w]);
+    total = 0.f;
+    float sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+        if (totals[w] == 0.f) continue;
+        const float f = tops[w] == most ? 1.f : expf(tops[w] - most);
+        total = fmaf(f, totals[w], total);
+        sum = fmaf(f, box[w][c], sum);
     }
     const int64_t row = i / a.hq, head = i - row * a.hq;
-    T* to = static_cast<T*>(a.o) + row * a.ldo + head * a.d;
-    const float inv = total > 0.f || total != total ? 1.f / total : 0.f;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-        if (lane + 32 * j < a.d) to[lane + 32 * j] = elem<T>::from_f32(v[j] * inv);
-    if (lane == 0) a.lse[i] = total > 0.f || total != total ? most + logf(total) : -INFINITY;
+    const bool any = total > 0.f || total != total;
+    if (c < a.d) static_cast<T*>(a.o)[row * a.ldo + head * a.d + c] = elem<T>::from_f32(any ? sum / total : 0.f);
+    if (c == 0) a.lse[i] = any ? most + logf(total) : -INFINITY;
 }
 
 // Sums of the splits' gradients in order; rows of `width` values, at `ld` in the result.
@@ -102,9 +126,26 @@ k_attn_sum(const float* part, int splits, int64_t rows, int width, T* to, int64_
     const int64_t i = (int64_t)blockIdx.x * kBlock + threadIdx.x, all = rows * width;
     if (i >= all) return;
     float s = 0.f;
+#pragma unroll 4
     for (int z = 0; z < splits; ++z) s += fetch(part + z * all + i);
     const int64_t row = i / width;
     to[row * ld + (i - row * width)] = elem<T>::from_f32(s);
+}
+
+// The largest of a block's values into a word that holds the bits of a non-negative float: those are ordered as the numbers
+// are, and the largest does not depend on the order of the blocks.  Values that are not finite have no say (their
+// rows' results are not either).  One atomic a block, and none where the word is as large already: with one a warp the
+// blocks queued up for it (480,000 rows of 32: 81 us against 9).
+__device__ __forceinline__ void block_most(float v, uint32_t* word)
+{
+    __shared__ uint32_t box[kBlock / 32];
+    const uint32_t b = __reduce_max_sync(FULL_MASK, v < INFINITY ? __float_as_uint(v) : 0u);
+    if ((threadIdx.x & 31) == 0) box[threadIdx.x >> 5] = b;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        const uint32_t all = __reduce_max_sync(FULL_MASK, threadIdx.x < kBlock / 32 ? box[threadIdx.x] : 0u);
+        if (threadIdx.x == 0 && all > *static_cast<volatile uint32_t*>(word)) atomicMax(word, all);
+    }
 }
 
 // minus the sum of do o over a head's channels, and minus lse to base 2: eight lanes to a row and head.  fp16 also takes the
@@ -151,12 +192,7 @@ k_attn_delta(AttnArgs a)
         a.delta[head * a.nq + row] = -s;
         a.lse2[head * a.nq + row] = lse == -INFINITY ? -INFINITY : -lse * 1.44269504088896340736f;
     }
-    if (MOST) {
-        // non-negative floats are ordered as their bits are; the largest does not depend on the order.  Rows that are
-        // not finite have no say (their results are not either)
-        const uint32_t b = __reduce_max_sync(FULL_MASK, most < INFINITY ? __float_as_uint(most) : 0u);
-        if ((threadIdx.x & 31) == 0) atomicMax(a.most, b);
-    }
+    if (MOST) block_most(most, a.most);
 }
 
 // fp16: the largest norm of a row of v.
@@ -178,16 +214,14 @@ k_attn_most_v(AttnArgs a)
     }
 #pragma unroll
     for (int o = 4; o; o >>= 1) most += __shfl_xor_sync(FULL_MASK, most, o);
-    const uint32_t b = __reduce_max_sync(FULL_MASK, most < INFINITY ? __float_as_uint(most) : 0u);
-    if ((threadIdx.x & 31) == 0) atomicMax(a.most + 1, b);
+    block_most(most, a.most + 1);
 }
 
 template <typename T>
 spc_status join_fwd(const AttnArgs& a, cudaStream_t st)
 {
-    const int64_t blocks = ceil_div(a.nq * a.hq, kBlock / 32);
-    if (blocks > INT32_MAX) return SPC_ERR_UNSUPPORTED;
-    return attn_start_kernel<k_attn_join<T>>(dim3((unsigned)blocks), kBlock, 0, st, a);
+    if (a.nq * a.hq > INT32_MAX) return SPC_ERR_UNSUPPORTED;
+    return attn_start_kernel<k_attn_join<T>>(dim3((unsigned)(a.nq * a.hq)), 32 * kJoinWarps, 0, st, a);
 }
 
 template <typename T>
