@@ -853,13 +853,6 @@ def _one_device(dev, *tensors):
             raise ValueError(f"a tensor of shape {tuple(t.shape)} is on {t.device}, expected {dev}")
 
 
-def _two_results(a, b, shape, dev, names):
-    """Two fp32 results of one shape: the caller's, checked, or new ones (in one allocation where both are)."""
-    if a is None and b is None:
-        return torch.empty((2, *shape), dtype=torch.float32, device=dev).unbind(0)
-    return _result(a, shape, torch.float32, dev, names[0]), _result(b, shape, torch.float32, dev, names[1])
-
-
 def _launch(dev, f, *args):
     """Calls a C entry with `dev` as the current device and its current stream as the last argument."""
     if torch._C._cuda_getDevice() == dev.index:
@@ -914,7 +907,8 @@ def spc_layer_norm_fwd(x: torch.Tensor, gamma: Optional[torch.Tensor], beta: Opt
     beta, beta_p = _optional(beta, torch.float32, (c,), "beta")
     _one_device(dev, gamma, beta)
     y = _result(out, (n, c), x.dtype, dev, "out")
-    mean, rstd = _two_results(mean, rstd, (n,), dev, ("mean", "rstd"))
+    mean = _result(mean, (n,), torch.float32, dev, "mean")
+    rstd = _result(rstd, (n,), torch.float32, dev, "rstd")
     code = _launch(dev, lib().spc_layer_norm_fwd, x.data_ptr(), gamma_p, beta_p, n, c, eps, _DTYPES[x.dtype], y.data_ptr(),
                    mean.data_ptr(), rstd.data_ptr())
     _check(code, "spc_layer_norm_fwd")
@@ -936,7 +930,8 @@ def spc_layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, gamma: Optional[torch.
     rstd, rstd_p = _optional(rstd, torch.float32, (n,), "rstd")
     _one_device(dev, dy, gamma, mean, rstd, ws)
     dx = _result(out, (n, c), x.dtype, dev, "out")
-    dgamma, dbeta = _two_results(dgamma, dbeta, (c,), dev, ("dgamma", "dbeta"))
+    dgamma = _result(dgamma, (c,), torch.float32, dev, "dgamma")
+    dbeta = _result(dbeta, (c,), torch.float32, dev, "dbeta")
     L = lib()
     ws = _room(ws, _launch_size(dev, L.spc_layer_norm_workspace_size, n, c), dev)
     code = _launch(dev, L.spc_layer_norm_bwd, dy.data_ptr(), x.data_ptr(), gamma_p, mean_p, rstd_p, n, c, _DTYPES[x.dtype],

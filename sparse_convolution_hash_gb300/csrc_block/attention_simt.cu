@@ -19,11 +19,21 @@ constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f
 template <int DP> struct Mat { float v[kTile][DP + kPad]; };
 struct Probs { float v[kTile][kTile + kPad]; };
 
-// Rows [row, end) of one head as fp32, zeros past the end and past d.
+// Rows [row, end) of one head as fp32, zeros past the end and past d: four channels at once where fp32 rows allow it.
 template <typename T, int DP>
 __device__ __forceinline__ void load(Mat<DP>& m, const void* base, int64_t ld, int head, int d, int64_t row, int64_t end)
 {
     const T* p = static_cast<const T*>(base) + (int64_t)head * d;
+    if (sizeof(T) == 4 && ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)(ld * 4) | (uintptr_t)(d * 4)) & 15) == 0) {
+#pragma unroll
+        for (int i = threadIdx.x; i < kTile * DP / 4; i += kThreads) {
+            const int r = i / (DP / 4), c = i % (DP / 4) * 4;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (row + r < end && c < d) v = *reinterpret_cast<const float4*>(p + (row + r) * ld + c);
+            *reinterpret_cast<float4*>(&m.v[r][c]) = v;
+        }
+        return;
+    }
     for (int i = threadIdx.x; i < kTile * DP; i += kThreads) {
         const int r = i / DP, c = i % DP;
         m.v[r][c] = row + r < end && c < d ? elem<T>::to_f32(p[(row + r) * ld + c]) : 0.f;
@@ -357,6 +367,7 @@ spc_status bwd(const AttnArgs& a, cudaStream_t st)
 template <typename T>
 spc_status any(const AttnArgs& a, bool backward, cudaStream_t st)
 {
+    if (a.d <= 16) return backward ? bwd<T, 16>(a, st) : fwd<T, 16>(a, st);
     if (a.d <= 32) return backward ? bwd<T, 32>(a, st) : fwd<T, 32>(a, st);
     if (a.d <= 64) return backward ? bwd<T, 64>(a, st) : fwd<T, 64>(a, st);
     return backward ? bwd<T, 128>(a, st) : fwd<T, 128>(a, st);

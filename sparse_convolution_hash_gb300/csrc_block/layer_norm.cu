@@ -87,10 +87,20 @@ __device__ __forceinline__ void store_row(T* row, const Place<V, WHOLE>& w, int 
 template <int V, bool WHOLE>
 __device__ __forceinline__ void load_affine(const float* p, float other, const Place<V, WHOLE>& w, int k, F2 (&f)[V / 2])
 {
+    if constexpr (WHOLE) {
 #pragma unroll
-    for (int j = 0; j < V / 2; ++j) {
-        f[j].x = p && w.in(k, 2 * j) ? fetch(p + w.at(k, 2 * j)) : other;
-        f[j].y = p && w.in(k, 2 * j + 1) ? fetch(p + w.at(k, 2 * j + 1)) : other;
+        for (int j = 0; j < V; j += 4) {
+            float4 v = make_float4(other, other, other, other);
+            if (p && w.in(k, 0)) v = *reinterpret_cast<const float4*>(p + w.at(k, j));
+            f[j / 2] = F2{v.x, v.y};
+            f[j / 2 + 1] = F2{v.z, v.w};
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < V / 2; ++j) {
+            f[j].x = p && w.in(k, 2 * j) ? fetch(p + w.at(k, 2 * j)) : other;
+            f[j].y = p && w.in(k, 2 * j + 1) ? fetch(p + w.at(k, 2 * j + 1)) : other;
+        }
     }
 }
 
@@ -498,7 +508,8 @@ template <typename T>
 spc_status any(const LayerNormArgs& a, float* part, bool backward, cudaStream_t st)
 {
     // 16-byte vectors where rows and tensors start on such a boundary
-    const bool whole = a.c % (16 / (int)sizeof(T)) == 0 && aligned16(a.x) && aligned16(a.out) && aligned16(a.dy);
+    const bool whole = a.c % (16 / (int)sizeof(T)) == 0 && aligned16(a.x) && aligned16(a.out) && aligned16(a.dy) &&
+                       aligned16(a.gamma) && aligned16(a.beta);
     if (backward) return whole ? bwd_any<T, true>(a, part, st) : bwd_any<T, false>(a, part, st);
     return whole ? fwd_any<T, true>(a, st) : fwd_any<T, false>(a, st);
 }
