@@ -32,7 +32,7 @@ Layout layout(int64_t nq, int64_t nk, int32_t segments, int32_t hq, int32_t hk, 
     Layout l = {};
     const bool tc = wide_enough(d, dt);
     if (tc && !backward) {
-        const AttnShape f = attn_shape(nq, segments, hq, hk);
+        const AttnShape f = attn_shape(nq, segments, hq, hk, d);
         l.splits = splits_for(nq, segments, hq / f.heads, nk, f.positions * f.tiles, kLeastShare, f.tiles == 2 ? 1 : 2);
     } else {
         l.splits = splits_for(nq, segments, hq, nk, kSimtRows, kLeastShare, 2);
@@ -266,8 +266,12 @@ spc_status row_sums(const AttnArgs& a, bool most, cudaStream_t st)
 }  // namespace
 
 // The query heads of a tile: as many of those that share a key head as divide them and leave a tile two positions.
-// Two tiles to a block where a segment has rows for them and the halved number of blocks still fills the SMs.
-AttnShape attn_shape(int64_t nq, int32_t segments, int32_t hq, int32_t hk)
+// A block of one tile leaves room for a second block on the SM, a block of two reads keys half as often.  One is faster
+// for heads of up to 64 channels whatever the length (8 heads, 32,768 rows in samples of 200 to 32,768: 131 against 158 us
+// at 200 rows, 606 against 642 at 8,192, 2,254 against 2,268 at 32,768), two for wider heads from some 1,500 rows
+// a segment on (8 heads of 128: 222 against 237 us at 600, 179 and 179 at 1,500, 303 against 289 at 3,000,
+// 736 against 674 at 8,192) where that many blocks still fill the SMs.
+AttnShape attn_shape(int64_t nq, int32_t segments, int32_t hq, int32_t hk, int32_t d)
 {
     AttnShape f;
     const int per = hq / hk;
@@ -275,9 +279,8 @@ AttnShape attn_shape(int64_t nq, int32_t segments, int32_t hq, int32_t hk)
     for (int g = 2; g <= std::min(per, 64); ++g)
         if (per % g == 0) f.heads = g;
     f.positions = 128 / f.heads;
-    const bool long_enough = nq / segments >= 2 * f.positions - f.positions / 2;
     const int64_t blocks = ceil_div(nq, 2 * f.positions) * (hq / f.heads);
-    f.tiles = long_enough && blocks >= sm_count() ? 2 : 1;
+    f.tiles = d > 64 && nq / segments >= 12 * f.positions && blocks >= sm_count() ? 2 : 1;
     return f;
 }
 

@@ -107,7 +107,7 @@ __device__ __forceinline__ void attn_share(int64_t lo, int64_t hi, int per, int 
 struct AttnShape {
     int heads, positions, tiles;
 };
-AttnShape attn_shape(int64_t nq, int32_t segments, int32_t hq, int32_t hk);
+AttnShape attn_shape(int64_t nq, int32_t segments, int32_t hq, int32_t hk, int32_t d);
 
 // Kernels for 16-bit heads of a multiple of 8 channels, up to 128, on 16-byte boundaries.
 bool attention_tc_supported(const AttnArgs& a, spc_dtype dt, bool backward);

@@ -5,12 +5,19 @@
 //   four warps for each tile take S, a thread to a row: running maximum, exponentials, P as 16 bits in the place of S;
 //   a warp loads the queries once and keys and values into a ring of stages (TMA);
 //   two warps for each tile issue S = Q K^T into tensor memory, and O += P V with P from tensor memory.  A warp's waits
-//     queue up behind its own products: one warp for all of them left the tensor cores idle half of the time
-//     (32,768 rows in 2 samples, 8 heads of 128: 2,005 us), a warp for each tile a third of it at d = 64.
-// S has two buffers a tile, so the next scores are there when a tile's exponentials are done, and with two tiles the
-// products of one run while the other's exponentials are taken.  O stays in tensor memory; it is
+//     queue up behind its own products: with one warp for all of them the tensor cores idled half of the time
+//     (32,768 rows in 2 samples, 8 heads of 128: 2,005 us against 1,371).
+// S has two buffers a tile, so the next scores are there when a tile's exponentials are done, and with two tiles (or two
+// blocks on an SM) the products of one run while the other's exponentials are taken.  O stays in tensor memory; it is
 // rescaled only when a row's maximum has grown by more than 2^8, so almost never after the first tiles
 // (sums and P carry the same factor, which the end divides out).
+//
+// Heads of 128: 1,620 to 1,660 TFLOP/s over 16,384 rows a sample, 85% of measured cuBLAS, bound by the tensor cores at the
+// pace of 64-column products (a product of 128 x 64 x 16 takes what its 6 KB take to leave shared memory, 48 cycles for 32
+// of arithmetic).  Heads of 64: 890 to 980, bound by the way from scores through exponentials and sums back to free scores, of which
+// two blocks an SM hide a part: exponentials fill 40% of their unit's time, instructions 53%, products 39%.  Tried and slower for heads
+// of 64: no running maximum but a check of each step's sum (613 us against 634, but 1,468 against 1,385 for heads
+// of 128), eight warps a tile (616 against 640), three score buffers (667), 128 keys a step (887).
 //
 // Every wait is bounded by the library's wait limit; one that runs out sets SPC_ERR_TIMEOUT, and each role then
 // waits (bounded) for what it has in flight itself before the block frees its tensor memory and returns.
@@ -29,7 +36,7 @@ struct Shape {
     static constexpr int kTile = 128 * 128 * kBoxes;          // bytes of a tile's queries
     static constexpr int kPart = kKeys * 128 * kBoxes;        // bytes of a step's keys, or values
     static constexpr int kStage = 2 * kPart;                  // the values of a step, the keys of the next but one
-    static constexpr int kStages = TILES == 1 && D == 128 ? 2 : 4;
+    static constexpr int kStages = TILES == 1 && D == 128 ? 2 : 4;  // what fits beside a second block
     static constexpr int kLoad = 4 * TILES;                   // the warp that loads; after it those that issue
     static constexpr int kThreads = 32 * (kLoad + 1 + 2 * TILES);
     static constexpr int kCols = TILES == 2 ? 512 : 256;      // tensor memory: 128 of scores and D of sums a tile
@@ -340,7 +347,7 @@ spc_status launch(const AttnArgs& a, const AttnShape& f, cudaStream_t st)
 template <typename T>
 spc_status typed(const AttnArgs& a, const AttnShape& f, cudaStream_t st)
 {
-    if (a.d <= 64) return f.tiles == 2 ? launch<T, 64, 2>(a, f, st) : launch<T, 64, 1>(a, f, st);
+    if (a.d <= 64) return launch<T, 64, 1>(a, f, st);
     return f.tiles == 2 ? launch<T, 128, 2>(a, f, st) : launch<T, 128, 1>(a, f, st);
 }
 
@@ -348,7 +355,7 @@ spc_status typed(const AttnArgs& a, const AttnShape& f, cudaStream_t st)
 
 spc_status attention_fwd_tc(const AttnArgs& a, spc_dtype dt, cudaStream_t st)
 {
-    const AttnShape f = attn_shape(a.nq, a.segments, a.hq, a.hk);
+    const AttnShape f = attn_shape(a.nq, a.segments, a.hq, a.hk, a.d);
     return dt == SPC_F16 ? typed<__half>(a, f, st) : typed<__nv_bfloat16>(a, f, st);
 }
 
