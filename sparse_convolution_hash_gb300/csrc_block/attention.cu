@@ -35,7 +35,7 @@ Layout layout(int64_t nq, int64_t nk, int32_t segments, int32_t hq, int32_t hk, 
         const AttnShape f = attn_shape(nq, segments, hq, hk, d);
         l.splits = splits_for(nq, segments, hq / f.heads, nk, f.positions * f.tiles, kLeastShare, f.tiles == 2 ? 1 : 2);
     } else {
-        l.splits = splits_for(nq, segments, hq, nk, kSimtRows, kLeastShare, 2);
+        l.splits = splits_for(nq, segments, hq, nk, kSimtRows, kLeastShare, tc ? 2 : 4);
     }
     l.splits_kv = backward ? splits_for(nk, segments, hk, nq * (hq / hk), kSimtRows, kLeastShare, 2) : 1;
     size_t at = 0;
@@ -59,26 +59,27 @@ Layout layout(int64_t nq, int64_t nk, int32_t segments, int32_t hq, int32_t hk, 
     return l;
 }
 
-// o and lse from the splits': weights exp(lse_z - lse).  A block to a row and head; its warps take the splits in turn, each
-// with a maximum and sum of its own, and join in order (a warp alone waits for memory once for every split: 24 us for
-// the 38 splits of 4 queries, 8 heads).
-constexpr int kJoinWarps = 8;
-template <typename T>
+// o and lse from the splits': weights exp(lse_z - lse).  WARPS warps to a row and head; they take the splits in turn, each
+// with a maximum and sum of its own, and join in order.  One where there are few splits, as there are many rows then;
+// eight beyond (one alone waits for memory once for every split: 24 us for the 38 splits of 4 queries, 8 heads).
+constexpr int kJoinWarps = 8, kFewSplits = 8;
+template <typename T, int WARPS>
 __global__ void __launch_bounds__(32 * kJoinWarps)
 k_attn_join(AttnArgs a)
 {
     __shared__ float box[kJoinWarps][4 * 32], tops[kJoinWarps], totals[kJoinWarps];
     wait_for_kernel_before();
-    const int64_t i = blockIdx.x, rows = a.nq * a.hq;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, mine = threadIdx.x >> 5, warp = mine % WARPS, first = mine - warp;
+    const int64_t i = (int64_t)blockIdx.x * (kJoinWarps / WARPS) + mine / WARPS, rows = a.nq * a.hq;
+    if (WARPS == 1 && i >= rows) return;
     float most = -INFINITY;
-    for (int z = warp + kJoinWarps * lane; z < a.splits; z += 32 * kJoinWarps) most = fmaxf(most, fetch(a.part_lse + z * rows + i));
+    for (int z = warp + WARPS * lane; z < a.splits; z += 32 * WARPS) most = fmaxf(most, fetch(a.part_lse + z * rows + i));
 #pragma unroll
     for (int o = 16; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(FULL_MASK, most, o));
     float total = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
     // an infinite or NaN sum is one split's: its weight is 1, so that it reaches the result
 #pragma unroll 4
-    for (int z = warp; z < a.splits; z += kJoinWarps) {
+    for (int z = warp; z < a.splits; z += WARPS) {
         const float l = fetch(a.part_lse + z * rows + i);
         const float* from = a.part + (z * rows + i) * a.d;
         float x[4];
@@ -90,31 +91,36 @@ k_attn_join(AttnArgs a)
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] = there ? fmaf(w, x[j], v[j]) : v[j];
     }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) box[warp][32 * j + lane] = v[j];
-    if (lane == 0) {
-        tops[warp] = most;
-        totals[warp] = total;
-    }
-    __syncthreads();
-    const int c = threadIdx.x;
-    if (c >= 128) return;
-    most = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) most = fmaxf(most, tops[w]);
-    total = 0.f;
-    float sum = 0.f;
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) {
-        if (totals[w] == 0.f) continue;
-        const float f = tops[w] == most ? 1.f : expf(tops[w] - most);
-        total = fmaf(f, totals[w], total);
-        sum = fmaf(f, box[w][c], sum);
-    }
     const int64_t row = i / a.hq, head = i - row * a.hq;
+    T* to = static_cast<T*>(a.o) + row * a.ldo + head * a.d;
+    if constexpr (WARPS > 1) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) box[mine][32 * j + lane] = v[j];
+        if (lane == 0) {
+            tops[mine] = most;
+            totals[mine] = total;
+        }
+        __syncthreads();
+        if (warp > 0) return;
+        most = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) most = fmaxf(most, tops[first + w]);
+        total = v[0] = v[1] = v[2] = v[3] = 0.f;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) {
+            if (totals[first + w] == 0.f) continue;
+            const float f = tops[first + w] == most ? 1.f : expf(tops[first + w] - most);
+            total = fmaf(f, totals[first + w], total);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = fmaf(f, box[first + w][32 * j + lane], v[j]);
+        }
+    }
     const bool any = total > 0.f || total != total;
-    if (c < a.d) static_cast<T*>(a.o)[row * a.ldo + head * a.d + c] = elem<T>::from_f32(any ? sum / total : 0.f);
-    if (c == 0) a.lse[i] = any ? most + logf(total) : -INFINITY;
+    const float inv = any ? 1.f / total : 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (lane + 32 * j < a.d) to[lane + 32 * j] = elem<T>::from_f32(v[j] * inv);
+    if (lane == 0) a.lse[i] = any ? most + logf(total) : -INFINITY;
 }
 
 // Sums of the splits' gradients in order; rows of `width` values, at `ld` in the result.
@@ -190,7 +196,7 @@ k_attn_delta(AttnArgs a)
         const int64_t row = i / a.hq, head = i - row * a.hq;
         const float lse = fetch(a.lse + i);
         a.delta[head * a.nq + row] = -s;
-        a.lse2[head * a.nq + row] = lse == -INFINITY ? -INFINITY : -lse * 1.44269504088896340736f;
+        a.lse2[head * a.nq + row] = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
     }
     if (MOST) block_most(most, a.most);
 }
@@ -220,8 +226,10 @@ k_attn_most_v(AttnArgs a)
 template <typename T>
 spc_status join_fwd(const AttnArgs& a, cudaStream_t st)
 {
-    if (a.nq * a.hq > INT32_MAX) return SPC_ERR_UNSUPPORTED;
-    return attn_start_kernel<k_attn_join<T>>(dim3((unsigned)(a.nq * a.hq)), 32 * kJoinWarps, 0, st, a);
+    const int64_t rows = a.nq * a.hq;
+    if (rows > INT32_MAX) return SPC_ERR_UNSUPPORTED;
+    if (a.splits > kFewSplits) return attn_start_kernel<k_attn_join<T, kJoinWarps>>(dim3((unsigned)rows), 32 * kJoinWarps, 0, st, a);
+    return attn_start_kernel<k_attn_join<T, 1>>(dim3((unsigned)ceil_div(rows, kJoinWarps)), 32 * kJoinWarps, 0, st, a);
 }
 
 template <typename T>

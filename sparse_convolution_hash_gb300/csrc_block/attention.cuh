@@ -12,6 +12,20 @@
 
 namespace spc {
 
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+
+namespace ptx {
+
+// 2^x, to about 2^-22 of itself; results below 2^-126 are 0.
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+}  // namespace ptx
+
 struct AttnArgs {
     const void* q;
     const void* k;

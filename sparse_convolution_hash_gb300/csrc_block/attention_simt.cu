@@ -14,7 +14,6 @@ namespace spc {
 namespace {
 
 constexpr int kThreads = 256, kTile = 64, kPad = 4;
-constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
 template <int DP> struct Mat { float v[kTile][DP + kPad]; };
 struct Probs { float v[kTile][kTile + kPad]; };
@@ -182,17 +181,15 @@ k_attn_simt(AttnArgs a)
             }
 #pragma unroll
             for (int x = 8; x; x >>= 1) most = fmaxf(most, __shfl_xor_sync(FULL_MASK, most, x));
-            const float base = most == -INFINITY ? 0.f : most, shrink = exp2f(m[i] - base);
+            const float base = most == -INFINITY ? 0.f : most, shrink = ptx::ex2(m[i] - base);
             float sum = 0.f;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float e = exp2f(s[i][j] - base);
+                const float e = ptx::ex2(s[i][j] - base);
                 sum += e;
                 p.v[4 * ty + i][tx + 16 * j] = e;
             }
-#pragma unroll
-            for (int x = 8; x; x >>= 1) sum += __shfl_xor_sync(FULL_MASK, sum, x);
-            l[i] = l[i] * shrink + sum;
+            l[i] = l[i] * shrink + sum;  // of this thread's columns: they join at the end
             m[i] = most;
 #pragma unroll
             for (int c = 0; c < DP / 16; ++c) o[i][c] *= shrink;
@@ -203,6 +200,8 @@ k_attn_simt(AttnArgs a)
     float mul[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int x = 8; x; x >>= 1) l[i] += __shfl_xor_sync(FULL_MASK, l[i], x);
         mul[i] = l[i] == 0.f ? 0.f : 1.f / l[i];
         if (l[i] == 0.f) {  // no keys: a zero, whatever stands in the sums
 #pragma unroll
@@ -239,7 +238,7 @@ __device__ __forceinline__ void tile_grad(const AttnArgs& a, const Mat<DP>& q, c
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const bool in = there && key + tx + 16 * j < key_end && lse != -INFINITY;
-            const float e = in ? exp2f(s[i][j] * to_log2 + lse) : 0.f;
+            const float e = in ? ptx::ex2(s[i][j] * to_log2 + lse) : 0.f;
             if (!BY_Q) p->v[4 * ty + i][tx + 16 * j] = e;
             ds.v[4 * ty + i][tx + 16 * j] = in ? e * (dp[i][j] + delta) : 0.f;
         }

@@ -17,7 +17,6 @@
 namespace spc {
 
 constexpr uint64_t kAttnDrainNs = 200000000ull;  // bound of the waits for a block's own copies and products
-constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
 template <typename T> struct AttnFmt;
 template <> struct AttnFmt<__half> { static constexpr uint32_t v = 0; static constexpr CUtensorMapDataType t = CU_TENSOR_MAP_DATA_TYPE_FLOAT16; };
@@ -82,14 +81,6 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
-}
-
-// 2^x, to about 2^-22 of itself; results below 2^-126 are 0.
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
 }
 
 }  // namespace ptx
