@@ -154,73 +154,64 @@ __device__ __forceinline__ void block_most(float v, uint32_t* word)
     }
 }
 
-// minus the sum of do o over a head's channels, and minus lse to base 2: eight lanes to a row and head.  fp16 also takes the
-// largest norm of a row of do (for the scale of ds, see the gradient kernels).
-template <typename T, bool MOST>
+// Rows of one head (blockIdx.y), LANES lanes to a row, four rows to a group of lanes so that their loads overlap.
+// DELTA: minus the sum of do o over the head's channels, and minus lse to base 2.  MOST (fp16): the largest squared norm of
+// a row of do, or (no DELTA) of v.
+constexpr int kRowsEach = 4;
+template <typename T, int LANES, bool DELTA, bool MOST>
 __global__ void __launch_bounds__(kBlock)
-k_attn_delta(AttnArgs a)
+k_attn_rows(AttnArgs a, bool whole)
 {
     wait_for_kernel_before();
-    const int64_t i = ((int64_t)blockIdx.x * kBlock + threadIdx.x) / 8, rows = a.nq * a.hq;
-    const int lane = threadIdx.x & 7;
-    float s = 0.f, most = 0.f;
-    if (i < rows) {
-        const int64_t row = i / a.hq, head = i - row * a.hq;
-        const T* o = static_cast<const T*>(a.o) + row * a.ldo + head * a.d;
-        const T* g = static_cast<const T*>(a.dout) + row * a.lddo + head * a.d;
-        constexpr int V = 16 / sizeof(T);
-        if (a.d % V == 0 && a.ldo % V == 0 && a.lddo % V == 0 && ((uintptr_t)a.o | (uintptr_t)a.dout) % 16 == 0) {
-            for (int c = lane * V; c < a.d; c += 8 * V) {
-                const Vec<T, V> x = *reinterpret_cast<const Vec<T, V>*>(o + c), y = *reinterpret_cast<const Vec<T, V>*>(g + c);
+    constexpr int V = 16 / sizeof(T), kGroups = kBlock / LANES;
+    const int lane = threadIdx.x % LANES, head = blockIdx.y;
+    const int64_t n = DELTA ? a.nq : a.nk, ld = DELTA ? a.lddo : a.ldv, row0 = (int64_t)blockIdx.x * (kGroups * kRowsEach) + threadIdx.x / LANES;
+    const T* g = static_cast<const T*>(DELTA ? a.dout : a.v) + (int64_t)head * a.d;
+    const T* o = static_cast<const T*>(a.o) + (int64_t)head * a.d;
+    float sum[kRowsEach], most[kRowsEach];
+#pragma unroll
+    for (int k = 0; k < kRowsEach; ++k) {
+        const int64_t row = row0 + k * kGroups;
+        sum[k] = most[k] = 0.f;
+        if (row >= n) continue;
+        if (whole) {
+            for (int c = lane * V; c < a.d; c += LANES * V) {
+                const Vec<T, V> x = *reinterpret_cast<const Vec<T, V>*>(g + row * ld + c);
+                Vec<T, V> y;
+                if (DELTA) y = *reinterpret_cast<const Vec<T, V>*>(o + row * a.ldo + c);
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
-                    const float u = elem<T>::to_f32(y.e[j]);
-                    s = fmaf(elem<T>::to_f32(x.e[j]), u, s);
-                    if (MOST) most = fmaf(u, u, most);
+                    const float u = elem<T>::to_f32(x.e[j]);
+                    if (DELTA) sum[k] = fmaf(elem<T>::to_f32(y.e[j]), u, sum[k]);
+                    if (MOST) most[k] = fmaf(u, u, most[k]);
                 }
             }
         } else {
-            for (int c = lane; c < a.d; c += 8) {
-                const float u = elem<T>::to_f32(g[c]);
-                s = fmaf(elem<T>::to_f32(o[c]), u, s);
-                if (MOST) most = fmaf(u, u, most);
+            for (int c = lane; c < a.d; c += LANES) {
+                const float u = elem<T>::to_f32(g[row * ld + c]);
+                if (DELTA) sum[k] = fmaf(elem<T>::to_f32(o[row * a.ldo + c]), u, sum[k]);
+                if (MOST) most[k] = fmaf(u, u, most[k]);
             }
         }
     }
+    float largest = 0.f;
 #pragma unroll
-    for (int o = 4; o; o >>= 1) {
-        s += __shfl_xor_sync(FULL_MASK, s, o);
-        if (MOST) most += __shfl_xor_sync(FULL_MASK, most, o);
-    }
-    if (i < rows && lane == 0) {
-        const int64_t row = i / a.hq, head = i - row * a.hq;
-        const float lse = fetch(a.lse + i);
-        a.delta[head * a.nq + row] = -s;
-        a.lse2[head * a.nq + row] = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
-    }
-    if (MOST) block_most(most, a.most);
-}
-
-// fp16: the largest norm of a row of v.
-__global__ void __launch_bounds__(kBlock)
-k_attn_most_v(AttnArgs a)
-{
-    wait_for_kernel_before();
-    const int64_t i = ((int64_t)blockIdx.x * kBlock + threadIdx.x) / 8, rows = a.nk * a.hk;
-    const int lane = threadIdx.x & 7;
-    float most = 0.f;
-    if (i < rows) {
-        const int64_t row = i / a.hk, head = i - row * a.hk;
-        const __half* v = static_cast<const __half*>(a.v) + row * a.ldv + head * a.d;
-        for (int c = lane * 8; c < a.d; c += 64) {
-            const Vec<__half, 8> x = *reinterpret_cast<const Vec<__half, 8>*>(v + c);
+    for (int k = 0; k < kRowsEach; ++k) {
+        const int64_t row = row0 + k * kGroups;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) most = fmaf(__half2float(x.e[j]), __half2float(x.e[j]), most);
+        for (int x = LANES / 2; x; x >>= 1) {
+            if (DELTA) sum[k] += __shfl_xor_sync(FULL_MASK, sum[k], x);
+            if (MOST) most[k] += __shfl_xor_sync(FULL_MASK, most[k], x);
+        }
+        // NaN and infinities have no say
+        if (MOST) largest = fmaxf(largest, most[k] < INFINITY ? most[k] : 0.f);
+        if (DELTA && row < n && lane == 0) {
+            const float lse = fetch(a.lse + row * a.hq + head);
+            a.delta[head * a.nq + row] = -sum[k];
+            a.lse2[head * a.nq + row] = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
         }
     }
-#pragma unroll
-    for (int o = 4; o; o >>= 1) most += __shfl_xor_sync(FULL_MASK, most, o);
-    block_most(most, a.most + 1);
+    if (MOST) block_most(largest, DELTA ? a.most : a.most + 1);
 }
 
 template <typename T>
@@ -253,22 +244,37 @@ spc_status join_bwd(const AttnArgs& a, cudaStream_t st)
     return s;
 }
 
+template <typename T, bool DELTA, bool MOST>
+spc_status rows_of(const AttnArgs& a, cudaStream_t st)
+{
+    constexpr int V = 16 / (int)sizeof(T);
+    const int64_t n = DELTA ? a.nq : a.nk;
+    if (n == 0) return SPC_OK;
+    const bool whole = a.d % V == 0 && (DELTA ? a.lddo : a.ldv) % V == 0 && aligned16(DELTA ? a.dout : a.v) &&
+                       (!DELTA || (a.ldo % V == 0 && aligned16(a.o)));
+    const int64_t vectors = ceil_div(a.d, V);
+    const int lanes = vectors <= 4 ? 4 : vectors <= 8 ? 8 : 16;
+    const int64_t blocks = ceil_div(n, (int64_t)(kBlock / lanes) * kRowsEach);
+    if (blocks > INT32_MAX) return SPC_ERR_UNSUPPORTED;
+    const dim3 grid((unsigned)blocks, (unsigned)(DELTA ? a.hq : a.hk));
+    switch (lanes) {
+    case 4: return attn_start_kernel<k_attn_rows<T, 4, DELTA, MOST>>(grid, kBlock, 0, st, a, whole);
+    case 8: return attn_start_kernel<k_attn_rows<T, 8, DELTA, MOST>>(grid, kBlock, 0, st, a, whole);
+    default: return attn_start_kernel<k_attn_rows<T, 16, DELTA, MOST>>(grid, kBlock, 0, st, a, whole);
+    }
+}
+
 template <typename T>
 spc_status row_sums(const AttnArgs& a, bool most, cudaStream_t st)
 {
-    const int64_t blocks = ceil_div(a.nq * a.hq * 8, kBlock);
-    if (blocks == 0) return SPC_OK;
-    if (blocks > INT32_MAX) return SPC_ERR_UNSUPPORTED;
     if constexpr (std::is_same<T, __half>::value) {
         if (most) {
             SPC_CUDA_TRY(cudaMemsetAsync(a.most, 0, 8, st));
-            const int64_t kv = ceil_div(a.nk * a.hk * 8, kBlock);
-            if (kv > INT32_MAX) return SPC_ERR_UNSUPPORTED;
-            spc_status s = attn_start_kernel<k_attn_most_v>(dim3((unsigned)kv), kBlock, 0, st, a);
-            return s != SPC_OK ? s : attn_start_kernel<k_attn_delta<T, true>>(dim3((unsigned)blocks), kBlock, 0, st, a);
+            const spc_status s = rows_of<T, false, true>(a, st);
+            return s != SPC_OK ? s : rows_of<T, true, true>(a, st);
         }
     }
-    return attn_start_kernel<k_attn_delta<T, false>>(dim3((unsigned)blocks), kBlock, 0, st, a);
+    return rows_of<T, true, false>(a, st);
 }
 
 }  // namespace
