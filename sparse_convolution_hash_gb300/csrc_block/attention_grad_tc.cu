@@ -5,10 +5,15 @@
 // with P = exp(S - lse) and dS = P (dP - delta), written as 16 bits in the place of S and dP, a thread to a lane.
 // Seven products where five would do, were dq summed across blocks; but then its bits would hang on their order.
 //
-// BUFS steps are in work at any time, each with four warps and 128 columns of tensor memory: while one's
-// probabilities are taken, the others' products run.  Three where heads of up to 64 channels leave the columns, two beyond;
-// one where the walk is a few steps long, so that two blocks share an SM and one's first loads and last
-// stores run beside the other's steps.
+// BUFS steps are in work at any time, each with 128 columns of tensor memory and four warps (eight for heads of more than
+// 64, where a block has the SM to itself): while one's probabilities are taken, the others' products run.  Three where heads of up to 64
+// channels leave the columns, two beyond; one where the walk is short, so that two blocks share an SM and one's first
+// loads and last stores run beside the other's steps.  S and dP are issued by one warp and the sums by another, as a warp's waits
+// queue up behind its own products (8,148 us with one of one lane, 6,731 with one, 5,984 with two; four gave 6,227).
+//
+// 32,768 rows in 2 samples, 8 heads of 128 bf16: 6.04 ms, 940 TFLOP/s of the five products that the formula needs and
+// 1,316 of the seven that run, 67% of measured cuBLAS.  The products' operands leave shared memory for 58% of the time (a
+// product of 128 x 64 x 16 reads 6 KB, 48 cycles for 32 of arithmetic), and each step still waits for its own chain of S, P and sums.
 //
 // fp16: P is kept times 2^14 and dS times a power of two for which the largest possible value, |P| <= 1 times
 // 2 max|do| max|v|, stays below 2^14, so small probabilities and gradients keep their digits.
@@ -32,10 +37,13 @@ struct Shape {
     static constexpr int kHalf = kStep * 128 * kBoxes;    // bytes of a step's rows of one operand
     static constexpr int kStage = 2 * kHalf;
     static constexpr int kStages = BUFS == 3 ? 6 : 4;
-    static constexpr int kThreads = 128 + 128 * BUFS;
+    static constexpr int kHalves = BUFS == 2 ? 2 : 1;     // four warps for each 64 / kHalves columns of a buffer
+    static constexpr int kThreads = 128 + 128 * BUFS * kHalves;
     static constexpr int kCols = BUFS == 1 ? 256 : 512;   // tensor memory
     static constexpr int kBars = 3 * kStages + 4 + 3 * BUFS;
     static_assert(BUFS * 128 + 2 * D <= kCols, "");
+    // where the 16 rows q of P (and dS) lie: each half's in the place of its own scores, which the other half's warps do not wait for
+    static __device__ constexpr int column(int q) { return kHalves == 2 ? (q >> 1) * 32 + (q & 1) * 8 : q * 8; }
     static constexpr size_t kSmem = 1024 + 2 * (size_t)kKept + (size_t)kStages * (kStage + 2 * kStep * 4) + 8 * kBars + 16;
 };
 
@@ -178,7 +186,7 @@ k_attn_grad_tc(AttnArgs a, uint64_t wait_ns, const __grid_constant__ CUtensorMap
         for (int i = 0; i < BUFS; ++i) {
             ptx::mbar_init(&sum_full[i], 1);
             ptx::mbar_init(&s_full[i], 1);
-            ptx::mbar_init(&p_full[i], 4);
+            ptx::mbar_init(&p_full[i], 4 * S::kHalves);
         }
         ptx::mbar_init(o_full, 1);
         ptx::mbar_init_fence();
@@ -274,11 +282,11 @@ k_attn_grad_tc(AttnArgs a, uint64_t wait_ns, const __grid_constant__ CUtensorMap
                         const uint64_t d1 = mn_desc + s * (S::kStage >> 4), d2 = d1 + (S::kHalf >> 4);
                         if (KEYS) {
 #pragma unroll
-                            for (int q = 0; q < kStep / 16; ++q) ptx::mma_f16_ts(sum1, p + q * 8, d2 + q * 128, idesc, q > 0 || j > 0);  // dV += P^T dO
+                            for (int q = 0; q < kStep / 16; ++q) ptx::mma_f16_ts(sum1, p + S::column(q), d2 + q * 128, idesc, q > 0 || j > 0);  // dV += P^T dO
                         }
 #pragma unroll
                         for (int q = 0; q < kStep / 16; ++q)  // dK += dS^T Q, dQ += dS K
-                            ptx::mma_f16_ts(KEYS ? sum2 : sum1, p + 64 + q * 8, d1 + q * 128, idesc, q > 0 || j > 0);
+                            ptx::mma_f16_ts(KEYS ? sum2 : sum1, p + 64 + S::column(q), d1 + q * 128, idesc, q > 0 || j > 0);
                         ptx::mma_commit(&sum_full[b]);
                         ptx::mma_commit(&empty[s]);
                         if (j + 1 == n) ptx::mma_commit(o_full);
@@ -338,7 +346,7 @@ k_attn_grad_tc(AttnArgs a, uint64_t wait_ns, const __grid_constant__ CUtensorMap
         }
     } else if (warp >= 4) {
         // ------------------------------------------- probabilities, their gradients, results
-        const int b = (warp - 4) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+        const int b = (warp - 4) / (4 * S::kHalves), half = ((warp - 4) >> 2) % S::kHalves, quarter = warp & 3, r = quarter * 32 + lane;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         const uint32_t s_at = tmem + lanes + b * 128;
         const Scales sc = scales<T>(a);
@@ -388,46 +396,32 @@ k_attn_grad_tc(AttnArgs a, uint64_t wait_ns, const __grid_constant__ CUtensorMap
                 }
             };
             // P and dS go in the place of columns that have been read, half as many
-            if constexpr (BUFS == 2) {  // the registers of fewer warps hold 32 columns at a time (5,984 us against 6,158 for 8 heads of 128)
+            constexpr int kColumns = kStep / S::kHalves;
+            const int x0 = half * kColumns;
+            uint32_t sv[2][16], dp[2][16];
+            ptx::tmem_ld16(s_at + x0, sv[0]);
+            ptx::tmem_ld16(s_at + 64 + x0, dp[0]);
 #pragma unroll
-                for (int x = 0; x < kStep; x += 32) {
-                    uint32_t sv[32], dp[32], p[16], ds[16];
-                    ptx::tmem_ld32(s_at + x, sv);
-                    ptx::tmem_ld32(s_at + 64 + x, dp);
-                    F2 ml[16], md[16];
-                    column_stats(ml, md, x);
-                    ptx::tmem_ld_wait();
-                    grad_of<T, 32>(sv, dp, both(c), ml, md, both(sc.ds), p, ds);
-                    cut(ds, x);
-                    if (KEYS) ptx::tmem_st16(s_at + x / 2, p);
-                    ptx::tmem_st16(s_at + 64 + x / 2, ds);
+            for (int x = 0; x < kColumns; x += 16) {
+                const int now = x >> 4 & 1;
+                uint32_t p[8], ds[8];
+                F2 ml[8], md[8];
+                column_stats(ml, md, x0 + x);
+                ptx::tmem_ld_wait();
+                if (x + 16 < kColumns) {  // the next columns while these are worked on
+                    ptx::tmem_ld16(s_at + x0 + x + 16, sv[now ^ 1]);
+                    ptx::tmem_ld16(s_at + 64 + x0 + x + 16, dp[now ^ 1]);
                 }
-            } else {
-                uint32_t sv[2][16], dp[2][16];
-                ptx::tmem_ld16(s_at, sv[0]);
-                ptx::tmem_ld16(s_at + 64, dp[0]);
-#pragma unroll
-                for (int x = 0; x < kStep; x += 16) {
-                    const int now = x >> 4 & 1;
-                    uint32_t p[8], ds[8];
-                    F2 ml[8], md[8];
-                    column_stats(ml, md, x);
-                    ptx::tmem_ld_wait();
-                    if (x + 16 < kStep) {  // the next columns while these are worked on
-                        ptx::tmem_ld16(s_at + x + 16, sv[now ^ 1]);
-                        ptx::tmem_ld16(s_at + 64 + x + 16, dp[now ^ 1]);
-                    }
-                    grad_of<T, 16>(sv[now], dp[now], both(c), ml, md, both(sc.ds), p, ds);
-                    cut(ds, x);
-                    if (KEYS) ptx::tmem_st8(s_at + x / 2, p);
-                    ptx::tmem_st8(s_at + 64 + x / 2, ds);
-                }
+                grad_of<T, 16>(sv[now], dp[now], both(c), ml, md, both(sc.ds), p, ds);
+                cut(ds, x0 + x);
+                if (KEYS) ptx::tmem_st8(s_at + x0 + x / 2, p);
+                ptx::tmem_st8(s_at + 64 + x0 + x / 2, ds);
             }
             ptx::tmem_st_wait();
             if (!KEYS && left < kStep) {
                 ok = attn_wait(&full[s], (j / S::kStages) & 1, wait_ns);
                 if (!ok) break;
-                attn_clear_rows<S::kBoxes>(ring_base + (uint32_t)s * S::kStage, kStep, (int)left, r, 128);
+                attn_clear_rows<S::kBoxes>(ring_base + (uint32_t)s * S::kStage, kStep, (int)left, half * 128 + r, 128 * S::kHalves);
             }
             ptx::tc_fence_before();
             __syncwarp();
@@ -444,15 +438,17 @@ k_attn_grad_tc(AttnArgs a, uint64_t wait_ns, const __grid_constant__ CUtensorMap
                     T* out = which == 0 ? static_cast<T*>(a.dv) + row * a.lddv + (int64_t)kept_head * a.d
                                         : static_cast<T*>(a.dk) + row * a.lddk + (int64_t)kept_head * a.d;
                     float* part = splits > 1 ? a.part_kv + ((which == 0 ? splits : 0) + blockIdx.z) * one + off : nullptr;
-                    if (n > 0) store_row<T>((which == 0 ? sum1 : sum2) + lanes, 0, 32, a.d, which == 0 ? sc.back_p : sc.back_ds * a.scale, there, out, part);
-                    else store_zeros<T>(0, 32, a.d, there, out, part);
+                    const int x0 = 32 * half, stride = 32 * S::kHalves;
+                    if (n > 0) store_row<T>((which == 0 ? sum1 : sum2) + lanes, x0, stride, a.d, which == 0 ? sc.back_p : sc.back_ds * a.scale, there, out, part);
+                    else store_zeros<T>(x0, stride, a.d, there, out, part);
                 }
             } else if (b < 2) {
                 T* out = static_cast<T*>(a.dq) + row * a.lddq + (int64_t)kept_head * a.d;
                 float* part = splits > 1 ? a.part + ((blockIdx.z * a.nq + row) * a.hq + kept_head) * a.d : nullptr;
-                constexpr int kStride = BUFS == 1 ? 32 : 64;
-                if (n > 0) store_row<T>(sum1 + lanes, 32 * b, kStride, a.d, sc.back_ds * a.scale, there, out, part);
-                else store_zeros<T>(32 * b, kStride, a.d, there, out, part);
+                const int x0 = 32 * (b * S::kHalves + half);
+                constexpr int kStride = 32 * (BUFS == 1 ? 1 : 2) * S::kHalves;
+                if (n > 0) store_row<T>(sum1 + lanes, x0, kStride, a.d, sc.back_ds * a.scale, there, out, part);
+                else store_zeros<T>(x0, kStride, a.d, there, out, part);
             }
         }
     }
