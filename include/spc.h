@@ -117,7 +117,7 @@ SPC_API const char* spc_status_string(spc_status s);
 SPC_API int32_t spc_version(void);
 
 /* Bound on the waits inside the pipelined tensor-core kernels (conv forward,
- * dinput, inverse, dfilter) of one warp role on another: a gather warp waiting
+ * dinput, inverse, dfilter, grouped products, attention) of one warp role on another: a gather warp waiting
  * for a free stage, the MMA thread waiting for a full one.  Such a wait never
  * lasts long in a healthy run; one that runs out makes the kernel set
  * SPC_ERR_TIMEOUT in the call's status word, wait for the copies and MMAs it
@@ -648,9 +648,9 @@ SPC_API spc_status spc_grouped_wgrad(const void* x, const void* dy, const int32_
  *  x      [n, c] of dtype dt.      y [n, c] of dtype dt out (may be x itself).
  *  gamma, beta  [c] fp32, or NULL (1 and 0).      eps > 0.
  *  mean, rstd   [n] fp32 out (what the backward pass reads).
- *  Rows of any length; they are held in registers up to 16,384 (16-bit) or 8,192 channels, and
- *  read in 16-byte words when x and y are 16-byte aligned and c is a multiple of 16 bytes,
- *  else element by element.
+ *  Rows of any length; they are held in registers up to 16,384 (16-bit) or 8,192 channels (8,192 in the
+ *  backward pass), and read in 16-byte words when x, y, gamma and beta are 16-byte aligned and c is a
+ *  multiple of 16 bytes, else element by element.
  */
 SPC_API spc_status spc_layer_norm_fwd(const void* x, const float* gamma, const float* beta, int64_t n,
                                       int32_t c, float eps, spc_dtype dt, void* y, float* mean,

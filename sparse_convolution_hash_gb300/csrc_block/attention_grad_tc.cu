@@ -12,8 +12,9 @@
 // queue up behind its own products (8,148 us with one of one lane, 6,731 with one, 5,984 with two; four gave 6,227).
 //
 // 32,768 rows in 2 samples, 8 heads of 128 bf16: 6.04 ms, 940 TFLOP/s of the five products that the formula needs and
-// 1,316 of the seven that run, 67% of measured cuBLAS.  The products' operands leave shared memory for 58% of the time (a
-// product of 128 x 64 x 16 reads 6 KB, 48 cycles for 32 of arithmetic), and each step still waits for its own chain of S, P and sums.
+// 1,316 of the seven that run, 67% of measured cuBLAS.  The kernel of dk and dv has shared memory at work 93% of the time: 59 for the
+// products' operands (a product of 128 x 64 x 16 reads 6 KB, 48 cycles for 32 of arithmetic), 34 for the columns' lse and
+// delta, which every thread reads.  That of dq waits for its own chain of S, dS and sums (operands 57%, tensor cores 51%).
 //
 // fp16: P is kept times 2^14 and dS times a power of two for which the largest possible value, |P| <= 1 times
 // 2 max|do| max|v|, stays below 2^14, so small probabilities and gradients keep their digits.

@@ -1,6 +1,6 @@
 // route.cu -- the experts of each token and their weights, and the gradient by the logits.
 //
-// A row of logits lies in the registers of L lanes (4 to 32), eight neighbouring experts to a lane (beyond 256
+// A row of logits lies in the registers of L lanes (1 to 32), eight neighbouring experts to a lane (beyond 256
 // experts four such chunks).  Each lane sorts its eight once; then the best of the lanes' firsts is taken k times and
 // its lane moves up, so a round costs a reduction and a few moves whatever the number of experts.  Without a bias and groups
 // the logits themselves are compared, which is exact; 16-bit ones are sorted together with their expert in one word.
@@ -648,7 +648,12 @@ k_route_grad(RouteGradArgs a, bool whole)
 }
 
 // Lanes to a row: eight experts each, up to a warp; beyond 256 experts four chunks of eight.
-int lanes_for(int experts) { return experts <= 32 ? 4 : experts <= 64 ? 8 : experts <= 128 ? 16 : 32; }
+int lanes_for(int experts)
+{
+    int L = 1;
+    while (L < 32 && L * kPer < experts) L *= 2;
+    return L;
+}
 
 template <auto KERNEL, typename A>
 spc_status start(const A& a, int L, size_t smem, bool whole, cudaStream_t st)
@@ -679,6 +684,8 @@ spc_status fwd(const RouteArgs& a, cudaStream_t st)
     const size_t smem = (size_t)(kBlock / L) * ((a.groups > 1 ? 8 * (size_t)(a.experts + a.groups) : 0) + 8 * (size_t)a.top_k);
     if (a.experts > 256) return start<k_route<T, 4, 32>>(a, L, smem, whole, st);
     switch (L) {
+    case 1: return start<k_route<T, 1, 1>>(a, L, smem, whole, st);
+    case 2: return start<k_route<T, 1, 2>>(a, L, smem, whole, st);
     case 4: return start<k_route<T, 1, 4>>(a, L, smem, whole, st);
     case 8: return start<k_route<T, 1, 8>>(a, L, smem, whole, st);
     case 16: return start<k_route<T, 1, 16>>(a, L, smem, whole, st);
@@ -694,6 +701,8 @@ spc_status bwd(const RouteGradArgs& a, cudaStream_t st)
     const size_t smem = 8 * (size_t)(kBlock / L) * a.top_k;
     if (a.experts > 256) return start<k_route_grad<T, 4, 32>>(a, L, smem, whole, st);
     switch (L) {
+    case 1: return start<k_route_grad<T, 1, 1>>(a, L, smem, whole, st);
+    case 2: return start<k_route_grad<T, 1, 2>>(a, L, smem, whole, st);
     case 4: return start<k_route_grad<T, 1, 4>>(a, L, smem, whole, st);
     case 8: return start<k_route_grad<T, 1, 8>>(a, L, smem, whole, st);
     case 16: return start<k_route_grad<T, 1, 16>>(a, L, smem, whole, st);

@@ -129,7 +129,8 @@ def test_rope_far_and_negative_cells():
 
 # ----------------------------------------------------------- routing to experts
 ROUTE = [  # n, experts, top_k, score, bias, groups, kept, renorm
-    (1, 1, 1, "softmax", False, 1, 1, True), (5, 4, 4, "sigmoid", True, 1, 1, False), (70, 8, 2, "softmax", False, 1, 1, True),
+    (1, 1, 1, "softmax", False, 1, 1, True), (300, 4, 3, "softmax", True, 4, 3, True), (290, 16, 5, "sigmoid", True, 2, 1, True),
+    (150, 12, 2, "softmax", False, 3, 2, False), (77, 8, 8, "sigmoid", False, 1, 1, True), (5, 4, 4, "sigmoid", True, 1, 1, False), (70, 8, 2, "softmax", False, 1, 1, True),
     (65, 64, 6, "softmax", True, 1, 1, False), (33, 60, 4, "sigmoid", True, 4, 2, True), (129, 256, 8, "sigmoid", True, 8, 4, True),
     (40, 160, 3, "softmax", False, 4, 3, True), (17, 128, 8, "softmax", False, 1, 1, False), (9, 1000, 32, "sigmoid", False, 1, 1, True),
     (6, 1024, 5, "softmax", True, 512, 7, True), (31, 33, 3, "sigmoid", False, 11, 2, False), (21, 1024, 8, "sigmoid", True, 1024, 9, True)]
