@@ -746,7 +746,7 @@ SPC_API spc_status spc_route_bwd(const float* dgate, const void* logits, const i
  *
  *  q      nq rows of [hq, d]; k, v  nk rows of [hk, d], of dtype dt; rows ldq, ldk, ldv elements
  *         apart (slices of one projection are read in place).  hk divides hq: query head h
- *         reads key head h / (hq / hk).  d 1 .. 128.
+ *         reads key head h / (hq / hk).  d 1 .. 128; hq <= 65535; nq, nk < 2^31 - 128.
  *  scale  > 0, finite.
  *  o      nq rows of [hq, d] of dtype dt out, ldo apart; it overlaps no argument.     lse [nq, hq] fp32 out.
  *  status device int32 sticky error word, or NULL (SPC_ERR_ROW_INDEX, SPC_ERR_TIMEOUT).

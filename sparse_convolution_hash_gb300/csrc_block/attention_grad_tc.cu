@@ -93,6 +93,7 @@ __device__ __forceinline__ void store_row(uint32_t at, int x0, int stride, int d
 #pragma unroll 1
     for (int x = x0; x < d; x += stride) {
         uint32_t v[32];
+        __syncwarp();
         ptx::tmem_ld32(at + x, v);
         ptx::tmem_ld_wait();
         if (!there) continue;

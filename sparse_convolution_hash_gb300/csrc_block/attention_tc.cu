@@ -293,6 +293,7 @@ k_attn_tc(AttnArgs a, Packing pk, uint64_t wait_ns, const __grid_constant__ CUte
             for (int x = 0; x < D && ok; x += 32) {
                 if (x >= a.d || (n == 0 && a.splits > 1)) break;  // the join passes over a split without keys
                 uint32_t v[32];
+                __syncwarp();
                 if (n > 0) {
                     ptx::tmem_ld32(o_at + x, v);
                     ptx::tmem_ld_wait();

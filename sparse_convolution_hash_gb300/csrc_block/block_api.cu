@@ -42,7 +42,7 @@ spc_status check_rope(const RopeArgs& a, const int32_t* pairs, const uint64_t* s
         all += pairs[i];
     }
     if (2 * all > a.d || (all > 0 && !steps)) return SPC_ERR_INVALID_ARG;
-    if (all > 128) return SPC_ERR_UNSUPPORTED;
+    if (all > 128 || a.heads > INT32_MAX / 4 || a.d > INT32_MAX / 4) return SPC_ERR_UNSUPPORTED;
     const int64_t width = (int64_t)a.heads * a.d;
     if (!stride_ok(a.ldx, width, a.n) || !stride_ok(a.ldy, width, a.n)) return SPC_ERR_INVALID_ARG;
     if (!rows_ok(a.x, a.n, dt) || !rows_ok(a.y, a.n, dt) || !on(a.coords, 16) || (a.n > 0 && !a.coords)) return SPC_ERR_INVALID_ARG;
@@ -67,6 +67,12 @@ bool among(const void* result, const void* const (&others)[N])
     return false;
 }
 
+// Rows are 32-bit numbers, also those of a tile that begins before the last one.
+bool attention_sizes_ok(int64_t nq, int64_t nk, int32_t segments, int32_t hq, int32_t d)
+{
+    return d <= 128 && hq <= 65535 && nq <= INT32_MAX - 128 && nk <= INT32_MAX - 128 && segments <= INT32_MAX - 4;
+}
+
 spc_status check_attention(const AttnArgs& a, spc_dtype dt, bool backward)
 {
     if (!dtype_ok(dt) || a.nq < 0 || a.nk < 0 || a.segments < 1 || a.hq < 1 || a.hk < 1 || a.d < 1) return SPC_ERR_INVALID_ARG;
@@ -87,8 +93,7 @@ spc_status check_attention(const AttnArgs& a, spc_dtype dt, bool backward)
     if (backward && (among(a.dq, {a.q, a.k, a.v, a.o, a.dout, a.dk, a.dv}) || among(a.dk, {a.q, a.k, a.v, a.o, a.dout, a.dv}) ||
                      among(a.dv, {a.q, a.k, a.v, a.o, a.dout})))
         return SPC_ERR_INVALID_ARG;
-    if (a.d > 128 || a.hq > 65535 || a.nq > INT32_MAX - 1 || a.nk > INT32_MAX - 1 || a.segments > INT32_MAX - 4) return SPC_ERR_UNSUPPORTED;
-    return SPC_OK;
+    return attention_sizes_ok(a.nq, a.nk, a.segments, a.hq, a.d) ? SPC_OK : SPC_ERR_UNSUPPORTED;
 }
 
 }  // namespace
@@ -175,7 +180,8 @@ spc_status spc_route_bwd(const float* dgate, const void* logits, const int32_t* 
 size_t spc_attention_workspace_size(int64_t nq, int64_t nk, int32_t segments, int32_t hq, int32_t hk, int32_t d, spc_dtype dt,
                                     int32_t backward)
 {
-    if (nq < 0 || nk < 0 || segments < 1 || hq < 1 || hk < 1 || hq % hk != 0 || d < 1 || d > 128 || !dtype_ok(dt)) return 0;
+    if (nq < 0 || nk < 0 || segments < 1 || hq < 1 || hk < 1 || hq % hk != 0 || d < 1 || !dtype_ok(dt)) return 0;
+    if (!attention_sizes_ok(nq, nk, segments, hq, d)) return 0;
     return attention_ws_bytes(nq, nk, segments, hq, hk, d, dt, backward != 0);
 }
 

@@ -112,6 +112,8 @@ def test_rope_refusals(L):
                     dict(y=256, ldy=24), dict(ldx=BIG * BIG // 4)):
             assert call(f, **bad) == INVALID, bad
         assert call(f, d=400, ldx=400, ldy=400, pairs=(100, 50, 50)) == UNSUPPORTED
+        for big in (dict(heads=2 ** 31 - 1, d=1, pairs=(0, 0, 0)), dict(d=2 ** 31 - 1)):
+            assert call(f, n=1, ldx=2 ** 31, ldy=2 ** 31, **big) == UNSUPPORTED
         assert call(f, n=0, x=None, y=None, coords=None) == OK and call(f, heads=0, ldx=0, ldy=0) == OK
 
 
@@ -157,7 +159,8 @@ def test_attention_refusals(L):
         assert bwd(**bad) == INVALID, bad
     for f in (fwd, bwd):
         assert f(d=129, ldq=258, ldk=258, ldv=258, ldo=258, **({} if f is fwd else dict(lddo=258, lddq=258, lddk=258, lddv=258))) == UNSUPPORTED
-        assert f(nq=1 << 31) == UNSUPPORTED and f(nk=1 << 31) == UNSUPPORTED
+        for n in (1 << 31, (1 << 31) - 128):
+            assert f(nq=n) == UNSUPPORTED and f(nk=n) == UNSUPPORTED
     # few queries over many keys are split: a workspace
     few = dict(nq=2, nk=100000, S=1)
     need = L.spc_attention_workspace_size(2, 100000, 1, 2, 2, 32, BF16, 0)
@@ -169,6 +172,7 @@ def test_attention_refusals(L):
     size = L.spc_attention_workspace_size
     assert size(100000, 100000, 1, 8, 8, 64, BF16, 0) == 0  # many queries: none
     assert size(-1, 1, 1, 1, 1, 1, 0, 0) == 0 and size(1, 1, 1, 3, 2, 1, 0, 0) == 0 and size(1, 1, 1, 1, 1, 129, 0, 1) == 0
+    assert size(1 << 40, 1, 1, 1, 1, 8, 0, 1) == 0 and size(1, (1 << 31) - 128, 1, 1, 1, 8, 0, 1) == 0
 
 
 def test_tensors_on_the_host_are_refused(L):

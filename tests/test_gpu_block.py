@@ -193,6 +193,24 @@ def test_route_masked_and_extreme_logits(score, renorm, biased):
     close(spc.spc_route_bwd(to(dgate), to(logits), got, score=kind, renorm=renorm), want, bound + 1e-30)
 
 
+@pytest.mark.parametrize("size", [2, 3, 8])
+@pytest.mark.parametrize("best", [3e38, math.inf])
+def test_route_groups_of_biases_at_the_end_of_fp32(size, best):
+    """Sums of a group's two best that fp32 does not hold: groups are kept as their sums in 64 bits have it."""
+    g = gen(12)
+    logits = normal(g, 20, 5 * size)
+    bias = torch.zeros(5 * size)
+    for group, two in enumerate([(-3e38, -3e38), (-3e38, -2e38), (2.5e38, 3e38), (best, 3e38), (0.0, 0.0)]):
+        bias[group * size:(group + 1) * size] = min(two)
+        bias[(group + 1) * size - 1] = max(two)
+    for kept in (1, 2, 4):
+        k = min(2 * kept - 1, size * kept)
+        (expert, gate), bound = ref.route_fwd(logits, k, "sigmoid", bias, 5, kept, True, 1.0)
+        got, w = spc.spc_route_fwd(to(logits), k, score=spc.SPC_SCORE_SIGMOID, bias=to(bias), groups=5, top_groups=kept)
+        assert torch.equal(got.cpu(), expert)
+        close(w, gate, bound)
+
+
 def test_route_reports_experts_out_of_range_and_feeds_row_segments():
     g, logits, _ = route_case(50, 16, False, "f32")
     expert, gate = spc.spc_route_fwd(to(logits), 2)
