@@ -90,12 +90,11 @@ __device__ __forceinline__ float rough_score(float l, bool sigmoid, float most, 
 {
     return sigmoid ? __fdividef(1.f, 1.f + __expf(fminf(-l, 88.f))) : __fdividef(__expf(l - most), sum);
 }
-__device__ __forceinline__ double rough_score(float l, bool sigmoid, float most, double sum) { return score_of<double>(l, sigmoid, most, sum); }
 
 struct RouteShared {
-    int32_t* expert;   // [k] of this row
-    float* logit;      // [k]
-    void* c;           // [experts], then [groups], of the scores' type; groups only
+    int32_t* expert;   // [k] of this row, and one more for the choice in fp32
+    float* logit;      // the same
+    void* c;           // [experts], then [groups], of 64 bits; groups only
 };
 
 // Scores as words that are ordered as they are (the least word for -inf and NaN, which are never chosen).
@@ -133,21 +132,6 @@ __device__ __forceinline__ void best_of_lanes(float& top, int& e, float& l, int 
     l = __shfl_sync(FULL_MASK, l, from, L);
     top = value_of(most);
     if (winner < 0) e = kNone;
-}
-template <int C, int L>
-__device__ __forceinline__ void best_of_lanes(double& top, int& e, float& l, int)
-{
-#pragma unroll
-    for (int o = L >> 1; o; o >>= 1) {
-        const double v = __shfl_xor_sync(FULL_MASK, top, o);
-        const int other = __shfl_xor_sync(FULL_MASK, e, o);
-        const float z = __shfl_xor_sync(FULL_MASK, l, o);
-        if (v > top || (v == top && other < e)) {
-            top = v;
-            e = other;
-            l = z;
-        }
-    }
 }
 
 // ---- a lane's eight in falling order.  Words of 64 bits: order_of(value), then the larger for the lower expert; of 32
@@ -223,25 +207,46 @@ __device__ __forceinline__ uint32_t take_best(uint64_t (&v)[8], int lane, int& e
 
 // A group's score from its two best.  What fp32 does not hold becomes its lowest number or infinity, which lie near every
 // other such sum, so that 64 bits decide.
-template <typename S>
-__device__ __forceinline__ S group_score(S first, S second)
+__device__ __forceinline__ float group_score(float first, float second)
 {
-    const S least = sizeof(S) == 4 ? -3.402823466e38f : -INFINITY;
-    return second > -INFINITY ? max(first + second, least) : first;
+    return second > -INFINITY ? fmaxf(first + second, -3.402823466e38f) : first;
 }
 
-// The row's k best, written to sh.expert and sh.logit by its lane 0.  S: the type that scores are compared in
-// (BY_LOGIT: the logits, exactly).  Returns whether two neighbours, or the border of the kept groups, lie
-// within the error of S: scores are off by 2^-20, or 2^-16 of the largest one (softmax), at most.
-template <typename T, typename S, bool BY_LOGIT, int C, int L>
-__device__ __forceinline__ bool choose(const RouteArgs& a, const T* row, const float (&l)[C][kPer], int lane, const RouteShared& sh)
+// Scores in fp32 are compared without their last three bits, where the place among the lane's eight stands: sorting
+// is a third of what it is with words of 64 bits.
+__device__ __forceinline__ uint32_t rough_rank(float v, int j)
 {
-    const S kLow = -INFINITY;
+    const uint32_t w = order_of(v);
+    return w ? (w & ~7u) | (uint32_t)(7 - j) : 0u;
+}
+template <int L>
+__device__ __forceinline__ uint32_t take_rough_best(uint32_t (&v)[8], int lane, int& e)
+{
+    const uint32_t mine = v[0] & ~7u, most = lanes_most<L>(mine);
+    const uint32_t at = (threadIdx.x & 31) - lane, votes = __ballot_sync(FULL_MASK, mine == most) >> at;
+    const int winner = __ffs(votes) - 1;
+    e = winner * kPer + 7 - (int)(__shfl_sync(FULL_MASK, v[0], winner, L) & 7u);
+    if (lane == winner) {
+#pragma unroll
+        for (int j = 0; j < 7; ++j) v[j] = v[j + 1];
+        v[7] = 0u;
+    }
+    return most;
+}
+
+// The row's k best, written to sh.expert and sh.logit by its lane 0.  By the logits, exactly
+// (BY_LOGIT), or by the scores in fp32: returns whether two neighbours, or the border of the kept groups, lie
+// within the error: scores are off by 2^-20, or 2^-16 of the largest one (softmax), and by 2^-20 of their own size, at most.
+template <typename T, bool BY_LOGIT, int C, int L>
+__device__ __forceinline__ bool choose(const RouteArgs& a, const T* row, const float (&l)[C][kPer], int lane, bool whole,
+                                       const RouteShared& sh)
+{
+    constexpr float kLow = -INFINITY;
     bool near = false;
-    S c[C][kPer], off = 0;
+    float c[C][kPer], off = 0;
     // groups of whole lanes, a power of two of them: no shared memory
     const int spread = a.experts / a.groups / kPer;
-    const bool in_lanes = C == 1 && sizeof(S) == 4 && a.experts == a.groups * spread * kPer && (spread & (spread - 1)) == 0;
+    const bool in_lanes = C == 1 && a.experts == a.groups * spread * kPer && (spread & (spread - 1)) == 0;
     if constexpr (BY_LOGIT) {
 #pragma unroll
         for (int i = 0; i < C; ++i) {
@@ -257,21 +262,32 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const T* row, const f
             for (int j = 0; j < kPer; ++j) most = fmaxf(most, l[i][j]);
         }
         most = lanes_max<L>(most);
-        const S sum = sigmoid ? (S)1 : exp_sum<S, C, L>(l, most);
-        off = sigmoid ? (S)0x1p-20 : (S)0x1p-16 / sum;
+        const float sum = sigmoid ? 1.f : exp_sum<float, C, L>(l, most);
+        off = sigmoid ? 0x1p-20f : 0x1p-16f / sum;
 #pragma unroll
         for (int i = 0; i < C; ++i) {
+            const int e0 = (i * L + lane) * kPer;
+            float b[kPer];
+            if (whole && a.bias && e0 < a.experts && (reinterpret_cast<uintptr_t>(a.bias) & 15) == 0) {
+#pragma unroll
+                for (int j = 0; j < kPer; j += 4) {
+                    const float4 v = *reinterpret_cast<const float4*>(a.bias + e0 + j);
+                    b[j] = v.x, b[j + 1] = v.y, b[j + 2] = v.z, b[j + 3] = v.w;
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) b[j] = a.bias && e0 + j < a.experts ? fetch(a.bias + e0 + j) : 0.f;
+            }
 #pragma unroll
             for (int j = 0; j < kPer; ++j) {
-                const int e = (i * L + lane) * kPer + j;
-                c[i][j] = l[i][j] > -INFINITY ? rough_score(l[i][j], sigmoid, most, sum) + (a.bias ? (S)fetch(a.bias + e) : (S)0) : kLow;
+                c[i][j] = l[i][j] > -INFINITY ? rough_score(l[i][j], sigmoid, most, sum) + b[j] : kLow;
                 if (!(c[i][j] > kLow)) c[i][j] = kLow;  // a bias of NaN
             }
         }
         if (a.groups > 1 && !in_lanes) {
             // a group's score: the sum of its two best (its only one's, where it has one)
-            S* by = static_cast<S*>(sh.c);
-            S* best = by + a.experts;
+            float* by = static_cast<float*>(sh.c);
+            float* best = by + a.experts;
             const int size = a.experts / a.groups;
             __syncwarp();
 #pragma unroll
@@ -285,31 +301,33 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const T* row, const f
             __syncwarp();
             // with fewer groups than lanes several lanes read a group, neighbours side by side
             const int share = a.groups >= L ? 1 : 1 << (31 - __clz(L / a.groups));
+            float size_of = 0;  // of the numbers that are added, which may cancel
             for (int g0 = 0; g0 < a.groups; g0 += L / share) {
                 const int g = g0 + lane / share;
-                S first = kLow, second = kLow;
+                float first = kLow, second = kLow;
                 if (g < a.groups) {
                     for (int e = lane & (share - 1); e < size; e += share) {
-                        const S v = by[g * size + e], low = min(v, first);
+                        const float v = by[g * size + e], low = min(v, first);
                         first = max(v, first);
                         second = max(second, low);
                     }
                 }
                 for (int o = 1; o < share; o <<= 1) {
-                    const S v = __shfl_xor_sync(FULL_MASK, first, o), w = __shfl_xor_sync(FULL_MASK, second, o);
+                    const float v = __shfl_xor_sync(FULL_MASK, first, o), w = __shfl_xor_sync(FULL_MASK, second, o);
                     second = max(max(second, w), min(first, v));
                     first = max(first, v);
                 }
                 if (g < a.groups && (lane & (share - 1)) == 0) best[g] = group_score(first, second);
+                if (first > kLow) size_of = max(size_of, fabsf(first) + (second > kLow ? fabsf(second) : 0.f));
             }
             __syncwarp();
-            S least_kept = INFINITY, best_left = kLow;
+            float least_kept = INFINITY, best_left = kLow;
             uint32_t kept_mask = 0;  // of this lane's groups: 1,024 groups on 32 lanes are 32
             for (int g = lane, q = 0; g < a.groups; g += L, ++q) {
-                const S mine = best[g];
+                const float mine = best[g];
                 int better = 0;
                 for (int o = 0; o < a.groups; ++o) {
-                    const S other = best[o];
+                    const float other = best[o];
                     better += other > mine || (other == mine && o < g);
                 }
                 const bool keep = better < a.top_groups && mine > kLow;
@@ -319,9 +337,10 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const T* row, const f
             }
             least_kept = -lanes_max<L>(-least_kept);
             best_left = lanes_max<L>(best_left);
-            near = best_left > kLow && !(least_kept - best_left > 4 * off + (S)0x1p-21 * (fabs(least_kept) + fabs(best_left)));
+            const float largest = lanes_max<L>(size_of);
+            near = best_left > kLow && !(least_kept - best_left > 4 * off + 0x1p-18f * largest);
             __syncwarp();
-            for (int g = lane, q = 0; g < a.groups; g += L, ++q) best[g] = kept_mask >> q & 1 ? (S)1 : (S)0;
+            for (int g = lane, q = 0; g < a.groups; g += L, ++q) best[g] = kept_mask >> q & 1 ? 1.f : 0.f;
             __syncwarp();
 #pragma unroll
             for (int i = 0; i < C; ++i) {
@@ -329,7 +348,7 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const T* row, const f
                 int e = (i * L + lane) * kPer, g = e / size, in = e - g * size;
 #pragma unroll
                 for (int j = 0; j < kPer; ++j, ++e) {
-                    if (e < a.experts && best[g] == (S)0) c[i][j] = kLow;
+                    if (e < a.experts && best[g] == 0.f) c[i][j] = kLow;
                     if (++in == size) {
                         in = 0;
                         ++g;
@@ -339,60 +358,77 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const T* row, const f
         }
     }
     const int rounds = BY_LOGIT ? a.top_k : a.top_k + 1;  // one more than asked for shows the gap to the first that is left out
-    S before = 0;
+    float before = 0;
     int before_e = 0;
     auto logit_at = [&](int e) { return fminf(elem<T>::to_f32(fetch(row + e)), 3.402823466e38f); };
     // equal logits and biases are a tie in any arithmetic
-    auto too_near = [&](S top, int e) {
-        if (!(before - top <= 2 * off + (S)0x1p-21 * (fabs(before) + fabs(top)))) return false;
+    auto too_near = [&](float top, int e) {
+        if (!(before - top <= 2 * off + 0x1p-19f * (fabsf(before) + fabsf(top)))) return false;
         const float b0 = a.bias ? fetch(a.bias + before_e) : 0.f, b1 = a.bias ? fetch(a.bias + e) : 0.f;
         return !(logit_at(before_e) == logit_at(e) && b0 == b1);
     };
-    if constexpr (C == 1 && sizeof(S) == 4) {
+    if constexpr (C == 1 && BY_LOGIT) {
         uint64_t v[kPer];
 #pragma unroll
         for (int j = 0; j < kPer; ++j) v[j] = rank_of(c[0][j], lane * kPer + j);
         sort8(v);
-        if (!BY_LOGIT && a.groups > 1 && in_lanes) {
+        for (int r = 0; r < a.top_k; ++r) {
+            int e;
+            const uint32_t most = take_best<L>(v, lane, e);
+            if (lane == 0) {
+                sh.expert[r] = most ? e : -1;
+                sh.logit[r] = value_of(most);
+            }
+        }
+    } else if constexpr (C == 1) {
+        uint32_t v[kPer];
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) v[j] = rough_rank(c[0][j], j);
+        sort8(v);
+        if (a.groups > 1 && in_lanes) {
             // a group's score: the sum of its two best (its only one's, where it has one)
-            S first = value_of((uint32_t)(v[0] >> 32)), second = value_of((uint32_t)(v[1] >> 32));
+            float first = value_of(v[0] & ~7u), second = value_of(v[1] & ~7u);
             for (int o = 1; o < spread; o <<= 1) {
-                const S x = __shfl_xor_sync(FULL_MASK, first, o), y = __shfl_xor_sync(FULL_MASK, second, o);
+                const float x = __shfl_xor_sync(FULL_MASK, first, o), y = __shfl_xor_sync(FULL_MASK, second, o);
                 second = max(max(second, y), min(first, x));
                 first = max(first, x);
             }
-            const S best = group_score(first, second);
+            const float best = group_score(first, second);
+            const float size_of = best > kLow ? fabsf(first) + (second > kLow ? fabsf(second) : 0.f) : 0.f;  // the numbers may cancel
             const int mine = lane / spread;
             int better = 0;
             for (int g = 0; g < a.groups; ++g) {
-                const S other = __shfl_sync(FULL_MASK, best, g * spread, L);
+                const float other = __shfl_sync(FULL_MASK, best, g * spread, L);
                 better += other > best || (other == best && g < mine);
             }
             const bool there = lane * kPer < a.experts && best > kLow, keep = there && better < a.top_groups;
-            const S least_kept = -lanes_max<L>(keep ? -best : kLow), best_left = lanes_max<L>(there && !keep ? best : kLow);
-            near = best_left > kLow && !(least_kept - best_left > 4 * off + (S)0x1p-21 * (fabs(least_kept) + fabs(best_left)));
+            const float least_kept = -lanes_max<L>(keep ? -best : kLow), best_left = lanes_max<L>(there && !keep ? best : kLow);
+            const float largest = lanes_max<L>(size_of);
+            near = best_left > kLow && !(least_kept - best_left > 4 * off + 0x1p-18f * largest);
             if (!keep) {
 #pragma unroll
-                for (int j = 0; j < kPer; ++j) v[j] = 0ull;
+                for (int j = 0; j < kPer; ++j) v[j] = 0u;
             }
         }
         for (int r = 0; r < rounds; ++r) {
             int e;
-            const uint32_t most = take_best<L>(v, lane, e);
-            const S top = value_of(most);
-            if (!BY_LOGIT) {
-                if (r > 0 && most) near |= too_near(top, e);
-                before = top;
-                before_e = most ? e : 0;
-            }
-            if (r < a.top_k && lane == 0) {
+            const uint32_t most = take_rough_best<L>(v, lane, e);
+            if (lane == 0) {
                 sh.expert[r] = most ? e : -1;
-                if (BY_LOGIT) sh.logit[r] = top;
+                sh.logit[r] = __uint_as_float(most);
             }
+        }
+        __syncwarp();
+        for (int r = lane; r < a.top_k; r += L) {
+            const int e = sh.expert[r + 1];
+            if (e < 0) break;
+            before = value_of(__float_as_uint(sh.logit[r]));
+            before_e = sh.expert[r];
+            near |= too_near(value_of(__float_as_uint(sh.logit[r + 1])), e);
         }
     } else {
         for (int r = 0; r < rounds; ++r) {
-            S top = kLow;
+            float top = kLow;
             int e_top = kNone;
             float l_top = 0.f;
 #pragma unroll
@@ -407,7 +443,7 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const T* row, const f
             }
             best_of_lanes<C, L>(top, e_top, l_top, lane);
             const bool found = e_top != kNone;
-            if (!BY_LOGIT && sizeof(S) == 4 && r > 0 && found) near |= too_near(top, e_top);
+            if (!BY_LOGIT && r > 0 && found) near |= too_near(top, e_top);
             before = top;
             before_e = found ? e_top : 0;
             if (r < a.top_k && lane == 0) {
@@ -456,13 +492,129 @@ __device__ __forceinline__ void choose16(const RouteArgs& a, const T* row, int l
     }
 }
 
-// The same choice in 64 bits, for the rows that need it.
+// The same choice in 64 bits, for the rows that need it.  Only the scores and the groups' sums are computed in
+// floating point, as it is slow (2 a cycle on an SM): comparisons are of words that are ordered as the scores are, 0 for
+// what is not available.  One such row is alone at the end of many a call: with comparisons of doubles it took 17 us.
+__device__ __forceinline__ uint64_t order_of(double v)
+{
+    const uint64_t b = (uint64_t)__double_as_longlong(v + 0.0);  // one zero
+    return v > -INFINITY ? b ^ (b >> 63 ? ~0ull : 1ull << 63) : 0ull;
+}
+__device__ __forceinline__ double value_of(uint64_t w) { return __longlong_as_double((long long)(w >> 63 ? w ^ (1ull << 63) : ~w)); }
+
 template <typename T, int C, int L>
 __device__ __noinline__ void choose_exactly(const RouteArgs& a, const T* row, int lane, bool whole, const RouteShared& sh)
 {
-    float l[C][kPer];
-    load_logits<T, C, L>(row, a.experts, lane, whole, l);
-    choose<T, double, false, C, L>(a, row, l, lane, sh);
+    uint64_t w[C][kPer];
+    {
+        float l[C][kPer];
+        load_logits<T, C, L>(row, a.experts, lane, whole, l);
+        const bool sigmoid = a.score == SPC_SCORE_SIGMOID;
+        float most = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) most = fmaxf(most, l[i][j]);
+        }
+        most = lanes_max<L>(most);
+        const double sum = sigmoid ? 1.0 : exp_sum<double, C, L>(l, most);
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) {
+                const int e = (i * L + lane) * kPer + j;
+                w[i][j] = l[i][j] > -INFINITY ? order_of(score_of<double>(l[i][j], sigmoid, most, sum) + (a.bias ? (double)fetch(a.bias + e) : 0.0)) : 0ull;
+            }
+        }
+    }
+    if (a.groups > 1) {
+        uint64_t* by = static_cast<uint64_t*>(sh.c);
+        uint64_t* best = by + a.experts;
+        const int size = a.experts / a.groups;
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) {
+                const int e = (i * L + lane) * kPer + j;
+                if (e < a.experts) by[e] = w[i][j];
+            }
+        }
+        __syncwarp();
+        const int share = a.groups >= L ? 1 : 1 << (31 - __clz(L / a.groups));
+        for (int g0 = 0; g0 < a.groups; g0 += L / share) {
+            const int g = g0 + lane / share;
+            uint64_t first = 0, second = 0;
+            if (g < a.groups) {
+                for (int e = lane & (share - 1); e < size; e += share) {
+                    const uint64_t v = by[g * size + e], low = min(v, first);
+                    first = max(v, first);
+                    second = max(second, low);
+                }
+            }
+            for (int o = 1; o < share; o <<= 1) {
+                const uint64_t x = __shfl_xor_sync(FULL_MASK, first, o), y = __shfl_xor_sync(FULL_MASK, second, o);
+                second = max(max(second, y), min(first, x));
+                first = max(first, x);
+            }
+            if (g < a.groups && (lane & (share - 1)) == 0) best[g] = second ? order_of(value_of(first) + value_of(second)) : first;
+        }
+        __syncwarp();
+        uint32_t kept = 0;  // of this lane's groups: 1,024 groups on 32 lanes are 32
+        for (int g = lane, q = 0; g < a.groups; g += L, ++q) {
+            const uint64_t mine = best[g];
+            int better = 0;
+            for (int o = 0; o < a.groups; ++o) {
+                const uint64_t other = best[o];
+                better += other > mine || (other == mine && o < g);
+            }
+            if (better < a.top_groups && mine) kept |= 1u << q;
+        }
+        __syncwarp();
+        for (int g = lane, q = 0; g < a.groups; g += L, ++q) best[g] = kept >> q & 1;
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            int e = (i * L + lane) * kPer, g = e / size, in = e - g * size;
+#pragma unroll
+            for (int j = 0; j < kPer; ++j, ++e) {
+                if (e < a.experts && !best[g]) w[i][j] = 0;
+                if (++in == size) {
+                    in = 0;
+                    ++g;
+                }
+            }
+        }
+    }
+    for (int r = 0; r < a.top_k; ++r) {
+        uint64_t top = 0;
+        int e = kNone;
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+#pragma unroll
+            for (int j = 0; j < kPer; ++j)
+                if (w[i][j] > top) {
+                    top = w[i][j];
+                    e = (i * L + lane) * kPer + j;
+                }
+        }
+        // the largest word, high half first, then the lowest expert that has it
+        const uint32_t high = lanes_most<L>((uint32_t)(top >> 32));
+        bool mine = top && (uint32_t)(top >> 32) == high;
+        const uint32_t low = lanes_most<L>(mine ? (uint32_t)top : 0u);
+        mine = mine && (uint32_t)top == low;
+        e = (int)~lanes_most<L>(~(uint32_t)(mine ? e : kNone));
+        if (lane == 0) {
+            sh.expert[r] = e != kNone ? e : -1;
+            sh.logit[r] = e != kNone ? fminf(elem<T>::to_f32(fetch(row + e)), 3.402823466e38f) : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+#pragma unroll
+            for (int j = 0; j < kPer; ++j)
+                if ((i * L + lane) * kPer + j == e) w[i][j] = 0;
+        }
+    }
 }
 
 // An expert's weight from its logit: its score, or its share of the chosen ones' scores.
@@ -512,8 +664,8 @@ k_route(RouteArgs a, bool whole)
     RouteShared sh;
     const int grouped = a.groups > 1 ? a.experts + a.groups : 0;
     sh.c = room + mine * grouped;
-    sh.logit = reinterpret_cast<float*>(room + rows * grouped) + mine * 2 * a.top_k;
-    sh.expert = reinterpret_cast<int32_t*>(sh.logit + a.top_k);
+    sh.logit = reinterpret_cast<float*>(room + rows * grouped) + mine * 2 * (a.top_k + 1);
+    sh.expert = reinterpret_cast<int32_t*>(sh.logit + a.top_k + 1);
     const T* logits = static_cast<const T*>(a.logits) + at * a.experts;
     const bool sigmoid = a.score == SPC_SCORE_SIGMOID, by_logit = !a.bias && a.groups == 1, all = !sigmoid && !a.renorm;
     float most = -INFINITY, sum = 1.f;
@@ -529,8 +681,8 @@ k_route(RouteArgs a, bool whole)
         load_logits<T, C, L>(logits, a.experts, lane, whole, l);
         if (chosen) {
         } else if (by_logit) {
-            choose<T, float, true, C, L>(a, logits, l, lane, sh);
-        } else if (__any_sync(FULL_MASK, choose<T, float, false, C, L>(a, logits, l, lane, sh))) {
+            choose<T, true, C, L>(a, logits, l, lane, whole, sh);
+        } else if (__any_sync(FULL_MASK, choose<T, false, C, L>(a, logits, l, lane, whole, sh))) {
             __syncwarp();
             choose_exactly<T, C, L>(a, logits, lane, whole, sh);
         }
@@ -690,7 +842,7 @@ spc_status fwd(const RouteArgs& a, cudaStream_t st)
 {
     const bool whole = a.experts % kPer == 0 && aligned16(a.logits);
     const int L = lanes_for(a.experts);
-    const size_t smem = (size_t)(kBlock / L) * ((a.groups > 1 ? 8 * (size_t)(a.experts + a.groups) : 0) + 8 * (size_t)a.top_k);
+    const size_t smem = (size_t)(kBlock / L) * ((a.groups > 1 ? 8 * (size_t)(a.experts + a.groups) : 0) + 8 * (size_t)(a.top_k + 1));
     if (a.experts > 256) return start<k_route<T, 4, 32>>(a, L, smem, whole, st);
     switch (L) {
     case 1: return start<k_route<T, 1, 1>>(a, L, smem, whole, st);

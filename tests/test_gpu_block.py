@@ -211,6 +211,23 @@ def test_route_groups_of_biases_at_the_end_of_fp32(size, best):
         close(w, gate, bound)
 
 
+@pytest.mark.parametrize("size", [3, 4, 8])
+def test_route_groups_whose_sums_cancel(size):
+    """Biases of +-100 beside scores below 1: in fp32 a sum of two has lost the scores' last seven bits."""
+    g = gen(13)
+    n, groups = 400, 6
+    experts = groups * size
+    level = torch.randint(0, 3, (n, experts), generator=g)
+    logits = (0.4 * level + 2.0 ** -18 * torch.randint(0, 5, (n, experts), generator=g)).float()
+    bias = torch.full((groups, size), -100.0)
+    bias[:, 0] = 100.0
+    bias[:, 2:] = -200.0
+    (expert, gate), bound = ref.route_fwd(logits, 3, "sigmoid", bias.view(-1), groups, 2, True, 1.0)
+    got, w = spc.spc_route_fwd(to(logits), 3, score=spc.SPC_SCORE_SIGMOID, bias=to(bias.view(-1)), groups=groups, top_groups=2)
+    assert torch.equal(got.cpu(), expert)
+    close(w, gate, bound)
+
+
 def test_route_reports_experts_out_of_range_and_feeds_row_segments():
     g, logits, _ = route_case(50, 16, False, "f32")
     expert, gate = spc.spc_route_fwd(to(logits), 2)
