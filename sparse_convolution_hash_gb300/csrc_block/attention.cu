@@ -34,6 +34,8 @@ Layout layout(int64_t nq, int64_t nk, int32_t segments, int32_t hq, int32_t hk, 
     if (tc && !backward) {
         const AttnShape f = attn_shape(nq, segments, hq, hk, d);
         l.splits = splits_for(nq, segments, hq / f.heads, nk, f.positions * f.tiles, kLeastShare, f.tiles == 2 ? 1 : 2);
+    } else if (!backward && dt == SPC_F32 && d <= kAttnNarrow) {
+        l.splits = splits_for(nq, segments, hq, nk, 32 * attn_rows_each(nq, nk, segments, hq), kLeastShare, 2);
     } else {
         l.splits = splits_for(nq, segments, hq, nk, kSimtRows, kLeastShare, tc ? 2 : 4);
     }
@@ -296,6 +298,12 @@ AttnShape attn_shape(int64_t nq, int32_t segments, int32_t hq, int32_t hk, int32
     const int64_t blocks = ceil_div(nq, 2 * f.positions) * (hq / f.heads);
     f.tiles = d > 64 && nq / segments >= 12 * f.positions && blocks >= sm_count() ? 2 : 1;
     return f;
+}
+
+int attn_rows_each(int64_t nq, int64_t nk, int32_t segments, int32_t hq)
+{
+    const int64_t shares = ceil_div(nq, 128) * hq * ceil_div(nk, kLeastShare);
+    return nq >= 450 * (int64_t)segments && shares >= 2 * (int64_t)sm_count() ? 4 : 2;
 }
 
 bool attention_tc_supported(const AttnArgs& a, spc_dtype dt, bool backward)

@@ -123,6 +123,12 @@ struct AttnShape {
 };
 AttnShape attn_shape(int64_t nq, int32_t segments, int32_t hq, int32_t hk, int32_t d);
 
+// fp32 heads so narrow that a thread of the forward kernel keeps whole rows, and how many: four read keys and values half as often
+// as two, two waste less of a block on short segments and give more blocks (8 heads of 16, us with four / two: 30,000 rows in
+// segments of 150 148 / 106, of 300 179 / 148, of 500 193 / 214, of 1,000 361 / 409; 4 heads: 1,000 rows 22 / 16, 2,000 37 / 43).
+constexpr int kAttnNarrow = 16;
+int attn_rows_each(int64_t nq, int64_t nk, int32_t segments, int32_t hq);
+
 // Kernels for 16-bit heads of a multiple of 8 channels, up to 128, on 16-byte boundaries.
 bool attention_tc_supported(const AttnArgs& a, spc_dtype dt, bool backward);
 size_t attention_ws_bytes(int64_t nq, int64_t nk, int32_t segments, int32_t hq, int32_t hk, int32_t d, spc_dtype dt, bool backward);

@@ -308,6 +308,37 @@ def test_attention_at_tile_borders(hq, hk, d, sizes_q, sizes_k, dtype):
     check_attention(*case, dtype, run_attention(*case, dtype))
 
 
+@pytest.mark.parametrize("hq,hk,d,sizes_q,sizes_k,outside", [
+    (1, 1, 16, [128], [128], 0), (2, 1, 12, [129, 1, 300], [257, 0, 131], 2), (3, 3, 4, [127], [1], 0), (4, 4, 8, [20], [5000], 0),
+    (4, 2, 16, [1500], [1500], 3), (1, 1, 16, [5, 4, 3], [33, 129, 4], 0), (2, 2, 16, [40] * 30, None, 0), (6, 2, 16, [1], [100], 1)])
+def test_attention_of_narrow_heads(hq, hk, d, sizes_q, sizes_k, outside):
+    case = attn_case(hq, hk, d, sizes_q, sizes_k, outside, "f32")
+    check_attention(*case, "f32", run_attention(*case, "f32"))
+
+
+def test_attention_of_narrow_heads_with_bad_values():
+    """NaN and infinities stay in their segment and their row, and keys that score -inf have no part."""
+    q, k, v, dout, seg, _ = attn_case(2, 2, 16, [140, 150, 60], None, 0, "f32")
+    o, lse = spc.spc_attention_fwd(to(q), to(k), to(v), offsets(*seg))
+    q[3, 0, 5] = math.nan
+    k[200, 1, 2], v[201, 0] = math.nan, math.inf
+    k[300, :], q[290:, :] = -math.inf, q[290:, :].abs() + 0.1  # no query of the last segment scores it
+    o2, lse2 = spc.spc_attention_fwd(to(q), to(k), to(v), offsets(*seg))
+    bad = torch.zeros(350, 2, dtype=torch.bool)
+    bad[3, 0] = bad[140:290, 1] = True
+    assert torch.equal(lse2.isnan().cpu(), bad)
+    assert not o2[bad.to(o2.device)].isfinite().any() and not o2[140:290, 0].isfinite().any()
+    same = ~bad
+    same[140:290, 0] = same[290:] = False
+    assert torch.equal(o2[same.to(o2.device)], o[same.to(o2.device)]) and torch.equal(lse2[:140][same[:140].to(o2.device)], lse[:140][same[:140].to(o2.device)])
+    keep = [i for i in range(290, 350) if i != 300]
+    want, _ = spc.spc_attention_fwd(to(q[290:]), to(k[keep]), to(v[keep]), offsets(0, 60), seg_k=offsets(0, 59))
+    assert torch.allclose(o2[290:], want, rtol=1e-5, atol=1e-5)
+    all_out = torch.full((70, 2, 16), -math.inf)
+    o3, lse3 = spc.spc_attention_fwd(to(q[290:]), to(all_out), to(v[:70]), offsets(0, 60), seg_k=offsets(0, 70))
+    assert not o3.any() and bool((lse3 == -math.inf).all())
+
+
 @pytest.mark.parametrize("scale", [1e-3, 1.0, 30.0])
 def test_attention_scales(scale):
     for dtype in ("f32", "bf16"):
