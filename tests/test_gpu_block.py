@@ -91,6 +91,30 @@ def test_layer_norm_in_place_far_means_and_odd_places(c, dtype):
         close(a, w, b)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n,c,skip,skip_affine", [(37, 6, 0, 0), (70, 46, 2, 0), (19, 334, 0, 0), (19, 334, 2, 1), (19, 334, 0, 2), (11, 1002, 6, 0),
+                                                  (5, 2050, 0, 0), (5, 4098, 2, 2), (3, 8186, 0, 0), (23, 333, 0, 0), (2, 9002, 2, 0), (64, 64, 2, 0)])
+def test_layer_norm_in_words_of_two_and_one(n, c, skip, skip_affine, dtype):
+    """Rows, gamma and beta off their 16-byte boundaries by a few elements."""
+    g = gen(n + c + skip)
+
+    def apart(t, by):
+        flat = torch.zeros(t.numel() + by, dtype=t.dtype, device=dev())
+        flat[by:] = to(t).view(-1)
+        return flat[by:].view(t.shape)
+
+    x, dy = normal(g, n, c, dtype=dtype), normal(g, n, c, dtype=dtype)
+    ga, be = 1 + 0.3 * normal(g, c), 0.3 * normal(g, c)
+    want, bound = ref.layer_norm_fwd(x, ga, be, 1e-5)
+    got = spc.spc_layer_norm_fwd(apart(x, skip), apart(ga, skip_affine), apart(be, skip_affine))
+    for a, w, b, name in zip(got, want, bound, ("y", "mean", "rstd")):
+        close(a, w, b, name)
+    want, bound = ref.layer_norm_bwd(dy, x, ga, got[1].cpu(), got[2].cpu())
+    back = spc.spc_layer_norm_bwd(apart(dy, skip), apart(x, skip), apart(ga, skip_affine), got[1], got[2])
+    for a, w, b, name in zip(back, want, bound, ("dx", "dgamma", "dbeta")):
+        close(a, w, b, name)
+
+
 # ------------------------------------------------------------ rotary positions
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("n,heads,d,pairs,extra", [
