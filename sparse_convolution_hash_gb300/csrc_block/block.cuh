@@ -46,6 +46,7 @@ struct RouteArgs {
     int64_t n;
     int32_t experts, top_k, score, groups, top_groups, renorm;
     float scale;
+    int32_t lanes_log2;     // of a group, set by route()
 };
 struct RouteGradArgs {
     const float* dgate;

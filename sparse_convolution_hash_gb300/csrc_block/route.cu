@@ -244,9 +244,7 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const T* row, const f
     constexpr float kLow = -INFINITY;
     bool near = false;
     float c[C][kPer], off = 0;
-    // groups of whole lanes, a power of two of them: no shared memory
-    const int spread = a.experts / a.groups / kPer;
-    const bool in_lanes = C == 1 && a.experts == a.groups * spread * kPer && (spread & (spread - 1)) == 0;
+    const bool in_lanes = C == 1 && a.lanes_log2 >= 0;  // no shared memory
     if constexpr (BY_LOGIT) {
 #pragma unroll
         for (int i = 0; i < C; ++i) {
@@ -388,17 +386,18 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const T* row, const f
         if (a.groups > 1 && in_lanes) {
             // a group's score: the sum of its two best (its only one's, where it has one)
             float first = value_of(v[0] & ~7u), second = value_of(v[1] & ~7u);
-            for (int o = 1; o < spread; o <<= 1) {
+            for (int o = 1; o < 1 << a.lanes_log2; o <<= 1) {
                 const float x = __shfl_xor_sync(FULL_MASK, first, o), y = __shfl_xor_sync(FULL_MASK, second, o);
                 second = max(max(second, y), min(first, x));
                 first = max(first, x);
             }
             const float best = group_score(first, second);
             const float size_of = best > kLow ? fabsf(first) + (second > kLow ? fabsf(second) : 0.f) : 0.f;  // the numbers may cancel
-            const int mine = lane / spread;
+            const int mine = lane >> a.lanes_log2;
             int better = 0;
+#pragma unroll 4
             for (int g = 0; g < a.groups; ++g) {
-                const float other = __shfl_sync(FULL_MASK, best, g * spread, L);
+                const float other = __shfl_sync(FULL_MASK, best, g << a.lanes_log2, L);
                 better += other > best || (other == best && g < mine);
             }
             const bool there = lane * kPer < a.experts && best > kLow, keep = there && better < a.top_groups;
@@ -837,9 +836,18 @@ spc_status start(const A& a, int L, size_t smem, bool whole, cudaStream_t st)
     return SPC_OK;
 }
 
-template <typename T>
-spc_status fwd(const RouteArgs& a, cudaStream_t st)
+// Of groups that are whole lanes, a power of two of them: that power, else -1.
+int lanes_log2_of(int experts, int groups)
 {
+    int p = 0;
+    while (groups * (kPer << p) < experts) ++p;
+    return groups * (kPer << p) == experts ? p : -1;
+}
+
+template <typename T>
+spc_status fwd(RouteArgs a, cudaStream_t st)
+{
+    a.lanes_log2 = lanes_log2_of(a.experts, a.groups);
     const bool whole = a.experts % kPer == 0 && aligned16(a.logits);
     const int L = lanes_for(a.experts);
     const size_t smem = (size_t)(kBlock / L) * ((a.groups > 1 ? 8 * (size_t)(a.experts + a.groups) : 0) + 8 * (size_t)(a.top_k + 1));
