@@ -8,7 +8,7 @@
 // two neighbours of the result lie closer than fp32's error (about one row in a hundred or fewer), made again in
 // 64 bits.  The choice is therefore that of the formula in 64 bits, whatever the order of the sums.
 //
-// Bound by instructions: a row of 64 experts in 16 bits is 128 bytes and some 200 instructions.
+// Bound by instructions: a row of 64 experts in 16 bits is 128 bytes and some 140 instructions, one of 256 in fp32 in groups 1,300.
 #include <math.h>
 
 #include "block.cuh"
