@@ -10,9 +10,10 @@ namespace {
 constexpr int kBlock = 256;
 
 // Splits along the other axis: few tiles leave SMs idle, so each tile's walk is cut until there are `blocks` for
-// every SM, in shares of at least `least` rows of an axis of n_other.
+// every SM, in shares of at least `least` rows of an axis of n_other.  An axis without rows has nothing to split, or to join.
 int splits_for(int64_t n, int32_t segments, int64_t heads, int64_t n_other, int rows, int least, int blocks)
 {
+    if (n == 0) return 1;
     const int64_t tiles = std::max<int64_t>(1, std::max<int64_t>(ceil_div(n, rows), std::min<int64_t>(n, segments))) * heads;
     const int64_t wanted = blocks * (int64_t)sm_count() / tiles;
     return (int)std::max<int64_t>(1, std::min<int64_t>(wanted, ceil_div(n_other, least)));
