@@ -7,9 +7,10 @@ import math
 import pytest
 import torch
 
+import block_ref as ref
 import sparse_convolution_hash_gb300 as spc
-from gpu_util import dev
-from test_gpu_block import TYPES, gen, normal
+from gpu_util import DT, dev
+from test_gpu_block import TYPES, close, gen, normal, to
 
 pytestmark = pytest.mark.gpu
 
@@ -41,3 +42,64 @@ def test_attention_gradients_where_one_side_has_no_rows(n, hq, hk, dtype):
     o, lse = spc.spc_attention_fwd(none_q, k, k, no, seg_k=all_)
     dq, dk, dv = spc.spc_attention_bwd(none_q, none_q, k, k, o, lse, no, seg_k=all_, dk=torch.full_like(k, 7), dv=torch.full_like(k, 7))
     assert dq.shape == none_q.shape and not dk.any() and not dv.any()
+
+
+# ------------------------------------------------------------------ ties at the border of a choice
+def check_choice(logits, top_k, score, bias, groups=1, kept=1):
+    (expert, gate), bound = ref.route_fwd(logits, top_k, score, bias, groups, kept, True, 1.0)
+    kind = spc.SPC_SCORE_SIGMOID if score == "sigmoid" else spc.SPC_SCORE_SOFTMAX
+    got, w = spc.spc_route_fwd(to(logits), top_k, score=kind, bias=to(bias), groups=groups, top_groups=kept)
+    wrong = (got.cpu() != expert).any(1).nonzero()[:, 0]
+    assert not len(wrong), f"{len(wrong)} rows, the first {int(wrong[0])}: {got[wrong[0]].tolist()}, not {expert[wrong[0]].tolist()}"
+    close(w, gate, bound)
+
+
+@pytest.mark.parametrize("score,low,high,dtype", [
+    ("sigmoid", 15.5, 16.0, "f32"), ("sigmoid", 15.5, 16.0, "f16"), ("sigmoid", 15.5, 16.0, "bf16"), ("softmax", 0.0, 2.0 ** -30, "f32"),
+    ("softmax", 0.0, 2.0 ** -30, "bf16"), ("softmax", 0.0, 2.0 ** -24, "f16"), ("sigmoid", 0.3, 0.3 + 2.0 ** -25, "f32"),
+    ("softmax", 0.3, 0.3 + 2.0 ** -25, "f32")])
+@pytest.mark.parametrize("experts", [3, 8, 16, 64, 256, 257, 1000])
+def test_route_tie_at_the_border_before_a_larger_score(experts, score, low, high, dtype):
+    """The last expert that is chosen and the first that is left out have equal logits, and a later one's score is larger by less than
+    fp32 shows.  Several ties and several places; every other row of the warp is far from any tie."""
+    far = -8.0 if score == "sigmoid" else -20.0
+    for top_k in (1, 2):
+        rows = []
+        g = gen(experts + top_k)
+        for r in range(24):
+            row = torch.linspace(far - 4, far, experts).double()
+            if r % 4 != 3:
+                place = torch.randperm(experts, generator=g)[:min(experts, top_k + 2 + r % 3)].sort().values
+                row[place] = low
+                row[place[-1]] = high
+            rows.append(row)
+        logits = torch.stack(rows).to(DT[dtype])
+        assert (logits.double() == torch.tensor(high, dtype=torch.float32).to(DT[dtype]).double()).any()
+        check_choice(logits, top_k, score, torch.zeros(experts))
+
+
+@pytest.mark.parametrize("experts", [8, 64, 256, 1024])
+@pytest.mark.parametrize("top_k", [1, 2, 8])
+@pytest.mark.parametrize("around,spread", [(12.0, 2.0), (0.0, 5.0), (8.0, 3.0), (0.0, 0.0)])
+@pytest.mark.parametrize("groups,kept", [(1, 1), (4, 2)])
+def test_route_of_saturated_scores(experts, top_k, around, spread, groups, kept):
+    """bf16 logits, many of them equal, whose sigmoids are nearly 1; and all equal."""
+    if top_k > experts // groups * kept:
+        pytest.skip("fewer experts than places")
+    logits = (around + spread * normal(gen(experts), 300, experts)).clamp(-25, 25).to(torch.bfloat16)
+    check_choice(logits, top_k, "sigmoid", torch.zeros(experts), groups, kept)
+
+
+def test_route_tie_at_the_border_of_biased_scores():
+    """Equal logits with equal biases at the border; behind them another bias makes up for a lower logit."""
+    logits = torch.full((40, 64), -6.0)
+    bias = torch.full((64,), 0.25)
+    logits[:, 5] = logits[:, 9] = 0.5
+    logits[:, 33] = 0.25
+    # the sum is larger than that of 5 and 9 by 2^-26 and some rounding, in fp32 the same
+    s = lambda v: 1 / (1 + math.exp(-v))  # noqa: E731
+    bias[5] = bias[9] = 0.0
+    bias[33] = torch.tensor(s(0.5) - s(0.25), dtype=torch.float64).float()
+    for more in range(8):
+        check_choice(logits, 1, "sigmoid", bias)
+        bias[33] = torch.nextafter(bias[33], torch.tensor(1.0))
