@@ -769,7 +769,8 @@ SPC_API spc_status spc_attention_fwd(const void* q, int64_t ldq, const void* k, 
  *   delta = sum over d of dout o,  ds = p (dout v^T - delta),
  *   dq = scale ds k,  dk = scale ds^T q,  dv = p^T dout,
  * dk and dv summed over the query heads that share a key head.  Rows of no segment give zeros.  p and ds are
- * rounded to dt before their products on tensor cores.  No atomics: results are run-to-run bit-identical.
+ * rounded to dt before their products on tensor cores (in fp16 ds times a power of two that a segment's and key head's own largest
+ * values set).  No atomics: results are run-to-run bit-identical.
  *
  *  o, lse  from the forward pass.    dout rows of [hq, d], lddo apart.
  *  dq, dk, dv  rows of dtype dt out, lddq, lddk, lddv apart; they overlap no argument nor one another.

@@ -25,7 +25,7 @@ bool wide_enough(int32_t d, spc_dtype dt) { return dt != SPC_F32 && d % 8 == 0; 
 
 struct Layout {
     int32_t splits, splits_kv;
-    size_t part, part_lse, part_kv, lse2, delta, most, bytes;
+    size_t part, part_lse, part_kv, lse2, delta, norm_do, norm_v, bytes;
 };
 
 Layout layout(int64_t nq, int64_t nk, int32_t segments, int32_t hq, int32_t hk, int32_t d, spc_dtype dt, bool backward)
@@ -56,7 +56,10 @@ Layout layout(int64_t nq, int64_t nk, int32_t segments, int32_t hq, int32_t hk, 
         if (l.splits_kv > 1) l.part_kv = take((size_t)nk * hk * d * 4 * 2 * l.splits_kv);
         l.lse2 = take(rows * 4);
         l.delta = take(rows * 4);
-        l.most = take(16);
+        if (tc && dt == SPC_F16) {
+            l.norm_do = take(rows * 4);
+            l.norm_v = take((size_t)nk * hk * 4);
+        }
     }
     l.bytes = at;
     return l;
@@ -141,27 +144,11 @@ k_attn_sum(const float* part, int splits, int64_t rows, int width, T* to, int64_
     to[row * ld + (i - row * width)] = elem<T>::from_f32(s);
 }
 
-// The largest of a block's values into a word that holds the bits of a non-negative float: those are ordered as the numbers
-// are, and the largest does not depend on the order of the blocks.  Values that are not finite have no say (their
-// rows' results are not either).  One atomic a block, and none where the word is as large already: with one a warp the
-// blocks queued up for it (480,000 rows of 32: 81 us against 9).
-__device__ __forceinline__ void block_most(float v, uint32_t* word)
-{
-    __shared__ uint32_t box[kBlock / 32];
-    const uint32_t b = __reduce_max_sync(FULL_MASK, v < INFINITY ? __float_as_uint(v) : 0u);
-    if ((threadIdx.x & 31) == 0) box[threadIdx.x >> 5] = b;
-    __syncthreads();
-    if (threadIdx.x < 32) {
-        const uint32_t all = __reduce_max_sync(FULL_MASK, threadIdx.x < kBlock / 32 ? box[threadIdx.x] : 0u);
-        if (threadIdx.x == 0 && all > *static_cast<volatile uint32_t*>(word)) atomicMax(word, all);
-    }
-}
-
 // Rows of one head (blockIdx.y), LANES lanes to a row, four rows to a group of lanes so that their loads overlap.
-// DELTA: minus the sum of do o over the head's channels, and minus lse to base 2.  MOST (fp16): the largest squared norm of
-// a row of do, or (no DELTA) of v.
+// DELTA: minus the sum of do o over the head's channels, and minus lse to base 2.  NORM (fp16): the norm of the row of do, or
+// (no DELTA) of v.
 constexpr int kRowsEach = 4;
-template <typename T, int LANES, bool DELTA, bool MOST>
+template <typename T, int LANES, bool DELTA, bool NORM>
 __global__ void __launch_bounds__(kBlock)
 k_attn_rows(AttnArgs a, bool whole)
 {
@@ -171,11 +158,11 @@ k_attn_rows(AttnArgs a, bool whole)
     const int64_t n = DELTA ? a.nq : a.nk, ld = DELTA ? a.lddo : a.ldv, row0 = (int64_t)blockIdx.x * (kGroups * kRowsEach) + threadIdx.x / LANES;
     const T* g = static_cast<const T*>(DELTA ? a.dout : a.v) + (int64_t)head * a.d;
     const T* o = static_cast<const T*>(a.o) + (int64_t)head * a.d;
-    float sum[kRowsEach], most[kRowsEach];
+    float sum[kRowsEach], square[kRowsEach];
 #pragma unroll
     for (int k = 0; k < kRowsEach; ++k) {
         const int64_t row = row0 + k * kGroups;
-        sum[k] = most[k] = 0.f;
+        sum[k] = square[k] = 0.f;
         if (row >= n) continue;
         if (whole) {
             for (int c = lane * V; c < a.d; c += LANES * V) {
@@ -186,35 +173,33 @@ k_attn_rows(AttnArgs a, bool whole)
                 for (int j = 0; j < V; ++j) {
                     const float u = elem<T>::to_f32(x.e[j]);
                     if (DELTA) sum[k] = fmaf(elem<T>::to_f32(y.e[j]), u, sum[k]);
-                    if (MOST) most[k] = fmaf(u, u, most[k]);
+                    if (NORM) square[k] = fmaf(u, u, square[k]);
                 }
             }
         } else {
             for (int c = lane; c < a.d; c += LANES) {
                 const float u = elem<T>::to_f32(g[row * ld + c]);
                 if (DELTA) sum[k] = fmaf(elem<T>::to_f32(o[row * a.ldo + c]), u, sum[k]);
-                if (MOST) most[k] = fmaf(u, u, most[k]);
+                if (NORM) square[k] = fmaf(u, u, square[k]);
             }
         }
     }
-    float largest = 0.f;
 #pragma unroll
     for (int k = 0; k < kRowsEach; ++k) {
         const int64_t row = row0 + k * kGroups;
 #pragma unroll
         for (int x = LANES / 2; x; x >>= 1) {
             if (DELTA) sum[k] += __shfl_xor_sync(FULL_MASK, sum[k], x);
-            if (MOST) most[k] += __shfl_xor_sync(FULL_MASK, most[k], x);
+            if (NORM) square[k] += __shfl_xor_sync(FULL_MASK, square[k], x);
         }
-        // NaN and infinities have no say
-        if (MOST) largest = fmaxf(largest, most[k] < INFINITY ? most[k] : 0.f);
+        // rows that are not finite have no say (their results are not finite either)
+        if (NORM && row < n && lane == 0) (DELTA ? a.norm_do : a.norm_v)[head * n + row] = square[k] < INFINITY ? sqrtf(square[k]) : 0.f;
         if (DELTA && row < n && lane == 0) {
             const float lse = fetch(a.lse + row * a.hq + head);
             a.delta[head * a.nq + row] = -sum[k];
             a.lse2[head * a.nq + row] = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
         }
     }
-    if (MOST) block_most(largest, DELTA ? a.most : a.most + 1);
 }
 
 template <typename T>
@@ -247,7 +232,7 @@ spc_status join_bwd(const AttnArgs& a, cudaStream_t st)
     return s;
 }
 
-template <typename T, bool DELTA, bool MOST>
+template <typename T, bool DELTA, bool NORM>
 spc_status rows_of(const AttnArgs& a, cudaStream_t st)
 {
     constexpr int V = 16 / (int)sizeof(T);
@@ -261,18 +246,17 @@ spc_status rows_of(const AttnArgs& a, cudaStream_t st)
     if (blocks > INT32_MAX) return SPC_ERR_UNSUPPORTED;
     const dim3 grid((unsigned)blocks, (unsigned)(DELTA ? a.hq : a.hk));
     switch (lanes) {
-    case 4: return attn_start_kernel<k_attn_rows<T, 4, DELTA, MOST>>(grid, kBlock, 0, st, a, whole);
-    case 8: return attn_start_kernel<k_attn_rows<T, 8, DELTA, MOST>>(grid, kBlock, 0, st, a, whole);
-    default: return attn_start_kernel<k_attn_rows<T, 16, DELTA, MOST>>(grid, kBlock, 0, st, a, whole);
+    case 4: return attn_start_kernel<k_attn_rows<T, 4, DELTA, NORM>>(grid, kBlock, 0, st, a, whole);
+    case 8: return attn_start_kernel<k_attn_rows<T, 8, DELTA, NORM>>(grid, kBlock, 0, st, a, whole);
+    default: return attn_start_kernel<k_attn_rows<T, 16, DELTA, NORM>>(grid, kBlock, 0, st, a, whole);
     }
 }
 
 template <typename T>
-spc_status row_sums(const AttnArgs& a, bool most, cudaStream_t st)
+spc_status row_sums(const AttnArgs& a, bool norms, cudaStream_t st)
 {
     if constexpr (std::is_same<T, __half>::value) {
-        if (most) {
-            SPC_CUDA_TRY(cudaMemsetAsync(a.most, 0, 8, st));
+        if (norms) {
             const spc_status s = rows_of<T, false, true>(a, st);
             return s != SPC_OK ? s : rows_of<T, true, true>(a, st);
         }
@@ -335,7 +319,8 @@ void attention_plan(AttnArgs& a, spc_dtype dt, void* ws, bool backward)
     a.part_kv = reinterpret_cast<float*>(base + l.part_kv);
     a.lse2 = reinterpret_cast<float*>(base + l.lse2);
     a.delta = reinterpret_cast<float*>(base + l.delta);
-    a.most = reinterpret_cast<uint32_t*>(base + l.most);
+    a.norm_do = reinterpret_cast<float*>(base + l.norm_do);
+    a.norm_v = reinterpret_cast<float*>(base + l.norm_v);
 }
 
 spc_status attention_fwd(const AttnArgs& a, spc_dtype dt, cudaStream_t st)

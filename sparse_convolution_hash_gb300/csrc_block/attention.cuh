@@ -55,7 +55,8 @@ struct AttnArgs {
     float* part_kv;           // [2][splits_kv][nk][hk][d]: dk, dv
     float* lse2;              // [hq][nq]: minus lse, to base 2 (-inf for a query without keys: no probability)
     float* delta;             // [hq][nq]: minus the sum of do o
-    uint32_t* most;           // fp16: bits of the largest squared norms of a row of do and of v
+    float* norm_do;           // fp16 on tensor cores: [hq][nq], [hk][nk]: norms of the rows of do and of v, 0 where not finite
+    float* norm_v;
 };
 
 inline int64_t attn_slots(int64_t n, int32_t segments, int32_t rows) { return n / rows + segments + 2; }

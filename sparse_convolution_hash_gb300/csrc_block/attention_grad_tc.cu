@@ -16,8 +16,12 @@
 // products' operands (a product of 128 x 64 x 16 reads 6 KB, 48 cycles for 32 of arithmetic), 34 for the columns' lse and
 // delta, which every thread reads.  That of dq waits for its own chain of S, dS and sums (operands 57%, tensor cores 51%).
 //
-// fp16: P is kept times 2^14 and dS times a power of two for which the largest possible value, |P| <= 1 times
-// 2 max|do| max|v|, stays below 2^14, so small probabilities and gradients keep their digits.
+// fp16: P is kept times 2^14, and each kept row's dS times a power of two for which the largest possible value on the block's walk
+// stays below 2^14, so small probabilities and gradients keep their digits.  With |P| <= 1 and |dP| <= |do| |v| that value is
+// |do| max|v| + |delta| for a row of dq, max|do| |v| + max|delta| for one of dk, the maxima over rows of the same segment and
+// heads: what other segments and heads hold has no say (one factor for the whole call lost the digits of segments whose do was
+// smaller than another's by 2^20).  The maxima cost a block some loads before its first step: 120,000 rows in 600 windows 357 us
+// against 348 with the one factor, 32,768 rows in 2 samples, 8 heads of 128 6.02 ms against 5.94.
 //
 // Waits are bounded as in the forward kernel.
 #include "attention_tc.cuh"
@@ -48,20 +52,17 @@ struct Shape {
     static constexpr size_t kSmem = 1024 + 2 * (size_t)kKept + (size_t)kStages * (kStage + 2 * kStep * 4) + 8 * kBars + 16;
 };
 
+// A lane's factors of P (2^up) and of dS beside P's, and what undoes them in the sums.
 struct Scales {
-    float up;      // log2 of P's factor
-    float ds;      // factor of dS beside P's
-    float back_p;  // what undoes them in the sums of P and dS
-    float back_ds;
+    float up, ds, back_p, back_ds;
 };
 
+// most: no dP - delta of this lane is larger.
 template <typename T>
-__device__ __forceinline__ Scales scales(const AttnArgs& a)
+__device__ __forceinline__ Scales scales(float most)
 {
     if constexpr (!std::is_same<T, __half>::value) return Scales{0.f, 1.f, 1.f, 1.f};
     else {
-        // do and v have these norms at most, and delta is a mean of such products
-        const float most = 2.f * sqrtf(__uint_as_float(fetch(a.most))) * sqrtf(__uint_as_float(fetch(a.most + 1)));
         int e = 0;
         if (most > 0.f && most < 3e38f) frexpf(most, &e);
         e = min(max(e, -100), 100);
@@ -351,15 +352,58 @@ k_attn_grad_tc(AttnArgs a, uint64_t wait_ns, const __grid_constant__ CUtensorMap
         const int b = (warp - 4) / (4 * S::kHalves), half = ((warp - 4) >> 2) % S::kHalves, quarter = warp & 3, r = quarter * 32 + lane;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         const uint32_t s_at = tmem + lanes + b * 128;
-        const Scales sc = scales<T>(a);
         const float c = a.scale * kLog2e;
         const int64_t row = t.row + r;
         const bool there = row < t.end;
         float my_lse = -INFINITY, my_delta = 0.f;
         if (!KEYS && there) {
-            my_lse = fetch(a.lse2 + (int64_t)kept_head * a.nq + row) + sc.up;
+            my_lse = fetch(a.lse2 + (int64_t)kept_head * a.nq + row);
             my_delta = fetch(a.delta + (int64_t)kept_head * a.nq + row);
         }
+        float most = 0.f;
+        if constexpr (std::is_same<T, __half>::value) {
+            const float mine = there ? fetch(KEYS ? a.norm_v + kept_head * a.nk + row : a.norm_do + kept_head * a.nq + row) : 0.f;
+            // the largest norms (and, of queries, |delta|) of the rows on the walk
+            constexpr int kWarps = 4 * BUFS * S::kHalves;
+            __shared__ float tops[2][kWarps];
+            float top = 0.f, top_delta = 0.f;
+            auto take = [&](int head, int64_t begin, int64_t end) {
+                const int64_t first = head * (KEYS ? a.nq : a.nk);
+                const float* norms = (KEYS ? a.norm_do : a.norm_v) + first;
+                const float* deltas = a.delta + first;
+#pragma unroll 4
+                for (int64_t at = begin + tid - 128; at < end; at += 32 * kWarps) {
+                    top = fmaxf(top, fetch(norms + at));
+                    if (KEYS) {
+                        const float delta = fabsf(fetch(deltas + at));
+                        top_delta = fmaxf(top_delta, delta < INFINITY ? delta : 0.f);
+                    }
+                }
+            };
+            if (splits == 1) {  // without the divisions (120,000 rows in 600 windows 366 us against 372)
+                for (int h = 0; h < (KEYS ? per : 1); ++h) take(KEYS ? kept_head * per + h : kept_head / per, t.lo, t.hi);
+            } else if (n > 0) {
+                const int first = step_head(0), last = step_head(n - 1);
+                const int64_t begin = step_row(0), end = min(t.hi, step_row(n - 1) + kStep);
+                for (int h = first; h <= last; ++h) take(h, h == first ? begin : t.lo, h == last ? end : t.hi);
+            }
+            // non-negative numbers are ordered as their bits
+            top = __uint_as_float(__reduce_max_sync(FULL_MASK, __float_as_uint(top)));
+            top_delta = __uint_as_float(__reduce_max_sync(FULL_MASK, __float_as_uint(top_delta)));
+            if (lane == 0) {
+                tops[0][warp - 4] = top;
+                tops[1][warp - 4] = top_delta;
+            }
+            ptx::bar_sync_named(1, 32 * kWarps);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                top = fmaxf(top, tops[0][w]);
+                top_delta = fmaxf(top_delta, tops[1][w]);
+            }
+            most = fmaf(top, mine, KEYS ? top_delta : fabsf(my_delta));
+        }
+        const Scales sc = scales<T>(most);
+        my_lse += sc.up;
         for (int j = b; j < n; j += BUFS) {
             const int s = j % S::kStages;
             ok = attn_wait(&s_full[b], (j / BUFS) & 1, wait_ns);

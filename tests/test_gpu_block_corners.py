@@ -103,3 +103,42 @@ def test_route_tie_at_the_border_of_biased_scores():
     for more in range(8):
         check_choice(logits, 1, "sigmoid", bias)
         bias[33] = torch.nextafter(bias[33], torch.tensor(1.0))
+
+
+# ------------------------------------------------------------------ gradients of very different size in fp16
+@pytest.mark.parametrize("hq,hk,d,sizes_q,sizes_k", [(2, 2, 64, [900, 900], None), (4, 2, 128, [300, 500], None), (2, 1, 32, [3000, 200], None),
+                                                     (4, 2, 64, [3, 2], [4000, 900]), (2, 2, 40, [4000, 70], [150, 30]), (2, 2, 36, [200, 200], None)])
+def test_attention_gradients_of_segments_and_heads_apart_in_fp16(hq, hk, d, sizes_q, sizes_k):
+    """dout and v of one segment, of rows of no segment and of another head are larger by up to 2^25 each: every segment and key
+    head keeps the digits that it has alone."""
+    g = gen(d + sum(sizes_q))
+    outside = 5
+    seg = [outside + sum(sizes_q[:i]) for i in range(len(sizes_q) + 1)]
+    seg_k = seg if sizes_k is None else [outside + sum(sizes_k[:i]) for i in range(len(sizes_k) + 1)]
+    nq, nk = seg[-1] + outside, seg_k[-1] + outside
+    q, k, v, dout = (normal(g, n, h, d) for n, h in ((nq, hq), (nk, hk), (nk, hk), (nq, hq)))
+    per = hq // hk
+    dout[:seg[1]] *= 2.0 ** 12
+    dout[seg[1]:] *= 2.0 ** -10
+    dout[:, per:] *= 2.0 ** -4  # the second key head's queries
+    dout[:outside] = dout[-outside:] = 6e4
+    v[:outside] = v[-outside:] = -6e4
+    q, k, v, dout = (t.half() for t in (q, k, v, dout))
+    t_seg, t_seg_k = offsets(*seg), None if seg_k is seg else offsets(*seg_k)
+    o, lse = spc.spc_attention_fwd(to(q), to(k), to(v), t_seg, seg_k=t_seg_k)
+    args = to(dout), to(q), to(k), to(v), o, lse, t_seg
+    grads = spc.spc_attention_bwd(*args, seg_k=t_seg_k)
+    again = spc.spc_attention_bwd(*args, seg_k=t_seg_k)
+    assert all(torch.equal(a, b) for a, b in zip(grads, again))
+    for s in range(len(sizes_q)):
+        a, b = slice(seg[s], seg[s + 1]), slice(seg_k[s], seg_k[s + 1])
+        for h in range(hk):
+            hs = slice(h * per, h * per + per), slice(h, h + 1)
+            own = [0, a.stop - a.start], [0, b.stop - b.start]
+            want, bound = ref.attention_bwd(dout[a, hs[0]], q[a, hs[0]], k[b, hs[1]], v[b, hs[1]], o[a, hs[0]].cpu(), lse[a, hs[0]].cpu(), *own,
+                                            d ** -0.5, d % 8 == 0)
+            for got, w, e, rows, heads, name in zip(grads, want, bound, (a, b, b), (hs[0], hs[1], hs[1]), ("dq", "dk", "dv")):
+                # the reference's own allowance of 2^-30 is for values of order 1
+                close(got[rows, heads], w, e - 2.0 ** -30, f"{name} of segment {s}, key head {h}")
+    for got, n in zip(grads, (nq, nk, nk)):
+        assert not got[:outside].any() and not got[n - outside:].any()
