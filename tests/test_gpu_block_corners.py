@@ -9,6 +9,7 @@ import torch
 
 import block_ref as ref
 import sparse_convolution_hash_gb300 as spc
+from block_ref import E
 from gpu_util import DT, dev
 from test_gpu_block import TYPES, close, gen, normal, to
 
@@ -142,3 +143,80 @@ def test_attention_gradients_of_segments_and_heads_apart_in_fp16(hq, hk, d, size
                 close(got[rows, heads], w, e - 2.0 ** -30, f"{name} of segment {s}, key head {h}")
     for got, n in zip(grads, (nq, nk, nk)):
         assert not got[:outside].any() and not got[n - outside:].any()
+
+
+# ------------------------------------------------------------------ rows whose values are nearly the same
+def norm_of_near_values(x, ga, be, eps):
+    """y, mean, rstd and their bounds where a row's mean is far from its spread.
+
+    The first mean is off by f = h mean|x| at most, h = (c / 512 + 64) E as in block_ref.  Differences from it round by E of themselves,
+    and their own mean, which is taken off again, by h of their mean size.  The sum of their squares is off by h and a few
+    roundings of itself, and so is what is taken off it.  A row whose mean is within about four spreads of zero keeps f."""
+    c = x.shape[1]
+    (y, mean, rstd), _ = ref.layer_norm_fwd(x, ga, be, eps)
+    x, ga = x.double(), ga.double()
+    far = (x - mean[:, None]).abs()
+    h = (c / 512 + 64) * E
+    f = h * x.abs().mean(1)
+    size = far.mean(1) + f
+    var = (far ** 2).mean(1)
+    kept = torch.where(mean ** 2 < 18 * var, f, 0.0)
+    off = 2 * E * (far + f[:, None]) + ((h + 2 * E) * size + kept)[:, None]
+    vb = 2 * (h + 6 * E) * (var + f * f) + 2 * f * (h + 2 * E) * size + kept ** 2
+    rb = vb / (var + eps) + 4 * E
+    xh = far * rstd[:, None]
+    yb = (off * rstd[:, None] * 1.01 + xh * rb[:, None]) * ga.abs() + 3 * E * xh * ga.abs() + E * y.abs()
+    return (y, mean, rstd), (yb + 1e-30, 2 * E * mean.abs() + (h + 2 * E) * size + kept, rstd * rb)
+
+
+CHANNELS = [5, 24, 64, 333, 334, 512, 1000, 1027, 4001, 8192, 16384, 20000]
+
+
+@pytest.mark.parametrize("c", CHANNELS)
+@pytest.mark.parametrize("dtype", TYPES)
+def test_layer_norm_of_equal_values(c, dtype):
+    """Rows of one value: y is beta."""
+    x = torch.tensor([30000.0, -1000.3, 0.1, 7.7, 0.0, 123.456, 65000.0])[:, None].expand(7, c).to(DT[dtype])
+    ga, be = 1 + 0.3 * normal(gen(c), c), 0.3 * normal(gen(c + 1), c)
+    want, bound = norm_of_near_values(x, ga, be, 1e-5)
+    got = spc.spc_layer_norm_fwd(to(x), to(ga), to(be))
+    close(got[0], want[0], bound[0] + ref.rounding(want[0], DT[dtype]), "y")
+    close(got[1], want[1], bound[1], "mean")
+    close(got[2], want[2], bound[2], "rstd")
+
+
+@pytest.mark.parametrize("c", CHANNELS)
+@pytest.mark.parametrize("mean,std", [(1000.3, 0.01), (1e6, 1.0), (-3e4, 0.1), (0.0, 1.0)])
+def test_layer_norm_of_a_small_spread_far_from_zero(c, mean, std):
+    x = (mean + std * torch.randn(40, c, generator=gen(c), dtype=torch.float64)).float()
+    ga, be = 1 + 0.3 * normal(gen(c), c), 0.3 * normal(gen(c + 1), c)
+    want, bound = norm_of_near_values(x, ga, be, 1e-5)
+    got = spc.spc_layer_norm_fwd(to(x), to(ga), to(be))
+    for a, w, b, name in zip(got, want, bound, ("y", "mean", "rstd")):
+        close(a, w, b, name)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_layer_norm_of_values_whose_squares_fp32_does_not_hold(dtype):
+    """rstd is 0 then, and y beta."""
+    x = torch.tensor([1e25, -1e25, 3e24, 0.0] * 10).repeat(3, 1).to(DT[dtype])
+    y, mean, rstd = spc.spc_layer_norm_fwd(to(x), None, None)
+    assert not y.any() and not rstd.any() and mean.isfinite().all()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("c", CHANNELS)
+def test_layer_norm_of_a_row_does_not_hang_on_its_neighbours(c, dtype):
+    """Bits of rows near zero are the same among rows far from it, in place too."""
+    x = normal(gen(c), 41, c, dtype=dtype)
+    ga, be = 1 + 0.3 * normal(gen(c), c), 0.3 * normal(gen(c + 1), c)
+    want = spc.spc_layer_norm_fwd(to(x), to(ga), to(be))
+    mixed = to(x).clone()
+    mixed[1::3] += 100
+    far = spc.spc_layer_norm_fwd(mixed[1::3].contiguous(), to(ga), to(be))
+    for out in (None, mixed):
+        got = spc.spc_layer_norm_fwd(mixed, to(ga), to(be), out=out)
+        for a, b, f in zip(got, want, far):
+            for first in (0, 2):
+                assert torch.equal(a[first::3], b[first::3])
+            assert torch.equal(a[1::3], f)
