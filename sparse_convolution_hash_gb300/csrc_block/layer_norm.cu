@@ -60,13 +60,13 @@ struct Place {
     __device__ __forceinline__ bool in(int k, int j) const { return at(k, j) < c; }
 };
 
-// Zeros where the row has ended, or there is no row: they add nothing to any sum.
-template <typename T, int V, int W>
+// Zeros where the row has ended, or there is no row: they add nothing to any sum.  AGAIN: the row's first word where it has ended.
+template <typename T, int V, int W, bool AGAIN = false>
 __device__ __forceinline__ void load_row(const T* row, const Place<V, W>& w, int k, bool there, Vec<T, V>& v)
 {
     if constexpr (W == V) {
         uint4 bits = make_uint4(0u, 0u, 0u, 0u);
-        if (there && w.in(k, 0)) bits = *reinterpret_cast<const uint4*>(row + w.at(k, 0));
+        if (there && (AGAIN || w.in(k, 0))) bits = *reinterpret_cast<const uint4*>(row + (w.in(k, 0) ? w.at(k, 0) : 0));
         memcpy(&v, &bits, 16);
     } else {
         // as bits, which no instruction touches until the row's turn comes
@@ -75,7 +75,7 @@ __device__ __forceinline__ void load_row(const T* row, const Place<V, W>& w, int
 #pragma unroll
         for (int q = 0; q < V / W; ++q) {
             words[q] = Bits{};
-            if (there && w.in(k, q * W)) words[q] = *reinterpret_cast<const Bits*>(row + w.at(k, q * W));
+            if (there && (AGAIN || w.in(k, q * W))) words[q] = *reinterpret_cast<const Bits*>(row + (w.in(k, q * W) ? w.at(k, q * W) : 0));
         }
         memcpy(&v, words, 16);
     }
@@ -283,6 +283,9 @@ __global__ void __launch_bounds__(kBwdBlock, 1)
 k_layer_norm_grad(LayerNormArgs a, int L, float* part)
 {
     constexpr int H = V / 2;
+    // Past a row's end xh of x = 0 is infinite where mean rstd is, and dy's zeros do not silence that.  The row's first word stands
+    // there instead, or, in long rows of single words, where those loads cost up to 15%, such a row's sum is taken again.
+    constexpr bool kAgain = W == V || K == 1;
     extern __shared__ float joint[];  // [units][2][c]
     __shared__ float box[2 * 16 * 2 * R];
     wait_for_kernel_before();
@@ -310,7 +313,7 @@ k_layer_norm_grad(LayerNormArgs a, int L, float* part)
             sr[r] = there ? fetch(a.rstd + row0 + r) : 0.f;
 #pragma unroll
             for (int k = 0; k < K; ++k) {
-                load_row<T, V, W>(x + (row0 + r) * a.c, w, k, there, xr[r][k]);
+                load_row<T, V, W, kAgain>(x + (row0 + r) * a.c, w, k, there, xr[r][k]);
                 load_row<T, V, W>(dy + (row0 + r) * a.c, w, k, there, dr[r][k]);
             }
         }
@@ -346,6 +349,17 @@ k_layer_norm_grad(LayerNormArgs a, int L, float* part)
             }
             s[2 * r] = p.x + p.y;
             s[2 * r + 1] = q.x + q.y;
+            if (!kAgain && fabsf(mr[r] * sr[r]) == INFINITY) {
+                s[2 * r + 1] = 0.f;
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        const F2 v = u[r][k][j / 2], h = xh[r][k][j / 2];
+                        if (w.in(k, j)) s[2 * r + 1] = j & 1 ? fmaf(v.y, h.y, s[2 * r + 1]) : fmaf(v.x, h.x, s[2 * r + 1]);
+                    }
+                }
+            }
             rs[r] = sr[r];
         }
         if (base + step < a.n) load(base + step + mine);

@@ -220,3 +220,18 @@ def test_layer_norm_of_a_row_does_not_hang_on_its_neighbours(c, dtype):
             for first in (0, 2):
                 assert torch.equal(a[first::3], b[first::3])
             assert torch.equal(a[1::3], f)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("c", [5, 24, 40, 333, 334, 1000, 1027, 4100, 8190])
+def test_layer_norm_gradient_where_mean_times_rstd_passes_fp32(c, dtype):
+    """Rows of one large value: their differences from the mean are 0, and nothing past a row's end takes part."""
+    g = gen(c)
+    x, dy = torch.full((9, c), 2.0 ** 112).to(DT[dtype]), normal(g, 9, c, dtype=dtype)
+    ga = 1 + 0.3 * normal(g, c)
+    mean, rstd = torch.full((9,), 2.0 ** 112), torch.full((9,), 2.0 ** 20)
+    x[4:], mean[4:], rstd[4:] = normal(g, 5, c, dtype=dtype), 0.1, 0.9
+    want, bound = ref.layer_norm_bwd(dy, x, ga, mean, rstd)
+    got = spc.spc_layer_norm_bwd(to(dy), to(x), to(ga), to(mean), to(rstd))
+    for a, w, b, name in zip(got, want, bound, ("dx", "dgamma", "dbeta")):
+        close(a, w, b, name)
