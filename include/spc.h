@@ -740,7 +740,7 @@ SPC_API spc_status spc_route_bwd(const float* dgate, const void* logits, const i
  * spc_attention_fwd -- each query attends to the keys of its own segment:
  *   s = scale q k^T,  p = softmax(s) over the segment's keys,  o = p v,
  *   lse = log(sum of exp(s)).
- * seg_q and seg_k (as above, any number of segments) hold the rows of each segment among the queries and the
+ * seg_q and seg_k (as above, up to 2^30 segments) hold the rows of each segment among the queries and the
  * keys; pass the same array for attention of rows among themselves.  Rows of the same
  * head are independent of other segments' values, NaN and infinities among them.  A query without keys
  * (an empty segment, rows outside all segments, scores all -inf) gives o = 0 and lse = -inf.

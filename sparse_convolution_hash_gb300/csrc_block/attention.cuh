@@ -59,6 +59,9 @@ struct AttnArgs {
     float* norm_v;
 };
 
+// What attn_tile's search numbers in 32 bits: a candidate and 31 steps of a 32nd of them.
+constexpr int32_t kAttnMostSegments = 1 << 30;
+
 inline int64_t attn_slots(int64_t n, int32_t segments, int32_t rows) { return n / rows + segments + 2; }
 
 // A tile: rows [row, end) of its own axis (at most P), the segment's rows [lo, hi) of the other one.

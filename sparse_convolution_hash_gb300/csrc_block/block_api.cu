@@ -70,7 +70,7 @@ bool among(const void* result, const void* const (&others)[N])
 // Rows are 32-bit numbers, also those of a tile that begins before the last one.
 bool attention_sizes_ok(int64_t nq, int64_t nk, int32_t segments, int32_t hq, int32_t d)
 {
-    return d <= 128 && hq <= 65535 && nq <= INT32_MAX - 128 && nk <= INT32_MAX - 128 && segments <= INT32_MAX - 4;
+    return d <= 128 && hq <= 65535 && nq <= INT32_MAX - 128 && nk <= INT32_MAX - 128 && segments <= kAttnMostSegments;
 }
 
 spc_status check_attention(const AttnArgs& a, spc_dtype dt, bool backward)
