@@ -1063,7 +1063,7 @@ def _attention_args(q, k, v, seg, seg_k, scale):
         seg_k = _typed(seg_k, torch.int32, "seg_k")
         _expect(seg_k, seg.shape, "seg_k")
     _one_device(dev, k, v, seg, seg_k)
-    return q, ldq, k, ldk, v, ldv, seg, seg_k, nq, nk, hq, hk, d, d ** -0.5 if scale is None else scale, dev
+    return q, ldq, k, ldk, v, ldv, seg, seg_k, nq, nk, hq, hk, d, max(d, 1) ** -0.5 if scale is None else scale, dev
 
 
 def spc_attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seg: torch.Tensor,

@@ -235,3 +235,13 @@ def test_layer_norm_gradient_where_mean_times_rstd_passes_fp32(c, dtype):
     got = spc.spc_layer_norm_bwd(to(dy), to(x), to(ga), to(mean), to(rstd))
     for a, w, b, name in zip(got, want, bound, ("dx", "dgamma", "dbeta")):
         close(a, w, b, name)
+
+
+# ------------------------------------------------------------------ calls that are refused
+def test_attention_refuses_heads_of_no_channels():
+    x = torch.zeros(4, 2, 0, device=dev())
+    for scale in (None, 1.0):
+        with pytest.raises(spc.SpcError):
+            spc.spc_attention_fwd(x, x, x, offsets(0, 4), scale=scale)
+        with pytest.raises(spc.SpcError):
+            spc.spc_attention_bwd(x, x, x, x, x, torch.zeros(4, 2, device=dev()), offsets(0, 4), scale=scale)
