@@ -113,24 +113,16 @@ __device__ __forceinline__ uint32_t lanes_most(uint32_t v)
     else return lanes_max<L>(v);
 }
 
-// The best of the lanes' values: (value, expert, logit), ties to the lowest expert; expert kNone where none is left.
-template <int C, int L>
-__device__ __forceinline__ void best_of_lanes(float& top, int& e, float& l, int lane)
+// The best of a warp's values: (value, expert, logit), ties to the lowest expert; expert kNone where none is left.
+__device__ __forceinline__ void best_of_warp(float& top, int& e, float& l)
 {
-    const uint32_t key = order_of(top), most = lanes_most<L>(key);
+    const uint32_t key = order_of(top), most = lanes_most<32>(key);
     const bool mine = key == most && e != kNone;
-    int winner;
-    if constexpr (C == 1) {  // lanes hold ascending experts
-        const uint32_t at = (threadIdx.x & 31) - lane, votes = __ballot_sync(FULL_MASK, mine) >> at;
-        winner = __ffs(L == 32 ? votes : votes & ((1u << (L & 31)) - 1)) - 1;
-    } else {
-        const uint32_t least = ~lanes_most<L>(~(mine ? (uint32_t)e : (uint32_t)kNone));
-        const uint32_t votes = __ballot_sync(FULL_MASK, mine && (uint32_t)e == least);
-        winner = __ffs(votes) - 1;
-    }
+    const uint32_t least = ~lanes_most<32>(~(mine ? (uint32_t)e : (uint32_t)kNone));
+    const int winner = __ffs(__ballot_sync(FULL_MASK, mine && (uint32_t)e == least)) - 1;
     const int from = max(winner, 0);
-    e = __shfl_sync(FULL_MASK, e, from, L);
-    l = __shfl_sync(FULL_MASK, l, from, L);
+    e = __shfl_sync(FULL_MASK, e, from);
+    l = __shfl_sync(FULL_MASK, l, from);
     top = value_of(most);
     if (winner < 0) e = kNone;
 }
@@ -436,6 +428,7 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const T* row, const f
                 if (v[j]) near |= too_near(value_of(v[j] & ~7u), lane * kPer + 7 - (int)(v[j] & 7u));
         }
     } else {
+        static_assert(L == 32, "several chunks to a lane, a warp to a row");
         bool at_border = false;  // the last that is chosen and the first that is left out are a tie
         for (int r = 0; r < rounds; ++r) {
             float top = kLow;
@@ -451,7 +444,7 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const T* row, const f
                         l_top = l[i][j];
                     }
             }
-            best_of_lanes<C, L>(top, e_top, l_top, lane);
+            best_of_warp(top, e_top, l_top);
             const bool found = e_top != kNone;
             if (!BY_LOGIT && found) {
                 if (r > 0) near |= too_near(top, e_top);
@@ -692,8 +685,9 @@ k_route(RouteArgs a, bool whole)
     const T* logits = static_cast<const T*>(a.logits) + at * a.experts;
     const bool sigmoid = a.score == SPC_SCORE_SIGMOID, by_logit = !a.bias && a.groups == 1, all = !sigmoid && !a.renorm;
     float most = -INFINITY, sum = 1.f;
+    constexpr bool kWords = sizeof(T) == 2 && C == 1;  // by_logit: expert and logit in one word
     bool chosen = false;
-    if constexpr (sizeof(T) == 2 && C == 1) {
+    if constexpr (kWords) {
         if (by_logit) {
             choose16<T, L>(a, logits, lane, whole, sh);
             chosen = true;
@@ -703,8 +697,8 @@ k_route(RouteArgs a, bool whole)
         float l[C][kPer];
         load_logits<T, C, L>(logits, a.experts, lane, whole, l);
         if (chosen) {
-        } else if (by_logit) {
-            choose<T, true, C, L>(a, logits, l, lane, whole, sh);
+        } else if (!kWords && by_logit) {
+            if constexpr (!kWords) choose<T, true, C, L>(a, logits, l, lane, whole, sh);
         } else if (__any_sync(FULL_MASK, choose<T, false, C, L>(a, logits, l, lane, whole, sh))) {
             __syncwarp();
             choose_exactly<T, C, L>(a, logits, lane, whole, sh);
