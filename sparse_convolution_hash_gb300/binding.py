@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 import os
 import threading
 from typing import Optional, Sequence
@@ -22,6 +23,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "_build", "libspc.so")
 
 SPC_OK = 0
+SPC_ERR_INVALID_ARG = 1
 STATUS_NAMES = {
     0: "SPC_OK", 1: "SPC_ERR_INVALID_ARG", 2: "SPC_ERR_COORD_RANGE", 3: "SPC_ERR_DUPLICATE",
     4: "SPC_ERR_TABLE_FULL", 5: "SPC_ERR_CAPACITY", 6: "SPC_ERR_UNSUPPORTED", 7: "SPC_ERR_CUDA",
@@ -847,6 +849,13 @@ def spc_grouped_wgrad(x: torch.Tensor, dy: torch.Tensor, seg: torch.Tensor,
 
 # A transformer block's layers.  Their tensors lie on one device, whichever is current.
 
+def _held(sizes: int, where: str):
+    """Refuses sizes and choices (or'ed together) that the library takes in 32 bits and that these do not hold, of which
+    ctypes would pass the low half."""
+    if not 0 <= sizes <= 0x7fffffff:
+        raise SpcError(SPC_ERR_INVALID_ARG, where)
+
+
 def _one_device(dev, *tensors):
     for t in tensors:
         if t is not None and t.device != dev:
@@ -902,6 +911,7 @@ def spc_layer_norm_fwd(x: torch.Tensor, gamma: Optional[torch.Tensor], beta: Opt
     rstd [n]).  Pass `out`, `mean` and `rstd` to call without allocating."""
     x = _matrix(x, "x")
     n, c = x.shape
+    _held(c, "spc_layer_norm_fwd")
     dev = x.device
     gamma, gamma_p = _optional(gamma, torch.float32, (c,), "gamma")
     beta, beta_p = _optional(beta, torch.float32, (c,), "beta")
@@ -922,6 +932,7 @@ def spc_layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, gamma: Optional[torch.
     the forward call."""
     x = _matrix(x, "x")
     n, c = x.shape
+    _held(c, "spc_layer_norm_bwd")
     dev = x.device
     dy = _typed(dy, x.dtype, "dy")
     _expect(dy, (n, c), "dy")
@@ -948,19 +959,22 @@ def _launch_size(dev, f, *args) -> int:
         return f(*args)
 
 
-@functools.lru_cache(maxsize=64)
-def _three(pairs: tuple):
+@functools.lru_cache(maxsize=64, typed=True)
+def _three(*pairs):
     """(C array, sum) of the numbers of turned pairs of channels for z, y and x."""
-    t = tuple(int(p) for p in pairs)
-    if len(t) != 3 or min(t) < 0:
-        raise ValueError("pairs must hold the number of turned pairs of channels for z, y and x")
+    try:
+        t = tuple(operator.index(p) for p in pairs)
+    except TypeError:
+        t = ()
+    if len(t) != 3 or min(t) < 0 or max(t) > 0x7fffffff:
+        raise ValueError("pairs must hold the number of turned pairs of channels for z, y and x, whole and not negative")
     return _I3(*t), sum(t)
 
 
 def spc_rope_steps(pairs: Sequence[int], base: float = 10000.0) -> torch.Tensor:
     """Steps of spc_rope_fwd for base^(-j / pairs[axis]) radians a cell, j = 0 .. pairs[axis] - 1: a CPU tensor
     [sum(pairs)] int64, 2^64 to a full turn.  Computed once, kept by the caller."""
-    counts, turned = _three(tuple(pairs))
+    counts, turned = _three(*pairs)
     steps = torch.empty(turned, dtype=torch.int64)
     _check(lib().spc_rope_steps(counts, base, steps.data_ptr() if turned else None), "spc_rope_steps")
     return steps
@@ -969,8 +983,9 @@ def spc_rope_steps(pairs: Sequence[int], base: float = 10000.0) -> torch.Tensor:
 def _rope(f, name: str, x: torch.Tensor, coords: torch.Tensor, steps: torch.Tensor, pairs, out):
     x, ldx = _head_rows(x, "x")
     n, heads, d = x.shape
+    _held(heads | d, name)
     dev = x.device
-    counts, turned = _three(tuple(pairs))
+    counts, turned = _three(*pairs)
     if not coords.is_cuda or coords.dtype is not torch.int32:
         raise ValueError("coords must be an int32 CUDA tensor")
     _expect(coords, (n, 4), "coords")
@@ -1010,6 +1025,7 @@ def spc_route_fwd(logits: torch.Tensor, top_k: int, score: int = SPC_SCORE_SOFTM
     for which no expert is available (logits of -inf or NaN) holds -1 and weight 0."""
     logits = _matrix(logits, "logits")
     n, experts = logits.shape
+    _held(experts | top_k | score | groups | top_groups, "spc_route_fwd")
     dev = logits.device
     bias, bias_p = _optional(bias, torch.float32, (experts,), "bias")
     _one_device(dev, bias)
@@ -1033,6 +1049,7 @@ def spc_route_bwd(dgate: torch.Tensor, logits: torch.Tensor, expert: torch.Tenso
     if expert.dim() != 2:
         raise ValueError("expert must have shape [n, top_k]")
     top_k = expert.shape[1]
+    _held(experts | top_k | score, "spc_route_bwd")
     _expect(expert, (n, top_k), "expert")
     dgate = _typed(dgate, torch.float32, "dgate")
     _expect(dgate, (n, top_k), "dgate")
@@ -1063,7 +1080,9 @@ def _attention_args(q, k, v, seg, seg_k, scale):
         seg_k = _typed(seg_k, torch.int32, "seg_k")
         _expect(seg_k, seg.shape, "seg_k")
     _one_device(dev, k, v, seg, seg_k)
-    return q, ldq, k, ldk, v, ldv, seg, seg_k, nq, nk, hq, hk, d, max(d, 1) ** -0.5 if scale is None else scale, dev
+    segments = seg.shape[0] - 1
+    _held(hq | hk | d | segments, "spc_attention")
+    return q, ldq, k, ldk, v, ldv, seg, seg_k, segments, nq, nk, hq, hk, d, max(d, 1) ** -0.5 if scale is None else scale, dev
 
 
 def spc_attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seg: torch.Tensor,
@@ -1076,11 +1095,11 @@ def spc_attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seg: to
     projection's rows are read in place.  `seg` [segments + 1] int32 holds the offsets of the queries'
     segments, `seg_k` those of the keys (None: the same rows).  scale None: d^-0.5.  A query without keys
     gives 0 and lse -inf.  Pass `out`, `lse` and `ws` to call without allocating."""
-    q, ldq, k, ldk, v, ldv, seg, seg_k, nq, nk, hq, hk, d, scale, dev = _attention_args(q, k, v, seg, seg_k, scale)
+    q, ldq, k, ldk, v, ldv, seg, seg_k, segments, nq, nk, hq, hk, d, scale, dev = _attention_args(q, k, v, seg, seg_k, scale)
     _one_device(dev, ws, status)
     o, ldo = _head_result(out, (nq, hq, d), q.dtype, dev, "out")
     lse = _result(lse, (nq, hq), torch.float32, dev, "lse")
-    L, dt, segments = lib(), _DTYPES[q.dtype], seg.shape[0] - 1
+    L, dt = lib(), _DTYPES[q.dtype]
     nbytes = _launch_size(dev, L.spc_attention_workspace_size, nq, nk, segments, hq, hk, d, dt, 0)
     if nbytes or ws is not None:
         ws = _room(ws, nbytes, dev)
@@ -1098,7 +1117,7 @@ def spc_attention_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: t
                       ws: Optional[torch.Tensor] = None):
     """Gradients of spc_attention_fwd: (dq [nq, hq, d], dk, dv [nk, hk, d]).  `o` and `lse` come from the forward
     call.  `dq`, `dk` and `dv` may be slices of one gradient of the projection's rows."""
-    q, ldq, k, ldk, v, ldv, seg, seg_k, nq, nk, hq, hk, d, scale, dev = _attention_args(q, k, v, seg, seg_k, scale)
+    q, ldq, k, ldk, v, ldv, seg, seg_k, segments, nq, nk, hq, hk, d, scale, dev = _attention_args(q, k, v, seg, seg_k, scale)
     dout, lddo = _head_rows(dout if dout.dtype is q.dtype else dout.to(q.dtype), "dout")
     _expect(dout, (nq, hq, d), "dout")
     o, ldo = _head_rows(o if o.dtype is q.dtype else o.to(q.dtype), "o")
@@ -1108,7 +1127,7 @@ def spc_attention_bwd(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: t
     dq, lddq = _head_result(dq, (nq, hq, d), q.dtype, dev, "dq")
     dk, lddk = _head_result(dk, (nk, hk, d), q.dtype, dev, "dk")
     dv, lddv = _head_result(dv, (nk, hk, d), q.dtype, dev, "dv")
-    L, dt, segments = lib(), _DTYPES[q.dtype], seg.shape[0] - 1
+    L, dt = lib(), _DTYPES[q.dtype]
     ws = _room(ws, _launch_size(dev, L.spc_attention_workspace_size, nq, nk, segments, hq, hk, d, dt, 1), dev)
     code = _launch(dev, L.spc_attention_bwd, dout.data_ptr(), lddo, q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv,
                    o.data_ptr(), ldo, lse_p, seg.data_ptr(), seg_k.data_ptr(), segments, nq, nk, hq, hk, d, scale, dt,

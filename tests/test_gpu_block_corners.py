@@ -245,3 +245,32 @@ def test_attention_refuses_heads_of_no_channels():
             spc.spc_attention_fwd(x, x, x, offsets(0, 4), scale=scale)
         with pytest.raises(spc.SpcError):
             spc.spc_attention_bwd(x, x, x, x, x, torch.zeros(4, 2, device=dev()), offsets(0, 4), scale=scale)
+
+
+def test_choices_that_32_bits_do_not_hold_are_refused():
+    """Not taken for their low halves: 2^32 + 1 groups are not one."""
+    x = torch.randn(5, 16, device=dev())
+    for bad in (dict(groups=2 ** 32 + 1), dict(groups=2, top_groups=2 ** 32 + 1), dict(score=2 ** 32), dict(groups=1 - 2 ** 32)):
+        with pytest.raises(spc.SpcError):
+            spc.spc_route_fwd(x, 2, **bad)
+    expert, gate = spc.spc_route_fwd(x, 2)
+    with pytest.raises(spc.SpcError):
+        spc.spc_route_bwd(gate, x, expert, score=2 ** 32)
+
+
+def test_rows_of_more_channels_than_32_bits_hold_are_refused():
+    """Not taken for rows of 8 channels, with the rest left as it was."""
+    n = 2 ** 32 + 8
+    x = torch.zeros(1, n, dtype=torch.float16, device=dev())
+    with pytest.raises(spc.SpcError):
+        spc.spc_layer_norm_fwd(x, None, None)
+    with pytest.raises(spc.SpcError):
+        spc.spc_route_fwd(x, 2)
+    coords, steps = torch.zeros(1, 4, dtype=torch.int32, device=dev()), spc.spc_rope_steps((1, 1, 1))
+    for heads, d in ((1, n), (n // 8, 8)):
+        with pytest.raises(spc.SpcError):
+            spc.spc_rope_fwd(x.view(1, heads, d), coords, steps, (1, 1, 1))
+    for heads, d in ((1, n), (n, 1)):
+        q = x.view(1, heads, d)
+        with pytest.raises(spc.SpcError):
+            spc.spc_attention_fwd(q, q, q, offsets(0, 1))
