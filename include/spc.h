@@ -643,8 +643,8 @@ SPC_API spc_status spc_grouped_wgrad(const void* x, const void* dy, const int32_
 /* --------------------------------------------------------------- layer norm
  * spc_layer_norm_fwd -- per row: mean and variance (divided by c) of its channels,
  * rstd = 1 / sqrt(variance + eps), y = gamma (x - mean) rstd + beta.  The variance is
- * summed around the mean, in fp32; where the mean is more than four spreads from zero, its rounding
- * is summed too and taken off, so that such a row keeps the digits of its spread.
+ * summed around the mean, in fp32; where the mean is more than 16 spreads from zero (256 in 16
+ * bits), its rounding is summed too and taken off, so that such a row keeps the digits of its spread.
  *
  *  x      [n, c] of dtype dt.      y [n, c] of dtype dt out (may be x itself).
  *  gamma, beta  [c] fp32, or NULL (1 and 0).      eps > 0.

@@ -3,7 +3,7 @@
 // A row is held in registers by a group of L threads (a part of a warp, a warp, or several warps), K vectors of V
 // channels to a thread (neighbours read as 16 bytes, or, where rows do not start on such a boundary, in words of two
 // channels, or one by one), so it is read once: the mean, then the sum of
-// squares around it, then the result.  Where the mean is more than four spreads from zero, what its rounding has left is
+// squares around it, then the result.  Where the mean is far from zero, what its rounding has left is
 // taken off as well: the mean of the differences from it, which goes off the mean, the differences and, squared, the variance (without:
 // rows of 1000.3 +- 0.01 off by up to a tenth, rows of one value not zero; with it for all rows 498,145 x 64 bf16 take 36 us against 28).
 // In the backward pass a block keeps its channels for all of its rows,
@@ -121,8 +121,14 @@ __device__ __forceinline__ void load_affine(const float* p, float other, const P
     }
 }
 
-// Whether a row's mean is more than four spreads from zero (not where fp32 does not hold the squares, or NaN).
-__device__ __forceinline__ bool far_from_zero(float mean, float var) { return var < INFINITY && mean * mean > 16.f * var; }
+// Whether a row's mean is so many spreads from zero that its rounding shows in the result: 16 in fp32, 256 in 16 bits (false where
+// fp32 does not hold the squares, and for NaN).  fp32 rows of 1,000 are off by 2.4e-6 at most at 15 spreads without, by 7e-7 at 17 with what
+// follows; but such rows take two to three times as long (498,145 x 64 bf16 71 us against 28).
+template <typename T>
+__device__ __forceinline__ bool far_from_zero(float mean, float var)
+{
+    return var < INFINITY && mean * mean > (sizeof(T) == 4 ? 0x1p8f : 0x1p16f) * var;
+}
 
 // A row that may be far from zero, from its start.  A call that reads the row again and gets nothing but addresses, so that it costs other
 // rows next to nothing: with the differences kept, 32,768 x 1,024 bf16 took 44 us against 30, and inline 498,145 x 64 bf16 34 against 28.
@@ -162,7 +168,7 @@ __device__ __noinline__ void far_row(const T* x, T* y, const float* gamma, const
         (turn == 0 ? mean : turn == 1 ? var : left) = got;
     }
     if (!there) return;
-    if (far_from_zero(mean, var)) var = fmaxf(var - left * left, 0.f);
+    if (far_from_zero<T>(mean, var)) var = fmaxf(var - left * left, 0.f);
     else left = 0.f;
     const float rstd = 1.f / sqrtf(var + eps);
 #pragma unroll 1
@@ -243,7 +249,7 @@ k_layer_norm(LayerNormArgs a, int L)
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         sq[r] = __fmul_rn(sq[r], inv);  // not one with the sum with eps
-        far |= far_from_zero(mean[r], sq[r]);
+        far |= far_from_zero<T>(mean[r], sq[r]);
     }
     if (__any_sync(FULL_MASK, far)) {  // the warps of a row hold the same numbers
         for (int64_t row = row0; row < row0 + R; ++row)
@@ -467,7 +473,7 @@ k_layer_norm_long(LayerNormArgs a)
         s = fmaf(d, d, s);
     }
     float var = block_sum(s, box) / (float)a.c;
-    if (far_from_zero(mean, var)) {
+    if (far_from_zero<T>(mean, var)) {
         left = block_sum(t, box) / (float)a.c;
         var = fmaxf(var - left * left, 0.f);
     }
