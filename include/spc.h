@@ -651,7 +651,8 @@ SPC_API spc_status spc_grouped_wgrad(const void* x, const void* dy, const int32_
  *  mean, rstd   [n] fp32 out (what the backward pass reads).
  *  Rows of any length; they are held in registers up to 16,384 (16-bit) or 8,192 channels (8,192 in the
  *  backward pass), and read in 16-byte words when x, y, gamma and beta are 16-byte aligned and c is a
- *  multiple of 16 bytes, else element by element.
+ *  multiple of 16 bytes, in words of two channels when rows start on such a boundary and gamma and beta
+ *  on 8 bytes, else channel by channel.
  */
 SPC_API spc_status spc_layer_norm_fwd(const void* x, const float* gamma, const float* beta, int64_t n,
                                       int32_t c, float eps, spc_dtype dt, void* y, float* mean,
