@@ -709,7 +709,8 @@ SPC_API spc_status spc_rope_bwd(const void* dy, int64_t lddy, const int32_t* coo
  *   - of the kept groups' experts the top_k largest c are chosen, largest first;
  *   - expert's weight  gate = scale p, or with renorm  scale p / (sum of the chosen p).
  * The bias counts in the choice only.  Equal c go to the lowest expert, equal groups to the
- * lowest group.  The choice is that of c in 64 bits (without bias and groups: of the logits).
+ * lowest group.  The choice is that of c in 64 bits (without bias and groups: of the logits); groups whose
+ * sums differ by no more than the rounding of 64 bits may go either way.
  * An expert whose logit is -inf or NaN, or whose bias is NaN or -inf, is not available; where fewer than top_k
  * are left the rest of a token's slots hold expert -1 (which spc_row_segments puts last) and gate 0.
  *
